@@ -165,6 +165,26 @@ int ulysses_plan_fused_backward_kernel(ulysses_plan_t plan, int* engine);
  * ULY_ROPE_ADJACENT. Must not race with launches using the plan. */
 int ulysses_plan_set_rope_pairs(ulysses_plan_t plan, int pairs);
 
+/*
+ * Position axes of the fused calls' RoPE: images (rows, columns) and video (time, height, width)
+ * give a token one coordinate per axis instead of its sequence index.
+ *   axes     0 (the default: one axis, the sequence index) or 1..4.
+ *   extents  `axes` entries >= 1: the grid extents[0] x extents[1] x ..., the last axis fastest,
+ *            laid along the global sequence from index `first`.
+ *   pairs    `axes` entries >= 0 with a sum of at most d/2: how many of the RoPE pairs each axis
+ *            turns, in order; pairs left over are not turned. Pair i of an axis with m pairs turns
+ *            by coordinate * rope_theta^(-i/m), the ladder of a head of 2m columns (with one axis
+ *            of d/2 pairs, rope_theta^(-2j/d) as without a grid).
+ *   first    >= 0; first + the product of the extents must not pass S. Tokens before and after the
+ *            grid (text beside an image, padding) are normalised but not turned.
+ * Every batch element has the same grid. It holds for the same calls as the pair layout, which it
+ * goes together with. The arrays are read during the call. ULY_EINVAL otherwise (the plan is then
+ * unchanged). The pages name the fused QK RMSNorm + RoPE without fixing its positions. Must not
+ * race with launches using the plan.
+ */
+int ulysses_plan_set_rope_grid(ulysses_plan_t plan, int axes, const int64_t* extents,
+                               const int64_t* pairs, int64_t first);
+
 /* Bytes of rank `rank`'s input and output tensors for `mode` (either pointer may be NULL). */
 int ulysses_plan_bytes(ulysses_plan_t plan, int mode, int rank, int64_t* in_bytes,
                        int64_t* out_bytes);

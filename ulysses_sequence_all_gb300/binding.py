@@ -27,6 +27,7 @@ DTYPE_CODES = {"uint8": ULY_U8, "float8_e4m3fn": ULY_F8E4M3, "float8_e5m2": ULY_
 # Every symbol include/ulysses.h declares.
 EXPORTS = ["ulysses_plan", "ulysses_plan_destroy", "ulysses_plan_set_chunk_bytes",
            "ulysses_plan_set_max_ctas", "ulysses_plan_set_rope_pairs",
+           "ulysses_plan_set_rope_grid",
            "ulysses_plan_bytes", "ulysses_plan_num_chunks", "ulysses_plan_chunk_rows",
            "ulysses_plan_auto_engine", "ulysses_plan_set_fused_engine", "ulysses_plan_fused_kernel",
            "ulysses_plan_fused_backward_kernel",
@@ -69,6 +70,8 @@ def _lib():
         lib.ulysses_plan_set_chunk_bytes.argtypes = [_p, _i64]
         lib.ulysses_plan_set_max_ctas.argtypes = [_p, _i64]
         lib.ulysses_plan_set_rope_pairs.argtypes = [_p, ctypes.c_int]
+        lib.ulysses_plan_set_rope_grid.argtypes = [_p, ctypes.c_int, ctypes.POINTER(_i64),
+                                                   ctypes.POINTER(_i64), _i64]
         lib.ulysses_plan_bytes.argtypes = [_p, ctypes.c_int, ctypes.c_int, ctypes.POINTER(_i64),
                                            ctypes.POINTER(_i64)]
         lib.ulysses_plan_num_chunks.argtypes = [_p, ctypes.c_int, ctypes.POINTER(_i64)]
@@ -189,6 +192,18 @@ def ulysses_plan_set_chunk_bytes(plan: Plan, max_chunk_bytes: int):
 def ulysses_plan_set_rope_pairs(plan: Plan, pairs: int):
     """RoPE pair layout of the fused calls with this plan: ULY_ROPE_ADJACENT or ULY_ROPE_HALF."""
     _check(_lib().ulysses_plan_set_rope_pairs(plan, pairs), "ulysses_plan_set_rope_pairs")
+
+
+def ulysses_plan_set_rope_grid(plan: Plan, extents: Sequence[int], pairs: Sequence[int],
+                               first: int = 0):
+    """Position axes of the fused calls with this plan: a grid of `extents` (the last axis fastest)
+    along the sequence from index `first`, axis a turning pairs[a] of the d/2 RoPE pairs; tokens
+    outside the grid are not turned. Empty sequences: one axis, the sequence index."""
+    if len(extents) != len(pairs):
+        raise ValueError("one pair count per axis")
+    n = len(extents)
+    _check(_lib().ulysses_plan_set_rope_grid(plan, n, (_i64 * n)(*extents), (_i64 * n)(*pairs),
+                                             first), "ulysses_plan_set_rope_grid")
 
 
 def ulysses_plan_set_max_ctas(plan: Plan, max_ctas: int):

@@ -367,7 +367,7 @@ int fused_prepare(const Plan& p, const void* const* q_in, const void* const* k_i
     a->eps = eps;
     a->stages = stages;
     a->stage_bytes = stage_bytes;
-    rope_turns(p.d, double(rope_theta), a->turn_hi, a->turn_lo);
+    rope_turns(p, double(rope_theta), a->turn_hi, a->turn_lo, &a->grid);
     return ULY_OK;
 }
 
@@ -458,7 +458,7 @@ int fused_bwd_run(const Plan& p, FusedBwdArgs& a, const DeviceInfo& dev, int64_t
     a.group_major = fused_bwd_uses_group_major(p) ? 1 : 0;  // the same choice as the geometry's
     a.n_eq = int32_t(p.n[0]);
     a.run = uint32_t(p.n[0] * p.d * p.e);
-    rope_turns(p.d, double(rope_theta), a.turn_hi, a.turn_lo);
+    rope_turns(p, double(rope_theta), a.turn_hi, a.turn_lo, &a.grid);
     for (int64_t c = 0; c < C; ++c) {
         ChunkRows rows;
         chunk_rows(p, C, c, &rows);
@@ -844,6 +844,33 @@ int ulysses_plan_set_rope_pairs(ulysses_plan_t plan, int pairs)
 {
     if (!plan || (pairs != ULY_ROPE_ADJACENT && pairs != ULY_ROPE_HALF)) return ULY_EINVAL;
     plan->p.rope_half = pairs == ULY_ROPE_HALF ? 1 : 0;
+    return ULY_OK;
+}
+
+int ulysses_plan_set_rope_grid(ulysses_plan_t plan, int axes, const int64_t* extents,
+                               const int64_t* pairs, int64_t first)
+{
+    if (!plan || axes < 0 || axes > kMaxRopeAxes) return ULY_EINVAL;
+    Plan& p = plan->p;
+    if (axes == 0) {
+        p.rope_axes = 0;
+        return ULY_OK;
+    }
+    if (!extents || !pairs || first < 0) return ULY_EINVAL;
+    int64_t tokens = 1, turned = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (extents[a] < 1 || pairs[a] < 0 || pairs[a] > p.d / 2) return ULY_EINVAL;
+        if (extents[a] > p.S / tokens) return ULY_EINVAL;  // the grid must lie in the sequence
+        tokens *= extents[a];
+        turned += pairs[a];
+    }
+    if (turned > p.d / 2 || first > p.S - tokens) return ULY_EINVAL;
+    p.rope_axes = axes;
+    p.rope_first = first;
+    for (int a = 0; a < axes; ++a) {
+        p.rope_extent[a] = extents[a];
+        p.rope_pairs[a] = pairs[a];
+    }
     return ULY_OK;
 }
 

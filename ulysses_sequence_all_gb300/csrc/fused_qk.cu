@@ -200,7 +200,7 @@ __host__ __device__ inline FusedSmem fused_smem_layout(int d, int tokens, int st
 // (rt_layout_for: any multiple of 8 up to 256); F16: fp16 elements (else bf16); HALF_PAIRS:
 // rotate-half RoPE pairs (else adjacent pairs). The row layouts (G lanes per row, H packed slots
 // per lane) are in fused_row.cuh.
-template <int D, bool F16, bool HALF_PAIRS>
+template <int D, bool F16, bool HALF_PAIRS, bool GRID>
 __global__ void __launch_bounds__(kFusedThreads, kFusedCtasPerSm)
     fused_qk_kernel(const __grid_constant__ FusedArgs a)
 {
@@ -314,7 +314,9 @@ __global__ void __launch_bounds__(kFusedThreads, kFusedCtasPerSm)
             for (int e = lane; e < (v_unit ? 0 : t.ntok * HALF); e += 32) {
                 const int tok = e / HALF, jj = e % HALF;
                 const float2 tj = turns[jj];
-                const float2 cs = rope_cos_sin(p0 + float(tok), tj.x, tj.y);
+                const float pos = p0 + float(tok);
+                const float2 cs =
+                    rope_cos_sin(GRID ? rope_coord(a.grid, pos, jj) : pos, tj.x, tj.y);
                 const int at = IO::table_at(tok, jj, dims);
                 table[at] = cs.x;
                 table[at + 2] = cs.y;
@@ -523,31 +525,38 @@ void fused_geometry(const Plan& p, int planes, int64_t* tokens_per_unit, int* st
     }
 }
 
-template <int D, bool F16, bool HALF>
+template <int D, bool F16, bool HALF, bool GRID>
 static cudaError_t launch_d(const FusedArgs& a, cudaStream_t stream, int device, int grid)
 {
     static std::atomic<unsigned long long> raised{0};  // devices with this variant's limit raised
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
     if (bit && !(raised.load() & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(fused_qk_kernel<D, F16, HALF>,
+        cudaError_t e = cudaFuncSetAttribute(fused_qk_kernel<D, F16, HALF, GRID>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kSmemPerCtaMax);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit);
     }
     const FusedSmem m = fused_smem_layout(a.d, a.tokens_per_unit, a.stages, a.stage_bytes);
-    fused_qk_kernel<D, F16, HALF><<<grid, kFusedThreads, m.total, stream>>>(a);
+    fused_qk_kernel<D, F16, HALF, GRID><<<grid, kFusedThreads, m.total, stream>>>(a);
     return cudaGetLastError();
+}
+
+template <int D, bool GRID>
+static cudaError_t launch_grid(const FusedArgs& a, cudaStream_t stream, int device, int grid)
+{
+    if (a.elem_f16)
+        return a.rope_half ? launch_d<D, true, true, GRID>(a, stream, device, grid)
+                           : launch_d<D, true, false, GRID>(a, stream, device, grid);
+    return a.rope_half ? launch_d<D, false, true, GRID>(a, stream, device, grid)
+                       : launch_d<D, false, false, GRID>(a, stream, device, grid);
 }
 
 template <int D>
 static cudaError_t launch_variant(const FusedArgs& a, cudaStream_t stream, int device, int grid)
 {
-    if (a.elem_f16)
-        return a.rope_half ? launch_d<D, true, true>(a, stream, device, grid)
-                           : launch_d<D, true, false>(a, stream, device, grid);
-    return a.rope_half ? launch_d<D, false, true>(a, stream, device, grid)
-                       : launch_d<D, false, false>(a, stream, device, grid);
+    return a.grid.axes > 0 ? launch_grid<D, true>(a, stream, device, grid)
+                           : launch_grid<D, false>(a, stream, device, grid);
 }
 
 cudaError_t fused_launch(const FusedArgs& a, cudaStream_t stream, int device, int sm_count,

@@ -226,7 +226,7 @@ __host__ __device__ inline int bwd_dw_rows_per_warp(int d)
 // (rt_layout_for: any multiple of 8 up to 256); F16: fp16 elements (else bf16); HALF_PAIRS:
 // rotate-half RoPE pairs (else adjacent pairs). The row layouts (G lanes per row, H packed slots
 // per lane) are in fused_row.cuh.
-template <int D, bool F16, bool HALF_PAIRS, bool GM>
+template <int D, bool F16, bool HALF_PAIRS, bool GM, bool GRID>
 __global__ void __launch_bounds__(bwd_threads(GM),
                                   GM ? 1 : HALF_PAIRS ? kBwdCtasPerSmHalf : kBwdCtasPerSm)
     fused_qk_bwd_kernel(const __grid_constant__ FusedBwdArgs a)
@@ -362,7 +362,9 @@ __global__ void __launch_bounds__(bwd_threads(GM),
             for (int e = lane; e < (is_v ? 0 : t.ntok * HALF); e += 32) {
                 const int tok = e / HALF, jj = e % HALF;
                 const float2 tj = turns[jj];
-                const float2 cs = rope_cos_sin(p0 + float(tok), tj.x, tj.y);
+                const float pos = p0 + float(tok);
+                const float2 cs =
+                    rope_cos_sin(GRID ? rope_coord(a.grid, pos, jj) : pos, tj.x, tj.y);
                 const int at = IO::table_at(tok, jj, dims);
                 table[at] = cs.x;
                 table[at + 2] = cs.y;
@@ -705,13 +707,13 @@ void fused_bwd_geometry(const Plan& p, bool group_major, int64_t* tokens_per_uni
     }
 }
 
-template <int D, bool F16, bool HALF, bool GM>
+template <int D, bool F16, bool HALF, bool GM, bool GRID>
 static cudaError_t bwd_launch_d(const FusedBwdArgs& a, cudaStream_t stream, int device, int grid)
 {
     static std::atomic<unsigned long long> raised{0};  // devices with this variant's limit raised
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
     if (bit && !(raised.load() & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(fused_qk_bwd_kernel<D, F16, HALF, GM>,
+        cudaError_t e = cudaFuncSetAttribute(fused_qk_bwd_kernel<D, F16, HALF, GM, GRID>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kSmemPerCtaMax);
         if (e != cudaSuccess) return e;
@@ -720,26 +722,34 @@ static cudaError_t bwd_launch_d(const FusedBwdArgs& a, cudaStream_t stream, int 
     const BwdSmem m =
         bwd_smem_layout(a.d, a.tokens_per_unit, a.stages, a.stage_bytes,
                         bwd_warps(GM) * bwd_dw_rows_per_warp(a.d));
-    fused_qk_bwd_kernel<D, F16, HALF, GM><<<grid, bwd_threads(GM), m.total, stream>>>(a);
+    fused_qk_bwd_kernel<D, F16, HALF, GM, GRID><<<grid, bwd_threads(GM), m.total, stream>>>(a);
     return cudaGetLastError();
 }
 
-template <int D, bool F16, bool HALF>
+template <int D, bool F16, bool HALF, bool GRID>
 static cudaError_t bwd_launch_gm(const FusedBwdArgs& a, cudaStream_t stream, int device, int grid)
 {
-    return a.group_major ? bwd_launch_d<D, F16, HALF, true>(a, stream, device, grid)
-                         : bwd_launch_d<D, F16, HALF, false>(a, stream, device, grid);
+    return a.group_major ? bwd_launch_d<D, F16, HALF, true, GRID>(a, stream, device, grid)
+                         : bwd_launch_d<D, F16, HALF, false, GRID>(a, stream, device, grid);
+}
+
+template <int D, bool GRID>
+static cudaError_t bwd_launch_grid(const FusedBwdArgs& a, cudaStream_t stream, int device,
+                                      int grid)
+{
+    if (a.elem_f16)
+        return a.rope_half ? bwd_launch_gm<D, true, true, GRID>(a, stream, device, grid)
+                           : bwd_launch_gm<D, true, false, GRID>(a, stream, device, grid);
+    return a.rope_half ? bwd_launch_gm<D, false, true, GRID>(a, stream, device, grid)
+                       : bwd_launch_gm<D, false, false, GRID>(a, stream, device, grid);
 }
 
 template <int D>
 static cudaError_t bwd_launch_variant(const FusedBwdArgs& a, cudaStream_t stream, int device,
                                       int grid)
 {
-    if (a.elem_f16)
-        return a.rope_half ? bwd_launch_gm<D, true, true>(a, stream, device, grid)
-                           : bwd_launch_gm<D, true, false>(a, stream, device, grid);
-    return a.rope_half ? bwd_launch_gm<D, false, true>(a, stream, device, grid)
-                       : bwd_launch_gm<D, false, false>(a, stream, device, grid);
+    return a.grid.axes > 0 ? bwd_launch_grid<D, true>(a, stream, device, grid)
+                           : bwd_launch_grid<D, false>(a, stream, device, grid);
 }
 
 // CTAs of the main kernel for a launch of `a` (the number of partial-sum slots it fills); at

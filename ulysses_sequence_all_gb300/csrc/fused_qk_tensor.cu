@@ -99,6 +99,7 @@ struct FusedTensorArgs {
     float eps;
     float turn_hi[kMaxFusedD / 2];  // theta^(-2j/d) / (2 pi) as hi + lo, j < d/2
     float turn_lo[kMaxFusedD / 2];
+    RopeGrid grid;
 };
 
 struct FtRecord {
@@ -169,7 +170,7 @@ __device__ __forceinline__ bool ft_wait(uint64_t* bar, uint32_t parity)
 // D: head dimension, a power of two, or below 8 for a.d with one of the run-time row layouts of
 // fused_row.cuh (rt_layout_for: any multiple of 8 up to 256); F16: fp16 elements (else bf16);
 // HALF_PAIRS: rotate-half RoPE pairs.
-template <int D, bool F16, bool HALF_PAIRS>
+template <int D, bool F16, bool HALF_PAIRS, bool GRID>
 __global__ void __launch_bounds__(kFtThreads, ULY_FT_CTAS_PER_SM)
     fused_qk_tensor_kernel(const __grid_constant__ FusedTensorArgs a)
 {
@@ -328,7 +329,9 @@ __global__ void __launch_bounds__(kFtThreads, ULY_FT_CTAS_PER_SM)
             for (int e = ctid; e < nrows * HALF; e += NW * 32) {
                 const int tok = e / HALF, jj = e - tok * HALF;
                 const float2 tj = turns[jj];
-                const float2 cs = rope_cos_sin(p0 + float(tok), tj.x, tj.y);
+                const float pos = p0 + float(tok);
+                const float2 cs =
+                    rope_cos_sin(GRID ? rope_coord(a.grid, pos, jj) : pos, tj.x, tj.y);
                 const int at = IO::table_at(tok, jj, dims);
                 table[at] = cs.x;
                 table[at + 2] = cs.y;
@@ -436,32 +439,40 @@ bool fused_tensor_preferred(const Plan& p)
     return fused_tensor_fits(p) && p.N * p.d * p.e <= 10240;
 }
 
-template <int D, bool F16, bool HALF>
+template <int D, bool F16, bool HALF, bool GRID>
 static cudaError_t ft_launch_d(const FusedTensorArgs& a, int smem, cudaStream_t stream, int device,
                                int grid)
 {
     static std::atomic<unsigned long long> raised{0};  // devices with this variant's limit raised
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
     if (bit && !(raised.load() & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(fused_qk_tensor_kernel<D, F16, HALF>,
+        cudaError_t e = cudaFuncSetAttribute(fused_qk_tensor_kernel<D, F16, HALF, GRID>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kSmemPerCtaMax);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit);
     }
-    fused_qk_tensor_kernel<D, F16, HALF><<<grid, kFtThreads, smem, stream>>>(a);
+    fused_qk_tensor_kernel<D, F16, HALF, GRID><<<grid, kFtThreads, smem, stream>>>(a);
     return cudaGetLastError();
+}
+
+template <int D, bool GRID>
+static cudaError_t ft_launch_grid(const FusedTensorArgs& a, bool f16, bool half, int smem,
+                                     cudaStream_t stream, int device, int grid)
+{
+    if (f16)
+        return half ? ft_launch_d<D, true, true, GRID>(a, smem, stream, device, grid)
+                    : ft_launch_d<D, true, false, GRID>(a, smem, stream, device, grid);
+    return half ? ft_launch_d<D, false, true, GRID>(a, smem, stream, device, grid)
+                : ft_launch_d<D, false, false, GRID>(a, smem, stream, device, grid);
 }
 
 template <int D>
 static cudaError_t ft_launch_variant(const FusedTensorArgs& a, bool f16, bool half, int smem,
                                      cudaStream_t stream, int device, int grid)
 {
-    if (f16)
-        return half ? ft_launch_d<D, true, true>(a, smem, stream, device, grid)
-                    : ft_launch_d<D, true, false>(a, smem, stream, device, grid);
-    return half ? ft_launch_d<D, false, true>(a, smem, stream, device, grid)
-                : ft_launch_d<D, false, false>(a, smem, stream, device, grid);
+    return a.grid.axes > 0 ? ft_launch_grid<D, true>(a, f16, half, smem, stream, device, grid)
+                           : ft_launch_grid<D, false>(a, f16, half, smem, stream, device, grid);
 }
 
 // One launch over the given rows of every shard (the plan must fit: fused_tensor_fits). `f`
@@ -533,6 +544,7 @@ cudaError_t fused_tensor_launch(const Plan& p, const FusedArgs& f, const ChunkRo
     a.eps = f.eps;
     std::memcpy(a.turn_hi, f.turn_hi, sizeof a.turn_hi);
     std::memcpy(a.turn_lo, f.turn_lo, sizeof a.turn_lo);
+    a.grid = f.grid;
     int64_t total = 0, total2 = 0;
     for (int k = 0; k < kMaxW; ++k) {
         const bool live = k < W;

@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "plan.h"
 #include "ptx.cuh"
 
 namespace uly {
@@ -54,6 +55,30 @@ __device__ __forceinline__ float2 rope_cos_sin(float p, float hi, float lo)
     float s, c;
     sincospif(2.0f * f, &s, &c);
     return make_float2(c, s);
+}
+
+// Whole part of a / s for whole numbers 0 <= a < 2^24, 1 <= s < 2^24, with inv = 1 / s rounded:
+// the product is within one of the quotient, and the remainder, exact in an fma, puts it right.
+__device__ __forceinline__ float whole_div(float a, float s, float inv)
+{
+    float q = floorf(a * inv);
+    const float r = fmaf(-q, s, a);
+    if (r < 0.0f) q -= 1.0f;
+    if (r >= s) q += 1.0f;
+    return q;
+}
+
+// The position that turns pair jj of the token at sequence index p: its coordinate on the axis
+// the pair belongs to, 0 (no turn) for a token outside the grid.
+__device__ __forceinline__ float rope_coord(const RopeGrid& g, float p, int jj)
+{
+    const float o = p - g.first;
+    if (!(o >= 0.0f && o < g.total)) return 0.0f;
+    int a = 0;
+#pragma unroll
+    for (int k = 0; k < kMaxRopeAxes - 1; ++k) a += jj >= g.pair_end[k] ? 1 : 0;
+    const float q = whole_div(o, g.stride[a], g.inv_stride[a]);
+    return fmaf(-g.extent[a], whole_div(q, g.extent[a], g.inv_extent[a]), q);
 }
 
 template <bool F16>

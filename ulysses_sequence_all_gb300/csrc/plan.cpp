@@ -263,15 +263,39 @@ void build_fused_bwd_units(const Plan& p, const ChunkRows& rows, int64_t tokens_
 
 // theta^(-2j/d) expressed in turns (divided by 2 pi), split into a float pair whose sum carries
 // about 48 significant bits, so that p * turn can be reduced modulo 1 exactly enough in fp32.
-void rope_turns(int64_t d, double theta, float* turn_hi, float* turn_lo)
+void rope_turns(const Plan& p, double theta, float* turn_hi, float* turn_lo, RopeGrid* grid)
 {
     const double two_pi = 6.283185307179586476925286766559;
-    for (int64_t j = 0; j < d / 2; ++j) {
-        const double t = std::pow(theta, -2.0 * double(j) / double(d)) / two_pi;
-        const float hi = float(t);
-        turn_hi[j] = hi;
-        turn_lo[j] = float(t - double(hi));
+    const int64_t half = p.d / 2;
+    *grid = RopeGrid{};
+    grid->axes = p.rope_axes;
+    int64_t total = 1;
+    for (int a = 0; a < p.rope_axes; ++a) total *= p.rope_extent[a];
+    grid->first = float(p.rope_first);
+    grid->total = float(total);
+    // Pair i of an axis with m pairs turns by coordinate * theta^(-i/m): the ladder of a head of
+    // 2m columns. One axis of d/2 pairs is the usual theta^(-2j/d); pairs left over do not turn.
+    int64_t j = 0, stride = total;
+    for (int a = 0; a < kMaxRopeAxes; ++a) {
+        const int last = p.rope_axes > 0 ? p.rope_axes - 1 : 0;
+        const int64_t m = p.rope_axes == 0 ? (a == 0 ? half : 0) : (a <= last ? p.rope_pairs[a] : 0);
+        for (int64_t i = 0; i < m; ++i, ++j) {
+            const double t = std::pow(theta, -double(i) / double(m)) / two_pi;
+            const float hi = float(t);
+            turn_hi[j] = hi;
+            turn_lo[j] = float(t - double(hi));
+        }
+        if (p.rope_axes > 0) {
+            if (a <= last) stride /= p.rope_extent[a];
+            const int64_t ext = p.rope_extent[a <= last ? a : last];
+            grid->pair_end[a] = a < last ? int32_t(j) : int32_t(half);
+            grid->stride[a] = float(stride);
+            grid->extent[a] = float(ext);
+            grid->inv_stride[a] = float(1.0 / double(stride));
+            grid->inv_extent[a] = float(1.0 / double(ext));
+        }
     }
+    for (; j < half; ++j) turn_hi[j] = turn_lo[j] = 0.0f;
 }
 
 }  // namespace uly

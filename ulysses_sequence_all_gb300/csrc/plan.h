@@ -10,6 +10,7 @@ namespace uly {
 constexpr int kMaxW = 8;
 constexpr int kMaxSeg = kMaxW * kMaxW;
 constexpr int kMaxFusedD = 256;
+constexpr int kMaxRopeAxes = 4;
 
 struct Plan {
     int W;
@@ -21,6 +22,12 @@ struct Plan {
     int64_t chunk_cap;  // max bytes one rank reads or writes per launch
     int64_t max_ctas;   // cap on the CTAs of any launch (0: none)
     int rope_half;      // the fused calls' RoPE pairs: (j, j + d/2) when set, else (2j, 2j + 1)
+    // Position axes of the fused calls' RoPE (0: one axis, the global sequence index): the grid
+    // rope_extent[0] x ... (the last axis fastest) covers sequence indices rope_first onwards, and
+    // axis a turns rope_pairs[a] of the d/2 pairs.
+    int rope_axes;
+    int64_t rope_extent[kMaxRopeAxes], rope_pairs[kMaxRopeAxes];
+    int64_t rope_first;
     int fused_engine;   // the fused forward's kernel: ULY_ENGINE_AUTO, _TMA (token units), _TENSOR
 };
 
@@ -93,6 +100,18 @@ struct RowRing {
 
 void build_row_tiles(const Plan& p, const ChunkRows& rows, int64_t tile_rows, RowTileArgs* a);
 
+// Position axes as the fused kernels take them (axes = 0: one axis, the sequence index). Axis a
+// of the token at grid index o = p - first is (o / stride[a]) mod extent[a] and turns pairs
+// pair_end[a - 1] .. pair_end[a] - 1. Every number is a whole number below 2^24, exact in fp32;
+// axes past the last repeat it, so a pair index always finds one.
+struct RopeGrid {
+    int32_t axes;
+    int32_t pair_end[kMaxRopeAxes];
+    float first, total;  // tokens first .. first + total - 1 lie on the grid, others are not turned
+    float stride[kMaxRopeAxes], extent[kMaxRopeAxes];
+    float inv_stride[kMaxRopeAxes], inv_extent[kMaxRopeAxes];
+};
+
 // ---- fused QK kernel's argument block ---------------------------------------------------------
 // Work is cut into blocks of `block_tokens` consecutive source rows (tokens) of one shard q and one
 // batch index, and each block into `units_per_block` work units:
@@ -136,6 +155,7 @@ struct FusedArgs {
     // theta^(-2j/d) / (2 pi) as an unevaluated sum hi + lo of two floats, j < d/2.
     float turn_hi[kMaxFusedD / 2];
     float turn_lo[kMaxFusedD / 2];
+    RopeGrid grid;
 };
 static_assert(sizeof(FusedArgs) <= 4096, "kernel parameter block");
 
@@ -175,6 +195,7 @@ struct FusedBwdArgs {
     float eps;
     float turn_hi[kMaxFusedD / 2];
     float turn_lo[kMaxFusedD / 2];
+    RopeGrid grid;
     // Row blocks (equal head groups): a unit's forward input arrives with one 4-D tensor-map copy
     // that lands it grouped by head group, [group][row][run], and its gradient with one copy per
     // rank in the same order (see encode_group_map).
@@ -188,7 +209,8 @@ static_assert(sizeof(FusedBwdArgs) <= 32764, "kernel parameter block");
 
 void build_fused_bwd_units(const Plan& p, const ChunkRows& rows, int64_t tokens_per_unit,
                            FusedBwdArgs* a);
-void rope_turns(int64_t d, double theta, float* turn_hi, float* turn_lo);
+// The RoPE turns of every pair and the position axes of the plan's fused calls.
+void rope_turns(const Plan& p, double theta, float* turn_hi, float* turn_lo, RopeGrid* grid);
 
 }  // namespace uly
 
