@@ -426,6 +426,40 @@ int ulysses_a2a_4d_packed_fused_backward(ulysses_plan_t plan, int planes, int q_
                                          size_t workspace_bytes, void* stream);
 
 /*
+ * Attention of every rank's heads over the whole sequence, between the two relayouts
+ * (fast-ulysses 0.2.1, README, "Quick start": a sequence-parallel attention block), for all W ranks
+ * in one call. Per rank r, on the head-side tensors that mode 0 writes:
+ *   q  (b, Sq, n_r, d)  queries of q_plan's head_splits n_r and S = Sq
+ *   k, v  (b, Skv, m_r, d)  keys and values of kv_plan's head_splits m_r and S = Skv
+ *   o  (b, Sq, n_r, d)  out: o_i = sum_j softmax_j(scale q_i . k_j) v_j, rounded once
+ *   lse  (b, n_r, Sq)  out, fp32: log sum_j exp(scale q_i . k_j), for the backward
+ * Only the totals Sq, Skv of the plans' seq_splits matter here. The plans have the same W, b, d
+ * (a multiple of 8, at most 128) and dtype (ULY_BF16 or ULY_F16); every rank has n_r = g m_r with
+ * one g <= 64: query head h reads key head h / g (shared key heads). Sq, Skv < 2^31 - 256.
+ *   kv_lens  NULL, or b device int32: batch element bb holds keys 0 .. kv_lens[bb] - 1 (clamped to
+ *            [0, Skv]), a padded batch or a cache with room left. What k and v hold past them is
+ *            not used, whatever it is.
+ *   causal   1: query i sees keys j <= q_start[bb] + i only; 0: every key.
+ *   q_start  NULL (zeros), or b device int32 (causal only): the position of the first query, such
+ *            as the keys already in a cache; negative values hide every key from the first rows.
+ * A row that sees no key gives o = 0 and lse = -infinity. Keys hidden from some rows only (causal)
+ * must be finite. scale > 0, finite. Products run on the tensor cores in 16 bits (the
+ * probabilities are rounded to the element type for the second one), maxima and sums in fp32.
+ * workspace  device memory of ulysses_attention_workspace bytes (0: may be NULL), 16-byte aligned:
+ *            partial results where few query rows leave the keys to be split over the SMs. Its
+ *            content does not matter and is not kept.
+ * The result does not depend on timing. q_plan's CTA cap holds for the launch.
+ * ULY_EINVAL, ULY_EALIGN (kv_lens and q_start: 4 bytes) and ULY_EOVERLAP as for the other calls.
+ */
+int ulysses_attention(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, const void* const* q,
+                      const void* const* k, const void* const* v, void* const* o,
+                      float* const* lse, const int32_t* kv_lens, const int32_t* q_start, int causal,
+                      float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ulysses_attention for these plans on the current device. */
+int ulysses_attention_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, size_t* bytes);
+
+/*
  * End-to-end form for host-resident data: copy each rank's input from host_in[k] to dev_in[k],
  * run the relayout, and copy each dev_out[k] back to host_out[k]. The work is cut into about
  * eight ranges of the global sequence (within the chunk cap) so that copies in and copies out

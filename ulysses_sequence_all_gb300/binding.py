@@ -37,6 +37,7 @@ EXPORTS = ["ulysses_plan", "ulysses_plan_destroy", "ulysses_plan_set_chunk_bytes
            "ulysses_a2a_4d_qk_fused_backward",
            "ulysses_qk_fused_backward_workspace", "ulysses_a2a_4d_qk_fused_backward_static",
            "ulysses_a2a_4d_qkv_fused_backward", "ulysses_a2a_4d_packed_fused_backward",
+           "ulysses_attention", "ulysses_attention_workspace",
            "ulysses_a2a_4d_host", "ulysses_a2a_4d_qk_fused_host", "ulysses_device_status",
            "ulysses_selftest_wait_timeout", "ulysses_last_cuda_error", "ulysses_strerror",
            "ulysses_version"]
@@ -105,6 +106,9 @@ def _lib():
         lib.ulysses_a2a_4d_qk_fused_backward_static.argtypes = [_p, _pp, _pp, _pp, _pp, _pp, _pp,
                                                                 _p, _p, ctypes.c_float,
                                                                 ctypes.c_float, _p]
+        lib.ulysses_attention.argtypes = [_p, _p, _pp, _pp, _pp, _pp, _pp, _p, _p, ctypes.c_int,
+                                          ctypes.c_float, _p, ctypes.c_size_t, _p]
+        lib.ulysses_attention_workspace.argtypes = [_p, _p, ctypes.POINTER(ctypes.c_size_t)]
         lib.ulysses_a2a_4d_host.argtypes = [_p, ctypes.c_int, _pp, _pp, _pp, _pp, _p]
         lib.ulysses_a2a_4d_qk_fused_host.argtypes = [_p, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _p,
                                                      ctypes.c_float, ctypes.c_float, _p]
@@ -359,6 +363,27 @@ def ulysses_a2a_4d_qk_fused_backward_static(plan: Plan, dq_out, dk_out, q_in, k_
         plan, _ptrs(dq_out), _ptrs(dk_out), _ptrs(q_in), _ptrs(k_in), _ptrs(dq_in), _ptrs(dk_in),
         _addr(rms_w), _addr(dw), eps, rope_theta, _stream(stream)),
         "ulysses_a2a_4d_qk_fused_backward_static")
+
+
+def ulysses_attention_workspace(q_plan: Plan, kv_plan: Plan) -> int:
+    """Workspace bytes ulysses_attention needs for these plans on the current device (often 0)."""
+    n = ctypes.c_size_t()
+    _check(_lib().ulysses_attention_workspace(q_plan, kv_plan, ctypes.byref(n)),
+           "ulysses_attention_workspace")
+    return n.value
+
+
+def ulysses_attention(q_plan: Plan, kv_plan: Plan, q, k, v, out, lse, scale: float,
+                      causal: bool = False, kv_lens=None, q_start=None, workspace=None,
+                      stream=None):
+    """Attention of every rank's heads over the whole sequence: per rank q, out (b, Sq, n_r, d),
+    k, v (b, Skv, m_r, d), lse (b, n_r, Sq) fp32. kv_lens, q_start: int32 device tensors of b
+    entries or None. `workspace` is a device tensor of at least
+    ulysses_attention_workspace(q_plan, kv_plan) bytes (None where that is 0)."""
+    _check(_lib().ulysses_attention(q_plan, kv_plan, _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out),
+                                    _ptrs(lse), _addr(kv_lens), _addr(q_start), int(causal), scale,
+                                    _addr(workspace), _nbytes(workspace), _stream(stream)),
+           "ulysses_attention")
 
 
 def ulysses_a2a_4d_host(plan: Plan, mode: int, host_in, host_out, dev_in, dev_out, stream=None):

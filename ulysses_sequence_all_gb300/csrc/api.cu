@@ -11,6 +11,7 @@
 #include <new>
 
 #include "../../include/ulysses.h"
+#include "attention.h"
 #include "plan.h"
 #include "tensor_map.h"
 
@@ -808,6 +809,146 @@ int run_host_pipe(const Plan& p, const PipeChunks& pc, HostPipe* hp, cudaStream_
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
 
+// ---- attention ----------------------------------------------------------------------------------
+// What the two plans of an attention call make together, or ULY_EINVAL.
+int attn_shape(const Plan& qp, const Plan& kp, AttnShape* s)
+{
+    if (qp.dtype != kp.dtype || (qp.dtype != ULY_BF16 && qp.dtype != ULY_F16)) return ULY_EINVAL;
+    if (qp.W != kp.W || qp.b != kp.b || qp.d != kp.d || qp.d > kAttnMaxD) return ULY_EINVAL;
+    const int64_t lim = int64_t(1) << 31;  // tensor-map coordinates; lse rows in 64 bits
+    if (qp.S >= lim - 2 * kAttnRows || kp.S >= lim - 2 * kAttnRows || qp.b * kp.N >= lim)
+        return ULY_EINVAL;
+    if (kp.N == 0 || qp.N % kp.N != 0) return ULY_EINVAL;
+    const int64_t group = qp.N / kp.N;
+    if (group > kAttnMaxGroup) return ULY_EINVAL;
+    std::memset(s, 0, sizeof *s);
+    s->W = qp.W;
+    s->b = int32_t(qp.b);
+    s->d = int32_t(qp.d);
+    s->f16 = qp.dtype == ULY_F16 ? 1 : 0;
+    s->Sq = qp.S;
+    s->Skv = kp.S;
+    s->group = int32_t(group);
+    int64_t heads = 0, rows = 0;
+    for (int r = 0; r < qp.W; ++r) {
+        if (qp.n[r] != group * kp.n[r]) return ULY_EINVAL;  // a rank holds the keys of its queries
+        s->n[r] = int32_t(qp.n[r]);
+        s->m[r] = int32_t(kp.n[r]);
+        s->head_begin[r] = int32_t(heads);
+        s->row_begin[r] = rows;
+        heads += qp.b * kp.n[r];
+        rows += qp.b * qp.n[r] * qp.S;
+    }
+    for (int r = qp.W; r <= kMaxW; ++r) {
+        s->head_begin[r] = int32_t(heads);
+        s->row_begin[r] = rows;
+    }
+    return ULY_OK;
+}
+
+int attn_grid(const Plan& p, const DeviceInfo& dev)
+{
+    return p.max_ctas > 0 && p.max_ctas < dev.sm_count ? int(p.max_ctas) : dev.sm_count;
+}
+
+// Tiles and splits of a forward call, and the bytes of its partial results (0 without splits).
+size_t attn_fwd_setup(const Plan& qp, const DeviceInfo& dev, AttnFwdArgs* a)
+{
+    const AttnShape& s = a->s;
+    a->tile_tokens = kAttnRows / s.group;
+    const int64_t pair = 2 * int64_t(a->tile_tokens);
+    a->q_blocks = (s.Sq + pair - 1) / pair;
+    const int64_t units = s.head_begin[s.W] * a->q_blocks;
+    a->splits = attn_fwd_splits(s, units, attn_grid(qp, dev));
+    a->units = units * a->splits;
+    if (a->splits == 1) return 0;
+    const size_t rows = size_t(s.row_begin[s.W]);
+    return size_t(a->splits) * ((rows * size_t(s.d) + rows) * sizeof(float));
+}
+
+// Masks and scale of an attention call.
+int attn_masks(AttnShape* s, float scale, int causal, const int32_t* kv_lens, const int32_t* q_start)
+{
+    if (!(scale > 0.0f) || !(scale <= 3.0e38f) || (causal != 0 && causal != 1)) return ULY_EINVAL;
+    if (q_start && !causal) return ULY_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(kv_lens) | reinterpret_cast<uintptr_t>(q_start)) & 3u)
+        return ULY_EALIGN;
+    s->scale = scale;
+    s->causal = causal;
+    s->kv_lens = kv_lens;
+    s->q_start = q_start;
+    return ULY_OK;
+}
+
+// Pointers and byte counts gathered for the overlap check of an attention call.
+struct RangeList {
+    const void* p[8 * kMaxW + 4];
+    int64_t n[8 * kMaxW + 4];
+    int count = 0;
+    void add(const void* ptr, int64_t bytes)
+    {
+        p[count] = ptr;
+        n[count++] = ptr ? bytes : 0;
+    }
+    int add_ranks(const void* const* ptrs, const int64_t* bytes, int W)
+    {
+        const int rc = check_ptrs(ptrs, bytes, W);
+        if (rc) return rc;
+        for (int r = 0; r < W; ++r) add(ptrs[r], bytes[r]);
+        return ULY_OK;
+    }
+};
+
+void attn_bytes(const Plan& qp, const Plan& kp, int64_t* q_b, int64_t* kv_b, int64_t* lse_b)
+{
+    for (int r = 0; r < qp.W; ++r) {
+        q_b[r] = head_side_bytes(qp, r);
+        kv_b[r] = head_side_bytes(kp, r);
+        lse_b[r] = qp.b * qp.n[r] * qp.S * int64_t(sizeof(float));
+    }
+}
+
+int attn_fwd_device(const Plan& qp, const Plan& kp, const void* const* q, const void* const* k,
+                    const void* const* v, void* const* o, float* const* lse,
+                    const int32_t* kv_lens, const int32_t* q_start, int causal, float scale,
+                    void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    AttnFwdArgs a;
+    std::memset(&a, 0, sizeof a);
+    int rc = attn_shape(qp, kp, &a.s);
+    if (rc) return rc;
+    if ((rc = attn_masks(&a.s, scale, causal, kv_lens, q_start))) return rc;
+    const int W = qp.W;
+    int64_t q_b[kMaxW], kv_b[kMaxW], lse_b[kMaxW];
+    attn_bytes(qp, kp, q_b, kv_b, lse_b);
+    RangeList ins, outs;
+    if ((rc = ins.add_ranks(q, q_b, W)) || (rc = ins.add_ranks(k, kv_b, W)) ||
+        (rc = ins.add_ranks(v, kv_b, W)) ||
+        (rc = outs.add_ranks(const_cast<const void* const*>(o), q_b, W)) ||
+        (rc = outs.add_ranks(reinterpret_cast<const void* const*>(lse), lse_b, W)))
+        return rc;
+    ins.add(kv_lens, qp.b * 4);
+    ins.add(q_start, qp.b * 4);
+    if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
+    DeviceInfo dev;
+    if ((rc = current_device(&dev))) return rc;
+    const size_t need = attn_fwd_setup(qp, dev, &a);
+    if (need) {
+        if (!workspace || workspace_bytes < need) return ULY_EINVAL;
+        if (!aligned16(workspace)) return ULY_EALIGN;
+        outs.add(workspace, int64_t(need));
+        a.part_o = static_cast<float*>(workspace);
+        if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
+        a.part_lse = a.part_o + size_t(a.splits) * size_t(a.s.row_begin[W]) * size_t(a.s.d);
+    }
+    for (int r = 0; r < W; ++r) {
+        a.o[r] = static_cast<uint8_t*>(o[r]);
+        a.lse[r] = lse[r];
+    }
+    const cudaError_t e = attn_fwd_launch(a, q, k, v, stream, dev.device, attn_grid(qp, dev));
+    return e == cudaSuccess ? ULY_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1108,6 +1249,28 @@ int ulysses_a2a_4d_packed_fused(ulysses_plan_t plan, int planes, int q_plane, in
                         static_cast<cudaStream_t>(stream));
 }
 
+int ulysses_attention_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, size_t* bytes)
+{
+    if (!q_plan || !kv_plan || !bytes) return ULY_EINVAL;
+    AttnFwdArgs a;
+    std::memset(&a, 0, sizeof a);
+    DeviceInfo dev;
+    int rc = attn_shape(q_plan->p, kv_plan->p, &a.s);
+    if (rc || (rc = current_device(&dev))) return rc;
+    *bytes = attn_fwd_setup(q_plan->p, dev, &a);
+    return ULY_OK;
+}
+
+int ulysses_attention(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, const void* const* q,
+                      const void* const* k, const void* const* v, void* const* o,
+                      float* const* lse, const int32_t* kv_lens, const int32_t* q_start, int causal,
+                      float scale, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!q_plan || !kv_plan) return ULY_EINVAL;
+    return attn_fwd_device(q_plan->p, kv_plan->p, q, k, v, o, lse, kv_lens, q_start, causal, scale,
+                           workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
 int ulysses_a2a_4d_host(ulysses_plan_t plan, int mode, const void* const* host_in,
                         void* const* host_out, void* const* dev_in, void* const* dev_out, void* stream)
 {
@@ -1201,12 +1364,13 @@ int ulysses_device_status(unsigned* status)
     if (!status) return ULY_EINVAL;
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e);
-    unsigned a = 0, b = 0, c = 0, t = 0;
+    unsigned a = 0, b = 0, c = 0, t = 0, f = 0;
     if ((e = relayout_status(&a, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = fused_status(&b, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = fused_bwd_status(&c, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = fused_tensor_status(&t, true)) != cudaSuccess) return cuda_fail(e);
-    *status = a | b | c | t;
+    if ((e = attn_fwd_status(&f, true)) != cudaSuccess) return cuda_fail(e);
+    *status = a | b | c | t | f;
     return *status ? ULY_EDEVICE : ULY_OK;
 }
 

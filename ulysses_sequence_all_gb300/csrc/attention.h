@@ -1,0 +1,55 @@
+// attention.h -- argument blocks of the attention kernels, shared by api.cu and attention_*.cu.
+//
+// All W ranks' heads run in one launch. Queries (b, Sq, n_r, d) and keys, values (b, Skv, m_r, d)
+// are the head-side tensors that mode 0 writes; `group` = n_r / m_r query heads share a key head.
+// A row tile is 128 rows of one (rank, batch element, key head): `tile_tokens` = 128 / group tokens
+// with their `group` heads each, row = token * group + head, so that shared heads read their keys
+// once. Rows past tile_tokens * group are computed on whatever lies there and never stored.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "plan.h"
+
+namespace uly {
+
+constexpr int kAttnMaxD = 128;
+constexpr int kAttnMaxGroup = 64;  // query heads that share a key head
+constexpr int kAttnRows = 128;     // rows of a query tile, and keys of a block
+
+// What every attention kernel needs to know of the call.
+struct AttnShape {
+    int64_t Sq, Skv;
+    int32_t W, b, d, f16;
+    int32_t group;
+    int32_t n[kMaxW], m[kMaxW];      // query and key heads of each rank
+    int32_t head_begin[kMaxW + 1];   // prefix of b * m_r over the ranks: (rank, batch, key head)
+    int64_t row_begin[kMaxW + 1];    // prefix of b * n_r * Sq: rows of the log-sum-exp arrays
+    const int32_t* kv_lens;          // (b) or null: keys of each batch element, clamped to [0, Skv]
+    const int32_t* q_start;          // (b) or null (zeros): position of the first query, causal only
+    int32_t causal;
+    float scale;
+};
+
+struct AttnFwdArgs {
+    AttnShape s;
+    CUtensorMap qmap[kMaxW], kmap[kMaxW], vmap[kMaxW], omap[kMaxW];
+    uint8_t* o[kMaxW];
+    float* lse[kMaxW];  // (b, n_r, Sq)
+    int32_t tile_tokens;
+    int64_t q_blocks;   // pairs of row tiles along the tokens
+    int64_t units;      // (rank, batch, key head) x q_blocks x splits
+    int32_t splits;     // parts of the keys, joined by a second kernel
+    float* part_o;      // [splits][rows][d] normalised partial outputs, splits > 1
+    float* part_lse;    // [splits][rows]
+};
+
+// Host side.
+int attn_fwd_splits(const AttnShape& s, int64_t units, int sm_count);
+cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
+                            const void* const* v, cudaStream_t stream, int device, int grid);
+cudaError_t attn_fwd_status(unsigned* status, bool clear);
+
+}  // namespace uly

@@ -586,6 +586,22 @@ bool encode_group_map(CUtensorMap* map, const void* base, int64_t run, int64_t r
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_head_map(CUtensorMap* map, const void* base, bool f16, int64_t d, int64_t n, int64_t S,
+                     int64_t b, int64_t box_heads, int64_t box_rows)
+{
+    EncodeTiledFn encode = encode_tiled_fn();
+    if (!encode) return false;
+    const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(n), cuuint64_t(S), cuuint64_t(b)};
+    const cuuint64_t strides[3] = {cuuint64_t(d * 2), cuuint64_t(n * d * 2), cuuint64_t(S * n * d * 2)};
+    const cuuint32_t boxdim[4] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows), 1};
+    const cuuint32_t estrides[4] = {1, 1, 1, 1};
+    return encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, boxdim, estrides,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int MODE, int K, int UNIT, int L>
 static cudaError_t tensor_launch_shape(const TensorArgs& a, unsigned grid, cudaStream_t stream,
                                        int device)

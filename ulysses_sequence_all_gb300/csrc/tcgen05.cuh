@@ -1,0 +1,174 @@
+// tcgen05.cuh -- inline-PTX wrappers of sm_103a's fifth-generation tensor cores as the attention
+// kernels use them: tensor memory, matrix products of 16-bit elements into fp32, their operand
+// descriptors, and moves between tensor memory and registers.
+//
+// Tensor memory has 128 lanes (accumulator rows) of 512 32-bit columns an SM; an address holds
+// the lane in its upper half and the column in its lower one, and warp w of a warpgroup reaches
+// lanes 32 w .. 32 w + 31 only. Operands in shared memory are tiles of 64 elements (128 bytes) by
+// any number of rows, as a tensor map with the 128-byte swizzle lands them: the 16-byte word c of
+// row r sits at word c ^ (r mod 8) of that row, tiles start on 1,024-byte boundaries.
+#pragma once
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace uly {
+
+constexpr int kTmemColumns = 512;
+
+// One warp allocates all of an SM's tensor memory; the base address arrives in shared memory.
+__device__ __forceinline__ void tmem_alloc(uint32_t* where)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(where)),
+                 "n"(kTmemColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t base)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base),
+                 "n"(kTmemColumns)
+                 : "memory");
+}
+
+// Order this thread's tensor-memory work before (after) a barrier that it passes next (has passed).
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// An arrival on `bar` once every product this thread has issued so far is complete.
+__device__ __forceinline__ void tc_commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+
+// Instruction descriptor: fp32 accumulator of 128 rows x n columns, A and B both bf16 or both
+// fp16; b_mn: B's rows in shared memory run along K (its columns, N, are contiguous).
+__host__ __device__ constexpr uint32_t tc_idesc(bool f16, int n, bool b_mn)
+{
+    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) |
+           (uint32_t(n >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+}
+
+constexpr uint64_t kDescSwizzle128 = (uint64_t(2) << 61) | (uint64_t(1) << 46);
+
+// Shared-memory operand whose rows are contiguous along K (64 elements a tile row): eight rows
+// every 1,024 bytes. A step of 16 elements along K is 32 bytes, four steps a tile.
+__device__ __forceinline__ uint64_t tc_desc_k(uint32_t addr)
+{
+    return kDescSwizzle128 | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 16) |
+           uint64_t((addr >> 4) & 0x3FFF);
+}
+
+// Shared-memory operand whose rows run along K: 64 columns of N contiguous, the next 64 at
+// `tile_bytes`; eight rows of K every 1,024 bytes. A step of 16 along K is 2,048 bytes.
+__device__ __forceinline__ uint64_t tc_desc_mn(uint32_t addr, uint32_t tile_bytes)
+{
+    return kDescSwizzle128 | (uint64_t(1024 >> 4) << 32) | (uint64_t(tile_bytes >> 4) << 16) |
+           uint64_t((addr >> 4) & 0x3FFF);
+}
+
+// D[tmem] (+)= A[smem] B[smem], one step of 16 along K, by one thread.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// The same with A in tensor memory (two 16-bit elements a column: 8 columns a step).
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          bool accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+// 32 consecutive columns of this thread's lane. The values are there after tmem_wait_ld, which
+// takes the registers so that no use of them moves ahead of it.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 2^x (subnormal results flushed to zero).
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A wait inside a CTA whose warps give up together: false once the phase did not complete within
+// the time limit, or once another warp of the CTA has given up (*dead).
+__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, volatile int* dead)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*dead) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+}  // namespace uly

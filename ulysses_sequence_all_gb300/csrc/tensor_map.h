@@ -25,4 +25,11 @@ bool encode_run_map(CUtensorMap* map, const void* base, int64_t run, int64_t row
 bool encode_group_map(CUtensorMap* map, const void* base, int64_t run, int64_t rows, int64_t W,
                       int64_t b, int64_t row_stride, int64_t batch_stride, int64_t box_rows);
 
+// A 4-D map over a head-side tensor (b, S, n, d) of 16-bit elements (fp16 or bf16): columns x
+// heads x rows x batch, boxes of 64 columns x box_heads x box_rows x 1 that land as box_rows *
+// box_heads rows of 128 bytes with the 128-byte swizzle (the layout of tcgen05.cuh). Columns past d
+// and rows past S read as zeros and are not written. box_heads and box_rows 1..256.
+bool encode_head_map(CUtensorMap* map, const void* base, bool f16, int64_t d, int64_t n, int64_t S,
+                     int64_t b, int64_t box_heads, int64_t box_rows);
+
 }  // namespace uly
