@@ -460,6 +460,32 @@ int ulysses_attention(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, const void*
 int ulysses_attention_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, size_t* bytes);
 
 /*
+ * Gradient of ulysses_attention (fast-ulysses 0.2.1, README, "Quick start": the block runs forward
+ * and backward), with the probabilities recomputed from the forward's lse. With P the probabilities,
+ * D_i = go_i . o_i and dS = P (go v^T - D):
+ *   dv = P^T go,  dk = scale dS^T q,  dq = scale dS k
+ * summed over the query heads of a shared key head, each rounded once. dq, dk, dv are shaped as q,
+ * k, v and written whole: keys that no row sees and rows that see no key get zeros. The plans,
+ * masks and scale are the forward's, o and lse its outputs, go the gradient of o; rows with
+ * lse = -infinity have no gradient. P and dS are rounded to the element type for their products,
+ * the sums are fp32 and in a fixed order: the same bits from run to run.
+ * workspace: device memory of ulysses_attention_backward_workspace bytes, 16-byte aligned; its
+ * content does not matter and is not kept.
+ * Three launches on `stream`; q_plan's CTA cap holds for the two that compute. Statuses as the
+ * forward's.
+ */
+int ulysses_attention_backward(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, void* const* dq,
+                               void* const* dk, void* const* dv, const void* const* q,
+                               const void* const* k, const void* const* v, const void* const* o,
+                               const float* const* lse, const void* const* go,
+                               const int32_t* kv_lens, const int32_t* q_start, int causal,
+                               float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ulysses_attention_backward for these plans (no CUDA call). */
+int ulysses_attention_backward_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan,
+                                         size_t* bytes);
+
+/*
  * End-to-end form for host-resident data: copy each rank's input from host_in[k] to dev_in[k],
  * run the relayout, and copy each dev_out[k] back to host_out[k]. The work is cut into about
  * eight ranges of the global sequence (within the chunk cap) so that copies in and copies out

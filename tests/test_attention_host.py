@@ -89,3 +89,46 @@ def test_null_plans_and_workspace_query():
     assert lib.ulysses_attention_workspace(qp, kp, None) == B.ULY_EINVAL
     assert lib.ulysses_attention(qp, kp, None, ptrs, ptrs, ptrs, ptrs, None, None, 0, 0.125, None, 0,
                                  None) == B.ULY_EINVAL
+
+
+def backward_status(qp, kp, **kw):
+    """The same for the backward, with a workspace that is long enough unless overridden."""
+    import ctypes
+    at = {name: [(16 * i + 1) * MB]
+          for i, name in enumerate(("q", "k", "v", "o", "lse", "go", "dq", "dk", "dv"))}
+    a = dict(at, scale=0.125, causal=0, kv_lens=0, q_start=0, ws=200 * MB,
+             ws_bytes=B.ulysses_attention_backward_workspace(qp, kp))
+    a.update(kw)
+    ptr = lambda x: None if a[x] is None else B._ptrs(a[x])
+    return B.library().ulysses_attention_backward(
+        qp, kp, *map(ptr, ("dq", "dk", "dv", "q", "k", "v", "o", "lse", "go")),
+        ctypes.c_void_p(a["kv_lens"]), ctypes.c_void_p(a["q_start"]), a["causal"], a["scale"],
+        ctypes.c_void_p(a["ws"]), a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({"scale": 0.0}, B.ULY_EINVAL),
+    ({"causal": -1}, B.ULY_EINVAL),
+    ({"q_start": 300 * MB}, B.ULY_EINVAL),
+    ({"kv_lens": 300 * MB + 2}, B.ULY_EALIGN),
+    ({"ws": 0}, B.ULY_EINVAL),
+    ({"ws_bytes": 64}, B.ULY_EINVAL),
+    ({"ws": 200 * MB + 4}, B.ULY_EALIGN),
+    ({"ws": MB}, B.ULY_EOVERLAP),
+    ({"go": [None]}, B.ULY_EINVAL),
+    ({"dk": None}, B.ULY_EINVAL),
+    ({"lse": [None]}, B.ULY_EINVAL),
+    ({"o": [MB + 2]}, B.ULY_EALIGN),
+    ({"dq": [MB]}, B.ULY_EOVERLAP),                          # the queries' own place
+    ({"dv": [113 * MB + 16]}, B.ULY_EOVERLAP),               # inside dk
+])
+def test_backward_refused_arguments(kw, want):
+    assert backward_status(*plans(), **kw) == want
+
+
+def test_backward_plans_that_do_not_go_together():
+    qp, kp = plans(kv=(1, 2, [128], [3], 64, "bfloat16"))
+    with pytest.raises(B.UlyssesError) as e:
+        B.ulysses_attention_backward_workspace(qp, kp)
+    assert e.value.status == B.ULY_EINVAL
+    assert B.library().ulysses_attention_backward(*(None,) * 13, 0, 0.125, None, 0, None) == B.ULY_EINVAL

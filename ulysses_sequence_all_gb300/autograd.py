@@ -15,6 +15,9 @@ plan for the backward:
 * ``packed_fused(plan, packed, planes, q_plane, k_plane, rms_w, eps, rope_theta)``: the call on
   any packing of C planes per token (QKVG, ...); its backward is
   ``ulysses_a2a_4d_packed_fused_backward``; a token's columns beyond its planes get zero gradient.
+* ``attention(q_plan, kv_plan, q, k, v, scale, causal, kv_lens, q_start)``: attention of every
+  rank's heads over the whole sequence; its backward is ``ulysses_attention_backward``, from the
+  output and the log-sum-exp that the forward keeps.
 
 Inputs and outputs are lists of W tensors (one per virtual rank) on the current CUDA device;
 the outputs are new tensors the caller owns. Nothing here computes: every step runs in the
@@ -191,3 +194,48 @@ def packed_fused(plan: B.Plan, packed, planes: int, q_plane: int, k_plane: int,
     out = _PackedFused.apply(plan, planes, q_plane, k_plane, eps, rope_theta, rms_w, *packed)
     W = len(packed)
     return [list(out[c * W:(c + 1) * W]) for c in range(planes)]
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q_plan, kv_plan, scale, causal, kv_lens, q_start, *qkv):
+        W = len(qkv) // 3
+        qkv = [x.contiguous() for x in qkv]
+        q, k, v = qkv[:W], qkv[W:2 * W], qkv[2 * W:]
+        kv_lens, q_start = _int32(kv_lens), _int32(q_start)
+        out = [torch.empty_like(x) for x in q]
+        lse = [torch.empty((x.shape[0], x.shape[2], x.shape[1]), dtype=torch.float32,
+                           device=x.device) for x in q]
+        need = B.ulysses_attention_workspace(q_plan, kv_plan)
+        ws = torch.empty(need, dtype=torch.uint8, device=q[0].device) if need else None
+        B.ulysses_attention(q_plan, kv_plan, q, k, v, out, lse, scale, causal, kv_lens, q_start, ws)
+        ctx.plans, ctx.scale, ctx.causal, ctx.W = (q_plan, kv_plan), scale, causal, W
+        ctx.save_for_backward(kv_lens, q_start, *qkv, *out, *lse)
+        return tuple(out)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        W = ctx.W
+        kv_lens, q_start, *saved = ctx.saved_tensors
+        q, k, v, out, lse = (saved[i * W:(i + 1) * W] for i in range(5))
+        go = _grads(grads, ctx.plans[0], 0, q[0])
+        dq, dk, dv = ([torch.empty_like(x) for x in t] for t in (q, k, v))
+        ws = torch.empty(B.ulysses_attention_backward_workspace(*ctx.plans), dtype=torch.uint8,
+                         device=q[0].device)
+        B.ulysses_attention_backward(*ctx.plans, dq, dk, dv, q, k, v, out, lse, go, ctx.scale,
+                                     ctx.causal, kv_lens, q_start, ws)
+        return (None,) * 6 + (*dq, *dk, *dv)
+
+
+def _int32(x):
+    """A mask's counts as the library takes them: contiguous int32 (None stays None)."""
+    return None if x is None else x.to(torch.int32).contiguous()
+
+
+def attention(q_plan: B.Plan, kv_plan: B.Plan, q, k, v, scale: float | None = None,
+              causal: bool = False, kv_lens=None, q_start=None):
+    """Attention of every rank's heads over the whole sequence, on the head-side tensors that mode
+    0 returns (lists of W: q (b, Sq, n_r, d), k and v (b, Skv, m_r, d)), differentiable in q, k and
+    v; `scale` defaults to d ** -0.5. Returns a list of W tensors shaped as q."""
+    scale = q_plan.d ** -0.5 if scale is None else scale
+    return list(_Attention.apply(q_plan, kv_plan, scale, causal, kv_lens, q_start, *q, *k, *v))

@@ -38,6 +38,7 @@ EXPORTS = ["ulysses_plan", "ulysses_plan_destroy", "ulysses_plan_set_chunk_bytes
            "ulysses_qk_fused_backward_workspace", "ulysses_a2a_4d_qk_fused_backward_static",
            "ulysses_a2a_4d_qkv_fused_backward", "ulysses_a2a_4d_packed_fused_backward",
            "ulysses_attention", "ulysses_attention_workspace",
+           "ulysses_attention_backward", "ulysses_attention_backward_workspace",
            "ulysses_a2a_4d_host", "ulysses_a2a_4d_qk_fused_host", "ulysses_device_status",
            "ulysses_selftest_wait_timeout", "ulysses_last_cuda_error", "ulysses_strerror",
            "ulysses_version"]
@@ -109,6 +110,11 @@ def _lib():
         lib.ulysses_attention.argtypes = [_p, _p, _pp, _pp, _pp, _pp, _pp, _p, _p, ctypes.c_int,
                                           ctypes.c_float, _p, ctypes.c_size_t, _p]
         lib.ulysses_attention_workspace.argtypes = [_p, _p, ctypes.POINTER(ctypes.c_size_t)]
+        lib.ulysses_attention_backward.argtypes = [_p, _p, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _pp,
+                                                   _pp, _p, _p, ctypes.c_int, ctypes.c_float, _p,
+                                                   ctypes.c_size_t, _p]
+        lib.ulysses_attention_backward_workspace.argtypes = [_p, _p,
+                                                             ctypes.POINTER(ctypes.c_size_t)]
         lib.ulysses_a2a_4d_host.argtypes = [_p, ctypes.c_int, _pp, _pp, _pp, _pp, _p]
         lib.ulysses_a2a_4d_qk_fused_host.argtypes = [_p, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _p,
                                                      ctypes.c_float, ctypes.c_float, _p]
@@ -384,6 +390,26 @@ def ulysses_attention(q_plan: Plan, kv_plan: Plan, q, k, v, out, lse, scale: flo
                                     _ptrs(lse), _addr(kv_lens), _addr(q_start), int(causal), scale,
                                     _addr(workspace), _nbytes(workspace), _stream(stream)),
            "ulysses_attention")
+
+
+def ulysses_attention_backward_workspace(q_plan: Plan, kv_plan: Plan) -> int:
+    """Workspace bytes ulysses_attention_backward needs for these plans."""
+    n = ctypes.c_size_t()
+    _check(_lib().ulysses_attention_backward_workspace(q_plan, kv_plan, ctypes.byref(n)),
+           "ulysses_attention_backward_workspace")
+    return n.value
+
+
+def ulysses_attention_backward(q_plan: Plan, kv_plan: Plan, dq, dk, dv, q, k, v, out, lse, go,
+                               scale: float, causal: bool = False, kv_lens=None, q_start=None,
+                               workspace=None, stream=None):
+    """Gradient of ulysses_attention into dq, dk, dv from its inputs, its outputs and the gradient
+    `go` of out. `workspace` is a device tensor of at least
+    ulysses_attention_backward_workspace(q_plan, kv_plan) bytes."""
+    _check(_lib().ulysses_attention_backward(
+        q_plan, kv_plan, _ptrs(dq), _ptrs(dk), _ptrs(dv), _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out),
+        _ptrs(lse), _ptrs(go), _addr(kv_lens), _addr(q_start), int(causal), scale,
+        _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_backward")
 
 
 def ulysses_a2a_4d_host(plan: Plan, mode: int, host_in, host_out, dev_in, dev_out, stream=None):

@@ -73,6 +73,13 @@ int current_device(DeviceInfo* info)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
     if (dev < 0 || dev >= 64) return ULY_EINVAL;
+    // A thread that has made no runtime call yet (autograd's, on its first backward) has no current
+    // context, and the driver's tensor-map encoder wants one: setting the device binds it.
+    static thread_local int bound = -1;
+    if (bound != dev) {
+        if ((e = cudaSetDevice(dev)) != cudaSuccess) return cuda_fail(e);
+        bound = dev;
+    }
     int sms = sm_counts[dev].load(std::memory_order_relaxed);
     if (sms == 0) {
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -949,6 +956,62 @@ int attn_fwd_device(const Plan& qp, const Plan& kp, const void* const* q, const 
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
 
+// Tiles of a backward call and the bytes of its workspace.
+size_t attn_bwd_setup(AttnBwdArgs* a)
+{
+    const AttnShape& s = a->s;
+    a->tile_tokens = kAttnRows / s.group;
+    a->q_tiles = (s.Sq + a->tile_tokens - 1) / a->tile_tokens;
+    a->k_blocks = (s.Skv + kAttnRows - 1) / kAttnRows;
+    return size_t(s.head_begin[s.W]) * size_t(a->q_tiles) * 2 * kAttnRows * sizeof(float);
+}
+
+int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const* dk,
+                    void* const* dv, const void* const* q, const void* const* k,
+                    const void* const* v, const void* const* o, const float* const* lse,
+                    const void* const* go, const int32_t* kv_lens, const int32_t* q_start,
+                    int causal, float scale, void* workspace, size_t workspace_bytes,
+                    cudaStream_t stream)
+{
+    AttnBwdArgs a;
+    std::memset(&a, 0, sizeof a);
+    int rc = attn_shape(qp, kp, &a.s);
+    if (rc) return rc;
+    if ((rc = attn_masks(&a.s, scale, causal, kv_lens, q_start))) return rc;
+    const int W = qp.W;
+    int64_t q_b[kMaxW], kv_b[kMaxW], lse_b[kMaxW];
+    attn_bytes(qp, kp, q_b, kv_b, lse_b);
+    RangeList ins, outs;
+    if ((rc = ins.add_ranks(q, q_b, W)) || (rc = ins.add_ranks(k, kv_b, W)) ||
+        (rc = ins.add_ranks(v, kv_b, W)) || (rc = ins.add_ranks(o, q_b, W)) ||
+        (rc = ins.add_ranks(reinterpret_cast<const void* const*>(lse), lse_b, W)) ||
+        (rc = ins.add_ranks(go, q_b, W)) ||
+        (rc = outs.add_ranks(const_cast<const void* const*>(dq), q_b, W)) ||
+        (rc = outs.add_ranks(const_cast<const void* const*>(dk), kv_b, W)) ||
+        (rc = outs.add_ranks(const_cast<const void* const*>(dv), kv_b, W)))
+        return rc;
+    ins.add(kv_lens, qp.b * 4);
+    ins.add(q_start, qp.b * 4);
+    const size_t need = attn_bwd_setup(&a);
+    if (!workspace || workspace_bytes < need) return ULY_EINVAL;
+    if (!aligned16(workspace)) return ULY_EALIGN;
+    outs.add(workspace, int64_t(need));
+    if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
+    DeviceInfo dev;
+    if ((rc = current_device(&dev))) return rc;
+    a.stats = static_cast<float*>(workspace);
+    for (int r = 0; r < W; ++r) {
+        a.o[r] = static_cast<const uint8_t*>(o[r]);
+        a.go[r] = static_cast<const uint8_t*>(go[r]);
+        a.lse[r] = lse[r];
+        a.dq[r] = static_cast<uint8_t*>(dq[r]);
+        a.dk[r] = static_cast<uint8_t*>(dk[r]);
+        a.dv[r] = static_cast<uint8_t*>(dv[r]);
+    }
+    const cudaError_t e = attn_bwd_launch(a, q, k, v, stream, dev.device, attn_grid(qp, dev));
+    return e == cudaSuccess ? ULY_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1271,6 +1334,31 @@ int ulysses_attention(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, const void*
                            workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
+int ulysses_attention_backward_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan,
+                                         size_t* bytes)
+{
+    if (!q_plan || !kv_plan || !bytes) return ULY_EINVAL;
+    AttnBwdArgs a;
+    std::memset(&a, 0, sizeof a);
+    const int rc = attn_shape(q_plan->p, kv_plan->p, &a.s);
+    if (rc) return rc;
+    *bytes = attn_bwd_setup(&a);
+    return ULY_OK;
+}
+
+int ulysses_attention_backward(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, void* const* dq,
+                               void* const* dk, void* const* dv, const void* const* q,
+                               const void* const* k, const void* const* v, const void* const* o,
+                               const float* const* lse, const void* const* go,
+                               const int32_t* kv_lens, const int32_t* q_start, int causal,
+                               float scale, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!q_plan || !kv_plan) return ULY_EINVAL;
+    return attn_bwd_device(q_plan->p, kv_plan->p, dq, dk, dv, q, k, v, o, lse, go, kv_lens, q_start,
+                           causal, scale, workspace, workspace_bytes,
+                           static_cast<cudaStream_t>(stream));
+}
+
 int ulysses_a2a_4d_host(ulysses_plan_t plan, int mode, const void* const* host_in,
                         void* const* host_out, void* const* dev_in, void* const* dev_out, void* stream)
 {
@@ -1364,13 +1452,14 @@ int ulysses_device_status(unsigned* status)
     if (!status) return ULY_EINVAL;
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e);
-    unsigned a = 0, b = 0, c = 0, t = 0, f = 0;
+    unsigned a = 0, b = 0, c = 0, t = 0, f = 0, g = 0;
     if ((e = relayout_status(&a, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = fused_status(&b, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = fused_bwd_status(&c, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = fused_tensor_status(&t, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = attn_fwd_status(&f, true)) != cudaSuccess) return cuda_fail(e);
-    *status = a | b | c | t | f;
+    if ((e = attn_bwd_status(&g, true)) != cudaSuccess) return cuda_fail(e);
+    *status = a | b | c | t | f | g;
     return *status ? ULY_EDEVICE : ULY_OK;
 }
 

@@ -46,10 +46,28 @@ struct AttnFwdArgs {
     float* part_lse;    // [splits][rows]
 };
 
+struct AttnBwdArgs {
+    AttnShape s;
+    CUtensorMap qmap[kMaxW], gmap[kMaxW], dqmap[kMaxW];  // boxes of a row tile: q, dO, dq
+    CUtensorMap kmap[kMaxW], vmap[kMaxW], dkmap[kMaxW], dvmap[kMaxW];  // boxes of a key block
+    const uint8_t* o[kMaxW];
+    const uint8_t* go[kMaxW];
+    const float* lse[kMaxW];
+    uint8_t* dq[kMaxW];
+    uint8_t* dk[kMaxW];
+    uint8_t* dv[kMaxW];
+    int32_t tile_tokens;
+    int64_t q_tiles, k_blocks;  // row tiles along the tokens, key blocks
+    float* stats;  // [(rank, batch, key head)][q_tiles][2][128]: lse in powers of two, delta
+};
+
 // Host side.
 int attn_fwd_splits(const AttnShape& s, int64_t units, int sm_count);
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
                             const void* const* v, cudaStream_t stream, int device, int grid);
 cudaError_t attn_fwd_status(unsigned* status, bool clear);
+cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* const* k,
+                            const void* const* v, cudaStream_t stream, int device, int grid);
+cudaError_t attn_bwd_status(unsigned* status, bool clear);
 
 }  // namespace uly

@@ -1,0 +1,943 @@
+// attention_bwd.cu -- gradients of attention with the probabilities recomputed.
+//
+// With P_ij = exp(s_ij - lse_i) over visible keys, D_i = sum_c dO_ic O_ic, dP = dO V^T and
+// dS = P (dP - D):  dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K. Keys shared by several
+// query heads sum over them. Five products of 2 d flops per (row, key) cannot be done without.
+//
+// Three launches. attn_bwd_stats_kernel writes each row's lse (in powers of two; +infinity where a
+// row sees nothing or does not exist, which makes its P zero) and D in row-tile order. Then
+// attn_bwd_kv_kernel holds a block of 128 keys and walks the row tiles that see it (dK, dV), and
+// attn_bwd_q_kernel holds a tile of 128 rows and walks its key blocks (dQ). S and dP are computed
+// by both, seven products in place of five: dQ is then summed in one accumulator in a fixed order,
+// with no fp32 copy of it in memory, no atomics, and the same bits from run to run.
+//
+// Both are bound by the tensor cores. One CTA per SM (352 threads): warp 8 loads (swizzled tensor
+// maps), warp 9 issues the products, warp 10 stores, warps 0-3 and 4-7 turn scores into P and dS,
+// each the half of the tile's columns in its 128 threads' rows, while the products of the other
+// operand run. All accumulators are in tensor memory (fp32); P and dS go back to it rounded to the
+// element type, over the columns they came from, and are A operands there.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+
+#include "../../include/ulysses.h"
+#include "attention.h"
+#include "fused_row.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.h"
+
+namespace uly {
+
+static __device__ unsigned g_attn_bwd_status;
+
+constexpr int kAbThreads = 352;
+constexpr int kAbLoadWarp = 8, kAbMmaWarp = 9, kAbStoreWarp = 10;
+constexpr int kAbStats = 2 * kAttnRows * 4;  // one tile's lse and D
+
+// Keys that batch element bb holds, and the position of its first query (beyond every key when the
+// mask is not causal).
+__device__ __forceinline__ void ab_limits(const AttnShape& s, int bb, int64_t* len, int64_t* pos0)
+{
+    *len = s.kv_lens ? min(s.Skv, int64_t(max(0, s.kv_lens[bb]))) : s.Skv;
+    *pos0 = s.causal ? (s.q_start ? int64_t(s.q_start[bb]) : 0) : s.Skv;
+}
+
+__device__ __forceinline__ void ab_head(const AttnShape& s, int64_t h, int* r, int* bb, int* kvh)
+{
+    int k = 0;
+    while (k + 1 < s.W && h >= s.head_begin[k + 1]) ++k;
+    const int local = int(h) - s.head_begin[k];
+    *r = k;
+    *bb = local / s.m[k];
+    *kvh = local - *bb * s.m[k];
+}
+
+// One row a half warp: lane c of it holds columns 8c .. 8c + 7.
+template <bool F16>
+__global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_constant__ AttnBwdArgs a)
+{
+    using E = ElemT<F16>;
+    const AttnShape& s = a.s;
+    const int sub = threadIdx.x & 15, slot = threadIdx.x >> 4;
+    const int64_t tiles = s.head_begin[s.W] * a.q_tiles;
+    for (int64_t at = blockIdx.x; at < tiles * (kAttnRows / 16); at += gridDim.x) {
+        const int64_t tile = at / (kAttnRows / 16);
+        const int row = int(at - tile * (kAttnRows / 16)) * 16 + slot;
+        const int64_t h = div_fast(tile, a.q_tiles);
+        int r, bb, kvh;
+        ab_head(s, h, &r, &bb, &kvh);
+        const int tok_in = row / s.group, head = kvh * s.group + row - tok_in * s.group;
+        const int64_t tok = (tile - h * a.q_tiles) * a.tile_tokens + tok_in;
+        const bool valid = tok_in < a.tile_tokens && tok < s.Sq;
+        float sum = 0.0f;
+        if (valid && sub * 8 < s.d) {
+            const int64_t off =
+                ((int64_t(bb) * s.Sq + tok) * s.n[r] + head) * s.d * 2 + sub * 16;
+            const uint4 x = ld_stream_v4(a.o[r] + off), y = ld_stream_v4(a.go[r] + off);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum = fmaf(E::lo(xs[i]), E::lo(ys[i]), sum);
+                sum = fmaf(E::hi(xs[i]), E::hi(ys[i]), sum);
+            }
+        }
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (sub == 0) {
+            float z = INFINITY;
+            if (valid) {
+                const float lse = a.lse[r][(int64_t(bb) * s.n[r] + head) * s.Sq + tok];
+                if (lse != -INFINITY) z = lse * 1.4426950408889634f;
+            }
+            float* out = a.stats + tile * 2 * kAttnRows + row;
+            out[0] = z;
+            out[kAttnRows] = valid ? sum : 0.0f;
+        }
+    }
+}
+
+// ---- dK and dV ----------------------------------------------------------------------------------
+
+// Tensor memory columns. S^T (then P^T) and dP^T (then dS^T): lanes are keys, columns rows of q.
+constexpr int kBkS = 0, kBkDp = 128, kBkDv = 256, kBkDk = 384;
+
+template <int DP>
+struct BkSmem {
+    static constexpr int kTile = kAttnRows * DP * 2;
+    static constexpr int kHalf = kAttnRows * 128;
+    static constexpr int kStages = DP == 128 ? 2 : 4;
+    static constexpr int kK = 1024, kV = kK + kTile;
+    static constexpr int kQ = kV + kTile;               // ring of q tiles
+    static constexpr int kG = kQ + kStages * kTile;     // ring of dO tiles
+    static constexpr int kStat = kG + kStages * kTile;  // ring of their lse and D
+    static constexpr int kTotal = kStat + kStages * kAbStats;
+    static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");
+};
+
+struct BkBars {
+    uint64_t k_full, v_full, kv_empty[2];  // key block landed; its place's store has read it
+    uint64_t q_full[4], q_empty[4], g_full[4], g_empty[4];
+    uint64_t s_full, p_ready, dp_full, ds_ready;
+    uint64_t acc_full, acc_free[2], staged[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int dead;
+};
+static_assert(sizeof(BkBars) <= 1024, "barriers");
+
+struct BkUnit {
+    int r, bb, kvh, n;       // n: row tiles from `first` on that see the block
+    int64_t h, kv0, first;
+    int64_t len, pos0;
+};
+
+__device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
+{
+    const AttnShape& s = a.s;
+    BkUnit t;
+    t.h = div_fast(u, a.k_blocks);
+    t.kv0 = (u - t.h * a.k_blocks) * kAttnRows;
+    ab_head(s, t.h, &t.r, &t.bb, &t.kvh);
+    ab_limits(s, t.bb, &t.len, &t.pos0);
+    // row i sees key kv0 when i >= kv0 - pos0
+    const int64_t row = max(int64_t(0), t.kv0 - t.pos0);
+    t.first = row / a.tile_tokens;
+    t.n = t.kv0 < t.len && t.first < a.q_tiles ? int(a.q_tiles - t.first) : 0;
+    return t;
+}
+
+template <int DP, bool F16>
+__global__ void __launch_bounds__(kAbThreads, 1)
+    attn_bwd_kv_kernel(const __grid_constant__ AttnBwdArgs a)
+{
+    using L = BkSmem<DP>;
+    using E = ElemT<F16>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    BkBars& bars = *reinterpret_cast<BkBars*>(smem);
+    volatile int* dead = &bars.dead;
+    const AttnShape& s = a.s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nk = (s.d + 15) / 16, halves = (s.d + 63) / 64;
+    const int64_t units = s.head_begin[s.W] * a.k_blocks;
+    constexpr int K = L::kStages;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&bars.k_full, 1);
+        mbar_init(&bars.v_full, 1);
+        for (int k = 0; k < K; ++k) {
+            mbar_init(&bars.q_full[k], 1);
+            mbar_init(&bars.q_empty[k], 1);
+            mbar_init(&bars.g_full[k], 1);
+            mbar_init(&bars.g_empty[k], 1);
+        }
+        mbar_init(&bars.s_full, 1);
+        mbar_init(&bars.p_ready, 8);
+        mbar_init(&bars.dp_full, 1);
+        mbar_init(&bars.ds_ready, 8);
+        mbar_init(&bars.acc_full, 1);
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&bars.kv_empty[k], 1);
+            mbar_init(&bars.acc_free[k], 4);
+            mbar_init(&bars.staged[k], 4);
+        }
+        mbar_init(&bars.drain, 1);
+        bars.dead = 0;
+        fence_barrier_init();
+    }
+    // Rows of a tile past tile_tokens * group never arrive: they are summed over with P = dS = 0,
+    // and must be numbers.
+    if (a.tile_tokens * s.group < kAttnRows) {
+        for (int i = threadIdx.x * 16; i < 2 * K * L::kTile; i += kAbThreads * 16)
+            st_shared_v4(smem + L::kQ + i, make_uint4(0, 0, 0, 0));
+        fence_proxy_async_shared();
+    }
+    if (warp == kAbMmaWarp) tmem_alloc(&bars.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+
+    if (warp == kAbLoadWarp) {
+        if (lane == 0) {
+            StageRing ring;
+            uint32_t uses = 0;
+            int64_t issued = 0;
+            const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
+            const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const BkUnit t = bk_unit(a, u);
+                if (t.n == 0) continue;
+                for (int w = 0; ok && w < 2; ++w) {
+                    // K's place is read by dK's store, V's by dV's
+                    if (uses > 0) ok = wait_or_dead(&bars.kv_empty[w], (uses - 1) & 1, dead);
+                    if (!ok) break;
+                    uint64_t* bar = w ? &bars.v_full : &bars.k_full;
+                    mbar_arrive_expect_tx(bar, kv_bytes);
+                    for (int h = 0; h < halves; ++h)
+                        tensor_g2s_4d(smem + (w ? L::kV : L::kK) + h * L::kHalf,
+                                      w ? &a.vmap[t.r] : &a.kmap[t.r], 64 * h, t.kvh, int(t.kv0),
+                                      t.bb, bar);
+                }
+                if (!ok) break;
+                ++uses;
+                for (int i = 0; ok && i < t.n; ++i) {
+                    const int64_t tile = t.first + i;
+                    if (issued >= K) ok = wait_or_dead(&bars.q_empty[ring.s], ring.phase ^ 1u, dead);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars.q_full[ring.s], q_bytes + kAbStats);
+                    bulk_g2s(smem + L::kStat + ring.s * kAbStats,
+                             a.stats + (t.h * a.q_tiles + tile) * 2 * kAttnRows, kAbStats,
+                             &bars.q_full[ring.s]);
+                    for (int h = 0; h < halves; ++h)
+                        tensor_g2s_4d(smem + L::kQ + ring.s * L::kTile + h * L::kHalf, &a.qmap[t.r],
+                                      64 * h, t.kvh * s.group, int(tile * a.tile_tokens), t.bb,
+                                      &bars.q_full[ring.s]);
+                    if (issued >= K) ok = wait_or_dead(&bars.g_empty[ring.s], ring.phase ^ 1u, dead);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars.g_full[ring.s], q_bytes);
+                    for (int h = 0; h < halves; ++h)
+                        tensor_g2s_4d(smem + L::kG + ring.s * L::kTile + h * L::kHalf, &a.gmap[t.r],
+                                      64 * h, t.kvh * s.group, int(tile * a.tile_tokens), t.bb,
+                                      &bars.g_full[ring.s]);
+                    ++issued;
+                    ring.next(K);
+                }
+            }
+            // leave no copy into this CTA's shared memory in flight (after a timeout the last q
+            // tile may have arrived without its dO: `issued` does not count it)
+            bool drained = true;
+            for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k) {
+                drained &= mbar_wait_bounded(&bars.q_full[k % K], uint32_t((k / K) & 1));
+                drained &= mbar_wait_bounded(&bars.g_full[k % K], uint32_t((k / K) & 1));
+            }
+            if (!ok) drained &= mbar_wait_bounded(&bars.q_full[ring.s], ring.phase);
+            if (uses > 0) {
+                drained &= mbar_wait_bounded(&bars.k_full, (uses - 1) & 1);
+                drained &= mbar_wait_bounded(&bars.v_full, (uses - 1) & 1);
+            }
+            if (!drained) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
+        }
+        __syncwarp();
+    } else if (warp == kAbMmaWarp) {
+        const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
+        const uint32_t id_d = tc_idesc(F16, 16 * nk, true);
+        const uint32_t k_at = smem_u32(smem + L::kK), v_at = smem_u32(smem + L::kV);
+        const uint32_t q_at = smem_u32(smem + L::kQ), g_at = smem_u32(smem + L::kG);
+        StageRing ring;
+        uint32_t uses = 0, tiles = 0;
+        bool ok = true;
+        auto all = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+        };
+        auto scores = [&](uint32_t d, uint32_t key, uint32_t row, uint64_t* bar) {
+            if (lane == 0) {
+                for (int ks = 0; ks < nk; ++ks) {
+                    const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
+                    tc_mma_ss(tmem + d, tc_desc_k(key + off), tc_desc_k(row + off), id_s, ks > 0);
+                }
+                tc_commit(bar);
+            }
+        };
+        auto sums = [&](uint32_t d, uint32_t p, uint32_t row, bool first) {
+            for (int ks = 0; ks < kAttnRows / 16; ++ks)  // each warpgroup's 64 columns in 32
+                tc_mma_ts(tmem + d, tmem + p + (ks >> 2) * 64 + (ks & 3) * 8,
+                          tc_desc_mn(row + ks * 2048, L::kHalf), id_d, !first || ks > 0);
+        };
+        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            const BkUnit t = bk_unit(a, u);
+            if (t.n == 0) continue;
+            ok = all(&bars.k_full, uses & 1) && all(&bars.q_full[ring.s], ring.phase);
+            if (!ok) break;
+            tc_fence_after();
+            scores(kBkS, k_at, q_at + ring.s * L::kTile, &bars.s_full);
+            ok = all(&bars.v_full, uses & 1) && all(&bars.g_full[ring.s], ring.phase);
+            if (!ok) break;
+            tc_fence_after();
+            scores(kBkDp, v_at, g_at + ring.s * L::kTile, &bars.dp_full);
+            if (uses > 0)
+                ok = all(&bars.acc_free[0], (uses - 1) & 1) && all(&bars.acc_free[1], (uses - 1) & 1);
+            for (int i = 0; ok && i < t.n; ++i) {
+                const int at = ring.s;
+                const bool more = i + 1 < t.n;
+                ring.next(K);
+                ok = all(&bars.p_ready, tiles & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    sums(kBkDv, kBkS, g_at + at * L::kTile, i == 0);
+                    tc_commit(&bars.g_empty[at]);
+                }
+                if (more) {
+                    ok = all(&bars.q_full[ring.s], ring.phase);
+                    if (!ok) break;
+                    scores(kBkS, k_at, q_at + ring.s * L::kTile, &bars.s_full);
+                }
+                ok = all(&bars.ds_ready, tiles & 1);
+                if (!ok) break;
+                ++tiles;
+                tc_fence_after();
+                if (lane == 0) {
+                    sums(kBkDk, kBkDp, q_at + at * L::kTile, i == 0);
+                    tc_commit(&bars.q_empty[at]);
+                }
+                if (more) {
+                    ok = all(&bars.g_full[ring.s], ring.phase);
+                    if (!ok) break;
+                    scores(kBkDp, v_at, g_at + ring.s * L::kTile, &bars.dp_full);
+                } else if (lane == 0) {
+                    tc_commit(&bars.acc_full);
+                }
+                __syncwarp();
+            }
+            ++uses;
+        }
+        if (lane == 0) {  // every product complete before tensor memory is given back
+            tc_commit(&bars.drain);
+            if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
+        }
+        __syncwarp();
+    } else if (warp == kAbStoreWarp) {
+        if (lane == 0) {
+            uint32_t uses = 0;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const BkUnit t = bk_unit(a, u);
+                if (t.n == 0) continue;
+                for (int w = 0; ok && w < 2; ++w) {
+                    ok = wait_or_dead(&bars.staged[w], uses & 1, dead);
+                    if (!ok) break;
+                    for (int h = 0; h < halves; ++h)
+                        tensor_s2g_4d(w ? &a.dvmap[t.r] : &a.dkmap[t.r], 64 * h, t.kvh, int(t.kv0),
+                                      t.bb, smem + (w ? L::kV : L::kK) + h * L::kHalf);
+                    bulk_commit();
+                    bulk_wait_read<0>();
+                    mbar_arrive(&bars.kv_empty[w]);
+                }
+                ++uses;
+            }
+            bulk_wait<0>();
+        }
+        __syncwarp();
+    } else {
+        const int wg = warp >> 2;  // columns 64 wg .. 64 wg + 63; then dK (0) or dV (1)
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = uint32_t(warp & 3) << 21;
+        const uint32_t s_at = tmem + lanes + kBkS + wg * 64;
+        const uint32_t dp_at = tmem + lanes + kBkDp + wg * 64;
+        const uint32_t acc_at = tmem + lanes + (wg ? kBkDv : kBkDk);
+        const float sl2 = s.scale * 1.4426950408889634f;
+        uint8_t* stage = smem + (wg ? L::kV : L::kK) + row * 128;
+        StageRing ring;
+        uint32_t uses = 0, tiles = 0;
+        bool ok = true;
+        auto all = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+        };
+        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            const BkUnit t = bk_unit(a, u);
+            const int64_t key = t.kv0 + row;
+            if (t.n == 0) {  // keys that no row sees
+                if (key < s.Skv) {
+                    uint8_t* out = (wg ? a.dv[t.r] : a.dk[t.r]) +
+                                   ((int64_t(t.bb) * s.Skv + key) * s.m[t.r] + t.kvh) * s.d * 2;
+                    for (int c = 0; c < s.d * 2; c += 16) st_v4(out + c, make_uint4(0, 0, 0, 0));
+                }
+                continue;
+            }
+            for (int i = 0; i < t.n; ++i) {
+                // the tile's columns from `lo` on see this key
+                const int64_t tok0 = (t.first + i) * a.tile_tokens;
+                int64_t lo = (key - t.pos0 - tok0) * s.group;
+                if (key >= t.len) lo = kAttnRows;
+                const int from = int(max(int64_t(-1), min(lo - 64 * wg, int64_t(64))));
+                ok = all(&bars.q_full[ring.s], ring.phase);  // the tile's lse and D
+                ok = ok && all(&bars.s_full, tiles & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const float4* z4 =
+                    reinterpret_cast<const float4*>(smem + L::kStat + ring.s * kAbStats) + wg * 16;
+                uint32_t x[2][32];
+                tmem_ld32(s_at, x[0]);
+                tmem_ld32(s_at + 32, x[1]);
+                tmem_wait_ld(x[0]);
+                tmem_wait_ld(x[1]);
+                const float2 k2 = make_float2(sl2, sl2);
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 z = z4[q * 8 + c];
+                        float2 e = __ffma2_rn(make_float2(__uint_as_float(x[q][4 * c]),
+                                                          __uint_as_float(x[q][4 * c + 1])),
+                                              k2, make_float2(-z.x, -z.y));
+                        float2 f = __ffma2_rn(make_float2(__uint_as_float(x[q][4 * c + 2]),
+                                                          __uint_as_float(x[q][4 * c + 3])),
+                                              k2, make_float2(-z.z, -z.w));
+                        x[q][4 * c] = __float_as_uint(ex2(e.x));
+                        x[q][4 * c + 1] = __float_as_uint(ex2(e.y));
+                        x[q][4 * c + 2] = __float_as_uint(ex2(f.x));
+                        x[q][4 * c + 3] = __float_as_uint(ex2(f.y));
+                    }
+                const bool masked = __any_sync(0xffffffffu, from > 0);
+                if (masked) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (q * 32 + c < from) x[q][c] = 0;
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        p[c] = E::pack(__uint_as_float(x[q][2 * c]), __uint_as_float(x[q][2 * c + 1]));
+                    tmem_st16(s_at + q * 16, p);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_ready);
+
+                ok = all(&bars.dp_full, tiles & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const float4* d4 = z4 + kAttnRows / 4;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t y[32], p[16];
+                    tmem_ld32(dp_at + q * 32, y);
+                    tmem_wait_ld(y);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 dd = d4[q * 8 + c];
+                        float v[4];
+                        v[0] = __uint_as_float(x[q][4 * c]) * (__uint_as_float(y[4 * c]) - dd.x);
+                        v[1] = __uint_as_float(x[q][4 * c + 1]) * (__uint_as_float(y[4 * c + 1]) - dd.y);
+                        v[2] = __uint_as_float(x[q][4 * c + 2]) * (__uint_as_float(y[4 * c + 2]) - dd.z);
+                        v[3] = __uint_as_float(x[q][4 * c + 3]) * (__uint_as_float(y[4 * c + 3]) - dd.w);
+                        if (masked) {  // zero times what lies past the last key may be NaN
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (q * 32 + 4 * c + k < from) v[k] = 0.0f;
+                        }
+                        p[2 * c] = E::pack(v[0], v[1]);
+                        p[2 * c + 1] = E::pack(v[2], v[3]);
+                    }
+                    // in 16 columns from 64 wg + 16 q on: behind what this thread has read
+                    tmem_st16(dp_at + q * 16, p);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.ds_ready);
+                ++tiles;
+                ring.next(K);
+            }
+            if (!ok) break;
+            ok = all(&bars.acc_full, uses & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const float f = wg ? 1.0f : s.scale;
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+                uint32_t y[32];
+                tmem_ld32(acc_at + c * 32, y);
+                tmem_wait_ld(y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = E::pack(__uint_as_float(y[8 * i + 2 * k]) * f,
+                                       __uint_as_float(y[8 * i + 2 * k + 1]) * f);
+                    const int word = (c & 1) * 4 + i;
+                    st_shared_v4(stage + (c >> 1) * L::kHalf + ((word ^ (row & 7)) << 4),
+                                 make_uint4(w[0], w[1], w[2], w[3]));
+                }
+            }
+            tc_fence_before();
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars.acc_free[wg]);
+                mbar_arrive(&bars.staged[wg]);
+            }
+            ++uses;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && bars.dead) atomicOr(&g_attn_bwd_status, kStatusWaitTimeout);
+    if (warp == kAbMmaWarp) tmem_free(tmem);
+}
+
+// ---- dQ -----------------------------------------------------------------------------------------
+
+// Tensor memory columns: two buffers of S (then dS), dP, dQ; lanes are rows of q, columns keys.
+constexpr int kBqS = 0, kBqDp = 256, kBqDq = 384;
+
+template <int DP>
+struct BqSmem {
+    static constexpr int kTile = kAttnRows * DP * 2;
+    static constexpr int kHalf = kAttnRows * 128;
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr int kQ = 1024, kG = kQ + kTile;
+    static constexpr int kRing = kG + kTile;  // K0 V0 K1 V1 ...
+    static constexpr int kTotal = kRing + kStages * kTile;
+    static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");
+};
+
+struct BqBars {
+    uint64_t q_full, g_full, q_empty;  // q_empty: the dQ store has read its place (dO's with it)
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t s_full[2], dp_full, ds_ready;
+    uint64_t acc_full, acc_free, staged, drain;
+    uint32_t tmem;
+    int dead;
+};
+static_assert(sizeof(BqBars) <= 1024, "barriers");
+
+struct BqUnit {
+    int r, bb, kvh, n;  // n: key blocks that the tile sees
+    int64_t h, tile, tok0, len, pos0;
+};
+
+__device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
+{
+    const AttnShape& s = a.s;
+    BqUnit t;
+    t.h = div_fast(u, a.q_tiles);
+    t.tile = u - t.h * a.q_tiles;
+    if (s.causal) t.tile = a.q_tiles - 1 - t.tile;  // the longest rows first
+    t.tok0 = t.tile * a.tile_tokens;
+    ab_head(s, t.h, &t.r, &t.bb, &t.kvh);
+    ab_limits(s, t.bb, &t.len, &t.pos0);
+    const int64_t last = min(t.tok0 + a.tile_tokens, s.Sq) - 1;
+    const int64_t keys = max(int64_t(0), min(t.len, t.pos0 + last + 1));
+    t.n = int((keys + kAttnRows - 1) / kAttnRows);
+    return t;
+}
+
+template <int DP, bool F16>
+__global__ void __launch_bounds__(kAbThreads, 1)
+    attn_bwd_q_kernel(const __grid_constant__ AttnBwdArgs a)
+{
+    using L = BqSmem<DP>;
+    using E = ElemT<F16>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    BqBars& bars = *reinterpret_cast<BqBars*>(smem);
+    volatile int* dead = &bars.dead;
+    const AttnShape& s = a.s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nk = (s.d + 15) / 16, halves = (s.d + 63) / 64;
+    const int64_t units = s.head_begin[s.W] * a.q_tiles;
+    constexpr int K = L::kStages;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&bars.q_full, 1);
+        mbar_init(&bars.g_full, 1);
+        mbar_init(&bars.q_empty, 1);
+        for (int k = 0; k < K; ++k) {
+            mbar_init(&bars.kv_full[k], 1);
+            mbar_init(&bars.kv_empty[k], 1);
+        }
+        mbar_init(&bars.s_full[0], 1);
+        mbar_init(&bars.s_full[1], 1);
+        mbar_init(&bars.dp_full, 1);
+        mbar_init(&bars.ds_ready, 8);
+        mbar_init(&bars.acc_full, 1);
+        mbar_init(&bars.acc_free, 8);
+        mbar_init(&bars.staged, 8);
+        mbar_init(&bars.drain, 1);
+        bars.dead = 0;
+        fence_barrier_init();
+    }
+    if (warp == kAbMmaWarp) tmem_alloc(&bars.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+
+    if (warp == kAbLoadWarp) {
+        if (lane == 0) {
+            StageRing ring;
+            uint32_t uses = 0;
+            int64_t issued = 0;
+            const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
+            const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const BqUnit t = bq_unit(a, u);
+                if (t.n == 0) continue;
+                if (uses > 0) ok = wait_or_dead(&bars.q_empty, (uses - 1) & 1, dead);
+                if (!ok) break;
+                for (int w = 0; w < 2; ++w) {
+                    uint64_t* bar = w ? &bars.g_full : &bars.q_full;
+                    mbar_arrive_expect_tx(bar, q_bytes);
+                    for (int h = 0; h < halves; ++h)
+                        tensor_g2s_4d(smem + (w ? L::kG : L::kQ) + h * L::kHalf,
+                                      w ? &a.gmap[t.r] : &a.qmap[t.r], 64 * h, t.kvh * s.group,
+                                      int(t.tok0), t.bb, bar);
+                }
+                ++uses;
+                for (int j = 0; j < 2 * t.n; ++j) {
+                    if (issued >= K) ok = wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, dead);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars.kv_full[ring.s], kv_bytes);
+                    for (int h = 0; h < halves; ++h)
+                        tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf,
+                                      (j & 1) ? &a.vmap[t.r] : &a.kmap[t.r], 64 * h, t.kvh,
+                                      (j >> 1) * kAttnRows, t.bb, &bars.kv_full[ring.s]);
+                    ++issued;
+                    ring.next(K);
+                }
+            }
+            bool drained = true;  // leave no copy into this CTA's shared memory in flight
+            for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k)
+                drained &= mbar_wait_bounded(&bars.kv_full[k % K], uint32_t((k / K) & 1));
+            if (uses > 0) {
+                drained &= mbar_wait_bounded(&bars.q_full, (uses - 1) & 1);
+                drained &= mbar_wait_bounded(&bars.g_full, (uses - 1) & 1);
+            }
+            if (!drained) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
+        }
+        __syncwarp();
+    } else if (warp == kAbMmaWarp) {
+        const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
+        const uint32_t id_d = tc_idesc(F16, 16 * nk, true);
+        const uint32_t q_at = smem_u32(smem + L::kQ), g_at = smem_u32(smem + L::kG);
+        const uint32_t ring_at = smem_u32(smem + L::kRing);
+        StageRing ring;
+        uint32_t uses = 0, blocks = 0;
+        bool ok = true;
+        auto all = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+        };
+        auto scores = [&](uint32_t d, uint32_t row, uint32_t key, uint64_t* bar) {
+            if (lane == 0) {
+                for (int ks = 0; ks < nk; ++ks) {
+                    const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
+                    tc_mma_ss(tmem + d, tc_desc_k(row + off), tc_desc_k(key + off), id_s, ks > 0);
+                }
+                tc_commit(bar);
+            }
+        };
+        // dS is zero past the last key, but zero times what K holds there may be NaN
+        auto clear_past = [&](int stage, int64_t past) {
+            if (past >= kAttnRows) return;
+            const int words = (kAttnRows - int(past)) * 8;
+            for (int h = 0; h < halves; ++h)
+                for (int w = lane; w < words; w += 32)
+                    st_shared_v4(smem + L::kRing + stage * L::kTile + h * L::kHalf + int(past) * 128 +
+                                     w * 16,
+                                 make_uint4(0, 0, 0, 0));
+            fence_proxy_async_shared();
+            __syncwarp();
+        };
+        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            const BqUnit t = bq_unit(a, u);
+            if (t.n == 0) continue;
+            const bool ragged = t.len < s.Skv;
+            int ks = ring.s;  // the stage of the current block's K
+            ok = all(&bars.q_full, uses & 1) && all(&bars.kv_full[ks], ring.phase);
+            if (!ok) break;
+            if (ragged) clear_past(ks, t.len);
+            tc_fence_after();
+            scores(kBqS + (blocks & 1) * 128, q_at, ring_at + ks * L::kTile,
+                   &bars.s_full[blocks & 1]);
+            ring.next(K);
+            ok = all(&bars.g_full, uses & 1) && all(&bars.kv_full[ring.s], ring.phase);
+            if (!ok) break;
+            scores(kBqDp, g_at, ring_at + ring.s * L::kTile, &bars.dp_full);
+            if (lane == 0) tc_commit(&bars.kv_empty[ring.s]);
+            ring.next(K);
+            if (uses > 0) ok = all(&bars.acc_free, (uses - 1) & 1);
+            for (int j = 0; ok && j < t.n; ++j, ++blocks) {
+                const bool more = j + 1 < t.n;
+                const int next_k = ring.s;
+                if (more) {
+                    ok = all(&bars.kv_full[next_k], ring.phase);
+                    if (!ok) break;
+                    if (ragged) clear_past(next_k, t.len - int64_t(j + 1) * kAttnRows);
+                    tc_fence_after();
+                    const uint32_t buf = (blocks + 1) & 1;
+                    scores(kBqS + buf * 128, q_at, ring_at + next_k * L::kTile, &bars.s_full[buf]);
+                    ring.next(K);
+                }
+                ok = all(&bars.ds_ready, blocks & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int kk = 0; kk < kAttnRows / 16; ++kk)
+                        tc_mma_ts(tmem + kBqDq,
+                                  tmem + kBqS + (blocks & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                                  tc_desc_mn(ring_at + ks * L::kTile + kk * 2048, L::kHalf), id_d,
+                                  j > 0 || kk > 0);
+                    tc_commit(&bars.kv_empty[ks]);
+                }
+                ks = next_k;
+                if (more) {
+                    ok = all(&bars.kv_full[ring.s], ring.phase);
+                    if (!ok) break;
+                    scores(kBqDp, g_at, ring_at + ring.s * L::kTile, &bars.dp_full);
+                    if (lane == 0) tc_commit(&bars.kv_empty[ring.s]);
+                    ring.next(K);
+                } else if (lane == 0) {
+                    tc_commit(&bars.acc_full);
+                }
+                __syncwarp();
+            }
+            ++uses;
+        }
+        if (lane == 0) {
+            tc_commit(&bars.drain);
+            if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
+        }
+        __syncwarp();
+    } else if (warp == kAbStoreWarp) {
+        if (lane == 0) {
+            uint32_t uses = 0;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const BqUnit t = bq_unit(a, u);
+                if (t.n == 0) continue;
+                ok = wait_or_dead(&bars.staged, uses & 1, dead);
+                if (!ok) break;
+                for (int h = 0; h < halves; ++h)
+                    tensor_s2g_4d(&a.dqmap[t.r], 64 * h, t.kvh * s.group, int(t.tok0), t.bb,
+                                  smem + L::kQ + h * L::kHalf);
+                bulk_commit();
+                bulk_wait_read<0>();
+                mbar_arrive(&bars.q_empty);
+                ++uses;
+            }
+            bulk_wait<0>();
+        }
+        __syncwarp();
+    } else {
+        const int wg = warp >> 2;  // keys 64 wg .. 64 wg + 63 of a block
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = uint32_t(warp & 3) << 21;
+        const uint32_t dp_at = tmem + lanes + kBqDp + wg * 64;
+        const float sl2 = s.scale * 1.4426950408889634f;
+        const int tok_in = row / s.group, head_in = row - tok_in * s.group;
+        uint8_t* stage = smem + L::kQ + row * 128;
+        uint32_t uses = 0, blocks = 0;
+        bool ok = true;
+        auto all = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+        };
+        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            const BqUnit t = bq_unit(a, u);
+            const int64_t tok = t.tok0 + tok_in;
+            if (t.n == 0) {
+                if (wg == 0 && tok_in < a.tile_tokens && tok < s.Sq) {
+                    uint8_t* out = a.dq[t.r] + ((int64_t(t.bb) * s.Sq + tok) * s.n[t.r] +
+                                                t.kvh * s.group + head_in) * s.d * 2;
+                    for (int c = 0; c < s.d * 2; c += 16) st_v4(out + c, make_uint4(0, 0, 0, 0));
+                }
+                continue;
+            }
+            const float* stat = a.stats + (t.h * a.q_tiles + t.tile) * 2 * kAttnRows + row;
+            const float z = -stat[0], delta = stat[kAttnRows];
+            const int64_t lim = min(t.len, t.pos0 + tok + 1);
+            for (int j = 0; j < t.n; ++j) {
+                const uint32_t s_at = tmem + lanes + kBqS + (blocks & 1) * 128 + wg * 64;
+                const int64_t left = lim - int64_t(j) * kAttnRows - 64 * wg;
+                const int seen = int(max(int64_t(0), min(left, int64_t(64))));
+                ok = all(&bars.s_full[blocks & 1], (blocks >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t x[2][32];
+                tmem_ld32(s_at, x[0]);
+                tmem_ld32(s_at + 32, x[1]);
+                tmem_wait_ld(x[0]);
+                tmem_wait_ld(x[1]);
+                const float2 k2 = make_float2(sl2, sl2), z2 = make_float2(z, z);
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[q][2 * c]),
+                                                                __uint_as_float(x[q][2 * c + 1])),
+                                                    k2, z2);
+                        x[q][2 * c] = __float_as_uint(ex2(e.x));
+                        x[q][2 * c + 1] = __float_as_uint(ex2(e.y));
+                    }
+                const bool masked = __any_sync(0xffffffffu, seen < 64);
+                ok = all(&bars.dp_full, blocks & 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t y[32], p[16];
+                    tmem_ld32(dp_at + q * 32, y);
+                    tmem_wait_ld(y);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        float v0 = __uint_as_float(x[q][2 * c]) * (__uint_as_float(y[2 * c]) - delta);
+                        float v1 = __uint_as_float(x[q][2 * c + 1]) *
+                                   (__uint_as_float(y[2 * c + 1]) - delta);
+                        if (masked) {
+                            if (q * 32 + 2 * c >= seen) v0 = 0.0f;
+                            if (q * 32 + 2 * c + 1 >= seen) v1 = 0.0f;
+                        }
+                        p[c] = E::pack(v0, v1);
+                    }
+                    tmem_st16(s_at + q * 16, p);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.ds_ready);
+                ++blocks;
+            }
+            if (!ok) break;
+            ok = all(&bars.acc_full, uses & 1);
+            if (!ok) break;
+            tc_fence_after();
+            // each warpgroup takes half of the columns (DP = 64: 32 of them)
+#pragma unroll
+            for (int cc = 0; cc < DP / 64; ++cc) {
+                const int c = wg * (DP / 64) + cc;
+                uint32_t y[32];
+                tmem_ld32(tmem + lanes + kBqDq + c * 32, y);
+                tmem_wait_ld(y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = E::pack(__uint_as_float(y[8 * i + 2 * k]) * s.scale,
+                                       __uint_as_float(y[8 * i + 2 * k + 1]) * s.scale);
+                    const int word = (c & 1) * 4 + i;
+                    st_shared_v4(stage + (c >> 1) * L::kHalf + ((word ^ (row & 7)) << 4),
+                                 make_uint4(w[0], w[1], w[2], w[3]));
+                }
+            }
+            tc_fence_before();
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars.acc_free);
+                mbar_arrive(&bars.staged);
+            }
+            ++uses;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && bars.dead) atomicOr(&g_attn_bwd_status, kStatusWaitTimeout);
+    if (warp == kAbMmaWarp) tmem_free(tmem);
+}
+
+template <int DP, bool F16>
+static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int device, int grid)
+{
+    static std::atomic<unsigned long long> raised{0};
+    const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
+    constexpr int smem_kv = BkSmem<DP>::kTotal + 1024, smem_q = BqSmem<DP>::kTotal + 1024;
+    cudaError_t e;
+    if (bit && !(raised.load() & bit)) {
+        e = cudaFuncSetAttribute(attn_bwd_kv_kernel<DP, F16>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(attn_bwd_q_kernel<DP, F16>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
+        if (e != cudaSuccess) return e;
+        raised.fetch_or(bit);
+    }
+    const int64_t heads = a.s.head_begin[a.s.W];
+    auto cap = [](int64_t n, int64_t most) { return unsigned(n < most ? n : most); };
+    attn_bwd_stats_kernel<F16><<<cap(heads * a.q_tiles * (kAttnRows / 16), int64_t(grid) * 16), 256, 0,
+                                 stream>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    attn_bwd_kv_kernel<DP, F16><<<cap(heads * a.k_blocks, grid), kAbThreads, smem_kv, stream>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    attn_bwd_q_kernel<DP, F16><<<cap(heads * a.q_tiles, grid), kAbThreads, smem_q, stream>>>(a);
+    return cudaGetLastError();
+}
+
+// The three launches over all ranks, `grid` CTAs of the product kernels at most. The shape, every
+// pointer and the workspace are set in `a`.
+cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* const* k,
+                            const void* const* v, cudaStream_t stream, int device, int grid)
+{
+    const AttnShape& s = a.s;
+    if (s.head_begin[s.W] == 0) return cudaSuccess;
+    for (int r = 0; r < s.W; ++r) {
+        if (s.n[r] == 0) continue;
+        auto rows = [&](CUtensorMap* map, const void* p) {
+            return encode_head_map(map, p, s.f16, s.d, s.n[r], s.Sq, s.b, s.group, a.tile_tokens);
+        };
+        auto keys = [&](CUtensorMap* map, const void* p) {
+            return encode_head_map(map, p, s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows);
+        };
+        if (!rows(&a.qmap[r], q[r]) || !rows(&a.gmap[r], a.go[r]) || !rows(&a.dqmap[r], a.dq[r]) ||
+            !keys(&a.kmap[r], k[r]) || !keys(&a.vmap[r], v[r]) || !keys(&a.dkmap[r], a.dk[r]) ||
+            !keys(&a.dvmap[r], a.dv[r]))
+            return cudaErrorInvalidValue;
+    }
+    if (s.d <= 64)
+        return s.f16 ? ab_launch<64, true>(a, stream, device, grid)
+                     : ab_launch<64, false>(a, stream, device, grid);
+    return s.f16 ? ab_launch<128, true>(a, stream, device, grid)
+                 : ab_launch<128, false>(a, stream, device, grid);
+}
+
+cudaError_t attn_bwd_status(unsigned* status, bool clear)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_attn_bwd_status, sizeof(unsigned));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_attn_bwd_status, &zero, sizeof(unsigned));
+}
+
+}  // namespace uly
