@@ -858,19 +858,14 @@ int attn_grid(const Plan& p, const DeviceInfo& dev)
     return p.max_ctas > 0 && p.max_ctas < dev.sm_count ? int(p.max_ctas) : dev.sm_count;
 }
 
-// Tiles and splits of a forward call, and the bytes of its partial results (0 without splits).
+// Units of a forward call, and the bytes of its partial results (0 where the keys are not split).
 size_t attn_fwd_setup(const Plan& qp, const DeviceInfo& dev, AttnFwdArgs* a)
 {
     const AttnShape& s = a->s;
-    a->tile_tokens = kAttnRows / s.group;
-    const int64_t pair = 2 * int64_t(a->tile_tokens);
-    a->q_blocks = (s.Sq + pair - 1) / pair;
-    const int64_t units = s.head_begin[s.W] * a->q_blocks;
-    a->splits = attn_fwd_splits(s, units, attn_grid(qp, dev));
-    a->units = units * a->splits;
-    if (a->splits == 1) return 0;
+    attn_fwd_split(a, attn_grid(qp, dev));
+    if (a->parts == 1) return 0;
     const size_t rows = size_t(s.row_begin[s.W]);
-    return size_t(a->splits) * ((rows * size_t(s.d) + rows) * sizeof(float));
+    return size_t(a->parts) * ((rows * size_t(s.d) + rows) * sizeof(float));
 }
 
 // Masks and scale of an attention call.
@@ -946,7 +941,7 @@ int attn_fwd_device(const Plan& qp, const Plan& kp, const void* const* q, const 
         outs.add(workspace, int64_t(need));
         a.part_o = static_cast<float*>(workspace);
         if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
-        a.part_lse = a.part_o + size_t(a.splits) * size_t(a.s.row_begin[W]) * size_t(a.s.d);
+        a.part_lse = a.part_o + size_t(a.parts) * size_t(a.s.row_begin[W]) * size_t(a.s.d);
     }
     for (int r = 0; r < W; ++r) {
         a.o[r] = static_cast<uint8_t*>(o[r]);

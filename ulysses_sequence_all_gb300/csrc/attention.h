@@ -35,15 +35,17 @@ struct AttnShape {
 
 struct AttnFwdArgs {
     AttnShape s;
-    CUtensorMap qmap[kMaxW], kmap[kMaxW], vmap[kMaxW], omap[kMaxW];
+    CUtensorMap qmap[kMaxW], kmap[kMaxW], vmap[kMaxW];
     uint8_t* o[kMaxW];
     float* lse[kMaxW];  // (b, n_r, Sq)
     int32_t tile_tokens;
     int64_t q_blocks;   // pairs of row tiles along the tokens
     int64_t units;      // (rank, batch, key head) x q_blocks x splits
-    int32_t splits;     // parts of the keys, joined by a second kernel
-    float* part_o;      // [splits][rows][d] normalised partial outputs, splits > 1
-    float* part_lse;    // [splits][rows]
+    int32_t splits;     // units along the keys
+    int32_t paired;     // a unit's two tiles are the same rows, each with its own part of the keys
+    int32_t parts;      // parts of the keys (splits, or twice as many when paired)
+    float* part_o;      // [parts][rows][d] normalised partial outputs, parts > 1, joined by a
+    float* part_lse;    // [parts][rows]    second kernel
 };
 
 struct AttnBwdArgs {
@@ -62,7 +64,7 @@ struct AttnBwdArgs {
 };
 
 // Host side.
-int attn_fwd_splits(const AttnShape& s, int64_t units, int sm_count);
+void attn_fwd_split(AttnFwdArgs* a, int sm_count);  // tiles, units and parts from the shape
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
                             const void* const* v, cudaStream_t stream, int device, int grid);
 cudaError_t attn_fwd_status(unsigned* status, bool clear);

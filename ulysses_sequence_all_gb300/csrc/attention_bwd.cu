@@ -276,8 +276,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
         };
         auto scores = [&](uint32_t d, uint32_t key, uint32_t row, uint64_t* bar) {
-            if (lane == 0) {
-                for (int ks = 0; ks < nk; ++ks) {
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    if (ks >= nk) break;
                     const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
                     tc_mma_ss(tmem + d, tc_desc_k(key + off), tc_desc_k(row + off), id_s, ks > 0);
                 }
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             }
         };
         auto sums = [&](uint32_t d, uint32_t p, uint32_t row, bool first) {
+#pragma unroll
             for (int ks = 0; ks < kAttnRows / 16; ++ks)  // each warpgroup's 64 columns in 32
                 tc_mma_ts(tmem + d, tmem + p + (ks >> 2) * 64 + (ks & 3) * 8,
                           tc_desc_mn(row + ks * 2048, L::kHalf), id_d, !first || ks > 0);
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 ok = all(&bars.p_ready, tiles & 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     sums(kBkDv, kBkS, g_at + at * L::kTile, i == 0);
                     tc_commit(&bars.g_empty[at]);
                 }
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 if (!ok) break;
                 ++tiles;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     sums(kBkDk, kBkDp, q_at + at * L::kTile, i == 0);
                     tc_commit(&bars.q_empty[at]);
                 }
@@ -330,14 +333,14 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     ok = all(&bars.g_full[ring.s], ring.phase);
                     if (!ok) break;
                     scores(kBkDp, v_at, g_at + ring.s * L::kTile, &bars.dp_full);
-                } else if (lane == 0) {
+                } else if (elect_one()) {
                     tc_commit(&bars.acc_full);
                 }
                 __syncwarp();
             }
             ++uses;
         }
-        if (lane == 0) {  // every product complete before tensor memory is given back
+        if (elect_one()) {  // every product complete before tensor memory is given back
             tc_commit(&bars.drain);
             if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
         }
@@ -662,8 +665,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
         };
         auto scores = [&](uint32_t d, uint32_t row, uint32_t key, uint64_t* bar) {
-            if (lane == 0) {
-                for (int ks = 0; ks < nk; ++ks) {
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    if (ks >= nk) break;
                     const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
                     tc_mma_ss(tmem + d, tc_desc_k(row + off), tc_desc_k(key + off), id_s, ks > 0);
                 }
@@ -697,7 +702,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             ok = all(&bars.g_full, uses & 1) && all(&bars.kv_full[ring.s], ring.phase);
             if (!ok) break;
             scores(kBqDp, g_at, ring_at + ring.s * L::kTile, &bars.dp_full);
-            if (lane == 0) tc_commit(&bars.kv_empty[ring.s]);
+            if (elect_one()) tc_commit(&bars.kv_empty[ring.s]);
             ring.next(K);
             if (uses > 0) ok = all(&bars.acc_free, (uses - 1) & 1);
             for (int j = 0; ok && j < t.n; ++j, ++blocks) {
@@ -715,7 +720,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 ok = all(&bars.ds_ready, blocks & 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
+#pragma unroll
                     for (int kk = 0; kk < kAttnRows / 16; ++kk)
                         tc_mma_ts(tmem + kBqDq,
                                   tmem + kBqS + (blocks & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
@@ -728,16 +734,16 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     ok = all(&bars.kv_full[ring.s], ring.phase);
                     if (!ok) break;
                     scores(kBqDp, g_at, ring_at + ring.s * L::kTile, &bars.dp_full);
-                    if (lane == 0) tc_commit(&bars.kv_empty[ring.s]);
+                    if (elect_one()) tc_commit(&bars.kv_empty[ring.s]);
                     ring.next(K);
-                } else if (lane == 0) {
+                } else if (elect_one()) {
                     tc_commit(&bars.acc_full);
                 }
                 __syncwarp();
             }
             ++uses;
         }
-        if (lane == 0) {
+        if (elect_one()) {
             tc_commit(&bars.drain);
             if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
         }

@@ -11,20 +11,23 @@
 // key) on the tensor cores, one exponential. The kernel is bound by the tensor cores where d = 128
 // and by exponentials and products alike where d = 64; with few rows by reading the keys.
 //
-// A CTA (one per SM, 352 threads) takes two tiles of 128 query rows that share their keys. Warp 8
+// A CTA (one per SM, 384 threads) takes two tiles of 128 query rows that share their keys. Warp 8
 // loads (tensor maps, swizzled): the query tiles, then a ring of key and value blocks. Warp 9
 // issues the products: S = Q K^T of one tile while the other tile's 128 threads turn their S into
-// probabilities, so the tensor cores always have one tile's work. Warps 0-3 and 4-7 are the two
-// tiles' softmax: tensor memory gives a thread a whole row, so maximum and sum need no exchange.
+// probabilities, so the tensor cores always have one tile's work; a unit's first scores follow the
+// last unit's products without a gap. Warps 0-3 and 4-7 are the two tiles' softmax: tensor memory
+// gives a thread a whole row, so maximum and sum need no exchange; they hold most of the registers.
 // P goes back to tensor memory over its own S in 16 bits, rounded to nearest (unit-scale values
 // in an fp32 sum: the output itself is rounded to the same type), and is the A operand of O += P V
-// there. O stays in tensor memory; it is rescaled only when a row's maximum has grown by more than
-// 2^8 since its last scale (P then stays below 2^8, far inside either type), by the softmax threads
-// themselves: the block's S is complete only after the previous O product. Warp 10 stores finished
-// output tiles, staged in the query tile's place.
+// there, whose first half starts when half of P is written. O stays in tensor memory; it is
+// rescaled only when a row's maximum has grown by more than 2^8 since its last scale (P then stays
+// below 2^8, far inside either type), by the softmax threads themselves: the block's S is complete
+// only after the previous O product. They also write the finished rows.
 //
-// With too few tiles to fill the SMs the keys are split into parts, each with its own normalised
-// fp32 output and lse, and attn_join_kernel adds them weighted by exp(lse_part - lse).
+// With few rows (one tile of them: single tokens) both tiles of a CTA are those rows, each over its
+// own part of the keys; with too few units to fill the SMs the keys are split further. A part has
+// its own normalised fp32 output and lse, and attn_join_kernel adds them weighted by
+// exp(lse_part - lse).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,8 +45,10 @@ namespace uly {
 
 static __device__ unsigned g_attn_fwd_status;
 
-constexpr int kAfThreads = 352;
-constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfStoreWarp = 10;
+constexpr int kAfThreads = 384;
+constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9;
+// Registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72.
+constexpr int kAfRegsSoftmax = 216, kAfRegsOther = 72;
 constexpr float kAfRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 
 // Tensor memory columns: the two tiles' scores (their probabilities over them), their outputs.
@@ -54,18 +59,17 @@ struct AfSmem {
     static constexpr int kTile = kAttnRows * DP * 2;  // a tile of 128 rows; a block of 128 keys
     static constexpr int kHalf = kAttnRows * 128;     // its part of 64 columns
     static constexpr int kStages = DP == 128 ? 5 : 8;
-    static constexpr int kBars = 0;
-    static constexpr int kQ = 1024;
+    static constexpr int kQ = 1024;  // barriers first
     static constexpr int kRing = kQ + 2 * kTile;
     static constexpr int kTotal = kRing + kStages * kTile;
     static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");  // and room to align the base
 };
 
 struct AfBars {
-    uint64_t q_full[2], q_empty[2];   // a tile's queries landed; its output store has read them
-    uint64_t s_full[2], p_ready[2];   // scores complete; probabilities (and a rescaled O) written
-    uint64_t o_full[2], o_free[2];    // output complete; read out
-    uint64_t o_staged[2];             // output tile in shared memory
+    uint64_t q_full[2], q_empty[2];  // a tile's queries landed; its last scores have read them
+    uint64_t s_full[2];              // scores complete
+    uint64_t p_half[2], p_ready[2];  // half of the probabilities (and a rescaled O) written; all
+    uint64_t o_full[2], o_free[2];   // output complete; read out
     uint64_t kv_full[8], kv_empty[8];
     uint64_t drain;
     uint32_t tmem;
@@ -75,12 +79,24 @@ static_assert(sizeof(AfBars) <= 1024, "barriers");
 
 struct AfUnit {
     int r, bb, kvh, sp;
-    int64_t tok[2];  // first token of each tile
-    int64_t lo;      // first key block of this part
-    int n[2];        // key blocks of each tile
-    int64_t len;     // keys of the batch element
-    int64_t pos0;    // position of query token 0; beyond every key when not causal
+    int64_t tok0, tok1;  // first token of each tile
+    int64_t lo0, lo1;    // first key block of each tile
+    int n0, n1;          // key blocks of each tile
+    int64_t len;         // keys of the batch element
+    int64_t pos0;        // position of query token 0; beyond every key when not causal
+    __device__ __forceinline__ int n(int k) const { return k ? n1 : n0; }
+    __device__ __forceinline__ int64_t lo(int k) const { return k ? lo1 : lo0; }
+    __device__ __forceinline__ int64_t tok(int k) const { return k ? tok1 : tok0; }
+    __device__ __forceinline__ int most() const { return max(n0, n1); }
 };
+
+// Key blocks that the tile of tokens from `tok` on sees.
+__device__ __forceinline__ int64_t af_blocks(const AttnFwdArgs& a, const AfUnit& t, int64_t tok)
+{
+    const int64_t last = min(tok + a.tile_tokens, a.s.Sq) - 1;
+    const int64_t keys = min(t.len, t.pos0 + last + 1);
+    return tok >= a.s.Sq || keys <= 0 ? 0 : (keys + kAttnRows - 1) / kAttnRows;
+}
 
 __device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
 {
@@ -100,28 +116,47 @@ __device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
     t.len = s.Skv;
     if (s.kv_lens) t.len = min(s.Skv, int64_t(max(0, s.kv_lens[t.bb])));
     t.pos0 = s.causal ? (s.q_start ? int64_t(s.q_start[t.bb]) : 0) : s.Skv;
-    int64_t blocks[2];
-    for (int k = 0; k < 2; ++k) {
-        t.tok[k] = (qb * 2 + k) * a.tile_tokens;
-        const int64_t last = min(t.tok[k] + a.tile_tokens, s.Sq) - 1;
-        int64_t keys = min(t.len, t.pos0 + last + 1);
-        if (t.tok[k] >= s.Sq || keys < 0) keys = 0;
-        blocks[k] = (keys + kAttnRows - 1) / kAttnRows;
+    if (a.paired) {
+        t.tok0 = t.tok1 = 0;
+        const int64_t total = af_blocks(a, t, 0);
+        const int64_t per = (total + a.parts - 1) / a.parts;
+        t.lo0 = (2 * t.sp) * per;
+        t.lo1 = t.lo0 + per;
+        t.n0 = int(max(int64_t(0), min(total - t.lo0, per)));
+        t.n1 = int(max(int64_t(0), min(total - t.lo1, per)));
+    } else {
+        t.tok0 = qb * 2 * a.tile_tokens;
+        t.tok1 = t.tok0 + a.tile_tokens;
+        const int64_t b0 = af_blocks(a, t, t.tok0), b1 = af_blocks(a, t, t.tok1);
+        const int64_t total = max(b0, b1);
+        const int64_t per = (total + a.splits - 1) / a.splits;
+        t.lo0 = t.lo1 = t.sp * per;
+        t.n0 = int(max(int64_t(0), min(b0 - t.lo0, per)));
+        t.n1 = int(max(int64_t(0), min(b1 - t.lo1, per)));
     }
-    const int64_t total = max(blocks[0], blocks[1]);
-    const int64_t per = (total + a.splits - 1) / a.splits;
-    t.lo = t.sp * per;
-    const int64_t hi = min(total, t.lo + per);
-    for (int k = 0; k < 2; ++k) t.n[k] = int(max(int64_t(0), min(blocks[k], hi) - t.lo));
     return t;
 }
 
-template <int DP, bool F16>
+// The CTA's next unit with any work at or after *u (false: none).
+__device__ __forceinline__ bool af_next(const AttnFwdArgs& a, int64_t* u, AfUnit* t)
+{
+    for (; *u < a.units; *u += gridDim.x) {
+        *t = af_unit(a, *u);
+        if (t->most() > 0) {
+            *u += gridDim.x;
+            return true;
+        }
+    }
+    return false;
+}
+
+template <int DP, bool F16, bool PAIRED>
 __global__ void __launch_bounds__(kAfThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnFwdArgs a)
 {
     using L = AfSmem<DP>;
     using E = ElemT<F16>;
+    constexpr int K = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -137,12 +172,12 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             mbar_init(&bars.q_full[t], 1);
             mbar_init(&bars.q_empty[t], 1);
             mbar_init(&bars.s_full[t], 1);
+            mbar_init(&bars.p_half[t], 4);
             mbar_init(&bars.p_ready[t], 4);
             mbar_init(&bars.o_full[t], 1);
             mbar_init(&bars.o_free[t], 4);
-            mbar_init(&bars.o_staged[t], 4);
         }
-        for (int k = 0; k < L::kStages; ++k) {
+        for (int k = 0; k < K; ++k) {
             mbar_init(&bars.kv_full[k], 1);
             mbar_init(&bars.kv_empty[k], 1);
         }
@@ -156,166 +191,236 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
 
-    if (warp == kAfLoadWarp) {
-        if (lane == 0) {
+    if (warp >= kAfLoadWarp) {
+        regs_shrink<kAfRegsOther>();
+        if (warp == kAfLoadWarp && lane == 0) {
             StageRing ring;
             uint32_t uses[2] = {0, 0};
             int64_t issued = 0;
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
-            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-                const AfUnit t = af_unit(a, u);
-                for (int k = 0; ok && k < 2; ++k) {
-                    if (t.n[k] == 0) continue;
+            auto queries = [&](const AfUnit& t) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (!ok || t.n(k) == 0) continue;
                     if (uses[k] > 0) ok = wait_or_dead(&bars.q_empty[k], (uses[k] - 1) & 1, dead);
-                    if (!ok) break;
+                    if (!ok) continue;
                     mbar_arrive_expect_tx(&bars.q_full[k], q_bytes);
                     for (int h = 0; h < halves; ++h)
                         tensor_g2s_4d(smem + L::kQ + k * L::kTile + h * L::kHalf, &a.qmap[t.r],
-                                      64 * h, t.kvh * s.group, int(t.tok[k]), t.bb, &bars.q_full[k]);
+                                      64 * h, t.kvh * s.group, int(t.tok(k)), t.bb, &bars.q_full[k]);
                     ++uses[k];
                 }
-                const int n = max(t.n[0], t.n[1]);
-                for (int j = 0; ok && j < 2 * n; ++j) {  // K0 V0 K1 V1 ...
-                    if (issued >= L::kStages)
-                        ok = wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, dead);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&bars.kv_full[ring.s], kv_bytes);
-                    const CUtensorMap* map = (j & 1) ? &a.vmap[t.r] : &a.kmap[t.r];
-                    for (int h = 0; h < halves; ++h)
-                        tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf, map, 64 * h,
-                                      t.kvh, int((t.lo + (j >> 1)) * kAttnRows), t.bb,
-                                      &bars.kv_full[ring.s]);
-                    ++issued;
-                    ring.next(L::kStages);
+            };
+            auto block = [&](const CUtensorMap* map, const AfUnit& t, int64_t at) {
+                if (!ok) return;
+                if (issued >= K) ok = wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, dead);
+                if (!ok) return;
+                mbar_arrive_expect_tx(&bars.kv_full[ring.s], kv_bytes);
+                for (int h = 0; h < halves; ++h)
+                    tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf, map, 64 * h,
+                                  t.kvh, int(at * kAttnRows), t.bb, &bars.kv_full[ring.s]);
+                ++issued;
+                ring.next(K);
+            };
+            int64_t u = blockIdx.x;
+            AfUnit t, next;
+            bool live = af_next(a, &u, &t);
+            if (live) {
+                queries(t);
+                if (PAIRED) {
+                    if (t.n0 > 0) block(&a.kmap[t.r], t, t.lo0);
+                    if (t.n1 > 0) block(&a.kmap[t.r], t, t.lo1);
                 }
             }
+            while (live && ok) {
+                const bool more = af_next(a, &u, &next);
+                const int n = t.most();
+                if constexpr (PAIRED) {  // the order of the products: V of a block, K of the next
+                    for (int j = 0; ok && j < n; ++j) {
+                        if (j + 1 == n && more) queries(next);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (j < t.n(k)) block(&a.vmap[t.r], t, t.lo(k) + j);
+                            if (j + 1 < t.n(k))
+                                block(&a.kmap[t.r], t, t.lo(k) + j + 1);
+                            else if (j + 1 == n && more && next.n(k) > 0)
+                                block(&a.kmap[next.r], next, next.lo(k));
+                        }
+                    }
+                } else {
+                    for (int j = 0; ok && j < n; ++j) {  // K0 V0 K1 V1 ...
+                        block(&a.kmap[t.r], t, t.lo0 + j);
+                        block(&a.vmap[t.r], t, t.lo0 + j);
+                    }
+                    if (more) queries(next);
+                }
+                t = next;
+                live = more;
+            }
             // leave no copy into this CTA's shared memory in flight
-            for (int64_t k = max(int64_t(0), issued - L::kStages); k < issued; ++k)
-                if (!mbar_wait_bounded(&bars.kv_full[k % L::kStages], uint32_t((k / L::kStages) & 1)))
+            for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k)
+                if (!mbar_wait_bounded(&bars.kv_full[k % K], uint32_t((k / K) & 1)))
                     atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
             for (int k = 0; k < 2; ++k)
                 if (uses[k] > 0 && !mbar_wait_bounded(&bars.q_full[k], (uses[k] - 1) & 1))
                     atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
-        }
-        __syncwarp();
-    } else if (warp == kAfMmaWarp) {
-        const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
-        const uint32_t id_o = tc_idesc(F16, 16 * nk, true);
-        const uint32_t q_at = smem_u32(smem + L::kQ), ring_at = smem_u32(smem + L::kRing);
-        StageRing ring;
-        uint32_t uses[2] = {0, 0}, blocks[2] = {0, 0};
-        bool ok = true;
-        auto all = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
-        };
-        auto scores = [&](int t, uint32_t k_addr) {  // S_t = Q_t K^T
-            for (int ks = 0; ks < nk; ++ks) {
-                const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
-                tc_mma_ss(tmem + kAfS + t * 128, tc_desc_k(q_at + t * L::kTile + off),
-                          tc_desc_k(k_addr + off), id_s, ks > 0);
-            }
-            tc_commit(&bars.s_full[t]);
-        };
-        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-            const AfUnit t = af_unit(a, u);
-            const int n = max(t.n[0], t.n[1]);
-            if (n == 0) continue;
-            for (int k = 0; ok && k < 2; ++k)
-                if (t.n[k] > 0) ok = all(&bars.q_full[k], uses[k] & 1);
-            ok = ok && all(&bars.kv_full[ring.s], ring.phase);
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
-                for (int k = 0; k < 2; ++k)
-                    if (t.n[k] > 0) scores(k, ring_at + ring.s * L::kTile);
-                tc_commit(&bars.kv_empty[ring.s]);
-            }
-            ring.next(L::kStages);
-            for (int j = 0; ok && j < n; ++j) {
-                const int vs = ring.s;
-                ok = all(&bars.kv_full[vs], ring.phase);
-                if (!ok) break;
-                // A masked probability is zero, but zero times whatever lies past the last key
-                // may be NaN: the block's rows past it become zeros.
-                const int64_t past = t.len - (t.lo + j) * kAttnRows;
-                if (past < kAttnRows && t.len < s.Skv) {
-                    const int rows = kAttnRows - int(past), words = rows * 8;
-                    for (int h = 0; h < halves; ++h)
-                        for (int w = lane; w < words; w += 32)
-                            st_shared_v4(smem + L::kRing + vs * L::kTile + h * L::kHalf +
-                                             int(past) * 128 + w * 16,
-                                         make_uint4(0, 0, 0, 0));
-                    fence_proxy_async_shared();
-                    __syncwarp();
+        } else if (warp == kAfMmaWarp) {
+            const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
+            const uint32_t id_o = tc_idesc(F16, 16 * nk, true);
+            const uint32_t q_at = smem_u32(smem + L::kQ), ring_at = smem_u32(smem + L::kRing);
+            StageRing ring;
+            uint32_t uses[2] = {0, 0}, blocks[2] = {0, 0};
+            bool ok = true;
+            auto all = [&](uint64_t* bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+            };
+            auto scores = [&](int k, int stage, bool last) {  // S_k = Q_k K^T
+                if (elect_one()) {
+                    const uint32_t k_addr = ring_at + stage * L::kTile;
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) {
+                        if (ks >= nk) break;
+                        const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
+                        tc_mma_ss(tmem + kAfS + k * 128, tc_desc_k(q_at + k * L::kTile + off),
+                                  tc_desc_k(k_addr + off), id_s, ks > 0);
+                    }
+                    tc_commit(&bars.s_full[k]);
+                    if (last) tc_commit(&bars.q_empty[k]);  // the tile's queries are done with
                 }
-                ring.next(L::kStages);
-                const int ks_stage = ring.s;
-                const bool more = j + 1 < n;
-                if (more) {
-                    ok = all(&bars.kv_full[ks_stage], ring.phase);
-                    if (!ok) break;
-                    ring.next(L::kStages);
-                }
-                for (int k = 0; ok && k < 2; ++k) {
-                    if (j >= t.n[k]) continue;
-                    ok = all(&bars.p_ready[k], blocks[k] & 1);
-                    ++blocks[k];
-                    if (ok && j == 0 && uses[k] > 0) ok = all(&bars.o_free[k], (uses[k] - 1) & 1);
-                    if (!ok) break;
+            };
+            auto first_scores = [&](const AfUnit& t, int k, int stage) {  // of a unit
+                ok = ok && all(&bars.q_full[k], uses[k] & 1);
+                if (!ok) return;
+                tc_fence_after();
+                scores(k, stage, t.n(k) == 1);
+            };
+            // A masked probability is zero, but zero times whatever lies past the last key may
+            // be NaN: a value block's rows past it become zeros.
+            auto clear_past = [&](const AfUnit& t, int stage, int64_t at) {
+                const int64_t past = t.len - at * kAttnRows;
+                if (past >= kAttnRows || t.len >= s.Skv) return;
+                const int words = (kAttnRows - int(past)) * 8;
+                for (int h = 0; h < halves; ++h)
+                    for (int w = lane; w < words; w += 32)
+                        st_shared_v4(smem + L::kRing + stage * L::kTile + h * L::kHalf +
+                                         int(past) * 128 + w * 16,
+                                     make_uint4(0, 0, 0, 0));
+                fence_proxy_async_shared();
+                __syncwarp();
+            };
+            auto output = [&](const AfUnit& t, int k, int stage, int j) {  // O_k += P_k V
+                ok = all(&bars.p_half[k], blocks[k] & 1);
+                if (ok && j == 0 && uses[k] > 0) ok = all(&bars.o_free[k], (uses[k] - 1) & 1);
+                if (!ok) return;
+                const uint32_t v_addr = ring_at + stage * L::kTile;
+                auto half = [&](int from) {
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t v_addr = ring_at + vs * L::kTile;
-                        for (int ks = 0; ks < kAttnRows / 16; ++ks)
+                    if (elect_one())
+#pragma unroll
+                        for (int ks = from; ks < from + 4; ++ks)
                             tc_mma_ts(tmem + kAfO + k * 128, tmem + kAfS + k * 128 + ks * 8,
                                       tc_desc_mn(v_addr + ks * 2048, L::kHalf), id_o,
                                       j > 0 || ks > 0);
-                        if (j + 1 < t.n[k])
-                            scores(k, ring_at + ks_stage * L::kTile);
-                        else
-                            tc_commit(&bars.o_full[k]);
-                    }
-                }
-                if (ok && lane == 0) {
-                    tc_commit(&bars.kv_empty[vs]);
-                    if (more) tc_commit(&bars.kv_empty[ks_stage]);
-                }
-                __syncwarp();
-            }
-            for (int k = 0; k < 2; ++k) uses[k] += t.n[k] > 0;
-        }
-        // every product complete before tensor memory is given back
-        if (lane == 0) {
-            tc_commit(&bars.drain);
-            if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
-        }
-        __syncwarp();
-    } else if (warp == kAfStoreWarp) {
-        if (lane == 0) {
-            uint32_t uses[2] = {0, 0};
-            bool ok = true;
-            for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-                const AfUnit t = af_unit(a, u);
-                for (int k = 0; ok && k < 2; ++k) {
-                    if (t.n[k] == 0) continue;
-                    ok = wait_or_dead(&bars.o_staged[k], uses[k] & 1, dead);
-                    if (!ok) break;
-                    if (a.splits == 1) {
-                        for (int h = 0; h < halves; ++h)
-                            tensor_s2g_4d(&a.omap[t.r], 64 * h, t.kvh * s.group, int(t.tok[k]), t.bb,
-                                          smem + L::kQ + k * L::kTile + h * L::kHalf);
-                        bulk_commit();
-                        bulk_wait_read<0>();
-                    }
-                    mbar_arrive(&bars.q_empty[k]);
+                };
+                half(0);
+                ok = all(&bars.p_ready[k], blocks[k] & 1);
+                if (!ok) return;
+                half(4);
+                ++blocks[k];
+                if (j + 1 == t.n(k)) {
+                    if (elect_one()) tc_commit(&bars.o_full[k]);
                     ++uses[k];
                 }
+            };
+            auto stage_ready = [&]() { return ok = ok && all(&bars.kv_full[ring.s], ring.phase); };
+            auto release = [&](int stage) {
+                if (ok && elect_one()) tc_commit(&bars.kv_empty[stage]);
+            };
+            int64_t u = blockIdx.x;
+            AfUnit t, next;
+            bool live = af_next(a, &u, &t);
+            if (live) {  // the first unit's first scores
+                if (!PAIRED) stage_ready();
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (t.n(k) == 0) continue;
+                    if (PAIRED) stage_ready();
+                    first_scores(t, k, ring.s);
+                    if (PAIRED) {
+                        release(ring.s);
+                        ring.next(K);
+                    }
+                }
+                if (!PAIRED) {
+                    release(ring.s);
+                    ring.next(K);
+                }
             }
-            bulk_wait<0>();
+            while (live && ok) {
+                const bool more = af_next(a, &u, &next);
+                const int n = t.most();
+                for (int j = 0; ok && j < n; ++j) {
+                    const bool last = j + 1 == n;
+                    if constexpr (PAIRED) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (ok && j < t.n(k)) {
+                                if (!stage_ready()) break;
+                                clear_past(t, ring.s, t.lo(k) + j);
+                                output(t, k, ring.s, j);
+                                release(ring.s);
+                                ring.next(K);
+                            }
+                            const bool same = j + 1 < t.n(k);
+                            if (ok && (same || (last && more && next.n(k) > 0))) {
+                                if (!stage_ready()) break;
+                                if (same)
+                                    scores(k, ring.s, j + 2 == t.n(k));
+                                else
+                                    first_scores(next, k, ring.s);
+                                release(ring.s);
+                                ring.next(K);
+                            }
+                        }
+                    } else {
+                        const int vs = ring.s;
+                        if (!stage_ready()) break;
+                        clear_past(t, vs, t.lo0 + j);
+                        ring.next(K);
+                        const int ks = ring.s;
+                        const bool any = !last || more;
+                        if (any) {
+                            if (!stage_ready()) break;
+                            ring.next(K);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if (ok && j < t.n(k)) output(t, k, vs, j);
+                            if (ok && j + 1 < t.n(k))
+                                scores(k, ks, j + 2 == t.n(k));
+                            else if (ok && last && more && next.n(k) > 0)
+                                first_scores(next, k, ks);
+                        }
+                        release(vs);
+                        if (any) release(ks);
+                    }
+                    __syncwarp();
+                }
+                t = next;
+                live = more;
+            }
+            // every product complete before tensor memory is given back
+            if (elect_one()) {
+                tc_commit(&bars.drain);
+                if (!mbar_wait_bounded(&bars.drain, 0))
+                    atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
+            }
         }
         __syncwarp();
     } else {  // softmax: tile w = warp / 4, one row a thread
+        regs_grow<kAfRegsSoftmax>();
         const int tile = warp >> 2;
         const int row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
@@ -323,31 +428,34 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         const uint32_t o_at = tmem + lanes + kAfO + tile * 128;
         const int tok_in = row / s.group, head_in = row - tok_in * s.group;
         const float sl2 = s.scale * 1.4426950408889634f;  // scores to powers of two
-        uint8_t* stage = smem + L::kQ + tile * L::kTile + row * 128;
         uint32_t uses = 0, blocks = 0;
         bool ok = true;
         auto all = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
         };
+        auto arrive = [&](uint64_t* bar) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
         for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
             const AfUnit t = af_unit(a, u);
-            const int64_t tok = t.tok[tile] + tok_in;
+            const int64_t tok = t.tok(tile) + tok_in;
             const bool valid = tok_in < a.tile_tokens && tok < s.Sq;
-            const int n = t.n[tile];
-            // this row's log-sum-exp, and its row over all ranks
-            const int64_t row_r =
-                (int64_t(t.bb) * s.n[t.r] + t.kvh * s.group + head_in) * s.Sq + tok;
-            const int64_t row_all = s.row_begin[t.r] + row_r;
-            float* lse = a.splits == 1 ? a.lse[t.r] + row_r
-                                       : a.part_lse + t.sp * s.row_begin[s.W] + row_all;
-            uint8_t* o_row = a.splits == 1
-                                 ? a.o[t.r] + ((int64_t(t.bb) * s.Sq + tok) * s.n[t.r] +
-                                               t.kvh * s.group + head_in) * s.d * 2
-                                 : nullptr;
+            const int n = t.n(tile);
+            const int part = PAIRED ? 2 * t.sp + tile : t.sp;
+            // this row's log-sum-exp and output, or its part of them
+            const int head = t.kvh * s.group + head_in;
+            const int64_t row_r = (int64_t(t.bb) * s.n[t.r] + head) * s.Sq + tok;
+            const int64_t row_part = part * s.row_begin[s.W] + s.row_begin[t.r] + row_r;
+            const bool whole = a.parts == 1;
+            float* lse = whole ? a.lse[t.r] + row_r : a.part_lse + row_part;
+            uint8_t* o_row = a.o[t.r] + ((int64_t(t.bb) * s.Sq + tok) * s.n[t.r] + head) * s.d * 2;
             if (n == 0) {  // nothing visible to any row of the tile
                 if (valid) {
                     *lse = -INFINITY;
-                    if (o_row)
+                    if (whole)
                         for (int c = 0; c < s.d * 2; c += 16)
                             st_v4(o_row + c, make_uint4(0, 0, 0, 0));
                 }
@@ -365,7 +473,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, x[q]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_wait_ld(x[q]);
-                const int64_t left = lim - (t.lo + j) * kAttnRows;  // visible keys of this block
+                const int64_t left = lim - (t.lo(tile) + j) * kAttnRows;  // visible keys of the block
                 if (__any_sync(0xffffffffu, left < kAttnRows)) {
                     const int seen = int(max(int64_t(0), min(left, int64_t(kAttnRows))));
 #pragma unroll
@@ -376,10 +484,11 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 float mx[4] = {m, m, m, m};
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
+                for (int c = 0; c < 32; c += 2)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(x[q][c]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int q = 0; q < 4; ++q)
+                        mx[q] = max3(mx[q], __uint_as_float(x[q][c]), __uint_as_float(x[q][c + 1]));
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 const bool grow = (top - m) * sl2 > kAfRescale;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? ex2((m - top) * sl2) : 1.0f;
@@ -415,53 +524,45 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                         p[i] = E::pack(e.x, e.y);
                     }
                     tmem_st16(s_at + q * 16, p);
+                    if (q == 1) arrive(&bars.p_half[tile]);
                 }
+                arrive(&bars.p_ready[tile]);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_ready[tile]);
             }
             if (!ok) break;
             ok = all(&bars.o_full[tile], uses & 1);
             if (!ok) break;
             tc_fence_after();
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays NaN
+            if (valid) *lse = l == 0.0f ? -INFINITY : m * s.scale + logf(l);
+            float* o_part = a.part_o + row_part * s.d;
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t y[32];
                 tmem_ld32(o_at + c * 32, y);
                 tmem_wait_ld(y);
-                if (a.splits == 1) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = E::pack(__uint_as_float(y[8 * i + 2 * k]) * inv,
-                                           __uint_as_float(y[8 * i + 2 * k + 1]) * inv);
-                        const int word = (c & 1) * 4 + i;  // 16-byte word of the tile row
-                        st_shared_v4(stage + (c >> 1) * L::kHalf + ((word ^ (row & 7)) << 4),
-                                     make_uint4(w[0], w[1], w[2], w[3]));
-                    }
-                } else if (valid) {
-                    float* dst = a.part_o + (t.sp * s.row_begin[s.W] + row_all) * s.d + c * 32;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c * 32 + i * 4 < s.d)
-                            *reinterpret_cast<float4*>(dst + i * 4) = make_float4(
-                                __uint_as_float(y[4 * i]) * inv, __uint_as_float(y[4 * i + 1]) * inv,
-                                __uint_as_float(y[4 * i + 2]) * inv,
-                                __uint_as_float(y[4 * i + 3]) * inv);
+                if (c == DP / 32 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.o_free[tile]);
                 }
-            }
-            if (valid) *lse = l == 0.0f ? -INFINITY : m * s.scale + logf(l);
-            tc_fence_before();
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars.o_free[tile]);
-                mbar_arrive(&bars.o_staged[tile]);
+                if (!valid) continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // eight columns
+                    if (c * 32 + i * 8 >= s.d) continue;
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(y[8 * i + k]) * inv;
+                    if (whole) {
+                        st_v4(o_row + (c * 32 + i * 8) * 2,
+                              make_uint4(E::pack(v[0], v[1]), E::pack(v[2], v[3]),
+                                         E::pack(v[4], v[5]), E::pack(v[6], v[7])));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(o_part + c * 32 + i * 8);
+                        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    }
+                }
             }
             ++uses;
         }
@@ -482,10 +583,10 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     for (int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5); row < rows;
          row += int64_t(gridDim.x) * 4) {
         float top = -INFINITY;
-        for (int p = 0; p < a.splits; ++p) top = fmaxf(top, a.part_lse[p * rows + row]);
+        for (int p = 0; p < a.parts; ++p) top = fmaxf(top, a.part_lse[p * rows + row]);
         float sum = 0.0f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < a.splits; ++p) {
+        for (int p = 0; p < a.parts; ++p) {
             const float z = a.part_lse[p * rows + row];
             if (z == -INFINITY) continue;  // an empty part wrote no output
             const float w = expf(z - top);
@@ -512,39 +613,56 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     }
 }
 
-// Parts of the keys: as many as still fit one wave of the SMs, each with four blocks of keys at
-// least (a part costs its start, an fp32 output and a share of the join).
-int attn_fwd_splits(const AttnShape& s, int64_t units, int sm_count)
+// Row tiles, units and parts of the keys. Where one tile holds all rows, a CTA's two tiles take a
+// part each. The keys are split further while the units still fit one wave of the SMs and a part
+// keeps four blocks (a part costs its start, an fp32 output and a share of the join).
+void attn_fwd_split(AttnFwdArgs* a, int sm_count)
 {
-    if (units <= 0) return 1;
+    const AttnShape& s = a->s;
+    a->tile_tokens = kAttnRows / s.group;
+    const int64_t pair = 2 * int64_t(a->tile_tokens);
     const int64_t blocks = (s.Skv + kAttnRows - 1) / kAttnRows;
-    int64_t n = sm_count / units;
-    if (n > blocks / 4) n = blocks / 4;
+    a->paired = s.Sq <= a->tile_tokens && blocks > 1;
+    a->q_blocks = a->paired ? 1 : (s.Sq + pair - 1) / pair;
+    const int64_t base = s.head_begin[s.W] * a->q_blocks;
+    int64_t n = base > 0 ? sm_count / base : 1;
+    const int64_t most = blocks / (a->paired ? 8 : 4);
+    if (n > most) n = most;
     if (n > 64) n = 64;
-    return n < 2 ? 1 : int(n);
+    if (n < 1) n = 1;
+    a->splits = int32_t(n);
+    a->parts = a->paired ? 2 * a->splits : a->splits;
+    a->units = base * a->splits;
 }
 
-template <int DP, bool F16>
-static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int device, int grid)
+template <int DP, bool F16, bool PAIRED>
+static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int device, int grid)
 {
     static std::atomic<unsigned long long> raised{0};
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
     constexpr int smem = AfSmem<DP>::kTotal + 1024;
     if (bit && !(raised.load() & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, F16>,
+        cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, F16, PAIRED>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit);
     }
-    attn_fwd_kernel<DP, F16><<<grid, kAfThreads, smem, stream>>>(a);
+    attn_fwd_kernel<DP, F16, PAIRED><<<grid, kAfThreads, smem, stream>>>(a);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || a.splits == 1) return e;
+    if (e != cudaSuccess || a.parts == 1) return e;
     const int64_t blocks = (a.s.row_begin[a.s.W] + 3) / 4;
     attn_join_kernel<F16><<<unsigned(blocks < 1 << 16 ? blocks : 1 << 16), 128, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
-// One launch over all ranks (and the join); `grid` CTAs at most. The shape, outputs, splits and
+template <int DP, bool F16>
+static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int device, int grid)
+{
+    return a.paired ? af_launch_mode<DP, F16, true>(a, stream, device, grid)
+                    : af_launch_mode<DP, F16, false>(a, stream, device, grid);
+}
+
+// One launch over all ranks (and the join); `grid` CTAs at most. The shape, outputs, parts and
 // their buffers are set in `a`.
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
                             const void* const* v, cudaStream_t stream, int device, int grid)
@@ -554,11 +672,8 @@ cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* co
     for (int r = 0; r < s.W; ++r) {
         if (s.n[r] == 0) continue;
         if (!encode_head_map(&a.qmap[r], q[r], s.f16, s.d, s.n[r], s.Sq, s.b, s.group, a.tile_tokens) ||
-            !encode_head_map(&a.omap[r], a.o[r], s.f16, s.d, s.n[r], s.Sq, s.b, s.group,
-                             a.tile_tokens) ||
-            (s.Skv > 0 &&
-             (!encode_head_map(&a.kmap[r], k[r], s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows) ||
-              !encode_head_map(&a.vmap[r], v[r], s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows))))
+            !encode_head_map(&a.kmap[r], k[r], s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows) ||
+            !encode_head_map(&a.vmap[r], v[r], s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows))
             return cudaErrorInvalidValue;
     }
     if (int64_t(grid) > a.units) grid = int(a.units);

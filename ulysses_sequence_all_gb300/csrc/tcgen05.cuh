@@ -16,6 +16,17 @@ namespace uly {
 
 constexpr int kTmemColumns = 512;
 
+// True in one lane of a converged warp, the same one every time. Products, their commits and tensor
+// copies are issued behind it: the compiler then knows that a single lane runs and keeps their
+// operands in uniform registers (behind `lane == 0` each product took about 100 cycles to issue).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 // One warp allocates all of an SM's tensor memory; the base address arrives in shared memory.
 __device__ __forceinline__ void tmem_alloc(uint32_t* where)
 {
@@ -146,6 +157,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The largest of three in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// Registers a thread from here on, for every warp of a warpgroup (the shares of all warpgroups
+// add up to what the block was launched with).
+template <int N>
+__device__ __forceinline__ void regs_grow()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_shrink()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 // 2^x (subnormal results flushed to zero).
 __device__ __forceinline__ float ex2(float x)
