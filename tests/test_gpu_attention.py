@@ -151,6 +151,28 @@ def test_ragged_keys_and_what_lies_past_them(shape, causal):
         q, k, v = inputs(*shape, dtype, seed=5)
 
 
+@pytest.mark.parametrize("ctas", [1, 3, 0])
+@pytest.mark.parametrize("shape", [(2, 6, 300, 1300, [1, 2], 2, 64), (1, 6, 1, 2600, [3], 2, 128)],
+                         ids=["tiles", "token"])
+def test_many_ragged_units_on_few_ctas(shape, ctas):
+    """Each CTA runs through many units of different lengths, its ring of stages round many times,
+    with NaN past the keys of every batch element."""
+    W, b, sq, skv, kv_heads, g, d = shape
+    qp, kp = plans(*shape, torch.bfloat16)
+    B.ulysses_plan_set_max_ctas(qp, ctas)
+    for seed, lens in enumerate(((1300, 100, 5, 900, 0, 1299), (640, 1280, 1, 2, 130, 129))):
+        q, k, v = inputs(*shape, torch.bfloat16, seed=seed)
+        n = i32(*lens)
+        for t in (k, v):
+            for x in t:
+                for bb, m in enumerate(lens):
+                    x[bb, m:] = math.nan
+        for kw in ({"kv_lens": n}, {"kv_lens": n, "causal": True}):
+            o, lse = attend(qp, kp, q, k, v, 0.2, **kw)
+            check(q, [torch.nan_to_num(x, 0, 0, 0) for x in k],
+                  [torch.nan_to_num(x, 0, 0, 0) for x in v], o, lse, 0.2, **kw)
+
+
 def test_causal_start_beyond_and_before_the_keys():
     shape = (1, 4, 40, 200, [1], 1, 64)
     qp, kp = plans(*shape, torch.bfloat16)

@@ -137,6 +137,28 @@ def test_ragged_keys_and_what_lies_past_them(shape, causal):
                     assert bool((x[bb, max(0, m):] == 0).all())
 
 
+@pytest.mark.parametrize("ctas", [1, 3, 0])
+def test_many_ragged_units_on_few_ctas(ctas):
+    """Each CTA runs through many units of different lengths, its rings of stages round many times,
+    with NaN past the keys of every batch element."""
+    shape = (2, 6, 300, 900, [1, 2], 3, 64)
+    W, b, sq, skv, kv_heads, g, d = shape
+    qp, kp = plans(*shape, torch.float16)
+    B.ulysses_plan_set_max_ctas(qp, ctas)
+    for seed, lens in enumerate(((900, 100, 5, 800, 0, 899), (640, 768, 1, 2, 130, 129))):
+        q, k, v = inputs(*shape, torch.float16, seed=seed)
+        n = i32(*lens)
+        for kw in ({"kv_lens": n}, {"kv_lens": n, "causal": True}):
+            o, lse, go = given(q, k, v, 0.2, **kw)
+            dirty = [[x.clone() for x in t] for t in (k, v)]
+            for t in dirty:
+                for x in t:
+                    for bb, m in enumerate(lens):
+                        x[bb, m:] = math.nan
+            got = gradients(qp, kp, q, *dirty, o, lse, go, 0.2, **kw)
+            check(got, q, k, v, o, lse, go, 0.2, **kw)
+
+
 def test_same_bits_every_time():
     shape = (2, 2, 300, 700, [1, 2], 2, 128)
     qp, kp = plans(*shape, torch.bfloat16)

@@ -957,7 +957,10 @@ size_t attn_bwd_setup(AttnBwdArgs* a)
     const AttnShape& s = a->s;
     a->tile_tokens = kAttnRows / s.group;
     a->q_tiles = (s.Sq + a->tile_tokens - 1) / a->tile_tokens;
-    a->k_blocks = (s.Skv + kAttnRows - 1) / kAttnRows;
+    const int64_t heads = s.head_begin[s.W];
+    a->q_order = {heads, a->q_tiles, attn_order_group(s, heads, s.Skv * s.d * 4)};
+    a->kv_order = {heads, (s.Skv + kAttnRows - 1) / kAttnRows,
+                   attn_order_group(s, heads, s.Sq * s.group * s.d * 4)};
     return size_t(s.head_begin[s.W]) * size_t(a->q_tiles) * 2 * kAttnRows * sizeof(float);
 }
 

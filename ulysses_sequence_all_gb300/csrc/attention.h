@@ -12,6 +12,9 @@
 #include <cstdint>
 
 #include "plan.h"
+#ifdef __CUDACC__
+#include "ptx.cuh"
+#endif
 
 namespace uly {
 
@@ -33,14 +36,39 @@ struct AttnShape {
     float scale;
 };
 
+// Order of the units of a kernel: groups of `group` heads, in a group by block (the longest first
+// when they differ), then by head. Waves of the grid run back and forth over it, which evens out
+// units whose length falls along the order. A group's shared operands fit the L2 cache.
+struct AttnOrder {
+    int64_t heads, blocks, group;
+};
+
+#ifdef __CUDACC__
+__device__ __forceinline__ int64_t attn_unit_at(int64_t wave)
+{
+    const int64_t c = (wave & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    return wave * gridDim.x + c;
+}
+
+__device__ __forceinline__ void attn_order(const AttnOrder& o, int64_t u, int64_t* head,
+                                           int64_t* block)
+{
+    const int64_t per = o.group * o.blocks;
+    const int64_t g = per > u ? 0 : div_fast(u, per);
+    const int64_t at = u - g * per, heads = min(o.group, o.heads - g * o.group);
+    *block = heads == 1 ? at : div_fast(at, heads);
+    *head = g * o.group + (at - *block * heads);
+}
+#endif
+
 struct AttnFwdArgs {
     AttnShape s;
     CUtensorMap qmap[kMaxW], kmap[kMaxW], vmap[kMaxW];
     uint8_t* o[kMaxW];
     float* lse[kMaxW];  // (b, n_r, Sq)
     int32_t tile_tokens;
-    int64_t q_blocks;   // pairs of row tiles along the tokens
-    int64_t units;      // (rank, batch, key head) x q_blocks x splits
+    AttnOrder order;    // (rank, batch, key head) x pairs of row tiles along the tokens
+    int64_t units;      // the same, x splits
     int32_t splits;     // units along the keys
     int32_t paired;     // a unit's two tiles are the same rows, each with its own part of the keys
     int32_t parts;      // parts of the keys (splits, or twice as many when paired)
@@ -50,8 +78,8 @@ struct AttnFwdArgs {
 
 struct AttnBwdArgs {
     AttnShape s;
-    CUtensorMap qmap[kMaxW], gmap[kMaxW], dqmap[kMaxW];  // boxes of a row tile: q, dO, dq
-    CUtensorMap kmap[kMaxW], vmap[kMaxW], dkmap[kMaxW], dvmap[kMaxW];  // boxes of a key block
+    CUtensorMap qmap[kMaxW], gmap[kMaxW];  // boxes of a row tile: q, dO
+    CUtensorMap kmap[kMaxW], vmap[kMaxW];  // boxes of a key block
     const uint8_t* o[kMaxW];
     const uint8_t* go[kMaxW];
     const float* lse[kMaxW];
@@ -59,11 +87,15 @@ struct AttnBwdArgs {
     uint8_t* dk[kMaxW];
     uint8_t* dv[kMaxW];
     int32_t tile_tokens;
-    int64_t q_tiles, k_blocks;  // row tiles along the tokens, key blocks
+    int64_t q_tiles;              // row tiles along the tokens
+    AttnOrder q_order, kv_order;  // (rank, batch, key head) x row tiles, x key blocks
     float* stats;  // [(rank, batch, key head)][q_tiles][2][128]: lse in powers of two, delta
 };
 
 // Host side.
+// Heads in a group: where blocks differ in length (causal), as many as hold `bytes` each within
+// about half of the L2 cache; else one (neighbouring CTAs then share a head's operands).
+int64_t attn_order_group(const AttnShape& s, int64_t heads, int64_t bytes);
 void attn_fwd_split(AttnFwdArgs* a, int sm_count);  // tiles, units and parts from the shape
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
                             const void* const* v, cudaStream_t stream, int device, int grid);

@@ -12,10 +12,12 @@
 // with no fp32 copy of it in memory, no atomics, and the same bits from run to run.
 //
 // Both are bound by the tensor cores. One CTA per SM (352 threads): warp 8 loads (swizzled tensor
-// maps), warp 9 issues the products, warp 10 stores, warps 0-3 and 4-7 turn scores into P and dS,
-// each the half of the tile's columns in its 128 threads' rows, while the products of the other
-// operand run. All accumulators are in tensor memory (fp32); P and dS go back to it rounded to the
-// element type, over the columns they came from, and are A operands there.
+// maps), one lane of warp 9 issues the products, warps 0-3 and 4-7 turn scores into P and dS, each
+// the half of the tile's columns in its 128 threads' rows, while the products of the other operand
+// run, and write the finished rows. A unit's first scores follow the last unit's products without a
+// gap. All accumulators are in tensor memory (fp32); P and dS go back to it rounded to the element
+// type, over the columns they came from, and are A operands there. Warp 10 of the dQ kernel zeroes
+// what a key block holds past a ragged batch element's last key.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,7 +36,7 @@ namespace uly {
 static __device__ unsigned g_attn_bwd_status;
 
 constexpr int kAbThreads = 352;
-constexpr int kAbLoadWarp = 8, kAbMmaWarp = 9, kAbStoreWarp = 10;
+constexpr int kAbLoadWarp = 8, kAbMmaWarp = 9, kAbCleanWarp = 10;
 constexpr int kAbStats = 2 * kAttnRows * 4;  // one tile's lse and D
 
 // Keys that batch element bb holds, and the position of its first query (beyond every key when the
@@ -99,6 +101,23 @@ __global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_consta
     }
 }
 
+// 32 columns from `col` on of an accumulator's row, times f, to the row of d elements at `out`.
+template <class E>
+__device__ __forceinline__ void ab_store32(uint8_t* out, int col, int d, const uint32_t (&y)[32],
+                                           float f)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (col + i * 8 >= d) continue;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[k] = E::pack(__uint_as_float(y[8 * i + 2 * k]) * f,
+                           __uint_as_float(y[8 * i + 2 * k + 1]) * f);
+        st_v4(out + (col + i * 8) * 2, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+}
+
 // ---- dK and dV ----------------------------------------------------------------------------------
 
 // Tensor memory columns. S^T (then P^T) and dP^T (then dS^T): lanes are keys, columns rows of q.
@@ -118,10 +137,10 @@ struct BkSmem {
 };
 
 struct BkBars {
-    uint64_t k_full, v_full, kv_empty[2];  // key block landed; its place's store has read it
+    uint64_t k_full, v_full, k_empty, v_empty;  // key block landed; its last scores have read it
     uint64_t q_full[4], q_empty[4], g_full[4], g_empty[4];
     uint64_t s_full, p_ready, dp_full, ds_ready;
-    uint64_t acc_full, acc_free[2], staged[2];
+    uint64_t acc_full, acc_free;
     uint64_t drain;
     uint32_t tmem;
     int dead;
@@ -138,8 +157,9 @@ __device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
 {
     const AttnShape& s = a.s;
     BkUnit t;
-    t.h = div_fast(u, a.k_blocks);
-    t.kv0 = (u - t.h * a.k_blocks) * kAttnRows;
+    int64_t block;
+    attn_order(a.kv_order, u, &t.h, &block);  // the first keys are seen by the most rows
+    t.kv0 = block * kAttnRows;
     ab_head(s, t.h, &t.r, &t.bb, &t.kvh);
     ab_limits(s, t.bb, &t.len, &t.pos0);
     // row i sees key kv0 when i >= kv0 - pos0
@@ -147,6 +167,22 @@ __device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
     t.first = row / a.tile_tokens;
     t.n = t.kv0 < t.len && t.first < a.q_tiles ? int(a.q_tiles - t.first) : 0;
     return t;
+}
+
+// The CTA's next unit with any work from *wave on (false: none).
+__device__ __forceinline__ bool bk_next(const AttnBwdArgs& a, int64_t units, int64_t* wave, BkUnit* t)
+{
+    for (; *wave * int64_t(gridDim.x) < units; ++*wave) {
+        const int64_t u = attn_unit_at(*wave);
+        if (u >= units) continue;
+        *t = bk_unit(a, u);
+        if (t->n > 0) {
+            ++*wave;
+            return true;
+        }
+    }
+    t->n = 0;
+    return false;
 }
 
 template <int DP, bool F16>
@@ -163,12 +199,14 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     const AttnShape& s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nk = (s.d + 15) / 16, halves = (s.d + 63) / 64;
-    const int64_t units = s.head_begin[s.W] * a.k_blocks;
+    const int64_t units = a.kv_order.heads * a.kv_order.blocks;
     constexpr int K = L::kStages;
 
     if (threadIdx.x == 0) {
         mbar_init(&bars.k_full, 1);
         mbar_init(&bars.v_full, 1);
+        mbar_init(&bars.k_empty, 1);
+        mbar_init(&bars.v_empty, 1);
         for (int k = 0; k < K; ++k) {
             mbar_init(&bars.q_full[k], 1);
             mbar_init(&bars.q_empty[k], 1);
@@ -180,11 +218,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.dp_full, 1);
         mbar_init(&bars.ds_ready, 8);
         mbar_init(&bars.acc_full, 1);
-        for (int k = 0; k < 2; ++k) {
-            mbar_init(&bars.kv_empty[k], 1);
-            mbar_init(&bars.acc_free[k], 4);
-            mbar_init(&bars.staged[k], 4);
-        }
+        mbar_init(&bars.acc_free, 8);
         mbar_init(&bars.drain, 1);
         bars.dead = 0;
         fence_barrier_init();
@@ -210,12 +244,12 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
-            for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const BkUnit t = bk_unit(a, u);
-                if (t.n == 0) continue;
+            int64_t wave = 0;
+            BkUnit t;
+            while (ok && bk_next(a, units, &wave, &t)) {
                 for (int w = 0; ok && w < 2; ++w) {
-                    // K's place is read by dK's store, V's by dV's
-                    if (uses > 0) ok = wait_or_dead(&bars.kv_empty[w], (uses - 1) & 1, dead);
+                    if (uses > 0)
+                        ok = wait_or_dead(w ? &bars.v_empty : &bars.k_empty, (uses - 1) & 1, dead);
                     if (!ok) break;
                     uint64_t* bar = w ? &bars.v_full : &bars.k_full;
                     mbar_arrive_expect_tx(bar, kv_bytes);
@@ -265,109 +299,88 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         }
         __syncwarp();
     } else if (warp == kAbMmaWarp) {
-        const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
-        const uint32_t id_d = tc_idesc(F16, 16 * nk, true);
-        const uint32_t k_at = smem_u32(smem + L::kK), v_at = smem_u32(smem + L::kV);
-        const uint32_t q_at = smem_u32(smem + L::kQ), g_at = smem_u32(smem + L::kG);
-        StageRing ring;
-        uint32_t uses = 0, tiles = 0;
-        bool ok = true;
-        auto all = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
-        };
-        auto scores = [&](uint32_t d, uint32_t key, uint32_t row, uint64_t* bar) {
-            if (elect_one()) {
+        if (elect_one()) {
+            const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
+            const uint32_t id_d = tc_idesc(F16, 16 * nk, true);
+            const uint64_t k_desc = tc_desc_k(smem_u32(smem + L::kK));
+            const uint64_t v_desc = tc_desc_k(smem_u32(smem + L::kV));
+            const uint64_t q_desc = tc_desc_k(smem_u32(smem + L::kQ));
+            const uint64_t g_desc = tc_desc_k(smem_u32(smem + L::kG));
+            const uint64_t qt_desc = tc_desc_mn(smem_u32(smem + L::kQ), L::kHalf);
+            const uint64_t gt_desc = tc_desc_mn(smem_u32(smem + L::kG), L::kHalf);
+            StageRing ring;
+            uint32_t uses = 0, tiles = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                return ok = ok && wait_or_dead(bar, parity, dead);
+            };
+            auto scores = [&](uint32_t d, uint64_t key, uint64_t row, uint64_t* bar) {
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
                     if (ks >= nk) break;
-                    const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
-                    tc_mma_ss(tmem + d, tc_desc_k(key + off), tc_desc_k(row + off), id_s, ks > 0);
+                    const uint32_t off = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
+                    tc_mma_ss(tmem + d, key + off, row + off, id_s, ks > 0);
                 }
                 tc_commit(bar);
-            }
-        };
-        auto sums = [&](uint32_t d, uint32_t p, uint32_t row, bool first) {
+            };
+            auto sums = [&](uint32_t d, uint32_t p, uint64_t row, bool first) {
 #pragma unroll
-            for (int ks = 0; ks < kAttnRows / 16; ++ks)  // each warpgroup's 64 columns in 32
-                tc_mma_ts(tmem + d, tmem + p + (ks >> 2) * 64 + (ks & 3) * 8,
-                          tc_desc_mn(row + ks * 2048, L::kHalf), id_d, !first || ks > 0);
-        };
-        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const BkUnit t = bk_unit(a, u);
-            if (t.n == 0) continue;
-            ok = all(&bars.k_full, uses & 1) && all(&bars.q_full[ring.s], ring.phase);
-            if (!ok) break;
-            tc_fence_after();
-            scores(kBkS, k_at, q_at + ring.s * L::kTile, &bars.s_full);
-            ok = all(&bars.v_full, uses & 1) && all(&bars.g_full[ring.s], ring.phase);
-            if (!ok) break;
-            tc_fence_after();
-            scores(kBkDp, v_at, g_at + ring.s * L::kTile, &bars.dp_full);
-            if (uses > 0)
-                ok = all(&bars.acc_free[0], (uses - 1) & 1) && all(&bars.acc_free[1], (uses - 1) & 1);
-            for (int i = 0; ok && i < t.n; ++i) {
-                const int at = ring.s;
-                const bool more = i + 1 < t.n;
-                ring.next(K);
-                ok = all(&bars.p_ready, tiles & 1);
-                if (!ok) break;
+                for (int ks = 0; ks < kAttnRows / 16; ++ks)  // each warpgroup's 64 columns in 32
+                    tc_mma_ts(tmem + d, tmem + p + (ks >> 2) * 64 + (ks & 3) * 8,
+                              row + ks * (2048 >> 4), id_d, !first || ks > 0);
+            };
+            // S^T (dP^T) of the ring's next row tile; `first`, `last` of the unit
+            auto next_s = [&](bool first, bool last, uint32_t use) {
+                if (first) wait(&bars.k_full, use & 1);
+                if (!wait(&bars.q_full[ring.s], ring.phase)) return;
                 tc_fence_after();
-                if (elect_one()) {
-                    sums(kBkDv, kBkS, g_at + at * L::kTile, i == 0);
-                    tc_commit(&bars.g_empty[at]);
-                }
-                if (more) {
-                    ok = all(&bars.q_full[ring.s], ring.phase);
-                    if (!ok) break;
-                    scores(kBkS, k_at, q_at + ring.s * L::kTile, &bars.s_full);
-                }
-                ok = all(&bars.ds_ready, tiles & 1);
-                if (!ok) break;
-                ++tiles;
+                scores(kBkS, k_desc, q_desc + ring.s * (L::kTile >> 4), &bars.s_full);
+                if (last) tc_commit(&bars.k_empty);
+            };
+            auto next_dp = [&](bool first, bool last, uint32_t use) {
+                if (first) wait(&bars.v_full, use & 1);
+                if (!wait(&bars.g_full[ring.s], ring.phase)) return;
                 tc_fence_after();
-                if (elect_one()) {
-                    sums(kBkDk, kBkDp, q_at + at * L::kTile, i == 0);
-                    tc_commit(&bars.q_empty[at]);
-                }
-                if (more) {
-                    ok = all(&bars.g_full[ring.s], ring.phase);
-                    if (!ok) break;
-                    scores(kBkDp, v_at, g_at + ring.s * L::kTile, &bars.dp_full);
-                } else if (elect_one()) {
-                    tc_commit(&bars.acc_full);
-                }
-                __syncwarp();
+                scores(kBkDp, v_desc, g_desc + ring.s * (L::kTile >> 4), &bars.dp_full);
+                if (last) tc_commit(&bars.v_empty);
+            };
+            int64_t wave = 0;
+            BkUnit t, next;
+            bool live = bk_next(a, units, &wave, &t);
+            if (live) {
+                next_s(true, t.n == 1, 0);
+                next_dp(true, t.n == 1, 0);
             }
-            ++uses;
-        }
-        if (elect_one()) {  // every product complete before tensor memory is given back
-            tc_commit(&bars.drain);
+            while (live && ok) {
+                const bool more = bk_next(a, units, &wave, &next);
+                for (int i = 0; ok && i < t.n; ++i, ++tiles) {
+                    const int at = ring.s;
+                    const bool end = i + 1 == t.n;           // the next tile is the next unit's
+                    const bool last = end ? next.n == 1 : i + 2 == t.n;
+                    ring.next(K);
+                    wait(&bars.p_ready, tiles & 1);
+                    if (i == 0 && uses > 0) wait(&bars.acc_free, (uses - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    sums(kBkDv, kBkS, gt_desc + at * (L::kTile >> 4), i == 0);
+                    tc_commit(&bars.g_empty[at]);
+                    if (!end || more) next_s(end, last, uses + 1);
+                    if (!wait(&bars.ds_ready, tiles & 1)) break;
+                    tc_fence_after();
+                    sums(kBkDk, kBkDp, qt_desc + at * (L::kTile >> 4), i == 0);
+                    tc_commit(&bars.q_empty[at]);
+                    if (end) tc_commit(&bars.acc_full);
+                    if (!end || more) next_dp(end, last, uses + 1);
+                }
+                ++uses;
+                t = next;
+                live = more;
+            }
+            tc_commit(&bars.drain);  // every product complete before tensor memory is given back
             if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
         }
         __syncwarp();
-    } else if (warp == kAbStoreWarp) {
-        if (lane == 0) {
-            uint32_t uses = 0;
-            bool ok = true;
-            for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const BkUnit t = bk_unit(a, u);
-                if (t.n == 0) continue;
-                for (int w = 0; ok && w < 2; ++w) {
-                    ok = wait_or_dead(&bars.staged[w], uses & 1, dead);
-                    if (!ok) break;
-                    for (int h = 0; h < halves; ++h)
-                        tensor_s2g_4d(w ? &a.dvmap[t.r] : &a.dkmap[t.r], 64 * h, t.kvh, int(t.kv0),
-                                      t.bb, smem + (w ? L::kV : L::kK) + h * L::kHalf);
-                    bulk_commit();
-                    bulk_wait_read<0>();
-                    mbar_arrive(&bars.kv_empty[w]);
-                }
-                ++uses;
-            }
-            bulk_wait<0>();
-        }
-        __syncwarp();
-    } else {
+    } else if (warp < kAbLoadWarp) {
         const int wg = warp >> 2;  // columns 64 wg .. 64 wg + 63; then dK (0) or dV (1)
         const int row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;
@@ -375,20 +388,21 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         const uint32_t dp_at = tmem + lanes + kBkDp + wg * 64;
         const uint32_t acc_at = tmem + lanes + (wg ? kBkDv : kBkDk);
         const float sl2 = s.scale * 1.4426950408889634f;
-        uint8_t* stage = smem + (wg ? L::kV : L::kK) + row * 128;
         StageRing ring;
         uint32_t uses = 0, tiles = 0;
         bool ok = true;
         auto all = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
         };
-        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        for (int64_t wave = 0; ok && wave * int64_t(gridDim.x) < units; ++wave) {
+            const int64_t u = attn_unit_at(wave);
+            if (u >= units) continue;
             const BkUnit t = bk_unit(a, u);
             const int64_t key = t.kv0 + row;
+            uint8_t* out = (wg ? a.dv[t.r] : a.dk[t.r]) +
+                           ((int64_t(t.bb) * s.Skv + key) * s.m[t.r] + t.kvh) * s.d * 2;
             if (t.n == 0) {  // keys that no row sees
                 if (key < s.Skv) {
-                    uint8_t* out = (wg ? a.dv[t.r] : a.dk[t.r]) +
-                                   ((int64_t(t.bb) * s.Skv + key) * s.m[t.r] + t.kvh) * s.d * 2;
                     for (int c = 0; c < s.d * 2; c += 16) st_v4(out + c, make_uint4(0, 0, 0, 0));
                 }
                 continue;
@@ -493,24 +507,12 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 uint32_t y[32];
                 tmem_ld32(acc_at + c * 32, y);
                 tmem_wait_ld(y);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = E::pack(__uint_as_float(y[8 * i + 2 * k]) * f,
-                                       __uint_as_float(y[8 * i + 2 * k + 1]) * f);
-                    const int word = (c & 1) * 4 + i;
-                    st_shared_v4(stage + (c >> 1) * L::kHalf + ((word ^ (row & 7)) << 4),
-                                 make_uint4(w[0], w[1], w[2], w[3]));
+                if (c == DP / 32 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.acc_free);
                 }
-            }
-            tc_fence_before();
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars.acc_free[wg]);
-                mbar_arrive(&bars.staged[wg]);
+                if (key < s.Skv) ab_store32<E>(out, c * 32, s.d, y, f);
             }
             ++uses;
         }
@@ -537,10 +539,10 @@ struct BqSmem {
 };
 
 struct BqBars {
-    uint64_t q_full, g_full, q_empty;  // q_empty: the dQ store has read its place (dO's with it)
-    uint64_t kv_full[8], kv_empty[8];
+    uint64_t q_full, g_full, q_empty, g_empty;  // row tile landed; its last scores have read it
+    uint64_t kv_full[8], kv_empty[8], clean[8];  // clean: K rows past the last key zeroed
     uint64_t s_full[2], dp_full, ds_ready;
-    uint64_t acc_full, acc_free, staged, drain;
+    uint64_t acc_full, acc_free, drain;
     uint32_t tmem;
     int dead;
 };
@@ -555,8 +557,7 @@ __device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
 {
     const AttnShape& s = a.s;
     BqUnit t;
-    t.h = div_fast(u, a.q_tiles);
-    t.tile = u - t.h * a.q_tiles;
+    attn_order(a.q_order, u, &t.h, &t.tile);
     if (s.causal) t.tile = a.q_tiles - 1 - t.tile;  // the longest rows first
     t.tok0 = t.tile * a.tile_tokens;
     ab_head(s, t.h, &t.r, &t.bb, &t.kvh);
@@ -565,6 +566,29 @@ __device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
     const int64_t keys = max(int64_t(0), min(t.len, t.pos0 + last + 1));
     t.n = int((keys + kAttnRows - 1) / kAttnRows);
     return t;
+}
+
+// The CTA's next unit with any work from *wave on (false: none).
+__device__ __forceinline__ bool bq_next(const AttnBwdArgs& a, int64_t units, int64_t* wave, BqUnit* t)
+{
+    for (; *wave * int64_t(gridDim.x) < units; ++*wave) {
+        const int64_t u = attn_unit_at(*wave);
+        if (u >= units) continue;
+        *t = bq_unit(a, u);
+        if (t->n > 0) {
+            ++*wave;
+            return true;
+        }
+    }
+    t->n = 0;
+    return false;
+}
+
+// Rows of a key block past the batch element's last key that the tensor holds; kAttnRows: none.
+__device__ __forceinline__ int bq_past(const AttnShape& s, const BqUnit& t, int block)
+{
+    const int64_t past = t.len - int64_t(block) * kAttnRows;
+    return past >= kAttnRows || t.len >= s.Skv ? kAttnRows : int(past);
 }
 
 template <int DP, bool F16>
@@ -581,16 +605,18 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     const AttnShape& s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nk = (s.d + 15) / 16, halves = (s.d + 63) / 64;
-    const int64_t units = s.head_begin[s.W] * a.q_tiles;
+    const int64_t units = a.q_order.heads * a.q_order.blocks;
     constexpr int K = L::kStages;
 
     if (threadIdx.x == 0) {
         mbar_init(&bars.q_full, 1);
         mbar_init(&bars.g_full, 1);
         mbar_init(&bars.q_empty, 1);
+        mbar_init(&bars.g_empty, 1);
         for (int k = 0; k < K; ++k) {
             mbar_init(&bars.kv_full[k], 1);
-            mbar_init(&bars.kv_empty[k], 1);
+            mbar_init(&bars.kv_empty[k], s.kv_lens ? 2 : 1);  // the products, and warp 10
+            mbar_init(&bars.clean[k], 1);
         }
         mbar_init(&bars.s_full[0], 1);
         mbar_init(&bars.s_full[1], 1);
@@ -598,7 +624,6 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.ds_ready, 8);
         mbar_init(&bars.acc_full, 1);
         mbar_init(&bars.acc_free, 8);
-        mbar_init(&bars.staged, 8);
         mbar_init(&bars.drain, 1);
         bars.dead = 0;
         fence_barrier_init();
@@ -617,10 +642,12 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
-            for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const BqUnit t = bq_unit(a, u);
-                if (t.n == 0) continue;
-                if (uses > 0) ok = wait_or_dead(&bars.q_empty, (uses - 1) & 1, dead);
+            int64_t wave = 0;
+            BqUnit t;
+            while (ok && bq_next(a, units, &wave, &t)) {
+                if (uses > 0)
+                    ok = wait_or_dead(&bars.q_empty, (uses - 1) & 1, dead) &&
+                         wait_or_dead(&bars.g_empty, (uses - 1) & 1, dead);
                 if (!ok) break;
                 for (int w = 0; w < 2; ++w) {
                     uint64_t* bar = w ? &bars.g_full : &bars.q_full;
@@ -653,119 +680,126 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             if (!drained) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
         }
         __syncwarp();
+    } else if (warp == kAbCleanWarp) {
+        // dS is zero past the last key, but zero times what K holds there may be NaN
+        if (s.kv_lens) {
+            StageRing ring;
+            int64_t wave = 0;
+            BqUnit t;
+            bool ok = true;
+            while (ok && bq_next(a, units, &wave, &t)) {
+                for (int j = 0; ok && j < 2 * t.n; ++j) {  // K0 V0 K1 V1 ...
+                    ok = __all_sync(0xffffffffu,
+                                    wait_or_dead(&bars.kv_full[ring.s], ring.phase, dead));
+                    if (!ok) break;
+                    const int past = (j & 1) ? kAttnRows : bq_past(s, t, j >> 1);
+                    if (past < kAttnRows) {
+                        for (int h = 0; h < halves; ++h)
+                            for (int w = past * 8 + lane; w < kAttnRows * 8; w += 32)
+                                st_shared_v4(smem + L::kRing + ring.s * L::kTile + h * L::kHalf +
+                                                 w * 16,
+                                             make_uint4(0, 0, 0, 0));
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.clean[ring.s]);
+                    }
+                    // every stage waits for this warp, so that it neither runs ahead of the ring
+                    // nor falls a turn behind
+                    if (lane == 0) mbar_arrive(&bars.kv_empty[ring.s]);
+                    ring.next(K);
+                }
+            }
+        }
+        __syncwarp();
     } else if (warp == kAbMmaWarp) {
-        const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
-        const uint32_t id_d = tc_idesc(F16, 16 * nk, true);
-        const uint32_t q_at = smem_u32(smem + L::kQ), g_at = smem_u32(smem + L::kG);
-        const uint32_t ring_at = smem_u32(smem + L::kRing);
-        StageRing ring;
-        uint32_t uses = 0, blocks = 0;
-        bool ok = true;
-        auto all = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
-        };
-        auto scores = [&](uint32_t d, uint32_t row, uint32_t key, uint64_t* bar) {
-            if (elect_one()) {
+        if (elect_one()) {
+            const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
+            const uint32_t id_d = tc_idesc(F16, 16 * nk, true);
+            const uint64_t q_desc = tc_desc_k(smem_u32(smem + L::kQ));
+            const uint64_t g_desc = tc_desc_k(smem_u32(smem + L::kG));
+            const uint64_t kv_desc = tc_desc_k(smem_u32(smem + L::kRing));
+            const uint64_t kt_desc = tc_desc_mn(smem_u32(smem + L::kRing), L::kHalf);
+            StageRing ring;
+            uint32_t uses = 0, blocks = 0;
+            uint32_t cleaned = 0;  // parity of each stage's `clean`
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                return ok = ok && wait_or_dead(bar, parity, dead);
+            };
+            auto scores = [&](uint32_t d, uint64_t row, uint64_t key, uint64_t* bar) {
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
                     if (ks >= nk) break;
-                    const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
-                    tc_mma_ss(tmem + d, tc_desc_k(row + off), tc_desc_k(key + off), id_s, ks > 0);
+                    const uint32_t off = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
+                    tc_mma_ss(tmem + d, row + off, key + off, id_s, ks > 0);
                 }
                 tc_commit(bar);
-            }
-        };
-        // dS is zero past the last key, but zero times what K holds there may be NaN
-        auto clear_past = [&](int stage, int64_t past) {
-            if (past >= kAttnRows) return;
-            const int words = (kAttnRows - int(past)) * 8;
-            for (int h = 0; h < halves; ++h)
-                for (int w = lane; w < words; w += 32)
-                    st_shared_v4(smem + L::kRing + stage * L::kTile + h * L::kHalf + int(past) * 128 +
-                                     w * 16,
-                                 make_uint4(0, 0, 0, 0));
-            fence_proxy_async_shared();
-            __syncwarp();
-        };
-        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const BqUnit t = bq_unit(a, u);
-            if (t.n == 0) continue;
-            const bool ragged = t.len < s.Skv;
-            int ks = ring.s;  // the stage of the current block's K
-            ok = all(&bars.q_full, uses & 1) && all(&bars.kv_full[ks], ring.phase);
-            if (!ok) break;
-            if (ragged) clear_past(ks, t.len);
-            tc_fence_after();
-            scores(kBqS + (blocks & 1) * 128, q_at, ring_at + ks * L::kTile,
-                   &bars.s_full[blocks & 1]);
-            ring.next(K);
-            ok = all(&bars.g_full, uses & 1) && all(&bars.kv_full[ring.s], ring.phase);
-            if (!ok) break;
-            scores(kBqDp, g_at, ring_at + ring.s * L::kTile, &bars.dp_full);
-            if (elect_one()) tc_commit(&bars.kv_empty[ring.s]);
-            ring.next(K);
-            if (uses > 0) ok = all(&bars.acc_free, (uses - 1) & 1);
-            for (int j = 0; ok && j < t.n; ++j, ++blocks) {
-                const bool more = j + 1 < t.n;
-                const int next_k = ring.s;
-                if (more) {
-                    ok = all(&bars.kv_full[next_k], ring.phase);
-                    if (!ok) break;
-                    if (ragged) clear_past(next_k, t.len - int64_t(j + 1) * kAttnRows);
-                    tc_fence_after();
-                    const uint32_t buf = (blocks + 1) & 1;
-                    scores(kBqS + buf * 128, q_at, ring_at + next_k * L::kTile, &bars.s_full[buf]);
-                    ring.next(K);
-                }
-                ok = all(&bars.ds_ready, blocks & 1);
-                if (!ok) break;
+            };
+            // S of a block (number `count` of the CTA's) from the ring's next stage, which it
+            // returns; dP from the stage after it. `first`, `last` of the unit.
+            auto next_s = [&](bool first, bool last, uint32_t use, uint32_t count) {
+                const int stage = ring.s;
+                if (first) wait(&bars.q_full, use & 1);
+                if (!wait(&bars.kv_full[stage], ring.phase)) return stage;
                 tc_fence_after();
-                if (elect_one()) {
+                scores(kBqS + (count & 1) * 128, q_desc, kv_desc + stage * (L::kTile >> 4),
+                       &bars.s_full[count & 1]);
+                if (last) tc_commit(&bars.q_empty);
+                ring.next(K);
+                return stage;
+            };
+            auto next_dp = [&](bool first, bool last, uint32_t use) {
+                if (first) wait(&bars.g_full, use & 1);
+                if (!wait(&bars.kv_full[ring.s], ring.phase)) return;
+                tc_fence_after();
+                scores(kBqDp, g_desc, kv_desc + ring.s * (L::kTile >> 4), &bars.dp_full);
+                tc_commit(&bars.kv_empty[ring.s]);
+                if (last) tc_commit(&bars.g_empty);
+                ring.next(K);
+            };
+            int64_t wave = 0;
+            BqUnit t, next;
+            bool live = bq_next(a, units, &wave, &t);
+            int ks = 0;  // the stage of the current block's K
+            if (live) {
+                ks = next_s(true, t.n == 1, 0, 0);
+                next_dp(true, t.n == 1, 0);
+            }
+            while (live && ok) {
+                const bool more = bq_next(a, units, &wave, &next);
+                for (int j = 0; ok && j < t.n; ++j, ++blocks) {
+                    const bool end = j + 1 == t.n;  // the next block is the next unit's
+                    const bool last = end ? next.n == 1 : j + 2 == t.n;
+                    int after = ks;
+                    if (!end) after = next_s(false, last, uses, blocks + 1);
+                    if (s.kv_lens && bq_past(s, t, j) < kAttnRows) {
+                        wait(&bars.clean[ks], (cleaned >> ks) & 1);
+                        cleaned ^= 1u << ks;
+                    }
+                    wait(&bars.ds_ready, blocks & 1);
+                    if (j == 0 && uses > 0) wait(&bars.acc_free, (uses - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t kd = kt_desc + ks * (L::kTile >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kAttnRows / 16; ++kk)
                         tc_mma_ts(tmem + kBqDq,
                                   tmem + kBqS + (blocks & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                                  tc_desc_mn(ring_at + ks * L::kTile + kk * 2048, L::kHalf), id_d,
-                                  j > 0 || kk > 0);
+                                  kd + kk * (2048 >> 4), id_d, j > 0 || kk > 0);
                     tc_commit(&bars.kv_empty[ks]);
+                    if (end) {
+                        tc_commit(&bars.acc_full);
+                        if (more) after = next_s(true, last, uses + 1, blocks + 1);
+                    }
+                    ks = after;
+                    if (!end || more) next_dp(end, last, uses + 1);
                 }
-                ks = next_k;
-                if (more) {
-                    ok = all(&bars.kv_full[ring.s], ring.phase);
-                    if (!ok) break;
-                    scores(kBqDp, g_at, ring_at + ring.s * L::kTile, &bars.dp_full);
-                    if (elect_one()) tc_commit(&bars.kv_empty[ring.s]);
-                    ring.next(K);
-                } else if (elect_one()) {
-                    tc_commit(&bars.acc_full);
-                }
-                __syncwarp();
+                ++uses;
+                t = next;
+                live = more;
             }
-            ++uses;
-        }
-        if (elect_one()) {
             tc_commit(&bars.drain);
             if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
-        }
-        __syncwarp();
-    } else if (warp == kAbStoreWarp) {
-        if (lane == 0) {
-            uint32_t uses = 0;
-            bool ok = true;
-            for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const BqUnit t = bq_unit(a, u);
-                if (t.n == 0) continue;
-                ok = wait_or_dead(&bars.staged, uses & 1, dead);
-                if (!ok) break;
-                for (int h = 0; h < halves; ++h)
-                    tensor_s2g_4d(&a.dqmap[t.r], 64 * h, t.kvh * s.group, int(t.tok0), t.bb,
-                                  smem + L::kQ + h * L::kHalf);
-                bulk_commit();
-                bulk_wait_read<0>();
-                mbar_arrive(&bars.q_empty);
-                ++uses;
-            }
-            bulk_wait<0>();
         }
         __syncwarp();
     } else {
@@ -775,19 +809,21 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         const uint32_t dp_at = tmem + lanes + kBqDp + wg * 64;
         const float sl2 = s.scale * 1.4426950408889634f;
         const int tok_in = row / s.group, head_in = row - tok_in * s.group;
-        uint8_t* stage = smem + L::kQ + row * 128;
         uint32_t uses = 0, blocks = 0;
         bool ok = true;
         auto all = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
         };
-        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        for (int64_t wave = 0; ok && wave * int64_t(gridDim.x) < units; ++wave) {
+            const int64_t u = attn_unit_at(wave);
+            if (u >= units) continue;
             const BqUnit t = bq_unit(a, u);
             const int64_t tok = t.tok0 + tok_in;
+            const bool valid = tok_in < a.tile_tokens && tok < s.Sq;
+            uint8_t* out = a.dq[t.r] + ((int64_t(t.bb) * s.Sq + tok) * s.n[t.r] +
+                                        t.kvh * s.group + head_in) * s.d * 2;
             if (t.n == 0) {
-                if (wg == 0 && tok_in < a.tile_tokens && tok < s.Sq) {
-                    uint8_t* out = a.dq[t.r] + ((int64_t(t.bb) * s.Sq + tok) * s.n[t.r] +
-                                                t.kvh * s.group + head_in) * s.d * 2;
+                if (wg == 0 && valid) {
                     for (int c = 0; c < s.d * 2; c += 16) st_v4(out + c, make_uint4(0, 0, 0, 0));
                 }
                 continue;
@@ -857,24 +893,12 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 uint32_t y[32];
                 tmem_ld32(tmem + lanes + kBqDq + c * 32, y);
                 tmem_wait_ld(y);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = E::pack(__uint_as_float(y[8 * i + 2 * k]) * s.scale,
-                                       __uint_as_float(y[8 * i + 2 * k + 1]) * s.scale);
-                    const int word = (c & 1) * 4 + i;
-                    st_shared_v4(stage + (c >> 1) * L::kHalf + ((word ^ (row & 7)) << 4),
-                                 make_uint4(w[0], w[1], w[2], w[3]));
+                if (cc == DP / 64 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.acc_free);
                 }
-            }
-            tc_fence_before();
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars.acc_free);
-                mbar_arrive(&bars.staged);
+                if (valid) ab_store32<E>(out, c * 32, s.d, y, s.scale);
             }
             ++uses;
         }
@@ -900,12 +924,12 @@ static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int devi
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit);
     }
-    const int64_t heads = a.s.head_begin[a.s.W];
+    const int64_t heads = a.q_order.heads;
     auto cap = [](int64_t n, int64_t most) { return unsigned(n < most ? n : most); };
     attn_bwd_stats_kernel<F16><<<cap(heads * a.q_tiles * (kAttnRows / 16), int64_t(grid) * 16), 256, 0,
                                  stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn_bwd_kv_kernel<DP, F16><<<cap(heads * a.k_blocks, grid), kAbThreads, smem_kv, stream>>>(a);
+    attn_bwd_kv_kernel<DP, F16><<<cap(heads * a.kv_order.blocks, grid), kAbThreads, smem_kv, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     attn_bwd_q_kernel<DP, F16><<<cap(heads * a.q_tiles, grid), kAbThreads, smem_q, stream>>>(a);
     return cudaGetLastError();
@@ -926,9 +950,8 @@ cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* co
         auto keys = [&](CUtensorMap* map, const void* p) {
             return encode_head_map(map, p, s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows);
         };
-        if (!rows(&a.qmap[r], q[r]) || !rows(&a.gmap[r], a.go[r]) || !rows(&a.dqmap[r], a.dq[r]) ||
-            !keys(&a.kmap[r], k[r]) || !keys(&a.vmap[r], v[r]) || !keys(&a.dkmap[r], a.dk[r]) ||
-            !keys(&a.dvmap[r], a.dv[r]))
+        if (!rows(&a.qmap[r], q[r]) || !rows(&a.gmap[r], a.go[r]) || !keys(&a.kmap[r], k[r]) ||
+            !keys(&a.vmap[r], v[r]))
             return cudaErrorInvalidValue;
     }
     if (s.d <= 64)

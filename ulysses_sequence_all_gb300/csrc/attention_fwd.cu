@@ -17,6 +17,7 @@
 // probabilities, so the tensor cores always have one tile's work; a unit's first scores follow the
 // last unit's products without a gap. Warps 0-3 and 4-7 are the two tiles' softmax: tensor memory
 // gives a thread a whole row, so maximum and sum need no exchange; they hold most of the registers.
+// Warp 10 zeroes what a value block holds past a ragged batch element's last key.
 // P goes back to tensor memory over its own S in 16 bits, rounded to nearest (unit-scale values
 // in an fp32 sum: the output itself is rounded to the same type), and is the A operand of O += P V
 // there, whose first half starts when half of P is written. O stays in tensor memory; it is
@@ -46,9 +47,9 @@ namespace uly {
 static __device__ unsigned g_attn_fwd_status;
 
 constexpr int kAfThreads = 384;
-constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9;
-// Registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72.
-constexpr int kAfRegsSoftmax = 216, kAfRegsOther = 72;
+constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfCleanWarp = 10;
+// Registers a thread: 384 x 168 at launch = 256 x 208 + 128 x 88.
+constexpr int kAfRegsSoftmax = 208, kAfRegsOther = 88;
 constexpr float kAfRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 
 // Tensor memory columns: the two tiles' scores (their probabilities over them), their outputs.
@@ -71,6 +72,7 @@ struct AfBars {
     uint64_t p_half[2], p_ready[2];  // half of the probabilities (and a rescaled O) written; all
     uint64_t o_full[2], o_free[2];   // output complete; read out
     uint64_t kv_full[8], kv_empty[8];
+    uint64_t clean[8];               // rows past the last key zeroed
     uint64_t drain;
     uint32_t tmem;
     int dead;
@@ -79,75 +81,125 @@ static_assert(sizeof(AfBars) <= 1024, "barriers");
 
 struct AfUnit {
     int r, bb, kvh, sp;
-    int64_t tok0, tok1;  // first token of each tile
-    int64_t lo0, lo1;    // first key block of each tile
-    int n0, n1;          // key blocks of each tile
-    int64_t len;         // keys of the batch element
-    int64_t pos0;        // position of query token 0; beyond every key when not causal
+    int tok0, tok1;  // first token of each tile
+    int lo0, lo1;    // first key block of each tile
+    int n0, n1;      // key blocks of each tile
+    int len;         // keys of the batch element
+    int pos0;        // position of query token 0; beyond every key when not causal
     __device__ __forceinline__ int n(int k) const { return k ? n1 : n0; }
-    __device__ __forceinline__ int64_t lo(int k) const { return k ? lo1 : lo0; }
-    __device__ __forceinline__ int64_t tok(int k) const { return k ? tok1 : tok0; }
+    __device__ __forceinline__ int lo(int k) const { return k ? lo1 : lo0; }
+    __device__ __forceinline__ int tok(int k) const { return k ? tok1 : tok0; }
     __device__ __forceinline__ int most() const { return max(n0, n1); }
 };
 
 // Key blocks that the tile of tokens from `tok` on sees.
-__device__ __forceinline__ int64_t af_blocks(const AttnFwdArgs& a, const AfUnit& t, int64_t tok)
+__device__ __forceinline__ int af_blocks(const AttnFwdArgs& a, const AfUnit& t, int64_t tok)
 {
     const int64_t last = min(tok + a.tile_tokens, a.s.Sq) - 1;
-    const int64_t keys = min(t.len, t.pos0 + last + 1);
-    return tok >= a.s.Sq || keys <= 0 ? 0 : (keys + kAttnRows - 1) / kAttnRows;
+    const int64_t keys = min(int64_t(t.len), t.pos0 + last + 1);
+    return tok >= a.s.Sq || keys <= 0 ? 0 : int((keys + kAttnRows - 1) / kAttnRows);
 }
 
 __device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
 {
     const AttnShape& s = a.s;
     AfUnit t;
-    const int64_t v = div_fast(u, a.splits);
+    const int64_t v = a.splits == 1 ? u : div_fast(u, a.splits);
     t.sp = int(u - v * a.splits);
-    const int64_t h = div_fast(v, a.q_blocks);
-    int64_t qb = v - h * a.q_blocks;
-    if (s.causal) qb = a.q_blocks - 1 - qb;  // the longest rows first
+    int64_t h, qb;
+    attn_order(a.order, v, &h, &qb);
+    if (s.causal) qb = a.order.blocks - 1 - qb;  // the longest rows first
     int r = 0;
     while (r + 1 < s.W && h >= s.head_begin[r + 1]) ++r;
     t.r = r;
     const int local = int(h) - s.head_begin[r];
     t.bb = local / s.m[r];
     t.kvh = local - t.bb * s.m[r];
-    t.len = s.Skv;
-    if (s.kv_lens) t.len = min(s.Skv, int64_t(max(0, s.kv_lens[t.bb])));
-    t.pos0 = s.causal ? (s.q_start ? int64_t(s.q_start[t.bb]) : 0) : s.Skv;
+    t.len = int(s.Skv);
+    if (s.kv_lens) t.len = min(t.len, max(0, s.kv_lens[t.bb]));
+    t.pos0 = s.causal ? (s.q_start ? s.q_start[t.bb] : 0) : int(s.Skv);
     if (a.paired) {
         t.tok0 = t.tok1 = 0;
-        const int64_t total = af_blocks(a, t, 0);
-        const int64_t per = (total + a.parts - 1) / a.parts;
-        t.lo0 = (2 * t.sp) * per;
+        const int total = af_blocks(a, t, 0);
+        const int per = (total + a.parts - 1) / a.parts;
+        t.lo0 = 2 * t.sp * per;
         t.lo1 = t.lo0 + per;
-        t.n0 = int(max(int64_t(0), min(total - t.lo0, per)));
-        t.n1 = int(max(int64_t(0), min(total - t.lo1, per)));
+        t.n0 = max(0, min(total - t.lo0, per));
+        t.n1 = max(0, min(total - t.lo1, per));
     } else {
-        t.tok0 = qb * 2 * a.tile_tokens;
-        t.tok1 = t.tok0 + a.tile_tokens;
-        const int64_t b0 = af_blocks(a, t, t.tok0), b1 = af_blocks(a, t, t.tok1);
-        const int64_t total = max(b0, b1);
-        const int64_t per = (total + a.splits - 1) / a.splits;
+        const int64_t tok = qb * 2 * a.tile_tokens;
+        t.tok0 = int(tok);
+        t.tok1 = int(tok + a.tile_tokens);
+        const int b0 = af_blocks(a, t, tok), b1 = af_blocks(a, t, tok + a.tile_tokens);
+        const int total = max(b0, b1);
+        const int per = (total + a.splits - 1) / a.splits;
         t.lo0 = t.lo1 = t.sp * per;
-        t.n0 = int(max(int64_t(0), min(b0 - t.lo0, per)));
-        t.n1 = int(max(int64_t(0), min(b1 - t.lo1, per)));
+        t.n0 = max(0, min(b0 - t.lo0, per));
+        t.n1 = max(0, min(b1 - t.lo1, per));
     }
     return t;
 }
 
-// The CTA's next unit with any work at or after *u (false: none).
-__device__ __forceinline__ bool af_next(const AttnFwdArgs& a, int64_t* u, AfUnit* t)
+// The CTA's next unit with any work from *wave on (false: none).
+__device__ __forceinline__ bool af_next(const AttnFwdArgs& a, int64_t* wave, AfUnit* t)
 {
-    for (; *u < a.units; *u += gridDim.x) {
-        *t = af_unit(a, *u);
+    for (;; ++*wave) {
+        const int64_t u = attn_unit_at(*wave);
+        if (*wave * int64_t(gridDim.x) >= a.units) return false;
+        if (u >= a.units) continue;
+        *t = af_unit(a, u);
         if (t->most() > 0) {
-            *u += gridDim.x;
+            ++*wave;
             return true;
         }
     }
-    return false;
+}
+
+// The order in which a CTA's queries and blocks of keys and values come: queries(t) before a unit's
+// first block, block(value, t, key block) for every stage of the ring; both return false to stop.
+// A unit's first scores are wanted before the last products of the unit before.
+template <bool PAIRED, class Queries, class Block>
+__device__ __forceinline__ void af_walk(const AttnFwdArgs& a, Queries queries, Block block)
+{
+    int64_t wave = 0;
+    AfUnit t, next;
+    bool live = af_next(a, &wave, &t);
+    if (!live || !queries(t)) return;
+    if (PAIRED) {
+        if (t.n0 > 0 && !block(false, t, t.lo0)) return;
+        if (t.n1 > 0 && !block(false, t, t.lo1)) return;
+    }
+    while (live) {
+        const bool more = af_next(a, &wave, &next);
+        const int n = t.most();
+        for (int j = 0; j < n; ++j) {
+            if constexpr (PAIRED) {  // V of a tile's block, then its next K
+                if (j + 1 == n && more && !queries(next)) return;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (j < t.n(k) && !block(true, t, t.lo(k) + j)) return;
+                    if (j + 1 < t.n(k)) {
+                        if (!block(false, t, t.lo(k) + j + 1)) return;
+                    } else if (j + 1 == n && more && next.n(k) > 0) {
+                        if (!block(false, next, next.lo(k))) return;
+                    }
+                }
+            } else {  // K0 V0 K1 V1 ...
+                if (!block(false, t, t.lo0 + j) || !block(true, t, t.lo0 + j)) return;
+            }
+        }
+        if (!PAIRED && more && !queries(next)) return;
+        t = next;
+        live = more;
+    }
+}
+
+// Rows of a value block past the batch element's last key, where any of them can hold a value
+// (past the tensor's end the copy itself writes zeros); kAttnRows: none.
+__device__ __forceinline__ int af_past(const AttnShape& s, const AfUnit& t, int block)
+{
+    const int past = t.len - block * kAttnRows;
+    return past >= kAttnRows || t.len >= s.Skv ? kAttnRows : past;
 }
 
 template <int DP, bool F16, bool PAIRED>
@@ -179,7 +231,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         }
         for (int k = 0; k < K; ++k) {
             mbar_init(&bars.kv_full[k], 1);
-            mbar_init(&bars.kv_empty[k], 1);
+            mbar_init(&bars.kv_empty[k], s.kv_lens ? 2 : 1);  // the products, and warp 10
+            mbar_init(&bars.clean[k], 1);
         }
         mbar_init(&bars.drain, 1);
         bars.dead = 0;
@@ -199,66 +252,33 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             int64_t issued = 0;
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
-            bool ok = true;
             auto queries = [&](const AfUnit& t) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    if (!ok || t.n(k) == 0) continue;
-                    if (uses[k] > 0) ok = wait_or_dead(&bars.q_empty[k], (uses[k] - 1) & 1, dead);
-                    if (!ok) continue;
+                    if (t.n(k) == 0) continue;
+                    if (uses[k] > 0 && !wait_or_dead(&bars.q_empty[k], (uses[k] - 1) & 1, dead))
+                        return false;
                     mbar_arrive_expect_tx(&bars.q_full[k], q_bytes);
                     for (int h = 0; h < halves; ++h)
                         tensor_g2s_4d(smem + L::kQ + k * L::kTile + h * L::kHalf, &a.qmap[t.r],
-                                      64 * h, t.kvh * s.group, int(t.tok(k)), t.bb, &bars.q_full[k]);
+                                      64 * h, t.kvh * s.group, t.tok(k), t.bb, &bars.q_full[k]);
                     ++uses[k];
                 }
+                return true;
             };
-            auto block = [&](const CUtensorMap* map, const AfUnit& t, int64_t at) {
-                if (!ok) return;
-                if (issued >= K) ok = wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, dead);
-                if (!ok) return;
+            auto block = [&](bool value, const AfUnit& t, int at) {
+                if (issued >= K && !wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, dead))
+                    return false;
+                const CUtensorMap* map = value ? &a.vmap[t.r] : &a.kmap[t.r];
                 mbar_arrive_expect_tx(&bars.kv_full[ring.s], kv_bytes);
                 for (int h = 0; h < halves; ++h)
                     tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf, map, 64 * h,
-                                  t.kvh, int(at * kAttnRows), t.bb, &bars.kv_full[ring.s]);
+                                  t.kvh, at * kAttnRows, t.bb, &bars.kv_full[ring.s]);
                 ++issued;
                 ring.next(K);
+                return true;
             };
-            int64_t u = blockIdx.x;
-            AfUnit t, next;
-            bool live = af_next(a, &u, &t);
-            if (live) {
-                queries(t);
-                if (PAIRED) {
-                    if (t.n0 > 0) block(&a.kmap[t.r], t, t.lo0);
-                    if (t.n1 > 0) block(&a.kmap[t.r], t, t.lo1);
-                }
-            }
-            while (live && ok) {
-                const bool more = af_next(a, &u, &next);
-                const int n = t.most();
-                if constexpr (PAIRED) {  // the order of the products: V of a block, K of the next
-                    for (int j = 0; ok && j < n; ++j) {
-                        if (j + 1 == n && more) queries(next);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            if (j < t.n(k)) block(&a.vmap[t.r], t, t.lo(k) + j);
-                            if (j + 1 < t.n(k))
-                                block(&a.kmap[t.r], t, t.lo(k) + j + 1);
-                            else if (j + 1 == n && more && next.n(k) > 0)
-                                block(&a.kmap[next.r], next, next.lo(k));
-                        }
-                    }
-                } else {
-                    for (int j = 0; ok && j < n; ++j) {  // K0 V0 K1 V1 ...
-                        block(&a.kmap[t.r], t, t.lo0 + j);
-                        block(&a.vmap[t.r], t, t.lo0 + j);
-                    }
-                    if (more) queries(next);
-                }
-                t = next;
-                live = more;
-            }
+            af_walk<PAIRED>(a, queries, block);
             // leave no copy into this CTA's shared memory in flight
             for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k)
                 if (!mbar_wait_bounded(&bars.kv_full[k % K], uint32_t((k / K) & 1)))
@@ -266,81 +286,96 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             for (int k = 0; k < 2; ++k)
                 if (uses[k] > 0 && !mbar_wait_bounded(&bars.q_full[k], (uses[k] - 1) & 1))
                     atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
-        } else if (warp == kAfMmaWarp) {
+        } else if (warp == kAfCleanWarp && s.kv_lens) {
+            // A masked probability is zero, but zero times whatever lies past the last key may be
+            // NaN: a value block's rows past it become zeros before its product.
+            StageRing ring;
+            af_walk<PAIRED>(
+                a, [](const AfUnit&) { return true; },
+                [&](bool value, const AfUnit& t, int at) {
+                    const int past = value ? af_past(s, t, at) : kAttnRows;
+                    if (!__all_sync(0xffffffffu,
+                                    wait_or_dead(&bars.kv_full[ring.s], ring.phase, dead)))
+                        return false;
+                    if (past < kAttnRows) {
+                        for (int h = 0; h < halves; ++h)
+                            for (int w = past * 8 + lane; w < kAttnRows * 8; w += 32)
+                                st_shared_v4(smem + L::kRing + ring.s * L::kTile + h * L::kHalf +
+                                                 w * 16,
+                                             make_uint4(0, 0, 0, 0));
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.clean[ring.s]);
+                    }
+                    // every stage waits for this warp, so that it neither runs ahead of the ring
+                    // nor falls a turn behind
+                    if (lane == 0) mbar_arrive(&bars.kv_empty[ring.s]);
+                    ring.next(K);
+                    return true;
+                });
+        } else if (warp == kAfMmaWarp && elect_one()) {
             const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
             const uint32_t id_o = tc_idesc(F16, 16 * nk, true);
-            const uint32_t q_at = smem_u32(smem + L::kQ), ring_at = smem_u32(smem + L::kRing);
+            const uint64_t q_desc = tc_desc_k(smem_u32(smem + L::kQ));
+            const uint64_t k_desc = tc_desc_k(smem_u32(smem + L::kRing));
+            const uint64_t v_desc = tc_desc_mn(smem_u32(smem + L::kRing), L::kHalf);
             StageRing ring;
             uint32_t uses[2] = {0, 0}, blocks[2] = {0, 0};
+            uint32_t cleaned = 0;  // parity of each stage's `clean`
             bool ok = true;
-            auto all = [&](uint64_t* bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                return ok = ok && wait_or_dead(bar, parity, dead);
             };
             auto scores = [&](int k, int stage, bool last) {  // S_k = Q_k K^T
-                if (elect_one()) {
-                    const uint32_t k_addr = ring_at + stage * L::kTile;
+                const uint64_t qd = q_desc + k * (L::kTile >> 4);
+                const uint64_t kd = k_desc + stage * (L::kTile >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) {
-                        if (ks >= nk) break;
-                        const uint32_t off = (ks >> 2) * L::kHalf + (ks & 3) * 32;
-                        tc_mma_ss(tmem + kAfS + k * 128, tc_desc_k(q_at + k * L::kTile + off),
-                                  tc_desc_k(k_addr + off), id_s, ks > 0);
-                    }
-                    tc_commit(&bars.s_full[k]);
-                    if (last) tc_commit(&bars.q_empty[k]);  // the tile's queries are done with
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    if (ks >= nk) break;
+                    const uint32_t off = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
+                    tc_mma_ss(tmem + kAfS + k * 128, qd + off, kd + off, id_s, ks > 0);
                 }
+                tc_commit(&bars.s_full[k]);
+                if (last) tc_commit(&bars.q_empty[k]);  // the tile's queries are done with
             };
             auto first_scores = [&](const AfUnit& t, int k, int stage) {  // of a unit
-                ok = ok && all(&bars.q_full[k], uses[k] & 1);
-                if (!ok) return;
+                if (!wait(&bars.q_full[k], uses[k] & 1)) return;
                 tc_fence_after();
                 scores(k, stage, t.n(k) == 1);
             };
-            // A masked probability is zero, but zero times whatever lies past the last key may
-            // be NaN: a value block's rows past it become zeros.
-            auto clear_past = [&](const AfUnit& t, int stage, int64_t at) {
-                const int64_t past = t.len - at * kAttnRows;
-                if (past >= kAttnRows || t.len >= s.Skv) return;
-                const int words = (kAttnRows - int(past)) * 8;
-                for (int h = 0; h < halves; ++h)
-                    for (int w = lane; w < words; w += 32)
-                        st_shared_v4(smem + L::kRing + stage * L::kTile + h * L::kHalf +
-                                         int(past) * 128 + w * 16,
-                                     make_uint4(0, 0, 0, 0));
-                fence_proxy_async_shared();
-                __syncwarp();
-            };
             auto output = [&](const AfUnit& t, int k, int stage, int j) {  // O_k += P_k V
-                ok = all(&bars.p_half[k], blocks[k] & 1);
-                if (ok && j == 0 && uses[k] > 0) ok = all(&bars.o_free[k], (uses[k] - 1) & 1);
+                wait(&bars.p_half[k], blocks[k] & 1);
+                if (j == 0 && uses[k] > 0) wait(&bars.o_free[k], (uses[k] - 1) & 1);
                 if (!ok) return;
-                const uint32_t v_addr = ring_at + stage * L::kTile;
+                const uint64_t vd = v_desc + stage * (L::kTile >> 4);
                 auto half = [&](int from) {
                     tc_fence_after();
-                    if (elect_one())
 #pragma unroll
-                        for (int ks = from; ks < from + 4; ++ks)
-                            tc_mma_ts(tmem + kAfO + k * 128, tmem + kAfS + k * 128 + ks * 8,
-                                      tc_desc_mn(v_addr + ks * 2048, L::kHalf), id_o,
-                                      j > 0 || ks > 0);
+                    for (int ks = from; ks < from + 4; ++ks)
+                        tc_mma_ts(tmem + kAfO + k * 128, tmem + kAfS + k * 128 + ks * 8,
+                                  vd + ks * (2048 >> 4), id_o, j > 0 || ks > 0);
                 };
                 half(0);
-                ok = all(&bars.p_ready[k], blocks[k] & 1);
-                if (!ok) return;
+                if (!wait(&bars.p_ready[k], blocks[k] & 1)) return;
                 half(4);
                 ++blocks[k];
                 if (j + 1 == t.n(k)) {
-                    if (elect_one()) tc_commit(&bars.o_full[k]);
+                    tc_commit(&bars.o_full[k]);
                     ++uses[k];
                 }
             };
-            auto stage_ready = [&]() { return ok = ok && all(&bars.kv_full[ring.s], ring.phase); };
-            auto release = [&](int stage) {
-                if (ok && elect_one()) tc_commit(&bars.kv_empty[stage]);
+            auto stage_ready = [&]() { return wait(&bars.kv_full[ring.s], ring.phase); };
+            auto values_ready = [&](const AfUnit& t, int at) {
+                stage_ready();
+                if (s.kv_lens && af_past(s, t, at) < kAttnRows) {
+                    wait(&bars.clean[ring.s], (cleaned >> ring.s) & 1);
+                    cleaned ^= 1u << ring.s;
+                }
+                return ok;
             };
-            int64_t u = blockIdx.x;
+            int64_t wave = 0;
             AfUnit t, next;
-            bool live = af_next(a, &u, &t);
+            bool live = af_next(a, &wave, &t);
             if (live) {  // the first unit's first scores
                 if (!PAIRED) stage_ready();
 #pragma unroll
@@ -349,45 +384,43 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     if (PAIRED) stage_ready();
                     first_scores(t, k, ring.s);
                     if (PAIRED) {
-                        release(ring.s);
+                        tc_commit(&bars.kv_empty[ring.s]);
                         ring.next(K);
                     }
                 }
                 if (!PAIRED) {
-                    release(ring.s);
+                    tc_commit(&bars.kv_empty[ring.s]);
                     ring.next(K);
                 }
             }
             while (live && ok) {
-                const bool more = af_next(a, &u, &next);
+                const bool more = af_next(a, &wave, &next);
                 const int n = t.most();
                 for (int j = 0; ok && j < n; ++j) {
                     const bool last = j + 1 == n;
                     if constexpr (PAIRED) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            if (ok && j < t.n(k)) {
-                                if (!stage_ready()) break;
-                                clear_past(t, ring.s, t.lo(k) + j);
+                            if (j < t.n(k)) {
+                                if (!values_ready(t, t.lo(k) + j)) break;
                                 output(t, k, ring.s, j);
-                                release(ring.s);
+                                tc_commit(&bars.kv_empty[ring.s]);
                                 ring.next(K);
                             }
                             const bool same = j + 1 < t.n(k);
-                            if (ok && (same || (last && more && next.n(k) > 0))) {
+                            if (same || (last && more && next.n(k) > 0)) {
                                 if (!stage_ready()) break;
                                 if (same)
                                     scores(k, ring.s, j + 2 == t.n(k));
                                 else
                                     first_scores(next, k, ring.s);
-                                release(ring.s);
+                                tc_commit(&bars.kv_empty[ring.s]);
                                 ring.next(K);
                             }
                         }
                     } else {
                         const int vs = ring.s;
-                        if (!stage_ready()) break;
-                        clear_past(t, vs, t.lo0 + j);
+                        if (!values_ready(t, t.lo0 + j)) break;
                         ring.next(K);
                         const int ks = ring.s;
                         const bool any = !last || more;
@@ -397,26 +430,23 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                         }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            if (ok && j < t.n(k)) output(t, k, vs, j);
-                            if (ok && j + 1 < t.n(k))
+                            if (j < t.n(k)) output(t, k, vs, j);
+                            if (!ok) break;
+                            if (j + 1 < t.n(k))
                                 scores(k, ks, j + 2 == t.n(k));
-                            else if (ok && last && more && next.n(k) > 0)
+                            else if (last && more && next.n(k) > 0)
                                 first_scores(next, k, ks);
                         }
-                        release(vs);
-                        if (any) release(ks);
+                        tc_commit(&bars.kv_empty[vs]);
+                        if (any) tc_commit(&bars.kv_empty[ks]);
                     }
-                    __syncwarp();
                 }
                 t = next;
                 live = more;
             }
             // every product complete before tensor memory is given back
-            if (elect_one()) {
-                tc_commit(&bars.drain);
-                if (!mbar_wait_bounded(&bars.drain, 0))
-                    atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
-            }
+            tc_commit(&bars.drain);
+            if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
         }
         __syncwarp();
     } else {  // softmax: tile w = warp / 4, one row a thread
@@ -439,9 +469,11 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        for (int64_t u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+        for (int64_t wave = 0; ok && wave * int64_t(gridDim.x) < a.units; ++wave) {
+            const int64_t u = attn_unit_at(wave);
+            if (u >= a.units) continue;
             const AfUnit t = af_unit(a, u);
-            const int64_t tok = t.tok(tile) + tok_in;
+            const int64_t tok = int64_t(t.tok(tile)) + tok_in;
             const bool valid = tok_in < a.tile_tokens && tok < s.Sq;
             const int n = t.n(tile);
             const int part = PAIRED ? 2 * t.sp + tile : t.sp;
@@ -461,7 +493,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 continue;
             }
-            const int64_t lim = min(t.len, t.pos0 + tok + 1);  // keys this row sees
+            const int64_t lim = min(int64_t(t.len), t.pos0 + tok + 1);  // keys this row sees
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < n; ++j) {
                 ok = all(&bars.s_full[tile], blocks & 1);
@@ -473,7 +505,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, x[q]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_wait_ld(x[q]);
-                const int64_t left = lim - (t.lo(tile) + j) * kAttnRows;  // visible keys of the block
+                const int64_t left = lim - int64_t(t.lo(tile) + j) * kAttnRows;  // visible keys of the block
                 if (__any_sync(0xffffffffu, left < kAttnRows)) {
                     const int seen = int(max(int64_t(0), min(left, int64_t(kAttnRows))));
 #pragma unroll
@@ -613,6 +645,15 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     }
 }
 
+int64_t attn_order_group(const AttnShape& s, int64_t heads, int64_t bytes)
+{
+    if (!s.causal) return 1;
+    int64_t g = (int64_t(64) << 20) / (bytes > 0 ? bytes : 1);
+    if (g > 256) g = 256;
+    if (g > heads) g = heads;
+    return g < 1 ? 1 : g;
+}
+
 // Row tiles, units and parts of the keys. Where one tile holds all rows, a CTA's two tiles take a
 // part each. The keys are split further while the units still fit one wave of the SMs and a part
 // keeps four blocks (a part costs its start, an fp32 output and a share of the join).
@@ -623,8 +664,10 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     const int64_t pair = 2 * int64_t(a->tile_tokens);
     const int64_t blocks = (s.Skv + kAttnRows - 1) / kAttnRows;
     a->paired = s.Sq <= a->tile_tokens && blocks > 1;
-    a->q_blocks = a->paired ? 1 : (s.Sq + pair - 1) / pair;
-    const int64_t base = s.head_begin[s.W] * a->q_blocks;
+    a->order.heads = s.head_begin[s.W];
+    a->order.blocks = a->paired ? 1 : (s.Sq + pair - 1) / pair;
+    a->order.group = attn_order_group(s, a->order.heads, s.Skv * s.d * 4);  // keys and values
+    const int64_t base = a->order.heads * a->order.blocks;
     int64_t n = base > 0 ? sm_count / base : 1;
     const int64_t most = blocks / (a->paired ? 8 : 4);
     if (n > most) n = most;
