@@ -435,7 +435,8 @@ int ulysses_a2a_4d_packed_fused_backward(ulysses_plan_t plan, int planes, int q_
  *   lse  (b, n_r, Sq)  out, fp32: log sum_j exp(scale q_i . k_j), for the backward
  * Only the totals Sq, Skv of the plans' seq_splits matter here. The plans have the same W, b, d
  * (a multiple of 8, at most 128) and dtype (ULY_BF16 or ULY_F16); every rank has n_r = g m_r with
- * one g <= 64: query head h reads key head h / g (shared key heads). Sq, Skv < 2^31 - 256.
+ * one g <= 64: query head h reads key head h / g (shared key heads). Skv and g Sq are at most
+ * 2^26.
  *   kv_lens  NULL, or b device int32: batch element bb holds keys 0 .. kv_lens[bb] - 1 (clamped to
  *            [0, Skv]), a padded batch or a cache with room left. What k and v hold past them is
  *            not used, whatever it is.

@@ -822,12 +822,13 @@ int attn_shape(const Plan& qp, const Plan& kp, AttnShape* s)
 {
     if (qp.dtype != kp.dtype || (qp.dtype != ULY_BF16 && qp.dtype != ULY_F16)) return ULY_EINVAL;
     if (qp.W != kp.W || qp.b != kp.b || qp.d != kp.d || qp.d > kAttnMaxD) return ULY_EINVAL;
-    const int64_t lim = int64_t(1) << 31;  // tensor-map coordinates; lse rows in 64 bits
-    if (qp.S >= lim - 2 * kAttnRows || kp.S >= lim - 2 * kAttnRows || qp.b * kp.N >= lim)
-        return ULY_EINVAL;
     if (kp.N == 0 || qp.N % kp.N != 0) return ULY_EINVAL;
     const int64_t group = qp.N / kp.N;
     if (group > kAttnMaxGroup) return ULY_EINVAL;
+    // A unit walks all of Skv, or all Sq * group rows: 2^26 keep it well inside the kernels' limit
+    // on a wait for a unit's end (and every coordinate in 32 bits).
+    const int64_t lim = int64_t(1) << 26;
+    if (qp.S > lim / group || kp.S > lim || qp.b * kp.N >= (int64_t(1) << 31)) return ULY_EINVAL;
     std::memset(s, 0, sizeof *s);
     s->W = qp.W;
     s->b = int32_t(qp.b);

@@ -11,19 +11,22 @@
 // key) on the tensor cores, one exponential. The kernel is bound by the tensor cores where d = 128
 // and by exponentials and products alike where d = 64; with few rows by reading the keys.
 //
-// A CTA (one per SM, 384 threads) takes two tiles of 128 query rows that share their keys. Warp 8
-// loads (tensor maps, swizzled): the query tiles, then a ring of key and value blocks. Warp 9
-// issues the products: S = Q K^T of one tile while the other tile's 128 threads turn their S into
-// probabilities, so the tensor cores always have one tile's work; a unit's first scores follow the
-// last unit's products without a gap. Warps 0-3 and 4-7 are the two tiles' softmax: tensor memory
-// gives a thread a whole row, so maximum and sum need no exchange; they hold most of the registers.
-// Warp 10 zeroes what a value block holds past a ragged batch element's last key.
+// A CTA (one per SM, 384 threads) takes two tiles of 128 query rows that share their keys, unit
+// after unit. Warp 11 works out the units ahead and leaves their records in shared memory. Warp 8
+// loads (tensor maps, swizzled): query tiles into a few slots, so that the next unit's arrive
+// during this one, and key and value blocks into a ring. One lane of warp 9 issues the products:
+// S = Q K^T of one tile while the other tile's 128 threads turn their S into probabilities, so the
+// tensor cores always have one tile's work; a unit's first scores follow the last unit's products
+// without a gap. Warps 0-3 and 4-7 are the two tiles' softmax: tensor memory gives a thread a whole
+// row, so maximum and sum need no exchange; they hold most of the registers. Warp 10 zeroes what a
+// value block holds past a ragged batch element's last key.
 // P goes back to tensor memory over its own S in 16 bits, rounded to nearest (unit-scale values
 // in an fp32 sum: the output itself is rounded to the same type), and is the A operand of O += P V
 // there, whose first half starts when half of P is written. O stays in tensor memory; it is
 // rescaled only when a row's maximum has grown by more than 2^8 since its last scale (P then stays
 // below 2^8, far inside either type), by the softmax threads themselves: the block's S is complete
-// only after the previous O product. They also write the finished rows.
+// only after the previous O product. They also write the finished rows, turned in the query tile's
+// slot so that a store covers whole 128-byte lines.
 //
 // With few rows (one tile of them: single tokens) both tiles of a CTA are those rows, each over its
 // own part of the keys; with too few units to fill the SMs the keys are split further. A part has
@@ -47,7 +50,10 @@ namespace uly {
 static __device__ unsigned g_attn_fwd_status;
 
 constexpr int kAfThreads = 384;
-constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfCleanWarp = 10;
+constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfCleanWarp = 10, kAfUnitWarp = 11;
+constexpr int kAfUnitSlots = 4;
+constexpr int kAfBarBytes = 1024;
+constexpr int kAfShortBlocks = 8;  // key blocks of a unit up to which it counts as short
 // Registers a thread: 384 x 168 at launch = 256 x 208 + 128 x 88.
 constexpr int kAfRegsSoftmax = 208, kAfRegsOther = 88;
 constexpr float kAfRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
@@ -55,29 +61,22 @@ constexpr float kAfRescale = 8.0f;  // log2 of the growth of a row's maximum tha
 // Tensor memory columns: the two tiles' scores (their probabilities over them), their outputs.
 constexpr int kAfS = 0, kAfO = 256;
 
-template <int DP>
+// How a launch uses its units: two tiles with long runs of shared keys; the same with few key
+// blocks, where the next queries need the room more than further keys; or one tile's rows twice,
+// over two parts of the keys.
+enum AfMode { kAfLong = 0, kAfShort = 1, kAfPaired = 2 };
+
+template <int DP, int MODE>
 struct AfSmem {
     static constexpr int kTile = kAttnRows * DP * 2;  // a tile of 128 rows; a block of 128 keys
     static constexpr int kHalf = kAttnRows * 128;     // its part of 64 columns
-    static constexpr int kStages = DP == 128 ? 5 : 8;
-    static constexpr int kQ = 1024;  // barriers first
-    static constexpr int kRing = kQ + 2 * kTile;
+    static constexpr int kSlots = DP == 64 ? 4 : MODE == kAfLong ? 3 : MODE == kAfShort ? 4 : 2;
+    static constexpr int kStages = DP == 64 ? 8 : 7 - kSlots;
+    static constexpr int kQ = kAfBarBytes;  // barriers first
+    static constexpr int kRing = kQ + kSlots * kTile;
     static constexpr int kTotal = kRing + kStages * kTile;
     static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");  // and room to align the base
 };
-
-struct AfBars {
-    uint64_t q_full[2], q_empty[2];  // a tile's queries landed; its last scores have read them
-    uint64_t s_full[2];              // scores complete
-    uint64_t p_half[2], p_ready[2];  // half of the probabilities (and a rescaled O) written; all
-    uint64_t o_full[2], o_free[2];   // output complete; read out
-    uint64_t kv_full[8], kv_empty[8];
-    uint64_t clean[8];               // rows past the last key zeroed
-    uint64_t drain;
-    uint32_t tmem;
-    int dead;
-};
-static_assert(sizeof(AfBars) <= 1024, "barriers");
 
 struct AfUnit {
     int r, bb, kvh, sp;
@@ -91,6 +90,21 @@ struct AfUnit {
     __device__ __forceinline__ int tok(int k) const { return k ? tok1 : tok0; }
     __device__ __forceinline__ int most() const { return max(n0, n1); }
 };
+
+struct AfBars {
+    uint64_t u_full[kAfUnitSlots], u_empty[kAfUnitSlots];  // unit records
+    uint64_t q_full[4], q_empty[4];  // query tile landed; its rows are written
+    uint64_t s_full[2];              // scores complete
+    uint64_t p_half[2], p_ready[2];  // half of the probabilities (and a rescaled O) written; all
+    uint64_t o_full[2], o_free[2];   // output complete; read out
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t clean[8];               // rows past the last key zeroed
+    uint64_t drain;
+    uint32_t tmem;
+    int dead;
+    AfUnit unit[kAfUnitSlots];       // r < 0: no more
+};
+static_assert(sizeof(AfBars) <= kAfBarBytes, "barriers");
 
 // Key blocks that the tile of tokens from `tok` on sees.
 __device__ __forceinline__ int af_blocks(const AttnFwdArgs& a, const AfUnit& t, int64_t tok)
@@ -140,57 +154,89 @@ __device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
     return t;
 }
 
-// The CTA's next unit with any work from *wave on (false: none).
-__device__ __forceinline__ bool af_next(const AttnFwdArgs& a, int64_t* wave, AfUnit* t)
-{
-    for (;; ++*wave) {
-        const int64_t u = attn_unit_at(*wave);
-        if (*wave * int64_t(gridDim.x) >= a.units) return false;
-        if (u >= a.units) continue;
-        *t = af_unit(a, u);
-        if (t->most() > 0) {
-            ++*wave;
-            return true;
-        }
+// A warp's (or thread's) way through the CTA's units.
+struct AfUnits {
+    AfBars* bars;
+    StageRing ring;
+    // The next unit; false: none, or the CTA has given up. WARP: called by a whole warp.
+    template <bool WARP>
+    __device__ __forceinline__ bool next(AfUnit* t)
+    {
+        bool ok = wait_or_dead(&bars->u_full[ring.s], ring.phase, &bars->dead);
+        if (WARP) ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        *t = bars->unit[ring.s];
+        if (t->r < 0) return false;
+        if (WARP) __syncwarp();
+        if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&bars->u_empty[ring.s]);
+        ring.next(kAfUnitSlots);
+        return true;
     }
+};
+
+// Where a tile's row goes: its output, its log-sum-exp (or its part's), whether there is such a row.
+struct AfRow {
+    int64_t tok, o, part;  // token; byte offset in the rank's output; row of the part arrays
+    float* lse;
+    bool valid;
+};
+
+__device__ __forceinline__ AfRow af_row(const AttnFwdArgs& a, const AfUnit& t, int tile, int tok_in,
+                                        int head_in)
+{
+    const AttnShape& s = a.s;
+    AfRow r;
+    r.tok = int64_t(t.tok(tile)) + tok_in;
+    r.valid = tok_in < a.tile_tokens && r.tok < s.Sq;
+    const int head = t.kvh * s.group + head_in;
+    const int64_t row = (int64_t(t.bb) * s.n[t.r] + head) * s.Sq + r.tok;
+    r.o = ((int64_t(t.bb) * s.Sq + r.tok) * s.n[t.r] + head) * s.d * 2;
+    r.part = (a.paired ? 2 * t.sp + tile : t.sp) * s.row_begin[s.W] + s.row_begin[t.r] + row;
+    r.lse = a.parts == 1 ? a.lse[t.r] + row : a.part_lse + r.part;
+    return r;
 }
 
-// The order in which a CTA's queries and blocks of keys and values come: queries(t) before a unit's
-// first block, block(value, t, key block) for every stage of the ring; both return false to stop.
-// A unit's first scores are wanted before the last products of the unit before.
-template <bool PAIRED, class Queries, class Block>
-__device__ __forceinline__ void af_walk(const AttnFwdArgs& a, Queries queries, Block block)
+// A row that sees no key (or no key of its part, which then has no output).
+__device__ __forceinline__ void af_empty_row(const AttnFwdArgs& a, const AfUnit& t, const AfRow& r)
 {
-    int64_t wave = 0;
-    AfUnit t, next;
-    bool live = af_next(a, &wave, &t);
-    if (!live || !queries(t)) return;
-    if (PAIRED) {
-        if (t.n0 > 0 && !block(false, t, t.lo0)) return;
-        if (t.n1 > 0 && !block(false, t, t.lo1)) return;
-    }
+    if (!r.valid) return;
+    *r.lse = -INFINITY;
+    if (a.parts == 1)
+        for (int c = 0; c < a.s.d * 2; c += 16) st_v4(a.o[t.r] + r.o + c, make_uint4(0, 0, 0, 0));
+}
+
+// The order in which a CTA's blocks of keys and values come, the products' own: block(value, t, key
+// block) for every stage of the ring, and queries(t) for a unit's query tiles, after its first keys
+// (a slot for them may have to wait for the unit before to finish, which those keys must not).
+// Both return false to stop.
+template <bool PAIRED, bool WARP, class Queries, class Block>
+__device__ __forceinline__ void af_walk(AfBars* bars, Queries queries, Block block)
+{
+    AfUnits units{bars};
+    AfUnit t;
+    bool live = units.next<WARP>(&t);
     while (live) {
-        const bool more = af_next(a, &wave, &next);
         const int n = t.most();
-        for (int j = 0; j < n; ++j) {
-            if constexpr (PAIRED) {  // V of a tile's block, then its next K
-                if (j + 1 == n && more && !queries(next)) return;
+        if constexpr (PAIRED) {  // each tile has keys of its own
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (t.n(k) > 0 && !block(false, t, t.lo(k))) return;
+            if (!queries(t)) return;
+            for (int j = 0; j < n; ++j) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (j < t.n(k) && !block(true, t, t.lo(k) + j)) return;
-                    if (j + 1 < t.n(k)) {
-                        if (!block(false, t, t.lo(k) + j + 1)) return;
-                    } else if (j + 1 == n && more && next.n(k) > 0) {
-                        if (!block(false, next, next.lo(k))) return;
-                    }
+                    if (j + 1 < t.n(k) && !block(false, t, t.lo(k) + j + 1)) return;
                 }
-            } else {  // K0 V0 K1 V1 ...
-                if (!block(false, t, t.lo0 + j) || !block(true, t, t.lo0 + j)) return;
+            }
+        } else {
+            if (!block(false, t, t.lo0) || !queries(t)) return;
+            for (int j = 0; j < n; ++j) {
+                if (!block(true, t, t.lo0 + j)) return;
+                if (j + 1 < n && !block(false, t, t.lo0 + j + 1)) return;
             }
         }
-        if (!PAIRED && more && !queries(next)) return;
-        t = next;
-        live = more;
+        live = units.next<WARP>(&t);
     }
 }
 
@@ -202,13 +248,14 @@ __device__ __forceinline__ int af_past(const AttnShape& s, const AfUnit& t, int 
     return past >= kAttnRows || t.len >= s.Skv ? kAttnRows : past;
 }
 
-template <int DP, bool F16, bool PAIRED>
+template <int DP, bool F16, int MODE>
 __global__ void __launch_bounds__(kAfThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnFwdArgs a)
 {
-    using L = AfSmem<DP>;
+    using L = AfSmem<DP, MODE>;
     using E = ElemT<F16>;
-    constexpr int K = L::kStages;
+    constexpr int K = L::kStages, Q = L::kSlots;
+    constexpr bool PAIRED = MODE == kAfPaired;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -220,9 +267,15 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     const int halves = (s.d + 63) / 64;  // tiles of 64 columns
 
     if (threadIdx.x == 0) {
+        for (int k = 0; k < kAfUnitSlots; ++k) {
+            mbar_init(&bars.u_full[k], 1);
+            mbar_init(&bars.u_empty[k], s.kv_lens ? 11 : 10);  // warps 0-9, and 10
+        }
+        for (int k = 0; k < Q; ++k) {
+            mbar_init(&bars.q_full[k], 1);
+            mbar_init(&bars.q_empty[k], 4);
+        }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&bars.q_full[t], 1);
-            mbar_init(&bars.q_empty[t], 1);
             mbar_init(&bars.s_full[t], 1);
             mbar_init(&bars.p_half[t], 4);
             mbar_init(&bars.p_ready[t], 4);
@@ -248,21 +301,23 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         regs_shrink<kAfRegsOther>();
         if (warp == kAfLoadWarp && lane == 0) {
             StageRing ring;
-            uint32_t uses[2] = {0, 0};
-            int64_t issued = 0;
+            StageRing slots;
+            int64_t issued = 0, tiles = 0;
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             auto queries = [&](const AfUnit& t) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (t.n(k) == 0) continue;
-                    if (uses[k] > 0 && !wait_or_dead(&bars.q_empty[k], (uses[k] - 1) & 1, dead))
+                    if (tiles >= Q && !wait_or_dead(&bars.q_empty[slots.s], slots.phase ^ 1u, dead))
                         return false;
-                    mbar_arrive_expect_tx(&bars.q_full[k], q_bytes);
+                    mbar_arrive_expect_tx(&bars.q_full[slots.s], q_bytes);
                     for (int h = 0; h < halves; ++h)
-                        tensor_g2s_4d(smem + L::kQ + k * L::kTile + h * L::kHalf, &a.qmap[t.r],
-                                      64 * h, t.kvh * s.group, t.tok(k), t.bb, &bars.q_full[k]);
-                    ++uses[k];
+                        tensor_g2s_4d(smem + L::kQ + slots.s * L::kTile + h * L::kHalf,
+                                      &a.qmap[t.r], 64 * h, t.kvh * s.group, t.tok(k), t.bb,
+                                      &bars.q_full[slots.s]);
+                    ++tiles;
+                    slots.next(Q);
                 }
                 return true;
             };
@@ -278,20 +333,20 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 ring.next(K);
                 return true;
             };
-            af_walk<PAIRED>(a, queries, block);
+            af_walk<PAIRED, false>(&bars, queries, block);
             // leave no copy into this CTA's shared memory in flight
             for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k)
                 if (!mbar_wait_bounded(&bars.kv_full[k % K], uint32_t((k / K) & 1)))
                     atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
-            for (int k = 0; k < 2; ++k)
-                if (uses[k] > 0 && !mbar_wait_bounded(&bars.q_full[k], (uses[k] - 1) & 1))
+            for (int64_t k = max(int64_t(0), tiles - Q); k < tiles; ++k)
+                if (!mbar_wait_bounded(&bars.q_full[k % Q], uint32_t((k / Q) & 1)))
                     atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
         } else if (warp == kAfCleanWarp && s.kv_lens) {
             // A masked probability is zero, but zero times whatever lies past the last key may be
             // NaN: a value block's rows past it become zeros before its product.
             StageRing ring;
-            af_walk<PAIRED>(
-                a, [](const AfUnit&) { return true; },
+            af_walk<PAIRED, true>(
+                &bars, [](const AfUnit&) { return true; },
                 [&](bool value, const AfUnit& t, int at) {
                     const int past = value ? af_past(s, t, at) : kAttnRows;
                     if (!__all_sync(0xffffffffu,
@@ -319,15 +374,16 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             const uint64_t q_desc = tc_desc_k(smem_u32(smem + L::kQ));
             const uint64_t k_desc = tc_desc_k(smem_u32(smem + L::kRing));
             const uint64_t v_desc = tc_desc_mn(smem_u32(smem + L::kRing), L::kHalf);
-            StageRing ring;
+            StageRing ring, slots;
+            int slot[2] = {0, 0};  // of each tile's queries
             uint32_t uses[2] = {0, 0}, blocks[2] = {0, 0};
             uint32_t cleaned = 0;  // parity of each stage's `clean`
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 return ok = ok && wait_or_dead(bar, parity, dead);
             };
-            auto scores = [&](int k, int stage, bool last) {  // S_k = Q_k K^T
-                const uint64_t qd = q_desc + k * (L::kTile >> 4);
+            auto scores = [&](int k, int stage) {  // S_k = Q_k K^T
+                const uint64_t qd = q_desc + slot[k] * (L::kTile >> 4);
                 const uint64_t kd = k_desc + stage * (L::kTile >> 4);
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
@@ -336,12 +392,13 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     tc_mma_ss(tmem + kAfS + k * 128, qd + off, kd + off, id_s, ks > 0);
                 }
                 tc_commit(&bars.s_full[k]);
-                if (last) tc_commit(&bars.q_empty[k]);  // the tile's queries are done with
             };
-            auto first_scores = [&](const AfUnit& t, int k, int stage) {  // of a unit
-                if (!wait(&bars.q_full[k], uses[k] & 1)) return;
+            auto first_scores = [&](int k, int stage) {  // of a unit, its tiles in order
+                if (!wait(&bars.q_full[slots.s], slots.phase)) return;
+                slot[k] = slots.s;
+                slots.next(Q);
                 tc_fence_after();
-                scores(k, stage, t.n(k) == 1);
+                scores(k, stage);
             };
             auto output = [&](const AfUnit& t, int k, int stage, int j) {  // O_k += P_k V
                 wait(&bars.p_half[k], blocks[k] & 1);
@@ -373,31 +430,33 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 return ok;
             };
-            int64_t wave = 0;
-            AfUnit t, next;
-            bool live = af_next(a, &wave, &t);
-            if (live) {  // the first unit's first scores
-                if (!PAIRED) stage_ready();
+            auto unit_scores = [&](const AfUnit& t) {  // a paired unit's first scores
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    if (t.n(k) == 0) continue;
-                    if (PAIRED) stage_ready();
-                    first_scores(t, k, ring.s);
-                    if (PAIRED) {
-                        tc_commit(&bars.kv_empty[ring.s]);
-                        ring.next(K);
-                    }
+                    if (t.n(k) == 0 || !stage_ready()) continue;
+                    first_scores(k, ring.s);
+                    tc_commit(&bars.kv_empty[ring.s]);
+                    ring.next(K);
                 }
-                if (!PAIRED) {
+            };
+            AfUnits units{&bars};
+            AfUnit t, next;
+            bool live = units.next<false>(&t);
+            if (live) {
+                if constexpr (PAIRED) {
+                    unit_scores(t);
+                } else if (stage_ready()) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (t.n(k) > 0) first_scores(k, ring.s);
                     tc_commit(&bars.kv_empty[ring.s]);
                     ring.next(K);
                 }
             }
             while (live && ok) {
-                const bool more = af_next(a, &wave, &next);
+                const bool more = units.next<false>(&next);
                 const int n = t.most();
                 for (int j = 0; ok && j < n; ++j) {
-                    const bool last = j + 1 == n;
                     if constexpr (PAIRED) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
@@ -407,18 +466,15 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                                 tc_commit(&bars.kv_empty[ring.s]);
                                 ring.next(K);
                             }
-                            const bool same = j + 1 < t.n(k);
-                            if (same || (last && more && next.n(k) > 0)) {
+                            if (j + 1 < t.n(k)) {
                                 if (!stage_ready()) break;
-                                if (same)
-                                    scores(k, ring.s, j + 2 == t.n(k));
-                                else
-                                    first_scores(next, k, ring.s);
+                                scores(k, ring.s);
                                 tc_commit(&bars.kv_empty[ring.s]);
                                 ring.next(K);
                             }
                         }
                     } else {
+                        const bool last = j + 1 == n;
                         const int vs = ring.s;
                         if (!values_ready(t, t.lo0 + j)) break;
                         ring.next(K);
@@ -433,20 +489,54 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                             if (j < t.n(k)) output(t, k, vs, j);
                             if (!ok) break;
                             if (j + 1 < t.n(k))
-                                scores(k, ks, j + 2 == t.n(k));
+                                scores(k, ks);
                             else if (last && more && next.n(k) > 0)
-                                first_scores(next, k, ks);
+                                first_scores(k, ks);
                         }
                         tc_commit(&bars.kv_empty[vs]);
                         if (any) tc_commit(&bars.kv_empty[ks]);
                     }
                 }
+                if (PAIRED && more) unit_scores(next);
                 t = next;
                 live = more;
             }
             // every product complete before tensor memory is given back
             tc_commit(&bars.drain);
             if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
+        }
+        else if (warp == kAfUnitWarp) {
+            StageRing ring;
+            bool ok = true;
+            int64_t made = 0;
+            auto publish = [&](const AfUnit& t) {
+                if (made >= kAfUnitSlots)
+                    ok = __all_sync(0xffffffffu,
+                                    wait_or_dead(&bars.u_empty[ring.s], ring.phase ^ 1u, dead));
+                if (ok && lane == 0) {
+                    bars.unit[ring.s] = t;
+                    mbar_arrive(&bars.u_full[ring.s]);
+                }
+                ++made;
+                ring.next(kAfUnitSlots);
+            };
+            AfUnit t;
+            for (int64_t wave = 0; ok && wave * int64_t(gridDim.x) < a.units; ++wave) {
+                const int64_t u = attn_unit_at(wave);
+                if (u >= a.units) continue;
+                t = af_unit(a, u);
+                if (t.most() > 0) {
+                    publish(t);
+                } else {  // nothing to do but say so (the other warps see units with work only)
+                    for (int i = lane; i < 2 * kAttnRows; i += 32) {
+                        const int tile = i / kAttnRows, row = i % kAttnRows;
+                        const int tok_in = row / s.group;
+                        af_empty_row(a, t, af_row(a, t, tile, tok_in, row - tok_in * s.group));
+                    }
+                }
+            }
+            t.r = -1;
+            if (ok) publish(t);
         }
         __syncwarp();
     } else {  // softmax: tile w = warp / 4, one row a thread
@@ -469,31 +559,25 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        for (int64_t wave = 0; ok && wave * int64_t(gridDim.x) < a.units; ++wave) {
-            const int64_t u = attn_unit_at(wave);
-            if (u >= a.units) continue;
-            const AfUnit t = af_unit(a, u);
-            const int64_t tok = int64_t(t.tok(tile)) + tok_in;
-            const bool valid = tok_in < a.tile_tokens && tok < s.Sq;
+        AfUnits units{&bars};
+        StageRing slots;
+        AfUnit t;
+        while (ok && units.next<true>(&t)) {
+            int slot = 0;  // of this tile's queries
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (t.n(k) == 0) continue;
+                if (k == tile) slot = slots.s;
+                slots.next(Q);
+            }
+            const AfRow to = af_row(a, t, tile, tok_in, head_in);
             const int n = t.n(tile);
-            const int part = PAIRED ? 2 * t.sp + tile : t.sp;
-            // this row's log-sum-exp and output, or its part of them
-            const int head = t.kvh * s.group + head_in;
-            const int64_t row_r = (int64_t(t.bb) * s.n[t.r] + head) * s.Sq + tok;
-            const int64_t row_part = part * s.row_begin[s.W] + s.row_begin[t.r] + row_r;
             const bool whole = a.parts == 1;
-            float* lse = whole ? a.lse[t.r] + row_r : a.part_lse + row_part;
-            uint8_t* o_row = a.o[t.r] + ((int64_t(t.bb) * s.Sq + tok) * s.n[t.r] + head) * s.d * 2;
-            if (n == 0) {  // nothing visible to any row of the tile
-                if (valid) {
-                    *lse = -INFINITY;
-                    if (whole)
-                        for (int c = 0; c < s.d * 2; c += 16)
-                            st_v4(o_row + c, make_uint4(0, 0, 0, 0));
-                }
+            if (n == 0) {
+                af_empty_row(a, t, to);
                 continue;
             }
-            const int64_t lim = min(int64_t(t.len), t.pos0 + tok + 1);  // keys this row sees
+            const int64_t lim = min(int64_t(t.len), t.pos0 + to.tok + 1);  // keys this row sees
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < n; ++j) {
                 ok = all(&bars.s_full[tile], blocks & 1);
@@ -566,8 +650,9 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays NaN
-            if (valid) *lse = l == 0.0f ? -INFINITY : m * s.scale + logf(l);
-            float* o_part = a.part_o + row_part * s.d;
+            if (to.valid) *to.lse = l == 0.0f ? -INFINITY : m * s.scale + logf(l);
+            float* o_part = a.part_o + to.part * s.d;
+            uint8_t* stage = smem + L::kQ + slot * L::kTile;  // the queries are done with
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t y[32];
@@ -578,24 +663,44 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.o_free[tile]);
                 }
-                if (!valid) continue;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // eight columns
-                    if (c * 32 + i * 8 >= s.d) continue;
                     float v[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(y[8 * i + k]) * inv;
                     if (whole) {
-                        st_v4(o_row + (c * 32 + i * 8) * 2,
-                              make_uint4(E::pack(v[0], v[1]), E::pack(v[2], v[3]),
-                                         E::pack(v[4], v[5]), E::pack(v[6], v[7])));
-                    } else {
+                        const int word = (c & 1) * 4 + i;
+                        st_shared_v4(stage + (c >> 1) * L::kHalf + row * 128 +
+                                         ((word ^ (row & 7)) << 4),
+                                     make_uint4(E::pack(v[0], v[1]), E::pack(v[2], v[3]),
+                                                E::pack(v[4], v[5]), E::pack(v[6], v[7])));
+                    } else if (to.valid && c * 32 + i * 8 < s.d) {
                         float4* dst = reinterpret_cast<float4*>(o_part + c * 32 + i * 8);
                         dst[0] = make_float4(v[0], v[1], v[2], v[3]);
                         dst[1] = make_float4(v[4], v[5], v[6], v[7]);
                     }
                 }
             }
+            if (whole) {  // this warp's 32 rows, 8 lanes a row's 64 columns
+                __syncwarp();
+                const int64_t at = to.valid ? to.o : -1;
+                const int word = lane & 7;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = i * 4 + (lane >> 3);
+                    const int64_t off = __shfl_sync(0xffffffffu, at, rr);
+#pragma unroll
+                    for (int h = 0; h < DP / 64; ++h) {
+                        if (off < 0 || h * 64 + word * 8 >= s.d) continue;
+                        st_v4(a.o[t.r] + off + h * 128 + word * 16,
+                              ld_shared_v4(stage + h * L::kHalf + ((warp & 3) * 32 + rr) * 128 +
+                                           ((word ^ (rr & 7)) << 4)));
+                    }
+                }
+                fence_proxy_async_shared();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.q_empty[slot]);
             ++uses;
         }
     }
@@ -678,19 +783,19 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     a->units = base * a->splits;
 }
 
-template <int DP, bool F16, bool PAIRED>
+template <int DP, bool F16, int MODE>
 static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int device, int grid)
 {
     static std::atomic<unsigned long long> raised{0};
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
-    constexpr int smem = AfSmem<DP>::kTotal + 1024;
+    constexpr int smem = AfSmem<DP, MODE>::kTotal + 1024;
     if (bit && !(raised.load() & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, F16, PAIRED>,
+        cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, F16, MODE>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit);
     }
-    attn_fwd_kernel<DP, F16, PAIRED><<<grid, kAfThreads, smem, stream>>>(a);
+    attn_fwd_kernel<DP, F16, MODE><<<grid, kAfThreads, smem, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.parts == 1) return e;
     const int64_t blocks = (a.s.row_begin[a.s.W] + 3) / 4;
@@ -701,8 +806,13 @@ static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int
 template <int DP, bool F16>
 static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int device, int grid)
 {
-    return a.paired ? af_launch_mode<DP, F16, true>(a, stream, device, grid)
-                    : af_launch_mode<DP, F16, false>(a, stream, device, grid);
+    if (a.paired) return af_launch_mode<DP, F16, kAfPaired>(a, stream, device, grid);
+    if constexpr (DP == 128) {  // (d <= 64 has room for both)
+        const int64_t blocks = (a.s.Skv + kAttnRows - 1) / kAttnRows;
+        if (blocks <= int64_t(kAfShortBlocks) * a.splits)
+            return af_launch_mode<DP, F16, kAfShort>(a, stream, device, grid);
+    }
+    return af_launch_mode<DP, F16, kAfLong>(a, stream, device, grid);
 }
 
 // One launch over all ranks (and the join); `grid` CTAs at most. The shape, outputs, parts and
