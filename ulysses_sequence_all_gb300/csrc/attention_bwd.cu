@@ -101,6 +101,13 @@ __global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_consta
     }
 }
 
+// P (dP - D) of two columns; d is -D.
+__device__ __forceinline__ float2 ab_ds(uint32_t p0, uint32_t p1, uint32_t y0, uint32_t y1, float2 d)
+{
+    return __fmul2_rn(make_float2(__uint_as_float(p0), __uint_as_float(p1)),
+                      __fadd2_rn(make_float2(__uint_as_float(y0), __uint_as_float(y1)), d));
+}
+
 // 32 columns from `col` on of an accumulator's row, times f, to the row of d elements at `out`.
 template <class E>
 __device__ __forceinline__ void ab_store32(uint8_t* out, int col, int d, const uint32_t (&y)[32],
@@ -466,26 +473,30 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const float4* d4 = z4 + kAttnRows / 4;
+                uint32_t y[2][32];
+                tmem_ld32(dp_at, y[0]);
+                tmem_ld32(dp_at + 32, y[1]);
+                tmem_wait_ld(y[0]);
+                tmem_wait_ld(y[1]);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    uint32_t y[32], p[16];
-                    tmem_ld32(dp_at + q * 32, y);
-                    tmem_wait_ld(y);
+                    uint32_t p[16];
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const float4 dd = d4[q * 8 + c];
-                        float v[4];
-                        v[0] = __uint_as_float(x[q][4 * c]) * (__uint_as_float(y[4 * c]) - dd.x);
-                        v[1] = __uint_as_float(x[q][4 * c + 1]) * (__uint_as_float(y[4 * c + 1]) - dd.y);
-                        v[2] = __uint_as_float(x[q][4 * c + 2]) * (__uint_as_float(y[4 * c + 2]) - dd.z);
-                        v[3] = __uint_as_float(x[q][4 * c + 3]) * (__uint_as_float(y[4 * c + 3]) - dd.w);
-                        if (masked) {  // zero times what lies past the last key may be NaN
+                        const float2 v = ab_ds(x[q][4 * c], x[q][4 * c + 1], y[q][4 * c],
+                                               y[q][4 * c + 1], make_float2(-dd.x, -dd.y));
+                        const float2 w = ab_ds(x[q][4 * c + 2], x[q][4 * c + 3], y[q][4 * c + 2],
+                                               y[q][4 * c + 3], make_float2(-dd.z, -dd.w));
+                        p[2 * c] = E::pack(v.x, v.y);
+                        p[2 * c + 1] = E::pack(w.x, w.y);
+                    }
+                    if (masked) {  // zero times what lies past the last key may be NaN
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (q * 32 + 4 * c + k < from) v[k] = 0.0f;
+                        for (int c = 0; c < 16; ++c) {
+                            if (q * 32 + 2 * c < from) p[c] &= 0xFFFF0000u;
+                            if (q * 32 + 2 * c + 1 < from) p[c] &= 0x0000FFFFu;
                         }
-                        p[2 * c] = E::pack(v[0], v[1]);
-                        p[2 * c + 1] = E::pack(v[2], v[3]);
                     }
                     // in 16 columns from 64 wg + 16 q on: behind what this thread has read
                     tmem_st16(dp_at + q * 16, p);
@@ -858,21 +869,26 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 ok = all(&bars.dp_full, blocks & 1);
                 if (!ok) break;
                 tc_fence_after();
+                uint32_t y[2][32];
+                tmem_ld32(dp_at, y[0]);
+                tmem_ld32(dp_at + 32, y[1]);
+                tmem_wait_ld(y[0]);
+                tmem_wait_ld(y[1]);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    uint32_t y[32], p[16];
-                    tmem_ld32(dp_at + q * 32, y);
-                    tmem_wait_ld(y);
+                    uint32_t p[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        float v0 = __uint_as_float(x[q][2 * c]) * (__uint_as_float(y[2 * c]) - delta);
-                        float v1 = __uint_as_float(x[q][2 * c + 1]) *
-                                   (__uint_as_float(y[2 * c + 1]) - delta);
-                        if (masked) {
-                            if (q * 32 + 2 * c >= seen) v0 = 0.0f;
-                            if (q * 32 + 2 * c + 1 >= seen) v1 = 0.0f;
+                        const float2 v = ab_ds(x[q][2 * c], x[q][2 * c + 1], y[q][2 * c],
+                                               y[q][2 * c + 1], make_float2(-delta, -delta));
+                        p[c] = E::pack(v.x, v.y);
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            if (q * 32 + 2 * c >= seen) p[c] &= 0xFFFF0000u;
+                            if (q * 32 + 2 * c + 1 >= seen) p[c] &= 0x0000FFFFu;
                         }
-                        p[c] = E::pack(v0, v1);
                     }
                     tmem_st16(s_at + q * 16, p);
                 }

@@ -189,12 +189,13 @@ __device__ __forceinline__ float ex2(float x)
 }
 
 // A wait inside a CTA whose warps give up together: false once the phase did not complete within
-// the time limit, or once another warp of the CTA has given up (*dead).
+// the time limit, or once another warp of the CTA has given up (*dead). A waiting thread is parked
+// by the hardware (up to 10 us at a time) instead of polling: the warps at work need the issue slots.
 __device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, volatile int* dead)
 {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_hint<10000>(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_wait_hint<10000>(bar, parity)) {
         if (*dead) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             *dead = 1;
