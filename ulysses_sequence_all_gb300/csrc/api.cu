@@ -948,7 +948,8 @@ int attn_fwd_device(const Plan& qp, const Plan& kp, const void* const* q, const 
         a.o[r] = static_cast<uint8_t*>(o[r]);
         a.lse[r] = lse[r];
     }
-    const cudaError_t e = attn_fwd_launch(a, q, k, v, stream, dev.device, attn_grid(qp, dev));
+    const cudaError_t e = attn_fwd_launch(a, q, k, v, stream, dev.device, attn_grid(qp, dev),
+                                          dev.sm_count);
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
 
@@ -1007,7 +1008,8 @@ int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const
         a.dk[r] = static_cast<uint8_t*>(dk[r]);
         a.dv[r] = static_cast<uint8_t*>(dv[r]);
     }
-    const cudaError_t e = attn_bwd_launch(a, q, k, v, stream, dev.device, attn_grid(qp, dev));
+    const cudaError_t e = attn_bwd_launch(a, q, k, v, stream, dev.device, attn_grid(qp, dev),
+                                          dev.sm_count);
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
 

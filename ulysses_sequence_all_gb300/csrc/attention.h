@@ -13,7 +13,7 @@
 
 #include "plan.h"
 #ifdef __CUDACC__
-#include "ptx.cuh"
+#include "tcgen05.cuh"
 #endif
 
 namespace uly {
@@ -37,19 +37,12 @@ struct AttnShape {
 };
 
 // Order of the units of a kernel: groups of `group` heads, in a group by block (the longest first
-// when they differ), then by head. Waves of the grid run back and forth over it, which evens out
-// units whose length falls along the order. A group's shared operands fit the L2 cache.
+// when they differ), then by head. A group's shared operands fit the L2 cache.
 struct AttnOrder {
     int64_t heads, blocks, group;
 };
 
 #ifdef __CUDACC__
-__device__ __forceinline__ int64_t attn_unit_at(int64_t wave)
-{
-    const int64_t c = (wave & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-    return wave * gridDim.x + c;
-}
-
 __device__ __forceinline__ void attn_order(const AttnOrder& o, int64_t u, int64_t* head,
                                            int64_t* block)
 {
@@ -59,6 +52,46 @@ __device__ __forceinline__ void attn_order(const AttnOrder& o, int64_t u, int64_
     *block = heads == 1 ? at : div_fast(at, heads);
     *head = g * o.group + (at - *block * heads);
 }
+
+// A CTA's units, asked for by one whole warp. A grid of one CTA per unit (gridDim.x == units): its
+// own, then those of CTAs that have not started, which it takes their place of as it gets there, so
+// that long and short units even out. A smaller grid (a CTA cap): every gridDim.x-th unit, back and
+// forth, which evens out units whose length falls along the order.
+struct AttnUnitSource {
+    int64_t units;
+    void* answer;     // 16 bytes of shared memory
+    uint64_t* bar;    // counts the answer; initialised for one arrival
+    volatile int* dead;
+    int64_t wave = 0;
+    uint32_t phase = 0;
+    bool over = false;
+    __device__ __forceinline__ int64_t next()  // -1: no more
+    {
+        const int64_t grid = gridDim.x;
+        if (grid < units) {
+            while (wave * grid < units) {
+                const int64_t c = (wave & 1) ? grid - 1 - blockIdx.x : blockIdx.x;
+                const int64_t u = wave++ * grid + c;
+                if (u < units) return u;
+            }
+            return -1;
+        }
+        if (wave++ == 0) return blockIdx.x;
+        if (over) return -1;
+        if ((threadIdx.x & 31) == 0) {
+            fence_proxy_async_shared();
+            mbar_arrive_expect_tx(bar, 16);
+            steal_cta(answer, bar);
+        }
+        __syncwarp();
+        const bool ok = __all_sync(0xffffffffu, wait_or_dead(bar, phase, dead));
+        phase ^= 1u;
+        const int64_t u = ok ? stolen_cta(answer) : -1;
+        __syncwarp();
+        over = u < 0;
+        return u;
+    }
+};
 #endif
 
 struct AttnFwdArgs {
@@ -93,15 +126,24 @@ struct AttnBwdArgs {
 };
 
 // Host side.
+// CTAs of a launch of `units`: one each, to be taken over by those that are done (AttnUnitSource),
+// or at most `cap` where the plan caps them or there are more than a grid holds.
+inline unsigned attn_ctas(int64_t units, int64_t cap, int sm_count)
+{
+    if (cap < sm_count || units > 0x7FFFFFFF) return unsigned(units < cap ? units : cap);
+    return unsigned(units);
+}
 // Heads in a group: where blocks differ in length (causal), as many as hold `bytes` each within
 // about half of the L2 cache; else one (neighbouring CTAs then share a head's operands).
 int64_t attn_order_group(const AttnShape& s, int64_t heads, int64_t bytes);
 void attn_fwd_split(AttnFwdArgs* a, int sm_count);  // tiles, units and parts from the shape
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
-                            const void* const* v, cudaStream_t stream, int device, int grid);
+                            const void* const* v, cudaStream_t stream, int device, int grid,
+                            int sm_count);
 cudaError_t attn_fwd_status(unsigned* status, bool clear);
 cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* const* k,
-                            const void* const* v, cudaStream_t stream, int device, int grid);
+                            const void* const* v, cudaStream_t stream, int device, int grid,
+                            int sm_count);
 cudaError_t attn_bwd_status(unsigned* status, bool clear);
 
 }  // namespace uly

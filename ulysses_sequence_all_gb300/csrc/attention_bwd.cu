@@ -11,13 +11,15 @@
 // by both, seven products in place of five: dQ is then summed in one accumulator in a fixed order,
 // with no fp32 copy of it in memory, no atomics, and the same bits from run to run.
 //
-// Both are bound by the tensor cores. One CTA per SM (352 threads): warp 8 loads (swizzled tensor
-// maps), one lane of warp 9 issues the products, warps 0-3 and 4-7 turn scores into P and dS, each
-// the half of the tile's columns in its 128 threads' rows, while the products of the other operand
-// run, and write the finished rows. A unit's first scores follow the last unit's products without a
-// gap. All accumulators are in tensor memory (fp32); P and dS go back to it rounded to the element
-// type, over the columns they came from, and are A operands there. Warp 10 of the dQ kernel zeroes
-// what a key block holds past a ragged batch element's last key.
+// Both are bound by the tensor cores. One CTA per SM (640 threads): 16 warps turn scores into P and
+// dS, each four the same 32 columns of the tile (16 warps rather than 8 with twice the columns: the
+// chain from scores to P is what the products wait for, and more warps hide its latencies). Warp 16
+// loads (swizzled tensor maps), one lane of warp 17 issues the products, which run on one operand
+// while the threads work on the other; a unit's first scores follow the last unit's products
+// without a gap. All accumulators are in tensor memory (fp32); P and dS go back to it rounded to
+// the element type, over the columns they came from, and are A operands there. Warp 18 of the dQ
+// kernel zeroes what a key block holds past a ragged batch element's last key. Warp 19 works out
+// the units ahead.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -35,8 +37,9 @@ namespace uly {
 
 static __device__ unsigned g_attn_bwd_status;
 
-constexpr int kAbThreads = 352;
-constexpr int kAbLoadWarp = 8, kAbMmaWarp = 9, kAbCleanWarp = 10;
+constexpr int kAbThreads = 640;
+constexpr int kAbLoadWarp = 16, kAbMmaWarp = 17, kAbCleanWarp = 18, kAbUnitWarp = 19;
+constexpr int kAbUnitSlots = 4;
 constexpr int kAbStats = 2 * kAttnRows * 4;  // one tile's lse and D
 
 // Keys that batch element bb holds, and the position of its first query (beyond every key when the
@@ -108,13 +111,12 @@ __device__ __forceinline__ float2 ab_ds(uint32_t p0, uint32_t p1, uint32_t y0, u
                       __fadd2_rn(make_float2(__uint_as_float(y0), __uint_as_float(y1)), d));
 }
 
-// 32 columns from `col` on of an accumulator's row, times f, to the row of d elements at `out`.
-template <class E>
-__device__ __forceinline__ void ab_store32(uint8_t* out, int col, int d, const uint32_t (&y)[32],
-                                           float f)
+// N columns from `col` on of an accumulator's row, times f, to the row of d elements at `out`.
+template <class E, int N>
+__device__ __forceinline__ void ab_store(uint8_t* out, int col, int d, const uint32_t (&y)[N], float f)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N / 8; ++i) {
         if (col + i * 8 >= d) continue;
         uint32_t w[4];
 #pragma unroll
@@ -122,6 +124,80 @@ __device__ __forceinline__ void ab_store32(uint8_t* out, int col, int d, const u
             w[k] = E::pack(__uint_as_float(y[8 * i + 2 * k]) * f,
                            __uint_as_float(y[8 * i + 2 * k + 1]) * f);
         st_v4(out + (col + i * 8) * 2, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+}
+
+// The units ahead, worked out by one warp (publish) and read by the others (next). Units without
+// work do not appear.
+template <class Unit>
+struct AbUnitBoard {
+    uint64_t full[kAbUnitSlots], empty[kAbUnitSlots], steal;
+    uint4 answer;
+    Unit unit[kAbUnitSlots];  // n < 0: no more
+};
+
+template <class Unit>
+__device__ __forceinline__ void ab_board_init(AbUnitBoard<Unit>& b, int readers)
+{
+    for (int k = 0; k < kAbUnitSlots; ++k) {
+        mbar_init(&b.full[k], 1);
+        mbar_init(&b.empty[k], readers);
+    }
+    mbar_init(&b.steal, 1);
+}
+
+template <class Unit>
+struct AbUnits {
+    AbUnitBoard<Unit>* board;
+    volatile int* dead;
+    StageRing ring;
+    // The next unit; false: none, or the CTA has given up. WARP: called by a whole warp.
+    template <bool WARP>
+    __device__ __forceinline__ bool next(Unit* t)
+    {
+        bool ok = wait_or_dead(&board->full[ring.s], ring.phase, dead);
+        if (WARP) ok = __all_sync(0xffffffffu, ok);
+        if (ok) *t = board->unit[ring.s];
+        if (!ok || t->n < 0) {
+            t->n = 0;
+            return false;
+        }
+        if (WARP) __syncwarp();
+        if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&board->empty[ring.s]);
+        ring.next(kAbUnitSlots);
+        return true;
+    }
+};
+
+// The warp that works the units out: decode(u) gives a unit, idle(t) deals with one without work.
+template <class Unit, class Decode, class Idle>
+__device__ __forceinline__ void ab_publish(AbUnitBoard<Unit>& b, int64_t units, volatile int* dead,
+                                           Decode decode, Idle idle)
+{
+    StageRing ring;
+    AttnUnitSource source{units, &b.answer, &b.steal, dead};
+    bool ok = true;
+    for (int64_t made = 0; ok;) {
+        const int64_t u = source.next();
+        Unit t;
+        t.n = -1;
+        if (u >= 0) {
+            t = decode(u);
+            if (t.n == 0) {
+                idle(t);
+                continue;
+            }
+        }
+        if (made >= kAbUnitSlots)
+            ok = __all_sync(0xffffffffu, wait_or_dead(&b.empty[ring.s], ring.phase ^ 1u, dead));
+        if (ok && (threadIdx.x & 31) == 0) {
+            b.unit[ring.s] = t;
+            mbar_arrive(&b.full[ring.s]);
+        }
+        __syncwarp();
+        ++made;
+        ring.next(kAbUnitSlots);
+        if (u < 0) break;
     }
 }
 
@@ -143,6 +219,12 @@ struct BkSmem {
     static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");
 };
 
+struct BkUnit {
+    int r, bb, kvh, n;       // n: row tiles from `first` on that see the block
+    int64_t h, kv0, first;
+    int64_t len, pos0;
+};
+
 struct BkBars {
     uint64_t k_full, v_full, k_empty, v_empty;  // key block landed; its last scores have read it
     uint64_t q_full[4], q_empty[4], g_full[4], g_empty[4];
@@ -151,14 +233,9 @@ struct BkBars {
     uint64_t drain;
     uint32_t tmem;
     int dead;
+    AbUnitBoard<BkUnit> board;
 };
 static_assert(sizeof(BkBars) <= 1024, "barriers");
-
-struct BkUnit {
-    int r, bb, kvh, n;       // n: row tiles from `first` on that see the block
-    int64_t h, kv0, first;
-    int64_t len, pos0;
-};
 
 __device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
 {
@@ -174,22 +251,6 @@ __device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
     t.first = row / a.tile_tokens;
     t.n = t.kv0 < t.len && t.first < a.q_tiles ? int(a.q_tiles - t.first) : 0;
     return t;
-}
-
-// The CTA's next unit with any work from *wave on (false: none).
-__device__ __forceinline__ bool bk_next(const AttnBwdArgs& a, int64_t units, int64_t* wave, BkUnit* t)
-{
-    for (; *wave * int64_t(gridDim.x) < units; ++*wave) {
-        const int64_t u = attn_unit_at(*wave);
-        if (u >= units) continue;
-        *t = bk_unit(a, u);
-        if (t->n > 0) {
-            ++*wave;
-            return true;
-        }
-    }
-    t->n = 0;
-    return false;
 }
 
 template <int DP, bool F16>
@@ -221,11 +282,12 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             mbar_init(&bars.g_empty[k], 1);
         }
         mbar_init(&bars.s_full, 1);
-        mbar_init(&bars.p_ready, 8);
+        mbar_init(&bars.p_ready, 16);
         mbar_init(&bars.dp_full, 1);
-        mbar_init(&bars.ds_ready, 8);
+        mbar_init(&bars.ds_ready, 16);
         mbar_init(&bars.acc_full, 1);
-        mbar_init(&bars.acc_free, 8);
+        mbar_init(&bars.acc_free, 16);
+        ab_board_init(bars.board, 18);  // warps 0-17
         mbar_init(&bars.drain, 1);
         bars.dead = 0;
         fence_barrier_init();
@@ -251,9 +313,9 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
-            int64_t wave = 0;
+            AbUnits<BkUnit> source{&bars.board, dead};
             BkUnit t;
-            while (ok && bk_next(a, units, &wave, &t)) {
+            while (ok && source.next<false>(&t)) {
                 for (int w = 0; ok && w < 2; ++w) {
                     if (uses > 0)
                         ok = wait_or_dead(w ? &bars.v_empty : &bars.k_empty, (uses - 1) & 1, dead);
@@ -332,8 +394,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             };
             auto sums = [&](uint32_t d, uint32_t p, uint64_t row, bool first) {
 #pragma unroll
-                for (int ks = 0; ks < kAttnRows / 16; ++ks)  // each warpgroup's 64 columns in 32
-                    tc_mma_ts(tmem + d, tmem + p + (ks >> 2) * 64 + (ks & 3) * 8,
+                for (int ks = 0; ks < kAttnRows / 16; ++ks)  // each warpgroup's 32 columns in 16
+                    tc_mma_ts(tmem + d, tmem + p + (ks >> 1) * 32 + (ks & 1) * 8,
                               row + ks * (2048 >> 4), id_d, !first || ks > 0);
             };
             // S^T (dP^T) of the ring's next row tile; `first`, `last` of the unit
@@ -351,15 +413,15 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 scores(kBkDp, v_desc, g_desc + ring.s * (L::kTile >> 4), &bars.dp_full);
                 if (last) tc_commit(&bars.v_empty);
             };
-            int64_t wave = 0;
+            AbUnits<BkUnit> source{&bars.board, dead};
             BkUnit t, next;
-            bool live = bk_next(a, units, &wave, &t);
+            bool live = source.next<false>(&t);
             if (live) {
                 next_s(true, t.n == 1, 0);
                 next_dp(true, t.n == 1, 0);
             }
             while (live && ok) {
-                const bool more = bk_next(a, units, &wave, &next);
+                const bool more = source.next<false>(&next);
                 for (int i = 0; ok && i < t.n; ++i, ++tiles) {
                     const int at = ring.s;
                     const bool end = i + 1 == t.n;           // the next tile is the next unit's
@@ -387,13 +449,24 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
         }
         __syncwarp();
+    } else if (warp == kAbUnitWarp) {
+        ab_publish<BkUnit>(
+            bars.board, units, dead, [&](int64_t u) { return bk_unit(a, u); },
+            [&](const BkUnit& t) {  // keys that no row sees
+                for (int i = lane; i < 2 * kAttnRows; i += 32) {
+                    const int64_t key = t.kv0 + i % kAttnRows;
+                    if (key >= s.Skv) continue;
+                    uint8_t* out = (i >= kAttnRows ? a.dv[t.r] : a.dk[t.r]) +
+                                   ((int64_t(t.bb) * s.Skv + key) * s.m[t.r] + t.kvh) * s.d * 2;
+                    for (int c = 0; c < s.d * 2; c += 16) st_v4(out + c, make_uint4(0, 0, 0, 0));
+                }
+            });
     } else if (warp < kAbLoadWarp) {
-        const int wg = warp >> 2;  // columns 64 wg .. 64 wg + 63; then dK (0) or dV (1)
+        const int wg = warp >> 2;  // columns 32 wg .. 32 wg + 31; then a half of dK (0, 1) or dV
         const int row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;
-        const uint32_t s_at = tmem + lanes + kBkS + wg * 64;
-        const uint32_t dp_at = tmem + lanes + kBkDp + wg * 64;
-        const uint32_t acc_at = tmem + lanes + (wg ? kBkDv : kBkDk);
+        const uint32_t s_at = tmem + lanes + kBkS + wg * 32;
+        const uint32_t dp_at = tmem + lanes + kBkDp + wg * 32;
         const float sl2 = s.scale * 1.4426950408889634f;
         StageRing ring;
         uint32_t uses = 0, tiles = 0;
@@ -401,110 +474,85 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         auto all = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
         };
-        for (int64_t wave = 0; ok && wave * int64_t(gridDim.x) < units; ++wave) {
-            const int64_t u = attn_unit_at(wave);
-            if (u >= units) continue;
-            const BkUnit t = bk_unit(a, u);
+        auto arrive = [&](uint64_t* bar) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        AbUnits<BkUnit> source{&bars.board, dead};
+        BkUnit t;
+        while (ok && source.next<true>(&t)) {
             const int64_t key = t.kv0 + row;
-            uint8_t* out = (wg ? a.dv[t.r] : a.dk[t.r]) +
-                           ((int64_t(t.bb) * s.Skv + key) * s.m[t.r] + t.kvh) * s.d * 2;
-            if (t.n == 0) {  // keys that no row sees
-                if (key < s.Skv) {
-                    for (int c = 0; c < s.d * 2; c += 16) st_v4(out + c, make_uint4(0, 0, 0, 0));
-                }
-                continue;
-            }
-            for (int i = 0; i < t.n; ++i) {
-                // the tile's columns from `lo` on see this key
-                const int64_t tok0 = (t.first + i) * a.tile_tokens;
-                int64_t lo = (key - t.pos0 - tok0) * s.group;
-                if (key >= t.len) lo = kAttnRows;
-                const int from = int(max(int64_t(-1), min(lo - 64 * wg, int64_t(64))));
+            // columns of the unit's first tile that see this key begin here, of each next one
+            // tile_tokens * group columns earlier
+            int64_t lo = (key - t.pos0 - t.first * a.tile_tokens) * s.group - 32 * wg;
+            if (key >= t.len) lo = int64_t(1) << 40;
+            for (int i = 0; i < t.n; ++i, lo -= a.tile_tokens * s.group) {
+                const int from = int(max(int64_t(-1), min(lo, int64_t(32))));
                 ok = all(&bars.q_full[ring.s], ring.phase);  // the tile's lse and D
                 ok = ok && all(&bars.s_full, tiles & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const float4* z4 =
-                    reinterpret_cast<const float4*>(smem + L::kStat + ring.s * kAbStats) + wg * 16;
-                uint32_t x[2][32];
-                tmem_ld32(s_at, x[0]);
-                tmem_ld32(s_at + 32, x[1]);
-                tmem_wait_ld(x[0]);
-                tmem_wait_ld(x[1]);
+                    reinterpret_cast<const float4*>(smem + L::kStat + ring.s * kAbStats) + wg * 8;
+                uint32_t x[32];
+                tmem_ld32(s_at, x);
+                tmem_wait_ld(x);
                 const float2 k2 = make_float2(sl2, sl2);
+                uint32_t p[16];
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float4 z = z4[q * 8 + c];
-                        float2 e = __ffma2_rn(make_float2(__uint_as_float(x[q][4 * c]),
-                                                          __uint_as_float(x[q][4 * c + 1])),
-                                              k2, make_float2(-z.x, -z.y));
-                        float2 f = __ffma2_rn(make_float2(__uint_as_float(x[q][4 * c + 2]),
-                                                          __uint_as_float(x[q][4 * c + 3])),
-                                              k2, make_float2(-z.z, -z.w));
-                        x[q][4 * c] = __float_as_uint(ex2(e.x));
-                        x[q][4 * c + 1] = __float_as_uint(ex2(e.y));
-                        x[q][4 * c + 2] = __float_as_uint(ex2(f.x));
-                        x[q][4 * c + 3] = __float_as_uint(ex2(f.y));
-                    }
+                for (int c = 0; c < 8; ++c) {
+                    const float4 z = z4[c];
+                    const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[4 * c]),
+                                                            __uint_as_float(x[4 * c + 1])),
+                                                k2, make_float2(-z.x, -z.y));
+                    const float2 f = __ffma2_rn(make_float2(__uint_as_float(x[4 * c + 2]),
+                                                            __uint_as_float(x[4 * c + 3])),
+                                                k2, make_float2(-z.z, -z.w));
+                    x[4 * c] = __float_as_uint(ex2(e.x));
+                    x[4 * c + 1] = __float_as_uint(ex2(e.y));
+                    x[4 * c + 2] = __float_as_uint(ex2(f.x));
+                    x[4 * c + 3] = __float_as_uint(ex2(f.y));
+                }
                 const bool masked = __any_sync(0xffffffffu, from > 0);
                 if (masked) {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (q * 32 + c < from) x[q][c] = 0;
+                    for (int c = 0; c < 32; ++c)
+                        if (c < from) x[c] = 0;
                 }
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        p[c] = E::pack(__uint_as_float(x[q][2 * c]), __uint_as_float(x[q][2 * c + 1]));
-                    tmem_st16(s_at + q * 16, p);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_ready);
+                for (int c = 0; c < 16; ++c)
+                    p[c] = E::pack(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1]));
+                tmem_st16(s_at, p);
+                arrive(&bars.p_ready);
 
                 ok = all(&bars.dp_full, tiles & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const float4* d4 = z4 + kAttnRows / 4;
-                uint32_t y[2][32];
-                tmem_ld32(dp_at, y[0]);
-                tmem_ld32(dp_at + 32, y[1]);
-                tmem_wait_ld(y[0]);
-                tmem_wait_ld(y[1]);
+                uint32_t y[32];
+                tmem_ld32(dp_at, y);
+                tmem_wait_ld(y);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float4 dd = d4[q * 8 + c];
-                        const float2 v = ab_ds(x[q][4 * c], x[q][4 * c + 1], y[q][4 * c],
-                                               y[q][4 * c + 1], make_float2(-dd.x, -dd.y));
-                        const float2 w = ab_ds(x[q][4 * c + 2], x[q][4 * c + 3], y[q][4 * c + 2],
-                                               y[q][4 * c + 3], make_float2(-dd.z, -dd.w));
-                        p[2 * c] = E::pack(v.x, v.y);
-                        p[2 * c + 1] = E::pack(w.x, w.y);
-                    }
-                    if (masked) {  // zero times what lies past the last key may be NaN
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            if (q * 32 + 2 * c < from) p[c] &= 0xFFFF0000u;
-                            if (q * 32 + 2 * c + 1 < from) p[c] &= 0x0000FFFFu;
-                        }
-                    }
-                    // in 16 columns from 64 wg + 16 q on: behind what this thread has read
-                    tmem_st16(dp_at + q * 16, p);
+                for (int c = 0; c < 8; ++c) {
+                    const float4 dd = d4[c];
+                    const float2 v = ab_ds(x[4 * c], x[4 * c + 1], y[4 * c], y[4 * c + 1],
+                                           make_float2(-dd.x, -dd.y));
+                    const float2 w = ab_ds(x[4 * c + 2], x[4 * c + 3], y[4 * c + 2], y[4 * c + 3],
+                                           make_float2(-dd.z, -dd.w));
+                    p[2 * c] = E::pack(v.x, v.y);
+                    p[2 * c + 1] = E::pack(w.x, w.y);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.ds_ready);
+                if (masked) {  // zero times what lies past the last key may be NaN
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        if (2 * c < from) p[c] &= 0xFFFF0000u;
+                        if (2 * c + 1 < from) p[c] &= 0x0000FFFFu;
+                    }
+                }
+                tmem_st16(dp_at, p);
+                arrive(&bars.ds_ready);
                 ++tiles;
                 ring.next(K);
             }
@@ -512,18 +560,22 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             ok = all(&bars.acc_full, uses & 1);
             if (!ok) break;
             tc_fence_after();
-            const float f = wg ? 1.0f : s.scale;
+            uint8_t* out = (wg >= 2 ? a.dv[t.r] : a.dk[t.r]) +
+                           ((int64_t(t.bb) * s.Skv + key) * s.m[t.r] + t.kvh) * s.d * 2;
+            const float f = wg >= 2 ? 1.0f : s.scale;
+            constexpr int kCols = DP / 2;
 #pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
+            for (int c = 0; c < kCols / 32; ++c) {
+                const int col = (wg & 1) * kCols + c * 32;
                 uint32_t y[32];
-                tmem_ld32(acc_at + c * 32, y);
+                tmem_ld32(tmem + lanes + (wg >= 2 ? kBkDv : kBkDk) + col, y);
                 tmem_wait_ld(y);
-                if (c == DP / 32 - 1) {
+                if (c == kCols / 32 - 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.acc_free);
                 }
-                if (key < s.Skv) ab_store32<E>(out, c * 32, s.d, y, f);
+                if (key < s.Skv) ab_store<E>(out, col, s.d, y, f);
             }
             ++uses;
         }
@@ -549,6 +601,11 @@ struct BqSmem {
     static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");
 };
 
+struct BqUnit {
+    int r, bb, kvh, n;  // n: key blocks that the tile sees
+    int64_t h, tile, tok0, len, pos0;
+};
+
 struct BqBars {
     uint64_t q_full, g_full, q_empty, g_empty;  // row tile landed; its last scores have read it
     uint64_t kv_full[8], kv_empty[8], clean[8];  // clean: K rows past the last key zeroed
@@ -556,13 +613,9 @@ struct BqBars {
     uint64_t acc_full, acc_free, drain;
     uint32_t tmem;
     int dead;
+    AbUnitBoard<BqUnit> board;
 };
 static_assert(sizeof(BqBars) <= 1024, "barriers");
-
-struct BqUnit {
-    int r, bb, kvh, n;  // n: key blocks that the tile sees
-    int64_t h, tile, tok0, len, pos0;
-};
 
 __device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
 {
@@ -577,22 +630,6 @@ __device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
     const int64_t keys = max(int64_t(0), min(t.len, t.pos0 + last + 1));
     t.n = int((keys + kAttnRows - 1) / kAttnRows);
     return t;
-}
-
-// The CTA's next unit with any work from *wave on (false: none).
-__device__ __forceinline__ bool bq_next(const AttnBwdArgs& a, int64_t units, int64_t* wave, BqUnit* t)
-{
-    for (; *wave * int64_t(gridDim.x) < units; ++*wave) {
-        const int64_t u = attn_unit_at(*wave);
-        if (u >= units) continue;
-        *t = bq_unit(a, u);
-        if (t->n > 0) {
-            ++*wave;
-            return true;
-        }
-    }
-    t->n = 0;
-    return false;
 }
 
 // Rows of a key block past the batch element's last key that the tensor holds; kAttnRows: none.
@@ -632,9 +669,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.s_full[0], 1);
         mbar_init(&bars.s_full[1], 1);
         mbar_init(&bars.dp_full, 1);
-        mbar_init(&bars.ds_ready, 8);
+        mbar_init(&bars.ds_ready, 16);
         mbar_init(&bars.acc_full, 1);
-        mbar_init(&bars.acc_free, 8);
+        mbar_init(&bars.acc_free, 16);
+        ab_board_init(bars.board, s.kv_lens ? 19 : 18);  // warps 0-17, and 18
         mbar_init(&bars.drain, 1);
         bars.dead = 0;
         fence_barrier_init();
@@ -653,9 +691,9 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
-            int64_t wave = 0;
+            AbUnits<BqUnit> source{&bars.board, dead};
             BqUnit t;
-            while (ok && bq_next(a, units, &wave, &t)) {
+            while (ok && source.next<false>(&t)) {
                 if (uses > 0)
                     ok = wait_or_dead(&bars.q_empty, (uses - 1) & 1, dead) &&
                          wait_or_dead(&bars.g_empty, (uses - 1) & 1, dead);
@@ -695,10 +733,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         // dS is zero past the last key, but zero times what K holds there may be NaN
         if (s.kv_lens) {
             StageRing ring;
-            int64_t wave = 0;
+            AbUnits<BqUnit> source{&bars.board, dead};
             BqUnit t;
             bool ok = true;
-            while (ok && bq_next(a, units, &wave, &t)) {
+            while (ok && source.next<true>(&t)) {
                 for (int j = 0; ok && j < 2 * t.n; ++j) {  // K0 V0 K1 V1 ...
                     ok = __all_sync(0xffffffffu,
                                     wait_or_dead(&bars.kv_full[ring.s], ring.phase, dead));
@@ -768,16 +806,16 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 if (last) tc_commit(&bars.g_empty);
                 ring.next(K);
             };
-            int64_t wave = 0;
+            AbUnits<BqUnit> source{&bars.board, dead};
             BqUnit t, next;
-            bool live = bq_next(a, units, &wave, &t);
+            bool live = source.next<false>(&t);
             int ks = 0;  // the stage of the current block's K
             if (live) {
                 ks = next_s(true, t.n == 1, 0, 0);
                 next_dp(true, t.n == 1, 0);
             }
             while (live && ok) {
-                const bool more = bq_next(a, units, &wave, &next);
+                const bool more = source.next<false>(&next);
                 for (int j = 0; ok && j < t.n; ++j, ++blocks) {
                     const bool end = j + 1 == t.n;  // the next block is the next unit's
                     const bool last = end ? next.n == 1 : j + 2 == t.n;
@@ -795,7 +833,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < kAttnRows / 16; ++kk)
                         tc_mma_ts(tmem + kBqDq,
-                                  tmem + kBqS + (blocks & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                                  tmem + kBqS + (blocks & 1) * 128 + (kk >> 1) * 32 + (kk & 1) * 8,
                                   kd + kk * (2048 >> 4), id_d, j > 0 || kk > 0);
                     tc_commit(&bars.kv_empty[ks]);
                     if (end) {
@@ -813,11 +851,24 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
         }
         __syncwarp();
+    } else if (warp == kAbUnitWarp) {
+        ab_publish<BqUnit>(
+            bars.board, units, dead, [&](int64_t u) { return bq_unit(a, u); },
+            [&](const BqUnit& t) {  // rows that see no key
+                for (int i = lane; i < kAttnRows; i += 32) {
+                    const int tok_in = i / s.group;
+                    const int64_t tok = t.tok0 + tok_in;
+                    if (tok_in >= a.tile_tokens || tok >= s.Sq) continue;
+                    uint8_t* out = a.dq[t.r] + ((int64_t(t.bb) * s.Sq + tok) * s.n[t.r] +
+                                                t.kvh * s.group + i - tok_in * s.group) * s.d * 2;
+                    for (int c = 0; c < s.d * 2; c += 16) st_v4(out + c, make_uint4(0, 0, 0, 0));
+                }
+            });
     } else {
-        const int wg = warp >> 2;  // keys 64 wg .. 64 wg + 63 of a block
+        const int wg = warp >> 2;  // keys 32 wg .. 32 wg + 31 of a block; then a quarter of dQ
         const int row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;
-        const uint32_t dp_at = tmem + lanes + kBqDp + wg * 64;
+        const uint32_t dp_at = tmem + lanes + kBqDp + wg * 32;
         const float sl2 = s.scale * 1.4426950408889634f;
         const int tok_in = row / s.group, head_in = row - tok_in * s.group;
         uint32_t uses = 0, blocks = 0;
@@ -825,97 +876,74 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         auto all = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
         };
-        for (int64_t wave = 0; ok && wave * int64_t(gridDim.x) < units; ++wave) {
-            const int64_t u = attn_unit_at(wave);
-            if (u >= units) continue;
-            const BqUnit t = bq_unit(a, u);
+        AbUnits<BqUnit> source{&bars.board, dead};
+        BqUnit t;
+        while (ok && source.next<true>(&t)) {
             const int64_t tok = t.tok0 + tok_in;
             const bool valid = tok_in < a.tile_tokens && tok < s.Sq;
-            uint8_t* out = a.dq[t.r] + ((int64_t(t.bb) * s.Sq + tok) * s.n[t.r] +
-                                        t.kvh * s.group + head_in) * s.d * 2;
-            if (t.n == 0) {
-                if (wg == 0 && valid) {
-                    for (int c = 0; c < s.d * 2; c += 16) st_v4(out + c, make_uint4(0, 0, 0, 0));
-                }
-                continue;
-            }
             const float* stat = a.stats + (t.h * a.q_tiles + t.tile) * 2 * kAttnRows + row;
             const float z = -stat[0], delta = stat[kAttnRows];
-            const int64_t lim = min(t.len, t.pos0 + tok + 1);
-            for (int j = 0; j < t.n; ++j) {
-                const uint32_t s_at = tmem + lanes + kBqS + (blocks & 1) * 128 + wg * 64;
-                const int64_t left = lim - int64_t(j) * kAttnRows - 64 * wg;
-                const int seen = int(max(int64_t(0), min(left, int64_t(64))));
+            int64_t left = min(t.len, t.pos0 + tok + 1) - 32 * wg;  // visible keys from here on
+            for (int j = 0; j < t.n; ++j, ++blocks, left -= kAttnRows) {
+                const uint32_t s_at = tmem + lanes + kBqS + (blocks & 1) * 128 + wg * 32;
+                const int seen = int(max(int64_t(0), min(left, int64_t(32))));
                 ok = all(&bars.s_full[blocks & 1], (blocks >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t x[2][32];
-                tmem_ld32(s_at, x[0]);
-                tmem_ld32(s_at + 32, x[1]);
-                tmem_wait_ld(x[0]);
-                tmem_wait_ld(x[1]);
+                uint32_t x[32];
+                tmem_ld32(s_at, x);
+                tmem_wait_ld(x);
                 const float2 k2 = make_float2(sl2, sl2), z2 = make_float2(z, z);
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const float2 e = __ffma2_rn(make_float2(__uint_as_float(x[q][2 * c]),
-                                                                __uint_as_float(x[q][2 * c + 1])),
-                                                    k2, z2);
-                        x[q][2 * c] = __float_as_uint(ex2(e.x));
-                        x[q][2 * c + 1] = __float_as_uint(ex2(e.y));
-                    }
-                const bool masked = __any_sync(0xffffffffu, seen < 64);
+                for (int c = 0; c < 16; ++c) {
+                    const float2 e = __ffma2_rn(
+                        make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), k2, z2);
+                    x[2 * c] = __float_as_uint(ex2(e.x));
+                    x[2 * c + 1] = __float_as_uint(ex2(e.y));
+                }
+                const bool masked = __any_sync(0xffffffffu, seen < 32);
                 ok = all(&bars.dp_full, blocks & 1);
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t y[2][32];
-                tmem_ld32(dp_at, y[0]);
-                tmem_ld32(dp_at + 32, y[1]);
-                tmem_wait_ld(y[0]);
-                tmem_wait_ld(y[1]);
+                uint32_t y[32], p[16];
+                tmem_ld32(dp_at, y);
+                tmem_wait_ld(y);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t p[16];
+                for (int c = 0; c < 16; ++c) {
+                    const float2 v = ab_ds(x[2 * c], x[2 * c + 1], y[2 * c], y[2 * c + 1],
+                                           make_float2(-delta, -delta));
+                    p[c] = E::pack(v.x, v.y);
+                }
+                if (masked) {  // zero times what lies past the last key may be NaN
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        const float2 v = ab_ds(x[q][2 * c], x[q][2 * c + 1], y[q][2 * c],
-                                               y[q][2 * c + 1], make_float2(-delta, -delta));
-                        p[c] = E::pack(v.x, v.y);
+                        if (2 * c >= seen) p[c] &= 0xFFFF0000u;
+                        if (2 * c + 1 >= seen) p[c] &= 0x0000FFFFu;
                     }
-                    if (masked) {
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            if (q * 32 + 2 * c >= seen) p[c] &= 0xFFFF0000u;
-                            if (q * 32 + 2 * c + 1 >= seen) p[c] &= 0x0000FFFFu;
-                        }
-                    }
-                    tmem_st16(s_at + q * 16, p);
                 }
+                tmem_st16(s_at, p);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.ds_ready);
-                ++blocks;
             }
             if (!ok) break;
             ok = all(&bars.acc_full, uses & 1);
             if (!ok) break;
             tc_fence_after();
-            // each warpgroup takes half of the columns (DP = 64: 32 of them)
-#pragma unroll
-            for (int cc = 0; cc < DP / 64; ++cc) {
-                const int c = wg * (DP / 64) + cc;
-                uint32_t y[32];
-                tmem_ld32(tmem + lanes + kBqDq + c * 32, y);
-                tmem_wait_ld(y);
-                if (cc == DP / 64 - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.acc_free);
-                }
-                if (valid) ab_store32<E>(out, c * 32, s.d, y, s.scale);
-            }
+            uint8_t* out = a.dq[t.r] + ((int64_t(t.bb) * s.Sq + tok) * s.n[t.r] +
+                                        t.kvh * s.group + head_in) * s.d * 2;
+            constexpr int kCols = DP / 4;
+            uint32_t y[kCols];
+            if constexpr (kCols == 32)
+                tmem_ld32(tmem + lanes + kBqDq + wg * kCols, y);
+            else
+                tmem_ld16(tmem + lanes + kBqDq + wg * kCols, y);
+            tmem_wait_ld(y);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.acc_free);
+            if (valid) ab_store<E>(out, wg * kCols, s.d, y, s.scale);
             ++uses;
         }
     }
@@ -925,7 +953,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
 }
 
 template <int DP, bool F16>
-static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int device, int grid)
+static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int device, int grid,
+                             int sm_count)
 {
     static std::atomic<unsigned long long> raised{0};
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
@@ -945,16 +974,19 @@ static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int devi
     attn_bwd_stats_kernel<F16><<<cap(heads * a.q_tiles * (kAttnRows / 16), int64_t(grid) * 16), 256, 0,
                                  stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn_bwd_kv_kernel<DP, F16><<<cap(heads * a.kv_order.blocks, grid), kAbThreads, smem_kv, stream>>>(a);
+    attn_bwd_kv_kernel<DP, F16><<<attn_ctas(heads * a.kv_order.blocks, grid, sm_count), kAbThreads,
+                                  smem_kv, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn_bwd_q_kernel<DP, F16><<<cap(heads * a.q_tiles, grid), kAbThreads, smem_q, stream>>>(a);
+    attn_bwd_q_kernel<DP, F16><<<attn_ctas(heads * a.q_tiles, grid, sm_count), kAbThreads, smem_q,
+                                 stream>>>(a);
     return cudaGetLastError();
 }
 
 // The three launches over all ranks, `grid` CTAs of the product kernels at most. The shape, every
 // pointer and the workspace are set in `a`.
 cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* const* k,
-                            const void* const* v, cudaStream_t stream, int device, int grid)
+                            const void* const* v, cudaStream_t stream, int device, int grid,
+                             int sm_count)
 {
     const AttnShape& s = a.s;
     if (s.head_begin[s.W] == 0) return cudaSuccess;
@@ -971,10 +1003,10 @@ cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* co
             return cudaErrorInvalidValue;
     }
     if (s.d <= 64)
-        return s.f16 ? ab_launch<64, true>(a, stream, device, grid)
-                     : ab_launch<64, false>(a, stream, device, grid);
-    return s.f16 ? ab_launch<128, true>(a, stream, device, grid)
-                 : ab_launch<128, false>(a, stream, device, grid);
+        return s.f16 ? ab_launch<64, true>(a, stream, device, grid, sm_count)
+                     : ab_launch<64, false>(a, stream, device, grid, sm_count);
+    return s.f16 ? ab_launch<128, true>(a, stream, device, grid, sm_count)
+                 : ab_launch<128, false>(a, stream, device, grid, sm_count);
 }
 
 cudaError_t attn_bwd_status(unsigned* status, bool clear)

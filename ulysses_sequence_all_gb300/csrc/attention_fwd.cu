@@ -53,6 +53,7 @@ constexpr int kAfThreads = 384;
 constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfCleanWarp = 10, kAfUnitWarp = 11;
 constexpr int kAfUnitSlots = 4;
 constexpr int kAfBarBytes = 1024;
+constexpr int kAfPairedWaves = 4;
 constexpr int kAfShortBlocks = 8;  // key blocks of a unit up to which it counts as short
 // Registers a thread: 384 x 168 at launch = 256 x 208 + 128 x 88.
 constexpr int kAfRegsSoftmax = 208, kAfRegsOther = 88;
@@ -99,7 +100,8 @@ struct AfBars {
     uint64_t o_full[2], o_free[2];   // output complete; read out
     uint64_t kv_full[8], kv_empty[8];
     uint64_t clean[8];               // rows past the last key zeroed
-    uint64_t drain;
+    uint64_t drain, steal;
+    uint4 answer;
     uint32_t tmem;
     int dead;
     AfUnit unit[kAfUnitSlots];       // r < 0: no more
@@ -288,6 +290,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             mbar_init(&bars.clean[k], 1);
         }
         mbar_init(&bars.drain, 1);
+        mbar_init(&bars.steal, 1);
         bars.dead = 0;
         fence_barrier_init();
     }
@@ -521,9 +524,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 ring.next(kAfUnitSlots);
             };
             AfUnit t;
-            for (int64_t wave = 0; ok && wave * int64_t(gridDim.x) < a.units; ++wave) {
-                const int64_t u = attn_unit_at(wave);
-                if (u >= a.units) continue;
+            AttnUnitSource source{a.units, &bars.answer, &bars.steal, dead};
+            for (int64_t u; ok && (u = source.next()) >= 0;) {
                 t = af_unit(a, u);
                 if (t.most() > 0) {
                     publish(t);
@@ -760,8 +762,8 @@ int64_t attn_order_group(const AttnShape& s, int64_t heads, int64_t bytes)
 }
 
 // Row tiles, units and parts of the keys. Where one tile holds all rows, a CTA's two tiles take a
-// part each. The keys are split further while the units still fit one wave of the SMs and a part
-// keeps four blocks (a part costs its start, an fp32 output and a share of the join).
+// part each. The keys are split further while a part keeps some blocks (a part costs its start, an
+// fp32 output and a share of the join).
 void attn_fwd_split(AttnFwdArgs* a, int sm_count)
 {
     const AttnShape& s = a->s;
@@ -773,8 +775,10 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     a->order.blocks = a->paired ? 1 : (s.Sq + pair - 1) / pair;
     a->order.group = attn_order_group(s, a->order.heads, s.Skv * s.d * 4);  // keys and values
     const int64_t base = a->order.heads * a->order.blocks;
-    int64_t n = base > 0 ? sm_count / base : 1;
-    const int64_t most = blocks / (a->paired ? 8 : 4);
+    // paired (bound by reading the keys, of lengths that may differ): several units an SM, to even
+    // out; else one wave of the SMs
+    int64_t n = base > 0 ? (a->paired ? kAfPairedWaves : 1) * int64_t(sm_count) / base : 1;
+    const int64_t most = blocks / (a->paired ? 16 : 4);
     if (n > most) n = most;
     if (n > 64) n = 64;
     if (n < 1) n = 1;
@@ -818,7 +822,8 @@ static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int devi
 // One launch over all ranks (and the join); `grid` CTAs at most. The shape, outputs, parts and
 // their buffers are set in `a`.
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
-                            const void* const* v, cudaStream_t stream, int device, int grid)
+                            const void* const* v, cudaStream_t stream, int device, int grid,
+                            int sm_count)
 {
     const AttnShape& s = a.s;
     if (a.units == 0) return cudaSuccess;
@@ -829,7 +834,7 @@ cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* co
             !encode_head_map(&a.vmap[r], v[r], s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows))
             return cudaErrorInvalidValue;
     }
-    if (int64_t(grid) > a.units) grid = int(a.units);
+    grid = int(attn_ctas(a.units, grid, sm_count));
     if (s.d <= 64)
         return s.f16 ? af_launch<64, true>(a, stream, device, grid)
                      : af_launch<64, false>(a, stream, device, grid);
