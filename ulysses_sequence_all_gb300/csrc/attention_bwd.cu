@@ -60,46 +60,59 @@ __device__ __forceinline__ void ab_head(const AttnShape& s, int64_t h, int* r, i
     *kvh = local - *bb * s.m[k];
 }
 
-// One row a half warp: lane c of it holds columns 8c .. 8c + 7.
-template <bool F16>
+// Half a tile of rows a CTA; LANES lanes a row, 8 columns each. Bound by reading O and dO.
+template <bool F16, int LANES>
 __global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_constant__ AttnBwdArgs a)
 {
     using E = ElemT<F16>;
     const AttnShape& s = a.s;
-    const int sub = threadIdx.x & 15, slot = threadIdx.x >> 4;
-    const int64_t tiles = s.head_begin[s.W] * a.q_tiles;
-    for (int64_t at = blockIdx.x; at < tiles * (kAttnRows / 16); at += gridDim.x) {
-        const int64_t tile = at / (kAttnRows / 16);
-        const int row = int(at - tile * (kAttnRows / 16)) * 16 + slot;
+    constexpr int kAtOnce = 256 / LANES, kTurns = kAttnRows / 2 / kAtOnce;
+    const int sub = threadIdx.x % LANES, slot = threadIdx.x / LANES;
+    const int64_t halves = 2 * s.head_begin[s.W] * a.q_tiles;
+    for (int64_t at = blockIdx.x; at < halves; at += gridDim.x) {
+        const int64_t tile = at >> 1;
+        const int row0 = int(at & 1) * (kAttnRows / 2) + slot;
         const int64_t h = div_fast(tile, a.q_tiles);
         int r, bb, kvh;
         ab_head(s, h, &r, &bb, &kvh);
-        const int tok_in = row / s.group, head = kvh * s.group + row - tok_in * s.group;
-        const int64_t tok = (tile - h * a.q_tiles) * a.tile_tokens + tok_in;
-        const bool valid = tok_in < a.tile_tokens && tok < s.Sq;
-        float sum = 0.0f;
-        if (valid && sub * 8 < s.d) {
-            const int64_t off =
-                ((int64_t(bb) * s.Sq + tok) * s.n[r] + head) * s.d * 2 + sub * 16;
-            const uint4 x = ld_stream_v4(a.o[r] + off), y = ld_stream_v4(a.go[r] + off);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        const int64_t tok0 = (tile - h * a.q_tiles) * a.tile_tokens;
+        uint4 x[kTurns], y[kTurns];
+        float lse[kTurns];
+        bool valid[kTurns];
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {  // every load before the first use
+            const int row = k * kAtOnce + row0;
+            const int tok_in = row / s.group, head = kvh * s.group + row - tok_in * s.group;
+            const int64_t tok = tok0 + tok_in;
+            valid[k] = tok_in < a.tile_tokens && tok < s.Sq;
+            x[k] = y[k] = make_uint4(0, 0, 0, 0);
+            lse[k] = -INFINITY;
+            if (valid[k] && sub * 8 < s.d) {
+                const int64_t off =
+                    ((int64_t(bb) * s.Sq + tok) * s.n[r] + head) * s.d * 2 + sub * 16;
+                x[k] = ld_stream_v4(a.o[r] + off);
+                y[k] = ld_stream_v4(a.go[r] + off);
+            }
+            if (valid[k] && sub == 0) lse[k] = a.lse[r][(int64_t(bb) * s.n[r] + head) * s.Sq + tok];
+        }
+#pragma unroll
+        for (int k = 0; k < kTurns; ++k) {
+            const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            const uint32_t ys[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+            float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 sum = fmaf(E::lo(xs[i]), E::lo(ys[i]), sum);
                 sum = fmaf(E::hi(xs[i]), E::hi(ys[i]), sum);
             }
-        }
 #pragma unroll
-        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (sub == 0) {
-            float z = INFINITY;
-            if (valid) {
-                const float lse = a.lse[r][(int64_t(bb) * s.n[r] + head) * s.Sq + tok];
-                if (lse != -INFINITY) z = lse * 1.4426950408889634f;
+            for (int off = LANES / 2; off > 0; off >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (sub == 0) {
+                float* out = a.stats + tile * 2 * kAttnRows + k * kAtOnce + row0;
+                out[0] = lse[k] == -INFINITY ? INFINITY : lse[k] * 1.4426950408889634f;
+                out[kAttnRows] = sum;
             }
-            float* out = a.stats + tile * 2 * kAttnRows + row;
-            out[0] = z;
-            out[kAttnRows] = valid ? sum : 0.0f;
         }
     }
 }
@@ -587,16 +600,17 @@ __global__ void __launch_bounds__(kAbThreads, 1)
 
 // ---- dQ -----------------------------------------------------------------------------------------
 
-// Tensor memory columns: two buffers of S (then dS), dP, dQ; lanes are rows of q, columns keys.
-constexpr int kBqS = 0, kBqDp = 256, kBqDq = 384;
+// Tensor memory columns: Q (16 bits, two a column), dS (the same), S, dP, dQ. Lanes are rows of q,
+// columns keys.
+constexpr int kBqQ = 0, kBqDs = 64, kBqS = 128, kBqDp = 256, kBqDq = 384;
 
 template <int DP>
 struct BqSmem {
     static constexpr int kTile = kAttnRows * DP * 2;
     static constexpr int kHalf = kAttnRows * 128;
-    static constexpr int kStages = DP == 128 ? 5 : 8;
-    static constexpr int kQ = 1024, kG = kQ + kTile;
-    static constexpr int kRing = kG + kTile;  // K0 V0 K1 V1 ...
+    static constexpr int kStages = DP == 128 ? 6 : 8;
+    static constexpr int kG = 1024;          // dO, the unit's
+    static constexpr int kRing = kG + kTile;  // Q K0 V0 K1 V1 ... of each unit
     static constexpr int kTotal = kRing + kStages * kTile;
     static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");
 };
@@ -607,9 +621,11 @@ struct BqUnit {
 };
 
 struct BqBars {
-    uint64_t q_full, g_full, q_empty, g_empty;  // row tile landed; its last scores have read it
-    uint64_t kv_full[8], kv_empty[8], clean[8];  // clean: K rows past the last key zeroed
-    uint64_t s_full[2], dp_full, ds_ready;
+    uint64_t full[8], empty[8], clean[8];  // ring stages; clean: K rows past the last key zeroed
+    uint64_t g_full, g_empty;              // dO landed; its last scores have read it
+    uint64_t q_ready;                      // Q in tensor memory
+    uint64_t s_full, s_read, dp_full, dp_read;  // scores complete; read
+    uint64_t ds_ready, dq_done;            // dS written; summed up
     uint64_t acc_full, acc_free, drain;
     uint32_t tmem;
     int dead;
@@ -639,6 +655,9 @@ __device__ __forceinline__ int bq_past(const AttnShape& s, const BqUnit& t, int 
     return past >= kAttnRows || t.len >= s.Skv ? kAttnRows : int(past);
 }
 
+// Q goes to tensor memory (the S products then read half as much shared memory), S and dP are free
+// again as soon as the threads have read them, and dS has columns of its own, so that the products
+// run S, dP of the next block and dQ of this one without waiting for the threads' arithmetic.
 template <int DP, bool F16>
 __global__ void __launch_bounds__(kAbThreads, 1)
     attn_bwd_q_kernel(const __grid_constant__ AttnBwdArgs a)
@@ -657,19 +676,20 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     constexpr int K = L::kStages;
 
     if (threadIdx.x == 0) {
-        mbar_init(&bars.q_full, 1);
-        mbar_init(&bars.g_full, 1);
-        mbar_init(&bars.q_empty, 1);
-        mbar_init(&bars.g_empty, 1);
         for (int k = 0; k < K; ++k) {
-            mbar_init(&bars.kv_full[k], 1);
-            mbar_init(&bars.kv_empty[k], s.kv_lens ? 2 : 1);  // the products, and warp 10
+            mbar_init(&bars.full[k], 1);
+            mbar_init(&bars.empty[k], s.kv_lens ? 2 : 1);  // the products, and warp 18
             mbar_init(&bars.clean[k], 1);
         }
-        mbar_init(&bars.s_full[0], 1);
-        mbar_init(&bars.s_full[1], 1);
+        mbar_init(&bars.g_full, 1);
+        mbar_init(&bars.g_empty, 1);
+        mbar_init(&bars.q_ready, 16);
+        mbar_init(&bars.s_full, 1);
+        mbar_init(&bars.s_read, 16);
         mbar_init(&bars.dp_full, 1);
+        mbar_init(&bars.dp_read, 16);
         mbar_init(&bars.ds_ready, 16);
+        mbar_init(&bars.dq_done, 1);
         mbar_init(&bars.acc_full, 1);
         mbar_init(&bars.acc_free, 16);
         ab_board_init(bars.board, s.kv_lens ? 19 : 18);  // warps 0-17, and 18
@@ -691,41 +711,36 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
+            auto stage = [&](const CUtensorMap* map, uint32_t bytes, int head, int row, int bb) {
+                if (issued >= K) ok = wait_or_dead(&bars.empty[ring.s], ring.phase ^ 1u, dead);
+                if (!ok) return;
+                mbar_arrive_expect_tx(&bars.full[ring.s], bytes);
+                for (int h = 0; h < halves; ++h)
+                    tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf, map, 64 * h,
+                                  head, row, bb, &bars.full[ring.s]);
+                ++issued;
+                ring.next(K);
+            };
             AbUnits<BqUnit> source{&bars.board, dead};
             BqUnit t;
             while (ok && source.next<false>(&t)) {
-                if (uses > 0)
-                    ok = wait_or_dead(&bars.q_empty, (uses - 1) & 1, dead) &&
-                         wait_or_dead(&bars.g_empty, (uses - 1) & 1, dead);
+                stage(&a.qmap[t.r], q_bytes, t.kvh * s.group, int(t.tok0), t.bb);
+                if (ok) stage(&a.kmap[t.r], kv_bytes, t.kvh, 0, t.bb);
+                if (ok && uses > 0) ok = wait_or_dead(&bars.g_empty, (uses - 1) & 1, dead);
                 if (!ok) break;
-                for (int w = 0; w < 2; ++w) {
-                    uint64_t* bar = w ? &bars.g_full : &bars.q_full;
-                    mbar_arrive_expect_tx(bar, q_bytes);
-                    for (int h = 0; h < halves; ++h)
-                        tensor_g2s_4d(smem + (w ? L::kG : L::kQ) + h * L::kHalf,
-                                      w ? &a.gmap[t.r] : &a.qmap[t.r], 64 * h, t.kvh * s.group,
-                                      int(t.tok0), t.bb, bar);
-                }
+                mbar_arrive_expect_tx(&bars.g_full, q_bytes);
+                for (int h = 0; h < halves; ++h)
+                    tensor_g2s_4d(smem + L::kG + h * L::kHalf, &a.gmap[t.r], 64 * h,
+                                  t.kvh * s.group, int(t.tok0), t.bb, &bars.g_full);
                 ++uses;
-                for (int j = 0; j < 2 * t.n; ++j) {
-                    if (issued >= K) ok = wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, dead);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&bars.kv_full[ring.s], kv_bytes);
-                    for (int h = 0; h < halves; ++h)
-                        tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf,
-                                      (j & 1) ? &a.vmap[t.r] : &a.kmap[t.r], 64 * h, t.kvh,
-                                      (j >> 1) * kAttnRows, t.bb, &bars.kv_full[ring.s]);
-                    ++issued;
-                    ring.next(K);
-                }
+                for (int j = 1; ok && j < 2 * t.n; ++j)
+                    stage((j & 1) ? &a.vmap[t.r] : &a.kmap[t.r], kv_bytes, t.kvh,
+                          (j >> 1) * kAttnRows, t.bb);
             }
             bool drained = true;  // leave no copy into this CTA's shared memory in flight
             for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k)
-                drained &= mbar_wait_bounded(&bars.kv_full[k % K], uint32_t((k / K) & 1));
-            if (uses > 0) {
-                drained &= mbar_wait_bounded(&bars.q_full, (uses - 1) & 1);
-                drained &= mbar_wait_bounded(&bars.g_full, (uses - 1) & 1);
-            }
+                drained &= mbar_wait_bounded(&bars.full[k % K], uint32_t((k / K) & 1));
+            if (uses > 0) drained &= mbar_wait_bounded(&bars.g_full, (uses - 1) & 1);
             if (!drained) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
         }
         __syncwarp();
@@ -737,11 +752,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             BqUnit t;
             bool ok = true;
             while (ok && source.next<true>(&t)) {
-                for (int j = 0; ok && j < 2 * t.n; ++j) {  // K0 V0 K1 V1 ...
-                    ok = __all_sync(0xffffffffu,
-                                    wait_or_dead(&bars.kv_full[ring.s], ring.phase, dead));
+                for (int j = -1; ok && j < 2 * t.n; ++j) {  // Q K0 V0 K1 V1 ...
+                    ok = __all_sync(0xffffffffu, wait_or_dead(&bars.full[ring.s], ring.phase, dead));
                     if (!ok) break;
-                    const int past = (j & 1) ? kAttnRows : bq_past(s, t, j >> 1);
+                    const int past = j < 0 || (j & 1) ? kAttnRows : bq_past(s, t, j >> 1);
                     if (past < kAttnRows) {
                         for (int h = 0; h < halves; ++h)
                             for (int w = past * 8 + lane; w < kAttnRows * 8; w += 32)
@@ -754,7 +768,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     }
                     // every stage waits for this warp, so that it neither runs ahead of the ring
                     // nor falls a turn behind
-                    if (lane == 0) mbar_arrive(&bars.kv_empty[ring.s]);
+                    if (lane == 0) mbar_arrive(&bars.empty[ring.s]);
                     ring.next(K);
                 }
             }
@@ -764,7 +778,6 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         if (elect_one()) {
             const uint32_t id_s = tc_idesc(F16, kAttnRows, false);
             const uint32_t id_d = tc_idesc(F16, 16 * nk, true);
-            const uint64_t q_desc = tc_desc_k(smem_u32(smem + L::kQ));
             const uint64_t g_desc = tc_desc_k(smem_u32(smem + L::kG));
             const uint64_t kv_desc = tc_desc_k(smem_u32(smem + L::kRing));
             const uint64_t kt_desc = tc_desc_mn(smem_u32(smem + L::kRing), L::kHalf);
@@ -775,34 +788,41 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 return ok = ok && wait_or_dead(bar, parity, dead);
             };
-            auto scores = [&](uint32_t d, uint64_t row, uint64_t key, uint64_t* bar) {
+            // S of the ring's next block, whose stage it returns; dP of the V in the stage after it.
+            // `first` of unit number `use`: its queries come before its keys.
+            auto make_s = [&](bool first, uint32_t use) {
+                if (first) {
+                    if (!wait(&bars.q_ready, use & 1)) return 0;
+                    mbar_arrive(&bars.empty[ring.s]);
+                    ring.next(K);
+                }
+                const int stage = ring.s;
+                if (!wait(&bars.full[stage], ring.phase)) return stage;
+                tc_fence_after();
+                const uint64_t key = kv_desc + stage * (L::kTile >> 4);
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    if (ks >= nk) break;
+                    tc_mma_ts(tmem + kBqS, tmem + kBqQ + ks * 8,
+                              key + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), id_s, ks > 0);
+                }
+                tc_commit(&bars.s_full);
+                ring.next(K);
+                return stage;
+            };
+            auto make_dp = [&](bool first, bool last, uint32_t use) {
+                if (first) wait(&bars.g_full, use & 1);
+                if (!wait(&bars.full[ring.s], ring.phase)) return;
+                tc_fence_after();
+                const uint64_t key = kv_desc + ring.s * (L::kTile >> 4);
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
                     if (ks >= nk) break;
                     const uint32_t off = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
-                    tc_mma_ss(tmem + d, row + off, key + off, id_s, ks > 0);
+                    tc_mma_ss(tmem + kBqDp, g_desc + off, key + off, id_s, ks > 0);
                 }
-                tc_commit(bar);
-            };
-            // S of a block (number `count` of the CTA's) from the ring's next stage, which it
-            // returns; dP from the stage after it. `first`, `last` of the unit.
-            auto next_s = [&](bool first, bool last, uint32_t use, uint32_t count) {
-                const int stage = ring.s;
-                if (first) wait(&bars.q_full, use & 1);
-                if (!wait(&bars.kv_full[stage], ring.phase)) return stage;
-                tc_fence_after();
-                scores(kBqS + (count & 1) * 128, q_desc, kv_desc + stage * (L::kTile >> 4),
-                       &bars.s_full[count & 1]);
-                if (last) tc_commit(&bars.q_empty);
-                ring.next(K);
-                return stage;
-            };
-            auto next_dp = [&](bool first, bool last, uint32_t use) {
-                if (first) wait(&bars.g_full, use & 1);
-                if (!wait(&bars.kv_full[ring.s], ring.phase)) return;
-                tc_fence_after();
-                scores(kBqDp, g_desc, kv_desc + ring.s * (L::kTile >> 4), &bars.dp_full);
-                tc_commit(&bars.kv_empty[ring.s]);
+                tc_commit(&bars.dp_full);
+                tc_commit(&bars.empty[ring.s]);
                 if (last) tc_commit(&bars.g_empty);
                 ring.next(K);
             };
@@ -811,16 +831,18 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             bool live = source.next<false>(&t);
             int ks = 0;  // the stage of the current block's K
             if (live) {
-                ks = next_s(true, t.n == 1, 0, 0);
-                next_dp(true, t.n == 1, 0);
+                ks = make_s(true, 0);
+                make_dp(true, t.n == 1, 0);
             }
             while (live && ok) {
                 const bool more = source.next<false>(&next);
                 for (int j = 0; ok && j < t.n; ++j, ++blocks) {
                     const bool end = j + 1 == t.n;  // the next block is the next unit's
-                    const bool last = end ? next.n == 1 : j + 2 == t.n;
                     int after = ks;
-                    if (!end) after = next_s(false, last, uses, blocks + 1);
+                    wait(&bars.s_read, blocks & 1);
+                    if (!end) after = make_s(false, uses);
+                    wait(&bars.dp_read, blocks & 1);
+                    if (!end) make_dp(false, j + 2 == t.n, uses);
                     if (s.kv_lens && bq_past(s, t, j) < kAttnRows) {
                         wait(&bars.clean[ks], (cleaned >> ks) & 1);
                         cleaned ^= 1u << ks;
@@ -832,16 +854,18 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     const uint64_t kd = kt_desc + ks * (L::kTile >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kAttnRows / 16; ++kk)
-                        tc_mma_ts(tmem + kBqDq,
-                                  tmem + kBqS + (blocks & 1) * 128 + (kk >> 1) * 32 + (kk & 1) * 8,
-                                  kd + kk * (2048 >> 4), id_d, j > 0 || kk > 0);
-                    tc_commit(&bars.kv_empty[ks]);
+                        tc_mma_ts(tmem + kBqDq, tmem + kBqDs + kk * 8, kd + kk * (2048 >> 4), id_d,
+                                  j > 0 || kk > 0);
+                    tc_commit(&bars.empty[ks]);
+                    tc_commit(&bars.dq_done);
                     if (end) {
                         tc_commit(&bars.acc_full);
-                        if (more) after = next_s(true, last, uses + 1, blocks + 1);
+                        if (more) {
+                            after = make_s(true, uses + 1);
+                            make_dp(true, next.n == 1, uses + 1);
+                        }
                     }
                     ks = after;
-                    if (!end || more) next_dp(end, last, uses + 1);
                 }
                 ++uses;
                 t = next;
@@ -868,31 +892,60 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         const int wg = warp >> 2;  // keys 32 wg .. 32 wg + 31 of a block; then a quarter of dQ
         const int row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;
+        const uint32_t s_at = tmem + lanes + kBqS + wg * 32;
         const uint32_t dp_at = tmem + lanes + kBqDp + wg * 32;
+        const uint32_t ds_at = tmem + lanes + kBqDs + wg * 16;
         const float sl2 = s.scale * 1.4426950408889634f;
         const int tok_in = row / s.group, head_in = row - tok_in * s.group;
         uint32_t uses = 0, blocks = 0;
+        int64_t stages = 0;  // of the ring before the current unit
         bool ok = true;
         auto all = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
         };
+        auto arrive = [&](uint64_t* bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        // This row of a unit's Q (warpgroups 0, 1: its halves) from its stage to tensor memory, which
+        // the scores made so far are done with.
+        auto copy = [&](int64_t at) {
+            const int stage = int(at % K);
+            ok = all(&bars.full[stage], uint32_t(at / K) & 1);
+            if (!ok) return;
+            if (wg < halves) {
+                const uint8_t* from = smem + L::kRing + stage * L::kTile + wg * L::kHalf + row * 128;
+                uint32_t v[32];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 w = ld_shared_v4(from + ((c ^ (row & 7)) << 4));
+                    v[4 * c] = w.x, v[4 * c + 1] = w.y, v[4 * c + 2] = w.z, v[4 * c + 3] = w.w;
+                }
+                tmem_st32(tmem + lanes + kBqQ + wg * 32, v);
+                tmem_wait_st();
+            }
+            arrive(&bars.q_ready);
+        };
         AbUnits<BqUnit> source{&bars.board, dead};
-        BqUnit t;
-        while (ok && source.next<true>(&t)) {
+        BqUnit t, next;
+        bool live = source.next<true>(&t);
+        if (live) copy(0);
+        while (live && ok) {
             const int64_t tok = t.tok0 + tok_in;
             const bool valid = tok_in < a.tile_tokens && tok < s.Sq;
             const float* stat = a.stats + (t.h * a.q_tiles + t.tile) * 2 * kAttnRows + row;
             const float z = -stat[0], delta = stat[kAttnRows];
             int64_t left = min(t.len, t.pos0 + tok + 1) - 32 * wg;  // visible keys from here on
             for (int j = 0; j < t.n; ++j, ++blocks, left -= kAttnRows) {
-                const uint32_t s_at = tmem + lanes + kBqS + (blocks & 1) * 128 + wg * 32;
                 const int seen = int(max(int64_t(0), min(left, int64_t(32))));
-                ok = all(&bars.s_full[blocks & 1], (blocks >> 1) & 1);
+                ok = all(&bars.s_full, blocks & 1);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t x[32];
                 tmem_ld32(s_at, x);
                 tmem_wait_ld(x);
+                arrive(&bars.s_read);
                 const float2 k2 = make_float2(sl2, sl2), z2 = make_float2(z, z);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
@@ -908,6 +961,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 uint32_t y[32], p[16];
                 tmem_ld32(dp_at, y);
                 tmem_wait_ld(y);
+                arrive(&bars.dp_read);
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const float2 v = ab_ds(x[2 * c], x[2 * c + 1], y[2 * c], y[2 * c + 1],
@@ -921,11 +975,18 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                         if (2 * c + 1 >= seen) p[c] &= 0x0000FFFFu;
                     }
                 }
-                tmem_st16(s_at, p);
+                if (blocks > 0) ok = all(&bars.dq_done, (blocks - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                tmem_st16(ds_at, p);
                 tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.ds_ready);
+                arrive(&bars.ds_ready);
+                if (j + 1 == t.n) {  // the next unit's queries (its S then runs beside the last dQ)
+                    stages += 1 + 2 * t.n;
+                    live = source.next<true>(&next);
+                    if (live) copy(stages);
+                    if (!ok) break;
+                }
             }
             if (!ok) break;
             ok = all(&bars.acc_full, uses & 1);
@@ -940,11 +1001,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             else
                 tmem_ld16(tmem + lanes + kBqDq + wg * kCols, y);
             tmem_wait_ld(y);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.acc_free);
+            arrive(&bars.acc_free);
             if (valid) ab_store<E>(out, wg * kCols, s.d, y, s.scale);
             ++uses;
+            t = next;
         }
     }
     __syncthreads();
@@ -970,9 +1030,9 @@ static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int devi
         raised.fetch_or(bit);
     }
     const int64_t heads = a.q_order.heads;
-    auto cap = [](int64_t n, int64_t most) { return unsigned(n < most ? n : most); };
-    attn_bwd_stats_kernel<F16><<<cap(heads * a.q_tiles * (kAttnRows / 16), int64_t(grid) * 16), 256, 0,
-                                 stream>>>(a);
+    const int64_t parts = 2 * heads * a.q_tiles;
+    attn_bwd_stats_kernel<F16, DP / 8><<<unsigned(parts < 0x7FFFFFFF ? parts : 0x7FFFFFFF), 256, 0,
+                                         stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     attn_bwd_kv_kernel<DP, F16><<<attn_ctas(heads * a.kv_order.blocks, grid, sm_count), kAbThreads,
                                   smem_kv, stream>>>(a);
