@@ -960,9 +960,9 @@ size_t attn_bwd_setup(AttnBwdArgs* a)
     a->tile_tokens = kAttnRows / s.group;
     a->q_tiles = (s.Sq + a->tile_tokens - 1) / a->tile_tokens;
     const int64_t heads = s.head_begin[s.W];
-    a->q_order = {heads, a->q_tiles, attn_order_group(s, heads, s.Skv * s.d * 4)};
+    a->q_order = {heads, a->q_tiles, attn_order_group(heads, s.Skv * s.d * 4)};
     a->kv_order = {heads, (s.Skv + kAttnRows - 1) / kAttnRows,
-                   attn_order_group(s, heads, s.Sq * s.group * s.d * 4)};
+                   attn_order_group(heads, s.Sq * s.group * s.d * 4)};
     return size_t(s.head_begin[s.W]) * size_t(a->q_tiles) * 2 * kAttnRows * sizeof(float);
 }
 

@@ -133,9 +133,10 @@ inline unsigned attn_ctas(int64_t units, int64_t cap, int sm_count)
     if (cap < sm_count || units > 0x7FFFFFFF) return unsigned(units < cap ? units : cap);
     return unsigned(units);
 }
-// Heads in a group: where blocks differ in length (causal), as many as hold `bytes` each within
-// about half of the L2 cache; else one (neighbouring CTAs then share a head's operands).
-int64_t attn_order_group(const AttnShape& s, int64_t heads, int64_t bytes);
+// Heads in a group: as many as hold `bytes` each within about half of the L2 cache. The heads of a
+// token lie next to one another, so the CTAs at work then read whole stretches of memory; with
+// longer operands a head at a time keeps those in the cache.
+int64_t attn_order_group(int64_t heads, int64_t bytes);
 void attn_fwd_split(AttnFwdArgs* a, int sm_count);  // tiles, units and parts from the shape
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
                             const void* const* v, cudaStream_t stream, int device, int grid,

@@ -53,7 +53,7 @@ constexpr int kAfThreads = 384;
 constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfCleanWarp = 10, kAfUnitWarp = 11;
 constexpr int kAfUnitSlots = 4;
 constexpr int kAfBarBytes = 1024;
-constexpr int kAfPairedWaves = 4;
+constexpr int kAfPairedWaves = 1;
 constexpr int kAfShortBlocks = 8;  // key blocks of a unit up to which it counts as short
 // Registers a thread: 384 x 168 at launch = 256 x 208 + 128 x 88.
 constexpr int kAfRegsSoftmax = 208, kAfRegsOther = 88;
@@ -684,6 +684,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
             }
             if (whole) {  // this warp's 32 rows, 8 lanes a row's 64 columns
+                // (before the stores: a fence behind them waits for them, some microseconds)
+                fence_proxy_async_shared();
                 __syncwarp();
                 const int64_t at = to.valid ? to.o : -1;
                 const int word = lane & 7;
@@ -699,7 +701,6 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                                            ((word ^ (rr & 7)) << 4)));
                     }
                 }
-                fence_proxy_async_shared();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.q_empty[slot]);
@@ -752,9 +753,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     }
 }
 
-int64_t attn_order_group(const AttnShape& s, int64_t heads, int64_t bytes)
+int64_t attn_order_group(int64_t heads, int64_t bytes)
 {
-    if (!s.causal) return 1;
     int64_t g = (int64_t(64) << 20) / (bytes > 0 ? bytes : 1);
     if (g > 256) g = 256;
     if (g > heads) g = heads;
@@ -773,13 +773,20 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     a->paired = s.Sq <= a->tile_tokens && blocks > 1;
     a->order.heads = s.head_begin[s.W];
     a->order.blocks = a->paired ? 1 : (s.Sq + pair - 1) / pair;
-    a->order.group = attn_order_group(s, a->order.heads, s.Skv * s.d * 4);  // keys and values
+    a->order.group = attn_order_group(a->order.heads, s.Skv * s.d * 4);  // keys and values
     const int64_t base = a->order.heads * a->order.blocks;
-    // paired (bound by reading the keys, of lengths that may differ): several units an SM, to even
-    // out; else one wave of the SMs
-    int64_t n = base > 0 ? (a->paired ? kAfPairedWaves : 1) * int64_t(sm_count) / base : 1;
-    const int64_t most = blocks / (a->paired ? 16 : 4);
-    if (n > most) n = most;
+    // Paired, bound by reading keys of lengths that may differ: several units an SM, to even out, of
+    // eight blocks a part at least; but any part where that leaves SMs idle (latency). Else one
+    // wave of the SMs.
+    int64_t n = 1;
+    if (base > 0 && a->paired) {
+        const int64_t many = kAfPairedWaves * int64_t(sm_count) / base, one = sm_count / base;
+        n = many < blocks / 16 ? many : blocks / 16;
+        const int64_t few = one < blocks / 2 ? one : blocks / 2;
+        if (n < few) n = few;
+    } else if (base > 0) {
+        n = sm_count / base < blocks / 4 ? sm_count / base : blocks / 4;
+    }
     if (n > 64) n = 64;
     if (n < 1) n = 1;
     a->splits = int32_t(n);
