@@ -55,8 +55,6 @@ constexpr int kAfUnitSlots = 4;
 constexpr int kAfBarBytes = 1024;
 constexpr int kAfPairedWaves = 1;
 constexpr int kAfShortBlocks = 8;  // key blocks of a unit up to which it counts as short
-// Registers a thread: 384 x 168 at launch = 256 x 208 + 128 x 88.
-constexpr int kAfRegsSoftmax = 208, kAfRegsOther = 88;
 constexpr float kAfRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 
 // Tensor memory columns: the two tiles' scores (their probabilities over them), their outputs.
@@ -73,6 +71,10 @@ struct AfSmem {
     static constexpr int kHalf = kAttnRows * 128;     // its part of 64 columns
     static constexpr int kSlots = DP == 64 ? 4 : MODE == kAfLong ? 3 : MODE == kAfShort ? 4 : 2;
     static constexpr int kStages = DP == 64 ? 8 : 7 - kSlots;
+    // Registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72 = 256 x 208 + 128 x 88 (what
+    // the roles take without spills)
+    static constexpr int kRegsSoftmax = MODE == kAfPaired ? 208 : 216;
+    static constexpr int kRegsOther = MODE == kAfPaired ? 88 : 72;
     static constexpr int kQ = kAfBarBytes;  // barriers first
     static constexpr int kRing = kQ + kSlots * kTile;
     static constexpr int kTotal = kRing + kStages * kTile;
@@ -169,10 +171,22 @@ struct AfUnits {
         if (!ok) return false;
         *t = bars->unit[ring.s];
         if (t->r < 0) return false;
+        release<WARP>();
+        return true;
+    }
+    // The same without giving its record back yet (release does): it can be read again.
+    __device__ __forceinline__ bool peek()
+    {
+        const bool ok = wait_or_dead(&bars->u_full[ring.s], ring.phase, &bars->dead);
+        return __all_sync(0xffffffffu, ok) && bars->unit[ring.s].r >= 0;
+    }
+    __device__ __forceinline__ const AfUnit& record() const { return bars->unit[ring.s]; }
+    template <bool WARP>
+    __device__ __forceinline__ void release()
+    {
         if (WARP) __syncwarp();
         if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&bars->u_empty[ring.s]);
         ring.next(kAfUnitSlots);
-        return true;
     }
 };
 
@@ -301,7 +315,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     const uint32_t tmem = bars.tmem;
 
     if (warp >= kAfLoadWarp) {
-        regs_shrink<kAfRegsOther>();
+        regs_shrink<L::kRegsOther>();
         if (warp == kAfLoadWarp && lane == 0) {
             StageRing ring;
             StageRing slots;
@@ -542,7 +556,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         }
         __syncwarp();
     } else {  // softmax: tile w = warp / 4, one row a thread
-        regs_grow<kAfRegsSoftmax>();
+        regs_grow<L::kRegsSoftmax>();
         const int tile = warp >> 2;
         const int row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
@@ -563,25 +577,29 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         };
         AfUnits units{&bars};
         StageRing slots;
-        AfUnit t;
-        while (ok && units.next<true>(&t)) {
-            int slot = 0;  // of this tile's queries
+        while (ok && units.peek()) {
+            // What the loop over the blocks does not need is read again after it: a row's scores
+            // take 128 registers.
+            int slot = 0, n, left;  // of this tile's queries; its blocks; keys seen from its first
+            {
+                const AfUnit& t = units.record();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (t.n(k) == 0) continue;
-                if (k == tile) slot = slots.s;
-                slots.next(Q);
+                for (int k = 0; k < 2; ++k) {
+                    if (t.n(k) == 0) continue;
+                    if (k == tile) slot = slots.s;
+                    slots.next(Q);
+                }
+                n = t.n(tile);
+                if (n == 0) {
+                    af_empty_row(a, t, af_row(a, t, tile, tok_in, head_in));
+                    units.release<true>();
+                    continue;
+                }
+                const int64_t seen = min(int64_t(t.len), t.pos0 + int64_t(t.tok(tile)) + tok_in + 1);
+                left = int(max(int64_t(-1), seen - int64_t(t.lo(tile)) * kAttnRows));
             }
-            const AfRow to = af_row(a, t, tile, tok_in, head_in);
-            const int n = t.n(tile);
-            const bool whole = a.parts == 1;
-            if (n == 0) {
-                af_empty_row(a, t, to);
-                continue;
-            }
-            const int64_t lim = min(int64_t(t.len), t.pos0 + to.tok + 1);  // keys this row sees
             float m = -INFINITY, l = 0.0f;
-            for (int j = 0; j < n; ++j) {
+            for (int j = 0; j < n; ++j, left -= kAttnRows) {
                 ok = all(&bars.s_full[tile], blocks & 1);
                 if (!ok) break;
                 ++blocks;
@@ -591,9 +609,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, x[q]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_wait_ld(x[q]);
-                const int64_t left = lim - int64_t(t.lo(tile) + j) * kAttnRows;  // visible keys of the block
                 if (__any_sync(0xffffffffu, left < kAttnRows)) {
-                    const int seen = int(max(int64_t(0), min(left, int64_t(kAttnRows))));
+                    const int seen = max(0, left);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -651,6 +668,10 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             ok = all(&bars.o_full[tile], uses & 1);
             if (!ok) break;
             tc_fence_after();
+            const AfUnit& t = units.record();
+            const AfRow to = af_row(a, t, tile, tok_in, head_in);
+            const bool whole = a.parts == 1;
+            uint8_t* o = a.o[t.r];
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays NaN
             if (to.valid) *to.lse = l == 0.0f ? -INFINITY : m * s.scale + logf(l);
             float* o_part = a.part_o + to.part * s.d;
@@ -696,7 +717,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
 #pragma unroll
                     for (int h = 0; h < DP / 64; ++h) {
                         if (off < 0 || h * 64 + word * 8 >= s.d) continue;
-                        st_v4(a.o[t.r] + off + h * 128 + word * 16,
+                        st_v4(o + off + h * 128 + word * 16,
                               ld_shared_v4(stage + h * L::kHalf + ((warp & 3) * 32 + rr) * 128 +
                                            ((word ^ (rr & 7)) << 4)));
                     }
@@ -704,6 +725,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.q_empty[slot]);
+            units.release<true>();
             ++uses;
         }
     }
