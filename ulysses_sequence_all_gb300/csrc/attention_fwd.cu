@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     if (grow) m = top;
                     l *= f;
                     if (j > 0) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < DP / 32; ++c) {
                             uint32_t y[32];
                             tmem_ld32(o_at + c * 32, y);
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             if (to.valid) *to.lse = l == 0.0f ? -INFINITY : m * s.scale + logf(l);
             float* o_part = a.part_o + to.part * s.d;
             uint8_t* stage = smem + L::kQ + slot * L::kTile;  // the queries are done with
-#pragma unroll
+#pragma unroll 1  // (rolled: short units go round all of this kernel's code all the time)
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t y[32];
                 tmem_ld32(o_at + c * 32, y);
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 __syncwarp();
                 const int64_t at = to.valid ? to.o : -1;
                 const int word = lane & 7;
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < 8; ++i) {
                     const int rr = i * 4 + (lane >> 3);
                     const int64_t off = __shfl_sync(0xffffffffu, at, rr);
