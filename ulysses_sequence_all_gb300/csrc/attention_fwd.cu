@@ -53,6 +53,7 @@ constexpr int kAfThreads = 384;
 constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfCleanWarp = 10, kAfUnitWarp = 11;
 constexpr int kAfUnitSlots = 4;
 constexpr int kAfBarBytes = 1024;
+constexpr int kAfMaxParts = 64;   // of the keys
 constexpr int kAfPairedWaves = 1;
 constexpr int kAfShortBlocks = 8;  // key blocks of a unit up to which it counts as short
 constexpr float kAfRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
@@ -62,21 +63,27 @@ constexpr int kAfS = 0, kAfO = 256;
 
 // How a launch uses its units: two tiles with long runs of shared keys; the same with few key
 // blocks, where the next queries need the room more than further keys; or one tile's rows twice,
-// over two parts of the keys.
-enum AfMode { kAfLong = 0, kAfShort = 1, kAfPaired = 2 };
+// over two parts of the keys, and the same with 32 rows at most (single tokens), whose queries take
+// a quarter of the room: the products read on past a slot's rows, into rows that nobody looks at.
+enum AfMode { kAfLong = 0, kAfShort = 1, kAfPaired = 2, kAfToken = 3 };
+constexpr int kAfTokenRows = 32;
 
 template <int DP, int MODE>
 struct AfSmem {
     static constexpr int kTile = kAttnRows * DP * 2;  // a tile of 128 rows; a block of 128 keys
     static constexpr int kHalf = kAttnRows * 128;     // its part of 64 columns
-    static constexpr int kSlots = DP == 64 ? 4 : MODE == kAfLong ? 3 : MODE == kAfShort ? 4 : 2;
-    static constexpr int kStages = DP == 64 ? 8 : 7 - kSlots;
+    static constexpr bool kPaired = MODE == kAfPaired || MODE == kAfToken;
+    static constexpr int kSlotHalf = MODE == kAfToken ? kAfTokenRows * 128 : kHalf;
+    static constexpr int kSlot = MODE == kAfToken ? kAfTokenRows * DP * 2 : kTile;
+    static constexpr int kSlots =
+        DP == 64 || MODE == kAfToken ? 4 : MODE == kAfLong ? 3 : MODE == kAfShort ? 4 : 2;
+    static constexpr int kStages = DP == 64 ? 8 : MODE == kAfToken ? 6 : 7 - kSlots;
     // Registers a thread: 384 x 168 at launch = 256 x 216 + 128 x 72 = 256 x 208 + 128 x 88 (what
     // the roles take without spills)
-    static constexpr int kRegsSoftmax = MODE == kAfPaired ? 208 : 216;
-    static constexpr int kRegsOther = MODE == kAfPaired ? 88 : 72;
+    static constexpr int kRegsSoftmax = kPaired ? 208 : 216;
+    static constexpr int kRegsOther = kPaired ? 88 : 72;
     static constexpr int kQ = kAfBarBytes;  // barriers first
-    static constexpr int kRing = kQ + kSlots * kTile;
+    static constexpr int kRing = kQ + kSlots * kSlot;
     static constexpr int kTotal = kRing + kStages * kTile;
     static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");  // and room to align the base
 };
@@ -271,7 +278,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     using L = AfSmem<DP, MODE>;
     using E = ElemT<F16>;
     constexpr int K = L::kStages, Q = L::kSlots;
-    constexpr bool PAIRED = MODE == kAfPaired;
+    constexpr bool PAIRED = L::kPaired;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                         return false;
                     mbar_arrive_expect_tx(&bars.q_full[slots.s], q_bytes);
                     for (int h = 0; h < halves; ++h)
-                        tensor_g2s_4d(smem + L::kQ + slots.s * L::kTile + h * L::kHalf,
+                        tensor_g2s_4d(smem + L::kQ + slots.s * L::kSlot + h * L::kSlotHalf,
                                       &a.qmap[t.r], 64 * h, t.kvh * s.group, t.tok(k), t.bb,
                                       &bars.q_full[slots.s]);
                     ++tiles;
@@ -400,13 +407,14 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 return ok = ok && wait_or_dead(bar, parity, dead);
             };
             auto scores = [&](int k, int stage) {  // S_k = Q_k K^T
-                const uint64_t qd = q_desc + slot[k] * (L::kTile >> 4);
+                const uint64_t qd = q_desc + slot[k] * (L::kSlot >> 4);
                 const uint64_t kd = k_desc + stage * (L::kTile >> 4);
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
                     if (ks >= nk) break;
-                    const uint32_t off = ((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4;
-                    tc_mma_ss(tmem + kAfS + k * 128, qd + off, kd + off, id_s, ks > 0);
+                    tc_mma_ss(tmem + kAfS + k * 128,
+                              qd + (((ks >> 2) * L::kSlotHalf + (ks & 3) * 32) >> 4),
+                              kd + (((ks >> 2) * L::kHalf + (ks & 3) * 32) >> 4), id_s, ks > 0);
                 }
                 tc_commit(&bars.s_full[k]);
             };
@@ -564,6 +572,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         const uint32_t o_at = tmem + lanes + kAfO + tile * 128;
         const int tok_in = row / s.group, head_in = row - tok_in * s.group;
         const float sl2 = s.scale * 1.4426950408889634f;  // scores to powers of two
+        const int rows = a.tile_tokens * s.group;         // of a tile
         uint32_t uses = 0, blocks = 0;
         bool ok = true;
         auto all = [&](uint64_t* bar, uint32_t parity) {
@@ -599,6 +608,24 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 left = int(max(int64_t(-1), seen - int64_t(t.lo(tile)) * kAttnRows));
             }
             float m = -INFINITY, l = 0.0f;
+            if (PAIRED && (warp & 3) * 32 >= rows) {  // none of the tile's rows: only keep step
+                for (int j = 0; j < n; ++j) {
+                    ok = all(&bars.s_full[tile], blocks & 1);
+                    if (!ok) break;
+                    ++blocks;
+                    arrive(&bars.p_half[tile]);
+                    arrive(&bars.p_ready[tile]);
+                }
+                if (ok) ok = all(&bars.o_full[tile], uses & 1);
+                if (!ok) break;
+                ++uses;
+                if (lane == 0) {
+                    mbar_arrive(&bars.o_free[tile]);
+                    mbar_arrive(&bars.q_empty[slot]);
+                }
+                units.release<true>();
+                continue;
+            }
             for (int j = 0; j < n; ++j, left -= kAttnRows) {
                 ok = all(&bars.s_full[tile], blocks & 1);
                 if (!ok) break;
@@ -675,7 +702,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);  // NaN stays NaN
             if (to.valid) *to.lse = l == 0.0f ? -INFINITY : m * s.scale + logf(l);
             float* o_part = a.part_o + to.part * s.d;
-            uint8_t* stage = smem + L::kQ + slot * L::kTile;  // the queries are done with
+            uint8_t* stage = smem + L::kQ + slot * L::kSlot;  // the queries are done with
 #pragma unroll 1  // (rolled: short units go round all of this kernel's code all the time)
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t y[32];
@@ -734,7 +761,9 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     if (warp == kAfMmaWarp) tmem_free(tmem);
 }
 
-// Joins the parts of the keys: one warp a row; lane c holds columns 4c .. 4c + 3.
+// Joins the parts of the keys: one warp a row; lane c holds columns 4c .. 4c + 3 of the outputs, and
+// the weights of parts c, c + 32, ... Every part's lse is on its way at once, then the outputs of
+// four parts at a time (one after the other, each waited for the memory's latency).
 template <bool F16>
 __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnFwdArgs a)
 {
@@ -742,24 +771,49 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const AttnShape& s = a.s;
     const int64_t rows = s.row_begin[s.W];
     const int lane = threadIdx.x & 31;
+    constexpr int kEach = kAfMaxParts / 32;
     for (int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5); row < rows;
          row += int64_t(gridDim.x) * 4) {
-        float top = -INFINITY;
-        for (int p = 0; p < a.parts; ++p) top = fmaxf(top, a.part_lse[p * rows + row]);
-        float sum = 0.0f;
+        float w[kEach], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int p = i * 32 + lane;
+            w[i] = p < a.parts ? a.part_lse[p * rows + row] : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) top = fmaxf(top, w[i]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {  // (NaN stays NaN)
+            w[i] = w[i] == -INFINITY ? 0.0f : expf(w[i] - top);
+            sum += w[i];
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < a.parts; ++p) {
-            const float z = a.part_lse[p * rows + row];
-            if (z == -INFINITY) continue;  // an empty part wrote no output
-            const float w = expf(z - top);
-            sum += w;
-            if (lane * 4 < s.d) {
-                const float4 o =
-                    *reinterpret_cast<const float4*>(a.part_o + (p * rows + row) * s.d + lane * 4);
-                acc.x = fmaf(w, o.x, acc.x);
-                acc.y = fmaf(w, o.y, acc.y);
-                acc.z = fmaf(w, o.z, acc.z);
-                acc.w = fmaf(w, o.w, acc.w);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            for (int p0 = 0; p0 < 32 && i * 32 + p0 < a.parts; p0 += 4) {
+                float4 o[4];
+                float f[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[k] = __shfl_sync(0xffffffffu, w[i], p0 + k);
+                    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    // an empty part (weight 0) wrote no output
+                    if (f[k] != 0.0f && lane * 4 < s.d)
+                        o[k] = *reinterpret_cast<const float4*>(
+                            a.part_o + ((i * 32 + p0 + k) * rows + row) * s.d + lane * 4);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    acc.x = fmaf(f[k], o[k].x, acc.x);
+                    acc.y = fmaf(f[k], o[k].y, acc.y);
+                    acc.z = fmaf(f[k], o[k].z, acc.z);
+                    acc.w = fmaf(f[k], o[k].w, acc.w);
+                }
             }
         }
         int r = 0;
@@ -793,6 +847,7 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     const int64_t pair = 2 * int64_t(a->tile_tokens);
     const int64_t blocks = (s.Skv + kAttnRows - 1) / kAttnRows;
     a->paired = s.Sq <= a->tile_tokens && blocks > 1;
+    if (a->paired) a->tile_tokens = int32_t(s.Sq);
     a->order.heads = s.head_begin[s.W];
     a->order.blocks = a->paired ? 1 : (s.Sq + pair - 1) / pair;
     a->order.group = attn_order_group(a->order.heads, s.Skv * s.d * 4);  // keys and values
@@ -809,7 +864,8 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     } else if (base > 0) {
         n = sm_count / base < blocks / 4 ? sm_count / base : blocks / 4;
     }
-    if (n > 64) n = 64;
+    const int64_t cap = kAfMaxParts / (a->paired ? 2 : 1);
+    if (n > cap) n = cap;
     if (n < 1) n = 1;
     a->splits = int32_t(n);
     a->parts = a->paired ? 2 * a->splits : a->splits;
@@ -839,7 +895,10 @@ static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int
 template <int DP, bool F16>
 static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int device, int grid)
 {
-    if (a.paired) return af_launch_mode<DP, F16, kAfPaired>(a, stream, device, grid);
+    if (a.paired)
+        return a.tile_tokens * a.s.group <= kAfTokenRows
+                   ? af_launch_mode<DP, F16, kAfToken>(a, stream, device, grid)
+                   : af_launch_mode<DP, F16, kAfPaired>(a, stream, device, grid);
     if constexpr (DP == 128) {  // (d <= 64 has room for both)
         const int64_t blocks = (a.s.Skv + kAttnRows - 1) / kAttnRows;
         if (blocks <= int64_t(kAfShortBlocks) * a.splits)
