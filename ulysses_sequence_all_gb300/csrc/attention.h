@@ -133,6 +133,25 @@ inline unsigned attn_ctas(int64_t units, int64_t cap, int sm_count)
     if (cap < sm_count || units > 0x7FFFFFFF) return unsigned(units < cap ? units : cap);
     return unsigned(units);
 }
+// A launch that may start before the kernel in front of it has finished (see let_next_start); the
+// kernel itself waits where it needs that (wait_for_previous). early = false: an ordinary launch.
+template <class Args>
+inline cudaError_t attn_launch_early(void (*kernel)(Args), unsigned grid, unsigned block, int smem,
+                                     cudaStream_t stream, const Args& a, bool early = true)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 // Heads in a group: as many as hold `bytes` each within about half of the L2 cache. The heads of a
 // token lie next to one another, so the CTAs at work then read whole stretches of memory; with
 // longer operands a head at a time keeps those in the cache.

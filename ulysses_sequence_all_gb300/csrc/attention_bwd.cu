@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_consta
     const AttnShape& s = a.s;
     constexpr int kAtOnce = 256 / LANES, kTurns = kAttnRows / 2 / kAtOnce;
     const int sub = threadIdx.x % LANES, slot = threadIdx.x / LANES;
+    let_next_start();
     const int64_t halves = 2 * s.head_begin[s.W] * a.q_tiles;
     for (int64_t at = blockIdx.x; at < halves; at += gridDim.x) {
         const int64_t tile = at >> 1;
@@ -313,6 +314,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         fence_proxy_async_shared();
     }
     if (warp == kAbMmaWarp) tmem_alloc(&bars.tmem);
+    wait_for_previous();  // the row statistics
+    let_next_start();     // dQ's CTAs fill the SMs that this kernel has no more units for
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1007,6 +1010,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             t = next;
         }
     }
+    wait_for_previous();  // dK and dV are done when this kernel is (nothing here needs them)
     __syncthreads();
     if (threadIdx.x == 0 && bars.dead) atomicOr(&g_attn_bwd_status, kStatusWaitTimeout);
     if (warp == kAbMmaWarp) tmem_free(tmem);
@@ -1034,12 +1038,13 @@ static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int devi
     attn_bwd_stats_kernel<F16, DP / 8><<<unsigned(parts < 0x7FFFFFFF ? parts : 0x7FFFFFFF), 256, 0,
                                          stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn_bwd_kv_kernel<DP, F16><<<attn_ctas(heads * a.kv_order.blocks, grid, sm_count), kAbThreads,
-                                  smem_kv, stream>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn_bwd_q_kernel<DP, F16><<<attn_ctas(heads * a.q_tiles, grid, sm_count), kAbThreads, smem_q,
-                                 stream>>>(a);
-    return cudaGetLastError();
+    e = attn_launch_early(attn_bwd_kv_kernel<DP, F16>,
+                          attn_ctas(heads * a.kv_order.blocks, grid, sm_count), kAbThreads, smem_kv,
+                          stream, a);
+    if (e != cudaSuccess) return e;
+    // (under a CTA cap dQ waits for its turn: the two together would pass it)
+    return attn_launch_early(attn_bwd_q_kernel<DP, F16>, attn_ctas(heads * a.q_tiles, grid, sm_count),
+                             kAbThreads, smem_q, stream, a, grid >= sm_count);
 }
 
 // The three launches over all ranks, `grid` CTAs of the product kernels at most. The shape, every

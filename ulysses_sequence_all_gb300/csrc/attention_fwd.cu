@@ -756,6 +756,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             ++uses;
         }
     }
+    let_next_start();
     __syncthreads();
     if (threadIdx.x == 0 && bars.dead) atomicOr(&g_attn_fwd_status, kStatusWaitTimeout);
     if (warp == kAfMmaWarp) tmem_free(tmem);
@@ -772,6 +773,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ 
     const int64_t rows = s.row_begin[s.W];
     const int lane = threadIdx.x & 31;
     constexpr int kEach = kAfMaxParts / 32;
+    wait_for_previous();
     for (int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5); row < rows;
          row += int64_t(gridDim.x) * 4) {
         float w[kEach], top = -INFINITY, sum = 0.0f;
@@ -888,8 +890,8 @@ static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.parts == 1) return e;
     const int64_t blocks = (a.s.row_begin[a.s.W] + 3) / 4;
-    attn_join_kernel<F16><<<unsigned(blocks < 1 << 16 ? blocks : 1 << 16), 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    return attn_launch_early(attn_join_kernel<F16>, unsigned(blocks < 1 << 16 ? blocks : 1 << 16), 128,
+                             0, stream, a);
 }
 
 template <int DP, bool F16>

@@ -226,6 +226,11 @@ __device__ __forceinline__ int64_t stolen_cta(const void* answer)
     return got ? int64_t(x) : -1;
 }
 
+// Programmatic launches: what comes before this kernel in its stream (and launched it early) is
+// complete and its writes are visible; the kernel behind it may start where there is room.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // 2^x (subnormal results flushed to zero).
 __device__ __forceinline__ float ex2(float x)
 {
