@@ -11,7 +11,10 @@
 // by both, seven products in place of five: dQ is then summed in one accumulator in a fixed order,
 // with no fp32 copy of it in memory, no atomics, and the same bits from run to run.
 //
-// Both are bound by the tensor cores. One CTA per SM (640 threads): 16 warps turn scores into P and
+// Both are bound by the products; those with both operands in shared memory take about 107 cycles
+// in place of 64. Measured at 16,380 tokens x 8 heads of 128: dK, dV 1,440 us (2,736 of the 3,000
+// cycles a tile are products), dQ 960 us, statistics 12 us; in all 1.05-1.1 PFLOP/s with five
+// products counted. One CTA per SM (640 threads): 16 warps turn scores into P and
 // dS, each four the same 32 columns of the tile (16 warps rather than 8 with twice the columns: the
 // chain from scores to P is what the products wait for, and more warps hide its latencies). Warp 16
 // loads (swizzled tensor maps), one lane of warp 17 issues the products, which run on one operand

@@ -8,8 +8,11 @@
 // gives zeros and lse = -infinity.
 //
 // One pass over the keys in blocks of 128 with the running maximum and sum: 4 d flops per (row,
-// key) on the tensor cores, one exponential. The kernel is bound by the tensor cores where d = 128
-// and by exponentials and products alike where d = 64; with few rows by reading the keys.
+// key) on the tensor cores, one exponential. With d = 128 it is bound by the products, those of S
+// by reading both operands from shared memory (about 107 cycles each in place of 64); with few rows
+// by reading the keys. Measured: 75,600 tokens x 8 heads of 128 in 13.0-13.8 ms, 1.7-1.8 PFLOP/s
+// (0.86-0.91 of the measured cuBLAS rate); 2 x 4,095 causal tokens, 32 heads over 8, in 0.20 ms; one
+// token each on 16 caches of 12,000-32,000 keys in 0.13 ms (0.79 of the copy peak).
 //
 // A CTA (one per SM, 384 threads) takes two tiles of 128 query rows that share their keys, unit
 // after unit. Warp 11 works out the units ahead and leaves their records in shared memory. Warp 8
