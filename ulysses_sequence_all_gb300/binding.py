@@ -156,8 +156,15 @@ def _nbytes(x) -> int:
     return x.numel() * x.element_size()
 
 
+_PTR_ARRAYS: dict = {}  # the ctypes array type of each length (making one costs as much as filling it)
+
+
 def _ptrs(xs: Sequence) -> ctypes.Array:
-    return (ctypes.c_void_p * len(xs))(*[_addr(x) for x in xs])
+    n = len(xs)
+    array = _PTR_ARRAYS.get(n)
+    if array is None:
+        array = _PTR_ARRAYS[n] = ctypes.c_void_p * n
+    return array(*[_addr(x) for x in xs])
 
 
 def _stream(stream) -> int:

@@ -273,29 +273,46 @@ void rope_turns(const Plan& p, double theta, float* turn_hi, float* turn_lo, Rop
     for (int a = 0; a < p.rope_axes; ++a) total *= p.rope_extent[a];
     grid->first = float(p.rope_first);
     grid->total = float(total);
+    // The pairs of each axis, and its place in the grid.
+    int64_t pairs[kMaxRopeAxes] = {half}, j = 0, stride = total;
+    const int last = p.rope_axes > 0 ? p.rope_axes - 1 : 0;
+    for (int a = 0; a < kMaxRopeAxes && p.rope_axes > 0; ++a) {
+        pairs[a] = a <= last ? p.rope_pairs[a] : 0;
+        j += pairs[a];
+        if (a <= last) stride /= p.rope_extent[a];
+        const int64_t ext = p.rope_extent[a <= last ? a : last];
+        grid->pair_end[a] = a < last ? int32_t(j) : int32_t(half);
+        grid->stride[a] = float(stride);
+        grid->extent[a] = float(ext);
+        grid->inv_stride[a] = float(1.0 / double(stride));
+        grid->inv_extent[a] = float(1.0 / double(ext));
+    }
     // Pair i of an axis with m pairs turns by coordinate * theta^(-i/m): the ladder of a head of
     // 2m columns. One axis of d/2 pairs is the usual theta^(-2j/d); pairs left over do not turn.
-    int64_t j = 0, stride = total;
-    for (int a = 0; a < kMaxRopeAxes; ++a) {
-        const int last = p.rope_axes > 0 ? p.rope_axes - 1 : 0;
-        const int64_t m = p.rope_axes == 0 ? (a == 0 ? half : 0) : (a <= last ? p.rope_pairs[a] : 0);
-        for (int64_t i = 0; i < m; ++i, ++j) {
-            const double t = std::pow(theta, -double(i) / double(m)) / two_pi;
-            const float hi = float(t);
-            turn_hi[j] = hi;
-            turn_lo[j] = float(t - double(hi));
+    // The powers are most of a small call's time on the host: a thread keeps its last ladder.
+    struct Ladder {
+        double theta = -1.0;
+        int64_t half = 0, pairs[kMaxRopeAxes] = {};
+        float hi[kMaxFusedD / 2], lo[kMaxFusedD / 2];
+    };
+    static thread_local Ladder kept;
+    if (kept.theta != theta || kept.half != half ||
+        std::memcmp(kept.pairs, pairs, sizeof pairs) != 0) {
+        j = 0;
+        for (int a = 0; a < kMaxRopeAxes; ++a) {
+            for (int64_t i = 0; i < pairs[a]; ++i, ++j) {
+                const double t = std::pow(theta, -double(i) / double(pairs[a])) / two_pi;
+                kept.hi[j] = float(t);
+                kept.lo[j] = float(t - double(kept.hi[j]));
+            }
         }
-        if (p.rope_axes > 0) {
-            if (a <= last) stride /= p.rope_extent[a];
-            const int64_t ext = p.rope_extent[a <= last ? a : last];
-            grid->pair_end[a] = a < last ? int32_t(j) : int32_t(half);
-            grid->stride[a] = float(stride);
-            grid->extent[a] = float(ext);
-            grid->inv_stride[a] = float(1.0 / double(stride));
-            grid->inv_extent[a] = float(1.0 / double(ext));
-        }
+        for (; j < half; ++j) kept.hi[j] = kept.lo[j] = 0.0f;
+        kept.theta = theta;
+        kept.half = half;
+        std::memcpy(kept.pairs, pairs, sizeof pairs);
     }
-    for (; j < half; ++j) turn_hi[j] = turn_lo[j] = 0.0f;
+    std::memcpy(turn_hi, kept.hi, size_t(half) * sizeof(float));
+    std::memcpy(turn_lo, kept.lo, size_t(half) * sizeof(float));
 }
 
 }  // namespace uly
