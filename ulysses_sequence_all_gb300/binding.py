@@ -170,7 +170,10 @@ def _ptrs(xs: Sequence) -> ctypes.Array:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None or not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch._C._cuda_getDevice())  # the same, without a Stream object (3 us a call)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream  # torch.cuda.Stream

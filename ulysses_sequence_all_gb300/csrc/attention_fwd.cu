@@ -57,8 +57,10 @@ constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfCleanWarp = 10, kAfUnitWarp = 
 constexpr int kAfUnitSlots = 4;
 constexpr int kAfBarBytes = 1024;
 constexpr int kAfMaxParts = 64;   // of the keys
-constexpr int kAfPairedWaves = 1;
-constexpr int kAfShortBlocks = 8;  // key blocks of a unit up to which it counts as short
+// Key blocks of a unit up to which it counts as short, and with ragged batches, which hold less than
+// the tensor. 75,600 queries x 40 heads of 128, short against long: 256 keys 477 : 529 us, 238 of 512
+// keys 535 : 612, 512 keys 739 : 699, 1,024 keys 1,309 : 1,103.
+constexpr int kAfShortBlocks = 3, kAfShortBlocksRagged = 4;
 constexpr float kAfRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 
 // Tensor memory columns: the two tiles' scores (their probabilities over them), their outputs.
@@ -857,18 +859,13 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     a->order.blocks = a->paired ? 1 : (s.Sq + pair - 1) / pair;
     a->order.group = attn_order_group(a->order.heads, s.Skv * s.d * 4);  // keys and values
     const int64_t base = a->order.heads * a->order.blocks;
-    // Paired, bound by reading keys of lengths that may differ: several units an SM, to even out, of
-    // eight blocks a part at least; but any part where that leaves SMs idle (latency). Else one
-    // wave of the SMs.
-    int64_t n = 1;
-    if (base > 0 && a->paired) {
-        const int64_t many = kAfPairedWaves * int64_t(sm_count) / base, one = sm_count / base;
-        n = many < blocks / 16 ? many : blocks / 16;
-        const int64_t few = one < blocks / 2 ? one : blocks / 2;
-        if (n < few) n = few;
-    } else if (base > 0) {
-        n = sm_count / base < blocks / 4 ? sm_count / base : blocks / 4;
-    }
+    // One wave of the SMs (finer parts of a ragged batch, evened out by stealing, measured slower: 16
+    // caches 133 us with 2 units a head, 149 with 4, 154 with 18: a unit's start and the join cost
+    // more than the lengths' difference), of a block a tile at least where rows are few (latency), of
+    // four blocks where a part's output is a whole tile.
+    int64_t n = base > 0 ? sm_count / base : 1;
+    const int64_t most = blocks / (a->paired ? 2 : 4);
+    if (n > most) n = most;
     const int64_t cap = kAfMaxParts / (a->paired ? 2 : 1);
     if (n > cap) n = cap;
     if (n < 1) n = 1;
@@ -906,7 +903,7 @@ static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int devi
                    : af_launch_mode<DP, F16, kAfPaired>(a, stream, device, grid);
     if constexpr (DP == 128) {  // (d <= 64 has room for both)
         const int64_t blocks = (a.s.Skv + kAttnRows - 1) / kAttnRows;
-        if (blocks <= int64_t(kAfShortBlocks) * a.splits)
+        if (blocks <= int64_t(a.s.kv_lens ? kAfShortBlocksRagged : kAfShortBlocks) * a.splits)
             return af_launch_mode<DP, F16, kAfShort>(a, stream, device, grid);
     }
     return af_launch_mode<DP, F16, kAfLong>(a, stream, device, grid);
