@@ -42,7 +42,8 @@ static __device__ unsigned g_attn_bwd_status;
 
 constexpr int kAbThreads = 640;
 constexpr int kAbLoadWarp = 16, kAbMmaWarp = 17, kAbCleanWarp = 18, kAbUnitWarp = 19;
-constexpr int kAbUnitSlots = 4;
+// Units known ahead of the slowest reader: one, so that CTAs do not pile up units others could take.
+constexpr int kAbUnitSlots = 1;
 constexpr int kAbStats = 2 * kAttnRows * 4;  // one tile's lse and D
 
 // Keys that batch element bb holds, and the position of its first query (beyond every key when the
@@ -194,7 +195,10 @@ __device__ __forceinline__ void ab_publish(AbUnitBoard<Unit>& b, int64_t units, 
     StageRing ring;
     AttnUnitSource source{units, &b.answer, &b.steal, dead};
     bool ok = true;
-    for (int64_t made = 0; ok;) {
+    for (int64_t made = 0;;) {
+        if (made >= kAbUnitSlots)  // before a unit is taken, not with one in hand
+            ok = __all_sync(0xffffffffu, wait_or_dead(&b.empty[ring.s], ring.phase ^ 1u, dead));
+        if (!ok) break;
         const int64_t u = source.next();
         Unit t;
         t.n = -1;
@@ -205,9 +209,7 @@ __device__ __forceinline__ void ab_publish(AbUnitBoard<Unit>& b, int64_t units, 
                 continue;
             }
         }
-        if (made >= kAbUnitSlots)
-            ok = __all_sync(0xffffffffu, wait_or_dead(&b.empty[ring.s], ring.phase ^ 1u, dead));
-        if (ok && (threadIdx.x & 31) == 0) {
+        if ((threadIdx.x & 31) == 0) {
             b.unit[ring.s] = t;
             mbar_arrive(&b.full[ring.s]);
         }
@@ -440,10 +442,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 next_dp(true, t.n == 1, 0);
             }
             while (live && ok) {
-                const bool more = source.next<false>(&next);
+                bool more = false;
                 for (int i = 0; ok && i < t.n; ++i, ++tiles) {
                     const int at = ring.s;
                     const bool end = i + 1 == t.n;           // the next tile is the next unit's
+                    if (end) more = source.next<false>(&next);
                     const bool last = end ? next.n == 1 : i + 2 == t.n;
                     ring.next(K);
                     wait(&bars.p_ready, tiles & 1);
@@ -841,9 +844,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 make_dp(true, t.n == 1, 0);
             }
             while (live && ok) {
-                const bool more = source.next<false>(&next);
+                bool more = false;
                 for (int j = 0; ok && j < t.n; ++j, ++blocks) {
                     const bool end = j + 1 == t.n;  // the next block is the next unit's
+                    if (end) more = source.next<false>(&next);
                     int after = ks;
                     wait(&bars.s_read, blocks & 1);
                     if (!end) after = make_s(false, uses);

@@ -54,7 +54,7 @@ static __device__ unsigned g_attn_fwd_status;
 
 constexpr int kAfThreads = 384;
 constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfCleanWarp = 10, kAfUnitWarp = 11;
-constexpr int kAfUnitSlots = 4;
+constexpr int kAfMaxUnitSlots = 4;
 constexpr int kAfBarBytes = 1024;
 constexpr int kAfMaxParts = 64;   // of the keys
 // Key blocks of a unit up to which it counts as short, and with ragged batches, which hold less than
@@ -87,6 +87,10 @@ struct AfSmem {
     // the roles take without spills)
     static constexpr int kRegsSoftmax = kPaired ? 208 : 216;
     static constexpr int kRegsOther = kPaired ? 88 : 72;
+    // Units known at a time: a few, so that the next one's copies start early; single tokens the one
+    // at work and the next, so that CTAs do not pile up what others could take (with four, 576 units
+    // on 152 CTAs ended between 26 and 129 us).
+    static constexpr int kUnitSlots = kPaired ? 2 : kAfMaxUnitSlots;
     static constexpr int kQ = kAfBarBytes;  // barriers first
     static constexpr int kRing = kQ + kSlots * kSlot;
     static constexpr int kTotal = kRing + kStages * kTile;
@@ -107,7 +111,7 @@ struct AfUnit {
 };
 
 struct AfBars {
-    uint64_t u_full[kAfUnitSlots], u_empty[kAfUnitSlots];  // unit records
+    uint64_t u_full[kAfMaxUnitSlots], u_empty[kAfMaxUnitSlots];  // unit records
     uint64_t q_full[4], q_empty[4];  // query tile landed; its rows are written
     uint64_t s_full[2];              // scores complete
     uint64_t p_half[2], p_ready[2];  // half of the probabilities (and a rescaled O) written; all
@@ -118,7 +122,7 @@ struct AfBars {
     uint4 answer;
     uint32_t tmem;
     int dead;
-    AfUnit unit[kAfUnitSlots];       // r < 0: no more
+    AfUnit unit[kAfMaxUnitSlots];    // r < 0: no more
 };
 static_assert(sizeof(AfBars) <= kAfBarBytes, "barriers");
 
@@ -171,6 +175,7 @@ __device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
 }
 
 // A warp's (or thread's) way through the CTA's units.
+template <int SLOTS>
 struct AfUnits {
     AfBars* bars;
     StageRing ring;
@@ -198,7 +203,7 @@ struct AfUnits {
     {
         if (WARP) __syncwarp();
         if (!WARP || (threadIdx.x & 31) == 0) mbar_arrive(&bars->u_empty[ring.s]);
-        ring.next(kAfUnitSlots);
+        ring.next(SLOTS);
     }
 };
 
@@ -237,12 +242,12 @@ __device__ __forceinline__ void af_empty_row(const AttnFwdArgs& a, const AfUnit&
 // block) for every stage of the ring, and queries(t) for a unit's query tiles, after its first keys
 // (a slot for them may have to wait for the unit before to finish, which those keys must not).
 // Both return false to stop.
-template <bool PAIRED, bool WARP, class Queries, class Block>
+template <bool PAIRED, int SLOTS, bool WARP, class Queries, class Block>
 __device__ __forceinline__ void af_walk(AfBars* bars, Queries queries, Block block)
 {
-    AfUnits units{bars};
+    AfUnits<SLOTS> units{bars};
     AfUnit t;
-    bool live = units.next<WARP>(&t);
+    bool live = units.template next<WARP>(&t);
     while (live) {
         const int n = t.most();
         if constexpr (PAIRED) {  // each tile has keys of its own
@@ -264,7 +269,7 @@ __device__ __forceinline__ void af_walk(AfBars* bars, Queries queries, Block blo
                 if (j + 1 < n && !block(false, t, t.lo0 + j + 1)) return;
             }
         }
-        live = units.next<WARP>(&t);
+        live = units.template next<WARP>(&t);
     }
 }
 
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     const int halves = (s.d + 63) / 64;  // tiles of 64 columns
 
     if (threadIdx.x == 0) {
-        for (int k = 0; k < kAfUnitSlots; ++k) {
+        for (int k = 0; k < L::kUnitSlots; ++k) {
             mbar_init(&bars.u_full[k], 1);
             mbar_init(&bars.u_empty[k], s.kv_lens ? 11 : 10);  // warps 0-9, and 10
         }
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 ring.next(K);
                 return true;
             };
-            af_walk<PAIRED, false>(&bars, queries, block);
+            af_walk<PAIRED, L::kUnitSlots, false>(&bars, queries, block);
             // leave no copy into this CTA's shared memory in flight
             for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k)
                 if (!mbar_wait_bounded(&bars.kv_full[k % K], uint32_t((k / K) & 1)))
@@ -374,7 +379,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             // A masked probability is zero, but zero times whatever lies past the last key may be
             // NaN: a value block's rows past it become zeros before its product.
             StageRing ring;
-            af_walk<PAIRED, true>(
+            af_walk<PAIRED, L::kUnitSlots, true>(
                 &bars, [](const AfUnit&) { return true; },
                 [&](bool value, const AfUnit& t, int at) {
                     const int past = value ? af_past(s, t, at) : kAttnRows;
@@ -469,9 +474,9 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     ring.next(K);
                 }
             };
-            AfUnits units{&bars};
+            AfUnits<L::kUnitSlots> units{&bars};
             AfUnit t, next;
-            bool live = units.next<false>(&t);
+            bool live = units.template next<false>(&t);
             if (live) {
                 if constexpr (PAIRED) {
                     unit_scores(t);
@@ -484,9 +489,11 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
             }
             while (live && ok) {
-                const bool more = units.next<false>(&next);
+                bool more = false;
                 const int n = t.most();
                 for (int j = 0; ok && j < n; ++j) {
+                    // (asked for as late as it is needed: see kUnitSlots)
+                    if (j + 1 == n) more = units.template next<false>(&next);
                     if constexpr (PAIRED) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
@@ -539,20 +546,24 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             StageRing ring;
             bool ok = true;
             int64_t made = 0;
-            auto publish = [&](const AfUnit& t) {
-                if (made >= kAfUnitSlots)
+            auto room = [&]() {  // before a unit is taken, not with one in hand
+                if (made >= L::kUnitSlots)
                     ok = __all_sync(0xffffffffu,
                                     wait_or_dead(&bars.u_empty[ring.s], ring.phase ^ 1u, dead));
-                if (ok && lane == 0) {
+                return ok;
+            };
+            auto publish = [&](const AfUnit& t) {
+                if (lane == 0) {
                     bars.unit[ring.s] = t;
                     mbar_arrive(&bars.u_full[ring.s]);
                 }
+                __syncwarp();
                 ++made;
-                ring.next(kAfUnitSlots);
+                ring.next(L::kUnitSlots);
             };
             AfUnit t;
             AttnUnitSource source{a.units, &bars.answer, &bars.steal, dead};
-            for (int64_t u; ok && (u = source.next()) >= 0;) {
+            for (int64_t u; room() && (u = source.next()) >= 0;) {
                 t = af_unit(a, u);
                 if (t.most() > 0) {
                     publish(t);
@@ -589,7 +600,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        AfUnits units{&bars};
+        AfUnits<L::kUnitSlots> units{&bars};
         StageRing slots;
         while (ok && units.peek()) {
             // What the loop over the blocks does not need is read again after it: a row's scores
@@ -606,7 +617,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 n = t.n(tile);
                 if (n == 0) {
                     af_empty_row(a, t, af_row(a, t, tile, tok_in, head_in));
-                    units.release<true>();
+                    units.template release<true>();
                     continue;
                 }
                 const int64_t seen = min(int64_t(t.len), t.pos0 + int64_t(t.tok(tile)) + tok_in + 1);
@@ -628,7 +639,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     mbar_arrive(&bars.o_free[tile]);
                     mbar_arrive(&bars.q_empty[slot]);
                 }
-                units.release<true>();
+                units.template release<true>();
                 continue;
             }
             for (int j = 0; j < n; ++j, left -= kAttnRows) {
@@ -757,7 +768,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.q_empty[slot]);
-            units.release<true>();
+            units.template release<true>();
             ++uses;
         }
     }
@@ -859,10 +870,9 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     a->order.blocks = a->paired ? 1 : (s.Sq + pair - 1) / pair;
     a->order.group = attn_order_group(a->order.heads, s.Skv * s.d * 4);  // keys and values
     const int64_t base = a->order.heads * a->order.blocks;
-    // One wave of the SMs (finer parts of a ragged batch, evened out by stealing, measured slower: 16
-    // caches 133 us with 2 units a head, 149 with 4, 154 with 18: a unit's start and the join cost
-    // more than the lengths' difference), of a block a tile at least where rows are few (latency), of
-    // four blocks where a part's output is a whole tile.
+    // One wave of the SMs (finer parts of a ragged batch, evened out by stealing, measured no faster:
+    // 16 caches 134 us with 2 units a head, 134 with 7, 136 with 9, 154 with 19), of a block a tile at
+    // least where rows are few (latency), of four blocks where a part's output is a whole tile.
     int64_t n = base > 0 ? sm_count / base : 1;
     const int64_t most = blocks / (a->paired ? 2 : 4);
     if (n > most) n = most;
