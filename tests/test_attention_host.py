@@ -48,6 +48,7 @@ def status(qp, kp, **kw):
     {"q": (1, 2, [64], [4], 136, "bfloat16"), "kv": (1, 2, [64], [4], 136, "bfloat16")},
     {"q": (1, 2, [64], [65], 64, "bfloat16"), "kv": (1, 2, [64], [1], 64, "bfloat16")},
     {"q": (2, 1, [9, 9], [4, 2], 64, "bfloat16"), "kv": (2, 1, [9, 9], [1, 2], 64, "bfloat16")},
+    {"kv": (1, 2, [2 ** 31], [2], 64, "bfloat16")},         # past tensor-map coordinates
     {"kv": (1, 2, [2 ** 26 + 1], [2], 64, "bfloat16")},     # more keys than a unit walks
     {"q": (1, 2, [2 ** 25 + 1], [4], 64, "bfloat16")},      # more rows: two heads share keys
 ])
