@@ -202,7 +202,8 @@ class _Attention(torch.autograd.Function):
         W = len(qkv) // 3
         qkv = [x.contiguous() for x in qkv]
         q, k, v = qkv[:W], qkv[W:2 * W], qkv[2 * W:]
-        kv_lens, q_start = _int32(kv_lens), _int32(q_start)
+        kv_lens = _counts(kv_lens, q_plan.b, q[0].device, "kv_lens")
+        q_start = _counts(q_start, q_plan.b, q[0].device, "q_start")
         out = [torch.empty_like(x) for x in q]
         lse = [torch.empty((x.shape[0], x.shape[2], x.shape[1]), dtype=torch.float32,
                            device=x.device) for x in q]
@@ -227,15 +228,39 @@ class _Attention(torch.autograd.Function):
         return (None,) * 6 + (*dq, *dk, *dv)
 
 
-def _int32(x):
-    """A mask's counts as the library takes them: contiguous int32 (None stays None)."""
-    return None if x is None else x.to(torch.int32).contiguous()
+def _counts(x, b, device, what):
+    """A mask's counts as the library takes them: b int32 on the device (None stays None); wider ones
+    that do not fit are beyond every key either way."""
+    if x is None:
+        return None
+    x = torch.as_tensor(x)
+    if x.numel() != b or x.is_floating_point() or x.is_complex():
+        raise ValueError(f"{what}: {b} whole numbers, one per batch element, not {x.dtype} "
+                         f"{tuple(x.shape)}")
+    if x.dtype == torch.int64:
+        x = x.clamp(-2 ** 31, 2 ** 31 - 1)
+    return x.to(device=device, dtype=torch.int32).contiguous()
+
+
+def _check_heads(plan, xs, what):
+    """W device tensors shaped as mode 0's outputs with this plan, in its type: the kernels read as
+    many elements as the plan says."""
+    shapes = _shapes(plan, 0)
+    if len(xs) != len(shapes):
+        raise ValueError(f"{what}: {len(shapes)} tensors, one per rank, not {len(xs)}")
+    for r, (x, sh) in enumerate(zip(xs, shapes)):
+        if tuple(x.shape) != sh or not x.is_cuda or B.DTYPE_CODES.get(str(x.dtype)[6:]) != plan.code:
+            raise ValueError(f"{what}[{r}]: {plan.dtype} {sh} on the device, not {x.dtype} "
+                             f"{tuple(x.shape)} on {x.device}")
 
 
 def attention(q_plan: B.Plan, kv_plan: B.Plan, q, k, v, scale: float | None = None,
               causal: bool = False, kv_lens=None, q_start=None):
     """Attention of every rank's heads over the whole sequence, on the head-side tensors that mode
     0 returns (lists of W: q (b, Sq, n_r, d), k and v (b, Skv, m_r, d)), differentiable in q, k and
-    v; `scale` defaults to d ** -0.5. Returns a list of W tensors shaped as q."""
+    v; `scale` defaults to d ** -0.5. kv_lens and q_start: b whole numbers, a tensor on any device or
+    a list. Returns a list of W tensors shaped as q."""
+    for plan, xs, what in ((q_plan, q, "q"), (kv_plan, k, "k"), (kv_plan, v, "v")):
+        _check_heads(plan, xs, what)
     scale = q_plan.d ** -0.5 if scale is None else scale
     return list(_Attention.apply(q_plan, kv_plan, scale, causal, kv_lens, q_start, *q, *k, *v))

@@ -156,6 +156,17 @@ def _nbytes(x) -> int:
     return x.numel() * x.element_size()
 
 
+def _counts(x, b: int, what: str) -> int:
+    """Address of a mask's counts: None, an address, or a device tensor of b int32, which the kernels
+    read as it stands."""
+    if x is None or isinstance(x, int):
+        return _addr(x)
+    if not x.is_cuda or str(x.dtype) != "torch.int32" or x.numel() != b or not x.is_contiguous():
+        raise ValueError(f"{what}: a contiguous int32 tensor of b = {b} entries on the device, not "
+                         f"{x.dtype} {tuple(x.shape)} on {x.device}")
+    return _addr(x)
+
+
 _PTR_ARRAYS: dict = {}  # the ctypes array type of each length (making one costs as much as filling it)
 
 
@@ -185,6 +196,7 @@ class Plan:
     def __init__(self, handle: int, W: int, b: int, seq_splits, head_splits, d: int, dtype: str):
         self.handle = handle
         self.W, self.b, self.d, self.dtype = W, b, d, dtype
+        self.code = DTYPE_CODES.get(dtype, dtype)  # ULY_BF16, ...
         self.seq_splits, self.head_splits = list(seq_splits), list(head_splits)
 
     def __del__(self):
@@ -397,7 +409,8 @@ def ulysses_attention(q_plan: Plan, kv_plan: Plan, q, k, v, out, lse, scale: flo
     entries or None. `workspace` is a device tensor of at least
     ulysses_attention_workspace(q_plan, kv_plan) bytes (None where that is 0)."""
     _check(_lib().ulysses_attention(q_plan, kv_plan, _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out),
-                                    _ptrs(lse), _addr(kv_lens), _addr(q_start), int(causal), scale,
+                                    _ptrs(lse), _counts(kv_lens, q_plan.b, "kv_lens"),
+                                    _counts(q_start, q_plan.b, "q_start"), int(causal), scale,
                                     _addr(workspace), _nbytes(workspace), _stream(stream)),
            "ulysses_attention")
 
@@ -418,7 +431,8 @@ def ulysses_attention_backward(q_plan: Plan, kv_plan: Plan, dq, dk, dv, q, k, v,
     ulysses_attention_backward_workspace(q_plan, kv_plan) bytes."""
     _check(_lib().ulysses_attention_backward(
         q_plan, kv_plan, _ptrs(dq), _ptrs(dk), _ptrs(dv), _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out),
-        _ptrs(lse), _ptrs(go), _addr(kv_lens), _addr(q_start), int(causal), scale,
+        _ptrs(lse), _ptrs(go), _counts(kv_lens, q_plan.b, "kv_lens"),
+        _counts(q_start, q_plan.b, "q_start"), int(causal), scale,
         _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_backward")
 
 
