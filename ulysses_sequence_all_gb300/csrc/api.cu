@@ -1,6 +1,7 @@
 // api.cu -- the extern "C" entry points declared in include/ulysses.h: argument checks, chunking,
 // argument blocks, launches. All device work goes to the caller's stream; nothing synchronises
 // except ulysses_device_status().
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -66,6 +67,23 @@ struct DeviceInfo {
     int sm_count;
 };
 
+// Whether this thread has a current context (no runtime call tells).
+bool context_current()
+{
+    using Fn = CUresult (*)(CUcontext*);
+    static const Fn get = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        return cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault,
+                                                &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<Fn>(p)
+                   : nullptr;
+    }();
+    CUcontext ctx = nullptr;
+    return get && get(&ctx) == CUDA_SUCCESS && ctx != nullptr;
+}
+
 int current_device(DeviceInfo* info)
 {
     static std::atomic<int> sm_counts[64];  // per device, filled on first use by any thread
@@ -74,12 +92,9 @@ int current_device(DeviceInfo* info)
     if (e != cudaSuccess) return cuda_fail(e);
     if (dev < 0 || dev >= 64) return ULY_EINVAL;
     // A thread that has made no runtime call yet (autograd's, on its first backward) has no current
-    // context, and the driver's tensor-map encoder wants one: setting the device binds it.
-    static thread_local int bound = -1;
-    if (bound != dev) {
-        if ((e = cudaSetDevice(dev)) != cudaSuccess) return cuda_fail(e);
-        bound = dev;
-    }
+    // context, and the driver's tensor-map encoder wants one: setting the device binds it. A context
+    // that the caller made current stays.
+    if (!context_current() && (e = cudaSetDevice(dev)) != cudaSuccess) return cuda_fail(e);
     int sms = sm_counts[dev].load(std::memory_order_relaxed);
     if (sms == 0) {
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
