@@ -449,7 +449,8 @@ int ulysses_a2a_4d_packed_fused_backward(ulysses_plan_t plan, int planes, int q_
  * workspace  device memory of ulysses_attention_workspace bytes (0: may be NULL), 16-byte aligned:
  *            partial results where few query rows leave the keys to be split over the SMs. Its
  *            content does not matter and is not kept.
- * The result does not depend on timing. q_plan's CTA cap holds for the launch.
+ * The result does not depend on timing. q_plan's CTA cap holds for each of the call's launches and
+ * changes no bit of the result.
  * ULY_EINVAL, ULY_EALIGN (kv_lens and q_start: 4 bytes) and ULY_EOVERLAP as for the other calls.
  */
 int ulysses_attention(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, const void* const* q,
@@ -472,8 +473,7 @@ int ulysses_attention_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, s
  * the sums are fp32 and in a fixed order: the same bits from run to run.
  * workspace: device memory of ulysses_attention_backward_workspace bytes, 16-byte aligned; its
  * content does not matter and is not kept.
- * Three launches on `stream`; q_plan's CTA cap holds for the two that compute. Statuses as the
- * forward's.
+ * Three launches on `stream`, under q_plan's CTA cap as the forward's. Statuses as the forward's.
  */
 int ulysses_attention_backward(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, void* const* dq,
                                void* const* dk, void* const* dv, const void* const* q,

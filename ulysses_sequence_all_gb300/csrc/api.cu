@@ -869,16 +869,16 @@ int attn_shape(const Plan& qp, const Plan& kp, AttnShape* s)
     return ULY_OK;
 }
 
-int attn_grid(const Plan& p, const DeviceInfo& dev)
+int64_t attn_cap(const Plan& p)
 {
-    return p.max_ctas > 0 && p.max_ctas < dev.sm_count ? int(p.max_ctas) : dev.sm_count;
+    return p.max_ctas > 0 && p.max_ctas < kAttnMostCtas ? p.max_ctas : kAttnMostCtas;
 }
 
 // Units of a forward call, and the bytes of its partial results (0 where the keys are not split).
-size_t attn_fwd_setup(const Plan& qp, const DeviceInfo& dev, AttnFwdArgs* a)
+size_t attn_fwd_setup(const DeviceInfo& dev, AttnFwdArgs* a)
 {
     const AttnShape& s = a->s;
-    attn_fwd_split(a, attn_grid(qp, dev));
+    attn_fwd_split(a, dev.sm_count);
     if (a->parts == 1) return 0;
     const size_t rows = size_t(s.row_begin[s.W]);
     return size_t(a->parts) * ((rows * size_t(s.d) + rows) * sizeof(float));
@@ -950,7 +950,7 @@ int attn_fwd_device(const Plan& qp, const Plan& kp, const void* const* q, const 
     if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
     DeviceInfo dev;
     if ((rc = current_device(&dev))) return rc;
-    const size_t need = attn_fwd_setup(qp, dev, &a);
+    const size_t need = attn_fwd_setup(dev, &a);
     if (need) {
         if (!workspace || workspace_bytes < need) return ULY_EINVAL;
         if (!aligned16(workspace)) return ULY_EALIGN;
@@ -963,7 +963,7 @@ int attn_fwd_device(const Plan& qp, const Plan& kp, const void* const* q, const 
         a.o[r] = static_cast<uint8_t*>(o[r]);
         a.lse[r] = lse[r];
     }
-    const cudaError_t e = attn_fwd_launch(a, q, k, v, stream, dev.device, attn_grid(qp, dev),
+    const cudaError_t e = attn_fwd_launch(a, q, k, v, stream, dev.device, attn_cap(qp),
                                           dev.sm_count);
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
@@ -1023,7 +1023,7 @@ int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const
         a.dk[r] = static_cast<uint8_t*>(dk[r]);
         a.dv[r] = static_cast<uint8_t*>(dv[r]);
     }
-    const cudaError_t e = attn_bwd_launch(a, q, k, v, stream, dev.device, attn_grid(qp, dev),
+    const cudaError_t e = attn_bwd_launch(a, q, k, v, stream, dev.device, attn_cap(qp),
                                           dev.sm_count);
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
@@ -1336,7 +1336,7 @@ int ulysses_attention_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, s
     DeviceInfo dev;
     int rc = attn_shape(q_plan->p, kv_plan->p, &a.s);
     if (rc || (rc = current_device(&dev))) return rc;
-    *bytes = attn_fwd_setup(q_plan->p, dev, &a);
+    *bytes = attn_fwd_setup(dev, &a);
     return ULY_OK;
 }
 

@@ -126,12 +126,12 @@ struct AttnBwdArgs {
 };
 
 // Host side.
-// CTAs of a launch of `units`: one each, to be taken over by those that are done (AttnUnitSource),
-// or at most `cap` where the plan caps them or there are more than a grid holds.
+constexpr int64_t kAttnMostCtas = 0x7FFFFFFF;  // of a grid, and the cap of a plan without one
+// CTAs of a launch of `units`: one each, to be taken over by those that are done (AttnUnitSource);
+// where the plan's cap or a grid holds fewer, as many as run at a time.
 inline unsigned attn_ctas(int64_t units, int64_t cap, int sm_count)
 {
-    if (cap < sm_count || units > 0x7FFFFFFF) return unsigned(units < cap ? units : cap);
-    return unsigned(units);
+    return unsigned(units <= cap ? units : cap < sm_count ? cap : sm_count);
 }
 // A launch that may start before the kernel in front of it has finished (see let_next_start); the
 // kernel itself waits where it needs that (wait_for_previous). early = false: an ordinary launch.
@@ -156,13 +156,15 @@ inline cudaError_t attn_launch_early(void (*kernel)(Args), unsigned grid, unsign
 // token lie next to one another, so the CTAs at work then read whole stretches of memory; with
 // longer operands a head at a time keeps those in the cache.
 int64_t attn_order_group(int64_t heads, int64_t bytes);
-void attn_fwd_split(AttnFwdArgs* a, int sm_count);  // tiles, units and parts from the shape
+// Tiles, units and parts of the keys from the shape and the device alone: a CTA cap changes no bit.
+void attn_fwd_split(AttnFwdArgs* a, int sm_count);
+// `cap`: CTAs of a launch at most; under one (below kAttnMostCtas) no kernel starts beside another.
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
-                            const void* const* v, cudaStream_t stream, int device, int grid,
+                            const void* const* v, cudaStream_t stream, int device, int64_t cap,
                             int sm_count);
 cudaError_t attn_fwd_status(unsigned* status, bool clear);
 cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* const* k,
-                            const void* const* v, cudaStream_t stream, int device, int grid,
+                            const void* const* v, cudaStream_t stream, int device, int64_t cap,
                             int sm_count);
 cudaError_t attn_bwd_status(unsigned* status, bool clear);
 

@@ -1024,7 +1024,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
 }
 
 template <int DP, bool F16>
-static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int device, int grid,
+static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int device, int64_t cap,
                              int sm_count)
 {
     static std::atomic<unsigned long long> raised{0};
@@ -1042,23 +1042,21 @@ static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int devi
     }
     const int64_t heads = a.q_order.heads;
     const int64_t parts = 2 * heads * a.q_tiles;
-    attn_bwd_stats_kernel<F16, DP / 8><<<unsigned(parts < 0x7FFFFFFF ? parts : 0x7FFFFFFF), 256, 0,
-                                         stream>>>(a);
+    const bool early = cap == kAttnMostCtas;  // (two at a time together would pass a cap)
+    attn_bwd_stats_kernel<F16, DP / 8><<<unsigned(parts < cap ? parts : cap), 256, 0, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = attn_launch_early(attn_bwd_kv_kernel<DP, F16>,
-                          attn_ctas(heads * a.kv_order.blocks, grid, sm_count), kAbThreads, smem_kv,
-                          stream, a);
+                          attn_ctas(heads * a.kv_order.blocks, cap, sm_count), kAbThreads, smem_kv,
+                          stream, a, early);
     if (e != cudaSuccess) return e;
-    // (under a CTA cap dQ waits for its turn: the two together would pass it)
-    return attn_launch_early(attn_bwd_q_kernel<DP, F16>, attn_ctas(heads * a.q_tiles, grid, sm_count),
-                             kAbThreads, smem_q, stream, a, grid >= sm_count);
+    return attn_launch_early(attn_bwd_q_kernel<DP, F16>, attn_ctas(heads * a.q_tiles, cap, sm_count),
+                             kAbThreads, smem_q, stream, a, early);
 }
 
-// The three launches over all ranks, `grid` CTAs of the product kernels at most. The shape, every
-// pointer and the workspace are set in `a`.
+// The three launches over all ranks. The shape, every pointer and the workspace are set in `a`.
 cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* const* k,
-                            const void* const* v, cudaStream_t stream, int device, int grid,
-                             int sm_count)
+                            const void* const* v, cudaStream_t stream, int device, int64_t cap,
+                            int sm_count)
 {
     const AttnShape& s = a.s;
     if (s.head_begin[s.W] == 0) return cudaSuccess;
@@ -1075,10 +1073,10 @@ cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* co
             return cudaErrorInvalidValue;
     }
     if (s.d <= 64)
-        return s.f16 ? ab_launch<64, true>(a, stream, device, grid, sm_count)
-                     : ab_launch<64, false>(a, stream, device, grid, sm_count);
-    return s.f16 ? ab_launch<128, true>(a, stream, device, grid, sm_count)
-                 : ab_launch<128, false>(a, stream, device, grid, sm_count);
+        return s.f16 ? ab_launch<64, true>(a, stream, device, cap, sm_count)
+                     : ab_launch<64, false>(a, stream, device, cap, sm_count);
+    return s.f16 ? ab_launch<128, true>(a, stream, device, cap, sm_count)
+                 : ab_launch<128, false>(a, stream, device, cap, sm_count);
 }
 
 cudaError_t attn_bwd_status(unsigned* status, bool clear)

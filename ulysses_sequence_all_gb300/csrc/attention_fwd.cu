@@ -885,7 +885,8 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
 }
 
 template <int DP, bool F16, int MODE>
-static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int device, int grid)
+static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int device, int64_t cap,
+                                  int sm_count)
 {
     static std::atomic<unsigned long long> raised{0};
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
@@ -896,33 +897,36 @@ static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit);
     }
-    attn_fwd_kernel<DP, F16, MODE><<<grid, kAfThreads, smem, stream>>>(a);
+    attn_fwd_kernel<DP, F16, MODE>
+        <<<attn_ctas(a.units, cap, sm_count), kAfThreads, smem, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.parts == 1) return e;
-    const int64_t blocks = (a.s.row_begin[a.s.W] + 3) / 4;
-    return attn_launch_early(attn_join_kernel<F16>, unsigned(blocks < 1 << 16 ? blocks : 1 << 16), 128,
-                             0, stream, a);
+    int64_t blocks = (a.s.row_begin[a.s.W] + 3) / 4;
+    if (blocks > 1 << 16) blocks = 1 << 16;
+    return attn_launch_early(attn_join_kernel<F16>, unsigned(blocks < cap ? blocks : cap), 128, 0,
+                             stream, a, cap == kAttnMostCtas);
 }
 
 template <int DP, bool F16>
-static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int device, int grid)
+static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int device, int64_t cap,
+                             int sm_count)
 {
     if (a.paired)
         return a.tile_tokens * a.s.group <= kAfTokenRows
-                   ? af_launch_mode<DP, F16, kAfToken>(a, stream, device, grid)
-                   : af_launch_mode<DP, F16, kAfPaired>(a, stream, device, grid);
+                   ? af_launch_mode<DP, F16, kAfToken>(a, stream, device, cap, sm_count)
+                   : af_launch_mode<DP, F16, kAfPaired>(a, stream, device, cap, sm_count);
     if constexpr (DP == 128) {  // (d <= 64 has room for both)
         const int64_t blocks = (a.s.Skv + kAttnRows - 1) / kAttnRows;
         if (blocks <= int64_t(a.s.kv_lens ? kAfShortBlocksRagged : kAfShortBlocks) * a.splits)
-            return af_launch_mode<DP, F16, kAfShort>(a, stream, device, grid);
+            return af_launch_mode<DP, F16, kAfShort>(a, stream, device, cap, sm_count);
     }
-    return af_launch_mode<DP, F16, kAfLong>(a, stream, device, grid);
+    return af_launch_mode<DP, F16, kAfLong>(a, stream, device, cap, sm_count);
 }
 
-// One launch over all ranks (and the join); `grid` CTAs at most. The shape, outputs, parts and
-// their buffers are set in `a`.
+// One launch over all ranks (and the join). The shape, outputs, parts and their buffers are set in
+// `a`.
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
-                            const void* const* v, cudaStream_t stream, int device, int grid,
+                            const void* const* v, cudaStream_t stream, int device, int64_t cap,
                             int sm_count)
 {
     const AttnShape& s = a.s;
@@ -934,12 +938,11 @@ cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* co
             !encode_head_map(&a.vmap[r], v[r], s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows))
             return cudaErrorInvalidValue;
     }
-    grid = int(attn_ctas(a.units, grid, sm_count));
     if (s.d <= 64)
-        return s.f16 ? af_launch<64, true>(a, stream, device, grid)
-                     : af_launch<64, false>(a, stream, device, grid);
-    return s.f16 ? af_launch<128, true>(a, stream, device, grid)
-                 : af_launch<128, false>(a, stream, device, grid);
+        return s.f16 ? af_launch<64, true>(a, stream, device, cap, sm_count)
+                     : af_launch<64, false>(a, stream, device, cap, sm_count);
+    return s.f16 ? af_launch<128, true>(a, stream, device, cap, sm_count)
+                 : af_launch<128, false>(a, stream, device, cap, sm_count);
 }
 
 cudaError_t attn_fwd_status(unsigned* status, bool clear)
