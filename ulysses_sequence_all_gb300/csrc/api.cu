@@ -978,7 +978,7 @@ size_t attn_bwd_setup(AttnBwdArgs* a)
     a->q_order = {heads, a->q_tiles, attn_order_group(heads, s.Skv * s.d * 4)};
     a->kv_order = {heads, (s.Skv + kAttnRows - 1) / kAttnRows,
                    attn_order_group(heads, s.Sq * s.group * s.d * 4)};
-    return size_t(s.head_begin[s.W]) * size_t(a->q_tiles) * 2 * kAttnRows * sizeof(float);
+    return size_t(heads) * size_t(a->q_tiles) * 2 * kAttnRows * sizeof(float) + 16;
 }
 
 int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const* dk,
@@ -1015,6 +1015,7 @@ int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const
     DeviceInfo dev;
     if ((rc = current_device(&dev))) return rc;
     a.stats = static_cast<float*>(workspace);
+    a.ready = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + need - 16);
     for (int r = 0; r < W; ++r) {
         a.o[r] = static_cast<const uint8_t*>(o[r]);
         a.go[r] = static_cast<const uint8_t*>(go[r]);

@@ -123,6 +123,7 @@ struct AttnBwdArgs {
     int64_t q_tiles;              // row tiles along the tokens
     AttnOrder q_order, kv_order;  // (rank, batch, key head) x row tiles, x key blocks
     float* stats;  // [(rank, batch, key head)][q_tiles][2][128]: lse in powers of two, delta
+    uint32_t* ready;  // 0 from the statistics kernel, 1 from dK, dV's once it has seen the statistics
 };
 
 // Host side.

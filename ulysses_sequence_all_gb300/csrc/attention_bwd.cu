@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_consta
     constexpr int kAtOnce = 256 / LANES, kTurns = kAttnRows / 2 / kAtOnce;
     const int sub = threadIdx.x % LANES, slot = threadIdx.x / LANES;
     let_next_start();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ready = 0;
     const int64_t halves = 2 * s.head_begin[s.W] * a.q_tiles;
     for (int64_t at = blockIdx.x; at < halves; at += gridDim.x) {
         const int64_t tile = at >> 1;
@@ -320,10 +321,12 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     }
     if (warp == kAbMmaWarp) tmem_alloc(&bars.tmem);
     wait_for_previous();  // the row statistics
-    let_next_start();     // dQ's CTAs fill the SMs that this kernel has no more units for
+    if (threadIdx.x == 0) release_word(a.ready, 1);
+    fence_proxy_async_global();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    let_next_start();  // dQ's CTAs fill the SMs that this kernel has no more units for
     const uint32_t tmem = bars.tmem;
 
     if (warp == kAbLoadWarp) {
@@ -637,7 +640,7 @@ struct BqBars {
     uint64_t ds_ready, dq_done;            // dS written; summed up
     uint64_t acc_full, acc_free, drain;
     uint32_t tmem;
-    int dead;
+    int dead, seen;
     AbUnitBoard<BqUnit> board;
 };
 static_assert(sizeof(BqBars) <= 1024, "barriers");
@@ -704,12 +707,17 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         ab_board_init(bars.board, s.kv_lens ? 19 : 18);  // warps 0-17, and 18
         mbar_init(&bars.drain, 1);
         bars.dead = 0;
+        // The kernel in front (dK, dV) waited for the statistics before it let this one start. What it
+        // had seen then is seen here through `ready`; if that is not there yet, after its end.
+        bars.seen = acquire_word(a.ready) == 1;
         fence_barrier_init();
     }
     if (warp == kAbMmaWarp) tmem_alloc(&bars.tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (!bars.seen) wait_for_previous();
+    fence_proxy_async_global();
     const uint32_t tmem = bars.tmem;
 
     if (warp == kAbLoadWarp) {
@@ -1017,7 +1025,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             t = next;
         }
     }
-    wait_for_previous();  // dK and dV are done when this kernel is (nothing here needs them)
+    wait_for_previous();  // dK and dV are done when this kernel is (nothing here reads them)
     __syncthreads();
     if (threadIdx.x == 0 && bars.dead) atomicOr(&g_attn_bwd_status, kStatusWaitTimeout);
     if (warp == kAbMmaWarp) tmem_free(tmem);

@@ -229,6 +229,20 @@ __device__ __forceinline__ int64_t stolen_cta(const void* answer)
 // Programmatic launches: what comes before this kernel in its stream (and launched it early) is
 // complete and its writes are visible; the kernel behind it may start where there is room.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A kernel that started early and has not waited yet may see only what it acquires: a word that the
+// kernel in front of it released after its own wait, which carries everything that one had seen.
+__device__ __forceinline__ void release_word(uint32_t* p, uint32_t v)
+{
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t acquire_word(const uint32_t* p)
+{
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+// Orders earlier ordinary accesses to global memory before later tensor and bulk copies of it.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // 2^x (subnormal results flushed to zero).
