@@ -443,8 +443,9 @@ int ulysses_a2a_4d_packed_fused_backward(ulysses_plan_t plan, int planes, int q_
  *   causal   1: query i sees keys j <= q_start[bb] + i only; 0: every key.
  *   q_start  NULL (zeros), or b device int32 (causal only): the position of the first query, such
  *            as the keys already in a cache; negative values hide every key from the first rows.
- * A row that sees no key gives o = 0 and lse = -infinity. Keys hidden from some rows only (causal)
- * must be finite. scale > 0, finite. Products run on the tensor cores in 16 bits (the
+ * A row that sees no key gives o = 0 and lse = -infinity. What k and v hold where no row sees it
+ * (past a key count, or causal past the last query's position) is not used either; keys hidden from
+ * some rows only (causal) must be finite. scale > 0, finite. Products run on the tensor cores in 16 bits (the
  * probabilities are rounded to the element type for the second one), maxima and sums in fp32.
  * workspace  device memory of ulysses_attention_workspace bytes (0: may be NULL), 16-byte aligned:
  *            partial results where few query rows leave the keys to be split over the SMs. Its

@@ -893,6 +893,7 @@ int attn_masks(AttnShape* s, float scale, int causal, const int32_t* kv_lens, co
         return ULY_EALIGN;
     s->scale = scale;
     s->causal = causal;
+    s->ragged = kv_lens || (causal && (q_start || s->Sq < s->Skv)) ? 1 : 0;
     s->kv_lens = kv_lens;
     s->q_start = q_start;
     return ULY_OK;

@@ -33,8 +33,25 @@ struct AttnShape {
     const int32_t* kv_lens;          // (b) or null: keys of each batch element, clamped to [0, Skv]
     const int32_t* q_start;          // (b) or null (zeros): position of the first query, causal only
     int32_t causal;
+    // Whether a block can hold keys that no row sees next to ones that rows do: what they hold is not
+    // used, whatever it is (key counts; causal, keys past the last row's position).
+    int32_t ragged;
     float scale;
 };
+
+#ifdef __CUDACC__
+// Keys of batch element bb that any row sees, and the position of its first query (beyond every key
+// when the mask is not causal).
+__device__ __forceinline__ void attn_limits(const AttnShape& s, int bb, int64_t* len, int64_t* pos0)
+{
+    *len = s.kv_lens ? min(s.Skv, int64_t(max(0, s.kv_lens[bb]))) : s.Skv;
+    *pos0 = s.Skv;
+    if (s.causal) {
+        *pos0 = s.q_start ? int64_t(s.q_start[bb]) : 0;
+        *len = min(*len, max(int64_t(0), *pos0 + s.Sq));
+    }
+}
+#endif
 
 // Order of the units of a kernel: groups of `group` heads, in a group by block (the longest first
 // when they differ), then by head. A group's shared operands fit the L2 cache.

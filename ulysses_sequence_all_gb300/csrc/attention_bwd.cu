@@ -46,14 +46,6 @@ constexpr int kAbLoadWarp = 16, kAbMmaWarp = 17, kAbCleanWarp = 18, kAbUnitWarp 
 constexpr int kAbUnitSlots = 1;
 constexpr int kAbStats = 2 * kAttnRows * 4;  // one tile's lse and D
 
-// Keys that batch element bb holds, and the position of its first query (beyond every key when the
-// mask is not causal).
-__device__ __forceinline__ void ab_limits(const AttnShape& s, int bb, int64_t* len, int64_t* pos0)
-{
-    *len = s.kv_lens ? min(s.Skv, int64_t(max(0, s.kv_lens[bb]))) : s.Skv;
-    *pos0 = s.causal ? (s.q_start ? int64_t(s.q_start[bb]) : 0) : s.Skv;
-}
-
 __device__ __forceinline__ void ab_head(const AttnShape& s, int64_t h, int* r, int* bb, int* kvh)
 {
     int k = 0;
@@ -265,7 +257,7 @@ __device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
     attn_order(a.kv_order, u, &t.h, &block);  // the first keys are seen by the most rows
     t.kv0 = block * kAttnRows;
     ab_head(s, t.h, &t.r, &t.bb, &t.kvh);
-    ab_limits(s, t.bb, &t.len, &t.pos0);
+    attn_limits(s, t.bb, &t.len, &t.pos0);
     // row i sees key kv0 when i >= kv0 - pos0
     const int64_t row = max(int64_t(0), t.kv0 - t.pos0);
     t.first = row / a.tile_tokens;
@@ -653,7 +645,7 @@ __device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
     if (s.causal) t.tile = a.q_tiles - 1 - t.tile;  // the longest rows first
     t.tok0 = t.tile * a.tile_tokens;
     ab_head(s, t.h, &t.r, &t.bb, &t.kvh);
-    ab_limits(s, t.bb, &t.len, &t.pos0);
+    attn_limits(s, t.bb, &t.len, &t.pos0);
     const int64_t last = min(t.tok0 + a.tile_tokens, s.Sq) - 1;
     const int64_t keys = max(int64_t(0), min(t.len, t.pos0 + last + 1));
     t.n = int((keys + kAttnRows - 1) / kAttnRows);
@@ -690,7 +682,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     if (threadIdx.x == 0) {
         for (int k = 0; k < K; ++k) {
             mbar_init(&bars.full[k], 1);
-            mbar_init(&bars.empty[k], s.kv_lens ? 2 : 1);  // the products, and warp 18
+            mbar_init(&bars.empty[k], s.ragged ? 2 : 1);  // the products, and warp 18
             mbar_init(&bars.clean[k], 1);
         }
         mbar_init(&bars.g_full, 1);
@@ -704,7 +696,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.dq_done, 1);
         mbar_init(&bars.acc_full, 1);
         mbar_init(&bars.acc_free, 16);
-        ab_board_init(bars.board, s.kv_lens ? 19 : 18);  // warps 0-17, and 18
+        ab_board_init(bars.board, s.ragged ? 19 : 18);  // warps 0-17, and 18
         mbar_init(&bars.drain, 1);
         bars.dead = 0;
         // The kernel in front (dK, dV) waited for the statistics before it let this one start. What it
@@ -763,7 +755,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         __syncwarp();
     } else if (warp == kAbCleanWarp) {
         // dS is zero past the last key, but zero times what K holds there may be NaN
-        if (s.kv_lens) {
+        if (s.ragged) {
             StageRing ring;
             AbUnits<BqUnit> source{&bars.board, dead};
             BqUnit t;
@@ -861,7 +853,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     if (!end) after = make_s(false, uses);
                     wait(&bars.dp_read, blocks & 1);
                     if (!end) make_dp(false, j + 2 == t.n, uses);
-                    if (s.kv_lens && bq_past(s, t, j) < kAttnRows) {
+                    if (s.ragged && bq_past(s, t, j) < kAttnRows) {
                         wait(&bars.clean[ks], (cleaned >> ks) & 1);
                         cleaned ^= 1u << ks;
                     }

@@ -102,7 +102,7 @@ struct AfUnit {
     int tok0, tok1;  // first token of each tile
     int lo0, lo1;    // first key block of each tile
     int n0, n1;      // key blocks of each tile
-    int len;         // keys of the batch element
+    int len;         // keys of the batch element that any row sees
     int pos0;        // position of query token 0; beyond every key when not causal
     __device__ __forceinline__ int n(int k) const { return k ? n1 : n0; }
     __device__ __forceinline__ int lo(int k) const { return k ? lo1 : lo0; }
@@ -149,9 +149,10 @@ __device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
     const int local = int(h) - s.head_begin[r];
     t.bb = local / s.m[r];
     t.kvh = local - t.bb * s.m[r];
-    t.len = int(s.Skv);
-    if (s.kv_lens) t.len = min(t.len, max(0, s.kv_lens[t.bb]));
-    t.pos0 = s.causal ? (s.q_start ? s.q_start[t.bb] : 0) : int(s.Skv);
+    int64_t len, pos0;
+    attn_limits(s, t.bb, &len, &pos0);
+    t.len = int(len);
+    t.pos0 = int(pos0);
     if (a.paired) {
         t.tok0 = t.tok1 = 0;
         const int total = af_blocks(a, t, 0);
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     if (threadIdx.x == 0) {
         for (int k = 0; k < L::kUnitSlots; ++k) {
             mbar_init(&bars.u_full[k], 1);
-            mbar_init(&bars.u_empty[k], s.kv_lens ? 11 : 10);  // warps 0-9, and 10
+            mbar_init(&bars.u_empty[k], s.ragged ? 11 : 10);  // warps 0-9, and 10
         }
         for (int k = 0; k < Q; ++k) {
             mbar_init(&bars.q_full[k], 1);
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         }
         for (int k = 0; k < K; ++k) {
             mbar_init(&bars.kv_full[k], 1);
-            mbar_init(&bars.kv_empty[k], s.kv_lens ? 2 : 1);  // the products, and warp 10
+            mbar_init(&bars.kv_empty[k], s.ragged ? 2 : 1);  // the products, and warp 10
             mbar_init(&bars.clean[k], 1);
         }
         mbar_init(&bars.drain, 1);
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             for (int64_t k = max(int64_t(0), tiles - Q); k < tiles; ++k)
                 if (!mbar_wait_bounded(&bars.q_full[k % Q], uint32_t((k / Q) & 1)))
                     atomicOr(&g_attn_fwd_status, kStatusDrainTimeout);
-        } else if (warp == kAfCleanWarp && s.kv_lens) {
+        } else if (warp == kAfCleanWarp && s.ragged) {
             // A masked probability is zero, but zero times whatever lies past the last key may be
             // NaN: a value block's rows past it become zeros before its product.
             StageRing ring;
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             auto stage_ready = [&]() { return wait(&bars.kv_full[ring.s], ring.phase); };
             auto values_ready = [&](const AfUnit& t, int at) {
                 stage_ready();
-                if (s.kv_lens && af_past(s, t, at) < kAttnRows) {
+                if (s.ragged && af_past(s, t, at) < kAttnRows) {
                     wait(&bars.clean[ring.s], (cleaned >> ring.s) & 1);
                     cleaned ^= 1u << ring.s;
                 }
