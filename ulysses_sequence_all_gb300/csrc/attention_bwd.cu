@@ -21,8 +21,8 @@
 // while the threads work on the other; a unit's first scores follow the last unit's products
 // without a gap. All accumulators are in tensor memory (fp32); P and dS go back to it rounded to
 // the element type, over the columns they came from, and are A operands there. Warp 18 of the dQ
-// kernel zeroes what a key block holds past a ragged batch element's last key. Warp 19 works out
-// the units ahead.
+// kernel zeroes what a key block holds past a ragged batch element's last key, the one of the dK, dV
+// kernel what rows that see no key hold. Warp 19 works out the units ahead.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_consta
             if (sub == 0) {
                 float* out = a.stats + tile * 2 * kAttnRows + k * kAtOnce + row0;
                 out[0] = lse[k] == -INFINITY ? INFINITY : lse[k] * 1.4426950408889634f;
-                out[kAttnRows] = sum;
+                out[kAttnRows] = lse[k] == -INFINITY ? 0.0f : sum;
             }
         }
     }
@@ -240,6 +240,7 @@ struct BkUnit {
 struct BkBars {
     uint64_t k_full, v_full, k_empty, v_empty;  // key block landed; its last scores have read it
     uint64_t q_full[4], q_empty[4], g_full[4], g_empty[4];
+    uint64_t clean[4];  // rows that see no key zeroed in both tiles
     uint64_t s_full, p_ready, dp_full, ds_ready;
     uint64_t acc_full, acc_free;
     uint64_t drain;
@@ -263,6 +264,15 @@ __device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
     t.first = row / a.tile_tokens;
     t.n = t.kv0 < t.len && t.first < a.q_tiles ? int(a.q_tiles - t.first) : 0;
     return t;
+}
+
+// Rows at the start of a unit's first tile that see no key at all (a start before the first key): their
+// P and dS are zero, but zero times what Q and dO hold there may be NaN. Later tiles have none, and
+// tiles with such rows only are not walked.
+__device__ __forceinline__ int bk_hidden(const AttnBwdArgs& a, const BkUnit& t)
+{
+    const int64_t tokens = -t.pos0 - t.first * a.tile_tokens;
+    return tokens > 0 ? int(min(tokens, int64_t(a.tile_tokens))) * a.s.group : 0;
 }
 
 template <int DP, bool F16>
@@ -289,9 +299,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.v_empty, 1);
         for (int k = 0; k < K; ++k) {
             mbar_init(&bars.q_full[k], 1);
-            mbar_init(&bars.q_empty[k], 1);
+            mbar_init(&bars.q_empty[k], s.q_start ? 2 : 1);  // the products, and warp 18
             mbar_init(&bars.g_full[k], 1);
-            mbar_init(&bars.g_empty[k], 1);
+            mbar_init(&bars.g_empty[k], s.q_start ? 2 : 1);
+            mbar_init(&bars.clean[k], 1);
         }
         mbar_init(&bars.s_full, 1);
         mbar_init(&bars.p_ready, 16);
@@ -299,7 +310,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.ds_ready, 16);
         mbar_init(&bars.acc_full, 1);
         mbar_init(&bars.acc_free, 16);
-        ab_board_init(bars.board, 18);  // warps 0-17
+        ab_board_init(bars.board, s.q_start ? 19 : 18);  // warps 0-17, and 18
         mbar_init(&bars.drain, 1);
         bars.dead = 0;
         fence_barrier_init();
@@ -395,6 +406,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const uint64_t gt_desc = tc_desc_mn(smem_u32(smem + L::kG), L::kHalf);
             StageRing ring;
             uint32_t uses = 0, tiles = 0;
+            uint32_t cleaned = 0;  // parity of each stage's `clean`
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 return ok = ok && wait_or_dead(bar, parity, dead);
@@ -414,10 +426,14 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     tc_mma_ts(tmem + d, tmem + p + (ks >> 1) * 32 + (ks & 1) * 8,
                               row + ks * (2048 >> 4), id_d, !first || ks > 0);
             };
-            // S^T (dP^T) of the ring's next row tile; `first`, `last` of the unit
-            auto next_s = [&](bool first, bool last, uint32_t use) {
+            // S^T (dP^T) of the ring's next row tile; `first`, `last` of unit u
+            auto next_s = [&](bool first, bool last, uint32_t use, const BkUnit& u) {
                 if (first) wait(&bars.k_full, use & 1);
                 if (!wait(&bars.q_full[ring.s], ring.phase)) return;
+                if (first && s.q_start && bk_hidden(a, u) > 0) {
+                    if (!wait(&bars.clean[ring.s], (cleaned >> ring.s) & 1)) return;
+                    cleaned ^= 1u << ring.s;
+                }
                 tc_fence_after();
                 scores(kBkS, k_desc, q_desc + ring.s * (L::kTile >> 4), &bars.s_full);
                 if (last) tc_commit(&bars.k_empty);
@@ -433,7 +449,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             BkUnit t, next;
             bool live = source.next<false>(&t);
             if (live) {
-                next_s(true, t.n == 1, 0);
+                next_s(true, t.n == 1, 0, t);
                 next_dp(true, t.n == 1, 0);
             }
             while (live && ok) {
@@ -450,7 +466,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     tc_fence_after();
                     sums(kBkDv, kBkS, gt_desc + at * (L::kTile >> 4), i == 0);
                     tc_commit(&bars.g_empty[at]);
-                    if (!end || more) next_s(end, last, uses + 1);
+                    if (!end || more) next_s(end, last, uses + 1, next);
                     if (!wait(&bars.ds_ready, tiles & 1)) break;
                     tc_fence_after();
                     sums(kBkDk, kBkDp, qt_desc + at * (L::kTile >> 4), i == 0);
@@ -464,6 +480,41 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             }
             tc_commit(&bars.drain);  // every product complete before tensor memory is given back
             if (!mbar_wait_bounded(&bars.drain, 0)) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
+        }
+        __syncwarp();
+    } else if (warp == kAbCleanWarp) {
+        if (s.q_start) {
+            StageRing ring;
+            AbUnits<BkUnit> source{&bars.board, dead};
+            BkUnit t;
+            bool ok = true;
+            while (ok && source.next<true>(&t)) {
+                for (int i = 0; ok && i < t.n; ++i) {
+                    ok = __all_sync(0xffffffffu, wait_or_dead(&bars.q_full[ring.s], ring.phase, dead));
+                    ok = ok &&
+                         __all_sync(0xffffffffu, wait_or_dead(&bars.g_full[ring.s], ring.phase, dead));
+                    if (!ok) break;
+                    const int hidden = i == 0 ? bk_hidden(a, t) : 0;
+                    if (hidden > 0) {
+                        for (int h = 0; h < halves; ++h)
+                            for (int w = lane; w < hidden * 8; w += 32) {
+                                const int at = ring.s * L::kTile + h * L::kHalf + w * 16;
+                                st_shared_v4(smem + L::kQ + at, make_uint4(0, 0, 0, 0));
+                                st_shared_v4(smem + L::kG + at, make_uint4(0, 0, 0, 0));
+                            }
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.clean[ring.s]);
+                    }
+                    // every stage waits for this warp, so that it neither runs ahead of the ring
+                    // nor falls a turn behind
+                    if (lane == 0) {
+                        mbar_arrive(&bars.q_empty[ring.s]);
+                        mbar_arrive(&bars.g_empty[ring.s]);
+                    }
+                    ring.next(K);
+                }
+            }
         }
         __syncwarp();
     } else if (warp == kAbUnitWarp) {
