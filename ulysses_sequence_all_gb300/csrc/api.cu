@@ -969,8 +969,8 @@ int attn_fwd_device(const Plan& qp, const Plan& kp, const void* const* q, const 
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
 
-// Tiles of a backward call and the bytes of its workspace.
-size_t attn_bwd_setup(AttnBwdArgs* a)
+// Tiles of a backward call, the bytes of its workspace and the places in it.
+size_t attn_bwd_setup(AttnBwdArgs* a, void* workspace)
 {
     const AttnShape& s = a->s;
     a->tile_tokens = kAttnRows / s.group;
@@ -979,7 +979,22 @@ size_t attn_bwd_setup(AttnBwdArgs* a)
     a->q_order = {heads, a->q_tiles, attn_order_group(heads, s.Skv * s.d * 4)};
     a->kv_order = {heads, (s.Skv + kAttnRows - 1) / kAttnRows,
                    attn_order_group(heads, s.Sq * s.group * s.d * 4)};
-    return size_t(heads) * size_t(a->q_tiles) * 2 * kAttnRows * sizeof(float) + 16;
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    size_t at = 0;
+    auto place = [&](size_t bytes) {
+        uint8_t* p = base ? base + at : nullptr;
+        at += (bytes + 15) & ~size_t(15);
+        return p;
+    };
+    const size_t tiles = size_t(heads) * size_t(a->q_tiles);
+    a->stats = reinterpret_cast<float*>(place(tiles * (s.f16 ? 3 : 2) * kAttnRows * sizeof(float)));
+    if (s.f16) {
+        a->row_bounds = reinterpret_cast<float2*>(place(tiles * 2 * sizeof(float2)));
+        a->key_norms = reinterpret_cast<float*>(
+            place(size_t(heads) * size_t(a->kv_order.blocks) * sizeof(float)));
+    }
+    a->ready = reinterpret_cast<uint32_t*>(place(sizeof(uint32_t)));
+    return at;
 }
 
 int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const* dk,
@@ -1008,18 +1023,17 @@ int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const
         return rc;
     ins.add(kv_lens, qp.b * 4);
     ins.add(q_start, qp.b * 4);
-    const size_t need = attn_bwd_setup(&a);
+    const size_t need = attn_bwd_setup(&a, workspace);
     if (!workspace || workspace_bytes < need) return ULY_EINVAL;
     if (!aligned16(workspace)) return ULY_EALIGN;
     outs.add(workspace, int64_t(need));
     if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
     DeviceInfo dev;
     if ((rc = current_device(&dev))) return rc;
-    a.stats = static_cast<float*>(workspace);
-    a.ready = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + need - 16);
     for (int r = 0; r < W; ++r) {
         a.o[r] = static_cast<const uint8_t*>(o[r]);
         a.go[r] = static_cast<const uint8_t*>(go[r]);
+        a.v[r] = static_cast<const uint8_t*>(v[r]);
         a.lse[r] = lse[r];
         a.dq[r] = static_cast<uint8_t*>(dq[r]);
         a.dk[r] = static_cast<uint8_t*>(dk[r]);
@@ -1360,7 +1374,7 @@ int ulysses_attention_backward_workspace(ulysses_plan_t q_plan, ulysses_plan_t k
     std::memset(&a, 0, sizeof a);
     const int rc = attn_shape(q_plan->p, kv_plan->p, &a.s);
     if (rc) return rc;
-    *bytes = attn_bwd_setup(&a);
+    *bytes = attn_bwd_setup(&a, nullptr);
     return ULY_OK;
 }
 

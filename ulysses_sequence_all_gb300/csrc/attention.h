@@ -21,6 +21,7 @@ namespace uly {
 constexpr int kAttnMaxD = 128;
 constexpr int kAttnMaxGroup = 64;  // query heads that share a key head
 constexpr int kAttnRows = 128;     // rows of a query tile, and keys of a block
+constexpr int kAttnPBits = 14;     // fp16 probabilities of the backward are held times 2^this
 
 // What every attention kernel needs to know of the call.
 struct AttnShape {
@@ -132,6 +133,7 @@ struct AttnBwdArgs {
     CUtensorMap kmap[kMaxW], vmap[kMaxW];  // boxes of a key block
     const uint8_t* o[kMaxW];
     const uint8_t* go[kMaxW];
+    const uint8_t* v[kMaxW];
     const float* lse[kMaxW];
     uint8_t* dq[kMaxW];
     uint8_t* dk[kMaxW];
@@ -139,7 +141,11 @@ struct AttnBwdArgs {
     int32_t tile_tokens;
     int64_t q_tiles;              // row tiles along the tokens
     AttnOrder q_order, kv_order;  // (rank, batch, key head) x row tiles, x key blocks
-    float* stats;  // [(rank, batch, key head)][q_tiles][2][128]: lse in powers of two, delta
+    // [(rank, batch, key head)][q_tiles][2][128]: lse in powers of two, delta; fp16 [3][128], the lse
+    // less kAttnPBits, and |dO|
+    float* stats;
+    float2* row_bounds;  // fp16: [(rank, batch, key head)][q_tiles][2]: largest |dO|, |delta| of half a tile
+    float* key_norms;    // fp16: [(rank, batch, key head)][key blocks]: largest |v|
     uint32_t* ready;  // 0 from the statistics kernel, 1 from dK, dV's once it has seen the statistics
 };
 

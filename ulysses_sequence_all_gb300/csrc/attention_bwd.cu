@@ -5,7 +5,8 @@
 // query heads sum over them. Five products of 2 d flops per (row, key) cannot be done without.
 //
 // Three launches. attn_bwd_stats_kernel writes each row's lse (in powers of two; +infinity where a
-// row sees nothing or does not exist, which makes its P zero) and D in row-tile order. Then
+// row sees nothing or does not exist, which makes its P zero) and D in row-tile order, with fp16 the
+// norms that give P and dS their place in its range as well (see ab_exponent). Then
 // attn_bwd_kv_kernel holds a block of 128 keys and walks the row tiles that see it (dK, dV), and
 // attn_bwd_q_kernel holds a tile of 128 rows and walks its key blocks (dQ). S and dP are computed
 // by both, seven products in place of five: dQ is then summed in one accumulator in a fixed order,
@@ -23,6 +24,8 @@
 // the element type, over the columns they came from, and are A operands there. Warp 18 of the dQ
 // kernel zeroes what a key block holds past a ragged batch element's last key, the one of the dK, dV
 // kernel what rows that see no key hold. Warp 19 works out the units ahead.
+// Roundings: P and dS to the element type (relative errors of half a step each, in sums of either
+// sign), the gradients once; every sum, the statistics and the exponents are fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -45,6 +48,8 @@ constexpr int kAbLoadWarp = 16, kAbMmaWarp = 17, kAbCleanWarp = 18, kAbUnitWarp 
 // Units known ahead of the slowest reader: one, so that CTAs do not pile up units others could take.
 constexpr int kAbUnitSlots = 1;
 constexpr int kAbStats = 2 * kAttnRows * 4;  // one tile's lse and D
+template <bool F16>
+constexpr int kAbStatArrays = F16 ? 3 : 2;  // a tile's arrays of row statistics
 
 __device__ __forceinline__ void ab_head(const AttnShape& s, int64_t h, int* r, int* bb, int* kvh)
 {
@@ -56,13 +61,38 @@ __device__ __forceinline__ void ab_head(const AttnShape& s, int64_t h, int* r, i
     *kvh = local - *bb * s.m[k];
 }
 
-// Half a tile of rows a CTA; LANES lanes a row, 8 columns each. Bound by reading O and dO.
+// The largest of all threads' values (256 of them), in every thread.
+__device__ __forceinline__ float ab_block_max(float x, float* shared)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = shared[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) x = fmaxf(x, shared[w]);
+    return x;
+}
+
+// Sum over the LANES lanes of a row.
+template <int LANES>
+__device__ __forceinline__ float ab_row_sum(float x)
+{
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
+// Half a tile of rows a CTA; LANES lanes a row, 8 columns each. Bound by reading O and dO. With fp16
+// also the largest |v| of each block of keys, and what else bounds dS (see ab_exponent).
 template <bool F16, int LANES>
 __global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_constant__ AttnBwdArgs a)
 {
     using E = ElemT<F16>;
     const AttnShape& s = a.s;
     constexpr int kAtOnce = 256 / LANES, kTurns = kAttnRows / 2 / kAtOnce;
+    __shared__ float shared[8];
     const int sub = threadIdx.x % LANES, slot = threadIdx.x / LANES;
     let_next_start();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ready = 0;
@@ -93,27 +123,91 @@ __global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_consta
             }
             if (valid[k] && sub == 0) lse[k] = a.lse[r][(int64_t(bb) * s.n[r] + head) * s.Sq + tok];
         }
+        float most_g = 0.0f, most_d = 0.0f;
 #pragma unroll
         for (int k = 0; k < kTurns; ++k) {
             const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             const uint32_t ys[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
-            float sum = 0.0f;
+            float sum = 0.0f, square = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 sum = fmaf(E::lo(xs[i]), E::lo(ys[i]), sum);
                 sum = fmaf(E::hi(xs[i]), E::hi(ys[i]), sum);
+                if (F16) {
+                    square = fmaf(E::lo(ys[i]), E::lo(ys[i]), square);
+                    square = fmaf(E::hi(ys[i]), E::hi(ys[i]), square);
+                }
             }
-#pragma unroll
-            for (int off = LANES / 2; off > 0; off >>= 1)
-                sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            sum = ab_row_sum<LANES>(sum);
+            if (F16) square = ab_row_sum<LANES>(square);
             if (sub == 0) {
-                float* out = a.stats + tile * 2 * kAttnRows + k * kAtOnce + row0;
-                out[0] = lse[k] == -INFINITY ? INFINITY : lse[k] * 1.4426950408889634f;
-                out[kAttnRows] = lse[k] == -INFINITY ? 0.0f : sum;
+                const bool none = lse[k] == -INFINITY;
+                const float z = lse[k] * 1.4426950408889634f;
+                float* out = a.stats + tile * kAbStatArrays<F16> * kAttnRows + k * kAtOnce + row0;
+                out[0] = none ? INFINITY : F16 ? z - kAttnPBits : z;
+                out[kAttnRows] = none ? 0.0f : sum;
+                if (F16) {
+                    const float norm = none ? 0.0f : sqrtf(square);
+                    out[2 * kAttnRows] = norm;
+                    most_g = fmaxf(most_g, norm);
+                    most_d = fmaxf(most_d, none ? 0.0f : fabsf(sum));
+                }
             }
         }
+        if (F16) {
+            most_g = ab_block_max(most_g, shared);
+            most_d = ab_block_max(most_d, shared);
+            if (threadIdx.x == 0) a.row_bounds[at] = make_float2(most_g, most_d);
+        }
+    }
+    if (!F16) return;
+    const int64_t blocks = a.kv_order.blocks, all = s.head_begin[s.W] * blocks;
+    // (the CTAs after those with rows first)
+    const int64_t from = (halves + gridDim.x - 1 - blockIdx.x) / gridDim.x * gridDim.x + blockIdx.x;
+    for (int64_t at = from - halves; at < all; at += gridDim.x) {
+        const int64_t h = div_fast(at, blocks), block = at - h * blocks;
+        int r, bb, kvh;
+        ab_head(s, h, &r, &bb, &kvh);
+        int64_t len, pos0;
+        attn_limits(s, bb, &len, &pos0);
+        uint4 v[2 * kTurns];
+#pragma unroll
+        for (int k = 0; k < 2 * kTurns; ++k) {
+            const int64_t key = block * kAttnRows + k * kAtOnce + slot;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (key < len && sub * 8 < s.d)
+                v[k] = ld_stream_v4(a.v[r] + ((int64_t(bb) * s.Skv + key) * s.m[r] + kvh) * s.d * 2 +
+                                    sub * 16);
+        }
+        float most = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2 * kTurns; ++k) {
+            const uint32_t vs[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            float square = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                square = fmaf(E::lo(vs[i]), E::lo(vs[i]), square);
+                square = fmaf(E::hi(vs[i]), E::hi(vs[i]), square);
+            }
+            most = fmaxf(most, ab_row_sum<LANES>(square));
+        }
+        most = ab_block_max(most, shared);
+        if (threadIdx.x == 0) a.key_norms[at] = sqrtf(most);
     }
 }
+
+// fp16 holds its 11 bits between 6e-5 and 65,504 only, and dS = P (dP - D) is as small as 1 / keys times
+// dO, or as large as dO v. So it is held times a power of two that a bound gives it:
+// |dP_ij - D_i| <= |dO_i| |v_j| + |D_i|, and P <= 1. dQ's rows have one each, dK's sums run over rows
+// and have one a unit (a key block with all the rows that see it); the gradients' last factor takes it
+// out again. The exponent with bound 2^e below 2^15 (a zero bound, or one of infinities: any will do).
+__device__ __forceinline__ int ab_exponent(float bound)
+{
+    const int x = (__float_as_int(bound) >> 23) - 127;
+    return 14 - max(-80, min(x, 60));
+}
+
+__device__ __forceinline__ float ab_power(int e) { return __int_as_float((e + 127) << 23); }
 
 // P (dP - D) of two columns; d is -D.
 __device__ __forceinline__ float2 ab_ds(uint32_t p0, uint32_t p1, uint32_t y0, uint32_t y1, float2 d)
@@ -233,6 +327,7 @@ struct BkSmem {
 
 struct BkUnit {
     int r, bb, kvh, n;       // n: row tiles from `first` on that see the block
+    int e;                   // fp16: dS is held times 2^e
     int64_t h, kv0, first;
     int64_t len, pos0;
 };
@@ -250,6 +345,7 @@ struct BkBars {
 };
 static_assert(sizeof(BkBars) <= 1024, "barriers");
 
+template <bool F16>  // called by a whole warp
 __device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
 {
     const AttnShape& s = a.s;
@@ -263,6 +359,22 @@ __device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
     const int64_t row = max(int64_t(0), t.kv0 - t.pos0);
     t.first = row / a.tile_tokens;
     t.n = t.kv0 < t.len && t.first < a.q_tiles ? int(a.q_tiles - t.first) : 0;
+    t.e = 0;
+    if (F16 && t.n > 0) {
+        const float2* rows = a.row_bounds + (t.h * a.q_tiles + t.first) * 2;
+        float2 most = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+        for (int64_t i = threadIdx.x & 31; i < 2 * int64_t(t.n); i += 32) {
+            const float2 x = rows[i];
+            most = make_float2(fmaxf(most.x, x.x), fmaxf(most.y, x.y));
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            most.x = fmaxf(most.x, __shfl_xor_sync(0xffffffffu, most.x, off));
+            most.y = fmaxf(most.y, __shfl_xor_sync(0xffffffffu, most.y, off));
+        }
+        t.e = ab_exponent(most.x * a.key_norms[t.h * a.kv_order.blocks + block] + most.y);
+    }
     return t;
 }
 
@@ -362,7 +474,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     if (!ok) break;
                     mbar_arrive_expect_tx(&bars.q_full[ring.s], q_bytes + kAbStats);
                     bulk_g2s(smem + L::kStat + ring.s * kAbStats,
-                             a.stats + (t.h * a.q_tiles + tile) * 2 * kAttnRows, kAbStats,
+                             a.stats + (t.h * a.q_tiles + tile) * kAbStatArrays<F16> * kAttnRows,
+                             kAbStats,
                              &bars.q_full[ring.s]);
                     for (int h = 0; h < halves; ++h)
                         tensor_g2s_4d(smem + L::kQ + ring.s * L::kTile + h * L::kHalf, &a.qmap[t.r],
@@ -519,7 +632,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         __syncwarp();
     } else if (warp == kAbUnitWarp) {
         ab_publish<BkUnit>(
-            bars.board, units, dead, [&](int64_t u) { return bk_unit(a, u); },
+            bars.board, units, dead, [&](int64_t u) { return bk_unit<F16>(a, u); },
             [&](const BkUnit& t) {  // keys that no row sees
                 for (int i = lane; i < 2 * kAttnRows; i += 32) {
                     const int64_t key = t.kv0 + i % kAttnRows;
@@ -556,6 +669,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             // tile_tokens * group columns earlier
             int64_t lo = (key - t.pos0 - t.first * a.tile_tokens) * s.group - 32 * wg;
             if (key >= t.len) lo = int64_t(1) << 40;
+            const float2 ds2 = make_float2(ab_power(t.e - kAttnPBits), ab_power(t.e - kAttnPBits));
             for (int i = 0; i < t.n; ++i, lo -= a.tile_tokens * s.group) {
                 const int from = int(max(int64_t(-1), min(lo, int64_t(32))));
                 ok = all(&bars.q_full[ring.s], ring.phase);  // the tile's lse and D
@@ -605,10 +719,14 @@ __global__ void __launch_bounds__(kAbThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const float4 dd = d4[c];
-                    const float2 v = ab_ds(x[4 * c], x[4 * c + 1], y[4 * c], y[4 * c + 1],
-                                           make_float2(-dd.x, -dd.y));
-                    const float2 w = ab_ds(x[4 * c + 2], x[4 * c + 3], y[4 * c + 2], y[4 * c + 3],
-                                           make_float2(-dd.z, -dd.w));
+                    float2 v = ab_ds(x[4 * c], x[4 * c + 1], y[4 * c], y[4 * c + 1],
+                                     make_float2(-dd.x, -dd.y));
+                    float2 w = ab_ds(x[4 * c + 2], x[4 * c + 3], y[4 * c + 2], y[4 * c + 3],
+                                     make_float2(-dd.z, -dd.w));
+                    if (F16) {
+                        v = __fmul2_rn(v, ds2);
+                        w = __fmul2_rn(w, ds2);
+                    }
                     p[2 * c] = E::pack(v.x, v.y);
                     p[2 * c + 1] = E::pack(w.x, w.y);
                 }
@@ -630,7 +748,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             tc_fence_after();
             uint8_t* out = (wg >= 2 ? a.dv[t.r] : a.dk[t.r]) +
                            ((int64_t(t.bb) * s.Skv + key) * s.m[t.r] + t.kvh) * s.d * 2;
-            const float f = wg >= 2 ? 1.0f : s.scale;
+            const float f = wg >= 2 ? (F16 ? ab_power(-kAttnPBits) : 1.0f)
+                                    : (F16 ? s.scale * ab_power(-t.e) : s.scale);
             constexpr int kCols = DP / 2;
 #pragma unroll
             for (int c = 0; c < kCols / 32; ++c) {
@@ -672,6 +791,7 @@ struct BqSmem {
 
 struct BqUnit {
     int r, bb, kvh, n;  // n: key blocks that the tile sees
+    float norm;         // fp16: the largest |v| in them
     int64_t h, tile, tok0, len, pos0;
 };
 
@@ -688,6 +808,7 @@ struct BqBars {
 };
 static_assert(sizeof(BqBars) <= 1024, "barriers");
 
+template <bool F16>  // called by a whole warp
 __device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
 {
     const AttnShape& s = a.s;
@@ -700,6 +821,15 @@ __device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
     const int64_t last = min(t.tok0 + a.tile_tokens, s.Sq) - 1;
     const int64_t keys = max(int64_t(0), min(t.len, t.pos0 + last + 1));
     t.n = int((keys + kAttnRows - 1) / kAttnRows);
+    t.norm = 0.0f;
+    if (F16) {
+        const float* norms = a.key_norms + t.h * a.kv_order.blocks;
+#pragma unroll 4
+        for (int i = threadIdx.x & 31; i < t.n; i += 32) t.norm = fmaxf(t.norm, norms[i]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            t.norm = fmaxf(t.norm, __shfl_xor_sync(0xffffffffu, t.norm, off));
+    }
     return t;
 }
 
@@ -938,7 +1068,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         __syncwarp();
     } else if (warp == kAbUnitWarp) {
         ab_publish<BqUnit>(
-            bars.board, units, dead, [&](int64_t u) { return bq_unit(a, u); },
+            bars.board, units, dead, [&](int64_t u) { return bq_unit<F16>(a, u); },
             [&](const BqUnit& t) {  // rows that see no key
                 for (int i = lane; i < kAttnRows; i += 32) {
                     const int tok_in = i / s.group;
@@ -995,8 +1125,15 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         while (live && ok) {
             const int64_t tok = t.tok0 + tok_in;
             const bool valid = tok_in < a.tile_tokens && tok < s.Sq;
-            const float* stat = a.stats + (t.h * a.q_tiles + t.tile) * 2 * kAttnRows + row;
-            const float z = -stat[0], delta = stat[kAttnRows];
+            const float* stat =
+                a.stats + (t.h * a.q_tiles + t.tile) * kAbStatArrays<F16> * kAttnRows + row;
+            float z = -stat[0], f = s.scale;
+            const float delta = stat[kAttnRows];
+            if (F16) {
+                const int e = ab_exponent(fmaf(stat[2 * kAttnRows], t.norm, fabsf(delta)));
+                z += float(e - kAttnPBits);
+                f *= ab_power(-e);
+            }
             int64_t left = min(t.len, t.pos0 + tok + 1) - 32 * wg;  // visible keys from here on
             for (int j = 0; j < t.n; ++j, ++blocks, left -= kAttnRows) {
                 const int seen = int(max(int64_t(0), min(left, int64_t(32))));
@@ -1063,7 +1200,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 tmem_ld16(tmem + lanes + kBqDq + wg * kCols, y);
             tmem_wait_ld(y);
             arrive(&bars.acc_free);
-            if (valid) ab_store<E>(out, wg * kCols, s.d, y, s.scale);
+            if (valid) ab_store<E>(out, wg * kCols, s.d, y, f);
             ++uses;
             t = next;
         }
@@ -1092,7 +1229,7 @@ static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int devi
         raised.fetch_or(bit);
     }
     const int64_t heads = a.q_order.heads;
-    const int64_t parts = 2 * heads * a.q_tiles;
+    const int64_t parts = 2 * heads * a.q_tiles + (F16 ? heads * a.kv_order.blocks : 0);
     const bool early = cap == kAttnMostCtas;  // (two at a time together would pass a cap)
     attn_bwd_stats_kernel<F16, DP / 8><<<unsigned(parts < cap ? parts : cap), 256, 0, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
