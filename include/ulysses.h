@@ -470,9 +470,9 @@ int ulysses_attention_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, s
  * summed over the query heads of a shared key head, each rounded once. dq, dk, dv are shaped as q,
  * k, v and written whole: keys that no row sees and rows that see no key get zeros. The plans,
  * masks and scale are the forward's, o and lse its outputs, go the gradient of o; rows that see no
- * key have no gradient, whatever q and go hold there. P and dS are rounded to the element type for their products
- * (fp16: times powers of two that keep them inside its range, whatever the size of go and the number
- * of keys), the sums are fp32 and in a fixed order: the same bits from run to run.
+ * key have no gradient, whatever q and go hold there. P and dS are rounded to the element type for
+ * their products (fp16: times powers of two that keep them inside its range, whatever the size of go
+ * and the number of keys), the sums are fp32 and in a fixed order: the same bits from run to run.
  * workspace: device memory of ulysses_attention_backward_workspace bytes, 16-byte aligned; its
  * content does not matter and is not kept.
  * Three launches on `stream`, under q_plan's CTA cap as the forward's. Statuses as the forward's.

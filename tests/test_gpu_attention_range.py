@@ -9,6 +9,7 @@ test_gpu_attention_backward.py), dP and D to 2^-20 of the magnitudes that they s
 import pytest
 import torch
 
+from attention_reference import forward
 from test_gpu_attention_backward import check, given, gradients, plans
 from ulysses_sequence_all_gb300 import binding as B
 
@@ -119,3 +120,28 @@ def test_rows_of_different_sizes(d):
     got = gradients(qp, kp, q, k, v, o, lse, go, 0.125)
     compare(got, q, k, v, o, lse, go, 0.125, rows=slice(0, None, 2))
     compare(got, q, k, v, o, lse, go, 0.125, rows=slice(1, None, 2))
+
+
+@pytest.mark.parametrize("lead", [17.5, 18.5])
+@pytest.mark.parametrize("d", [64, 128])
+def test_forward_small_weights_together(d, lead):
+    """One key with most of the weight and 60,000 with about e^-lead of it each, all under one running
+    maximum: together they are the output, although fp16 rounds each to nothing beside a 1. Bound: half
+    a step for the result and for each probability, 1e-4 for scores and sums, 1e-4 for what the roundings
+    of probabilities at 2^-18 leave on average; and the tensor cores cut their fp32 sums off instead of
+    rounding them, by less than 2^-23 of the sum for every 16 keys."""
+    n, sq, g = 60_000, 700, 64
+    qp, kp = plans(1, 1, sq, n, [1], g, d, torch.float16)
+    rnd = rand(7)
+    q, k, v = rnd(0.2, 1, sq, g, d), rnd(0.2, 1, n, 1, d), 1 + rnd(0.1, 1, n, 1, d)
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    k[:, 1000], v[:, 1000] = 0.0, 0.0
+    k[:, 1000, :, 0] = lead / 8
+    assert B.ulysses_attention_workspace(qp, kp) == 0  # not split: the parts would have maxima of their own
+    o, lse = torch.empty_like(q), torch.empty(1, g, sq, device="cuda")
+    B.ulysses_attention(qp, kp, [q], [k], [v], [o], [lse], scale=1.0)
+    want, z, _ = forward(q[:, :3], k, v, 1.0)
+    assert 3e-4 < want.mean() < 3e-3
+    err = ((o[:, :3].double() - want).abs() / want.abs()).max().item()
+    assert err <= 2 * U + 2e-4 + n / 16 * 2.0 ** -23, err
+    assert (lse[:, :, :3].double() - z).abs().max() < 3e-5 + 2.0 ** -22 * 20
