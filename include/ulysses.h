@@ -520,7 +520,8 @@ int ulysses_a2a_4d_qk_fused_host(ulysses_plan_t plan, const void* const* q_host_
 
 /* Synchronise the current device, then return in *status the device status word accumulated by
  * this library's kernels since the last call (0 = no kernel timed out) and clear it. Returns
- * ULY_EDEVICE when the word was non-zero. Bits: 1 (a pipeline wait gave up after 2 s: the
+ * ULY_EDEVICE when the word was non-zero. Bits: 1 (a pipeline wait gave up after 2 s, in the
+ * attention kernels 2 s in which nothing moved: the
  * outputs of the calls since the last check are incomplete; discard them), 2 (a kernel gave up
  * waiting for its own bulk copies into shared memory before exiting: such a copy never completed,
  * so it may still land in shared memory a later kernel owns; discard the outputs and treat the
@@ -536,6 +537,15 @@ int ulysses_device_status(unsigned* status);
  * so the context stays usable; ulysses_device_status() then reports ULY_EDEVICE with status 1.
  */
 int ulysses_selftest_wait_timeout(unsigned limit_us, void* stream);
+
+/*
+ * Self-test of the attention kernels' failure path: calls that this process makes from now on have a
+ * limit of limit_us microseconds (0 .. 2,000,000, the default) on a wait in which nothing moves; with 0
+ * a wait gives up at its second look, some ten microseconds in, so that any call with long units gives
+ * up at once: its kernels set the timeout bit (1) of the device status word, leave outputs unwritten and
+ * return normally. Set it back to 2,000,000 afterwards.
+ */
+int ulysses_selftest_attention_wait_limit(unsigned limit_us);
 
 /* The cudaError_t value of the last ULY_ECUDA returned on this host thread (0 if none). */
 int ulysses_last_cuda_error(void);

@@ -40,7 +40,8 @@ EXPORTS = ["ulysses_plan", "ulysses_plan_destroy", "ulysses_plan_set_chunk_bytes
            "ulysses_attention", "ulysses_attention_workspace",
            "ulysses_attention_backward", "ulysses_attention_backward_workspace",
            "ulysses_a2a_4d_host", "ulysses_a2a_4d_qk_fused_host", "ulysses_device_status",
-           "ulysses_selftest_wait_timeout", "ulysses_last_cuda_error", "ulysses_strerror",
+           "ulysses_selftest_wait_timeout", "ulysses_selftest_attention_wait_limit",
+           "ulysses_last_cuda_error", "ulysses_strerror",
            "ulysses_version"]
 
 
@@ -120,6 +121,7 @@ def _lib():
                                                      ctypes.c_float, ctypes.c_float, _p]
         lib.ulysses_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint)]
         lib.ulysses_selftest_wait_timeout.argtypes = [ctypes.c_uint, _p]
+        lib.ulysses_selftest_attention_wait_limit.argtypes = [ctypes.c_uint]
         lib.ulysses_last_cuda_error.argtypes = []
         lib.ulysses_strerror.argtypes = [ctypes.c_int]
         lib.ulysses_strerror.restype = ctypes.c_char_p
@@ -463,6 +465,13 @@ def ulysses_selftest_wait_timeout(limit_us: int, stream=None):
     """Queue the failure-path self-test kernel (a wait that must time out after limit_us)."""
     _check(_lib().ulysses_selftest_wait_timeout(limit_us, _stream(stream)),
            "ulysses_selftest_wait_timeout")
+
+
+def ulysses_selftest_attention_wait_limit(limit_us: int):
+    """Limit of a wait in the attention kernels in which nothing moves, for calls from now on (0: give
+    up at once; 2,000,000: the default)."""
+    _check(_lib().ulysses_selftest_attention_wait_limit(limit_us),
+           "ulysses_selftest_attention_wait_limit")
 
 
 def ulysses_strerror(status: int) -> str:

@@ -14,6 +14,7 @@
 #include "../../include/ulysses.h"
 #include "attention.h"
 #include "plan.h"
+#include "ptx.cuh"
 #include "tensor_map.h"
 
 namespace uly {
@@ -832,6 +833,9 @@ int run_host_pipe(const Plan& p, const PipeChunks& pc, HostPipe* hp, cudaStream_
 }
 
 // ---- attention ----------------------------------------------------------------------------------
+constexpr uint32_t kAttnWaitUs = uint32_t(kWaitLimitNs / 1000);
+std::atomic<uint32_t> attention_wait_us{kAttnWaitUs};  // of launches from now on (self-test)
+
 // What the two plans of an attention call make together, or ULY_EINVAL.
 int attn_shape(const Plan& qp, const Plan& kp, AttnShape* s)
 {
@@ -840,8 +844,7 @@ int attn_shape(const Plan& qp, const Plan& kp, AttnShape* s)
     if (kp.N == 0 || qp.N % kp.N != 0) return ULY_EINVAL;
     const int64_t group = qp.N / kp.N;
     if (group > kAttnMaxGroup) return ULY_EINVAL;
-    // A unit walks all of Skv, or all Sq * group rows: 2^26 keep it well inside the kernels' limit
-    // on a wait for a unit's end (and every coordinate in 32 bits).
+    // Every coordinate, and a unit's count of rows or keys, stays well inside 32 bits.
     const int64_t lim = int64_t(1) << 26;
     if (qp.S > lim / group || kp.S > lim || qp.b * kp.N >= (int64_t(1) << 31)) return ULY_EINVAL;
     std::memset(s, 0, sizeof *s);
@@ -892,6 +895,7 @@ int attn_masks(AttnShape* s, float scale, int causal, const int32_t* kv_lens, co
     if ((reinterpret_cast<uintptr_t>(kv_lens) | reinterpret_cast<uintptr_t>(q_start)) & 3u)
         return ULY_EALIGN;
     s->scale = scale;
+    s->wait_us = attention_wait_us.load(std::memory_order_relaxed);
     s->causal = causal;
     s->ragged = kv_lens || (causal && (q_start || s->Sq < s->Skv)) ? 1 : 0;
     s->kv_lens = kv_lens;
@@ -1500,6 +1504,13 @@ int ulysses_selftest_wait_timeout(unsigned limit_us, void* stream)
     if (limit_us < 1 || limit_us > 1000000u) return ULY_EINVAL;
     cudaError_t e = selftest_timeout_launch(uint64_t(limit_us) * 1000u, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
+}
+
+int ulysses_selftest_attention_wait_limit(unsigned limit_us)
+{
+    if (limit_us > kAttnWaitUs) return ULY_EINVAL;
+    attention_wait_us.store(limit_us, std::memory_order_relaxed);
+    return ULY_OK;
 }
 
 int ulysses_last_cuda_error(void) { return t_last_cuda_error; }

@@ -37,6 +37,7 @@ struct AttnShape {
     // Whether a block can hold keys that no row sees next to ones that rows do: what they hold is not
     // used, whatever it is (key counts; causal, keys past the last row's position).
     int32_t ragged;
+    uint32_t wait_us;  // limit of a wait in which nothing moves (CtaLife)
     float scale;
 };
 
@@ -71,7 +72,7 @@ __device__ __forceinline__ void attn_order(const AttnOrder& o, int64_t u, int64_
     *head = g * o.group + (at - *block * heads);
 }
 
-// A CTA's units, asked for by one whole warp. A grid of one CTA per unit (gridDim.x == units): its
+// A CTA's units, asked for by one whole warp, the one that watches (CtaLife). A grid of one CTA per unit (gridDim.x == units): its
 // own, then those of CTAs that have not started, which it takes their place of as it gets there, so
 // that long and short units even out. A smaller grid (a CTA cap): every gridDim.x-th unit, back and
 // forth, which evens out units whose length falls along the order.
@@ -79,7 +80,7 @@ struct AttnUnitSource {
     int64_t units;
     void* answer;     // 16 bytes of shared memory
     uint64_t* bar;    // counts the answer; initialised for one arrival
-    volatile int* dead;
+    volatile CtaLife* life;
     int64_t wave = 0;
     uint32_t phase = 0;
     bool over = false;
@@ -102,7 +103,9 @@ struct AttnUnitSource {
             steal_cta(answer, bar);
         }
         __syncwarp();
-        const bool ok = __all_sync(0xffffffffu, wait_or_dead(bar, phase, dead));
+        const bool ok = __all_sync(0xffffffffu, wait_watching(bar, phase, life));
+        // (an answer on its way lands before this CTA's shared memory may be another's)
+        if (!ok && !mbar_wait_bounded(bar, phase)) life->stuck = 1;
         phase ^= 1u;
         const int64_t u = ok ? stolen_cta(answer) : -1;
         __syncwarp();

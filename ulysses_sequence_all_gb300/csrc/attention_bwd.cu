@@ -254,13 +254,13 @@ __device__ __forceinline__ void ab_board_init(AbUnitBoard<Unit>& b, int readers)
 template <class Unit>
 struct AbUnits {
     AbUnitBoard<Unit>* board;
-    volatile int* dead;
+    volatile CtaLife* life;
     StageRing ring;
     // The next unit; false: none, or the CTA has given up. WARP: called by a whole warp.
     template <bool WARP>
     __device__ __forceinline__ bool next(Unit* t)
     {
-        bool ok = wait_or_dead(&board->full[ring.s], ring.phase, dead);
+        bool ok = wait_or_dead(&board->full[ring.s], ring.phase, life);
         if (WARP) ok = __all_sync(0xffffffffu, ok);
         if (ok) *t = board->unit[ring.s];
         if (!ok || t->n < 0) {
@@ -276,15 +276,15 @@ struct AbUnits {
 
 // The warp that works the units out: decode(u) gives a unit, idle(t) deals with one without work.
 template <class Unit, class Decode, class Idle>
-__device__ __forceinline__ void ab_publish(AbUnitBoard<Unit>& b, int64_t units, volatile int* dead,
+__device__ __forceinline__ void ab_publish(AbUnitBoard<Unit>& b, int64_t units, volatile CtaLife* life,
                                            Decode decode, Idle idle)
 {
     StageRing ring;
-    AttnUnitSource source{units, &b.answer, &b.steal, dead};
+    AttnUnitSource source{units, &b.answer, &b.steal, life};
     bool ok = true;
     for (int64_t made = 0;;) {
         if (made >= kAbUnitSlots)  // before a unit is taken, not with one in hand
-            ok = __all_sync(0xffffffffu, wait_or_dead(&b.empty[ring.s], ring.phase ^ 1u, dead));
+            ok = __all_sync(0xffffffffu, wait_watching(&b.empty[ring.s], ring.phase ^ 1u, life));
         if (!ok) break;
         const int64_t u = source.next();
         Unit t;
@@ -340,7 +340,7 @@ struct BkBars {
     uint64_t acc_full, acc_free;
     uint64_t drain;
     uint32_t tmem;
-    int dead;
+    CtaLife life;
     AbUnitBoard<BkUnit> board;
 };
 static_assert(sizeof(BkBars) <= 1024, "barriers");
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     BkBars& bars = *reinterpret_cast<BkBars*>(smem);
-    volatile int* dead = &bars.dead;
+    volatile CtaLife* life = &bars.life;
     const AttnShape& s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nk = (s.d + 15) / 16, halves = (s.d + 63) / 64;
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.acc_free, 16);
         ab_board_init(bars.board, s.q_start ? 19 : 18);  // warps 0-17, and 18
         mbar_init(&bars.drain, 1);
-        bars.dead = 0;
+        life_init(bars.life, s.wait_us, kAbThreads / 32);
         fence_barrier_init();
     }
     // Rows of a tile past tile_tokens * group never arrive: they are summed over with P = dS = 0,
@@ -447,17 +447,19 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     if (warp == kAbLoadWarp) {
         if (lane == 0) {
             StageRing ring;
-            uint32_t uses = 0;
-            int64_t issued = 0;
+            uint32_t blocks[2] = {0, 0};    // copies issued: of K and V blocks,
+            int64_t q_tiles = 0, g_tiles = 0;  // of q and dO tiles
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
-            AbUnits<BkUnit> source{&bars.board, dead};
+            AbUnits<BkUnit> source{&bars.board, life};
             BkUnit t;
             while (ok && source.next<false>(&t)) {
-                for (int w = 0; ok && w < 2; ++w) {
-                    if (uses > 0)
-                        ok = wait_or_dead(w ? &bars.v_empty : &bars.k_empty, (uses - 1) & 1, dead);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (ok && blocks[w] > 0)
+                        ok = wait_or_dead(w ? &bars.v_empty : &bars.k_empty, (blocks[w] - 1) & 1,
+                                          life);
                     if (!ok) break;
                     uint64_t* bar = w ? &bars.v_full : &bars.k_full;
                     mbar_arrive_expect_tx(bar, kv_bytes);
@@ -465,12 +467,12 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                         tensor_g2s_4d(smem + (w ? L::kV : L::kK) + h * L::kHalf,
                                       w ? &a.vmap[t.r] : &a.kmap[t.r], 64 * h, t.kvh, int(t.kv0),
                                       t.bb, bar);
+                    ++blocks[w];
                 }
                 if (!ok) break;
-                ++uses;
                 for (int i = 0; ok && i < t.n; ++i) {
                     const int64_t tile = t.first + i;
-                    if (issued >= K) ok = wait_or_dead(&bars.q_empty[ring.s], ring.phase ^ 1u, dead);
+                    if (q_tiles >= K) ok = wait_or_dead(&bars.q_empty[ring.s], ring.phase ^ 1u, life);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&bars.q_full[ring.s], q_bytes + kAbStats);
                     bulk_g2s(smem + L::kStat + ring.s * kAbStats,
@@ -481,29 +483,27 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                         tensor_g2s_4d(smem + L::kQ + ring.s * L::kTile + h * L::kHalf, &a.qmap[t.r],
                                       64 * h, t.kvh * s.group, int(tile * a.tile_tokens), t.bb,
                                       &bars.q_full[ring.s]);
-                    if (issued >= K) ok = wait_or_dead(&bars.g_empty[ring.s], ring.phase ^ 1u, dead);
+                    ++q_tiles;
+                    if (g_tiles >= K) ok = wait_or_dead(&bars.g_empty[ring.s], ring.phase ^ 1u, life);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&bars.g_full[ring.s], q_bytes);
                     for (int h = 0; h < halves; ++h)
                         tensor_g2s_4d(smem + L::kG + ring.s * L::kTile + h * L::kHalf, &a.gmap[t.r],
                                       64 * h, t.kvh * s.group, int(tile * a.tile_tokens), t.bb,
                                       &bars.g_full[ring.s]);
-                    ++issued;
+                    life->loads = uint32_t(++g_tiles);
                     ring.next(K);
                 }
             }
-            // leave no copy into this CTA's shared memory in flight (after a timeout the last q
-            // tile may have arrived without its dO: `issued` does not count it)
+            // leave no copy into this CTA's shared memory in flight (a loader that gave up may have
+            // issued a K block without its V, a q tile without its dO)
             bool drained = true;
-            for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k) {
+            for (int64_t k = max(int64_t(0), q_tiles - K); k < q_tiles; ++k)
                 drained &= mbar_wait_bounded(&bars.q_full[k % K], uint32_t((k / K) & 1));
+            for (int64_t k = max(int64_t(0), g_tiles - K); k < g_tiles; ++k)
                 drained &= mbar_wait_bounded(&bars.g_full[k % K], uint32_t((k / K) & 1));
-            }
-            if (!ok) drained &= mbar_wait_bounded(&bars.q_full[ring.s], ring.phase);
-            if (uses > 0) {
-                drained &= mbar_wait_bounded(&bars.k_full, (uses - 1) & 1);
-                drained &= mbar_wait_bounded(&bars.v_full, (uses - 1) & 1);
-            }
+            if (blocks[0] > 0) drained &= mbar_wait_bounded(&bars.k_full, (blocks[0] - 1) & 1);
+            if (blocks[1] > 0) drained &= mbar_wait_bounded(&bars.v_full, (blocks[1] - 1) & 1);
             if (!drained) atomicOr(&g_attn_bwd_status, kStatusDrainTimeout);
         }
         __syncwarp();
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             uint32_t cleaned = 0;  // parity of each stage's `clean`
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                return ok = ok && wait_or_dead(bar, parity, dead);
+                return ok = ok && wait_or_dead(bar, parity, life);
             };
             auto scores = [&](uint32_t d, uint64_t key, uint64_t row, uint64_t* bar) {
 #pragma unroll
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 scores(kBkDp, v_desc, g_desc + ring.s * (L::kTile >> 4), &bars.dp_full);
                 if (last) tc_commit(&bars.v_empty);
             };
-            AbUnits<BkUnit> source{&bars.board, dead};
+            AbUnits<BkUnit> source{&bars.board, life};
             BkUnit t, next;
             bool live = source.next<false>(&t);
             if (live) {
@@ -598,14 +598,14 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     } else if (warp == kAbCleanWarp) {
         if (s.q_start) {
             StageRing ring;
-            AbUnits<BkUnit> source{&bars.board, dead};
+            AbUnits<BkUnit> source{&bars.board, life};
             BkUnit t;
             bool ok = true;
             while (ok && source.next<true>(&t)) {
                 for (int i = 0; ok && i < t.n; ++i) {
-                    ok = __all_sync(0xffffffffu, wait_or_dead(&bars.q_full[ring.s], ring.phase, dead));
+                    ok = __all_sync(0xffffffffu, wait_or_dead(&bars.q_full[ring.s], ring.phase, life));
                     ok = ok &&
-                         __all_sync(0xffffffffu, wait_or_dead(&bars.g_full[ring.s], ring.phase, dead));
+                         __all_sync(0xffffffffu, wait_or_dead(&bars.g_full[ring.s], ring.phase, life));
                     if (!ok) break;
                     const int hidden = i == 0 ? bk_hidden(a, t) : 0;
                     if (hidden > 0) {
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         __syncwarp();
     } else if (warp == kAbUnitWarp) {
         ab_publish<BkUnit>(
-            bars.board, units, dead, [&](int64_t u) { return bk_unit<F16>(a, u); },
+            bars.board, units, life, [&](int64_t u) { return bk_unit<F16>(a, u); },
             [&](const BkUnit& t) {  // keys that no row sees
                 for (int i = lane; i < 2 * kAttnRows; i += 32) {
                     const int64_t key = t.kv0 + i % kAttnRows;
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         uint32_t uses = 0, tiles = 0;
         bool ok = true;
         auto all = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, life));
         };
         auto arrive = [&](uint64_t* bar) {
             tmem_wait_st();
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        AbUnits<BkUnit> source{&bars.board, dead};
+        AbUnits<BkUnit> source{&bars.board, life};
         BkUnit t;
         while (ok && source.next<true>(&t)) {
             const int64_t key = t.kv0 + row;
@@ -767,8 +767,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             ++uses;
         }
     }
+    life_end(bars.life, warp == kAbUnitWarp);
     __syncthreads();
-    if (threadIdx.x == 0 && bars.dead) atomicOr(&g_attn_bwd_status, kStatusWaitTimeout);
+    if (threadIdx.x == 0 && life_status(bars.life) != 0)
+        atomicOr(&g_attn_bwd_status, life_status(bars.life));
     if (warp == kAbMmaWarp) tmem_free(tmem);
 }
 
@@ -803,7 +805,8 @@ struct BqBars {
     uint64_t ds_ready, dq_done;            // dS written; summed up
     uint64_t acc_full, acc_free, drain;
     uint32_t tmem;
-    int dead, seen;
+    int seen;
+    CtaLife life;
     AbUnitBoard<BqUnit> board;
 };
 static_assert(sizeof(BqBars) <= 1024, "barriers");
@@ -853,7 +856,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     BqBars& bars = *reinterpret_cast<BqBars*>(smem);
-    volatile int* dead = &bars.dead;
+    volatile CtaLife* life = &bars.life;
     const AttnShape& s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nk = (s.d + 15) / 16, halves = (s.d + 63) / 64;
@@ -879,7 +882,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.acc_free, 16);
         ab_board_init(bars.board, s.ragged ? 19 : 18);  // warps 0-17, and 18
         mbar_init(&bars.drain, 1);
-        bars.dead = 0;
+        life_init(bars.life, s.wait_us, kAbThreads / 32);
         // The kernel in front (dK, dV) waited for the statistics before it let this one start. What it
         // had seen then is seen here through `ready`; if that is not there yet, after its end.
         bars.seen = acquire_word(a.ready) == 1;
@@ -902,21 +905,21 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
             auto stage = [&](const CUtensorMap* map, uint32_t bytes, int head, int row, int bb) {
-                if (issued >= K) ok = wait_or_dead(&bars.empty[ring.s], ring.phase ^ 1u, dead);
+                if (issued >= K) ok = wait_or_dead(&bars.empty[ring.s], ring.phase ^ 1u, life);
                 if (!ok) return;
                 mbar_arrive_expect_tx(&bars.full[ring.s], bytes);
                 for (int h = 0; h < halves; ++h)
                     tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf, map, 64 * h,
                                   head, row, bb, &bars.full[ring.s]);
-                ++issued;
+                life->loads = uint32_t(++issued);
                 ring.next(K);
             };
-            AbUnits<BqUnit> source{&bars.board, dead};
+            AbUnits<BqUnit> source{&bars.board, life};
             BqUnit t;
             while (ok && source.next<false>(&t)) {
                 stage(&a.qmap[t.r], q_bytes, t.kvh * s.group, int(t.tok0), t.bb);
                 if (ok) stage(&a.kmap[t.r], kv_bytes, t.kvh, 0, t.bb);
-                if (ok && uses > 0) ok = wait_or_dead(&bars.g_empty, (uses - 1) & 1, dead);
+                if (ok && uses > 0) ok = wait_or_dead(&bars.g_empty, (uses - 1) & 1, life);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&bars.g_full, q_bytes);
                 for (int h = 0; h < halves; ++h)
@@ -938,12 +941,12 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         // dS is zero past the last key, but zero times what K holds there may be NaN
         if (s.ragged) {
             StageRing ring;
-            AbUnits<BqUnit> source{&bars.board, dead};
+            AbUnits<BqUnit> source{&bars.board, life};
             BqUnit t;
             bool ok = true;
             while (ok && source.next<true>(&t)) {
                 for (int j = -1; ok && j < 2 * t.n; ++j) {  // Q K0 V0 K1 V1 ...
-                    ok = __all_sync(0xffffffffu, wait_or_dead(&bars.full[ring.s], ring.phase, dead));
+                    ok = __all_sync(0xffffffffu, wait_or_dead(&bars.full[ring.s], ring.phase, life));
                     if (!ok) break;
                     const int past = j < 0 || (j & 1) ? kAttnRows : bq_past(s, t, j >> 1);
                     if (past < kAttnRows) {
@@ -976,7 +979,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             uint32_t cleaned = 0;  // parity of each stage's `clean`
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                return ok = ok && wait_or_dead(bar, parity, dead);
+                return ok = ok && wait_or_dead(bar, parity, life);
             };
             // S of the ring's next block, whose stage it returns; dP of the V in the stage after it.
             // `first` of unit number `use`: its queries come before its keys.
@@ -1016,7 +1019,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 if (last) tc_commit(&bars.g_empty);
                 ring.next(K);
             };
-            AbUnits<BqUnit> source{&bars.board, dead};
+            AbUnits<BqUnit> source{&bars.board, life};
             BqUnit t, next;
             bool live = source.next<false>(&t);
             int ks = 0;  // the stage of the current block's K
@@ -1068,7 +1071,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         __syncwarp();
     } else if (warp == kAbUnitWarp) {
         ab_publish<BqUnit>(
-            bars.board, units, dead, [&](int64_t u) { return bq_unit<F16>(a, u); },
+            bars.board, units, life, [&](int64_t u) { return bq_unit<F16>(a, u); },
             [&](const BqUnit& t) {  // rows that see no key
                 for (int i = lane; i < kAttnRows; i += 32) {
                     const int tok_in = i / s.group;
@@ -1092,7 +1095,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         int64_t stages = 0;  // of the ring before the current unit
         bool ok = true;
         auto all = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, life));
         };
         auto arrive = [&](uint64_t* bar) {
             tc_fence_before();
@@ -1118,7 +1121,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             }
             arrive(&bars.q_ready);
         };
-        AbUnits<BqUnit> source{&bars.board, dead};
+        AbUnits<BqUnit> source{&bars.board, life};
         BqUnit t, next;
         bool live = source.next<true>(&t);
         if (live) copy(0);
@@ -1205,9 +1208,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             t = next;
         }
     }
+    life_end(bars.life, warp == kAbUnitWarp);
     wait_for_previous();  // dK and dV are done when this kernel is (nothing here reads them)
     __syncthreads();
-    if (threadIdx.x == 0 && bars.dead) atomicOr(&g_attn_bwd_status, kStatusWaitTimeout);
+    if (threadIdx.x == 0 && life_status(bars.life) != 0)
+        atomicOr(&g_attn_bwd_status, life_status(bars.life));
     if (warp == kAbMmaWarp) tmem_free(tmem);
 }
 

@@ -128,7 +128,7 @@ struct AfBars {
     uint64_t drain, steal;
     uint4 answer;
     uint32_t tmem;
-    int dead;
+    CtaLife life;
     AfUnit unit[kAfMaxUnitSlots];    // r < 0: no more
 };
 static_assert(sizeof(AfBars) <= kAfBarBytes, "barriers");
@@ -191,7 +191,7 @@ struct AfUnits {
     template <bool WARP>
     __device__ __forceinline__ bool next(AfUnit* t)
     {
-        bool ok = wait_or_dead(&bars->u_full[ring.s], ring.phase, &bars->dead);
+        bool ok = wait_or_dead(&bars->u_full[ring.s], ring.phase, &bars->life);
         if (WARP) ok = __all_sync(0xffffffffu, ok);
         if (!ok) return false;
         *t = bars->unit[ring.s];
@@ -202,7 +202,7 @@ struct AfUnits {
     // The same without giving its record back yet (release does): it can be read again.
     __device__ __forceinline__ bool peek()
     {
-        const bool ok = wait_or_dead(&bars->u_full[ring.s], ring.phase, &bars->dead);
+        const bool ok = wait_or_dead(&bars->u_full[ring.s], ring.phase, &bars->life);
         return __all_sync(0xffffffffu, ok) && bars->unit[ring.s].r >= 0;
     }
     __device__ __forceinline__ const AfUnit& record() const { return bars->unit[ring.s]; }
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     AfBars& bars = *reinterpret_cast<AfBars*>(smem);
-    volatile int* dead = &bars.dead;
+    volatile CtaLife* life = &bars.life;
     const AttnShape& s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nk = (s.d + 15) / 16;      // steps of 16 along the head dimension
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         }
         mbar_init(&bars.drain, 1);
         mbar_init(&bars.steal, 1);
-        bars.dead = 0;
+        life_init(bars.life, s.wait_us, kAfThreads / 32);
         fence_barrier_init();
     }
     if (warp == kAfMmaWarp) tmem_alloc(&bars.tmem);
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (t.n(k) == 0) continue;
-                    if (tiles >= Q && !wait_or_dead(&bars.q_empty[slots.s], slots.phase ^ 1u, dead))
+                    if (tiles >= Q && !wait_or_dead(&bars.q_empty[slots.s], slots.phase ^ 1u, life))
                         return false;
                     mbar_arrive_expect_tx(&bars.q_full[slots.s], q_bytes);
                     for (int h = 0; h < halves; ++h)
@@ -364,14 +364,14 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 return true;
             };
             auto block = [&](bool value, const AfUnit& t, int at) {
-                if (issued >= K && !wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, dead))
+                if (issued >= K && !wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, life))
                     return false;
                 const CUtensorMap* map = value ? &a.vmap[t.r] : &a.kmap[t.r];
                 mbar_arrive_expect_tx(&bars.kv_full[ring.s], kv_bytes);
                 for (int h = 0; h < halves; ++h)
                     tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf, map, 64 * h,
                                   t.kvh, at * kAttnRows, t.bb, &bars.kv_full[ring.s]);
-                ++issued;
+                life->loads = uint32_t(++issued);
                 ring.next(K);
                 return true;
             };
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 [&](bool value, const AfUnit& t, int at) {
                     const int past = value ? af_past(s, t, at) : kAttnRows;
                     if (!__all_sync(0xffffffffu,
-                                    wait_or_dead(&bars.kv_full[ring.s], ring.phase, dead)))
+                                    wait_or_dead(&bars.kv_full[ring.s], ring.phase, life)))
                         return false;
                     if (past < kAttnRows) {
                         for (int h = 0; h < halves; ++h)
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             uint32_t cleaned = 0;  // parity of each stage's `clean`
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                return ok = ok && wait_or_dead(bar, parity, dead);
+                return ok = ok && wait_or_dead(bar, parity, life);
             };
             auto scores = [&](int k, int stage) {  // S_k = Q_k K^T
                 const uint64_t qd = q_desc + slot[k] * (L::kSlot >> 4);
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             auto room = [&]() {  // before a unit is taken, not with one in hand
                 if (made >= L::kUnitSlots)
                     ok = __all_sync(0xffffffffu,
-                                    wait_or_dead(&bars.u_empty[ring.s], ring.phase ^ 1u, dead));
+                                    wait_watching(&bars.u_empty[ring.s], ring.phase ^ 1u, life));
                 return ok;
             };
             auto publish = [&](const AfUnit& t) {
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 ring.next(L::kUnitSlots);
             };
             AfUnit t;
-            AttnUnitSource source{a.units, &bars.answer, &bars.steal, dead};
+            AttnUnitSource source{a.units, &bars.answer, &bars.steal, life};
             for (int64_t u; room() && (u = source.next()) >= 0;) {
                 t = af_unit(a, u);
                 if (t.most() > 0) {
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         uint32_t uses = 0, blocks = 0;
         bool ok = true;
         auto all = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+            return __all_sync(0xffffffffu, wait_or_dead(bar, parity, life));
         };
         auto arrive = [&](uint64_t* bar) {
             tmem_wait_st();
@@ -782,9 +782,11 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             ++uses;
         }
     }
+    life_end(bars.life, warp == kAfUnitWarp);
     let_next_start();
     __syncthreads();
-    if (threadIdx.x == 0 && bars.dead) atomicOr(&g_attn_fwd_status, kStatusWaitTimeout);
+    if (threadIdx.x == 0 && life_status(bars.life) != 0)
+        atomicOr(&g_attn_fwd_status, life_status(bars.life));
     if (warp == kAfMmaWarp) tmem_free(tmem);
 }
 
