@@ -49,6 +49,25 @@ def test_ragged_keys(shape, causal, dtype):
         fwd.check(q, zero(k), zero(v), o, lse, 0.2, **kw)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("skv", [77, 256, 384, 500, 513])
+@pytest.mark.parametrize("b", [1, 3])
+def test_padded_text(b, skv, dtype):
+    """Few key blocks with key counts at d = 128, in either layout: more units than CTAs, of all lengths."""
+    shape = (2, b, 4100, skv, [4, 3], 1, 128)
+    qp, kp = plans(*shape, dtype)
+    for part in (1.0, 0.6, 0.3):
+        q, k, v = inputs(*shape, dtype, seed=9)
+        lens = [max(1, int(skv * part) - 40 * i) for i in range(b)]
+        for t in (k, v):
+            for x in t:
+                for bb, m in enumerate(lens):
+                    x[bb, m:] = math.nan
+        o, lse = attend(qp, kp, q, k, v, 0.1, kv_lens=i32(*lens))
+        zero = lambda t: [torch.nan_to_num(x, 0, 0, 0) for x in t]
+        fwd.check(q, zero(k), zero(v), o, lse, 0.1, kv_lens=i32(*lens))
+
+
 @pytest.mark.parametrize("shape", [(1, 200, 1, 700, [1], 1, 64), (2, 90, 1, 400, [1, 2], 8, 128),
                                    (1, 170, 5, 520, [1], 16, 128)],
                          ids=lambda s: "x".join(map(str, (s[1], s[2], s[3], s[5], s[6]))))

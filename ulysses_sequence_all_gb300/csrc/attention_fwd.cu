@@ -61,10 +61,15 @@ constexpr int kAfLoadWarp = 8, kAfMmaWarp = 9, kAfCleanWarp = 10, kAfUnitWarp = 
 constexpr int kAfMaxUnitSlots = 4;
 constexpr int kAfBarBytes = 1024;
 constexpr int kAfMaxParts = 64;   // of the keys
-// Key blocks of a unit up to which it counts as short, and with ragged batches, which hold less than
-// the tensor. 75,600 queries x 40 heads of 128, short against long: 256 keys 477 : 529 us, 238 of 512
-// keys 535 : 612, 512 keys 739 : 699, 1,024 keys 1,309 : 1,103.
-constexpr int kAfShortBlocks = 3, kAfShortBlocksRagged = 4;
+// Key blocks of a unit up to which it counts as short; more of them for one batch element with a key
+// count (a padded text), whose tensor has room that the count, which the host does not see, may leave
+// unused. 75,600 queries x 40 heads of 128, short : long in us. No counts: 77 keys 377 : 426, 256
+// 477 : 481, 384 616 : 561, 512 751 : 671. One element that holds all, 5/6, 2/3, 1/2, 1/3 of 384 keys:
+// 606 : 588, 620 : 620, 622 : 619, 528 : 585, 405 : 456; of 512: 739 : 692, 743 : 725, 620 : 623,
+// 490 : 526, 526 : 585 (so a full one loses 3 and 7 % by the rule, a third of one gains 11 %); of 640:
+// 880 : 787, 880 : 813, 744 : 730, 620 : 621, 529 : 585. Two to eight elements of different lengths, 512
+// keys at most: 832-883 : 767-806.
+constexpr int kAfShortBlocks = 2, kAfShortBlocksPadded = 4;
 constexpr float kAfRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 // fp16 probabilities are held times 2^7 (2^15 at most with the above): what many keys weigh together
 // may be a good part of a row although each has less than fp16's smallest 2^-25 of the largest.
@@ -929,7 +934,8 @@ static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int devi
                    : af_launch_mode<DP, F16, kAfPaired>(a, stream, device, cap, sm_count);
     if constexpr (DP == 128) {  // (d <= 64 has room for both)
         const int64_t blocks = (a.s.Skv + kAttnRows - 1) / kAttnRows;
-        if (blocks <= int64_t(a.s.kv_lens ? kAfShortBlocksRagged : kAfShortBlocks) * a.splits)
+        const bool padded = a.s.kv_lens && a.s.b == 1;
+        if (blocks <= int64_t(padded ? kAfShortBlocksPadded : kAfShortBlocks) * a.splits)
             return af_launch_mode<DP, F16, kAfShort>(a, stream, device, cap, sm_count);
     }
     return af_launch_mode<DP, F16, kAfLong>(a, stream, device, cap, sm_count);
