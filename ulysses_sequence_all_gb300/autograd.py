@@ -20,12 +20,14 @@ plan for the backward:
   output and the log-sum-exp that the forward keeps.
 
 Inputs and outputs are lists of W tensors (one per virtual rank) on the current CUDA device;
-the outputs are new tensors the caller owns. Nothing here computes: every step runs in the
+the outputs are new tensors the caller owns. The relayout can be differentiated again, the others
+once: a gradient of theirs raises where it is differentiated. Nothing here computes: every step runs in the
 library's kernels, on the current stream.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
@@ -65,12 +67,9 @@ class _A2A4D(torch.autograd.Function):
         return tuple(outs)
 
     @staticmethod
-    def backward(ctx, *grads):
-        plan, mode = ctx.plan, ctx.mode
-        gs = _grads(grads, plan, mode, ctx.like)
-        back = _empty(plan, 1 - mode, gs[0])
-        B.ulysses_a2a_4d(plan, 1 - mode, gs, back)
-        return (None, None, *back)
+    def backward(ctx, *grads):  # a relayout itself, and as differentiable
+        gs = _grads(grads, ctx.plan, ctx.mode, ctx.like)
+        return (None, None, *_A2A4D.apply(ctx.plan, 1 - ctx.mode, *gs))
 
 
 def a2a_4d(plan: B.Plan, xs, mode: int = 0):
@@ -94,6 +93,7 @@ class _QKFused(torch.autograd.Function):
         return tuple(qo + ko)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         plan, W = ctx.plan, ctx.W
         rms_w, *qk = ctx.saved_tensors
@@ -123,6 +123,7 @@ class _QKVFused(torch.autograd.Function):
         return tuple(qo + ko + vo)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         plan, W = ctx.plan, ctx.W
         rms_w, *qkv = ctx.saved_tensors
@@ -171,6 +172,7 @@ class _PackedFused(torch.autograd.Function):
         return tuple(t for plane in outs for t in plane)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         plan, W = ctx.plan, ctx.W
         rms_w, *packed = ctx.saved_tensors
@@ -215,6 +217,7 @@ class _Attention(torch.autograd.Function):
         return tuple(out)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         W = ctx.W
         kv_lens, q_start, *saved = ctx.saved_tensors
