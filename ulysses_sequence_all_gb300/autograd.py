@@ -79,6 +79,15 @@ def a2a_4d(plan: B.Plan, xs, mode: int = 0):
     return list(_A2A4D.apply(plan, mode, *xs))
 
 
+def _rope_plan(ctx):
+    """The forward's plan, which rotates as it did then: the gradient of other positions or pairs would be
+    another function's."""
+    if ctx.plan.rope != ctx.rope:
+        raise RuntimeError(f"the plan's RoPE settings changed between forward {ctx.rope} and backward "
+                           f"{ctx.plan.rope}")
+    return ctx.plan
+
+
 class _QKFused(torch.autograd.Function):
     @staticmethod
     def forward(ctx, plan, eps, rope_theta, rms_w, *qk):
@@ -88,6 +97,7 @@ class _QKFused(torch.autograd.Function):
         rms_w = rms_w.contiguous()
         qo, ko = _empty(plan, 0, q[0]), _empty(plan, 0, q[0])
         B.ulysses_a2a_4d_qk_fused(plan, q, k, qo, ko, rms_w, eps, rope_theta)
+        ctx.rope = plan.rope
         ctx.plan, ctx.eps, ctx.theta, ctx.W = plan, eps, rope_theta, W
         ctx.save_for_backward(rms_w, *q, *k)
         return tuple(qo + ko)
@@ -95,7 +105,7 @@ class _QKFused(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, *grads):
-        plan, W = ctx.plan, ctx.W
+        plan, W = _rope_plan(ctx), ctx.W
         rms_w, *qk = ctx.saved_tensors
         q, k = qk[:W], qk[W:]
         like = q[0]
@@ -118,6 +128,7 @@ class _QKVFused(torch.autograd.Function):
         like = qkv[0]
         qo, ko, vo = _empty(plan, 0, like), _empty(plan, 0, like), _empty(plan, 0, like)
         B.ulysses_a2a_4d_qkv_fused(plan, qkv, qo, ko, vo, rms_w, eps, rope_theta)
+        ctx.rope = plan.rope
         ctx.plan, ctx.eps, ctx.theta, ctx.W = plan, eps, rope_theta, len(qkv)
         ctx.save_for_backward(rms_w, *qkv)
         return tuple(qo + ko + vo)
@@ -125,7 +136,7 @@ class _QKVFused(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, *grads):
-        plan, W = ctx.plan, ctx.W
+        plan, W = _rope_plan(ctx), ctx.W
         rms_w, *qkv = ctx.saved_tensors
         like = qkv[0]
         gq = _grads(grads[:W], plan, 0, like)
@@ -166,6 +177,7 @@ class _PackedFused(torch.autograd.Function):
         outs = [_empty(plan, 0, like) for _ in range(planes)]
         B.ulysses_a2a_4d_packed_fused(plan, planes, q_plane, k_plane, pitch, packed, outs, rms_w,
                                       eps, rope_theta)
+        ctx.rope = plan.rope
         ctx.plan, ctx.eps, ctx.theta, ctx.W = plan, eps, rope_theta, len(packed)
         ctx.planes, ctx.q_plane, ctx.k_plane, ctx.pitch = planes, q_plane, k_plane, pitch
         ctx.save_for_backward(rms_w, *packed)
@@ -174,7 +186,7 @@ class _PackedFused(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, *grads):
-        plan, W = ctx.plan, ctx.W
+        plan, W = _rope_plan(ctx), ctx.W
         rms_w, *packed = ctx.saved_tensors
         like = packed[0]
         gs = [_grads(grads[c * W:(c + 1) * W], plan, 0, like) for c in range(ctx.planes)]

@@ -199,6 +199,7 @@ class Plan:
         self.handle = handle
         self.W, self.b, self.d, self.dtype = W, b, d, dtype
         self.code = DTYPE_CODES.get(dtype, dtype)  # ULY_BF16, ...
+        self.rope = (ULY_ROPE_ADJACENT, ((), (), 0))  # the fused calls' pair layout and position axes
         self.seq_splits, self.head_splits = list(seq_splits), list(head_splits)
 
     def __del__(self):
@@ -226,6 +227,7 @@ def ulysses_plan_set_chunk_bytes(plan: Plan, max_chunk_bytes: int):
 def ulysses_plan_set_rope_pairs(plan: Plan, pairs: int):
     """RoPE pair layout of the fused calls with this plan: ULY_ROPE_ADJACENT or ULY_ROPE_HALF."""
     _check(_lib().ulysses_plan_set_rope_pairs(plan, pairs), "ulysses_plan_set_rope_pairs")
+    plan.rope = (pairs, plan.rope[1])
 
 
 def ulysses_plan_set_rope_grid(plan: Plan, extents: Sequence[int], pairs: Sequence[int],
@@ -238,6 +240,7 @@ def ulysses_plan_set_rope_grid(plan: Plan, extents: Sequence[int], pairs: Sequen
     n = len(extents)
     _check(_lib().ulysses_plan_set_rope_grid(plan, n, (_i64 * n)(*extents), (_i64 * n)(*pairs),
                                              first), "ulysses_plan_set_rope_grid")
+    plan.rope = (plan.rope[0], (tuple(extents), tuple(pairs), first) if n else ((), (), 0))
 
 
 def ulysses_plan_set_max_ctas(plan: Plan, max_ctas: int):
