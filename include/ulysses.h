@@ -177,6 +177,8 @@ int ulysses_plan_set_rope_pairs(ulysses_plan_t plan, int pairs);
  *            of d/2 pairs, rope_theta^(-2j/d) as without a grid).
  *   first    >= 0; first + the product of the extents must not pass S. Tokens before and after the
  *            grid (text beside an image, padding) are normalised but not turned.
+ * Every axis has a ladder of its own, and its coordinates count 0, 1, 2, ...: axes that share one
+ * ladder over all d/2 pairs, and coordinates with an offset or a scale, cannot be expressed.
  * Every batch element has the same grid. It holds for the same calls as the pair layout, which it
  * goes together with. The arrays are read during the call. ULY_EINVAL otherwise (the plan is then
  * unchanged). The pages name the fused QK RMSNorm + RoPE without fixing its positions. Must not

@@ -29,7 +29,7 @@ def attention_block(plan: B.Plan, qkv, rms_w, eps: float = 1e-6, rope_theta: flo
                     scale: float | None = None, causal: bool = False, kv_lens=None):
     """Attention of packed shards: qkv is W tensors (b, s_q, 3, N, d), rms_w (2, d) fp32 the norm
     weights of q and k. The plan's RoPE settings hold (ulysses_plan_set_rope_grid gives positions
-    of several axes). kv_lens: b int32 counts where the batch is padded at its end. Differentiable
+    of several axes). kv_lens: b key counts where the batch is padded at its end. Differentiable
     in qkv and rms_w. Returns W tensors (b, s_q, N, d)."""
     q, k, v = A.qkv_fused(plan, qkv, rms_w, eps, rope_theta)
     o = A.attention(plan, plan, q, k, v, scale, causal, kv_lens)

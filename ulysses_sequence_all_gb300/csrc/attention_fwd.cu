@@ -10,9 +10,9 @@
 // One pass over the keys in blocks of 128 with the running maximum and sum: 4 d flops per (row,
 // key) on the tensor cores, one exponential. With d = 128 it is bound by the products, those of S
 // by reading both operands from shared memory (about 107 cycles each in place of 64); with few rows
-// by reading the keys. Measured: 75,600 tokens x 8 heads of 128 in 13.0-13.8 ms, 1.7-1.8 PFLOP/s
-// (0.86-0.91 of the measured cuBLAS rate); 2 x 4,095 causal tokens, 32 heads over 8, in 0.20 ms; one
-// token each on 16 caches of 12,000-32,000 keys in 0.13 ms (0.79 of the copy peak).
+// by reading the keys. Measured: 75,600 tokens x 8 heads of 128 in 13.7-13.8 ms, 1.69-1.70 PFLOP/s
+// (0.86 of the measured cuBLAS rate); 2 x 4,095 causal tokens, 32 heads over 8, in 0.197 ms; one
+// token each on 16 caches of 12,000-32,000 keys in 0.126 ms (0.81 of the copy peak).
 //
 // A CTA (one per SM, 384 threads) takes two tiles of 128 query rows that share their keys, unit
 // after unit. Warp 11 works out the units ahead and leaves their records in shared memory. Warp 8
@@ -22,7 +22,8 @@
 // tensor cores always have one tile's work; a unit's first scores follow the last unit's products
 // without a gap. Warps 0-3 and 4-7 are the two tiles' softmax: tensor memory gives a thread a whole
 // row, so maximum and sum need no exchange; they hold most of the registers. Warp 10 zeroes what a
-// value block holds past a ragged batch element's last key.
+// value block holds past the last key that any row of its batch element sees. Warp 11 also watches that
+// the others get on (CtaLife).
 // P goes back to tensor memory over its own S in 16 bits, rounded to nearest (unit-scale values
 // in an fp32 sum: the output itself is rounded to the same type), and is the A operand of O += P V
 // there, whose first half starts when half of P is written. O stays in tensor memory; it is
@@ -888,8 +889,10 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     a->order.group = attn_order_group(a->order.heads, s.Skv * s.d * 4);  // keys and values
     const int64_t base = a->order.heads * a->order.blocks;
     // One wave of the SMs (finer parts of a ragged batch, evened out by stealing, measured no faster:
-    // 16 caches 134 us with 2 units a head, 134 with 7, 136 with 9, 154 with 19), of a block a tile at
-    // least where rows are few (latency), of four blocks where a part's output is a whole tile.
+    // 16 caches of 4 key heads 134 us with 2 units a head, 134 with 7, 136 with 9, 154 with 19; no other
+    // number of heads was measured, and between half as many units as SMs and all of them, where n is
+    // 1, the rest of the SMs have none), of a block a tile at least where rows are few (latency), of
+    // four blocks where a part's output is a whole tile.
     int64_t n = base > 0 ? sm_count / base : 1;
     const int64_t most = blocks / (a->paired ? 2 : 4);
     if (n > most) n = most;
