@@ -52,7 +52,7 @@ enum {
     ULY_ECHUNK = -4,   /* the chunk cap is smaller than one sequence row on some rank */
     ULY_ECUDA = -5,    /* a CUDA runtime call failed; ulysses_last_cuda_error() has the code */
     ULY_ENOMEM = -6,   /* host memory for a plan could not be allocated */
-    ULY_EDEVICE = -7,  /* a kernel recorded a wait timeout in the device status word */
+    ULY_EDEVICE = -7,  /* a kernel recorded a wait timeout or a bad page in the device status word */
     ULY_ESCRATCH = -8  /* the call needs more scratch than the library's static array holds */
 };
 
@@ -491,6 +491,64 @@ int ulysses_attention_backward_workspace(ulysses_plan_t q_plan, ulysses_plan_t k
                                          size_t* bytes);
 
 /*
+ * A key-value cache held in pages, for answering token by token after a long prompt (the pages have no
+ * counterpart: their collective ends where attention begins). Rank r's keys, and its values, lie in a
+ * pool (pages, page, m_r, d): the head-side tensor of cache_plan, a plan whose batch b is the number of
+ * pages and whose sequence S is the tokens of a page, a multiple of 8; only the total of its seq_splits
+ * matters. Every rank has the same pages:
+ *   page_table  (b, table_pages) device int32: batch element bb's token at position j is row j % page of
+ *               page page_table[bb][j / page]. Entries that no token needs may hold anything. Batch
+ *               elements may share pages (a common beginning). table_pages * page is at most 2^29.
+ * An entry that is needed and lies outside [0, pages) is not followed: it sets bit 4 of the device
+ * status word (ulysses_device_status), reads as keys and values of zeros, and is not written to.
+ *
+ * ulysses_cache_append writes new tokens to their places: token i < counts[bb] of batch element bb
+ * becomes position starts[bb] + i.
+ *   kv_plan     b, the new tokens S of each batch element, head_splits m_r, d and dtype of the pools (any
+ *               dtype: it is a byte move).
+ *   k, v        W device pointers each: (b, S, m_r, d), as mode 0 writes them.
+ *   k_pages, v_pages   W device pointers each, the pools, changed in those rows only.
+ *   starts      b device int32, >= 0.
+ *   counts      NULL (all S tokens), or b device int32 (clamped to [0, S]): a padded batch, whose rows
+ *               past the count are neither read nor written.
+ * Two tokens of a call must not have the same place (one of them would win, or parts of each). A position
+ * below 0 or past the table has no place either: bit 4. One launch on `stream`, under kv_plan's CTA cap.
+ */
+int ulysses_cache_append(ulysses_plan_t kv_plan, ulysses_plan_t cache_plan, const void* const* k,
+                         const void* const* v, void* const* k_pages, void* const* v_pages,
+                         const int32_t* page_table, int64_t table_pages, const int32_t* starts,
+                         const int32_t* counts, void* stream);
+
+/*
+ * Attention of each batch element's last tokens over its pages: the query at position p sees the keys
+ * j < kv_lens[bb] with j <= p and, with a window, j > p - window or j < sinks.
+ *   q, o, lse   as ulysses_attention's, q_plan's S queries of each batch element (one, or a few drafted
+ *               ones; any number is computed, in passes over the keys of 32 rows = g S / 32 each).
+ *   kv_lens     b device int32 (clamped to what the table has room for): the tokens in the cache, those
+ *               of this call included (append them first).
+ *   q_start     NULL: the queries are the last S tokens, positions kv_lens[bb] - S and on; or b device
+ *               int32, the position of the first (negative ones see nothing).
+ *   window      0: none; else >= 1. Pages that hold neither one of the first `sinks` tokens nor one of the
+ *               window are not looked at: they may have been given back.
+ *   sinks       >= 0; without a window it has no effect.
+ *   workspace   device memory of ulysses_attention_paged_workspace bytes, 16-byte aligned: parts of
+ *               sequences that several CTAs share. Its content does not matter and is not kept; two calls
+ *               in flight at once need two.
+ * Plans: the same W, d (a multiple of 8, at most 128) and dtype (ULY_BF16 or ULY_F16), n_r = g m_r with
+ * g <= 64. Empty rows, what keys and values hold where no row sees it, precision, the CTA cap and statuses
+ * are as ulysses_attention's; ULY_EALIGN for page_table off 4 bytes. Two launches on `stream`.
+ */
+int ulysses_attention_paged(ulysses_plan_t q_plan, ulysses_plan_t cache_plan, const void* const* q,
+                            const void* const* k_pages, const void* const* v_pages, void* const* o,
+                            float* const* lse, const int32_t* page_table, int64_t table_pages,
+                            const int32_t* kv_lens, const int32_t* q_start, int64_t window,
+                            int64_t sinks, float scale, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Workspace bytes of ulysses_attention_paged for these plans on the current device. */
+int ulysses_attention_paged_workspace(ulysses_plan_t q_plan, ulysses_plan_t cache_plan, size_t* bytes);
+
+/*
  * End-to-end form for host-resident data: copy each rank's input from host_in[k] to dev_in[k],
  * run the relayout, and copy each dev_out[k] back to host_out[k]. The work is cut into about
  * eight ranges of the global sequence (within the chunk cap) so that copies in and copies out
@@ -527,8 +585,9 @@ int ulysses_a2a_4d_qk_fused_host(ulysses_plan_t plan, const void* const* q_host_
  * outputs of the calls since the last check are incomplete; discard them), 2 (a kernel gave up
  * waiting for its own bulk copies into shared memory before exiting: such a copy never completed,
  * so it may still land in shared memory a later kernel owns; discard the outputs and treat the
- * CUDA context as suspect, i.e. reset it with cudaDeviceReset before further work). Neither bit
- * is set unless the hardware stalls for seconds. */
+ * CUDA context as suspect, i.e. reset it with cudaDeviceReset before further work): neither of these is
+ * set unless the hardware stalls for seconds. 4: a call on a paged cache needed a page that is not in
+ * its pool, or a place that its table does not have (its outputs are not what was asked for). */
 int ulysses_device_status(unsigned* status);
 
 /*

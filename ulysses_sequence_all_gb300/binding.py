@@ -39,6 +39,7 @@ EXPORTS = ["ulysses_plan", "ulysses_plan_destroy", "ulysses_plan_set_chunk_bytes
            "ulysses_a2a_4d_qkv_fused_backward", "ulysses_a2a_4d_packed_fused_backward",
            "ulysses_attention", "ulysses_attention_workspace",
            "ulysses_attention_backward", "ulysses_attention_backward_workspace",
+           "ulysses_attention_paged", "ulysses_attention_paged_workspace", "ulysses_cache_append",
            "ulysses_a2a_4d_host", "ulysses_a2a_4d_qk_fused_host", "ulysses_device_status",
            "ulysses_selftest_wait_timeout", "ulysses_selftest_attention_wait_limit",
            "ulysses_last_cuda_error", "ulysses_strerror",
@@ -116,6 +117,10 @@ def _lib():
                                                    ctypes.c_size_t, _p]
         lib.ulysses_attention_backward_workspace.argtypes = [_p, _p,
                                                              ctypes.POINTER(ctypes.c_size_t)]
+        lib.ulysses_attention_paged.argtypes = [_p, _p, _pp, _pp, _pp, _pp, _pp, _p, _i64, _p, _p, _i64,
+                                                _i64, ctypes.c_float, _p, ctypes.c_size_t, _p]
+        lib.ulysses_attention_paged_workspace.argtypes = [_p, _p, ctypes.POINTER(ctypes.c_size_t)]
+        lib.ulysses_cache_append.argtypes = [_p, _p, _pp, _pp, _pp, _pp, _p, _i64, _p, _p, _p]
         lib.ulysses_a2a_4d_host.argtypes = [_p, ctypes.c_int, _pp, _pp, _pp, _pp, _p]
         lib.ulysses_a2a_4d_qk_fused_host.argtypes = [_p, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _p,
                                                      ctypes.c_float, ctypes.c_float, _p]
@@ -167,6 +172,15 @@ def _counts(x, b: int, what: str) -> int:
         raise ValueError(f"{what}: a contiguous int32 tensor of b = {b} entries on the device, not "
                          f"{x.dtype} {tuple(x.shape)} on {x.device}")
     return _addr(x)
+
+
+def _page_table(x, b: int) -> tuple[int, int]:
+    """Address and pages a row of a page table: a contiguous device tensor (b, pages) of int32."""
+    if not x.is_cuda or str(x.dtype) != "torch.int32" or x.dim() != 2 or x.shape[0] != b or \
+            not x.is_contiguous():
+        raise ValueError(f"page_table: a contiguous int32 tensor of b = {b} rows on the device, not "
+                         f"{x.dtype} {tuple(x.shape)} on {x.device}")
+    return _addr(x), x.shape[1]
 
 
 _PTR_ARRAYS: dict = {}  # the ctypes array type of each length (making one costs as much as filling it)
@@ -439,6 +453,41 @@ def ulysses_attention_backward(q_plan: Plan, kv_plan: Plan, dq, dk, dv, q, k, v,
         _ptrs(lse), _ptrs(go), _counts(kv_lens, q_plan.b, "kv_lens"),
         _counts(q_start, q_plan.b, "q_start"), int(causal), scale,
         _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_backward")
+
+
+def ulysses_attention_paged_workspace(q_plan: Plan, cache_plan: Plan) -> int:
+    """Workspace bytes ulysses_attention_paged needs for these plans on the current device."""
+    n = ctypes.c_size_t()
+    _check(_lib().ulysses_attention_paged_workspace(q_plan, cache_plan, ctypes.byref(n)),
+           "ulysses_attention_paged_workspace")
+    return n.value
+
+
+def ulysses_attention_paged(q_plan: Plan, cache_plan: Plan, q, k_pages, v_pages, out, lse, page_table,
+                            kv_lens, scale: float, q_start=None, window: int = 0, sinks: int = 0,
+                            workspace=None, stream=None):
+    """Attention of each sequence's last tokens over its pages: per rank q, out (b, Sq, n_r, d), lse
+    (b, n_r, Sq) fp32, k_pages, v_pages (pages, page, m_r, d), cache_plan's batch being the pages and its
+    sequence a page. page_table: int32 device tensor (b, pages a sequence); kv_lens: int32 device tensor
+    of b entries; q_start the same or None (the queries are the last Sq tokens). window 0: none.
+    `workspace` is a device tensor of at least ulysses_attention_paged_workspace(q_plan, cache_plan)
+    bytes."""
+    table, pages = _page_table(page_table, q_plan.b)
+    _check(_lib().ulysses_attention_paged(
+        q_plan, cache_plan, _ptrs(q), _ptrs(k_pages), _ptrs(v_pages), _ptrs(out), _ptrs(lse), table,
+        pages, _counts(kv_lens, q_plan.b, "kv_lens"), _counts(q_start, q_plan.b, "q_start"), window,
+        sinks, scale, _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_paged")
+
+
+def ulysses_cache_append(kv_plan: Plan, cache_plan: Plan, k, v, k_pages, v_pages, page_table, starts,
+                         counts=None, stream=None):
+    """Write new tokens' keys and values (per rank (b, S, m_r, d)) to positions starts[bb] + i of their
+    sequences' pages, i < counts[bb] (None: all). starts, counts: int32 device tensors of b entries."""
+    table, pages = _page_table(page_table, kv_plan.b)
+    _check(_lib().ulysses_cache_append(
+        kv_plan, cache_plan, _ptrs(k), _ptrs(v), _ptrs(k_pages), _ptrs(v_pages), table, pages,
+        _counts(starts, kv_plan.b, "starts"), _counts(counts, kv_plan.b, "counts"), _stream(stream)),
+        "ulysses_cache_append")
 
 
 def ulysses_a2a_4d_host(plan: Plan, mode: int, host_in, host_out, dev_in, dev_out, stream=None):

@@ -13,6 +13,7 @@
 
 #include "../../include/ulysses.h"
 #include "attention.h"
+#include "paged.h"
 #include "plan.h"
 #include "ptx.cuh"
 #include "tensor_map.h"
@@ -1048,6 +1049,161 @@ int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
 
+// ---- the paged cache, and windows of few rows -----------------------------------------------------
+
+// Shape of a call whose queries are q_plan's and whose keys are the pages of `cp` (its batch: pages; its
+// sequence: a page), or ULY_EINVAL.
+int paged_shape(const Plan& qp, const Plan& cp, PagedArgs* a)
+{
+    if (qp.dtype != cp.dtype || (qp.dtype != ULY_BF16 && qp.dtype != ULY_F16)) return ULY_EINVAL;
+    if (qp.W != cp.W || qp.d != cp.d || qp.d > kAttnMaxD) return ULY_EINVAL;
+    if (cp.N == 0 || qp.N % cp.N != 0) return ULY_EINVAL;
+    const int64_t group = qp.N / cp.N, lim = int64_t(1) << 26, most = int64_t(1) << 31;
+    if (group > kAttnMaxGroup || qp.S > lim / group || cp.S > lim) return ULY_EINVAL;
+    if (cp.b >= most || qp.b >= most / cp.N) return ULY_EINVAL;
+    std::memset(a, 0, sizeof *a);
+    a->W = qp.W;
+    a->b = int32_t(qp.b);
+    a->d = int32_t(qp.d);
+    a->f16 = qp.dtype == ULY_F16 ? 1 : 0;
+    a->group = int32_t(group);
+    a->Sq = qp.S;
+    a->pages = int32_t(cp.b);
+    a->page = int32_t(cp.S);
+    for (int r = 0; r < kMaxW; ++r) {
+        const int64_t m = r < cp.W ? cp.n[r] : 0;
+        if (r < qp.W && qp.n[r] != group * m) return ULY_EINVAL;  // a rank holds the keys of its queries
+        a->n[r] = int32_t(group * m);
+        a->m_begin[r + 1] = a->m_begin[r] + int32_t(m);
+    }
+    return ULY_OK;
+}
+
+// Work shares and passes of a call; the bytes of its workspace and the places in it.
+int paged_setup(const DeviceInfo& dev, PagedArgs* a, void* workspace, size_t* bytes)
+{
+    attn_paged_split(a, dev.sm_count);
+    if (int64_t(a->b) * a->row_groups >= int64_t(1) << 31) return ULY_EINVAL;
+    const size_t rows = 2 * size_t(a->parts) * size_t(a->rows);
+    const size_t o = rows * size_t(a->d) * sizeof(float), lse = rows * sizeof(float);
+    *bytes = o + lse + size_t(a->parts) * sizeof(PagedShared);
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    if (!base) return ULY_OK;
+    a->part_o = reinterpret_cast<float*>(base);
+    a->part_lse = reinterpret_cast<float*>(base + o);
+    a->shared = reinterpret_cast<PagedShared*>(base + o + lse);
+    return ULY_OK;
+}
+
+// The launch of a call whose masks and pages are set in `a`; kv_bytes: of a rank's keys.
+int paged_device(const Plan& qp, PagedArgs& a, const int64_t* kv_bytes, const void* const* q,
+                 const void* const* k, const void* const* v, void* const* o, float* const* lse,
+                 float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!(scale > 0.0f) || !(scale <= 3.0e38f)) return ULY_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(a.kv_lens) | reinterpret_cast<uintptr_t>(a.q_start) |
+         reinterpret_cast<uintptr_t>(a.table)) & 3u)
+        return ULY_EALIGN;
+    const int W = qp.W;
+    int64_t q_b[kMaxW], lse_b[kMaxW];
+    for (int r = 0; r < W; ++r) {
+        q_b[r] = head_side_bytes(qp, r);
+        lse_b[r] = qp.b * qp.n[r] * qp.S * int64_t(sizeof(float));
+    }
+    RangeList ins, outs;
+    int rc;
+    if ((rc = ins.add_ranks(q, q_b, W)) || (rc = ins.add_ranks(k, kv_bytes, W)) ||
+        (rc = ins.add_ranks(v, kv_bytes, W)) ||
+        (rc = outs.add_ranks(const_cast<const void* const*>(o), q_b, W)) ||
+        (rc = outs.add_ranks(reinterpret_cast<const void* const*>(lse), lse_b, W)))
+        return rc;
+    ins.add(a.kv_lens, qp.b * 4);
+    ins.add(a.q_start, qp.b * 4);
+    ins.add(a.table, qp.b * a.table_pages * 4);
+    if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
+    DeviceInfo dev;
+    if ((rc = current_device(&dev))) return rc;
+    size_t need = 0;
+    if ((rc = paged_setup(dev, &a, workspace, &need))) return rc;
+    if (!workspace || workspace_bytes < need) return ULY_EINVAL;
+    if (!aligned16(workspace)) return ULY_EALIGN;
+    outs.add(workspace, int64_t(need));
+    if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
+    a.scale = scale;
+    a.wait_us = attention_wait_us.load(std::memory_order_relaxed);
+    for (int r = 0; r < W; ++r) {
+        a.q[r] = static_cast<const uint8_t*>(q[r]);
+        a.o[r] = static_cast<uint8_t*>(o[r]);
+        a.lse[r] = lse[r];
+    }
+    const cudaError_t e = attn_paged_launch(a, k, v, stream, dev.device, attn_cap(qp), dev.sm_count);
+    return e == cudaSuccess ? ULY_OK : cuda_fail(e);
+}
+
+// Room that a page table gives a sequence; ULY_EINVAL for pages or tables that no call takes.
+constexpr int64_t kPagedMostKeys = int64_t(1) << 29;
+int paged_room(const Plan& cp, int64_t table_pages, int64_t* room)
+{
+    if (cp.S % 8 != 0 || table_pages < 1 || table_pages > kPagedMostKeys / cp.S) return ULY_EINVAL;
+    *room = table_pages * cp.S;
+    return ULY_OK;
+}
+
+constexpr int64_t kNoWindow = int64_t(1) << 40;
+
+int append_device(const Plan& np, const Plan& cp, const void* const* k, const void* const* v,
+                  void* const* k_pages, void* const* v_pages, const int32_t* table, int64_t table_pages,
+                  const int32_t* starts, const int32_t* counts, cudaStream_t stream)
+{
+    if (np.dtype != cp.dtype || np.W != cp.W || np.d != cp.d || !table || !starts) return ULY_EINVAL;
+    int64_t room;
+    int rc = paged_room(cp, table_pages, &room);
+    if (rc) return rc;
+    if ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(starts) |
+         reinterpret_cast<uintptr_t>(counts)) & 3u)
+        return ULY_EALIGN;
+    AppendArgs a;
+    std::memset(&a, 0, sizeof a);
+    const int W = np.W;
+    int64_t new_b[kMaxW], pool_b[kMaxW];
+    for (int r = 0; r < W; ++r) {
+        if (np.n[r] != cp.n[r]) return ULY_EINVAL;
+        new_b[r] = head_side_bytes(np, r);
+        pool_b[r] = head_side_bytes(cp, r);
+        const int64_t words = np.n[r] * np.d * np.e / 16;
+        if (words >= int64_t(1) << 31) return ULY_EINVAL;
+        a.words[r] = uint32_t(words);
+    }
+    RangeList ins, outs;
+    if ((rc = ins.add_ranks(k, new_b, W)) || (rc = ins.add_ranks(v, new_b, W)) ||
+        (rc = outs.add_ranks(const_cast<const void* const*>(k_pages), pool_b, W)) ||
+        (rc = outs.add_ranks(const_cast<const void* const*>(v_pages), pool_b, W)))
+        return rc;
+    ins.add(table, np.b * table_pages * 4);
+    ins.add(starts, np.b * 4);
+    ins.add(counts, np.b * 4);
+    if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
+    DeviceInfo dev;
+    if ((rc = current_device(&dev))) return rc;
+    for (int r = 0; r < W; ++r) {
+        a.src[0][r] = static_cast<const uint8_t*>(k[r]);
+        a.src[1][r] = static_cast<const uint8_t*>(v[r]);
+        a.dst[0][r] = static_cast<uint8_t*>(k_pages[r]);
+        a.dst[1][r] = static_cast<uint8_t*>(v_pages[r]);
+    }
+    a.table = table;
+    a.starts = starts;
+    a.counts = counts;
+    a.b = np.b;
+    a.tokens = np.S;
+    a.table_pages = table_pages;
+    a.pages = cp.b;
+    a.page = cp.S;
+    a.W = W;
+    const cudaError_t e = cache_append_launch(a, stream, attn_cap(np), dev.sm_count);
+    return e == cudaSuccess ? ULY_OK : cuda_fail(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1395,6 +1551,54 @@ int ulysses_attention_backward(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, vo
                            static_cast<cudaStream_t>(stream));
 }
 
+int ulysses_attention_paged_workspace(ulysses_plan_t q_plan, ulysses_plan_t cache_plan, size_t* bytes)
+{
+    if (!q_plan || !cache_plan || !bytes) return ULY_EINVAL;
+    PagedArgs a;
+    DeviceInfo dev;
+    int rc = paged_shape(q_plan->p, cache_plan->p, &a);
+    if (rc || (rc = current_device(&dev))) return rc;
+    return paged_setup(dev, &a, nullptr, bytes);
+}
+
+int ulysses_attention_paged(ulysses_plan_t q_plan, ulysses_plan_t cache_plan, const void* const* q,
+                            const void* const* k_pages, const void* const* v_pages, void* const* o,
+                            float* const* lse, const int32_t* page_table, int64_t table_pages,
+                            const int32_t* kv_lens, const int32_t* q_start, int64_t window,
+                            int64_t sinks, float scale, void* workspace, size_t workspace_bytes,
+                            void* stream)
+{
+    if (!q_plan || !cache_plan || !page_table || !kv_lens || window < 0 || sinks < 0) return ULY_EINVAL;
+    const Plan& cp = cache_plan->p;
+    PagedArgs a;
+    int64_t room;
+    int rc = paged_shape(q_plan->p, cp, &a);
+    if (rc || (rc = paged_room(cp, table_pages, &room))) return rc;
+    a.table = page_table;
+    a.table_pages = table_pages;
+    a.kv_lens = kv_lens;
+    a.q_start = q_start;
+    a.from_end = 1;
+    a.box = cp.S % 16 == 0 ? 16 : 8;
+    a.room = int32_t(room);
+    a.window = window ? window : kNoWindow;
+    a.sinks = int32_t(sinks < room ? sinks : room);
+    int64_t kv_b[kMaxW];
+    for (int r = 0; r < cp.W; ++r) kv_b[r] = head_side_bytes(cp, r);
+    return paged_device(q_plan->p, a, kv_b, q, k_pages, v_pages, o, lse, scale, workspace,
+                        workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int ulysses_cache_append(ulysses_plan_t kv_plan, ulysses_plan_t cache_plan, const void* const* k,
+                         const void* const* v, void* const* k_pages, void* const* v_pages,
+                         const int32_t* page_table, int64_t table_pages, const int32_t* starts,
+                         const int32_t* counts, void* stream)
+{
+    if (!kv_plan || !cache_plan) return ULY_EINVAL;
+    return append_device(kv_plan->p, cache_plan->p, k, v, k_pages, v_pages, page_table, table_pages,
+                         starts, counts, static_cast<cudaStream_t>(stream));
+}
+
 int ulysses_a2a_4d_host(ulysses_plan_t plan, int mode, const void* const* host_in,
                         void* const* host_out, void* const* dev_in, void* const* dev_out, void* stream)
 {
@@ -1488,14 +1692,16 @@ int ulysses_device_status(unsigned* status)
     if (!status) return ULY_EINVAL;
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e);
-    unsigned a = 0, b = 0, c = 0, t = 0, f = 0, g = 0;
+    unsigned a = 0, b = 0, c = 0, t = 0, f = 0, g = 0, p = 0, w = 0;
     if ((e = relayout_status(&a, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = fused_status(&b, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = fused_bwd_status(&c, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = fused_tensor_status(&t, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = attn_fwd_status(&f, true)) != cudaSuccess) return cuda_fail(e);
     if ((e = attn_bwd_status(&g, true)) != cudaSuccess) return cuda_fail(e);
-    *status = a | b | c | t | f | g;
+    if ((e = attn_paged_status(&p, true)) != cudaSuccess) return cuda_fail(e);
+    if ((e = cache_append_status(&w, true)) != cudaSuccess) return cuda_fail(e);
+    *status = a | b | c | t | f | g | p | w;
     return *status ? ULY_EDEVICE : ULY_OK;
 }
 
@@ -1525,7 +1731,7 @@ const char* ulysses_strerror(int status)
         case ULY_ECHUNK: return "chunk cap smaller than one sequence row";
         case ULY_ECUDA: return "CUDA runtime error (see ulysses_last_cuda_error)";
         case ULY_ENOMEM: return "out of host memory";
-        case ULY_EDEVICE: return "a kernel wait timed out (device status word set)";
+        case ULY_EDEVICE: return "a kernel wait timed out or a page was not in its pool (device status word set)";
         case ULY_ESCRATCH: return "needs more scratch than the library's static array holds";
         default: return "unknown status";
     }

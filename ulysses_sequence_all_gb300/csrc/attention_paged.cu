@@ -1,0 +1,733 @@
+// attention_paged.cu -- attention of the last few tokens of each sequence over a key-value cache held
+// in pages (or, without a table, over contiguous keys and values), with or without a sliding window.
+//
+// The query at position p sees the keys j < len with j <= p and (j > p - window or j < sinks). Per row
+// o = sum_j exp(s_j - m) v_j / l and lse = m + log l as in attention_fwd.cu; a row that sees no key
+// gives zeros and -infinity.
+//
+// With R = group * tokens query rows a key head, each 4 d bytes of a key and its value carry 4 d R
+// flops: below some 200 rows memory bounds it, and the design is made to keep copies in flight. All the
+// work (the blocks of 64 keys that any row of a (batch element, row group, key head) sees) is laid end
+// to end and cut into as many equal shares as CTAs run at a time, two an SM, whatever the sequences'
+// lengths: a CTA finds its share from the lengths by one scan. Each of its 4 warps takes 16 keys of a
+// block and is its own pipeline: one lane copies its next tiles (tensor maps, a box per page) into a
+// ring of its own, the warp waits for nothing but its own barrier, and no warp waits for another until
+// a sequence ends. There the warps' maxima, sums and outputs are joined through the ring's free slots;
+// a sequence that several CTAs share leaves its parts as normalised fp32 outputs with their lse, which
+// attn_paged_join_kernel adds in order: the same bits from run to run.
+//
+// Products: S^T = K Q^T and O^T += V^T P^T with keys (and columns of V) as the 16 rows of an
+// m16n8k16 product, so that a tile of 8 query rows costs no more than its own work. A product of this
+// size reads its fragments straight from the tiles that the copies left and keeps its sums in
+// registers: at R = 8 the products take a tenth of the time that the copies take, and the fifth
+// generation's 128 rows and the trip through tensor memory would buy nothing. P^T's fragments are S^T's
+// transposed, 8x8 blocks at a time.
+// P is rounded to the element type (fp16: times 2^7, so that many keys of little weight are not lost),
+// relative to a maximum that may lag by 2^8; maxima, sums and outputs are fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+
+#include "../../include/ulysses.h"
+#include "attention.h"
+#include "fused_row.cuh"
+#include "paged.h"
+#include "tensor_map.h"
+
+namespace uly {
+
+static __device__ unsigned g_attn_paged_status;
+
+constexpr int kPgThreads = 32 * kPagedWarps;
+constexpr float kPgRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
+constexpr float kPgUpF16 = 7.0f;    // fp16 probabilities are held times 2^this
+constexpr int kPgJoinThreads = 256;
+
+// ---- what there is to do ----------------------------------------------------------------------------
+
+// A batch element's row group: the keys that its rows see, and the blocks that hold them.
+struct PagedEntry {
+    int bb, rg;
+    int n;              // blocks, one at least: rows that see no key are written as well
+    int first, near;    // the first tokens' blocks 0 .. first - 1; the others from block `near` on
+    int snk, lo, end;   // some row sees key j: j < snk, or lo <= j < end
+    int len;
+    int64_t pos0;       // position of query token 0
+    int64_t t0, t1;     // its tokens
+    __device__ __forceinline__ int block(int j) const { return j < first ? j : near + j - first; }
+    __device__ __forceinline__ bool sees(int a, int b) const  // any of keys a .. b - 1
+    {
+        return a < end && (min(b, end) > lo || a < snk);
+    }
+};
+
+__device__ __forceinline__ PagedEntry paged_entry(const PagedArgs& a, int e)
+{
+    PagedEntry t;
+    t.bb = a.row_groups == 1 ? e : e / a.row_groups;
+    t.rg = e - t.bb * a.row_groups;
+    t.len = a.kv_lens ? max(0, min(a.kv_lens[t.bb], a.room)) : a.room;
+    t.pos0 = a.q_start ? int64_t(a.q_start[t.bb]) : a.from_end ? t.len - a.Sq : 0;
+    const int64_t row = int64_t(t.rg) * a.rows, rows = a.Sq * a.group;
+    t.t0 = div_fast(row, a.group);
+    t.t1 = div_fast(min(row + a.rows, rows) - 1, a.group) + 1;
+    t.end = int(max(int64_t(0), min(int64_t(t.len), t.pos0 + t.t1)));
+    t.lo = int(max(int64_t(0), min(int64_t(t.end), t.pos0 + t.t0 + 1 - a.window)));
+    t.snk = min(a.sinks, t.lo);
+    t.near = t.lo / kPagedBlock;
+    t.first = min((t.snk + kPagedBlock - 1) / kPagedBlock, t.near);
+    t.n = max(1, t.first + (t.end + kPagedBlock - 1) / kPagedBlock - t.near);
+    return t;
+}
+
+// The way through a share's blocks: entry by entry, in an entry head by head (the heads of a token lie
+// next to one another), in a head block by block.
+struct PagedWalk {
+    int64_t left;
+    int e, head, j;
+    PagedEntry en;
+    __device__ __forceinline__ void step(const PagedArgs& a)
+    {
+        --left;
+        if (++j < en.n) return;
+        j = 0;
+        if (++head < a.m_begin[a.W]) return;
+        head = 0;
+        if (left > 0) en = paged_entry(a, ++e);
+    }
+};
+
+__device__ __forceinline__ int64_t paged_share(int64_t total, int parts, int64_t c)  // its first block
+{
+    const int64_t q = total / parts, rem = total - q * parts;
+    return c * q + min(c, rem);
+}
+
+__device__ __forceinline__ int paged_owner(int64_t total, int parts, int64_t block)
+{
+    const int64_t q = total / parts, rem = total - q * parts, big = rem * (q + 1);
+    return int(block < big ? block / (q + 1) : rem + (block - big) / q);
+}
+
+// ---- the kernel -------------------------------------------------------------------------------------
+
+template <int DP>
+struct PgSmem {
+    static constexpr int kHalf = kPagedTile * 128;            // 64 columns of a tile
+    static constexpr int kV = kHalf * (DP / 64);              // values after keys
+    static constexpr int kTile = 2 * kV;
+    static constexpr int kStages = DP == 128 ? 3 : 6;
+    static constexpr int kTiles = 2048;                       // PgShared first
+    static constexpr int kTotal = kTiles + kPagedWarps * kStages * kTile;
+    static_assert(2 * (kTotal + 1024 + kSmemReservedPerCta) <= kSmemPerSm, "two CTAs an SM");
+};
+
+struct PgShared {
+    uint64_t full[kPagedWarps][6];
+    PagedWalk load[kPagedWarps];
+    float2 ml[kPagedWarps][kPagedMaxRows];  // each warp's maxima and sums
+    int slot[kPagedWarps];                  // where its outputs lie
+    int64_t warp_sum[kPagedWarps];
+    int64_t total, before;  // blocks of all; of the entries before `entry`
+    int entry;
+};
+static_assert(sizeof(PgShared) <= 2048, "shared memory");
+
+template <bool F16>
+__device__ __forceinline__ void pg_mma(float (&c)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+}
+
+// Four 8x8 blocks of 16-bit elements; lane l gives the address of row l % 8 of block l / 8.
+template <bool TRANS>
+__device__ __forceinline__ void pg_ldmatrix(uint32_t (&x)[4], uint32_t addr)
+{
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(addr)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(addr)
+                     : "memory");
+}
+
+__device__ __forceinline__ uint32_t pg_transpose(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// RT: tiles of 8 query rows.
+template <int DP, bool F16, int RT>
+__global__ void __launch_bounds__(kPgThreads, 2)
+    attn_paged_kernel(const __grid_constant__ PagedArgs a)
+{
+    using L = PgSmem<DP>;
+    using E = ElemT<F16>;
+    constexpr int K = L::kStages, kD = DP / 16, kRows = 8 * RT;
+    constexpr int kRound = RT < 2 ? RT : 2;  // tiles of rows whose outputs a slot holds
+    constexpr float kUp = F16 ? kPgUpF16 : 0.0f;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    PgShared& sh = *reinterpret_cast<PgShared*>(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* ring_at = smem + L::kTiles + warp * K * L::kTile;
+    const int nk = (a.d + 15) / 16, halves = (a.d + 63) / 64, heads = a.m_begin[a.W];
+    const float sl2 = a.scale * 1.4426950408889634f;
+    const int quad = lane >> 2, pair = (lane & 3) * 2;  // fragments: key (column of V); query row
+
+    if (lane == 0) {
+        for (int k = 0; k < K; ++k) mbar_init(&sh.full[warp][k], 1);
+        fence_barrier_init();
+    }
+
+    // How many blocks there are, and in which entry this CTA's share begins.
+    const int entries = a.b * a.row_groups;
+    const int each = (entries + kPgThreads - 1) / kPgThreads;
+    const int e0 = min(entries, int(threadIdx.x) * each), e1 = min(entries, e0 + each);
+    int64_t mine = 0;
+    for (int e = e0; e < e1; ++e) mine += paged_entry(a, e).n;
+    int64_t upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += x;
+    }
+    if (lane == 31) sh.warp_sum[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kPagedWarps; ++w) {
+        if (w < warp) upto += sh.warp_sum[w];
+        total += sh.warp_sum[w];
+    }
+    const int64_t before = upto - mine;
+    total *= heads;
+
+    StageRing ring, fill;
+    int flying = 0;  // lane 0: copies that have not been waited for
+    bool ok = true;
+
+    for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
+        const int64_t begin = paged_share(total, a.parts, c), stop = paged_share(total, a.parts, c + 1);
+        __syncthreads();
+        if (begin >= before * heads && begin < upto * heads) {
+            int64_t at = before;
+            int e = e0;
+            for (int n; begin >= (at + (n = paged_entry(a, e).n)) * heads; ++e) at += n;
+            sh.entry = e;
+            sh.before = at;
+        }
+        __syncthreads();
+        PagedShared shared = {0, 0, 0, 0};
+        if (begin < stop) {
+            PagedWalk walk;
+            walk.left = stop - begin;
+            walk.e = sh.entry;
+            walk.en = paged_entry(a, walk.e);
+            const int64_t off = begin - sh.before * heads;
+            walk.head = int(div_fast(off, walk.en.n));
+            walk.j = int(off - int64_t(walk.head) * walk.en.n);
+            if (lane == 0) sh.load[warp] = walk;
+
+            // This warp's next tile that any row sees anything of.
+            auto issue = [&]() {
+                if (lane == 0 && ok) {
+                    PagedWalk& w = sh.load[warp];
+                    while (w.left > 0) {
+                        const PagedEntry& en = w.en;
+                        const int key0 = en.block(w.j) * kPagedBlock + warp * kPagedTile;
+                        const bool any = en.sees(key0, key0 + kPagedTile);
+                        if (any) {
+                            int r = 0;
+                            while (r + 1 < a.W && w.head >= a.m_begin[r + 1]) ++r;
+                            const int kvh = w.head - a.m_begin[r];
+                            int boxes = 0;
+                            for (int k = 0; k < kPagedTile; k += a.box)
+                                boxes += en.sees(key0 + k, key0 + k + a.box);
+                            uint64_t* bar = &sh.full[warp][fill.s];
+                            mbar_arrive_expect_tx(bar, uint32_t(boxes * a.box * 256 * halves));
+                            for (int k = 0; k < kPagedTile; k += a.box) {
+                                const int key = key0 + k;
+                                if (!en.sees(key, key + a.box)) continue;
+                                int page = en.bb, row = key;
+                                if (a.table) {
+                                    const int p = key / a.page;
+                                    page = a.table[int64_t(en.bb) * a.table_pages + p];
+                                    row = key - p * a.page;
+                                    // (outside the pool a copy reads zeros)
+                                    if (page < 0 || page >= a.pages)
+                                        atomicOr(&g_attn_paged_status, kStatusBadPage);
+                                }
+                                uint8_t* to = ring_at + fill.s * L::kTile + k * 128;
+                                for (int h = 0; h < halves; ++h) {
+                                    tensor_g2s_4d(to + h * L::kHalf, &a.kmap[r], 64 * h, kvh, row, page,
+                                                  bar);
+                                    tensor_g2s_4d(to + L::kV + h * L::kHalf, &a.vmap[r], 64 * h, kvh,
+                                                  row, page, bar);
+                                }
+                            }
+                            ++flying;
+                            fill.next(K);
+                        }
+                        w.step(a);
+                        if (any) break;
+                    }
+                }
+                __syncwarp();
+            };
+            __syncwarp();
+            for (int k = 0; k < K; ++k) issue();
+
+            int64_t at = begin;  // the walk's block
+            bool pending = false;
+            while (walk.left > 0) {
+                const PagedEntry en = walk.en;
+                const int64_t seg = at - walk.j, seg_end = seg + en.n;  // its blocks
+                int r = 0;
+                while (r + 1 < a.W && walk.head >= a.m_begin[r + 1]) ++r;
+                const int head = walk.head, kvh = head - a.m_begin[r];
+                const int64_t row0 = int64_t(en.rg) * kRows, row_end = a.Sq * a.group;
+                uint32_t q[RT][kD][2];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const int64_t row = row0 + t * 8 + quad;
+                    const int64_t tok = div_fast(row, a.group);
+                    const uint8_t* src =
+                        a.q[r] + (((int64_t(en.bb) * a.Sq + tok) * a.n[r] + kvh * a.group + row -
+                                   tok * a.group) * a.d + pair) * 2;
+#pragma unroll
+                    for (int ks = 0; ks < kD; ++ks)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            q[t][ks][h] = 0;
+                            if (row < row_end && ks * 16 + h * 8 < a.d)
+                                q[t][ks][h] = __ldg(reinterpret_cast<const uint32_t*>(
+                                    src + (ks * 16 + h * 8) * 2));
+                        }
+                }
+                // keys that every row sees: below hi_all, and from lo_all on or first tokens
+                const int hi_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t0 + 1)));
+                const int lo_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t1 - a.window)));
+                float m[RT][2], l[RT][2], o[RT][kD][4];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) m[t][i] = -INFINITY, l[t][i] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kD; ++i)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[t][i][x] = 0.0f;
+                }
+                bool used = false;
+                int slot = 0;
+                do {
+                    const int key0 = en.block(walk.j) * kPagedBlock + warp * kPagedTile;
+                    if (ok && en.sees(key0, key0 + kPagedTile)) {
+                        if (pending) issue();
+                        ok = __all_sync(0xffffffffu,
+                                        mbar_wait_bounded(&sh.full[warp][ring.s], ring.phase,
+                                                          uint64_t(a.wait_us) * 1000u));
+                        if (ok) {
+                            --flying;
+                            slot = ring.s;
+                            ring.next(K);
+                            pending = used = true;
+                            uint8_t* tile = ring_at + slot * L::kTile;
+                            const bool edge = key0 + kPagedTile > hi_all ||
+                                              (key0 < lo_all && key0 + kPagedTile > a.sinks);
+                            if (edge) {
+                                // A masked probability is zero, but zero times what no row sees (or
+                                // was not even copied) may be NaN.
+                                for (int i = lane; i < kPagedTile * 8 * halves; i += 32) {
+                                    const int k = (i >> 3) & (kPagedTile - 1), h = i / (kPagedTile * 8);
+                                    if (!en.sees(key0 + k, key0 + k + 1))
+                                        st_shared_v4(tile + L::kV + h * L::kHalf + k * 128 + (i & 7) * 16,
+                                                     make_uint4(0, 0, 0, 0));
+                                }
+                                fence_proxy_async_shared();  // (before the copy into this slot)
+                                __syncwarp();
+                            }
+                            // S^T
+                            float s[RT][4];
+#pragma unroll
+                            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) s[t][x] = 0.0f;
+                            const uint32_t tile_at = smem_u32(tile);
+                            {
+                                const int k = ((lane >> 3) & 1) * 8 + (lane & 7), w = lane >> 4;
+#pragma unroll
+                                for (int ks = 0; ks < kD; ++ks) {
+                                    if (ks >= nk) break;
+                                    uint32_t x[4];
+                                    pg_ldmatrix<false>(x, tile_at + (ks >> 2) * L::kHalf + k * 128 +
+                                                              ((((ks & 3) * 2 + w) ^ (k & 7)) << 4));
+#pragma unroll
+                                    for (int t = 0; t < RT; ++t)
+                                        pg_mma<F16>(s[t], x, q[t][ks][0], q[t][ks][1]);
+                                }
+                            }
+                            if (edge) {
+#pragma unroll
+                                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        const int64_t row = row0 + t * 8 + pair + i;
+                                        const int64_t p = en.pos0 + div_fast(row, a.group);
+                                        const int64_t hi = min(int64_t(en.len), p + 1), lo = p + 1 - a.window;
+#pragma unroll
+                                        for (int x = 0; x < 2; ++x) {
+                                            const int key = key0 + quad + 8 * x;
+                                            if (key >= hi || (key < lo && key >= a.sinks))
+                                                s[t][2 * x + i] = -INFINITY;
+                                        }
+                                    }
+                            }
+                            bool grow = false;
+#pragma unroll
+                            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    grow |= (fmaxf(s[t][i], s[t][2 + i]) - m[t][i]) * sl2 > kPgRescale;
+                            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                                for (int t = 0; t < RT; ++t) {
+                                    float f[2];
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        float top = fmaxf(s[t][i], s[t][2 + i]);
+#pragma unroll
+                                        for (int x = 4; x < 32; x <<= 1)
+                                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                                        const bool up = (top - m[t][i]) * sl2 > kPgRescale;
+                                        f[i] = up ? ex2((m[t][i] - top) * sl2) : 1.0f;
+                                        if (up) m[t][i] = top;
+                                        l[t][i] *= f[i];
+                                    }
+#pragma unroll
+                                    for (int i = 0; i < kD; ++i) {
+                                        o[t][i][0] *= f[0], o[t][i][2] *= f[0];
+                                        o[t][i][1] *= f[1], o[t][i][3] *= f[1];
+                                    }
+                                }
+                            }
+                            uint32_t p[RT][2];
+#pragma unroll
+                            for (int t = 0; t < RT; ++t) {
+                                float e[4];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const float base = (m[t][i] == -INFINITY ? 0.0f : -m[t][i] * sl2) + kUp;
+                                    e[i] = ex2(fmaf(s[t][i], sl2, base));
+                                    e[2 + i] = ex2(fmaf(s[t][2 + i], sl2, base));
+                                    l[t][i] += e[i] + e[2 + i];
+                                }
+                                p[t][0] = pg_transpose(E::pack(e[0], e[1]));
+                                p[t][1] = pg_transpose(E::pack(e[2], e[3]));
+                            }
+                            // O^T
+                            {
+                                const int k = (lane >> 4) * 8 + (lane & 7), w = (lane >> 3) & 1;
+                                const uint32_t v_at = tile_at + L::kV + k * 128;
+#pragma unroll
+                                for (int i = 0; i < kD; ++i) {
+                                    if (i >= nk) break;
+                                    uint32_t x[4];
+                                    pg_ldmatrix<true>(x, v_at + (i >> 2) * L::kHalf +
+                                                             ((((i & 3) * 2 + w) ^ (k & 7)) << 4));
+#pragma unroll
+                                    for (int t = 0; t < RT; ++t) pg_mma<F16>(o[t][i], x, p[t][0], p[t][1]);
+                                }
+                            }
+                        }
+                    }
+                    ++at;
+                    walk.step(a);
+                } while (walk.left > 0 && at < seg_end);
+
+                // Join the warps: a row's maximum, sum and output.
+                const bool whole = seg >= begin && seg_end <= stop;
+                const int64_t part = 2 * int64_t(c) + (seg >= begin ? 1 : 0);
+                if (seg >= begin && seg_end > stop)
+                    shared = {paged_owner(total, a.parts, seg_end - 1) - c + 1, en.bb, en.rg, head};
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1)
+                            l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], x);
+                        if (lane < 4) sh.ml[warp][t * 8 + pair + i] = make_float2(m[t][i], l[t][i]);
+                    }
+                if (lane == 0) sh.slot[warp] = used ? slot : -1;
+                float* own = reinterpret_cast<float*>(ring_at + slot * L::kTile);
+#pragma unroll
+                for (int t0 = 0; t0 < RT; t0 += kRound) {
+                    if (t0 > 0) __syncthreads();
+                    __syncwarp();
+                    if (used) {
+#pragma unroll
+                        for (int t = 0; t < kRound; ++t)
+#pragma unroll
+                            for (int i = 0; i < kD; ++i)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    own[(t * 8 + pair + (x & 1)) * DP +
+                                        ((i * 16 + (x >> 1) * 8 + quad) ^ (pair << 2))] = o[t0 + t][i][x];
+                    }
+                    __syncthreads();
+                    for (int it = threadIdx.x; it < kRound * 8 * (DP / 8); it += kPgThreads) {
+                        const int row = it / (DP / 8), col = it % (DP / 8) * 8;
+                        const int64_t to = row0 + t0 * 8 + row;
+                        if (col >= a.d) continue;
+                        float top = -INFINITY, sum = 0.0f, y[8];
+#pragma unroll
+                        for (int w = 0; w < kPagedWarps; ++w) top = fmaxf(top, sh.ml[w][t0 * 8 + row].x);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+#pragma unroll
+                        for (int w = 0; w < kPagedWarps; ++w) {
+                            const float2 z = sh.ml[w][t0 * 8 + row];
+                            if (sh.slot[w] < 0 || z.x == -INFINITY) continue;
+                            const float f = ex2((z.x - top) * sl2);
+                            sum = fmaf(f, z.y, sum);
+                            const float* from = reinterpret_cast<const float*>(
+                                smem + L::kTiles + (w * K + sh.slot[w]) * L::kTile);
+#pragma unroll
+                            for (int k = 0; k < 8; k += 4) {
+                                const float4 v = *reinterpret_cast<const float4*>(
+                                    from + row * DP + ((col + k) ^ (((row >> 1) & 3) << 3)));
+                                y[k] = fmaf(f, v.x, y[k]);
+                                y[k + 1] = fmaf(f, v.y, y[k + 1]);
+                                y[k + 2] = fmaf(f, v.z, y[k + 2]);
+                                y[k + 3] = fmaf(f, v.w, y[k + 3]);
+                            }
+                        }
+                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // NaN stays NaN
+                        const float lse = sum == 0.0f ? -INFINITY
+                                                      : top * a.scale + (logf(sum) - kUp * 0.69314718056f);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] *= inv;
+                        if (!whole) {
+                            const int64_t at_row = part * kRows + t0 * 8 + row;
+                            float4* dst = reinterpret_cast<float4*>(a.part_o + at_row * a.d + col);
+                            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                            if (col == 0) a.part_lse[at_row] = lse;
+                        } else if (to < row_end) {
+                            const int64_t tok = div_fast(to, a.group);
+                            const int64_t h = kvh * a.group + (to - tok * a.group);
+                            st_v4(a.o[r] + (((int64_t(en.bb) * a.Sq + tok) * a.n[r] + h) * a.d + col) * 2,
+                                  make_uint4(E::pack(y[0], y[1]), E::pack(y[2], y[3]),
+                                             E::pack(y[4], y[5]), E::pack(y[6], y[7])));
+                            if (col == 0) a.lse[r][(int64_t(en.bb) * a.n[r] + h) * a.Sq + tok] = lse;
+                        }
+                    }
+                }
+                fence_proxy_async_shared();  // (a copy comes into this slot next)
+                __syncthreads();
+                if (pending) issue();
+                pending = false;
+            }
+        }
+        if (threadIdx.x == 0) a.shared[c] = shared;
+    }
+    if (!ok && lane == 0) {
+        atomicOr(&g_attn_paged_status, kStatusWaitTimeout);
+        // leave no copy into this CTA's shared memory in flight
+        for (; flying > 0; --flying) {
+            if (!mbar_wait_bounded(&sh.full[warp][ring.s], ring.phase))
+                atomicOr(&g_attn_paged_status, kStatusDrainTimeout);
+            ring.next(K);
+        }
+    }
+    let_next_start();
+}
+
+// Joins what several CTAs made of a row group: block x looks at CTA x's note. `y_rows` of its warps take
+// a row each, the others of a row every (warps / y_rows)-th part; a lane has 4 columns.
+template <bool F16>
+__global__ void __launch_bounds__(kPgJoinThreads)
+    attn_paged_join_kernel(const __grid_constant__ PagedArgs a, int y_rows)
+{
+    using E = ElemT<F16>;
+    constexpr int kWarps = kPgJoinThreads / 32;
+    __shared__ float4 acc_at[kWarps][32];
+    __shared__ float2 ml_at[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ways = kWarps / y_rows, way = warp % ways;
+    wait_for_previous();
+    for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
+        const PagedShared s = a.shared[c];
+        if (s.parts == 0) continue;
+        for (int row0 = blockIdx.y * y_rows; row0 < a.rows; row0 += gridDim.y * y_rows) {
+            const int row = row0 + warp / ways;
+            float top = -INFINITY, sum = 0.0f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            auto slot = [&](int p) {
+                return (p == 0 ? 2 * int64_t(c) + 1 : 2 * int64_t(c + p)) * a.rows + row;
+            };
+            for (int p = way; p < s.parts; p += ways) top = fmaxf(top, a.part_lse[slot(p)]);
+            for (int p0 = way; p0 < s.parts; p0 += 4 * ways) {
+                float4 o[4];
+                float f[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int p = p0 + k * ways;
+                    f[k] = -INFINITY;
+                    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p >= s.parts) continue;
+                    f[k] = a.part_lse[slot(p)];
+                    if (lane * 4 < a.d)
+                        o[k] = *reinterpret_cast<const float4*>(a.part_o + slot(p) * a.d + lane * 4);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float w = f[k] == -INFINITY ? 0.0f : expf(f[k] - top);  // (NaN stays NaN)
+                    sum += w;
+                    acc.x = fmaf(w, o[k].x, acc.x);
+                    acc.y = fmaf(w, o[k].y, acc.y);
+                    acc.z = fmaf(w, o[k].z, acc.z);
+                    acc.w = fmaf(w, o[k].w, acc.w);
+                }
+            }
+            if (ways > 1) {  // the ways of a row, in order
+                acc_at[warp][lane] = acc;
+                if (lane == 0) ml_at[warp] = make_float2(top, sum);
+                __syncthreads();
+                if (way == 0) {
+                    float most = top;
+                    for (int w = 1; w < ways; ++w) most = fmaxf(most, ml_at[warp + w].x);
+                    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    sum = 0.0f;
+                    for (int w = 0; w < ways; ++w) {
+                        const float2 z = ml_at[warp + w];
+                        if (z.x == -INFINITY && z.y == 0.0f) continue;
+                        const float f = expf(z.x - most);
+                        const float4 y = acc_at[warp + w][lane];
+                        sum = fmaf(f, z.y, sum);
+                        acc.x = fmaf(f, y.x, acc.x);
+                        acc.y = fmaf(f, y.y, acc.y);
+                        acc.z = fmaf(f, y.z, acc.z);
+                        acc.w = fmaf(f, y.w, acc.w);
+                    }
+                    top = most;
+                }
+                __syncthreads();
+            }
+            const int64_t to = int64_t(s.group) * a.rows + row;
+            if (way != 0 || to >= a.Sq * a.group) continue;
+            int r = 0;
+            while (r + 1 < a.W && s.head >= a.m_begin[r + 1]) ++r;
+            const int64_t tok = div_fast(to, a.group);
+            const int64_t h = int64_t(s.head - a.m_begin[r]) * a.group + (to - tok * a.group);
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            if (lane * 4 < a.d)
+                st_v2(a.o[r] + (((int64_t(s.bb) * a.Sq + tok) * a.n[r] + h) * a.d + lane * 4) * 2,
+                      E::pack(acc.x * inv, acc.y * inv), E::pack(acc.z * inv, acc.w * inv));
+            if (lane == 0)
+                a.lse[r][(int64_t(s.bb) * a.n[r] + h) * a.Sq + tok] = sum == 0.0f ? top : top + logf(sum);
+        }
+    }
+}
+
+// ---- host -------------------------------------------------------------------------------------------
+
+void attn_paged_split(PagedArgs* a, int sm_count)
+{
+    const int64_t rows = a->Sq * a->group;
+    a->rows = rows <= 8 ? 8 : rows <= 16 ? 16 : kPagedMaxRows;
+    a->row_groups = int32_t((rows + a->rows - 1) / a->rows);
+    a->parts = 2 * sm_count;
+}
+
+template <int DP, bool F16, int RT>
+static cudaError_t pg_launch(const PagedArgs& a, cudaStream_t stream, int device, int64_t cap,
+                             int sm_count)
+{
+    static std::atomic<unsigned long long> raised{0};
+    const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
+    constexpr int smem = PgSmem<DP>::kTotal + 1024;
+    if (bit && !(raised.load() & bit)) {
+        cudaError_t e = cudaFuncSetAttribute(attn_paged_kernel<DP, F16, RT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        raised.fetch_or(bit);
+    }
+    const unsigned grid = unsigned(a.parts < cap ? a.parts : cap);
+    attn_paged_kernel<DP, F16, RT><<<grid, kPgThreads, smem, stream>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // Few sequences are shared by many CTAs each: then a block has one row, its warps the parts.
+    const int64_t groups = int64_t(a.b) * a.row_groups * a.m_begin[a.W];
+    const int y_rows = groups * 8 <= a.parts ? 1 : kPgJoinThreads / 32;
+    unsigned y = unsigned(a.rows / y_rows);
+    if (int64_t(grid) * y > cap) y = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, y);
+    cfg.blockDim = dim3(kPgJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = cap == kAttnMostCtas ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, attn_paged_join_kernel<F16>, a, y_rows);
+}
+
+template <int DP, bool F16>
+static cudaError_t pg_launch_rows(const PagedArgs& a, cudaStream_t stream, int device, int64_t cap,
+                                  int sm_count)
+{
+    if (a.rows == 8) return pg_launch<DP, F16, 1>(a, stream, device, cap, sm_count);
+    if (a.rows == 16) return pg_launch<DP, F16, 2>(a, stream, device, cap, sm_count);
+    return pg_launch<DP, F16, 4>(a, stream, device, cap, sm_count);
+}
+
+cudaError_t attn_paged_launch(PagedArgs& a, const void* const* k, const void* const* v,
+                              cudaStream_t stream, int device, int64_t cap, int sm_count)
+{
+    if (a.m_begin[a.W] == 0) return cudaSuccess;
+    for (int r = 0; r < a.W; ++r) {
+        const int m = a.m_begin[r + 1] - a.m_begin[r];
+        if (m == 0) continue;
+        if (!encode_head_map(&a.kmap[r], k[r], a.f16, a.d, m, a.page, a.pages, 1, a.box) ||
+            !encode_head_map(&a.vmap[r], v[r], a.f16, a.d, m, a.page, a.pages, 1, a.box))
+            return cudaErrorInvalidValue;
+    }
+    if (a.d <= 64)
+        return a.f16 ? pg_launch_rows<64, true>(a, stream, device, cap, sm_count)
+                     : pg_launch_rows<64, false>(a, stream, device, cap, sm_count);
+    return a.f16 ? pg_launch_rows<128, true>(a, stream, device, cap, sm_count)
+                 : pg_launch_rows<128, false>(a, stream, device, cap, sm_count);
+}
+
+cudaError_t attn_paged_status(unsigned* status, bool clear)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_attn_paged_status, sizeof(unsigned));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_attn_paged_status, &zero, sizeof(unsigned));
+}
+
+}  // namespace uly

@@ -1,0 +1,72 @@
+// paged.h -- argument blocks of the kernels of the paged key-value cache, shared by api.cu,
+// cache_append.cu and attention_paged.cu.
+//
+// A rank's keys (and values) lie in a pool of pages, (pages, page, m_r, d): the head-side tensor of a
+// plan whose batch is the pages and whose sequence is a page. Key j of batch element bb is row
+// j % page of page table[bb][j / page].
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "plan.h"
+
+namespace uly {
+
+constexpr unsigned kStatusBadPage = 4u;  // a page outside the pool was needed
+constexpr int kPagedTile = 16;           // keys that a warp takes at a time
+constexpr int kPagedWarps = 4;
+constexpr int kPagedBlock = kPagedTile * kPagedWarps;
+constexpr int kPagedMaxRows = 32;        // query rows of one pass over the keys
+
+struct AppendArgs {
+    const uint8_t* src[2][kMaxW];  // new keys, values: (b, tokens, m_r, d)
+    uint8_t* dst[2][kMaxW];        // pools: (pages, page, m_r, d)
+    uint32_t words[kMaxW];         // 16-byte words of a token, m_r * d * e / 16
+    const int32_t *table, *starts, *counts;  // counts: null (all tokens)
+    int64_t b, tokens, table_pages;
+    int64_t pages, page;
+    int32_t W;
+};
+
+// A batch element's row group (`rows` query rows) that several CTAs share: CTA `first` holds its
+// beginning, the next parts - 1 the rest.
+struct PagedShared {
+    int32_t parts;  // 0: none
+    int32_t bb, group, head;
+};
+
+struct PagedArgs {
+    CUtensorMap kmap[kMaxW], vmap[kMaxW];  // boxes of `box` rows of a page, one head
+    const uint8_t* q[kMaxW];
+    uint8_t* o[kMaxW];
+    float* lse[kMaxW];
+    int32_t n[kMaxW], m_begin[kMaxW + 1];  // query heads; prefix of key heads over the ranks
+    const int32_t* table;    // (b, table_pages); null: batch element bb's only page is bb
+    const int32_t* kv_lens;  // (b) or null: `room`
+    const int32_t* q_start;  // (b) or null: from_end: the keys' count less Sq, else zeros
+    int64_t Sq, table_pages;
+    int32_t W, b, d, group, f16;
+    int32_t pages, page, box, from_end;
+    int32_t room;            // keys that a batch element's pages can hold
+    int32_t sinks;
+    int64_t window;          // beyond every position where there is none
+    int32_t rows, row_groups;  // query rows of a pass (8, 16, 32); passes of a key head
+    int32_t parts;             // shares of all the work, one CTA at a time works on one
+    float scale;
+    uint32_t wait_us;
+    float* part_o;         // [2 parts][rows][d] normalised partial outputs
+    float* part_lse;       // [2 parts][rows]
+    PagedShared* shared;   // [parts]
+};
+
+cudaError_t cache_append_launch(const AppendArgs& a, cudaStream_t stream, int64_t cap, int sm_count);
+// Rows, passes and shares from the shape and the device alone: a CTA cap changes no bit.
+void attn_paged_split(PagedArgs* a, int sm_count);
+cudaError_t attn_paged_launch(PagedArgs& a, const void* const* k, const void* const* v,
+                              cudaStream_t stream, int device, int64_t cap, int sm_count);
+cudaError_t cache_append_status(unsigned* status, bool clear);
+cudaError_t attn_paged_status(unsigned* status, bool clear);
+
+}  // namespace uly
