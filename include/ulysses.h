@@ -491,8 +491,48 @@ int ulysses_attention_backward_workspace(ulysses_plan_t q_plan, ulysses_plan_t k
                                          size_t* bytes);
 
 /*
- * A key-value cache held in pages, for answering token by token after a long prompt (the pages have no
- * counterpart: their collective ends where attention begins). Rank r's keys, and its values, lie in a
+ * ulysses_attention with a sliding window: the query at position p = q_start[bb] + i sees the keys
+ * j < kv_lens[bb] with j <= p and j > p - window or j < sinks, its own key, those of the window - 1
+ * positions before it and the sequence's first ones. Work grows with the window, not with the sequence.
+ *   window  >= 1 (1: the query's own key); one that reaches past the first key is causal attention.
+ *   sinks   >= 0 first tokens that stay visible.
+ * Everything else is as for ulysses_attention with causal = 1: shapes, plans, masks, empty rows, what
+ * hidden keys may hold (anything where no row of the batch element sees them, before a window that
+ * continues a cache too; finite where only some rows do), precision, order of sums, the CTA cap, statuses.
+ * workspace  device memory of ulysses_attention_window_workspace bytes (0: may be NULL), 16-byte aligned.
+ */
+int ulysses_attention_window(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, const void* const* q,
+                             const void* const* k, const void* const* v, void* const* o,
+                             float* const* lse, const int32_t* kv_lens, const int32_t* q_start,
+                             int64_t window, int64_t sinks, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ulysses_attention_window for these plans and this window on the current device. */
+int ulysses_attention_window_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, int64_t window,
+                                       int64_t sinks, size_t* bytes);
+
+/*
+ * Gradient of ulysses_attention_window, as ulysses_attention_backward with the window and the first tokens
+ * of the forward. First tokens are seen by every row behind them: with enough rows their gradients are
+ * summed in several parts (fp32, in the workspace), which a fourth launch adds in order.
+ * workspace  device memory of ulysses_attention_window_backward_workspace bytes, 16-byte aligned.
+ */
+int ulysses_attention_window_backward(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, void* const* dq,
+                                      void* const* dk, void* const* dv, const void* const* q,
+                                      const void* const* k, const void* const* v, const void* const* o,
+                                      const float* const* lse, const void* const* go,
+                                      const int32_t* kv_lens, const int32_t* q_start, int64_t window,
+                                      int64_t sinks, float scale, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ulysses_attention_window_backward for these plans and this window on the current
+ * device. */
+int ulysses_attention_window_backward_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan,
+                                                int64_t window, int64_t sinks, size_t* bytes);
+
+/*
+ * A key-value cache held in pages, for answering token by token after a long prompt (the collective
+ * that this library restates ends where attention begins and has no counterpart). Rank r's keys, and its values, lie in a
  * pool (pages, page, m_r, d): the head-side tensor of cache_plan, a plan whose batch b is the number of
  * pages and whose sequence S is the tokens of a page, a multiple of 8; only the total of its seq_splits
  * matters. Every rank has the same pages:

@@ -26,13 +26,14 @@ def axis_pairs(d: int, axes: int) -> list[int]:
 
 
 def attention_block(plan: B.Plan, qkv, rms_w, eps: float = 1e-6, rope_theta: float = 1e4,
-                    scale: float | None = None, causal: bool = False, kv_lens=None):
+                    scale: float | None = None, causal: bool = False, kv_lens=None,
+                    window: int | None = None, sinks: int = 0):
     """Attention of packed shards: qkv is W tensors (b, s_q, 3, N, d), rms_w (2, d) fp32 the norm
     weights of q and k. The plan's RoPE settings hold (ulysses_plan_set_rope_grid gives positions
-    of several axes). kv_lens: b key counts where the batch is padded at its end. Differentiable
-    in qkv and rms_w. Returns W tensors (b, s_q, N, d)."""
+    of several axes). kv_lens: b key counts where the batch is padded at its end. window, sinks: causal
+    attention to the last `window` tokens and the first `sinks`. Differentiable in qkv and rms_w. Returns W tensors (b, s_q, N, d)."""
     q, k, v = A.qkv_fused(plan, qkv, rms_w, eps, rope_theta)
-    o = A.attention(plan, plan, q, k, v, scale, causal, kv_lens)
+    o = A.attention(plan, plan, q, k, v, scale, causal, kv_lens, window=window, sinks=sinks)
     return A.a2a_4d(plan, o, mode=1)
 
 
@@ -44,6 +45,8 @@ def main(argv=None):
     ap.add_argument("--ranks", type=int, default=8)
     ap.add_argument("--d", type=int, default=128)
     ap.add_argument("--backward", action="store_true")
+    ap.add_argument("--window", type=int, help="causal attention to the last WINDOW tokens")
+    ap.add_argument("--sinks", type=int, default=0, help="first tokens that stay visible beside them")
     args = ap.parse_args(argv)
     W, d, N = args.ranks, args.d, args.heads
     if N % W:
@@ -72,11 +75,12 @@ def main(argv=None):
         return out
 
     q, k, v = timed("norm, rotation, to heads", lambda: A.qkv_fused(plan, qkv, rms_w, 1e-6, 1e4))
-    o = timed("attention", lambda: A.attention(plan, plan, q, k, v))
+    o = timed("attention", lambda: A.attention(plan, plan, q, k, v, window=args.window,
+                                                    sinks=args.sinks))
     timed("back to the sequence", lambda: A.a2a_4d(plan, o, mode=1))
     if args.backward:
         def step():
-            out = attention_block(plan, qkv, rms_w)
+            out = attention_block(plan, qkv, rms_w, window=args.window, sinks=args.sinks)
             torch.autograd.backward(out, [torch.ones_like(x) for x in out])
         timed("block, forward and backward", step)
     if B.ulysses_device_status():

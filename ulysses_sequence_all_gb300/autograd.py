@@ -15,9 +15,10 @@ plan for the backward:
 * ``packed_fused(plan, packed, planes, q_plane, k_plane, rms_w, eps, rope_theta)``: the call on
   any packing of C planes per token (QKVG, ...); its backward is
   ``ulysses_a2a_4d_packed_fused_backward``; a token's columns beyond its planes get zero gradient.
-* ``attention(q_plan, kv_plan, q, k, v, scale, causal, kv_lens, q_start)``: attention of every
-  rank's heads over the whole sequence; its backward is ``ulysses_attention_backward``, from the
-  output and the log-sum-exp that the forward keeps.
+* ``attention(q_plan, kv_plan, q, k, v, scale, causal, kv_lens, q_start, window, sinks)``: attention
+  of every rank's heads over the whole sequence, or with a sliding window and the first tokens; its
+  backward is ``ulysses_attention_backward`` (``ulysses_attention_window_backward``), from the output
+  and the log-sum-exp that the forward keeps.
 
 Inputs and outputs are lists of W tensors (one per virtual rank) on the current CUDA device;
 the outputs are new tensors the caller owns. The relayout can be differentiated again, the others
@@ -212,7 +213,7 @@ def packed_fused(plan: B.Plan, packed, planes: int, q_plane: int, k_plane: int,
 
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q_plan, kv_plan, scale, causal, kv_lens, q_start, *qkv):
+    def forward(ctx, q_plan, kv_plan, scale, causal, kv_lens, q_start, window, *qkv):
         W = len(qkv) // 3
         qkv = [x.contiguous() for x in qkv]
         q, k, v = qkv[:W], qkv[W:2 * W], qkv[2 * W:]
@@ -221,10 +222,14 @@ class _Attention(torch.autograd.Function):
         out = [torch.empty_like(x) for x in q]
         lse = [torch.empty((x.shape[0], x.shape[2], x.shape[1]), dtype=torch.float32,
                            device=x.device) for x in q]
-        need = B.ulysses_attention_workspace(q_plan, kv_plan)
+        need = (B.ulysses_attention_window_workspace(q_plan, kv_plan, *window) if window else
+                B.ulysses_attention_workspace(q_plan, kv_plan))
         ws = torch.empty(need, dtype=torch.uint8, device=q[0].device) if need else None
-        B.ulysses_attention(q_plan, kv_plan, q, k, v, out, lse, scale, causal, kv_lens, q_start, ws)
-        ctx.plans, ctx.scale, ctx.causal, ctx.W = (q_plan, kv_plan), scale, causal, W
+        if window:
+            B.ulysses_attention_window(q_plan, kv_plan, q, k, v, out, lse, scale, *window, kv_lens, q_start, ws)
+        else:
+            B.ulysses_attention(q_plan, kv_plan, q, k, v, out, lse, scale, causal, kv_lens, q_start, ws)
+        ctx.plans, ctx.scale, ctx.causal, ctx.W, ctx.window = (q_plan, kv_plan), scale, causal, W, window
         ctx.save_for_backward(kv_lens, q_start, *qkv, *out, *lse)
         return tuple(out)
 
@@ -236,11 +241,17 @@ class _Attention(torch.autograd.Function):
         q, k, v, out, lse = (saved[i * W:(i + 1) * W] for i in range(5))
         go = _grads(grads, ctx.plans[0], 0, q[0])
         dq, dk, dv = ([torch.empty_like(x) for x in t] for t in (q, k, v))
-        ws = torch.empty(B.ulysses_attention_backward_workspace(*ctx.plans), dtype=torch.uint8,
-                         device=q[0].device)
-        B.ulysses_attention_backward(*ctx.plans, dq, dk, dv, q, k, v, out, lse, go, ctx.scale,
-                                     ctx.causal, kv_lens, q_start, ws)
-        return (None,) * 6 + (*dq, *dk, *dv)
+        window = ctx.window
+        need = (B.ulysses_attention_window_backward_workspace(*ctx.plans, *window) if window else
+                B.ulysses_attention_backward_workspace(*ctx.plans))
+        ws = torch.empty(need, dtype=torch.uint8, device=q[0].device)
+        if window:
+            B.ulysses_attention_window_backward(*ctx.plans, dq, dk, dv, q, k, v, out, lse, go, ctx.scale,
+                                                *window, kv_lens, q_start, ws)
+        else:
+            B.ulysses_attention_backward(*ctx.plans, dq, dk, dv, q, k, v, out, lse, go, ctx.scale,
+                                         ctx.causal, kv_lens, q_start, ws)
+        return (None,) * 7 + (*dq, *dk, *dv)
 
 
 def _counts(x, b, device, what):
@@ -270,12 +281,17 @@ def _check_heads(plan, xs, what):
 
 
 def attention(q_plan: B.Plan, kv_plan: B.Plan, q, k, v, scale: float | None = None,
-              causal: bool = False, kv_lens=None, q_start=None):
+              causal: bool = False, kv_lens=None, q_start=None, window: int | None = None,
+              sinks: int = 0):
     """Attention of every rank's heads over the whole sequence, on the head-side tensors that mode
     0 returns (lists of W: q (b, Sq, n_r, d), k and v (b, Skv, m_r, d)), differentiable in q, k and
     v; `scale` defaults to d ** -0.5. kv_lens and q_start: b whole numbers, a tensor on any device or
-    a list. Returns a list of W tensors shaped as q."""
+    a list. With a `window` the query at position p sees the keys j <= p that are younger than p - window
+    or among the first `sinks` (`causal` need not be given then). Returns a list of W tensors shaped as q."""
+    if window is None and sinks:
+        raise ValueError("sinks: the first tokens that stay visible beside a window, which is not given")
     for plan, xs, what in ((q_plan, q, "q"), (kv_plan, k, "k"), (kv_plan, v, "v")):
         _check_heads(plan, xs, what)
     scale = q_plan.d ** -0.5 if scale is None else scale
-    return list(_Attention.apply(q_plan, kv_plan, scale, causal, kv_lens, q_start, *q, *k, *v))
+    window = None if window is None else (window, sinks)
+    return list(_Attention.apply(q_plan, kv_plan, scale, causal, kv_lens, q_start, window, *q, *k, *v))

@@ -39,6 +39,8 @@ EXPORTS = ["ulysses_plan", "ulysses_plan_destroy", "ulysses_plan_set_chunk_bytes
            "ulysses_a2a_4d_qkv_fused_backward", "ulysses_a2a_4d_packed_fused_backward",
            "ulysses_attention", "ulysses_attention_workspace",
            "ulysses_attention_backward", "ulysses_attention_backward_workspace",
+           "ulysses_attention_window", "ulysses_attention_window_workspace",
+           "ulysses_attention_window_backward", "ulysses_attention_window_backward_workspace",
            "ulysses_attention_paged", "ulysses_attention_paged_workspace", "ulysses_cache_append",
            "ulysses_a2a_4d_host", "ulysses_a2a_4d_qk_fused_host", "ulysses_device_status",
            "ulysses_selftest_wait_timeout", "ulysses_selftest_attention_wait_limit",
@@ -117,6 +119,15 @@ def _lib():
                                                    ctypes.c_size_t, _p]
         lib.ulysses_attention_backward_workspace.argtypes = [_p, _p,
                                                              ctypes.POINTER(ctypes.c_size_t)]
+        lib.ulysses_attention_window.argtypes = [_p, _p, _pp, _pp, _pp, _pp, _pp, _p, _p, _i64, _i64,
+                                                 ctypes.c_float, _p, ctypes.c_size_t, _p]
+        lib.ulysses_attention_window_workspace.argtypes = [_p, _p, _i64, _i64,
+                                                           ctypes.POINTER(ctypes.c_size_t)]
+        lib.ulysses_attention_window_backward.argtypes = [
+            _p, _p, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _pp, _p, _p, _i64, _i64, ctypes.c_float, _p,
+            ctypes.c_size_t, _p]
+        lib.ulysses_attention_window_backward_workspace.argtypes = [_p, _p, _i64, _i64,
+                                                                    ctypes.POINTER(ctypes.c_size_t)]
         lib.ulysses_attention_paged.argtypes = [_p, _p, _pp, _pp, _pp, _pp, _pp, _p, _i64, _p, _p, _i64,
                                                 _i64, ctypes.c_float, _p, ctypes.c_size_t, _p]
         lib.ulysses_attention_paged_workspace.argtypes = [_p, _p, ctypes.POINTER(ctypes.c_size_t)]
@@ -453,6 +464,48 @@ def ulysses_attention_backward(q_plan: Plan, kv_plan: Plan, dq, dk, dv, q, k, v,
         _ptrs(lse), _ptrs(go), _counts(kv_lens, q_plan.b, "kv_lens"),
         _counts(q_start, q_plan.b, "q_start"), int(causal), scale,
         _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_backward")
+
+
+def ulysses_attention_window_workspace(q_plan: Plan, kv_plan: Plan, window: int, sinks: int = 0) -> int:
+    """Workspace bytes ulysses_attention_window needs for these plans on the current device."""
+    n = ctypes.c_size_t()
+    _check(_lib().ulysses_attention_window_workspace(q_plan, kv_plan, window, sinks, ctypes.byref(n)),
+           "ulysses_attention_window_workspace")
+    return n.value
+
+
+def ulysses_attention_window(q_plan: Plan, kv_plan: Plan, q, k, v, out, lse, scale: float, window: int,
+                             sinks: int = 0, kv_lens=None, q_start=None, workspace=None, stream=None):
+    """Causal attention in which the query at position p sees the keys j > p - window and the first
+    `sinks` ones. Tensors and masks as ulysses_attention. `workspace` is a device tensor of at least
+    ulysses_attention_window_workspace(q_plan, kv_plan, window, sinks) bytes (None where that is 0)."""
+    _check(_lib().ulysses_attention_window(
+        q_plan, kv_plan, _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out), _ptrs(lse),
+        _counts(kv_lens, q_plan.b, "kv_lens"), _counts(q_start, q_plan.b, "q_start"), window, sinks, scale,
+        _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_window")
+
+
+def ulysses_attention_window_backward_workspace(q_plan: Plan, kv_plan: Plan, window: int,
+                                                sinks: int = 0) -> int:
+    """Workspace bytes ulysses_attention_window_backward needs for these plans on the current device."""
+    n = ctypes.c_size_t()
+    _check(_lib().ulysses_attention_window_backward_workspace(q_plan, kv_plan, window, sinks,
+                                                              ctypes.byref(n)),
+           "ulysses_attention_window_backward_workspace")
+    return n.value
+
+
+def ulysses_attention_window_backward(q_plan: Plan, kv_plan: Plan, dq, dk, dv, q, k, v, out, lse, go,
+                                      scale: float, window: int, sinks: int = 0, kv_lens=None,
+                                      q_start=None, workspace=None, stream=None):
+    """Gradient of ulysses_attention_window into dq, dk, dv from its inputs, its outputs and the gradient
+    `go` of out. `workspace` is a device tensor of at least
+    ulysses_attention_window_backward_workspace(q_plan, kv_plan, window, sinks) bytes."""
+    _check(_lib().ulysses_attention_window_backward(
+        q_plan, kv_plan, _ptrs(dq), _ptrs(dk), _ptrs(dv), _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out),
+        _ptrs(lse), _ptrs(go), _counts(kv_lens, q_plan.b, "kv_lens"),
+        _counts(q_start, q_plan.b, "q_start"), window, sinks, scale, _addr(workspace), _nbytes(workspace),
+        _stream(stream)), "ulysses_attention_window_backward")
 
 
 def ulysses_attention_paged_workspace(q_plan: Plan, cache_plan: Plan) -> int:

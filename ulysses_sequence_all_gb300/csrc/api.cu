@@ -837,6 +837,8 @@ int run_host_pipe(const Plan& p, const PipeChunks& pc, HostPipe* hp, cudaStream_
 constexpr uint32_t kAttnWaitUs = uint32_t(kWaitLimitNs / 1000);
 std::atomic<uint32_t> attention_wait_us{kAttnWaitUs};  // of launches from now on (self-test)
 
+constexpr int64_t kAttnFar = int64_t(1) << 40;  // a window beyond every position
+
 // What the two plans of an attention call make together, or ULY_EINVAL.
 int attn_shape(const Plan& qp, const Plan& kp, AttnShape* s)
 {
@@ -904,6 +906,20 @@ int attn_masks(AttnShape* s, float scale, int causal, const int32_t* kv_lens, co
     return ULY_OK;
 }
 
+struct Window {
+    int64_t keys, sinks;
+};
+
+// The window of a windowed call.
+int attn_window(AttnShape* s, int64_t window, int64_t sinks)
+{
+    if (window < 1 || sinks < 0) return ULY_EINVAL;
+    s->causal = 1;
+    s->window = window < kAttnFar ? window : kAttnFar;
+    s->sinks = int32_t(sinks < s->Skv ? sinks : s->Skv);
+    return ULY_OK;
+}
+
 // Pointers and byte counts gathered for the overlap check of an attention call.
 struct RangeList {
     const void* p[8 * kMaxW + 4];
@@ -934,14 +950,15 @@ void attn_bytes(const Plan& qp, const Plan& kp, int64_t* q_b, int64_t* kv_b, int
 
 int attn_fwd_device(const Plan& qp, const Plan& kp, const void* const* q, const void* const* k,
                     const void* const* v, void* const* o, float* const* lse,
-                    const int32_t* kv_lens, const int32_t* q_start, int causal, float scale,
-                    void* workspace, size_t workspace_bytes, cudaStream_t stream)
+                    const int32_t* kv_lens, const int32_t* q_start, int causal, const Window* window,
+                    float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream)
 {
     AttnFwdArgs a;
     std::memset(&a, 0, sizeof a);
     int rc = attn_shape(qp, kp, &a.s);
     if (rc) return rc;
     if ((rc = attn_masks(&a.s, scale, causal, kv_lens, q_start))) return rc;
+    if (window && (rc = attn_window(&a.s, window->keys, window->sinks))) return rc;
     const int W = qp.W;
     int64_t q_b[kMaxW], kv_b[kMaxW], lse_b[kMaxW];
     attn_bytes(qp, kp, q_b, kv_b, lse_b);
@@ -974,8 +991,8 @@ int attn_fwd_device(const Plan& qp, const Plan& kp, const void* const* q, const 
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
 
-// Tiles of a backward call, the bytes of its workspace and the places in it.
-size_t attn_bwd_setup(AttnBwdArgs* a, void* workspace)
+// Tiles of a backward call, the bytes of its workspace and the places in it. sm_count: with a window.
+size_t attn_bwd_setup(AttnBwdArgs* a, void* workspace, int sm_count)
 {
     const AttnShape& s = a->s;
     a->tile_tokens = kAttnRows / s.group;
@@ -999,6 +1016,12 @@ size_t attn_bwd_setup(AttnBwdArgs* a, void* workspace)
             place(size_t(heads) * size_t(a->kv_order.blocks) * sizeof(float)));
     }
     a->ready = reinterpret_cast<uint32_t*>(place(sizeof(uint32_t)));
+    if (s.window) {
+        attn_bwd_split(a, sm_count);
+        if (a->chunks > 1)
+            a->part = reinterpret_cast<float*>(place(size_t(heads) * size_t(a->sink_keys) *
+                                                     size_t(a->chunks) * 2 * size_t(s.d) * sizeof(float)));
+    }
     return at;
 }
 
@@ -1006,14 +1029,15 @@ int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const
                     void* const* dv, const void* const* q, const void* const* k,
                     const void* const* v, const void* const* o, const float* const* lse,
                     const void* const* go, const int32_t* kv_lens, const int32_t* q_start,
-                    int causal, float scale, void* workspace, size_t workspace_bytes,
-                    cudaStream_t stream)
+                    int causal, const Window* window, float scale, void* workspace,
+                    size_t workspace_bytes, cudaStream_t stream)
 {
     AttnBwdArgs a;
     std::memset(&a, 0, sizeof a);
     int rc = attn_shape(qp, kp, &a.s);
     if (rc) return rc;
     if ((rc = attn_masks(&a.s, scale, causal, kv_lens, q_start))) return rc;
+    if (window && (rc = attn_window(&a.s, window->keys, window->sinks))) return rc;
     const int W = qp.W;
     int64_t q_b[kMaxW], kv_b[kMaxW], lse_b[kMaxW];
     attn_bytes(qp, kp, q_b, kv_b, lse_b);
@@ -1028,13 +1052,14 @@ int attn_bwd_device(const Plan& qp, const Plan& kp, void* const* dq, void* const
         return rc;
     ins.add(kv_lens, qp.b * 4);
     ins.add(q_start, qp.b * 4);
-    const size_t need = attn_bwd_setup(&a, workspace);
+    DeviceInfo dev = {0, 0};
+    if (window && (rc = current_device(&dev))) return rc;
+    const size_t need = attn_bwd_setup(&a, workspace, dev.sm_count);
     if (!workspace || workspace_bytes < need) return ULY_EINVAL;
     if (!aligned16(workspace)) return ULY_EALIGN;
     outs.add(workspace, int64_t(need));
     if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
-    DeviceInfo dev;
-    if ((rc = current_device(&dev))) return rc;
+    if (!window && (rc = current_device(&dev))) return rc;
     for (int r = 0; r < W; ++r) {
         a.o[r] = static_cast<const uint8_t*>(o[r]);
         a.go[r] = static_cast<const uint8_t*>(go[r]);
@@ -1149,7 +1174,42 @@ int paged_room(const Plan& cp, int64_t table_pages, int64_t* room)
     return ULY_OK;
 }
 
-constexpr int64_t kNoWindow = int64_t(1) << 40;
+// Attention over contiguous keys with a window. Few rows (those of one pass of the paged kernel, which
+// reads a batch element's keys as its only page) go there.
+bool window_of_few_rows(const Plan& qp, const Plan& kp)
+{
+    return kp.N > 0 && qp.S * (qp.N / kp.N) <= kPagedMaxRows;
+}
+
+int window_pages(const Plan& qp, const Plan& kp, const Window& w, PagedArgs* a)
+{
+    AttnShape s;
+    int rc = attn_shape(qp, kp, &s);
+    if (rc || (rc = attn_window(&s, w.keys, w.sinks)) || (rc = paged_shape(qp, kp, a))) return rc;
+    a->box = kPagedTile;
+    a->room = int32_t(kp.S);
+    a->window = s.window;
+    a->sinks = s.sinks;
+    return ULY_OK;
+}
+
+int window_device(const Plan& qp, const Plan& kp, const void* const* q, const void* const* k,
+                  const void* const* v, void* const* o, float* const* lse, const int32_t* kv_lens,
+                  const int32_t* q_start, const Window& w, float scale, void* workspace,
+                  size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!window_of_few_rows(qp, kp))
+        return attn_fwd_device(qp, kp, q, k, v, o, lse, kv_lens, q_start, 1, &w, scale, workspace,
+                               workspace_bytes, stream);
+    PagedArgs a;
+    const int rc = window_pages(qp, kp, w, &a);
+    if (rc) return rc;
+    a.kv_lens = kv_lens;
+    a.q_start = q_start;
+    int64_t kv_b[kMaxW];
+    for (int r = 0; r < kp.W; ++r) kv_b[r] = head_side_bytes(kp, r);
+    return paged_device(qp, a, kv_b, q, k, v, o, lse, scale, workspace, workspace_bytes, stream);
+}
 
 int append_device(const Plan& np, const Plan& cp, const void* const* k, const void* const* v,
                   void* const* k_pages, void* const* v_pages, const int32_t* table, int64_t table_pages,
@@ -1522,7 +1582,7 @@ int ulysses_attention(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, const void*
                       float scale, void* workspace, size_t workspace_bytes, void* stream)
 {
     if (!q_plan || !kv_plan) return ULY_EINVAL;
-    return attn_fwd_device(q_plan->p, kv_plan->p, q, k, v, o, lse, kv_lens, q_start, causal, scale,
+    return attn_fwd_device(q_plan->p, kv_plan->p, q, k, v, o, lse, kv_lens, q_start, causal, nullptr, scale,
                            workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
@@ -1534,7 +1594,7 @@ int ulysses_attention_backward_workspace(ulysses_plan_t q_plan, ulysses_plan_t k
     std::memset(&a, 0, sizeof a);
     const int rc = attn_shape(q_plan->p, kv_plan->p, &a.s);
     if (rc) return rc;
-    *bytes = attn_bwd_setup(&a, nullptr);
+    *bytes = attn_bwd_setup(&a, nullptr, 0);
     return ULY_OK;
 }
 
@@ -1547,8 +1607,68 @@ int ulysses_attention_backward(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, vo
 {
     if (!q_plan || !kv_plan) return ULY_EINVAL;
     return attn_bwd_device(q_plan->p, kv_plan->p, dq, dk, dv, q, k, v, o, lse, go, kv_lens, q_start,
-                           causal, scale, workspace, workspace_bytes,
+                           causal, nullptr, scale, workspace, workspace_bytes,
                            static_cast<cudaStream_t>(stream));
+}
+
+int ulysses_attention_window_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, int64_t window,
+                                       int64_t sinks, size_t* bytes)
+{
+    if (!q_plan || !kv_plan || !bytes) return ULY_EINVAL;
+    const Plan &qp = q_plan->p, &kp = kv_plan->p;
+    const Window w = {window, sinks};
+    DeviceInfo dev;
+    int rc;
+    if (window_of_few_rows(qp, kp)) {
+        PagedArgs a;
+        if ((rc = window_pages(qp, kp, w, &a)) || (rc = current_device(&dev))) return rc;
+        return paged_setup(dev, &a, nullptr, bytes);
+    }
+    AttnFwdArgs a;
+    std::memset(&a, 0, sizeof a);
+    if ((rc = attn_shape(qp, kp, &a.s)) || (rc = attn_window(&a.s, window, sinks)) ||
+        (rc = current_device(&dev)))
+        return rc;
+    *bytes = attn_fwd_setup(dev, &a);
+    return ULY_OK;
+}
+
+int ulysses_attention_window(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, const void* const* q,
+                             const void* const* k, const void* const* v, void* const* o,
+                             float* const* lse, const int32_t* kv_lens, const int32_t* q_start,
+                             int64_t window, int64_t sinks, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream)
+{
+    if (!q_plan || !kv_plan) return ULY_EINVAL;
+    return window_device(q_plan->p, kv_plan->p, q, k, v, o, lse, kv_lens, q_start, {window, sinks}, scale,
+                         workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int ulysses_attention_window_backward_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_plan,
+                                                int64_t window, int64_t sinks, size_t* bytes)
+{
+    if (!q_plan || !kv_plan || !bytes) return ULY_EINVAL;
+    AttnBwdArgs a;
+    std::memset(&a, 0, sizeof a);
+    DeviceInfo dev;
+    int rc = attn_shape(q_plan->p, kv_plan->p, &a.s);
+    if (rc || (rc = attn_window(&a.s, window, sinks)) || (rc = current_device(&dev))) return rc;
+    *bytes = attn_bwd_setup(&a, nullptr, dev.sm_count);
+    return ULY_OK;
+}
+
+int ulysses_attention_window_backward(ulysses_plan_t q_plan, ulysses_plan_t kv_plan, void* const* dq,
+                                      void* const* dk, void* const* dv, const void* const* q,
+                                      const void* const* k, const void* const* v, const void* const* o,
+                                      const float* const* lse, const void* const* go,
+                                      const int32_t* kv_lens, const int32_t* q_start, int64_t window,
+                                      int64_t sinks, float scale, void* workspace,
+                                      size_t workspace_bytes, void* stream)
+{
+    if (!q_plan || !kv_plan) return ULY_EINVAL;
+    const Window w = {window, sinks};
+    return attn_bwd_device(q_plan->p, kv_plan->p, dq, dk, dv, q, k, v, o, lse, go, kv_lens, q_start, 1, &w,
+                           scale, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int ulysses_attention_paged_workspace(ulysses_plan_t q_plan, ulysses_plan_t cache_plan, size_t* bytes)
@@ -1581,7 +1701,7 @@ int ulysses_attention_paged(ulysses_plan_t q_plan, ulysses_plan_t cache_plan, co
     a.from_end = 1;
     a.box = cp.S % 16 == 0 ? 16 : 8;
     a.room = int32_t(room);
-    a.window = window ? window : kNoWindow;
+    a.window = window && window < kAttnFar ? window : kAttnFar;
     a.sinks = int32_t(sinks < room ? sinks : room);
     int64_t kv_b[kMaxW];
     for (int r = 0; r < cp.W; ++r) kv_b[r] = head_side_bytes(cp, r);

@@ -39,6 +39,9 @@ struct AttnShape {
     int32_t ragged;
     uint32_t wait_us;  // limit of a wait in which nothing moves (CtaLife)
     float scale;
+    // Causal with a window (0: none): the query at position p sees j <= p with j > p - window or j < sinks.
+    int32_t sinks;
+    int64_t window;
 };
 
 #ifdef __CUDACC__
@@ -52,6 +55,40 @@ __device__ __forceinline__ void attn_limits(const AttnShape& s, int bb, int64_t*
         *pos0 = s.q_start ? int64_t(s.q_start[bb]) : 0;
         *len = min(*len, max(int64_t(0), *pos0 + s.Sq));
     }
+}
+#endif
+
+// The key blocks that a unit walks: 0, 1, ...; with a window 0 .. first - 1, which hold the first tokens
+// that it sees besides, and then those from first + gap on.
+#ifdef __CUDACC__
+template <bool WIN>
+struct AttnBlocks {
+    __device__ __forceinline__ int block(int j) const { return j; }
+};
+template <>
+struct AttnBlocks<true> {
+    int first, gap;
+    __device__ __forceinline__ int block(int j) const { return j < first ? j : j + gap; }
+    // `lo`: the first key in the window of the unit's first row
+    __device__ __forceinline__ void set(const AttnShape& s, int64_t lo)
+    {
+        const int near = int(lo / kAttnRows);
+        first = min(int((min(int64_t(s.sinks), lo) + kAttnRows - 1) / kAttnRows), near);
+        gap = near - first;
+    }
+    // of blocks 0 .. n - 1, those of the list
+    __device__ __forceinline__ int count(int n) const { return min(n, first) + max(0, n - (first + gap)); }
+};
+
+// With a window, the rows of a key block between the first tokens and the window of the batch element's
+// first row, which no row sees: x .. y - 1 (none where y <= x).
+template <bool WIN>
+__device__ __forceinline__ int2 attn_between(const AttnShape& s, int64_t pos0, int64_t block)
+{
+    if constexpr (!WIN) return make_int2(0, 0);
+    const int64_t key0 = block * kAttnRows, lo = pos0 + 1 - s.window;
+    return make_int2(int(max(int64_t(0), min(int64_t(kAttnRows), s.sinks - key0))),
+                     int(max(int64_t(0), min(int64_t(kAttnRows), lo - key0))));
 }
 #endif
 
@@ -149,6 +186,13 @@ struct AttnBwdArgs {
     float* stats;
     float2* row_bounds;  // fp16: [(rank, batch, key head)][q_tiles][2]: largest |dO|, |delta| of half a tile
     float* key_norms;    // fp16: [(rank, batch, key head)][key blocks]: largest |v|
+    // With a window: dK, dV's units. A block of first tokens is seen by every later row; its row tiles are
+    // cut into `chunks` units of chunk_tiles each, whose sums for the first tokens go to `part`,
+    // [(rank, batch, key head)][sink_keys][chunks][2][d] fp32, and are added in order by a last kernel.
+    AttnOrder kv_units;  // (rank, batch, key head) x (blocks, those of the first tokens chunks times)
+    int32_t sink_keys, sink_blocks, chunks;
+    int64_t chunk_tiles;
+    float* part;
     uint32_t* ready;  // 0 from the statistics kernel, 1 from dK, dV's once it has seen the statistics
 };
 
@@ -185,6 +229,8 @@ inline cudaError_t attn_launch_early(void (*kernel)(Args), unsigned grid, unsign
 int64_t attn_order_group(int64_t heads, int64_t bytes);
 // Tiles, units and parts of the keys from the shape and the device alone: a CTA cap changes no bit.
 void attn_fwd_split(AttnFwdArgs* a, int sm_count);
+// The units of dK, dV with a window, from the shape and the device alone.
+void attn_bwd_split(AttnBwdArgs* a, int sm_count);
 // `cap`: CTAs of a launch at most; under one (below kAttnMostCtas) no kernel starts beside another.
 cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* const* k,
                             const void* const* v, cudaStream_t stream, int device, int64_t cap,

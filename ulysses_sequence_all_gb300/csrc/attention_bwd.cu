@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(256) attn_bwd_stats_kernel(const __grid_consta
         for (int k = 0; k < 2 * kTurns; ++k) {
             const int64_t key = block * kAttnRows + k * kAtOnce + slot;
             v[k] = make_uint4(0, 0, 0, 0);
-            if (key < len && sub * 8 < s.d)
+            const bool some = !s.window || key < s.sinks || key > pos0 - s.window;  // of all rows
+            if (key < len && some && sub * 8 < s.d)
                 v[k] = ld_stream_v4(a.v[r] + ((int64_t(bb) * s.Skv + key) * s.m[r] + kvh) * s.d * 2 +
                                     sub * 16);
         }
@@ -326,13 +327,24 @@ struct BkSmem {
     static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");
 };
 
-struct BkUnit {
+// With a window: which of a first-token block's chunks of row tiles a unit is, and how many there are.
+template <bool WIN>
+struct BkChunk {
+};
+template <>
+struct BkChunk<true> {
+    int c, chunks;
+};
+
+template <bool WIN>
+struct BkUnit : BkChunk<WIN> {
     int r, bb, kvh, n;       // n: row tiles from `first` on that see the block
     int e;                   // fp16: dS is held times 2^e
     int64_t h, kv0, first;
     int64_t len, pos0;
 };
 
+template <bool WIN>
 struct BkBars {
     uint64_t k_full, v_full, k_empty, v_empty;  // key block landed; its last scores have read it
     uint64_t q_full[4], q_empty[4], g_full[4], g_empty[4];
@@ -342,24 +354,58 @@ struct BkBars {
     uint64_t drain;
     uint32_t tmem;
     CtaLife life;
-    AbUnitBoard<BkUnit> board;
+    AbUnitBoard<BkUnit<WIN>> board;
 };
-static_assert(sizeof(BkBars) <= 1024, "barriers");
+static_assert(sizeof(BkBars<true>) <= 1024, "barriers");
 
-template <bool F16>  // called by a whole warp
-__device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
+// The row tiles that see any of the 128 keys from kv0 on: *first and how many.
+template <bool WIN>
+__device__ __forceinline__ int bk_tiles(const AttnBwdArgs& a, int64_t kv0, int64_t len, int64_t pos0,
+                                        int64_t* first)
+{
+    // row i sees key kv0 when i >= kv0 - pos0
+    const int64_t row = max(int64_t(0), kv0 - pos0);
+    *first = row / a.tile_tokens;
+    int64_t end = a.q_tiles;
+    if (WIN && kv0 >= a.s.sinks) {  // the last key's window ends before row key + window - pos0
+        const int64_t rows = max(int64_t(0), min(kv0 + kAttnRows, len) - 1 + a.s.window - pos0);
+        end = min(end, (rows + a.tile_tokens - 1) / a.tile_tokens);
+    }
+    return kv0 < len && *first < end ? int(end - *first) : 0;
+}
+
+template <bool F16, bool WIN>  // called by a whole warp
+__device__ __forceinline__ BkUnit<WIN> bk_unit(const AttnBwdArgs& a, int64_t u)
 {
     const AttnShape& s = a.s;
-    BkUnit t;
+    BkUnit<WIN> t;
     int64_t block;
-    attn_order(a.kv_order, u, &t.h, &block);  // the first keys are seen by the most rows
+    // the first keys are seen by the most rows
+    if constexpr (WIN) {
+        attn_order(a.kv_units, u, &t.h, &block);
+        t.c = 0;
+        if (block < int64_t(a.sink_blocks) * a.chunks) {
+            const int64_t at = block / a.chunks;
+            t.c = int(block - at * a.chunks);
+            block = at;
+        } else {
+            block -= int64_t(a.sink_blocks) * (a.chunks - 1);
+        }
+    } else {
+        attn_order(a.kv_order, u, &t.h, &block);
+    }
     t.kv0 = block * kAttnRows;
     ab_head(s, t.h, &t.r, &t.bb, &t.kvh);
     attn_limits(s, t.bb, &t.len, &t.pos0);
-    // row i sees key kv0 when i >= kv0 - pos0
-    const int64_t row = max(int64_t(0), t.kv0 - t.pos0);
-    t.first = row / a.tile_tokens;
-    t.n = t.kv0 < t.len && t.first < a.q_tiles ? int(a.q_tiles - t.first) : 0;
+    t.n = bk_tiles<WIN>(a, t.kv0, t.len, t.pos0, &t.first);
+    if constexpr (WIN) {
+        t.chunks = 1;
+        if (t.kv0 < s.sinks) {
+            t.chunks = int((t.n + a.chunk_tiles - 1) / a.chunk_tiles);
+            t.first += t.c * a.chunk_tiles;
+            t.n = int(max(int64_t(0), min(a.chunk_tiles, t.n - t.c * a.chunk_tiles)));
+        }
+    }
     t.e = 0;
     if (F16 && t.n > 0) {
         const float2* rows = a.row_bounds + (t.h * a.q_tiles + t.first) * 2;
@@ -381,14 +427,29 @@ __device__ __forceinline__ BkUnit bk_unit(const AttnBwdArgs& a, int64_t u)
 
 // Rows at the start of a unit's first tile that see no key at all (a start before the first key): their
 // P and dS are zero, but zero times what Q and dO hold there may be NaN. Later tiles have none, and
-// tiles with such rows only are not walked.
-__device__ __forceinline__ int bk_hidden(const AttnBwdArgs& a, const BkUnit& t)
+// tiles with such rows only are not walked. With a window and no first tokens, also the rows from `y` on
+// of a unit's last tile, whose window begins past the last key; (x, kAttnRows): none.
+template <bool WIN>
+__device__ __forceinline__ int2 bk_hidden(const AttnBwdArgs& a, const BkUnit<WIN>& t, int64_t tile)
 {
-    const int64_t tokens = -t.pos0 - t.first * a.tile_tokens;
-    return tokens > 0 ? int(min(tokens, int64_t(a.tile_tokens))) * a.s.group : 0;
+    int2 h = make_int2(0, kAttnRows);
+    const int64_t tokens = -t.pos0 - tile * a.tile_tokens;
+    if (tile == t.first && tokens > 0) h.x = int(min(tokens, int64_t(a.tile_tokens))) * a.s.group;
+    if (WIN && a.s.sinks == 0) {
+        const int64_t seen = t.len + a.s.window - 1 - t.pos0 - tile * a.tile_tokens;
+        if (seen < a.tile_tokens) h.y = int(max(int64_t(0), seen)) * a.s.group;
+    }
+    return h;
 }
 
-template <int DP, bool F16>
+template <bool WIN>
+__device__ __forceinline__ bool bk_unclean(const AttnBwdArgs& a, const BkUnit<WIN>& t, int64_t tile)
+{
+    const int2 h = bk_hidden<WIN>(a, t, tile);
+    return h.x > 0 || h.y < kAttnRows;
+}
+
+template <int DP, bool F16, bool WIN>
 __global__ void __launch_bounds__(kAbThreads, 1)
     attn_bwd_kv_kernel(const __grid_constant__ AttnBwdArgs a)
 {
@@ -397,12 +458,15 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
-    BkBars& bars = *reinterpret_cast<BkBars*>(smem);
+    using Unit = BkUnit<WIN>;
+    BkBars<WIN>& bars = *reinterpret_cast<BkBars<WIN>*>(smem);
     volatile CtaLife* life = &bars.life;
     const AttnShape& s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nk = (s.d + 15) / 16, halves = (s.d + 63) / 64;
-    const int64_t units = a.kv_order.heads * a.kv_order.blocks;
+    const AttnOrder& order = WIN ? a.kv_units : a.kv_order;
+    const int64_t units = order.heads * order.blocks;
+    const bool cleans = WIN || s.q_start;  // warp 18 has tiles to look at
     constexpr int K = L::kStages;
 
     if (threadIdx.x == 0) {
@@ -412,9 +476,9 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.v_empty, 1);
         for (int k = 0; k < K; ++k) {
             mbar_init(&bars.q_full[k], 1);
-            mbar_init(&bars.q_empty[k], s.q_start ? 2 : 1);  // the products, and warp 18
+            mbar_init(&bars.q_empty[k], cleans ? 2 : 1);  // the products, and warp 18
             mbar_init(&bars.g_full[k], 1);
-            mbar_init(&bars.g_empty[k], s.q_start ? 2 : 1);
+            mbar_init(&bars.g_empty[k], cleans ? 2 : 1);
             mbar_init(&bars.clean[k], 1);
         }
         mbar_init(&bars.s_full, 1);
@@ -423,7 +487,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         mbar_init(&bars.ds_ready, 16);
         mbar_init(&bars.acc_full, 1);
         mbar_init(&bars.acc_free, 16);
-        ab_board_init(bars.board, s.q_start ? 19 : 18);  // warps 0-17, and 18
+        ab_board_init(bars.board, cleans ? 19 : 18);  // warps 0-17, and 18
         mbar_init(&bars.drain, 1);
         life_init(bars.life, s.wait_us, kAbThreads / 32);
         fence_barrier_init();
@@ -453,9 +517,9 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
-            AbUnits<BkUnit> source{&bars.board, life};
-            BkUnit t;
-            while (ok && source.next<false>(&t)) {
+            AbUnits<Unit> source{&bars.board, life};
+            Unit t;
+            while (ok && source.template next<false>(&t)) {
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     if (ok && blocks[w] > 0)
@@ -541,10 +605,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                               row + ks * (2048 >> 4), id_d, !first || ks > 0);
             };
             // S^T (dP^T) of the ring's next row tile; `first`, `last` of unit u
-            auto next_s = [&](bool first, bool last, uint32_t use, const BkUnit& u) {
+            auto next_s = [&](bool first, bool last, uint32_t use, const Unit& u, int64_t tile) {
                 if (first) wait(&bars.k_full, use & 1);
                 if (!wait(&bars.q_full[ring.s], ring.phase)) return;
-                if (first && s.q_start && bk_hidden(a, u) > 0) {
+                if ((WIN || (first && s.q_start)) && bk_unclean<WIN>(a, u, tile)) {
                     if (!wait(&bars.clean[ring.s], (cleaned >> ring.s) & 1)) return;
                     cleaned ^= 1u << ring.s;
                 }
@@ -559,11 +623,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 scores(kBkDp, v_desc, g_desc + ring.s * (L::kTile >> 4), &bars.dp_full);
                 if (last) tc_commit(&bars.v_empty);
             };
-            AbUnits<BkUnit> source{&bars.board, life};
-            BkUnit t, next;
-            bool live = source.next<false>(&t);
+            AbUnits<Unit> source{&bars.board, life};
+            Unit t, next;
+            bool live = source.template next<false>(&t);
             if (live) {
-                next_s(true, t.n == 1, 0, t);
+                next_s(true, t.n == 1, 0, t, t.first);
                 next_dp(true, t.n == 1, 0);
             }
             while (live && ok) {
@@ -571,7 +635,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 for (int i = 0; ok && i < t.n; ++i, ++tiles) {
                     const int at = ring.s;
                     const bool end = i + 1 == t.n;           // the next tile is the next unit's
-                    if (end) more = source.next<false>(&next);
+                    if (end) more = source.template next<false>(&next);
                     const bool last = end ? next.n == 1 : i + 2 == t.n;
                     ring.next(K);
                     wait(&bars.p_ready, tiles & 1);
@@ -580,7 +644,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     tc_fence_after();
                     sums(kBkDv, kBkS, gt_desc + at * (L::kTile >> 4), i == 0);
                     tc_commit(&bars.g_empty[at]);
-                    if (!end || more) next_s(end, last, uses + 1, next);
+                    if (!end || more)
+                        next_s(end, last, uses + 1, end ? next : t, end ? next.first : t.first + i + 1);
                     if (!wait(&bars.ds_ready, tiles & 1)) break;
                     tc_fence_after();
                     sums(kBkDk, kBkDp, qt_desc + at * (L::kTile >> 4), i == 0);
@@ -597,21 +662,23 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         }
         __syncwarp();
     } else if (warp == kAbCleanWarp) {
-        if (s.q_start) {
+        if (cleans) {
             StageRing ring;
-            AbUnits<BkUnit> source{&bars.board, life};
-            BkUnit t;
+            AbUnits<Unit> source{&bars.board, life};
+            Unit t;
             bool ok = true;
-            while (ok && source.next<true>(&t)) {
+            while (ok && source.template next<true>(&t)) {
                 for (int i = 0; ok && i < t.n; ++i) {
                     ok = __all_sync(0xffffffffu, wait_or_dead(&bars.q_full[ring.s], ring.phase, life));
                     ok = ok &&
                          __all_sync(0xffffffffu, wait_or_dead(&bars.g_full[ring.s], ring.phase, life));
                     if (!ok) break;
-                    const int hidden = i == 0 ? bk_hidden(a, t) : 0;
-                    if (hidden > 0) {
+                    const int2 hidden =
+                        WIN || i == 0 ? bk_hidden<WIN>(a, t, t.first + i) : make_int2(0, kAttnRows);
+                    if (hidden.x > 0 || hidden.y < kAttnRows) {
                         for (int h = 0; h < halves; ++h)
-                            for (int w = lane; w < hidden * 8; w += 32) {
+                            for (int w = lane; w < kAttnRows * 8; w += 32) {
+                                if (w >= hidden.x * 8 && w < hidden.y * 8) continue;
                                 const int at = ring.s * L::kTile + h * L::kHalf + w * 16;
                                 st_shared_v4(smem + L::kQ + at, make_uint4(0, 0, 0, 0));
                                 st_shared_v4(smem + L::kG + at, make_uint4(0, 0, 0, 0));
@@ -632,9 +699,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         }
         __syncwarp();
     } else if (warp == kAbUnitWarp) {
-        ab_publish<BkUnit>(
-            bars.board, units, life, [&](int64_t u) { return bk_unit<F16>(a, u); },
-            [&](const BkUnit& t) {  // keys that no row sees
+        ab_publish<Unit>(
+            bars.board, units, life, [&](int64_t u) { return bk_unit<F16, WIN>(a, u); },
+            [&](const Unit& t) {  // keys that no row sees
+                if constexpr (WIN)
+                    if (t.c > 0) return;
                 for (int i = lane; i < 2 * kAttnRows; i += 32) {
                     const int64_t key = t.kv0 + i % kAttnRows;
                     if (key >= s.Skv) continue;
@@ -662,17 +731,22 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        AbUnits<BkUnit> source{&bars.board, life};
-        BkUnit t;
-        while (ok && source.next<true>(&t)) {
+        AbUnits<Unit> source{&bars.board, life};
+        Unit t;
+        while (ok && source.template next<true>(&t)) {
             const int64_t key = t.kv0 + row;
             // columns of the unit's first tile that see this key begin here, of each next one
             // tile_tokens * group columns earlier
             int64_t lo = (key - t.pos0 - t.first * a.tile_tokens) * s.group - 32 * wg;
             if (key >= t.len) lo = int64_t(1) << 40;
+            int64_t hi = int64_t(1) << 40;  // and those whose window it is in end here
+            if (WIN && key >= s.sinks)
+                hi = (key + s.window - t.pos0 - t.first * a.tile_tokens) * s.group - 32 * wg;
             const float2 ds2 = make_float2(ab_power(t.e - kAttnPBits), ab_power(t.e - kAttnPBits));
-            for (int i = 0; i < t.n; ++i, lo -= a.tile_tokens * s.group) {
+            for (int i = 0; i < t.n;
+                 ++i, lo -= a.tile_tokens * s.group, hi -= WIN ? a.tile_tokens * s.group : 0) {
                 const int from = int(max(int64_t(-1), min(lo, int64_t(32))));
+                const int to = WIN ? int(max(int64_t(0), min(hi, int64_t(32)))) : 32;
                 ok = all(&bars.q_full[ring.s], ring.phase);  // the tile's lse and D
                 ok = ok && all(&bars.s_full, tiles & 1);
                 if (!ok) break;
@@ -698,11 +772,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     x[4 * c + 2] = __float_as_uint(ex2(f.x));
                     x[4 * c + 3] = __float_as_uint(ex2(f.y));
                 }
-                const bool masked = __any_sync(0xffffffffu, from > 0);
+                const bool masked = __any_sync(0xffffffffu, from > 0 || (WIN && to < 32));
                 if (masked) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
-                        if (c < from) x[c] = 0;
+                        if (c < from || (WIN && c >= to)) x[c] = 0;
                 }
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
@@ -734,8 +808,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 if (masked) {  // zero times what lies past the last key may be NaN
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        if (2 * c < from) p[c] &= 0xFFFF0000u;
-                        if (2 * c + 1 < from) p[c] &= 0x0000FFFFu;
+                        if (2 * c < from || (WIN && 2 * c >= to)) p[c] &= 0xFFFF0000u;
+                        if (2 * c + 1 < from || (WIN && 2 * c + 1 >= to)) p[c] &= 0x0000FFFFu;
                     }
                 }
                 tmem_st16(dp_at, p);
@@ -762,6 +836,21 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.acc_free);
+                }
+                if constexpr (WIN) {
+                    if (t.chunks > 1 && key < a.sink_keys) {  // a part of what all rows give a first token
+                        float* part = a.part + (((t.h * a.sink_keys + key) * a.chunks + t.c) * 2 +
+                                                (wg >= 2 ? 1 : 0)) * s.d + col;
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            if (col + k < s.d)
+                                *reinterpret_cast<float4*>(part + k) =
+                                    make_float4(__uint_as_float(y[k]) * f, __uint_as_float(y[k + 1]) * f,
+                                                __uint_as_float(y[k + 2]) * f,
+                                                __uint_as_float(y[k + 3]) * f);
+                        continue;
+                    }
+                    if (t.c > 0) continue;  // the other keys' rows are all in the first chunk
                 }
                 if (key < s.Skv) ab_store<E>(out, col, s.d, y, f);
             }
@@ -792,12 +881,14 @@ struct BqSmem {
     static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");
 };
 
-struct BqUnit {
-    int r, bb, kvh, n;  // n: key blocks that the tile sees
+template <bool WIN>
+struct BqUnit : AttnBlocks<WIN> {
+    int r, bb, kvh, n;  // n: key blocks that the tile sees, block(0 .. n - 1)
     float norm;         // fp16: the largest |v| in them
     int64_t h, tile, tok0, len, pos0;
 };
 
+template <bool WIN>
 struct BqBars {
     uint64_t full[8], empty[8], clean[8];  // ring stages; clean: K rows past the last key zeroed
     uint64_t g_full, g_empty;              // dO landed; its last scores have read it
@@ -808,15 +899,15 @@ struct BqBars {
     uint32_t tmem;
     int seen;
     CtaLife life;
-    AbUnitBoard<BqUnit> board;
+    AbUnitBoard<BqUnit<WIN>> board;
 };
-static_assert(sizeof(BqBars) <= 1024, "barriers");
+static_assert(sizeof(BqBars<true>) <= 1024, "barriers");
 
-template <bool F16>  // called by a whole warp
-__device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
+template <bool F16, bool WIN>  // called by a whole warp
+__device__ __forceinline__ BqUnit<WIN> bq_unit(const AttnBwdArgs& a, int64_t u)
 {
     const AttnShape& s = a.s;
-    BqUnit t;
+    BqUnit<WIN> t;
     attn_order(a.q_order, u, &t.h, &t.tile);
     if (s.causal) t.tile = a.q_tiles - 1 - t.tile;  // the longest rows first
     t.tok0 = t.tile * a.tile_tokens;
@@ -825,11 +916,16 @@ __device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
     const int64_t last = min(t.tok0 + a.tile_tokens, s.Sq) - 1;
     const int64_t keys = max(int64_t(0), min(t.len, t.pos0 + last + 1));
     t.n = int((keys + kAttnRows - 1) / kAttnRows);
+    if constexpr (WIN) {
+        t.set(s, max(int64_t(0), min(keys, t.pos0 + t.tok0 + 1 - s.window)));
+        t.n = t.count(t.n);
+    }
     t.norm = 0.0f;
     if (F16) {
         const float* norms = a.key_norms + t.h * a.kv_order.blocks;
 #pragma unroll 4
-        for (int i = threadIdx.x & 31; i < t.n; i += 32) t.norm = fmaxf(t.norm, norms[i]);
+        for (int i = threadIdx.x & 31; i < t.n; i += 32)
+            t.norm = fmaxf(t.norm, norms[t.block(i)]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             t.norm = fmaxf(t.norm, __shfl_xor_sync(0xffffffffu, t.norm, off));
@@ -838,16 +934,25 @@ __device__ __forceinline__ BqUnit bq_unit(const AttnBwdArgs& a, int64_t u)
 }
 
 // Rows of a key block past the batch element's last key that the tensor holds; kAttnRows: none.
-__device__ __forceinline__ int bq_past(const AttnShape& s, const BqUnit& t, int block)
+template <bool WIN>
+__device__ __forceinline__ int bq_past(const AttnShape& s, const BqUnit<WIN>& t, int block)
 {
     const int64_t past = t.len - int64_t(block) * kAttnRows;
     return past >= kAttnRows || t.len >= s.Skv ? kAttnRows : int(past);
 }
 
+// Whether a key block holds rows that warp 18 zeroes.
+template <bool WIN>
+__device__ __forceinline__ bool bq_unclean(const AttnShape& s, const BqUnit<WIN>& t, int block)
+{
+    const int2 b = attn_between<WIN>(s, t.pos0, block);
+    return bq_past(s, t, block) < kAttnRows || b.y > b.x;
+}
+
 // Q goes to tensor memory (the S products then read half as much shared memory), S and dP are free
 // again as soon as the threads have read them, and dS has columns of its own, so that the products
 // run S, dP of the next block and dQ of this one without waiting for the threads' arithmetic.
-template <int DP, bool F16>
+template <int DP, bool F16, bool WIN>
 __global__ void __launch_bounds__(kAbThreads, 1)
     attn_bwd_q_kernel(const __grid_constant__ AttnBwdArgs a)
 {
@@ -856,7 +961,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
-    BqBars& bars = *reinterpret_cast<BqBars*>(smem);
+    using Unit = BqUnit<WIN>;
+    BqBars<WIN>& bars = *reinterpret_cast<BqBars<WIN>*>(smem);
     volatile CtaLife* life = &bars.life;
     const AttnShape& s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -915,11 +1021,11 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 life->loads = uint32_t(++issued);
                 ring.next(K);
             };
-            AbUnits<BqUnit> source{&bars.board, life};
-            BqUnit t;
-            while (ok && source.next<false>(&t)) {
+            AbUnits<Unit> source{&bars.board, life};
+            Unit t;
+            while (ok && source.template next<false>(&t)) {
                 stage(&a.qmap[t.r], q_bytes, t.kvh * s.group, int(t.tok0), t.bb);
-                if (ok) stage(&a.kmap[t.r], kv_bytes, t.kvh, 0, t.bb);
+                if (ok) stage(&a.kmap[t.r], kv_bytes, t.kvh, t.block(0) * kAttnRows, t.bb);
                 if (ok && uses > 0) ok = wait_or_dead(&bars.g_empty, (uses - 1) & 1, life);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&bars.g_full, q_bytes);
@@ -929,7 +1035,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 ++uses;
                 for (int j = 1; ok && j < 2 * t.n; ++j)
                     stage((j & 1) ? &a.vmap[t.r] : &a.kmap[t.r], kv_bytes, t.kvh,
-                          (j >> 1) * kAttnRows, t.bb);
+                          t.block(j >> 1) * kAttnRows, t.bb);
             }
             bool drained = true;  // leave no copy into this CTA's shared memory in flight
             for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k)
@@ -942,20 +1048,28 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         // dS is zero past the last key, but zero times what K holds there may be NaN
         if (s.ragged) {
             StageRing ring;
-            AbUnits<BqUnit> source{&bars.board, life};
-            BqUnit t;
+            AbUnits<Unit> source{&bars.board, life};
+            Unit t;
             bool ok = true;
-            while (ok && source.next<true>(&t)) {
+            while (ok && source.template next<true>(&t)) {
                 for (int j = -1; ok && j < 2 * t.n; ++j) {  // Q K0 V0 K1 V1 ...
                     ok = __all_sync(0xffffffffu, wait_or_dead(&bars.full[ring.s], ring.phase, life));
                     if (!ok) break;
-                    const int past = j < 0 || (j & 1) ? kAttnRows : bq_past(s, t, j >> 1);
-                    if (past < kAttnRows) {
-                        for (int h = 0; h < halves; ++h)
+                    int past = kAttnRows;
+                    int2 between = make_int2(0, 0);
+                    if (j >= 0 && !(j & 1)) {
+                        past = bq_past(s, t, t.block(j >> 1));
+                        between = attn_between<WIN>(s, t.pos0, t.block(j >> 1));
+                    }
+                    if (past < kAttnRows || between.y > between.x) {
+                        for (int h = 0; h < halves; ++h) {
+                            uint8_t* rows = smem + L::kRing + ring.s * L::kTile + h * L::kHalf;
                             for (int w = past * 8 + lane; w < kAttnRows * 8; w += 32)
-                                st_shared_v4(smem + L::kRing + ring.s * L::kTile + h * L::kHalf +
-                                                 w * 16,
-                                             make_uint4(0, 0, 0, 0));
+                                st_shared_v4(rows + w * 16, make_uint4(0, 0, 0, 0));
+                            if constexpr (WIN)
+                                for (int w = between.x * 8 + lane; w < between.y * 8; w += 32)
+                                    st_shared_v4(rows + w * 16, make_uint4(0, 0, 0, 0));
+                        }
                         fence_proxy_async_shared();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars.clean[ring.s]);
@@ -1020,9 +1134,9 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 if (last) tc_commit(&bars.g_empty);
                 ring.next(K);
             };
-            AbUnits<BqUnit> source{&bars.board, life};
-            BqUnit t, next;
-            bool live = source.next<false>(&t);
+            AbUnits<Unit> source{&bars.board, life};
+            Unit t, next;
+            bool live = source.template next<false>(&t);
             int ks = 0;  // the stage of the current block's K
             if (live) {
                 ks = make_s(true, 0);
@@ -1032,13 +1146,13 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 bool more = false;
                 for (int j = 0; ok && j < t.n; ++j, ++blocks) {
                     const bool end = j + 1 == t.n;  // the next block is the next unit's
-                    if (end) more = source.next<false>(&next);
+                    if (end) more = source.template next<false>(&next);
                     int after = ks;
                     wait(&bars.s_read, blocks & 1);
                     if (!end) after = make_s(false, uses);
                     wait(&bars.dp_read, blocks & 1);
                     if (!end) make_dp(false, j + 2 == t.n, uses);
-                    if (s.ragged && bq_past(s, t, j) < kAttnRows) {
+                    if (s.ragged && bq_unclean(s, t, t.block(j))) {
                         wait(&bars.clean[ks], (cleaned >> ks) & 1);
                         cleaned ^= 1u << ks;
                     }
@@ -1071,9 +1185,9 @@ __global__ void __launch_bounds__(kAbThreads, 1)
         }
         __syncwarp();
     } else if (warp == kAbUnitWarp) {
-        ab_publish<BqUnit>(
-            bars.board, units, life, [&](int64_t u) { return bq_unit<F16>(a, u); },
-            [&](const BqUnit& t) {  // rows that see no key
+        ab_publish<Unit>(
+            bars.board, units, life, [&](int64_t u) { return bq_unit<F16, WIN>(a, u); },
+            [&](const Unit& t) {  // rows that see no key
                 for (int i = lane; i < kAttnRows; i += 32) {
                     const int tok_in = i / s.group;
                     const int64_t tok = t.tok0 + tok_in;
@@ -1122,9 +1236,9 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             }
             arrive(&bars.q_ready);
         };
-        AbUnits<BqUnit> source{&bars.board, life};
-        BqUnit t, next;
-        bool live = source.next<true>(&t);
+        AbUnits<Unit> source{&bars.board, life};
+        Unit t, next;
+        bool live = source.template next<true>(&t);
         if (live) copy(0);
         while (live && ok) {
             const int64_t tok = t.tok0 + tok_in;
@@ -1139,8 +1253,17 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 f *= ab_power(-e);
             }
             int64_t left = min(t.len, t.pos0 + tok + 1) - 32 * wg;  // visible keys from here on
-            for (int j = 0; j < t.n; ++j, ++blocks, left -= kAttnRows) {
-                const int seen = int(max(int64_t(0), min(left, int64_t(32))));
+            const int64_t low = WIN ? t.pos0 + tok + 1 - s.window : 0;  // the row's window begins here
+            for (int j = 0; j < t.n; ++j, ++blocks, left -= WIN ? 0 : kAttnRows) {
+                int seen = 0, from = 0, to = 0;  // keys in view; those from .. to - 1 of them not
+                if constexpr (WIN) {
+                    const int64_t key0 = t.block(j) * int64_t(kAttnRows) + 32 * wg;
+                    seen = int(max(int64_t(0), min(left + 32 * wg - key0, int64_t(32))));
+                    from = int(max(int64_t(0), min(s.sinks - key0, int64_t(32))));
+                    to = int(max(int64_t(0), min(low - key0, int64_t(32))));
+                } else {
+                    seen = int(max(int64_t(0), min(left, int64_t(32))));
+                }
                 ok = all(&bars.s_full, blocks & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -1156,7 +1279,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     x[2 * c] = __float_as_uint(ex2(e.x));
                     x[2 * c + 1] = __float_as_uint(ex2(e.y));
                 }
-                const bool masked = __any_sync(0xffffffffu, seen < 32);
+                const bool masked = __any_sync(0xffffffffu, seen < 32 || (WIN && to > from));
                 ok = all(&bars.dp_full, blocks & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -1173,8 +1296,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 if (masked) {  // zero times what lies past the last key may be NaN
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        if (2 * c >= seen) p[c] &= 0xFFFF0000u;
-                        if (2 * c + 1 >= seen) p[c] &= 0x0000FFFFu;
+                        if (2 * c >= seen || (WIN && 2 * c >= from && 2 * c < to))
+                            p[c] &= 0xFFFF0000u;
+                        if (2 * c + 1 >= seen || (WIN && 2 * c + 1 >= from && 2 * c + 1 < to))
+                            p[c] &= 0x0000FFFFu;
                     }
                 }
                 if (blocks > 0) ok = all(&bars.dq_done, (blocks - 1) & 1);
@@ -1185,7 +1310,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 arrive(&bars.ds_ready);
                 if (j + 1 == t.n) {  // the next unit's queries (its S then runs beside the last dQ)
                     stages += 1 + 2 * t.n;
-                    live = source.next<true>(&next);
+                    live = source.template next<true>(&next);
                     if (live) copy(stages);
                     if (!ok) break;
                 }
@@ -1217,7 +1342,40 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     if (warp == kAbMmaWarp) tmem_free(tmem);
 }
 
-template <int DP, bool F16>
+// Adds the chunks of the first tokens' gradients: one warp a key, a lane 4 columns of dK and of dV.
+template <bool F16, bool WIN = true>
+__global__ void __launch_bounds__(128) attn_bwd_join_kernel(const __grid_constant__ AttnBwdArgs a)
+{
+    using E = ElemT<F16>;
+    const AttnShape& s = a.s;
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = int64_t(s.head_begin[s.W]) * a.sink_keys;
+    for (int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5); row < rows;
+         row += int64_t(gridDim.x) * 4) {
+        const int64_t h = div_fast(row, a.sink_keys), key = row - h * a.sink_keys;
+        int r, bb, kvh;
+        ab_head(s, h, &r, &bb, &kvh);
+        int64_t len, pos0, first;
+        attn_limits(s, bb, &len, &pos0);
+        const int64_t n = bk_tiles<WIN>(a, key / kAttnRows * kAttnRows, len, pos0, &first);
+        const int64_t chunks = (n + a.chunk_tiles - 1) / a.chunk_tiles;
+        if (chunks <= 1 || lane * 4 >= s.d) continue;  // written already
+        const float* from = a.part + row * a.chunks * 2 * s.d + lane * 4;
+        const int64_t to = (((int64_t(bb) * s.Skv + key) * s.m[r] + kvh) * s.d + lane * 4) * 2;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int64_t c = 0; c < chunks; ++c) {
+                const float4 x = *reinterpret_cast<const float4*>(from + (c * 2 + w) * s.d);
+                sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+            }
+            st_v2((w ? a.dv[r] : a.dk[r]) + to, E::pack(sum.x, sum.y), E::pack(sum.z, sum.w));
+        }
+    }
+}
+
+template <int DP, bool F16, bool WIN = false>
 static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int device, int64_t cap,
                              int sm_count)
 {
@@ -1226,10 +1384,10 @@ static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int devi
     constexpr int smem_kv = BkSmem<DP>::kTotal + 1024, smem_q = BqSmem<DP>::kTotal + 1024;
     cudaError_t e;
     if (bit && !(raised.load() & bit)) {
-        e = cudaFuncSetAttribute(attn_bwd_kv_kernel<DP, F16>,
+        e = cudaFuncSetAttribute(attn_bwd_kv_kernel<DP, F16, WIN>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem_kv);
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(attn_bwd_q_kernel<DP, F16>,
+        e = cudaFuncSetAttribute(attn_bwd_q_kernel<DP, F16, WIN>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem_q);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit);
@@ -1239,12 +1397,39 @@ static cudaError_t ab_launch(const AttnBwdArgs& a, cudaStream_t stream, int devi
     const bool early = cap == kAttnMostCtas;  // (two at a time together would pass a cap)
     attn_bwd_stats_kernel<F16, DP / 8><<<unsigned(parts < cap ? parts : cap), 256, 0, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = attn_launch_early(attn_bwd_kv_kernel<DP, F16>,
-                          attn_ctas(heads * a.kv_order.blocks, cap, sm_count), kAbThreads, smem_kv,
-                          stream, a, early);
+    const int64_t kv_units = heads * (WIN ? a.kv_units.blocks : a.kv_order.blocks);
+    e = attn_launch_early(attn_bwd_kv_kernel<DP, F16, WIN>, attn_ctas(kv_units, cap, sm_count), kAbThreads,
+                          smem_kv, stream, a, early);
     if (e != cudaSuccess) return e;
-    return attn_launch_early(attn_bwd_q_kernel<DP, F16>, attn_ctas(heads * a.q_tiles, cap, sm_count),
-                             kAbThreads, smem_q, stream, a, early);
+    e = attn_launch_early(attn_bwd_q_kernel<DP, F16, WIN>, attn_ctas(heads * a.q_tiles, cap, sm_count),
+                          kAbThreads, smem_q, stream, a, early);
+    if constexpr (WIN) {
+        if (e != cudaSuccess || a.chunks == 1) return e;
+        // (not early: dQ's kernel ends after dK, dV's, whose parts these are)
+        int64_t blocks = (heads * a.sink_keys + 3) / 4;
+        if (blocks > 1 << 16) blocks = 1 << 16;
+        attn_bwd_join_kernel<F16><<<unsigned(blocks < cap ? blocks : cap), 128, 0, stream>>>(a);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+// The units of dK, dV with a window. A block of first tokens is walked by every row behind it, many times
+// what the others are: cut into units of a quarter of an SM's share of all the row tiles, but no shorter
+// than a window, so that the block's other keys have all their rows in the first.
+void attn_bwd_split(AttnBwdArgs* a, int sm_count)
+{
+    const AttnShape& s = a->s;
+    const int64_t blocks = a->kv_order.blocks, heads = a->kv_order.heads;
+    a->sink_keys = int32_t(s.sinks < s.Skv ? s.sinks : s.Skv);
+    a->sink_blocks = (a->sink_keys + kAttnRows - 1) / kAttnRows;
+    const int64_t reach = s.window >= s.Sq ? a->q_tiles : (s.window + kAttnRows - 2) / a->tile_tokens + 2;
+    const int64_t most = reach < a->q_tiles ? reach : a->q_tiles;
+    const int64_t all = heads * (blocks * most + int64_t(a->sink_blocks) * a->q_tiles);
+    const int64_t share = all / (4 * int64_t(sm_count));
+    a->chunk_tiles = share > reach ? share : reach;
+    a->chunks = a->sink_blocks ? int32_t((a->q_tiles + a->chunk_tiles - 1) / a->chunk_tiles) : 1;
+    a->kv_units = {heads, blocks + int64_t(a->sink_blocks) * (a->chunks - 1), a->kv_order.group};
 }
 
 // The three launches over all ranks. The shape, every pointer and the workspace are set in `a`.
@@ -1265,6 +1450,13 @@ cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* co
         if (!rows(&a.qmap[r], q[r]) || !rows(&a.gmap[r], a.go[r]) || !keys(&a.kmap[r], k[r]) ||
             !keys(&a.vmap[r], v[r]))
             return cudaErrorInvalidValue;
+    }
+    if (s.window) {
+        if (s.d <= 64)
+            return s.f16 ? ab_launch<64, true, true>(a, stream, device, cap, sm_count)
+                         : ab_launch<64, false, true>(a, stream, device, cap, sm_count);
+        return s.f16 ? ab_launch<128, true, true>(a, stream, device, cap, sm_count)
+                     : ab_launch<128, false, true>(a, stream, device, cap, sm_count);
     }
     if (s.d <= 64)
         return s.f16 ? ab_launch<64, true>(a, stream, device, cap, sm_count)

@@ -110,10 +110,11 @@ struct AfSmem {
     static_assert(kTotal + 1024 <= kSmemPerCtaMax, "shared memory");  // and room to align the base
 };
 
-struct AfUnit {
+template <bool WIN>
+struct AfUnit : AttnBlocks<WIN> {
     int r, bb, kvh, sp;
     int tok0, tok1;  // first token of each tile
-    int lo0, lo1;    // first key block of each tile
+    int lo0, lo1;    // first key block of each tile (with a window, in the order of block())
     int n0, n1;      // key blocks of each tile
     int len;         // keys of the batch element that any row sees
     int pos0;        // position of query token 0; beyond every key when not causal
@@ -123,6 +124,7 @@ struct AfUnit {
     __device__ __forceinline__ int most() const { return max(n0, n1); }
 };
 
+template <bool WIN>
 struct AfBars {
     uint64_t u_full[kAfMaxUnitSlots], u_empty[kAfMaxUnitSlots];  // unit records
     uint64_t q_full[4], q_empty[4];  // query tile landed; its rows are written
@@ -135,22 +137,27 @@ struct AfBars {
     uint4 answer;
     uint32_t tmem;
     CtaLife life;
-    AfUnit unit[kAfMaxUnitSlots];    // r < 0: no more
+    AfUnit<WIN> unit[kAfMaxUnitSlots];  // r < 0: no more
 };
-static_assert(sizeof(AfBars) <= kAfBarBytes, "barriers");
+static_assert(sizeof(AfBars<true>) <= kAfBarBytes, "barriers");
 
-// Key blocks that the tile of tokens from `tok` on sees.
-__device__ __forceinline__ int af_blocks(const AttnFwdArgs& a, const AfUnit& t, int64_t tok)
+// Key blocks that the tile of tokens from `tok` on sees; with a window, those of block()'s list up to
+// its last key (of two tiles of tokens the second's window may begin a block later: masked).
+template <bool WIN>
+__device__ __forceinline__ int af_blocks(const AttnFwdArgs& a, const AfUnit<WIN>& t, int64_t tok)
 {
     const int64_t last = min(tok + a.tile_tokens, a.s.Sq) - 1;
     const int64_t keys = min(int64_t(t.len), t.pos0 + last + 1);
-    return tok >= a.s.Sq || keys <= 0 ? 0 : int((keys + kAttnRows - 1) / kAttnRows);
+    const int n = tok >= a.s.Sq || keys <= 0 ? 0 : int((keys + kAttnRows - 1) / kAttnRows);
+    if constexpr (WIN) return t.count(n);
+    return n;
 }
 
-__device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
+template <bool WIN>
+__device__ __forceinline__ AfUnit<WIN> af_unit(const AttnFwdArgs& a, int64_t u)
 {
     const AttnShape& s = a.s;
-    AfUnit t;
+    AfUnit<WIN> t;
     const int64_t v = a.splits == 1 ? u : div_fast(u, a.splits);
     t.sp = int(u - v * a.splits);
     int64_t h, qb;
@@ -166,7 +173,7 @@ __device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
     attn_limits(s, t.bb, &len, &pos0);
     t.len = int(len);
     t.pos0 = int(pos0);
-    if (a.paired) {
+    if (!WIN && a.paired) {
         t.tok0 = t.tok1 = 0;
         const int total = af_blocks(a, t, 0);
         const int per = (total + a.parts - 1) / a.parts;
@@ -178,6 +185,8 @@ __device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
         const int64_t tok = qb * 2 * a.tile_tokens;
         t.tok0 = int(tok);
         t.tok1 = int(tok + a.tile_tokens);
+        if constexpr (WIN)  // from the first row's window on
+            t.set(s, max(int64_t(0), min(len, pos0 + tok + 1 - s.window)));
         const int b0 = af_blocks(a, t, tok), b1 = af_blocks(a, t, tok + a.tile_tokens);
         const int total = max(b0, b1);
         const int per = (total + a.splits - 1) / a.splits;
@@ -189,13 +198,13 @@ __device__ __forceinline__ AfUnit af_unit(const AttnFwdArgs& a, int64_t u)
 }
 
 // A warp's (or thread's) way through the CTA's units.
-template <int SLOTS>
+template <int SLOTS, bool WIN>
 struct AfUnits {
-    AfBars* bars;
+    AfBars<WIN>* bars;
     StageRing ring;
     // The next unit; false: none, or the CTA has given up. WARP: called by a whole warp.
     template <bool WARP>
-    __device__ __forceinline__ bool next(AfUnit* t)
+    __device__ __forceinline__ bool next(AfUnit<WIN>* t)
     {
         bool ok = wait_or_dead(&bars->u_full[ring.s], ring.phase, &bars->life);
         if (WARP) ok = __all_sync(0xffffffffu, ok);
@@ -211,7 +220,7 @@ struct AfUnits {
         const bool ok = wait_or_dead(&bars->u_full[ring.s], ring.phase, &bars->life);
         return __all_sync(0xffffffffu, ok) && bars->unit[ring.s].r >= 0;
     }
-    __device__ __forceinline__ const AfUnit& record() const { return bars->unit[ring.s]; }
+    __device__ __forceinline__ const AfUnit<WIN>& record() const { return bars->unit[ring.s]; }
     template <bool WARP>
     __device__ __forceinline__ void release()
     {
@@ -228,7 +237,8 @@ struct AfRow {
     bool valid;
 };
 
-__device__ __forceinline__ AfRow af_row(const AttnFwdArgs& a, const AfUnit& t, int tile, int tok_in,
+template <bool WIN>
+__device__ __forceinline__ AfRow af_row(const AttnFwdArgs& a, const AfUnit<WIN>& t, int tile, int tok_in,
                                         int head_in)
 {
     const AttnShape& s = a.s;
@@ -244,7 +254,8 @@ __device__ __forceinline__ AfRow af_row(const AttnFwdArgs& a, const AfUnit& t, i
 }
 
 // A row that sees no key (or no key of its part, which then has no output).
-__device__ __forceinline__ void af_empty_row(const AttnFwdArgs& a, const AfUnit& t, const AfRow& r)
+template <bool WIN>
+__device__ __forceinline__ void af_empty_row(const AttnFwdArgs& a, const AfUnit<WIN>& t, const AfRow& r)
 {
     if (!r.valid) return;
     *r.lse = -INFINITY;
@@ -256,11 +267,11 @@ __device__ __forceinline__ void af_empty_row(const AttnFwdArgs& a, const AfUnit&
 // block) for every stage of the ring, and queries(t) for a unit's query tiles, after its first keys
 // (a slot for them may have to wait for the unit before to finish, which those keys must not).
 // Both return false to stop.
-template <bool PAIRED, int SLOTS, bool WARP, class Queries, class Block>
-__device__ __forceinline__ void af_walk(AfBars* bars, Queries queries, Block block)
+template <bool PAIRED, int SLOTS, bool WARP, bool WIN, class Queries, class Block>
+__device__ __forceinline__ void af_walk(AfBars<WIN>* bars, Queries queries, Block block)
 {
-    AfUnits<SLOTS> units{bars};
-    AfUnit t;
+    AfUnits<SLOTS, WIN> units{bars};
+    AfUnit<WIN> t;
     bool live = units.template next<WARP>(&t);
     while (live) {
         const int n = t.most();
@@ -277,10 +288,10 @@ __device__ __forceinline__ void af_walk(AfBars* bars, Queries queries, Block blo
                 }
             }
         } else {
-            if (!block(false, t, t.lo0) || !queries(t)) return;
+            if (!block(false, t, t.block(t.lo0)) || !queries(t)) return;
             for (int j = 0; j < n; ++j) {
-                if (!block(true, t, t.lo0 + j)) return;
-                if (j + 1 < n && !block(false, t, t.lo0 + j + 1)) return;
+                if (!block(true, t, t.block(t.lo0 + j))) return;
+                if (j + 1 < n && !block(false, t, t.block(t.lo0 + j + 1))) return;
             }
         }
         live = units.template next<WARP>(&t);
@@ -289,13 +300,22 @@ __device__ __forceinline__ void af_walk(AfBars* bars, Queries queries, Block blo
 
 // Rows of a value block past the batch element's last key, where any of them can hold a value
 // (past the tensor's end the copy itself writes zeros); kAttnRows: none.
-__device__ __forceinline__ int af_past(const AttnShape& s, const AfUnit& t, int block)
+template <bool WIN>
+__device__ __forceinline__ int af_past(const AttnShape& s, const AfUnit<WIN>& t, int block)
 {
     const int past = t.len - block * kAttnRows;
     return past >= kAttnRows || t.len >= s.Skv ? kAttnRows : past;
 }
 
-template <int DP, bool F16, int MODE>
+// Whether a value block holds rows that warp 10 zeroes.
+template <bool WIN>
+__device__ __forceinline__ bool af_unclean(const AttnShape& s, const AfUnit<WIN>& t, int block)
+{
+    const int2 b = attn_between<WIN>(s, t.pos0, block);
+    return af_past(s, t, block) < kAttnRows || b.y > b.x;
+}
+
+template <int DP, bool F16, int MODE, bool WIN>
 __global__ void __launch_bounds__(kAfThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnFwdArgs a)
 {
@@ -303,10 +323,12 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     using E = ElemT<F16>;
     constexpr int K = L::kStages, Q = L::kSlots;
     constexpr bool PAIRED = L::kPaired;
+    static_assert(!WIN || !PAIRED, "few rows with a window: attention_paged.cu");
+    using Unit = AfUnit<WIN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
-    AfBars& bars = *reinterpret_cast<AfBars*>(smem);
+    AfBars<WIN>& bars = *reinterpret_cast<AfBars<WIN>*>(smem);
     volatile CtaLife* life = &bars.life;
     const AttnShape& s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -353,7 +375,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             int64_t issued = 0, tiles = 0;
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
-            auto queries = [&](const AfUnit& t) {
+            auto queries = [&](const Unit& t) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (t.n(k) == 0) continue;
@@ -369,7 +391,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 return true;
             };
-            auto block = [&](bool value, const AfUnit& t, int at) {
+            auto block = [&](bool value, const Unit& t, int at) {
                 if (issued >= K && !wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, life))
                     return false;
                 const CUtensorMap* map = value ? &a.vmap[t.r] : &a.kmap[t.r];
@@ -394,18 +416,23 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             // NaN: a value block's rows past it become zeros before its product.
             StageRing ring;
             af_walk<PAIRED, L::kUnitSlots, true>(
-                &bars, [](const AfUnit&) { return true; },
-                [&](bool value, const AfUnit& t, int at) {
+                &bars, [](const Unit&) { return true; },
+                [&](bool value, const Unit& t, int at) {
                     const int past = value ? af_past(s, t, at) : kAttnRows;
+                    const int2 between =
+                        value ? attn_between<WIN>(s, t.pos0, at) : make_int2(0, 0);
                     if (!__all_sync(0xffffffffu,
                                     wait_or_dead(&bars.kv_full[ring.s], ring.phase, life)))
                         return false;
-                    if (past < kAttnRows) {
-                        for (int h = 0; h < halves; ++h)
+                    if (past < kAttnRows || between.y > between.x) {
+                        for (int h = 0; h < halves; ++h) {
+                            uint8_t* rows = smem + L::kRing + ring.s * L::kTile + h * L::kHalf;
                             for (int w = past * 8 + lane; w < kAttnRows * 8; w += 32)
-                                st_shared_v4(smem + L::kRing + ring.s * L::kTile + h * L::kHalf +
-                                                 w * 16,
-                                             make_uint4(0, 0, 0, 0));
+                                st_shared_v4(rows + w * 16, make_uint4(0, 0, 0, 0));
+                            if constexpr (WIN)
+                                for (int w = between.x * 8 + lane; w < between.y * 8; w += 32)
+                                    st_shared_v4(rows + w * 16, make_uint4(0, 0, 0, 0));
+                        }
                         fence_proxy_async_shared();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bars.clean[ring.s]);
@@ -449,7 +476,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 tc_fence_after();
                 scores(k, stage);
             };
-            auto output = [&](const AfUnit& t, int k, int stage, int j) {  // O_k += P_k V
+            auto output = [&](const Unit& t, int k, int stage, int j) {  // O_k += P_k V
                 wait(&bars.p_half[k], blocks[k] & 1);
                 if (j == 0 && uses[k] > 0) wait(&bars.o_free[k], (uses[k] - 1) & 1);
                 if (!ok) return;
@@ -471,15 +498,15 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
             };
             auto stage_ready = [&]() { return wait(&bars.kv_full[ring.s], ring.phase); };
-            auto values_ready = [&](const AfUnit& t, int at) {
+            auto values_ready = [&](const Unit& t, int at) {
                 stage_ready();
-                if (s.ragged && af_past(s, t, at) < kAttnRows) {
+                if (s.ragged && af_unclean(s, t, at)) {
                     wait(&bars.clean[ring.s], (cleaned >> ring.s) & 1);
                     cleaned ^= 1u << ring.s;
                 }
                 return ok;
             };
-            auto unit_scores = [&](const AfUnit& t) {  // a paired unit's first scores
+            auto unit_scores = [&](const Unit& t) {  // a paired unit's first scores
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (t.n(k) == 0 || !stage_ready()) continue;
@@ -488,8 +515,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     ring.next(K);
                 }
             };
-            AfUnits<L::kUnitSlots> units{&bars};
-            AfUnit t, next;
+            AfUnits<L::kUnitSlots, WIN> units{&bars};
+            Unit t, next;
             bool live = units.template next<false>(&t);
             if (live) {
                 if constexpr (PAIRED) {
@@ -527,7 +554,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     } else {
                         const bool last = j + 1 == n;
                         const int vs = ring.s;
-                        if (!values_ready(t, t.lo0 + j)) break;
+                        if (!values_ready(t, t.block(t.lo0 + j))) break;
                         ring.next(K);
                         const int ks = ring.s;
                         const bool any = !last || more;
@@ -566,7 +593,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                                     wait_watching(&bars.u_empty[ring.s], ring.phase ^ 1u, life));
                 return ok;
             };
-            auto publish = [&](const AfUnit& t) {
+            auto publish = [&](const Unit& t) {
                 if (lane == 0) {
                     bars.unit[ring.s] = t;
                     mbar_arrive(&bars.u_full[ring.s]);
@@ -575,10 +602,10 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 ++made;
                 ring.next(L::kUnitSlots);
             };
-            AfUnit t;
+            Unit t;
             AttnUnitSource source{a.units, &bars.answer, &bars.steal, life};
             for (int64_t u; room() && (u = source.next()) >= 0;) {
-                t = af_unit(a, u);
+                t = af_unit<WIN>(a, u);
                 if (t.most() > 0) {
                     publish(t);
                 } else {  // nothing to do but say so (the other warps see units with work only)
@@ -615,14 +642,16 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        AfUnits<L::kUnitSlots> units{&bars};
+        AfUnits<L::kUnitSlots, WIN> units{&bars};
         StageRing slots;
         while (ok && units.peek()) {
             // What the loop over the blocks does not need is read again after it: a row's scores
             // take 128 registers.
             int slot = 0, n, left;  // of this tile's queries; its blocks; keys seen from its first
+            int at = 0, low = 0;    // with a window: the block, its row's first key
+            AttnBlocks<WIN> list;
             {
-                const AfUnit& t = units.record();
+                const Unit& t = units.record();
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (t.n(k) == 0) continue;
@@ -637,6 +666,13 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 const int64_t seen = min(int64_t(t.len), t.pos0 + int64_t(t.tok(tile)) + tok_in + 1);
                 left = int(max(int64_t(-1), seen - int64_t(t.lo(tile)) * kAttnRows));
+                if constexpr (WIN) {
+                    list = t;
+                    at = t.lo(tile);
+                    left = int(max(int64_t(0), seen));
+                    low = int(max(int64_t(0), min(int64_t(t.len), t.pos0 + int64_t(t.tok(tile)) + tok_in + 1 -
+                                                                      s.window)));
+                }
             }
             float m = -INFINITY, l = 0.0f;
             if (PAIRED && (warp & 3) * 32 >= rows) {  // none of the tile's rows: only keep step
@@ -657,7 +693,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 units.template release<true>();
                 continue;
             }
-            for (int j = 0; j < n; ++j, left -= kAttnRows) {
+            for (int j = 0; j < n; ++j, left -= WIN ? 0 : kAttnRows) {
                 ok = all(&bars.s_full[tile], blocks & 1);
                 if (!ok) break;
                 ++blocks;
@@ -667,8 +703,22 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, x[q]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_wait_ld(x[q]);
-                if (__any_sync(0xffffffffu, left < kAttnRows)) {
-                    const int seen = max(0, left);
+                int from = 0, to = 0;  // keys of the block between the first tokens and the row's window
+                int seen = left;
+                if constexpr (WIN) {
+                    const int key0 = list.block(at + j) * kAttnRows;
+                    seen = left - key0;
+                    from = s.sinks - key0;
+                    to = low - key0;
+                    if (__any_sync(0xffffffffu, to > max(0, from) && from < kAttnRows)) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (q * 32 + c >= from && q * 32 + c < to) x[q][c] = 0xFF800000u;
+                    }
+                }
+                if (__any_sync(0xffffffffu, seen < kAttnRows)) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -726,7 +776,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             ok = all(&bars.o_full[tile], uses & 1);
             if (!ok) break;
             tc_fence_after();
-            const AfUnit& t = units.record();
+            const Unit& t = units.record();
             const AfRow to = af_row(a, t, tile, tok_in, head_in);
             const bool whole = a.parts == 1;
             uint8_t* o = a.o[t.r];
@@ -876,17 +926,30 @@ int64_t attn_order_group(int64_t heads, int64_t bytes)
 // Row tiles, units and parts of the keys. Where one tile holds all rows, a CTA's two tiles take a
 // part each. The keys are split further while a part keeps some blocks (a part costs its start, an
 // fp32 output and a share of the join).
+// Key blocks of a unit at most.
+static int64_t af_most_blocks(const AttnShape& s, int64_t pair)
+{
+    const int64_t all = (s.Skv + kAttnRows - 1) / kAttnRows;
+    if (!s.window) return all;
+    // (a window of w keys over `pair` tokens, anywhere in a block; the first tokens)
+    const int64_t near = s.window >= s.Skv ? all : (s.window + pair - 2) / kAttnRows + 2;
+    const int64_t some = near + (s.sinks + kAttnRows - 1) / kAttnRows;
+    return some < all ? some : all;
+}
+
 void attn_fwd_split(AttnFwdArgs* a, int sm_count)
 {
     const AttnShape& s = a->s;
     a->tile_tokens = kAttnRows / s.group;
     const int64_t pair = 2 * int64_t(a->tile_tokens);
-    const int64_t blocks = (s.Skv + kAttnRows - 1) / kAttnRows;
-    a->paired = s.Sq <= a->tile_tokens && blocks > 1;
+    const int64_t blocks = af_most_blocks(s, pair);
+    a->paired = !s.window && s.Sq <= a->tile_tokens && blocks > 1;
     if (a->paired) a->tile_tokens = int32_t(s.Sq);
     a->order.heads = s.head_begin[s.W];
     a->order.blocks = a->paired ? 1 : (s.Sq + pair - 1) / pair;
-    a->order.group = attn_order_group(a->order.heads, s.Skv * s.d * 4);  // keys and values
+    // keys and values (with a window, those of a unit)
+    a->order.group =
+        attn_order_group(a->order.heads, (s.window ? blocks * kAttnRows : s.Skv) * s.d * 4);
     const int64_t base = a->order.heads * a->order.blocks;
     // One wave of the SMs (finer parts of a ragged batch, evened out by stealing, measured no faster:
     // 16 caches of 4 key heads 134 us with 2 units a head, 134 with 7, 136 with 9, 154 with 19; no other
@@ -904,7 +967,7 @@ void attn_fwd_split(AttnFwdArgs* a, int sm_count)
     a->units = base * a->splits;
 }
 
-template <int DP, bool F16, int MODE>
+template <int DP, bool F16, int MODE, bool WIN = false>
 static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int device, int64_t cap,
                                   int sm_count)
 {
@@ -912,12 +975,12 @@ static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
     constexpr int smem = AfSmem<DP, MODE>::kTotal + 1024;
     if (bit && !(raised.load() & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, F16, MODE>,
+        cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, F16, MODE, WIN>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit);
     }
-    attn_fwd_kernel<DP, F16, MODE>
+    attn_fwd_kernel<DP, F16, MODE, WIN>
         <<<attn_ctas(a.units, cap, sm_count), kAfThreads, smem, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || a.parts == 1) return e;
@@ -931,6 +994,12 @@ template <int DP, bool F16>
 static cudaError_t af_launch(const AttnFwdArgs& a, cudaStream_t stream, int device, int64_t cap,
                              int sm_count)
 {
+    if (a.s.window) {
+        if constexpr (DP == 128)
+            if (af_most_blocks(a.s, 2 * int64_t(a.tile_tokens)) <= kAfShortBlocksPadded * a.splits)
+                return af_launch_mode<DP, F16, kAfShort, true>(a, stream, device, cap, sm_count);
+        return af_launch_mode<DP, F16, kAfLong, true>(a, stream, device, cap, sm_count);
+    }
     if (a.paired)
         return a.tile_tokens * a.s.group <= kAfTokenRows
                    ? af_launch_mode<DP, F16, kAfToken>(a, stream, device, cap, sm_count)
