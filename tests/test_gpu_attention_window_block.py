@@ -73,9 +73,14 @@ def test_block(window, sinks):
     xd, wd = x.double().requires_grad_(), w.double().requires_grad_()
     want = plain_block(xd, wd, window, sinks)
     want.backward(go.double())
-    for got, ref in ((torch.cat(out, 1), want), (torch.cat([t.grad for t in shards], 1), xd.grad),
-                     (wl.grad, wd.grad)):
-        assert float((got.double() - ref).abs().max() / ref.abs().max()) < 2e-2
+    # A row that sees one key (a window of 1) has P = 1 and dS = go . v - go . o = 0. Both are fp32 sums of 64
+    # products, 41 of magnitude together, so dS comes out as 2^-22 * 41 at most, and the norm weights' gradient
+    # as that times scale * |k| (1/8) over 2 * 256 * 6 rows: 3.8e-3 in place of the 0 that is exact.
+    near_zero = 2 * sum(seq) * sum(heads) / 8 * 41 * 2.0 ** -22
+    for got, ref, least in ((torch.cat(out, 1), want, 0.0),
+                            (torch.cat([t.grad for t in shards], 1), xd.grad, 0.0),
+                            (wl.grad, wd.grad, near_zero)):
+        assert float((got.double() - ref).detach().abs().max()) < 2e-2 * float(ref.detach().abs().max()) + least
 
 
 def test_prompt_with_a_window_then_tokens_over_the_pages():
