@@ -1186,7 +1186,7 @@ int window_pages(const Plan& qp, const Plan& kp, const Window& w, PagedArgs* a)
     AttnShape s;
     int rc = attn_shape(qp, kp, &s);
     if (rc || (rc = attn_window(&s, w.keys, w.sinks)) || (rc = paged_shape(qp, kp, a))) return rc;
-    a->box = kPagedTile;
+    a->box = kPagedBlock;
     a->room = int32_t(kp.S);
     a->window = s.window;
     a->sinks = s.sinks;
@@ -1699,7 +1699,8 @@ int ulysses_attention_paged(ulysses_plan_t q_plan, ulysses_plan_t cache_plan, co
     a.kv_lens = kv_lens;
     a.q_start = q_start;
     a.from_end = 1;
-    a.box = cp.S % 16 == 0 ? 16 : 8;
+    a.box = 8;  // rows of a copy: as many as divide a page and a block
+    while (a.box < kPagedBlock && cp.S % (2 * a.box) == 0) a.box *= 2;
     a.room = int32_t(room);
     a.window = window && window < kAttnFar ? window : kAttnFar;
     a.sinks = int32_t(sinks < room ? sinks : room);

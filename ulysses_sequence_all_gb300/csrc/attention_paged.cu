@@ -9,12 +9,12 @@
 // flops: below some 200 rows memory bounds it, and the design is made to keep copies in flight. All the
 // work (the blocks of 64 keys that any row of a (batch element, row group, key head) sees) is laid end
 // to end and cut into as many equal shares as CTAs run at a time, two an SM, whatever the sequences'
-// lengths: a CTA finds its share from the lengths by one scan. Each of its 4 warps takes 16 keys of a
-// block and is its own pipeline: one lane copies its next tiles (tensor maps, a box per page) into a
-// ring of its own, the warp waits for nothing but its own barrier, and no warp waits for another until
-// a sequence ends. There the warps' maxima, sums and outputs are joined through the ring's free slots;
-// a sequence that several CTAs share leaves its parts as normalised fp32 outputs with their lse, which
-// attn_paged_join_kernel adds in order: the same bits from run to run.
+// lengths: a CTA finds its share from the lengths by one scan. Warp 4 walks the share and copies block
+// after block into a ring (tensor maps, a lane a page, the table read a block ahead); warps 0-3 take 16
+// keys of a block each and wait for no one but the copies until a sequence ends. There the warps'
+// maxima, sums and outputs are joined through the last block's stage; a sequence that several CTAs share
+// leaves its parts as normalised fp32 outputs with their lse, which attn_paged_join_kernel adds in order:
+// the same bits from run to run.
 //
 // Products: S^T = K Q^T and O^T += V^T P^T with keys (and columns of V) as the 16 rows of an
 // m16n8k16 product, so that a tile of 8 query rows costs no more than its own work. A product of this
@@ -41,7 +41,10 @@ namespace uly {
 
 static __device__ unsigned g_attn_paged_status;
 
-constexpr int kPgThreads = 32 * kPagedWarps;
+constexpr int kPgThreads = 2 * 32 * kPagedWarps;  // warps 0-3, and a warpgroup with the copying one
+// Registers a thread: 256 x 128 at launch = 128 x 176 + 128 x 80, or 128 x 208 + 128 x 48 with 32 rows
+template <int RT>
+constexpr int kPgRegsProducts = RT == 4 ? 208 : 176;
 constexpr float kPgRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 constexpr float kPgUpF16 = 7.0f;    // fp16 probabilities are held times 2^this
 constexpr int kPgJoinThreads = 256;
@@ -114,24 +117,24 @@ __device__ __forceinline__ int paged_owner(int64_t total, int parts, int64_t blo
 
 // ---- the kernel -------------------------------------------------------------------------------------
 
-template <int DP>
+template <int DP, int RT>
 struct PgSmem {
-    static constexpr int kHalf = kPagedTile * 128;            // 64 columns of a tile
+    static constexpr int kHalf = kPagedBlock * 128;           // 64 columns of a block
     static constexpr int kV = kHalf * (DP / 64);              // values after keys
-    static constexpr int kTile = 2 * kV;
+    static constexpr int kBlock = 2 * kV;
     static constexpr int kStages = DP == 128 ? 3 : 6;
-    static constexpr int kTiles = 2048;                       // PgShared first
-    static constexpr int kTotal = kTiles + kPagedWarps * kStages * kTile;
+    static constexpr int kRing = 2048;                        // PgShared first
+    static constexpr int kQ = kRing + kStages * kBlock;       // 32 rows of queries (fewer: in registers)
+    static constexpr int kTotal = kQ + (RT == 4 ? kPagedMaxRows * DP * 2 : 0);
     static_assert(2 * (kTotal + 1024 + kSmemReservedPerCta) <= kSmemPerSm, "two CTAs an SM");
 };
 
 struct PgShared {
-    uint64_t full[kPagedWarps][6];
-    PagedWalk load[kPagedWarps];
+    uint64_t full[6], empty[6];
     float2 ml[kPagedWarps][kPagedMaxRows];  // each warp's maxima and sums
-    int slot[kPagedWarps];                  // where its outputs lie
-    int64_t warp_sum[kPagedWarps];
-    int64_t total, before;  // blocks of all; of the entries before `entry`
+    int used[kPagedWarps];                  // whether it has outputs
+    int64_t warp_sum[kPgThreads / 32];
+    int64_t before;  // blocks of the entries before `entry`
     int entry;
 };
 static_assert(sizeof(PgShared) <= 2048, "shared memory");
@@ -176,32 +179,40 @@ __device__ __forceinline__ uint32_t pg_transpose(uint32_t x)
     return y;
 }
 
+__device__ __forceinline__ void pg_sync()  // the four warps with products
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kPagedWarps) : "memory");
+}
+
 // RT: tiles of 8 query rows.
 template <int DP, bool F16, int RT>
 __global__ void __launch_bounds__(kPgThreads, 2)
     attn_paged_kernel(const __grid_constant__ PagedArgs a)
 {
-    using L = PgSmem<DP>;
+    using L = PgSmem<DP, RT>;
     using E = ElemT<F16>;
     constexpr int K = L::kStages, kD = DP / 16, kRows = 8 * RT;
-    constexpr int kRound = RT < 2 ? RT : 2;  // tiles of rows whose outputs a slot holds
+    constexpr int kRound = RT < 2 ? RT : 2;       // tiles of rows whose outputs a warp's part of a stage holds
+    constexpr int kPartRows = 2048 / (DP * 4);    // rows of outputs in 16 rows of a tile's 128 bytes
+    constexpr bool kQShared = RT == 4;
     constexpr float kUp = F16 ? kPgUpF16 : 0.0f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     PgShared& sh = *reinterpret_cast<PgShared*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t* ring_at = smem + L::kTiles + warp * K * L::kTile;
-    const int nk = (a.d + 15) / 16, halves = (a.d + 63) / 64, heads = a.m_begin[a.W];
-    const float sl2 = a.scale * 1.4426950408889634f;
-    const int quad = lane >> 2, pair = (lane & 3) * 2;  // fragments: key (column of V); query row
+    const int halves = (a.d + 63) / 64, heads = a.m_begin[a.W];
+    const uint64_t limit = uint64_t(a.wait_us) * 1000u;
 
-    if (lane == 0) {
-        for (int k = 0; k < K; ++k) mbar_init(&sh.full[warp][k], 1);
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < K; ++k) {
+            mbar_init(&sh.full[k], 1);
+            mbar_init(&sh.empty[k], kPagedWarps);
+        }
         fence_barrier_init();
     }
 
-    // How many blocks there are, and in which entry this CTA's share begins.
+    // How many blocks there are, and in which entry a share begins.
     const int entries = a.b * a.row_groups;
     const int each = (entries + kPgThreads - 1) / kPgThreads;
     const int e0 = min(entries, int(threadIdx.x) * each), e1 = min(entries, e0 + each);
@@ -216,105 +227,152 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     if (lane == 31) sh.warp_sum[warp] = upto;
     __syncthreads();
     int64_t total = 0;
-    for (int w = 0; w < kPagedWarps; ++w) {
+#pragma unroll
+    for (int w = 0; w < kPgThreads / 32; ++w) {
         if (w < warp) upto += sh.warp_sum[w];
         total += sh.warp_sum[w];
     }
-    const int64_t before = upto - mine;
     total *= heads;
 
-    StageRing ring, fill;
-    int flying = 0;  // lane 0: copies that have not been waited for
+    StageRing ring;
+    int64_t issued = 0;  // warp 4: blocks copied
     bool ok = true;
 
-    for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
-        const int64_t begin = paged_share(total, a.parts, c), stop = paged_share(total, a.parts, c + 1);
+    // Share c: its blocks begin .. stop - 1, and the walk through them. Called by every warp.
+    int64_t begin = 0, stop = 0;
+    PagedWalk walk;
+    auto share = [&](int c) {
+        begin = paged_share(total, a.parts, c);
+        stop = paged_share(total, a.parts, c + 1);
         __syncthreads();
-        if (begin >= before * heads && begin < upto * heads) {
-            int64_t at = before;
+        if (begin >= (upto - mine) * heads && begin < upto * heads) {
+            int64_t at = upto - mine;
             int e = e0;
             for (int n; begin >= (at + (n = paged_entry(a, e).n)) * heads; ++e) at += n;
             sh.entry = e;
             sh.before = at;
         }
         __syncthreads();
-        PagedShared shared = {0, 0, 0, 0};
-        if (begin < stop) {
-            PagedWalk walk;
-            walk.left = stop - begin;
+        walk.left = stop - begin;
+        if (walk.left > 0) {
             walk.e = sh.entry;
             walk.en = paged_entry(a, walk.e);
             const int64_t off = begin - sh.before * heads;
             walk.head = int(div_fast(off, walk.en.n));
             walk.j = int(off - int64_t(walk.head) * walk.en.n);
-            if (lane == 0) sh.load[warp] = walk;
+        }
+    };
 
-            // This warp's next tile that any row sees anything of.
-            auto issue = [&]() {
-                if (lane == 0 && ok) {
-                    PagedWalk& w = sh.load[warp];
-                    while (w.left > 0) {
-                        const PagedEntry& en = w.en;
-                        const int key0 = en.block(w.j) * kPagedBlock + warp * kPagedTile;
-                        const bool any = en.sees(key0, key0 + kPagedTile);
-                        if (any) {
-                            int r = 0;
-                            while (r + 1 < a.W && w.head >= a.m_begin[r + 1]) ++r;
-                            const int kvh = w.head - a.m_begin[r];
-                            int boxes = 0;
-                            for (int k = 0; k < kPagedTile; k += a.box)
-                                boxes += en.sees(key0 + k, key0 + k + a.box);
-                            uint64_t* bar = &sh.full[warp][fill.s];
-                            mbar_arrive_expect_tx(bar, uint32_t(boxes * a.box * 256 * halves));
-                            for (int k = 0; k < kPagedTile; k += a.box) {
-                                const int key = key0 + k;
-                                if (!en.sees(key, key + a.box)) continue;
-                                int page = en.bb, row = key;
-                                if (a.table) {
-                                    const int p = key / a.page;
-                                    page = a.table[int64_t(en.bb) * a.table_pages + p];
-                                    row = key - p * a.page;
-                                    // (outside the pool a copy reads zeros)
-                                    if (page < 0 || page >= a.pages)
-                                        atomicOr(&g_attn_paged_status, kStatusBadPage);
-                                }
-                                uint8_t* to = ring_at + fill.s * L::kTile + k * 128;
-                                for (int h = 0; h < halves; ++h) {
-                                    tensor_g2s_4d(to + h * L::kHalf, &a.kmap[r], 64 * h, kvh, row, page,
-                                                  bar);
-                                    tensor_g2s_4d(to + L::kV + h * L::kHalf, &a.vmap[r], 64 * h, kvh,
-                                                  row, page, bar);
-                                }
-                            }
-                            ++flying;
-                            fill.next(K);
+    if (warp >= kPagedWarps) {  // the copies
+        regs_shrink<256 - kPgRegsProducts<RT>>();
+        for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
+            share(c);
+            if (warp > kPagedWarps) continue;
+            const int box = lane * a.box;  // this lane's rows of a block
+            bool seen = false;             // some row sees one of them; their page, its row
+            int page = 0, row = 0, r = 0, kvh = 0;
+            bool live = false;             // a block is in hand
+            auto look = [&]() {            // the walk's next block that any row sees anything of
+                live = false;
+                while (walk.left > 0) {
+                    const int key0 = walk.en.block(walk.j) * kPagedBlock;
+                    live = walk.en.sees(key0, key0 + kPagedBlock);
+                    if (live) {
+                        r = 0;
+                        while (r + 1 < a.W && walk.head >= a.m_begin[r + 1]) ++r;
+                        kvh = walk.head - a.m_begin[r];
+                        const int key = key0 + box;
+                        seen = box < kPagedBlock && walk.en.sees(key, key + a.box);
+                        page = walk.en.bb;
+                        row = key;
+                        if (a.table && seen) {
+                            const int p = int(uint32_t(key) / uint32_t(a.page));
+                            page = a.table[int64_t(walk.en.bb) * a.table_pages + p];
+                            row = key - p * a.page;
                         }
-                        w.step(a);
-                        if (any) break;
+                    }
+                    walk.step(a);
+                    if (live) break;
+                }
+            };
+            look();
+            while (live && ok) {
+                const bool now_seen = seen;
+                const int now_page = page, now_row = row, now_r = r, now_kvh = kvh;
+                look();
+                if (issued >= K)
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait_bounded(&sh.empty[ring.s], ring.phase ^ 1u, limit));
+                if (!ok) break;
+                const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, now_seen));
+                uint64_t* bar = &sh.full[ring.s];
+                if (lane == 0) mbar_arrive_expect_tx(bar, boxes * uint32_t(a.box) * 256u * halves);
+                __syncwarp();
+                if (now_seen) {
+                    // (outside the pool a copy reads zeros)
+                    if (now_page < 0 || now_page >= a.pages)
+                        atomicOr(&g_attn_paged_status, kStatusBadPage);
+                    uint8_t* to = smem + L::kRing + ring.s * L::kBlock + box * 128;
+                    for (int h = 0; h < halves; ++h) {
+                        tensor_g2s_4d(to + h * L::kHalf, &a.kmap[now_r], 64 * h, now_kvh, now_row,
+                                      now_page, bar);
+                        tensor_g2s_4d(to + L::kV + h * L::kHalf, &a.vmap[now_r], 64 * h, now_kvh, now_row,
+                                      now_page, bar);
                     }
                 }
                 __syncwarp();
-            };
-            __syncwarp();
-            for (int k = 0; k < K; ++k) issue();
+                ++issued;
+                ring.next(K);
+            }
+        }
+        if (!ok && lane == 0) atomicOr(&g_attn_paged_status, kStatusWaitTimeout);
+        // leave no copy into this CTA's shared memory in flight
+        if (lane == 0)
+            for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k)
+                if (!mbar_wait_bounded(&sh.full[k % K], uint32_t((k / K) & 1)))
+                    atomicOr(&g_attn_paged_status, kStatusDrainTimeout);
+        let_next_start();
+        return;
+    }
 
-            int64_t at = begin;  // the walk's block
-            bool pending = false;
-            while (walk.left > 0) {
-                const PagedEntry en = walk.en;
-                const int64_t seg = at - walk.j, seg_end = seg + en.n;  // its blocks
-                int r = 0;
-                while (r + 1 < a.W && walk.head >= a.m_begin[r + 1]) ++r;
-                const int head = walk.head, kvh = head - a.m_begin[r];
-                const int64_t row0 = int64_t(en.rg) * kRows, row_end = a.Sq * a.group;
-                uint32_t q[RT][kD][2];
+    // the products
+    regs_grow<kPgRegsProducts<RT>>();
+    const int nk = (a.d + 15) / 16;
+    const float sl2 = a.scale * 1.4426950408889634f;
+    const int quad = lane >> 2, pair = (lane & 3) * 2;  // fragments: key (column of V); query row
+    for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
+        share(c);
+        PagedShared shared = {0, 0, 0, 0};
+        int64_t at = begin;  // the walk's block
+        while (walk.left > 0) {
+            const PagedEntry en = walk.en;
+            const int64_t seg = at - walk.j, seg_end = seg + en.n;  // its blocks
+            int r = 0;
+            while (r + 1 < a.W && walk.head >= a.m_begin[r + 1]) ++r;
+            const int head = walk.head, kvh = head - a.m_begin[r];
+            const int64_t row0 = int64_t(en.rg) * kRows, row_end = a.Sq * a.group;
+            auto query = [&](int64_t row) {  // its first byte
+                const int64_t tok = div_fast(row, a.group);
+                return a.q[r] + ((int64_t(en.bb) * a.Sq + tok) * a.n[r] + kvh * a.group + row -
+                                 tok * a.group) * a.d * 2;
+            };
+            uint32_t q[kQShared ? 1 : RT][kD][2];
+            if constexpr (kQShared) {
+                for (int i = threadIdx.x; i < kRows * (DP / 8); i += 32 * kPagedWarps) {
+                    const int row = i / (DP / 8), w = i % (DP / 8);
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (row0 + row < row_end && w * 8 < a.d)
+                        x = *reinterpret_cast<const uint4*>(query(row0 + row) + w * 16);
+                    st_shared_v4(smem + L::kQ + (w >> 3) * kRows * 128 + row * 128 +
+                                     (((w & 7) ^ (row & 7)) << 4),
+                                 x);
+                }
+                pg_sync();
+            } else {
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
                     const int64_t row = row0 + t * 8 + quad;
-                    const int64_t tok = div_fast(row, a.group);
-                    const uint8_t* src =
-                        a.q[r] + (((int64_t(en.bb) * a.Sq + tok) * a.n[r] + kvh * a.group + row -
-                                   tok * a.group) * a.d + pair) * 2;
+                    const uint8_t* src = query(row) + pair * 2;
 #pragma unroll
                     for (int ks = 0; ks < kD; ++ks)
 #pragma unroll
@@ -325,242 +383,258 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                                     src + (ks * 16 + h * 8) * 2));
                         }
                 }
-                // keys that every row sees: below hi_all, and from lo_all on or first tokens
-                const int hi_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t0 + 1)));
-                const int lo_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t1 - a.window)));
-                float m[RT][2], l[RT][2], o[RT][kD][4];
+            }
+            // keys that every row sees: below hi_all, and from lo_all on or first tokens
+            const int hi_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t0 + 1)));
+            const int lo_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t1 - a.window)));
+            float m[RT][2], l[RT][2], o[RT][kD][4];
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
+            for (int t = 0; t < RT; ++t) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) m[t][i] = -INFINITY, l[t][i] = 0.0f;
+                for (int i = 0; i < 2; ++i) m[t][i] = -INFINITY, l[t][i] = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < kD; ++i)
+                for (int i = 0; i < kD; ++i)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) o[t][i][x] = 0.0f;
-                }
-                bool used = false;
-                int slot = 0;
-                do {
-                    const int key0 = en.block(walk.j) * kPagedBlock + warp * kPagedTile;
-                    if (ok && en.sees(key0, key0 + kPagedTile)) {
-                        if (pending) issue();
-                        ok = __all_sync(0xffffffffu,
-                                        mbar_wait_bounded(&sh.full[warp][ring.s], ring.phase,
-                                                          uint64_t(a.wait_us) * 1000u));
-                        if (ok) {
-                            --flying;
-                            slot = ring.s;
-                            ring.next(K);
-                            pending = used = true;
-                            uint8_t* tile = ring_at + slot * L::kTile;
-                            const bool edge = key0 + kPagedTile > hi_all ||
-                                              (key0 < lo_all && key0 + kPagedTile > a.sinks);
-                            if (edge) {
-                                // A masked probability is zero, but zero times what no row sees (or
-                                // was not even copied) may be NaN.
-                                for (int i = lane; i < kPagedTile * 8 * halves; i += 32) {
-                                    const int k = (i >> 3) & (kPagedTile - 1), h = i / (kPagedTile * 8);
-                                    if (!en.sees(key0 + k, key0 + k + 1))
-                                        st_shared_v4(tile + L::kV + h * L::kHalf + k * 128 + (i & 7) * 16,
-                                                     make_uint4(0, 0, 0, 0));
-                                }
-                                fence_proxy_async_shared();  // (before the copy into this slot)
-                                __syncwarp();
+                    for (int x = 0; x < 4; ++x) o[t][i][x] = 0.0f;
+            }
+            bool used = false;  // this warp has seen keys of the sequence
+            int stage = -1;     // of the sequence's last block here, held until its outputs are joined
+            do {
+                const int block0 = en.block(walk.j) * kPagedBlock, key0 = block0 + warp * kPagedTile;
+                if (ok && en.sees(block0, block0 + kPagedBlock)) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[ring.s], ring.phase, limit));
+                    if (!ok) continue;
+                    stage = ring.s;
+                    ring.next(K);
+                    uint8_t* keys = smem + L::kRing + stage * L::kBlock + warp * (kPagedTile * 128);
+                    if (en.sees(key0, key0 + kPagedTile)) {
+                        used = true;
+                        const bool edge = key0 + kPagedTile > hi_all ||
+                                          (key0 < lo_all && key0 + kPagedTile > a.sinks);
+                        if (edge) {
+                            // A masked probability is zero, but zero times what no row sees (or
+                            // was not even copied) may be NaN.
+                            for (int i = lane; i < kPagedTile * 8 * halves; i += 32) {
+                                const int k = (i >> 3) & (kPagedTile - 1), h = i / (kPagedTile * 8);
+                                if (!en.sees(key0 + k, key0 + k + 1))
+                                    st_shared_v4(keys + L::kV + h * L::kHalf + k * 128 + (i & 7) * 16,
+                                                 make_uint4(0, 0, 0, 0));
                             }
-                            // S^T
-                            float s[RT][4];
+                            fence_proxy_async_shared();  // (before the next copy into this stage)
+                            __syncwarp();
+                        }
+                        // S^T, in two sums (a sum of eight products waits for each of them)
+                        float s[RT][4], s2[RT][4];
 #pragma unroll
-                            for (int t = 0; t < RT; ++t)
+                        for (int t = 0; t < RT; ++t)
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) s[t][x] = 0.0f;
-                            const uint32_t tile_at = smem_u32(tile);
-                            {
-                                const int k = ((lane >> 3) & 1) * 8 + (lane & 7), w = lane >> 4;
+                            for (int x = 0; x < 4; ++x) s[t][x] = s2[t][x] = 0.0f;
+                        const uint32_t keys_at = smem_u32(keys);
+                        {
+                            const int k = ((lane >> 3) & 1) * 8 + (lane & 7), w = lane >> 4;
 #pragma unroll
-                                for (int ks = 0; ks < kD; ++ks) {
-                                    if (ks >= nk) break;
-                                    uint32_t x[4];
-                                    pg_ldmatrix<false>(x, tile_at + (ks >> 2) * L::kHalf + k * 128 +
-                                                              ((((ks & 3) * 2 + w) ^ (k & 7)) << 4));
+                            for (int ks = 0; ks < kD; ++ks) {
+                                if (ks >= nk) break;
+                                uint32_t x[4];
+                                pg_ldmatrix<false>(x, keys_at + (ks >> 2) * L::kHalf + k * 128 +
+                                                          ((((ks & 3) * 2 + w) ^ (k & 7)) << 4));
+                                if constexpr (kQShared) {
+                                    const int qr = ((lane >> 4) & 1) * 8 + (lane & 7);
+                                    const uint32_t q_at =
+                                        smem_u32(smem + L::kQ) + (ks >> 2) * kRows * 128 + qr * 128 +
+                                        ((((ks & 3) * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+#pragma unroll
+                                    for (int t = 0; t < RT; t += 2) {
+                                        uint32_t y[4];
+                                        pg_ldmatrix<false>(y, q_at + t * 8 * 128);
+                                        pg_mma<F16>(s[t], x, y[0], y[1]);
+                                        pg_mma<F16>(s[t + 1], x, y[2], y[3]);
+                                    }
+                                } else {
 #pragma unroll
                                     for (int t = 0; t < RT; ++t)
-                                        pg_mma<F16>(s[t], x, q[t][ks][0], q[t][ks][1]);
+                                        pg_mma<F16>((ks & 1) ? s2[t] : s[t], x, q[t][ks][0], q[t][ks][1]);
                                 }
                             }
-                            if (edge) {
-#pragma unroll
-                                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                                    for (int i = 0; i < 2; ++i) {
-                                        const int64_t row = row0 + t * 8 + pair + i;
-                                        const int64_t p = en.pos0 + div_fast(row, a.group);
-                                        const int64_t hi = min(int64_t(en.len), p + 1), lo = p + 1 - a.window;
-#pragma unroll
-                                        for (int x = 0; x < 2; ++x) {
-                                            const int key = key0 + quad + 8 * x;
-                                            if (key >= hi || (key < lo && key >= a.sinks))
-                                                s[t][2 * x + i] = -INFINITY;
-                                        }
-                                    }
-                            }
-                            bool grow = false;
+                        }
+                        if constexpr (!kQShared) {
 #pragma unroll
                             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                                for (int i = 0; i < 2; ++i)
-                                    grow |= (fmaxf(s[t][i], s[t][2 + i]) - m[t][i]) * sl2 > kPgRescale;
-                            if (__any_sync(0xffffffffu, grow)) {
+                                for (int x = 0; x < 4; ++x) s[t][x] += s2[t][x];
+                        }
+                        if (edge) {
 #pragma unroll
-                                for (int t = 0; t < RT; ++t) {
-                                    float f[2];
-#pragma unroll
-                                    for (int i = 0; i < 2; ++i) {
-                                        float top = fmaxf(s[t][i], s[t][2 + i]);
-#pragma unroll
-                                        for (int x = 4; x < 32; x <<= 1)
-                                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                                        const bool up = (top - m[t][i]) * sl2 > kPgRescale;
-                                        f[i] = up ? ex2((m[t][i] - top) * sl2) : 1.0f;
-                                        if (up) m[t][i] = top;
-                                        l[t][i] *= f[i];
-                                    }
-#pragma unroll
-                                    for (int i = 0; i < kD; ++i) {
-                                        o[t][i][0] *= f[0], o[t][i][2] *= f[0];
-                                        o[t][i][1] *= f[1], o[t][i][3] *= f[1];
-                                    }
-                                }
-                            }
-                            uint32_t p[RT][2];
-#pragma unroll
-                            for (int t = 0; t < RT; ++t) {
-                                float e[4];
+                            for (int t = 0; t < RT; ++t)
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
-                                    const float base = (m[t][i] == -INFINITY ? 0.0f : -m[t][i] * sl2) + kUp;
-                                    e[i] = ex2(fmaf(s[t][i], sl2, base));
-                                    e[2 + i] = ex2(fmaf(s[t][2 + i], sl2, base));
-                                    l[t][i] += e[i] + e[2 + i];
+                                    const int64_t row = row0 + t * 8 + pair + i;
+                                    const int64_t p = en.pos0 + div_fast(row, a.group);
+                                    const int64_t hi = min(int64_t(en.len), p + 1), lo = p + 1 - a.window;
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x) {
+                                        const int key = key0 + quad + 8 * x;
+                                        if (key >= hi || (key < lo && key >= a.sinks))
+                                            s[t][2 * x + i] = -INFINITY;
+                                    }
                                 }
-                                p[t][0] = pg_transpose(E::pack(e[0], e[1]));
-                                p[t][1] = pg_transpose(E::pack(e[2], e[3]));
-                            }
-                            // O^T
-                            {
-                                const int k = (lane >> 4) * 8 + (lane & 7), w = (lane >> 3) & 1;
-                                const uint32_t v_at = tile_at + L::kV + k * 128;
+                        }
+                        bool grow = false;
+#pragma unroll
+                        for (int t = 0; t < RT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                grow |= (fmaxf(s[t][i], s[t][2 + i]) - m[t][i]) * sl2 > kPgRescale;
+                        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                            for (int t = 0; t < RT; ++t) {
+                                float f[2];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    float top = fmaxf(s[t][i], s[t][2 + i]);
+#pragma unroll
+                                    for (int x = 4; x < 32; x <<= 1)
+                                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                                    const bool up = (top - m[t][i]) * sl2 > kPgRescale;
+                                    f[i] = up ? ex2((m[t][i] - top) * sl2) : 1.0f;
+                                    if (up) m[t][i] = top;
+                                    l[t][i] *= f[i];
+                                }
 #pragma unroll
                                 for (int i = 0; i < kD; ++i) {
-                                    if (i >= nk) break;
-                                    uint32_t x[4];
-                                    pg_ldmatrix<true>(x, v_at + (i >> 2) * L::kHalf +
-                                                             ((((i & 3) * 2 + w) ^ (k & 7)) << 4));
-#pragma unroll
-                                    for (int t = 0; t < RT; ++t) pg_mma<F16>(o[t][i], x, p[t][0], p[t][1]);
+                                    o[t][i][0] *= f[0], o[t][i][2] *= f[0];
+                                    o[t][i][1] *= f[1], o[t][i][3] *= f[1];
                                 }
                             }
                         }
-                    }
-                    ++at;
-                    walk.step(a);
-                } while (walk.left > 0 && at < seg_end);
-
-                // Join the warps: a row's maximum, sum and output.
-                const bool whole = seg >= begin && seg_end <= stop;
-                const int64_t part = 2 * int64_t(c) + (seg >= begin ? 1 : 0);
-                if (seg >= begin && seg_end > stop)
-                    shared = {paged_owner(total, a.parts, seg_end - 1) - c + 1, en.bb, en.rg, head};
+                        uint32_t p[RT][2];
 #pragma unroll
-                for (int t = 0; t < RT; ++t)
+                        for (int t = 0; t < RT; ++t) {
+                            float e[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                            for (int i = 0; i < 2; ++i) {
+                                const float base = (m[t][i] == -INFINITY ? 0.0f : -m[t][i] * sl2) + kUp;
+                                e[i] = ex2(fmaf(s[t][i], sl2, base));
+                                e[2 + i] = ex2(fmaf(s[t][2 + i], sl2, base));
+                                l[t][i] += e[i] + e[2 + i];
+                            }
+                            p[t][0] = pg_transpose(E::pack(e[0], e[1]));
+                            p[t][1] = pg_transpose(E::pack(e[2], e[3]));
+                        }
+                        // O^T
+                        {
+                            const int k = (lane >> 4) * 8 + (lane & 7), w = (lane >> 3) & 1;
+                            const uint32_t v_at = keys_at + L::kV + k * 128;
 #pragma unroll
-                        for (int x = 4; x < 32; x <<= 1)
-                            l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], x);
-                        if (lane < 4) sh.ml[warp][t * 8 + pair + i] = make_float2(m[t][i], l[t][i]);
-                    }
-                if (lane == 0) sh.slot[warp] = used ? slot : -1;
-                float* own = reinterpret_cast<float*>(ring_at + slot * L::kTile);
+                            for (int i = 0; i < kD; ++i) {
+                                if (i >= nk) break;
+                                uint32_t x[4];
+                                pg_ldmatrix<true>(x, v_at + (i >> 2) * L::kHalf +
+                                                         ((((i & 3) * 2 + w) ^ (k & 7)) << 4));
 #pragma unroll
-                for (int t0 = 0; t0 < RT; t0 += kRound) {
-                    if (t0 > 0) __syncthreads();
-                    __syncwarp();
-                    if (used) {
-#pragma unroll
-                        for (int t = 0; t < kRound; ++t)
-#pragma unroll
-                            for (int i = 0; i < kD; ++i)
-#pragma unroll
-                                for (int x = 0; x < 4; ++x)
-                                    own[(t * 8 + pair + (x & 1)) * DP +
-                                        ((i * 16 + (x >> 1) * 8 + quad) ^ (pair << 2))] = o[t0 + t][i][x];
-                    }
-                    __syncthreads();
-                    for (int it = threadIdx.x; it < kRound * 8 * (DP / 8); it += kPgThreads) {
-                        const int row = it / (DP / 8), col = it % (DP / 8) * 8;
-                        const int64_t to = row0 + t0 * 8 + row;
-                        if (col >= a.d) continue;
-                        float top = -INFINITY, sum = 0.0f, y[8];
-#pragma unroll
-                        for (int w = 0; w < kPagedWarps; ++w) top = fmaxf(top, sh.ml[w][t0 * 8 + row].x);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] = 0.0f;
-#pragma unroll
-                        for (int w = 0; w < kPagedWarps; ++w) {
-                            const float2 z = sh.ml[w][t0 * 8 + row];
-                            if (sh.slot[w] < 0 || z.x == -INFINITY) continue;
-                            const float f = ex2((z.x - top) * sl2);
-                            sum = fmaf(f, z.y, sum);
-                            const float* from = reinterpret_cast<const float*>(
-                                smem + L::kTiles + (w * K + sh.slot[w]) * L::kTile);
-#pragma unroll
-                            for (int k = 0; k < 8; k += 4) {
-                                const float4 v = *reinterpret_cast<const float4*>(
-                                    from + row * DP + ((col + k) ^ (((row >> 1) & 3) << 3)));
-                                y[k] = fmaf(f, v.x, y[k]);
-                                y[k + 1] = fmaf(f, v.y, y[k + 1]);
-                                y[k + 2] = fmaf(f, v.z, y[k + 2]);
-                                y[k + 3] = fmaf(f, v.w, y[k + 3]);
+                                for (int t = 0; t < RT; ++t) pg_mma<F16>(o[t][i], x, p[t][0], p[t][1]);
                             }
                         }
-                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // NaN stays NaN
-                        const float lse = sum == 0.0f ? -INFINITY
-                                                      : top * a.scale + (logf(sum) - kUp * 0.69314718056f);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] *= inv;
-                        if (!whole) {
-                            const int64_t at_row = part * kRows + t0 * 8 + row;
-                            float4* dst = reinterpret_cast<float4*>(a.part_o + at_row * a.d + col);
-                            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-                            if (col == 0) a.part_lse[at_row] = lse;
-                        } else if (to < row_end) {
-                            const int64_t tok = div_fast(to, a.group);
-                            const int64_t h = kvh * a.group + (to - tok * a.group);
-                            st_v4(a.o[r] + (((int64_t(en.bb) * a.Sq + tok) * a.n[r] + h) * a.d + col) * 2,
-                                  make_uint4(E::pack(y[0], y[1]), E::pack(y[2], y[3]),
-                                             E::pack(y[4], y[5]), E::pack(y[6], y[7])));
-                            if (col == 0) a.lse[r][(int64_t(en.bb) * a.n[r] + h) * a.Sq + tok] = lse;
-                        }
+                    }
+                    const int next = walk.left > 1 && walk.j + 1 < en.n
+                                         ? en.block(walk.j + 1) * kPagedBlock : en.end;
+                    if (en.sees(next, next + kPagedBlock)) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+                        stage = -1;
                     }
                 }
-                fence_proxy_async_shared();  // (a copy comes into this slot next)
-                __syncthreads();
-                if (pending) issue();
-                pending = false;
+            } while (walk.step(a), ++at, walk.left > 0 && at < seg_end);
+
+            // Join the warps: a row's maximum, sum and output.
+            const bool whole = seg >= begin && seg_end <= stop;
+            const int64_t part = 2 * int64_t(c) + (seg >= begin ? 1 : 0);
+            if (seg >= begin && seg_end > stop)
+                shared = {paged_owner(total, a.parts, seg_end - 1) - c + 1, en.bb, en.rg, head};
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1)
+                        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], x);
+                    if (lane < 4) sh.ml[warp][t * 8 + pair + i] = make_float2(m[t][i], l[t][i]);
+                }
+            used = used && stage >= 0;  // (it has given up otherwise)
+            if (lane == 0) sh.used[warp] = used;
+            // Row `row` of warp w's outputs lies where its keys and values of the last block were.
+            auto out_at = [&](int w, int row, int col) {
+                return reinterpret_cast<float*>(smem + L::kRing + stage * L::kBlock +
+                                                (row / kPartRows) * L::kHalf + w * (kPagedTile * 128)) +
+                       (row % kPartRows) * DP + (col ^ (((row >> 1) & 3) << 3));
+            };
+#pragma unroll
+            for (int t0 = 0; t0 < RT; t0 += kRound) {
+                if (t0 > 0) pg_sync();
+                __syncwarp();
+                if (used) {
+#pragma unroll
+                    for (int t = 0; t < kRound; ++t)
+#pragma unroll
+                        for (int i = 0; i < kD; ++i)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                *out_at(warp, t * 8 + pair + (x & 1), i * 16 + (x >> 1) * 8 + quad) =
+                                    o[t0 + t][i][x];
+                }
+                pg_sync();
+                for (int it = threadIdx.x; it < kRound * 8 * (DP / 8); it += 32 * kPagedWarps) {
+                    const int row = it / (DP / 8), col = it % (DP / 8) * 8;
+                    const int64_t to = row0 + t0 * 8 + row;
+                    if (col >= a.d) continue;
+                    float top = -INFINITY, sum = 0.0f, y[8];
+#pragma unroll
+                    for (int w = 0; w < kPagedWarps; ++w) top = fmaxf(top, sh.ml[w][t0 * 8 + row].x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kPagedWarps; ++w) {
+                        const float2 z = sh.ml[w][t0 * 8 + row];
+                        if (!sh.used[w] || stage < 0 || z.x == -INFINITY) continue;
+                        const float f = ex2((z.x - top) * sl2);
+                        sum = fmaf(f, z.y, sum);
+#pragma unroll
+                        for (int k = 0; k < 8; k += 4) {
+                            const float4 v = *reinterpret_cast<const float4*>(out_at(w, row, col + k));
+                            y[k] = fmaf(f, v.x, y[k]);
+                            y[k + 1] = fmaf(f, v.y, y[k + 1]);
+                            y[k + 2] = fmaf(f, v.z, y[k + 2]);
+                            y[k + 3] = fmaf(f, v.w, y[k + 3]);
+                        }
+                    }
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // NaN stays NaN
+                    const float lse = sum == 0.0f ? -INFINITY
+                                                  : top * a.scale + (logf(sum) - kUp * 0.69314718056f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] *= inv;
+                    if (!whole) {
+                        const int64_t at_row = part * kRows + t0 * 8 + row;
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + at_row * a.d + col);
+                        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                        if (col == 0) a.part_lse[at_row] = lse;
+                    } else if (to < row_end) {
+                        const int64_t tok = div_fast(to, a.group);
+                        const int64_t h = kvh * a.group + (to - tok * a.group);
+                        st_v4(a.o[r] + (((int64_t(en.bb) * a.Sq + tok) * a.n[r] + h) * a.d + col) * 2,
+                              make_uint4(E::pack(y[0], y[1]), E::pack(y[2], y[3]), E::pack(y[4], y[5]),
+                                         E::pack(y[6], y[7])));
+                        if (col == 0) a.lse[r][(int64_t(en.bb) * a.n[r] + h) * a.Sq + tok] = lse;
+                    }
+                }
             }
+            fence_proxy_async_shared();  // (a copy comes into this stage next)
+            pg_sync();
+            if (stage >= 0 && lane == 0) mbar_arrive(&sh.empty[stage]);
         }
         if (threadIdx.x == 0) a.shared[c] = shared;
     }
-    if (!ok && lane == 0) {
-        atomicOr(&g_attn_paged_status, kStatusWaitTimeout);
-        // leave no copy into this CTA's shared memory in flight
-        for (; flying > 0; --flying) {
-            if (!mbar_wait_bounded(&sh.full[warp][ring.s], ring.phase))
-                atomicOr(&g_attn_paged_status, kStatusDrainTimeout);
-            ring.next(K);
-        }
-    }
+    if (!ok && lane == 0) atomicOr(&g_attn_paged_status, kStatusWaitTimeout);
     let_next_start();
 }
 
@@ -667,7 +741,7 @@ static cudaError_t pg_launch(const PagedArgs& a, cudaStream_t stream, int device
 {
     static std::atomic<unsigned long long> raised{0};
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
-    constexpr int smem = PgSmem<DP>::kTotal + 1024;
+    constexpr int smem = PgSmem<DP, RT>::kTotal + 1024;
     if (bit && !(raised.load() & bit)) {
         cudaError_t e = cudaFuncSetAttribute(attn_paged_kernel<DP, F16, RT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
