@@ -202,7 +202,10 @@ def _ptrs(xs: Sequence) -> ctypes.Array:
     array = _PTR_ARRAYS.get(n)
     if array is None:
         array = _PTR_ARRAYS[n] = ctypes.c_void_p * n
-    return array(*[_addr(x) for x in xs])
+    try:
+        return array(*[x.data_ptr() for x in xs])
+    except AttributeError:  # addresses, or None, among them
+        return array(*[_addr(x) for x in xs])
 
 
 def _stream(stream) -> int:

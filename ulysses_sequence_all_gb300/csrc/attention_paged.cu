@@ -42,12 +42,15 @@ namespace uly {
 static __device__ unsigned g_attn_paged_status;
 
 constexpr int kPgThreads = 2 * 32 * kPagedWarps;  // warps 0-3, and a warpgroup with the copying one
-// Registers a thread: 256 x 128 at launch = 128 x 176 + 128 x 80, or 128 x 208 + 128 x 48 with 32 rows
-template <int RT>
-constexpr int kPgRegsProducts = RT == 4 ? 208 : 176;
+// Registers a thread: 256 x 128 at launch = 128 x this + 128 x (256 - this), what the roles take
+template <int DP, int RT>
+constexpr int kPgRegsProducts = RT == 1 ? 176 : DP == 64 ? (RT == 2 ? 176 : 200) : RT == 2 ? 192 : 216;
 constexpr float kPgRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 constexpr float kPgUpF16 = 7.0f;    // fp16 probabilities are held times 2^this
-constexpr int kPgJoinThreads = 256;
+constexpr int kPgJoinThreads = 256, kPgJoinParts = 8;
+// What a sequence's end (its join, the next one's queries) costs a CTA, in blocks of keys. 0, 1, 2, 3: one
+// token on 256 sequences of 100-2,000 keys 191, 173, 172, 174 us; of 100-200 keys 58, 56, 54, 54 us.
+constexpr int kPgEnd = 2;
 
 // ---- what there is to do ----------------------------------------------------------------------------
 
@@ -89,30 +92,36 @@ __device__ __forceinline__ PagedEntry paged_entry(const PagedArgs& a, int e)
 // The way through a share's blocks: entry by entry, in an entry head by head (the heads of a token lie
 // next to one another), in a head block by block.
 struct PagedWalk {
-    int64_t left;
+    int64_t left;  // of the share, from the sequence's beginning (its end included) on
     int e, head, j;
     PagedEntry en;
+    __device__ __forceinline__ bool more() const { return left > j + kPgEnd; }
+    // blocks of the sequence that are the share's: j .. stop() - 1
+    __device__ __forceinline__ int stop() const { return int(min(int64_t(en.n), left - kPgEnd)); }
     __device__ __forceinline__ void step(const PagedArgs& a)
     {
-        --left;
         if (++j < en.n) return;
         j = 0;
+        left -= en.n + kPgEnd;
         if (++head < a.m_begin[a.W]) return;
         head = 0;
-        if (left > 0) en = paged_entry(a, ++e);
+        if (more()) en = paged_entry(a, ++e);
     }
 };
 
-__device__ __forceinline__ int64_t paged_share(int64_t total, int parts, int64_t c)  // its first block
+// The work is measured in blocks, a sequence (of one row group and head) of n as kPgEnd + n, its end first:
+// equal shares of that are equal times, however short the sequences are. A share that begins inside an end
+// begins with the sequence.
+__device__ __forceinline__ int64_t paged_share(int64_t total, int parts, int64_t c)  // where it begins
 {
     const int64_t q = total / parts, rem = total - q * parts;
     return c * q + min(c, rem);
 }
 
-__device__ __forceinline__ int paged_owner(int64_t total, int parts, int64_t block)
+__device__ __forceinline__ int paged_owner(int64_t total, int parts, int64_t at)
 {
     const int64_t q = total / parts, rem = total - q * parts, big = rem * (q + 1);
-    return int(block < big ? block / (q + 1) : rem + (block - big) / q);
+    return int(at < big ? at / (q + 1) : rem + (at - big) / q);
 }
 
 // ---- the kernel -------------------------------------------------------------------------------------
@@ -217,7 +226,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     const int each = (entries + kPgThreads - 1) / kPgThreads;
     const int e0 = min(entries, int(threadIdx.x) * each), e1 = min(entries, e0 + each);
     int64_t mine = 0;
-    for (int e = e0; e < e1; ++e) mine += paged_entry(a, e).n;
+    for (int e = e0; e < e1; ++e) mine += paged_entry(a, e).n + kPgEnd;
     int64_t upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -248,23 +257,27 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         if (begin >= (upto - mine) * heads && begin < upto * heads) {
             int64_t at = upto - mine;
             int e = e0;
-            for (int n; begin >= (at + (n = paged_entry(a, e).n)) * heads; ++e) at += n;
+            for (int n; begin >= (at + (n = paged_entry(a, e).n + kPgEnd)) * heads; ++e) at += n;
             sh.entry = e;
             sh.before = at;
         }
         __syncthreads();
-        walk.left = stop - begin;
-        if (walk.left > 0) {
+        walk.left = walk.j = 0;
+        if (begin < stop) {
             walk.e = sh.entry;
             walk.en = paged_entry(a, walk.e);
             const int64_t off = begin - sh.before * heads;
-            walk.head = int(div_fast(off, walk.en.n));
-            walk.j = int(off - int64_t(walk.head) * walk.en.n);
+            walk.head = int(div_fast(off, walk.en.n + kPgEnd));
+            const int x = int(off - int64_t(walk.head) * (walk.en.n + kPgEnd));
+            walk.j = max(0, x - kPgEnd);
+            walk.left = stop - begin + x;
         }
     };
 
     if (warp >= kPagedWarps) {  // the copies
-        regs_shrink<256 - kPgRegsProducts<RT>>();
+        regs_shrink<256 - kPgRegsProducts<DP, RT>>();
+        if (warp > kPagedWarps && lane < a.W && a.n[lane] > 0)  // (the first copies else wait for them)
+            prefetch_map(warp & 1 ? &a.kmap[lane] : &a.vmap[lane]);
         for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
             share(c);
             if (warp > kPagedWarps) continue;
@@ -274,7 +287,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             bool live = false;             // a block is in hand
             auto look = [&]() {            // the walk's next block that any row sees anything of
                 live = false;
-                while (walk.left > 0) {
+                while (walk.more()) {
                     const int key0 = walk.en.block(walk.j) * kPagedBlock;
                     live = walk.en.sees(key0, key0 + kPagedBlock);
                     if (live) {
@@ -336,27 +349,29 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     }
 
     // the products
-    regs_grow<kPgRegsProducts<RT>>();
+    regs_grow<kPgRegsProducts<DP, RT>>();
     const int nk = (a.d + 15) / 16;
     const float sl2 = a.scale * 1.4426950408889634f;
     const int quad = lane >> 2, pair = (lane & 3) * 2;  // fragments: key (column of V); query row
     for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
         share(c);
-        PagedShared shared = {0, 0, 0, 0};
-        int64_t at = begin;  // the walk's block
-        while (walk.left > 0) {
-            const PagedEntry en = walk.en;
-            const int64_t seg = at - walk.j, seg_end = seg + en.n;  // its blocks
-            int r = 0;
-            while (r + 1 < a.W && walk.head >= a.m_begin[r + 1]) ++r;
-            const int head = walk.head, kvh = head - a.m_begin[r];
-            const int64_t row0 = int64_t(en.rg) * kRows, row_end = a.Sq * a.group;
+        PagedShared shared = {0, 0, 0, 0, 0};
+        uint32_t q[kQShared ? 1 : RT][kD][2];
+        // The walk's rank and key head; its queries to registers (32 rows: to shared memory).
+        auto place = [&](int* r, int* kvh) {
+            *r = 0;
+            while (*r + 1 < a.W && walk.head >= a.m_begin[*r + 1]) ++*r;
+            *kvh = walk.head - a.m_begin[*r];
+        };
+        auto queries = [&]() {
+            int r, kvh;
+            place(&r, &kvh);
+            const int64_t row0 = int64_t(walk.en.rg) * kRows, row_end = a.Sq * a.group;
             auto query = [&](int64_t row) {  // its first byte
                 const int64_t tok = div_fast(row, a.group);
-                return a.q[r] + ((int64_t(en.bb) * a.Sq + tok) * a.n[r] + kvh * a.group + row -
+                return a.q[r] + ((int64_t(walk.en.bb) * a.Sq + tok) * a.n[r] + kvh * a.group + row -
                                  tok * a.group) * a.d * 2;
             };
-            uint32_t q[kQShared ? 1 : RT][kD][2];
             if constexpr (kQShared) {
                 for (int i = threadIdx.x; i < kRows * (DP / 8); i += 32 * kPagedWarps) {
                     const int row = i / (DP / 8), w = i % (DP / 8);
@@ -384,6 +399,16 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                         }
                 }
             }
+        };
+        if (walk.more()) queries();
+        while (walk.more()) {
+            const PagedEntry en = walk.en;
+            int r, kvh;
+            place(&r, &kvh);
+            const int head = walk.head, from = walk.j, to_block = walk.stop();
+            const int64_t place = int64_t(walk.e) * heads + head;
+            const int64_t at_end = stop - walk.left + kPgEnd + en.n;  // where the sequence ends in the work
+            const int64_t row0 = int64_t(en.rg) * kRows, row_end = a.Sq * a.group;
             // keys that every row sees: below hi_all, and from lo_all on or first tokens
             const int hi_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t0 + 1)));
             const int lo_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t1 - a.window)));
@@ -399,8 +424,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             }
             bool used = false;  // this warp has seen keys of the sequence
             int stage = -1;     // of the sequence's last block here, held until its outputs are joined
-            do {
-                const int block0 = en.block(walk.j) * kPagedBlock, key0 = block0 + warp * kPagedTile;
+            for (int j = from; j < to_block; ++j) {
+                const int block0 = en.block(j) * kPagedBlock, key0 = block0 + warp * kPagedTile;
                 if (ok && en.sees(block0, block0 + kPagedBlock)) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[ring.s], ring.phase, limit));
                     if (!ok) continue;
@@ -536,21 +561,27 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                             }
                         }
                     }
-                    const int next = walk.left > 1 && walk.j + 1 < en.n
-                                         ? en.block(walk.j + 1) * kPagedBlock : en.end;
+                    const int next =
+                        j + 1 < to_block ? en.block(j + 1) * kPagedBlock : en.end;
                     if (en.sees(next, next + kPagedBlock)) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh.empty[stage]);
                         stage = -1;
                     }
                 }
-            } while (walk.step(a), ++at, walk.left > 0 && at < seg_end);
+            }
+            walk.j = to_block - 1;
+            walk.step(a);
+            if (!kQShared && walk.more()) queries();  // (they arrive during the join)
 
             // Join the warps: a row's maximum, sum and output.
-            const bool whole = seg >= begin && seg_end <= stop;
-            const int64_t part = 2 * int64_t(c) + (seg >= begin ? 1 : 0);
-            if (seg >= begin && seg_end > stop)
-                shared = {paged_owner(total, a.parts, seg_end - 1) - c + 1, en.bb, en.rg, head};
+            const bool whole = from == 0 && to_block == en.n;
+            const int64_t part = 2 * int64_t(c) + (from == 0 ? 1 : 0);
+            if (from == 0) {
+                shared = {0, 0, 0, 0, 0};
+                if (!whole) shared = {paged_owner(total, a.parts, at_end - 1) - c + 1, c, en.bb, en.rg, head};
+                if (a.by_group && threadIdx.x == 0) a.shared[place] = shared;
+            }
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -628,20 +659,21 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                     }
                 }
             }
+            if (kQShared && walk.more()) queries();  // (its barrier is the next one as well)
             fence_proxy_async_shared();  // (a copy comes into this stage next)
             pg_sync();
             if (stage >= 0 && lane == 0) mbar_arrive(&sh.empty[stage]);
         }
-        if (threadIdx.x == 0) a.shared[c] = shared;
+        if (!a.by_group && threadIdx.x == 0) a.shared[c] = shared;
     }
     if (!ok && lane == 0) atomicOr(&g_attn_paged_status, kStatusWaitTimeout);
     let_next_start();
 }
 
-// Joins what several CTAs made of a row group: block x looks at CTA x's note. `y_rows` of its warps take
+// Joins what several CTAs made of a row group: block x looks at note x. `y_rows` of its warps take
 // a row each, the others of a row every (warps / y_rows)-th part; a lane has 4 columns.
 template <bool F16>
-__global__ void __launch_bounds__(kPgJoinThreads)
+__global__ void __launch_bounds__(kPgJoinThreads, 2)
     attn_paged_join_kernel(const __grid_constant__ PagedArgs a, int y_rows)
 {
     using E = ElemT<F16>;
@@ -651,22 +683,22 @@ __global__ void __launch_bounds__(kPgJoinThreads)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ways = kWarps / y_rows, way = warp % ways;
     wait_for_previous();
-    for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
-        const PagedShared s = a.shared[c];
+    for (int note = blockIdx.x; note < a.notes; note += gridDim.x) {
+        const PagedShared s = a.shared[note];
         if (s.parts == 0) continue;
         for (int row0 = blockIdx.y * y_rows; row0 < a.rows; row0 += gridDim.y * y_rows) {
             const int row = row0 + warp / ways;
             float top = -INFINITY, sum = 0.0f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             auto slot = [&](int p) {
-                return (p == 0 ? 2 * int64_t(c) + 1 : 2 * int64_t(c + p)) * a.rows + row;
+                return (p == 0 ? 2 * int64_t(s.cta) + 1 : 2 * int64_t(s.cta + p)) * a.rows + row;
             };
-            for (int p = way; p < s.parts; p += ways) top = fmaxf(top, a.part_lse[slot(p)]);
-            for (int p0 = way; p0 < s.parts; p0 += 4 * ways) {
-                float4 o[4];
-                float f[4];
+            // eight parts at a time, all on their way at once, relative to the largest lse so far
+            for (int p0 = way; p0 < s.parts; p0 += kPgJoinParts * ways) {
+                float4 o[kPgJoinParts];
+                float f[kPgJoinParts];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kPgJoinParts; ++k) {
                     const int p = p0 + k * ways;
                     f[k] = -INFINITY;
                     o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -675,8 +707,15 @@ __global__ void __launch_bounds__(kPgJoinThreads)
                     if (lane * 4 < a.d)
                         o[k] = *reinterpret_cast<const float4*>(a.part_o + slot(p) * a.d + lane * 4);
                 }
+                float most = top;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kPgJoinParts; ++k) most = fmaxf(most, f[k]);
+                const float keep = top == -INFINITY ? 0.0f : expf(top - most);
+                top = most;
+                sum *= keep;
+                acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+                for (int k = 0; k < kPgJoinParts; ++k) {
                     const float w = f[k] == -INFINITY ? 0.0f : expf(f[k] - top);  // (NaN stays NaN)
                     sum += w;
                     acc.x = fmaf(w, o[k].x, acc.x);
@@ -733,6 +772,9 @@ void attn_paged_split(PagedArgs* a, int sm_count)
     a->rows = rows <= 8 ? 8 : rows <= 16 ? 16 : kPagedMaxRows;
     a->row_groups = int32_t((rows + a->rows - 1) / a->rows);
     a->parts = 2 * sm_count;
+    const int64_t groups = int64_t(a->b) * a->row_groups * a->m_begin[a->W];
+    a->by_group = groups <= a->parts;
+    a->notes = int32_t(a->by_group ? groups : a->parts);
 }
 
 template <int DP, bool F16, int RT>
@@ -753,12 +795,11 @@ static cudaError_t pg_launch(const PagedArgs& a, cudaStream_t stream, int device
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // Few sequences are shared by many CTAs each: then a block has one row, its warps the parts.
-    const int64_t groups = int64_t(a.b) * a.row_groups * a.m_begin[a.W];
-    const int y_rows = groups * 8 <= a.parts ? 1 : kPgJoinThreads / 32;
-    unsigned y = unsigned(a.rows / y_rows);
-    if (int64_t(grid) * y > cap) y = 1;
+    const int y_rows = a.notes * 8 <= a.parts ? 1 : kPgJoinThreads / 32;
+    unsigned x = unsigned(a.notes < cap ? a.notes : cap), y = unsigned(a.rows / y_rows);
+    if (int64_t(x) * y > cap) y = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, y);
+    cfg.gridDim = dim3(x, y);
     cfg.blockDim = dim3(kPgJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};

@@ -30,11 +30,11 @@ struct AppendArgs {
     int32_t W;
 };
 
-// A batch element's row group (`rows` query rows) that several CTAs share: CTA `first` holds its
-// beginning, the next parts - 1 the rest.
+// A batch element's row group (`rows` query rows) of a key head that several shares of the work have
+// parts of: share `cta` its beginning, the next parts - 1 the rest.
 struct PagedShared {
     int32_t parts;  // 0: none
-    int32_t bb, group, head;
+    int32_t cta, bb, group, head;
 };
 
 struct PagedArgs {
@@ -54,11 +54,12 @@ struct PagedArgs {
     int64_t window;          // beyond every position where there is none
     int32_t rows, row_groups;  // query rows of a pass (8, 16, 32); passes of a key head
     int32_t parts;             // shares of all the work, one CTA at a time works on one
+    int32_t by_group, notes;   // `shared` has an entry for each row group and head, or for each share
     float scale;
     uint32_t wait_us;
     float* part_o;         // [2 parts][rows][d] normalised partial outputs
     float* part_lse;       // [2 parts][rows]
-    PagedShared* shared;   // [parts]
+    PagedShared* shared;   // [notes], at most parts
 };
 
 cudaError_t cache_append_launch(const AppendArgs& a, cudaStream_t stream, int64_t cap, int sm_count);

@@ -160,6 +160,12 @@ __device__ __forceinline__ void tensor_g2s_3d(void* dst_smem, const void* map, i
         : "memory");
 }
 
+// Fetches a tensor map ahead of the first copy that uses it.
+__device__ __forceinline__ void prefetch_map(const void* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // The same for a 4-D map: coordinates (c0, c1, c2, c3), c0 the innermost.
 __device__ __forceinline__ void tensor_g2s_4d(void* dst_smem, const void* map, int c0, int c1,
                                               int c2, int c3, uint64_t* bar)
