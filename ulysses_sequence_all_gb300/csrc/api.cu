@@ -917,6 +917,8 @@ int attn_window(AttnShape* s, int64_t window, int64_t sinks)
     s->causal = 1;
     s->window = window < kAttnFar ? window : kAttnFar;
     s->sinks = int32_t(sinks < s->Skv ? sinks : s->Skv);
+    const int32_t unit = s->sinks <= kAttnSharedSinks ? 8 : kAttnRows;
+    s->sink_rows = (s->sinks + unit - 1) / unit * unit;
     return ULY_OK;
 }
 

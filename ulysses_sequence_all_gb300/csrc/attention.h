@@ -41,8 +41,12 @@ struct AttnShape {
     float scale;
     // Causal with a window (0: none): the query at position p sees j <= p with j > p - window or j < sinks.
     int32_t sinks;
+    int32_t sink_rows;  // rows that they take in a unit's blocks: see AttnBlocks
     int64_t window;
 };
+// Up to here first tokens share a block with keys of the window (a copy of 8 k rows in front of theirs);
+// more of them have blocks of their own.
+constexpr int kAttnSharedSinks = 64;
 
 #ifdef __CUDACC__
 // Keys of batch element bb that any row sees, and the position of its first query (beyond every key
@@ -58,37 +62,60 @@ __device__ __forceinline__ void attn_limits(const AttnShape& s, int bb, int64_t*
 }
 #endif
 
-// The key blocks that a unit walks: 0, 1, ...; with a window 0 .. first - 1, which hold the first tokens
-// that it sees besides, and then those from first + gap on.
+// The key blocks that a unit walks are rows 128 j .. 128 j + 127 of its list of keys: 0, 1, ...; with a
+// window the first tokens (rows below `pad`, of which those from `sinks` on are masked), then the keys
+// from `begin` on, the first in the window of the unit's first row. So that a list has no row before its
+// window, blocks begin at any key.
 #ifdef __CUDACC__
 template <bool WIN>
 struct AttnBlocks {
-    __device__ __forceinline__ int block(int j) const { return j; }
 };
 template <>
 struct AttnBlocks<true> {
-    int first, gap;
-    __device__ __forceinline__ int block(int j) const { return j < first ? j : j + gap; }
-    // `lo`: the first key in the window of the unit's first row
-    __device__ __forceinline__ void set(const AttnShape& s, int64_t lo)
+    int pad, begin;
+    __device__ __forceinline__ void set(const AttnShape& s, int64_t first)
     {
-        const int near = int(lo / kAttnRows);
-        first = min(int((min(int64_t(s.sinks), lo) + kAttnRows - 1) / kAttnRows), near);
-        gap = near - first;
+        const bool apart = first > s.sink_rows;
+        pad = apart ? s.sink_rows : 0;
+        begin = apart ? int(first) : 0;
     }
-    // of blocks 0 .. n - 1, those of the list
-    __device__ __forceinline__ int count(int n) const { return min(n, first) + max(0, n - (first + gap)); }
+    // Rows that hold the keys below `end` that anyone may see.
+    __device__ __forceinline__ int rows(const AttnShape& s, int64_t end) const
+    {
+        return end > begin ? int(end - begin) + pad : pad ? int(max(int64_t(0), min(int64_t(s.sinks), end))) : 0;
+    }
+    __device__ __forceinline__ int key(int row) const { return row < pad ? row : row - pad + begin; }
+    // The rows of block j that hold what no row of the batch element sees between the first tokens and its
+    // first window, or first tokens that are none: x .. y - 1 (none where y <= x).
+    __device__ __forceinline__ int2 between(const AttnShape& s, int64_t pos0, int j) const
+    {
+        const int64_t to = pad ? pad : begin ? 0 : pos0 + 1 - s.window, row0 = int64_t(j) * kAttnRows;
+        return make_int2(int(max(int64_t(0), min(int64_t(kAttnRows), s.sinks - row0))),
+                         int(max(int64_t(0), min(int64_t(kAttnRows), to - row0))));
+    }
 };
 
-// With a window, the rows of a key block between the first tokens and the window of the batch element's
-// first row, which no row sees: x .. y - 1 (none where y <= x).
-template <bool WIN>
-__device__ __forceinline__ int2 attn_between(const AttnShape& s, int64_t pos0, int64_t block)
+// Copies key block j (of a list, with a window) of a head: the `halves` tiles of 64 columns, kHalf apart.
+template <bool WIN, int HALF>
+__device__ __forceinline__ void attn_load_keys(uint8_t* to, int halves, const CUtensorMap* map,
+                                               const CUtensorMap* sink_map, const CUtensorMap* rest_map,
+                                               const AttnBlocks<WIN>& list, int head, int j, int bb,
+                                               uint64_t* bar)
 {
-    if constexpr (!WIN) return make_int2(0, 0);
-    const int64_t key0 = block * kAttnRows, lo = pos0 + 1 - s.window;
-    return make_int2(int(max(int64_t(0), min(int64_t(kAttnRows), s.sinks - key0))),
-                     int(max(int64_t(0), min(int64_t(kAttnRows), lo - key0))));
+    if constexpr (WIN) {
+        if (j == 0 && list.pad > 0 && list.pad < kAttnRows) {
+            for (int h = 0; h < halves; ++h) {
+                tensor_g2s_4d(to + h * HALF, sink_map, 64 * h, head, 0, bb, bar);
+                tensor_g2s_4d(to + h * HALF + list.pad * 128, rest_map, 64 * h, head, list.begin, bb, bar);
+            }
+            return;
+        }
+        for (int h = 0; h < halves; ++h)
+            tensor_g2s_4d(to + h * HALF, map, 64 * h, head, list.key(j * kAttnRows), bb, bar);
+    } else {
+        for (int h = 0; h < halves; ++h)
+            tensor_g2s_4d(to + h * HALF, map, 64 * h, head, j * kAttnRows, bb, bar);
+    }
 }
 #endif
 
@@ -155,6 +182,8 @@ struct AttnUnitSource {
 struct AttnFwdArgs {
     AttnShape s;
     CUtensorMap qmap[kMaxW], kmap[kMaxW], vmap[kMaxW];
+    CUtensorMap kmap_sink[kMaxW], vmap_sink[kMaxW];  // with a window: boxes of sink_rows, and of the rest
+    CUtensorMap kmap_rest[kMaxW], vmap_rest[kMaxW];  // of a block
     uint8_t* o[kMaxW];
     float* lse[kMaxW];  // (b, n_r, Sq)
     int32_t tile_tokens;
@@ -171,6 +200,8 @@ struct AttnBwdArgs {
     AttnShape s;
     CUtensorMap qmap[kMaxW], gmap[kMaxW];  // boxes of a row tile: q, dO
     CUtensorMap kmap[kMaxW], vmap[kMaxW];  // boxes of a key block
+    CUtensorMap kmap_sink[kMaxW], vmap_sink[kMaxW];  // dQ with a window: as the forward's
+    CUtensorMap kmap_rest[kMaxW], vmap_rest[kMaxW];
     const uint8_t* o[kMaxW];
     const uint8_t* go[kMaxW];
     const uint8_t* v[kMaxW];
@@ -229,6 +260,9 @@ inline cudaError_t attn_launch_early(void (*kernel)(Args), unsigned grid, unsign
 int64_t attn_order_group(int64_t heads, int64_t bytes);
 // Tiles, units and parts of the keys from the shape and the device alone: a CTA cap changes no bit.
 void attn_fwd_split(AttnFwdArgs* a, int sm_count);
+// Maps of a block that first tokens share with keys of the window (where there is one).
+bool encode_sink_maps(const AttnShape& s, int r, const void* k, const void* v, CUtensorMap* k_sink,
+                      CUtensorMap* v_sink, CUtensorMap* k_rest, CUtensorMap* v_rest);
 // The units of dK, dV with a window, from the shape and the device alone.
 void attn_bwd_split(AttnBwdArgs* a, int sm_count);
 // `cap`: CTAs of a launch at most; under one (below kAttnMostCtas) no kernel starts beside another.

@@ -519,22 +519,19 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             bool ok = true;
             AbUnits<Unit> source{&bars.board, life};
             Unit t;
+            // (K and V come after the unit's first q and dO: those do not wait for the last unit's end)
+            auto keys = [&](int w) {
+                if (blocks[w] > 0)
+                    ok = wait_or_dead(w ? &bars.v_empty : &bars.k_empty, (blocks[w] - 1) & 1, life);
+                if (!ok) return;
+                uint64_t* bar = w ? &bars.v_full : &bars.k_full;
+                mbar_arrive_expect_tx(bar, kv_bytes);
+                for (int h = 0; h < halves; ++h)
+                    tensor_g2s_4d(smem + (w ? L::kV : L::kK) + h * L::kHalf,
+                                  w ? &a.vmap[t.r] : &a.kmap[t.r], 64 * h, t.kvh, int(t.kv0), t.bb, bar);
+                ++blocks[w];
+            };
             while (ok && source.template next<false>(&t)) {
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (ok && blocks[w] > 0)
-                        ok = wait_or_dead(w ? &bars.v_empty : &bars.k_empty, (blocks[w] - 1) & 1,
-                                          life);
-                    if (!ok) break;
-                    uint64_t* bar = w ? &bars.v_full : &bars.k_full;
-                    mbar_arrive_expect_tx(bar, kv_bytes);
-                    for (int h = 0; h < halves; ++h)
-                        tensor_g2s_4d(smem + (w ? L::kV : L::kK) + h * L::kHalf,
-                                      w ? &a.vmap[t.r] : &a.kmap[t.r], 64 * h, t.kvh, int(t.kv0),
-                                      t.bb, bar);
-                    ++blocks[w];
-                }
-                if (!ok) break;
                 for (int i = 0; ok && i < t.n; ++i) {
                     const int64_t tile = t.first + i;
                     if (q_tiles >= K) ok = wait_or_dead(&bars.q_empty[ring.s], ring.phase ^ 1u, life);
@@ -549,7 +546,9 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                                       64 * h, t.kvh * s.group, int(tile * a.tile_tokens), t.bb,
                                       &bars.q_full[ring.s]);
                     ++q_tiles;
-                    if (g_tiles >= K) ok = wait_or_dead(&bars.g_empty[ring.s], ring.phase ^ 1u, life);
+                    if (i == 0) keys(0);
+                    if (ok && g_tiles >= K)
+                        ok = wait_or_dead(&bars.g_empty[ring.s], ring.phase ^ 1u, life);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&bars.g_full[ring.s], q_bytes);
                     for (int h = 0; h < halves; ++h)
@@ -557,6 +556,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                                       64 * h, t.kvh * s.group, int(tile * a.tile_tokens), t.bb,
                                       &bars.g_full[ring.s]);
                     life->loads = uint32_t(++g_tiles);
+                    if (i == 0) keys(1);
                     ring.next(K);
                 }
             }
@@ -883,7 +883,7 @@ struct BqSmem {
 
 template <bool WIN>
 struct BqUnit : AttnBlocks<WIN> {
-    int r, bb, kvh, n;  // n: key blocks that the tile sees, block(0 .. n - 1)
+    int r, bb, kvh, n;  // n: key blocks that the tile sees (with a window, of its list)
     float norm;         // fp16: the largest |v| in them
     int64_t h, tile, tok0, len, pos0;
 };
@@ -916,20 +916,24 @@ __device__ __forceinline__ BqUnit<WIN> bq_unit(const AttnBwdArgs& a, int64_t u)
     const int64_t last = min(t.tok0 + a.tile_tokens, s.Sq) - 1;
     const int64_t keys = max(int64_t(0), min(t.len, t.pos0 + last + 1));
     t.n = int((keys + kAttnRows - 1) / kAttnRows);
+    int near = 0;  // the first block (of all keys) that it sees keys of beside the first tokens
     if constexpr (WIN) {
         t.set(s, max(int64_t(0), min(keys, t.pos0 + t.tok0 + 1 - s.window)));
-        t.n = t.count(t.n);
+        near = t.begin / kAttnRows;
     }
     t.norm = 0.0f;
     if (F16) {
         const float* norms = a.key_norms + t.h * a.kv_order.blocks;
 #pragma unroll 4
-        for (int i = threadIdx.x & 31; i < t.n; i += 32)
-            t.norm = fmaxf(t.norm, norms[t.block(i)]);
+        for (int i = near + int(threadIdx.x & 31); i < t.n; i += 32) t.norm = fmaxf(t.norm, norms[i]);
+        if constexpr (WIN)
+            for (int i = threadIdx.x & 31; i * kAttnRows < min(t.pad, s.sinks); i += 32)
+                t.norm = fmaxf(t.norm, norms[i]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             t.norm = fmaxf(t.norm, __shfl_xor_sync(0xffffffffu, t.norm, off));
     }
+    if constexpr (WIN) t.n = (t.rows(s, keys) + kAttnRows - 1) / kAttnRows;
     return t;
 }
 
@@ -937,7 +941,8 @@ __device__ __forceinline__ BqUnit<WIN> bq_unit(const AttnBwdArgs& a, int64_t u)
 template <bool WIN>
 __device__ __forceinline__ int bq_past(const AttnShape& s, const BqUnit<WIN>& t, int block)
 {
-    const int64_t past = t.len - int64_t(block) * kAttnRows;
+    int64_t past = t.len - int64_t(block) * kAttnRows;
+    if constexpr (WIN) past += t.pad - t.begin;
     return past >= kAttnRows || t.len >= s.Skv ? kAttnRows : int(past);
 }
 
@@ -945,8 +950,11 @@ __device__ __forceinline__ int bq_past(const AttnShape& s, const BqUnit<WIN>& t,
 template <bool WIN>
 __device__ __forceinline__ bool bq_unclean(const AttnShape& s, const BqUnit<WIN>& t, int block)
 {
-    const int2 b = attn_between<WIN>(s, t.pos0, block);
-    return bq_past(s, t, block) < kAttnRows || b.y > b.x;
+    if constexpr (WIN) {
+        const int2 b = t.between(s, t.pos0, block);
+        if (b.y > b.x) return true;
+    }
+    return bq_past(s, t, block) < kAttnRows;
 }
 
 // Q goes to tensor memory (the S products then read half as much shared memory), S and dP are free
@@ -1011,21 +1019,31 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             const uint32_t q_bytes = uint32_t(halves) * a.tile_tokens * s.group * 128u;
             const uint32_t kv_bytes = uint32_t(halves) * L::kHalf;
             bool ok = true;
-            auto stage = [&](const CUtensorMap* map, uint32_t bytes, int head, int row, int bb) {
+            auto stage = [&](uint32_t bytes, auto copy) {
                 if (issued >= K) ok = wait_or_dead(&bars.empty[ring.s], ring.phase ^ 1u, life);
                 if (!ok) return;
                 mbar_arrive_expect_tx(&bars.full[ring.s], bytes);
-                for (int h = 0; h < halves; ++h)
-                    tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf, map, 64 * h,
-                                  head, row, bb, &bars.full[ring.s]);
+                copy(smem + L::kRing + ring.s * L::kTile, &bars.full[ring.s]);
                 life->loads = uint32_t(++issued);
                 ring.next(K);
+            };
+            auto keys = [&](const Unit& t, int j, bool value) {
+                stage(kv_bytes, [&](uint8_t* to, uint64_t* bar) {
+                    attn_load_keys<WIN, L::kHalf>(to, halves, value ? &a.vmap[t.r] : &a.kmap[t.r],
+                                                  value ? &a.vmap_sink[t.r] : &a.kmap_sink[t.r],
+                                                  value ? &a.vmap_rest[t.r] : &a.kmap_rest[t.r], t, t.kvh,
+                                                  j, t.bb, bar);
+                });
             };
             AbUnits<Unit> source{&bars.board, life};
             Unit t;
             while (ok && source.template next<false>(&t)) {
-                stage(&a.qmap[t.r], q_bytes, t.kvh * s.group, int(t.tok0), t.bb);
-                if (ok) stage(&a.kmap[t.r], kv_bytes, t.kvh, t.block(0) * kAttnRows, t.bb);
+                stage(q_bytes, [&](uint8_t* to, uint64_t* bar) {
+                    for (int h = 0; h < halves; ++h)
+                        tensor_g2s_4d(to + h * L::kHalf, &a.qmap[t.r], 64 * h, t.kvh * s.group, int(t.tok0),
+                                      t.bb, bar);
+                });
+                if (ok) keys(t, 0, false);
                 if (ok && uses > 0) ok = wait_or_dead(&bars.g_empty, (uses - 1) & 1, life);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&bars.g_full, q_bytes);
@@ -1033,9 +1051,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     tensor_g2s_4d(smem + L::kG + h * L::kHalf, &a.gmap[t.r], 64 * h,
                                   t.kvh * s.group, int(t.tok0), t.bb, &bars.g_full);
                 ++uses;
-                for (int j = 1; ok && j < 2 * t.n; ++j)
-                    stage((j & 1) ? &a.vmap[t.r] : &a.kmap[t.r], kv_bytes, t.kvh,
-                          t.block(j >> 1) * kAttnRows, t.bb);
+                for (int j = 1; ok && j < 2 * t.n; ++j) keys(t, j >> 1, j & 1);
             }
             bool drained = true;  // leave no copy into this CTA's shared memory in flight
             for (int64_t k = max(int64_t(0), issued - K); k < issued; ++k)
@@ -1058,8 +1074,8 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     int past = kAttnRows;
                     int2 between = make_int2(0, 0);
                     if (j >= 0 && !(j & 1)) {
-                        past = bq_past(s, t, t.block(j >> 1));
-                        between = attn_between<WIN>(s, t.pos0, t.block(j >> 1));
+                        past = bq_past(s, t, j >> 1);
+                        if constexpr (WIN) between = t.between(s, t.pos0, j >> 1);
                     }
                     if (past < kAttnRows || between.y > between.x) {
                         for (int h = 0; h < halves; ++h) {
@@ -1152,7 +1168,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                     if (!end) after = make_s(false, uses);
                     wait(&bars.dp_read, blocks & 1);
                     if (!end) make_dp(false, j + 2 == t.n, uses);
-                    if (s.ragged && bq_unclean(s, t, t.block(j))) {
+                    if (s.ragged && bq_unclean(s, t, j)) {
                         wait(&bars.clean[ks], (cleaned >> ks) & 1);
                         cleaned ^= 1u << ks;
                     }
@@ -1253,16 +1269,18 @@ __global__ void __launch_bounds__(kAbThreads, 1)
                 f *= ab_power(-e);
             }
             int64_t left = min(t.len, t.pos0 + tok + 1) - 32 * wg;  // visible keys from here on
-            const int64_t low = WIN ? t.pos0 + tok + 1 - s.window : 0;  // the row's window begins here
-            for (int j = 0; j < t.n; ++j, ++blocks, left -= WIN ? 0 : kAttnRows) {
-                int seen = 0, from = 0, to = 0;  // keys in view; those from .. to - 1 of them not
+            int64_t low = 0;  // (of the list) the row's window begins here
+            if constexpr (WIN) {
+                left = t.rows(s, left + 32 * wg) - 32 * wg;
+                low = max(int64_t(0), min(t.len, t.pos0 + tok + 1 - s.window) - t.begin) + t.pad;
+            }
+            for (int j = 0; j < t.n; ++j, ++blocks, left -= kAttnRows) {
+                const int seen = int(max(int64_t(0), min(left, int64_t(32))));
+                int from = 0, to = 0;  // keys in view are those below `seen`, but from .. to - 1
                 if constexpr (WIN) {
-                    const int64_t key0 = t.block(j) * int64_t(kAttnRows) + 32 * wg;
-                    seen = int(max(int64_t(0), min(left + 32 * wg - key0, int64_t(32))));
-                    from = int(max(int64_t(0), min(s.sinks - key0, int64_t(32))));
-                    to = int(max(int64_t(0), min(low - key0, int64_t(32))));
-                } else {
-                    seen = int(max(int64_t(0), min(left, int64_t(32))));
+                    const int64_t row0 = j * int64_t(kAttnRows) + 32 * wg;
+                    from = int(max(int64_t(0), min(s.sinks - row0, int64_t(32))));
+                    to = int(max(int64_t(0), min(low - row0, int64_t(32))));
                 }
                 ok = all(&bars.s_full, blocks & 1);
                 if (!ok) break;
@@ -1448,7 +1466,9 @@ cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* co
             return encode_head_map(map, p, s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows);
         };
         if (!rows(&a.qmap[r], q[r]) || !rows(&a.gmap[r], a.go[r]) || !keys(&a.kmap[r], k[r]) ||
-            !keys(&a.vmap[r], v[r]))
+            !keys(&a.vmap[r], v[r]) ||
+            !encode_sink_maps(s, r, k[r], v[r], &a.kmap_sink[r], &a.vmap_sink[r], &a.kmap_rest[r],
+                              &a.vmap_rest[r]))
             return cudaErrorInvalidValue;
     }
     if (s.window) {

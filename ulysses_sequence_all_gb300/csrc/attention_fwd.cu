@@ -114,7 +114,7 @@ template <bool WIN>
 struct AfUnit : AttnBlocks<WIN> {
     int r, bb, kvh, sp;
     int tok0, tok1;  // first token of each tile
-    int lo0, lo1;    // first key block of each tile (with a window, in the order of block())
+    int lo0, lo1;    // first key block of each tile
     int n0, n1;      // key blocks of each tile
     int len;         // keys of the batch element that any row sees
     int pos0;        // position of query token 0; beyond every key when not causal
@@ -141,16 +141,16 @@ struct AfBars {
 };
 static_assert(sizeof(AfBars<true>) <= kAfBarBytes, "barriers");
 
-// Key blocks that the tile of tokens from `tok` on sees; with a window, those of block()'s list up to
+// Key blocks that the tile of tokens from `tok` on sees; with a window, those of the unit's list up to
 // its last key (of two tiles of tokens the second's window may begin a block later: masked).
 template <bool WIN>
 __device__ __forceinline__ int af_blocks(const AttnFwdArgs& a, const AfUnit<WIN>& t, int64_t tok)
 {
     const int64_t last = min(tok + a.tile_tokens, a.s.Sq) - 1;
     const int64_t keys = min(int64_t(t.len), t.pos0 + last + 1);
-    const int n = tok >= a.s.Sq || keys <= 0 ? 0 : int((keys + kAttnRows - 1) / kAttnRows);
-    if constexpr (WIN) return t.count(n);
-    return n;
+    if (tok >= a.s.Sq || keys <= 0) return 0;
+    if constexpr (WIN) return (t.rows(a.s, keys) + kAttnRows - 1) / kAttnRows;
+    return int((keys + kAttnRows - 1) / kAttnRows);
 }
 
 template <bool WIN>
@@ -288,10 +288,10 @@ __device__ __forceinline__ void af_walk(AfBars<WIN>* bars, Queries queries, Bloc
                 }
             }
         } else {
-            if (!block(false, t, t.block(t.lo0)) || !queries(t)) return;
+            if (!block(false, t, t.lo0) || !queries(t)) return;
             for (int j = 0; j < n; ++j) {
-                if (!block(true, t, t.block(t.lo0 + j))) return;
-                if (j + 1 < n && !block(false, t, t.block(t.lo0 + j + 1))) return;
+                if (!block(true, t, t.lo0 + j)) return;
+                if (j + 1 < n && !block(false, t, t.lo0 + j + 1)) return;
             }
         }
         live = units.template next<WARP>(&t);
@@ -303,7 +303,8 @@ __device__ __forceinline__ void af_walk(AfBars<WIN>* bars, Queries queries, Bloc
 template <bool WIN>
 __device__ __forceinline__ int af_past(const AttnShape& s, const AfUnit<WIN>& t, int block)
 {
-    const int past = t.len - block * kAttnRows;
+    int past = t.len - block * kAttnRows;
+    if constexpr (WIN) past += t.pad - t.begin;
     return past >= kAttnRows || t.len >= s.Skv ? kAttnRows : past;
 }
 
@@ -311,8 +312,11 @@ __device__ __forceinline__ int af_past(const AttnShape& s, const AfUnit<WIN>& t,
 template <bool WIN>
 __device__ __forceinline__ bool af_unclean(const AttnShape& s, const AfUnit<WIN>& t, int block)
 {
-    const int2 b = attn_between<WIN>(s, t.pos0, block);
-    return af_past(s, t, block) < kAttnRows || b.y > b.x;
+    if constexpr (WIN) {
+        const int2 b = t.between(s, t.pos0, block);
+        if (b.y > b.x) return true;
+    }
+    return af_past(s, t, block) < kAttnRows;
 }
 
 template <int DP, bool F16, int MODE, bool WIN>
@@ -394,11 +398,12 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             auto block = [&](bool value, const Unit& t, int at) {
                 if (issued >= K && !wait_or_dead(&bars.kv_empty[ring.s], ring.phase ^ 1u, life))
                     return false;
-                const CUtensorMap* map = value ? &a.vmap[t.r] : &a.kmap[t.r];
                 mbar_arrive_expect_tx(&bars.kv_full[ring.s], kv_bytes);
-                for (int h = 0; h < halves; ++h)
-                    tensor_g2s_4d(smem + L::kRing + ring.s * L::kTile + h * L::kHalf, map, 64 * h,
-                                  t.kvh, at * kAttnRows, t.bb, &bars.kv_full[ring.s]);
+                attn_load_keys<WIN, L::kHalf>(
+                    smem + L::kRing + ring.s * L::kTile, halves, value ? &a.vmap[t.r] : &a.kmap[t.r],
+                    value ? &a.vmap_sink[t.r] : &a.kmap_sink[t.r],
+                    value ? &a.vmap_rest[t.r] : &a.kmap_rest[t.r], t, t.kvh, at, t.bb,
+                    &bars.kv_full[ring.s]);
                 life->loads = uint32_t(++issued);
                 ring.next(K);
                 return true;
@@ -419,8 +424,9 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 &bars, [](const Unit&) { return true; },
                 [&](bool value, const Unit& t, int at) {
                     const int past = value ? af_past(s, t, at) : kAttnRows;
-                    const int2 between =
-                        value ? attn_between<WIN>(s, t.pos0, at) : make_int2(0, 0);
+                    int2 between = make_int2(0, 0);
+                    if constexpr (WIN)
+                        if (value) between = t.between(s, t.pos0, at);
                     if (!__all_sync(0xffffffffu,
                                     wait_or_dead(&bars.kv_full[ring.s], ring.phase, life)))
                         return false;
@@ -554,7 +560,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     } else {
                         const bool last = j + 1 == n;
                         const int vs = ring.s;
-                        if (!values_ready(t, t.block(t.lo0 + j))) break;
+                        if (!values_ready(t, t.lo0 + j)) break;
                         ring.next(K);
                         const int ks = ring.s;
                         const bool any = !last || more;
@@ -648,8 +654,9 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             // What the loop over the blocks does not need is read again after it: a row's scores
             // take 128 registers.
             int slot = 0, n, left;  // of this tile's queries; its blocks; keys seen from its first
-            int at = 0, low = 0;    // with a window: the block, its row's first key
-            AttnBlocks<WIN> list;
+            // with a window: where the row's begins in the tile's blocks, where the first tokens end, the
+            // blocks up to any row's of the warp
+            int low = 0, sinks = 0, edge = 0;
             {
                 const Unit& t = units.record();
 #pragma unroll
@@ -665,13 +672,15 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     continue;
                 }
                 const int64_t seen = min(int64_t(t.len), t.pos0 + int64_t(t.tok(tile)) + tok_in + 1);
-                left = int(max(int64_t(-1), seen - int64_t(t.lo(tile)) * kAttnRows));
                 if constexpr (WIN) {
-                    list = t;
-                    at = t.lo(tile);
-                    left = int(max(int64_t(0), seen));
-                    low = int(max(int64_t(0), min(int64_t(t.len), t.pos0 + int64_t(t.tok(tile)) + tok_in + 1 -
-                                                                      s.window)));
+                    const int64_t first = t.pos0 + int64_t(t.tok(tile)) + tok_in + 1 - s.window;
+                    low = int(max(int64_t(0), min(int64_t(t.len), first) - t.begin)) + t.pad -
+                          t.lo(tile) * kAttnRows;
+                    left = t.rows(s, seen) - t.lo(tile) * kAttnRows;
+                    sinks = s.sinks - t.lo(tile) * kAttnRows;
+                    edge = (__reduce_max_sync(0xffffffffu, low) + kAttnRows - 1) >> 7;
+                } else {
+                    left = int(max(int64_t(-1), seen - int64_t(t.lo(tile)) * kAttnRows));
                 }
             }
             float m = -INFINITY, l = 0.0f;
@@ -693,7 +702,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 units.template release<true>();
                 continue;
             }
-            for (int j = 0; j < n; ++j, left -= WIN ? 0 : kAttnRows) {
+            for (int j = 0; j < n; ++j, left -= kAttnRows) {
                 ok = all(&bars.s_full[tile], blocks & 1);
                 if (!ok) break;
                 ++blocks;
@@ -703,14 +712,9 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, x[q]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_wait_ld(x[q]);
-                int from = 0, to = 0;  // keys of the block between the first tokens and the row's window
-                int seen = left;
-                if constexpr (WIN) {
-                    const int key0 = list.block(at + j) * kAttnRows;
-                    seen = left - key0;
-                    from = s.sinks - key0;
-                    to = low - key0;
-                    if (__any_sync(0xffffffffu, to > max(0, from) && from < kAttnRows)) {
+                if (WIN && j < edge) {  // between the first tokens and the row's window
+                    const int from = sinks - j * kAttnRows, to = low - j * kAttnRows;
+                    if (from < kAttnRows) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -718,7 +722,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                                 if (q * 32 + c >= from && q * 32 + c < to) x[q][c] = 0xFF800000u;
                     }
                 }
-                if (__any_sync(0xffffffffu, seen < kAttnRows)) {
+                if (__any_sync(0xffffffffu, left < kAttnRows)) {
+                    const int seen = max(0, left);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -923,6 +928,17 @@ int64_t attn_order_group(int64_t heads, int64_t bytes)
     return g < 1 ? 1 : g;
 }
 
+bool encode_sink_maps(const AttnShape& s, int r, const void* k, const void* v, CUtensorMap* k_sink,
+                      CUtensorMap* v_sink, CUtensorMap* k_rest, CUtensorMap* v_rest)
+{
+    if (!s.window || s.sink_rows == 0 || s.sink_rows >= kAttnRows) return true;
+    const int64_t rest = kAttnRows - s.sink_rows;
+    return encode_head_map(k_sink, k, s.f16, s.d, s.m[r], s.Skv, s.b, 1, s.sink_rows) &&
+           encode_head_map(v_sink, v, s.f16, s.d, s.m[r], s.Skv, s.b, 1, s.sink_rows) &&
+           encode_head_map(k_rest, k, s.f16, s.d, s.m[r], s.Skv, s.b, 1, rest) &&
+           encode_head_map(v_rest, v, s.f16, s.d, s.m[r], s.Skv, s.b, 1, rest);
+}
+
 // Row tiles, units and parts of the keys. Where one tile holds all rows, a CTA's two tiles take a
 // part each. The keys are split further while a part keeps some blocks (a part costs its start, an
 // fp32 output and a share of the join).
@@ -931,9 +947,9 @@ static int64_t af_most_blocks(const AttnShape& s, int64_t pair)
 {
     const int64_t all = (s.Skv + kAttnRows - 1) / kAttnRows;
     if (!s.window) return all;
-    // (a window of w keys over `pair` tokens, anywhere in a block; the first tokens)
-    const int64_t near = s.window >= s.Skv ? all : (s.window + pair - 2) / kAttnRows + 2;
-    const int64_t some = near + (s.sinks + kAttnRows - 1) / kAttnRows;
+    // (a window of w keys over `pair` tokens; the first tokens)
+    const int64_t near = s.window >= s.Skv ? s.Skv : s.window + pair - 1;
+    const int64_t some = (near + s.sink_rows + kAttnRows - 1) / kAttnRows;
     return some < all ? some : all;
 }
 
@@ -1026,6 +1042,9 @@ cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* co
         if (!encode_head_map(&a.qmap[r], q[r], s.f16, s.d, s.n[r], s.Sq, s.b, s.group, a.tile_tokens) ||
             !encode_head_map(&a.kmap[r], k[r], s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows) ||
             !encode_head_map(&a.vmap[r], v[r], s.f16, s.d, s.m[r], s.Skv, s.b, 1, kAttnRows))
+            return cudaErrorInvalidValue;
+        if (!encode_sink_maps(s, r, k[r], v[r], &a.kmap_sink[r], &a.vmap_sink[r], &a.kmap_rest[r],
+                              &a.vmap_rest[r]))
             return cudaErrorInvalidValue;
     }
     if (s.d <= 64)
