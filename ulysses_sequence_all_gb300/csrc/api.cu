@@ -1180,7 +1180,10 @@ int paged_room(const Plan& cp, int64_t table_pages, int64_t* room)
 // reads a batch element's keys as its only page) go there.
 bool window_of_few_rows(const Plan& qp, const Plan& kp)
 {
-    return kp.N > 0 && qp.S * (qp.N / kp.N) <= kPagedMaxRows;
+    #ifndef FEW
+#define FEW kPagedMaxRows
+#endif
+    return kp.N > 0 && qp.S * (qp.N / kp.N) <= FEW;
 }
 
 int window_pages(const Plan& qp, const Plan& kp, const Window& w, PagedArgs* a)

@@ -44,7 +44,7 @@ static __device__ unsigned g_attn_paged_status;
 constexpr int kPgThreads = 2 * 32 * kPagedWarps;  // warps 0-3, and a warpgroup with the copying one
 // Registers a thread: 256 x 128 at launch = 128 x this + 128 x (256 - this), what the roles take
 template <int DP, int RT>
-constexpr int kPgRegsProducts = RT == 1 ? 176 : DP == 64 ? (RT == 2 ? 176 : 200) : RT == 2 ? 192 : 216;
+constexpr int kPgRegsProducts = DP == 128 && RT == 2 ? 192 : 176;
 constexpr float kPgRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 constexpr float kPgUpF16 = 7.0f;    // fp16 probabilities are held times 2^this
 constexpr int kPgJoinThreads = 256, kPgJoinParts = 8;
@@ -126,22 +126,21 @@ __device__ __forceinline__ int paged_owner(int64_t total, int parts, int64_t at)
 
 // ---- the kernel -------------------------------------------------------------------------------------
 
-template <int DP, int RT>
+template <int DP>
 struct PgSmem {
     static constexpr int kHalf = kPagedBlock * 128;           // 64 columns of a block
     static constexpr int kV = kHalf * (DP / 64);              // values after keys
     static constexpr int kBlock = 2 * kV;
     static constexpr int kStages = DP == 128 ? 3 : 6;
     static constexpr int kRing = 2048;                        // PgShared first
-    static constexpr int kQ = kRing + kStages * kBlock;       // 32 rows of queries (fewer: in registers)
-    static constexpr int kTotal = kQ + (RT == 4 ? kPagedMaxRows * DP * 2 : 0);
+    static constexpr int kTotal = kRing + kStages * kBlock;
     static_assert(2 * (kTotal + 1024 + kSmemReservedPerCta) <= kSmemPerSm, "two CTAs an SM");
 };
 
 struct PgShared {
     uint64_t full[6], empty[6];
-    float2 ml[kPagedWarps][kPagedMaxRows];  // each warp's maxima and sums
-    int used[kPagedWarps];                  // whether it has outputs
+    float2 ml[kPagedWarps][16];  // each warp's maxima and sums
+    int used[kPagedWarps];       // whether it has outputs
     int64_t warp_sum[kPgThreads / 32];
     int64_t before;  // blocks of the entries before `entry`
     int entry;
@@ -193,17 +192,17 @@ __device__ __forceinline__ void pg_sync()  // the four warps with products
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kPagedWarps) : "memory");
 }
 
-// RT: tiles of 8 query rows.
-template <int DP, bool F16, int RT>
+// RT: tiles of 8 query rows of a warp. RH: groups of such rows; warps w with the same w % RH share a group
+// and part the block's four tiles of keys between them.
+template <int DP, bool F16, int RT, int RH>
 __global__ void __launch_bounds__(kPgThreads, 2)
     attn_paged_kernel(const __grid_constant__ PagedArgs a)
 {
-    using L = PgSmem<DP, RT>;
+    using L = PgSmem<DP>;
     using E = ElemT<F16>;
-    constexpr int K = L::kStages, kD = DP / 16, kRows = 8 * RT;
-    constexpr int kRound = RT < 2 ? RT : 2;       // tiles of rows whose outputs a warp's part of a stage holds
-    constexpr int kPartRows = 2048 / (DP * 4);    // rows of outputs in 16 rows of a tile's 128 bytes
-    constexpr bool kQShared = RT == 4;
+    constexpr int K = L::kStages, kD = DP / 16;
+    constexpr int kMine = 8 * RT, kRows = kMine * RH;  // query rows of a warp, of a pass
+    constexpr int kPartRows = 2048 / (DP * 4);         // rows of outputs in 16 rows of a tile's 128 bytes
     constexpr float kUp = F16 ? kPgUpF16 : 0.0f;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -356,8 +355,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
         share(c);
         PagedShared shared = {0, 0, 0, 0, 0};
-        uint32_t q[kQShared ? 1 : RT][kD][2];
-        // The walk's rank and key head; its queries to registers (32 rows: to shared memory).
+        uint32_t q[RT][kD][2];
+        // The walk's rank and key head; this warp's queries of it.
         auto place = [&](int* r, int* kvh) {
             *r = 0;
             while (*r + 1 < a.W && walk.head >= a.m_begin[*r + 1]) ++*r;
@@ -366,38 +365,25 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         auto queries = [&]() {
             int r, kvh;
             place(&r, &kvh);
-            const int64_t row0 = int64_t(walk.en.rg) * kRows, row_end = a.Sq * a.group;
+            const int64_t row0 = int64_t(walk.en.rg) * kRows + (warp % RH) * kMine, row_end = a.Sq * a.group;
             auto query = [&](int64_t row) {  // its first byte
                 const int64_t tok = div_fast(row, a.group);
                 return a.q[r] + ((int64_t(walk.en.bb) * a.Sq + tok) * a.n[r] + kvh * a.group + row -
                                  tok * a.group) * a.d * 2;
             };
-            if constexpr (kQShared) {
-                for (int i = threadIdx.x; i < kRows * (DP / 8); i += 32 * kPagedWarps) {
-                    const int row = i / (DP / 8), w = i % (DP / 8);
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row0 + row < row_end && w * 8 < a.d)
-                        x = *reinterpret_cast<const uint4*>(query(row0 + row) + w * 16);
-                    st_shared_v4(smem + L::kQ + (w >> 3) * kRows * 128 + row * 128 +
-                                     (((w & 7) ^ (row & 7)) << 4),
-                                 x);
-                }
-                pg_sync();
-            } else {
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const int64_t row = row0 + t * 8 + quad;
-                    const uint8_t* src = query(row) + pair * 2;
+            for (int t = 0; t < RT; ++t) {
+                const int64_t row = row0 + t * 8 + quad;
+                const uint8_t* src = query(row) + pair * 2;
 #pragma unroll
-                    for (int ks = 0; ks < kD; ++ks)
+                for (int ks = 0; ks < kD; ++ks)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            q[t][ks][h] = 0;
-                            if (row < row_end && ks * 16 + h * 8 < a.d)
-                                q[t][ks][h] = __ldg(reinterpret_cast<const uint32_t*>(
-                                    src + (ks * 16 + h * 8) * 2));
-                        }
-                }
+                    for (int h = 0; h < 2; ++h) {
+                        q[t][ks][h] = 0;
+                        if (row < row_end && ks * 16 + h * 8 < a.d)
+                            q[t][ks][h] =
+                                __ldg(reinterpret_cast<const uint32_t*>(src + (ks * 16 + h * 8) * 2));
+                    }
             }
         };
         if (walk.more()) queries();
@@ -408,7 +394,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             const int head = walk.head, from = walk.j, to_block = walk.stop();
             const int64_t place = int64_t(walk.e) * heads + head;
             const int64_t at_end = stop - walk.left + kPgEnd + en.n;  // where the sequence ends in the work
-            const int64_t row0 = int64_t(en.rg) * kRows, row_end = a.Sq * a.group;
+            const int64_t pass0 = int64_t(en.rg) * kRows, row_end = a.Sq * a.group;
+            const int64_t row0 = pass0 + (warp % RH) * kMine;
             // keys that every row sees: below hi_all, and from lo_all on or first tokens
             const int hi_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t0 + 1)));
             const int lo_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t1 - a.window)));
@@ -425,14 +412,17 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             bool used = false;  // this warp has seen keys of the sequence
             int stage = -1;     // of the sequence's last block here, held until its outputs are joined
             for (int j = from; j < to_block; ++j) {
-                const int block0 = en.block(j) * kPagedBlock, key0 = block0 + warp * kPagedTile;
+                const int block0 = en.block(j) * kPagedBlock;
                 if (ok && en.sees(block0, block0 + kPagedBlock)) {
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[ring.s], ring.phase, limit));
                     if (!ok) continue;
                     stage = ring.s;
                     ring.next(K);
-                    uint8_t* keys = smem + L::kRing + stage * L::kBlock + warp * (kPagedTile * 128);
-                    if (en.sees(key0, key0 + kPagedTile)) {
+#pragma unroll 1
+                    for (int i = warp / RH; i < kPagedWarps; i += kPagedWarps / RH) {
+                        const int key0 = block0 + i * kPagedTile;
+                        uint8_t* keys = smem + L::kRing + stage * L::kBlock + i * (kPagedTile * 128);
+                        if (!en.sees(key0, key0 + kPagedTile)) continue;
                         used = true;
                         const bool edge = key0 + kPagedTile > hi_all ||
                                           (key0 < lo_all && key0 + kPagedTile > a.sinks);
@@ -463,31 +453,15 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                                 uint32_t x[4];
                                 pg_ldmatrix<false>(x, keys_at + (ks >> 2) * L::kHalf + k * 128 +
                                                           ((((ks & 3) * 2 + w) ^ (k & 7)) << 4));
-                                if constexpr (kQShared) {
-                                    const int qr = ((lane >> 4) & 1) * 8 + (lane & 7);
-                                    const uint32_t q_at =
-                                        smem_u32(smem + L::kQ) + (ks >> 2) * kRows * 128 + qr * 128 +
-                                        ((((ks & 3) * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
 #pragma unroll
-                                    for (int t = 0; t < RT; t += 2) {
-                                        uint32_t y[4];
-                                        pg_ldmatrix<false>(y, q_at + t * 8 * 128);
-                                        pg_mma<F16>(s[t], x, y[0], y[1]);
-                                        pg_mma<F16>(s[t + 1], x, y[2], y[3]);
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int t = 0; t < RT; ++t)
-                                        pg_mma<F16>((ks & 1) ? s2[t] : s[t], x, q[t][ks][0], q[t][ks][1]);
-                                }
+                                for (int t = 0; t < RT; ++t)
+                                    pg_mma<F16>((ks & 1) ? s2[t] : s[t], x, q[t][ks][0], q[t][ks][1]);
                             }
                         }
-                        if constexpr (!kQShared) {
 #pragma unroll
-                            for (int t = 0; t < RT; ++t)
+                        for (int t = 0; t < RT; ++t)
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) s[t][x] += s2[t][x];
-                        }
+                            for (int x = 0; x < 4; ++x) s[t][x] += s2[t][x];
                         if (edge) {
 #pragma unroll
                             for (int t = 0; t < RT; ++t)
@@ -572,7 +546,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             }
             walk.j = to_block - 1;
             walk.step(a);
-            if (!kQShared && walk.more()) queries();  // (they arrive during the join)
+            if (walk.more()) queries();  // (they arrive during the join)
 
             // Join the warps: a row's maximum, sum and output.
             const bool whole = from == 0 && to_block == en.n;
@@ -593,73 +567,69 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                 }
             used = used && stage >= 0;  // (it has given up otherwise)
             if (lane == 0) sh.used[warp] = used;
-            // Row `row` of warp w's outputs lies where its keys and values of the last block were.
+            // Row `row` of warp w's outputs lies where tile w's keys and values of the last block were.
+            if constexpr (RH > 1) pg_sync();  // (which other warps read as well)
             auto out_at = [&](int w, int row, int col) {
                 return reinterpret_cast<float*>(smem + L::kRing + stage * L::kBlock +
                                                 (row / kPartRows) * L::kHalf + w * (kPagedTile * 128)) +
                        (row % kPartRows) * DP + (col ^ (((row >> 1) & 3) << 3));
             };
+            __syncwarp();
+            if (used) {
 #pragma unroll
-            for (int t0 = 0; t0 < RT; t0 += kRound) {
-                if (t0 > 0) pg_sync();
-                __syncwarp();
-                if (used) {
+                for (int t = 0; t < RT; ++t)
 #pragma unroll
-                    for (int t = 0; t < kRound; ++t)
+                    for (int i = 0; i < kD; ++i)
 #pragma unroll
-                        for (int i = 0; i < kD; ++i)
+                        for (int x = 0; x < 4; ++x)
+                            *out_at(warp, t * 8 + pair + (x & 1), i * 16 + (x >> 1) * 8 + quad) = o[t][i][x];
+            }
+            pg_sync();
+            for (int it = threadIdx.x; it < kRows * (DP / 8); it += 32 * kPagedWarps) {
+                const int row = it / (DP / 8), col = it % (DP / 8) * 8;
+                const int rh = row / kMine, in = row - rh * kMine;  // the warps' group, the row in it
+                const int64_t to = pass0 + row;
+                if (col >= a.d) continue;
+                float top = -INFINITY, sum = 0.0f, y[8];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                *out_at(warp, t * 8 + pair + (x & 1), i * 16 + (x >> 1) * 8 + quad) =
-                                    o[t0 + t][i][x];
+                for (int w = 0; w < kPagedWarps; w += RH) top = fmaxf(top, sh.ml[w + rh][in].x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kPagedWarps; w += RH) {
+                    const float2 z = sh.ml[w + rh][in];
+                    if (!sh.used[w + rh] || stage < 0 || z.x == -INFINITY) continue;
+                    const float f = ex2((z.x - top) * sl2);
+                    sum = fmaf(f, z.y, sum);
+#pragma unroll
+                    for (int k = 0; k < 8; k += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(out_at(w + rh, in, col + k));
+                        y[k] = fmaf(f, v.x, y[k]);
+                        y[k + 1] = fmaf(f, v.y, y[k + 1]);
+                        y[k + 2] = fmaf(f, v.z, y[k + 2]);
+                        y[k + 3] = fmaf(f, v.w, y[k + 3]);
+                    }
                 }
-                pg_sync();
-                for (int it = threadIdx.x; it < kRound * 8 * (DP / 8); it += 32 * kPagedWarps) {
-                    const int row = it / (DP / 8), col = it % (DP / 8) * 8;
-                    const int64_t to = row0 + t0 * 8 + row;
-                    if (col >= a.d) continue;
-                    float top = -INFINITY, sum = 0.0f, y[8];
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // NaN stays NaN
+                const float lse = sum == 0.0f ? -INFINITY
+                                              : top * a.scale + (logf(sum) - kUp * 0.69314718056f);
 #pragma unroll
-                    for (int w = 0; w < kPagedWarps; ++w) top = fmaxf(top, sh.ml[w][t0 * 8 + row].x);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < kPagedWarps; ++w) {
-                        const float2 z = sh.ml[w][t0 * 8 + row];
-                        if (!sh.used[w] || stage < 0 || z.x == -INFINITY) continue;
-                        const float f = ex2((z.x - top) * sl2);
-                        sum = fmaf(f, z.y, sum);
-#pragma unroll
-                        for (int k = 0; k < 8; k += 4) {
-                            const float4 v = *reinterpret_cast<const float4*>(out_at(w, row, col + k));
-                            y[k] = fmaf(f, v.x, y[k]);
-                            y[k + 1] = fmaf(f, v.y, y[k + 1]);
-                            y[k + 2] = fmaf(f, v.z, y[k + 2]);
-                            y[k + 3] = fmaf(f, v.w, y[k + 3]);
-                        }
-                    }
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // NaN stays NaN
-                    const float lse = sum == 0.0f ? -INFINITY
-                                                  : top * a.scale + (logf(sum) - kUp * 0.69314718056f);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] *= inv;
-                    if (!whole) {
-                        const int64_t at_row = part * kRows + t0 * 8 + row;
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + at_row * a.d + col);
-                        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-                        if (col == 0) a.part_lse[at_row] = lse;
-                    } else if (to < row_end) {
-                        const int64_t tok = div_fast(to, a.group);
-                        const int64_t h = kvh * a.group + (to - tok * a.group);
-                        st_v4(a.o[r] + (((int64_t(en.bb) * a.Sq + tok) * a.n[r] + h) * a.d + col) * 2,
-                              make_uint4(E::pack(y[0], y[1]), E::pack(y[2], y[3]), E::pack(y[4], y[5]),
-                                         E::pack(y[6], y[7])));
-                        if (col == 0) a.lse[r][(int64_t(en.bb) * a.n[r] + h) * a.Sq + tok] = lse;
-                    }
+                for (int k = 0; k < 8; ++k) y[k] *= inv;
+                if (!whole) {
+                    const int64_t at_row = part * kRows + row;
+                    float4* dst = reinterpret_cast<float4*>(a.part_o + at_row * a.d + col);
+                    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    if (col == 0) a.part_lse[at_row] = lse;
+                } else if (to < row_end) {
+                    const int64_t tok = div_fast(to, a.group);
+                    const int64_t h = kvh * a.group + (to - tok * a.group);
+                    st_v4(a.o[r] + (((int64_t(en.bb) * a.Sq + tok) * a.n[r] + h) * a.d + col) * 2,
+                          make_uint4(E::pack(y[0], y[1]), E::pack(y[2], y[3]), E::pack(y[4], y[5]),
+                                     E::pack(y[6], y[7])));
+                    if (col == 0) a.lse[r][(int64_t(en.bb) * a.n[r] + h) * a.Sq + tok] = lse;
                 }
             }
-            if (kQShared && walk.more()) queries();  // (its barrier is the next one as well)
             fence_proxy_async_shared();  // (a copy comes into this stage next)
             pg_sync();
             if (stage >= 0 && lane == 0) mbar_arrive(&sh.empty[stage]);
@@ -769,7 +739,8 @@ __global__ void __launch_bounds__(kPgJoinThreads, 2)
 void attn_paged_split(PagedArgs* a, int sm_count)
 {
     const int64_t rows = a->Sq * a->group;
-    a->rows = rows <= 8 ? 8 : rows <= 16 ? 16 : kPagedMaxRows;
+    a->rows = 8;
+    while (a->rows < kPagedMaxRows && a->rows < rows) a->rows *= 2;
     a->row_groups = int32_t((rows + a->rows - 1) / a->rows);
     a->parts = 2 * sm_count;
     const int64_t groups = int64_t(a->b) * a->row_groups * a->m_begin[a->W];
@@ -777,25 +748,27 @@ void attn_paged_split(PagedArgs* a, int sm_count)
     a->notes = int32_t(a->by_group ? groups : a->parts);
 }
 
-template <int DP, bool F16, int RT>
+template <int DP, bool F16, int RT, int RH>
 static cudaError_t pg_launch(const PagedArgs& a, cudaStream_t stream, int device, int64_t cap,
                              int sm_count)
 {
     static std::atomic<unsigned long long> raised{0};
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
-    constexpr int smem = PgSmem<DP, RT>::kTotal + 1024;
+    constexpr int smem = PgSmem<DP>::kTotal + 1024;
     if (bit && !(raised.load() & bit)) {
-        cudaError_t e = cudaFuncSetAttribute(attn_paged_kernel<DP, F16, RT>,
+        cudaError_t e = cudaFuncSetAttribute(attn_paged_kernel<DP, F16, RT, RH>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         raised.fetch_or(bit);
     }
     const unsigned grid = unsigned(a.parts < cap ? a.parts : cap);
-    attn_paged_kernel<DP, F16, RT><<<grid, kPgThreads, smem, stream>>>(a);
+    attn_paged_kernel<DP, F16, RT, RH><<<grid, kPgThreads, smem, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // Few sequences are shared by many CTAs each: then a block has one row, its warps the parts.
-    const int y_rows = a.notes * 8 <= a.parts ? 1 : kPgJoinThreads / 32;
+    // Few sequences are shared by many CTAs each: then a block has fewer rows, its warps more of the parts
+    // (as many as they have on their way at once).
+    int y_rows = kPgJoinThreads / 32;
+    while (y_rows > 1 && int64_t(a.notes) * kPgJoinParts * (kPgJoinThreads / 32 / y_rows) < a.parts) y_rows /= 2;
     unsigned x = unsigned(a.notes < cap ? a.notes : cap), y = unsigned(a.rows / y_rows);
     if (int64_t(x) * y > cap) y = 1;
     cudaLaunchConfig_t cfg = {};
@@ -814,9 +787,10 @@ template <int DP, bool F16>
 static cudaError_t pg_launch_rows(const PagedArgs& a, cudaStream_t stream, int device, int64_t cap,
                                   int sm_count)
 {
-    if (a.rows == 8) return pg_launch<DP, F16, 1>(a, stream, device, cap, sm_count);
-    if (a.rows == 16) return pg_launch<DP, F16, 2>(a, stream, device, cap, sm_count);
-    return pg_launch<DP, F16, 4>(a, stream, device, cap, sm_count);
+    if (a.rows == 8) return pg_launch<DP, F16, 1, 1>(a, stream, device, cap, sm_count);
+    if (a.rows == 16) return pg_launch<DP, F16, 2, 1>(a, stream, device, cap, sm_count);
+    if (a.rows == 32) return pg_launch<DP, F16, 2, 2>(a, stream, device, cap, sm_count);
+    return pg_launch<DP, F16, 2, 4>(a, stream, device, cap, sm_count);
 }
 
 cudaError_t attn_paged_launch(PagedArgs& a, const void* const* k, const void* const* v,

@@ -18,7 +18,7 @@ constexpr unsigned kStatusBadPage = 4u;  // a page outside the pool was needed
 constexpr int kPagedTile = 16;           // keys that a warp takes at a time
 constexpr int kPagedWarps = 4;
 constexpr int kPagedBlock = kPagedTile * kPagedWarps;
-constexpr int kPagedMaxRows = 32;        // query rows of one pass over the keys
+constexpr int kPagedMaxRows = 64;        // query rows of one pass over the keys
 
 struct AppendArgs {
     const uint8_t* src[2][kMaxW];  // new keys, values: (b, tokens, m_r, d)
@@ -52,7 +52,7 @@ struct PagedArgs {
     int32_t room;            // keys that a batch element's pages can hold
     int32_t sinks;
     int64_t window;          // beyond every position where there is none
-    int32_t rows, row_groups;  // query rows of a pass (8, 16, 32); passes of a key head
+    int32_t rows, row_groups;  // query rows of a pass (8, 16, 32, 64); passes of a key head
     int32_t parts;             // shares of all the work, one CTA at a time works on one
     int32_t by_group, notes;   // `shared` has an entry for each row group and head, or for each share
     float scale;
