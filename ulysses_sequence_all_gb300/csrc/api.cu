@@ -910,6 +910,15 @@ struct Window {
     int64_t keys, sinks;
 };
 
+// Rows of the first tokens in a unit's blocks, which begin at multiples of `align` (a power of two).
+void attn_sink_rows(AttnShape* s, int align)
+{
+    s->align = align;
+    int32_t unit = align > 8 ? align : 8;
+    if ((s->sinks + unit - 1) / unit * unit > kAttnSharedSinks) unit = kAttnRows;
+    s->sink_rows = (s->sinks + unit - 1) / unit * unit;
+}
+
 // The window of a windowed call.
 int attn_window(AttnShape* s, int64_t window, int64_t sinks)
 {
@@ -917,8 +926,7 @@ int attn_window(AttnShape* s, int64_t window, int64_t sinks)
     s->causal = 1;
     s->window = window < kAttnFar ? window : kAttnFar;
     s->sinks = int32_t(sinks < s->Skv ? sinks : s->Skv);
-    const int32_t unit = s->sinks <= kAttnSharedSinks ? 8 : kAttnRows;
-    s->sink_rows = (s->sinks + unit - 1) / unit * unit;
+    attn_sink_rows(s, 1);
     return ULY_OK;
 }
 
@@ -1106,6 +1114,40 @@ int paged_shape(const Plan& qp, const Plan& cp, PagedArgs* a)
     return ULY_OK;
 }
 
+// What of a call over pages the kernel of many rows needs, from what the one of few rows does.
+void pages_args(const PagedArgs& p, AttnFwdArgs* a)
+{
+    std::memset(a, 0, sizeof *a);
+    AttnShape& s = a->s;
+    s.W = p.W;
+    s.b = p.b;
+    s.d = p.d;
+    s.f16 = p.f16;
+    s.group = p.group;
+    s.Sq = p.Sq;
+    s.Skv = p.room;
+    for (int r = 0; r < kMaxW; ++r) {
+        s.n[r] = p.n[r];
+        s.m[r] = p.m_begin[r + 1] - p.m_begin[r];
+        s.head_begin[r + 1] = s.head_begin[r] + p.b * s.m[r];
+        s.row_begin[r + 1] = s.row_begin[r] + int64_t(p.b) * s.n[r] * p.Sq;
+    }
+    s.kv_lens = p.kv_lens;
+    s.q_start = p.q_start;
+    s.causal = s.ragged = s.from_end = 1;
+    s.window = p.window;
+    s.sinks = p.sinks;
+    a->pages.table = p.table;
+    a->pages.table_pages = p.table_pages;
+    a->pages.pages = p.pages;
+    a->pages.page = p.page;
+    a->pages.box = 8;  // rows of a copy: as many as divide a page and a block
+    while (a->pages.box < kAttnRows && p.page % (2 * a->pages.box) == 0) a->pages.box *= 2;
+    attn_sink_rows(&s, a->pages.box);
+}
+
+bool pages_of_few_rows(const PagedArgs& a) { return a.Sq * a.group <= kPagedFewRows; }
+
 // Work shares and passes of a call; the bytes of its workspace and the places in it.
 int paged_setup(const DeviceInfo& dev, PagedArgs* a, void* workspace, size_t* bytes)
 {
@@ -1120,6 +1162,13 @@ int paged_setup(const DeviceInfo& dev, PagedArgs* a, void* workspace, size_t* by
     a->part_lse = reinterpret_cast<float*>(base + o);
     a->shared = reinterpret_cast<PagedShared*>(base + o + lse);
     return ULY_OK;
+}
+
+size_t pages_setup(const DeviceInfo& dev, AttnFwdArgs* a)
+{
+    attn_fwd_split_pages(a, dev.sm_count);
+    const size_t rows = size_t(a->s.row_begin[a->s.W]);
+    return a->parts == 1 ? 0 : size_t(a->parts) * ((rows * size_t(a->s.d) + rows) * sizeof(float));
 }
 
 // The launch of a call whose masks and pages are set in `a`; kv_bytes: of a rank's keys.
@@ -1151,6 +1200,27 @@ int paged_device(const Plan& qp, PagedArgs& a, const int64_t* kv_bytes, const vo
     DeviceInfo dev;
     if ((rc = current_device(&dev))) return rc;
     size_t need = 0;
+    if (a.table && !pages_of_few_rows(a)) {
+        AttnFwdArgs f;
+        pages_args(a, &f);
+        need = pages_setup(dev, &f);
+        if (need) {
+            if (!workspace || workspace_bytes < need) return ULY_EINVAL;
+            if (!aligned16(workspace)) return ULY_EALIGN;
+            outs.add(workspace, int64_t(need));
+            if ((rc = check_overlap(ins.p, ins.n, ins.count, outs.p, outs.n, outs.count))) return rc;
+            f.part_o = static_cast<float*>(workspace);
+            f.part_lse = f.part_o + size_t(f.parts) * size_t(f.s.row_begin[W]) * size_t(a.d);
+        }
+        f.s.scale = scale;
+        f.s.wait_us = attention_wait_us.load(std::memory_order_relaxed);
+        for (int r = 0; r < W; ++r) {
+            f.o[r] = static_cast<uint8_t*>(o[r]);
+            f.lse[r] = lse[r];
+        }
+        const cudaError_t e = attn_fwd_launch(f, q, k, v, stream, dev.device, attn_cap(qp), dev.sm_count);
+        return e == cudaSuccess ? ULY_OK : cuda_fail(e);
+    }
     if ((rc = paged_setup(dev, &a, workspace, &need))) return rc;
     if (!workspace || workspace_bytes < need) return ULY_EINVAL;
     if (!aligned16(workspace)) return ULY_EALIGN;
@@ -1180,10 +1250,7 @@ int paged_room(const Plan& cp, int64_t table_pages, int64_t* room)
 // reads a batch element's keys as its only page) go there.
 bool window_of_few_rows(const Plan& qp, const Plan& kp)
 {
-    #ifndef FEW
-#define FEW kPagedMaxRows
-#endif
-    return kp.N > 0 && qp.S * (qp.N / kp.N) <= FEW;
+        return kp.N > 0 && qp.S * (qp.N / kp.N) <= kWindowFewRows;
 }
 
 int window_pages(const Plan& qp, const Plan& kp, const Window& w, PagedArgs* a)
@@ -1683,6 +1750,12 @@ int ulysses_attention_paged_workspace(ulysses_plan_t q_plan, ulysses_plan_t cach
     DeviceInfo dev;
     int rc = paged_shape(q_plan->p, cache_plan->p, &a);
     if (rc || (rc = current_device(&dev))) return rc;
+    if (!pages_of_few_rows(a)) {
+        AttnFwdArgs f;
+        pages_args(a, &f);
+        *bytes = pages_setup(dev, &f);
+        return ULY_OK;
+    }
     return paged_setup(dev, &a, nullptr, bytes);
 }
 

@@ -43,6 +43,8 @@ struct AttnShape {
     int32_t sinks;
     int32_t sink_rows;  // rows that they take in a unit's blocks: see AttnBlocks
     int64_t window;
+    int32_t align;      // a unit's window begins at a multiple of this (1; pages: rows of a copy)
+    int32_t from_end;   // without q_start the queries are the last Sq tokens
 };
 // Up to here first tokens share a block with keys of the window (a copy of 8 k rows in front of theirs);
 // more of them have blocks of their own.
@@ -56,7 +58,7 @@ __device__ __forceinline__ void attn_limits(const AttnShape& s, int bb, int64_t*
     *len = s.kv_lens ? min(s.Skv, int64_t(max(0, s.kv_lens[bb]))) : s.Skv;
     *pos0 = s.Skv;
     if (s.causal) {
-        *pos0 = s.q_start ? int64_t(s.q_start[bb]) : 0;
+        *pos0 = s.q_start ? int64_t(s.q_start[bb]) : s.from_end ? *len - s.Sq : 0;
         *len = min(*len, max(int64_t(0), *pos0 + s.Sq));
     }
 }
@@ -73,8 +75,10 @@ struct AttnBlocks {
 template <>
 struct AttnBlocks<true> {
     int pad, begin;
-    __device__ __forceinline__ void set(const AttnShape& s, int64_t first)
+    // `first`: the first key in the first row's window, at most `end`, that of the keys anyone sees
+    __device__ __forceinline__ void set(const AttnShape& s, int64_t first, int64_t end)
     {
+        if (first < end && s.align > 1) first -= first % s.align;
         const bool apart = first > s.sink_rows;
         pad = apart ? s.sink_rows : 0;
         begin = apart ? int(first) : 0;
@@ -89,7 +93,7 @@ struct AttnBlocks<true> {
     // first window, or first tokens that are none: x .. y - 1 (none where y <= x).
     __device__ __forceinline__ int2 between(const AttnShape& s, int64_t pos0, int j) const
     {
-        const int64_t to = pad ? pad : begin ? 0 : pos0 + 1 - s.window, row0 = int64_t(j) * kAttnRows;
+        const int64_t to = pad + max(int64_t(0), pos0 + 1 - s.window - begin), row0 = int64_t(j) * kAttnRows;
         return make_int2(int(max(int64_t(0), min(int64_t(kAttnRows), s.sinks - row0))),
                          int(max(int64_t(0), min(int64_t(kAttnRows), to - row0))));
     }
@@ -179,8 +183,17 @@ struct AttnUnitSource {
 };
 #endif
 
+// Keys and values in pages (see paged.h): key j of batch element bb is row j % page of page
+// table[bb][j / page]; a copy takes `box` rows of one.
+struct AttnPages {
+    const int32_t* table;
+    int64_t table_pages;
+    int32_t pages, page, box;
+};
+
 struct AttnFwdArgs {
     AttnShape s;
+    AttnPages pages;
     CUtensorMap qmap[kMaxW], kmap[kMaxW], vmap[kMaxW];
     CUtensorMap kmap_sink[kMaxW], vmap_sink[kMaxW];  // with a window: boxes of sink_rows, and of the rest
     CUtensorMap kmap_rest[kMaxW], vmap_rest[kMaxW];  // of a block
@@ -260,6 +273,8 @@ inline cudaError_t attn_launch_early(void (*kernel)(Args), unsigned grid, unsign
 int64_t attn_order_group(int64_t heads, int64_t bytes);
 // Tiles, units and parts of the keys from the shape and the device alone: a CTA cap changes no bit.
 void attn_fwd_split(AttnFwdArgs* a, int sm_count);
+// The same over pages, whatever their tables have room for.
+void attn_fwd_split_pages(AttnFwdArgs* a, int sm_count);
 // Maps of a block that first tokens share with keys of the window (where there is one).
 bool encode_sink_maps(const AttnShape& s, int r, const void* k, const void* v, CUtensorMap* k_sink,
                       CUtensorMap* v_sink, CUtensorMap* k_rest, CUtensorMap* v_rest);
@@ -270,6 +285,12 @@ cudaError_t attn_fwd_launch(AttnFwdArgs& a, const void* const* q, const void* co
                             const void* const* v, cudaStream_t stream, int device, int64_t cap,
                             int sm_count);
 cudaError_t attn_fwd_status(unsigned* status, bool clear);
+cudaError_t attn_fwd_window_launch(const AttnFwdArgs& a, cudaStream_t stream, int device, int64_t cap,
+                                   int sm_count);
+cudaError_t attn_fwd_window_status(unsigned* status, bool clear);
+cudaError_t attn_fwd_pages_launch(const AttnFwdArgs& a, cudaStream_t stream, int device, int64_t cap,
+                                  int sm_count);
+cudaError_t attn_fwd_pages_status(unsigned* status, bool clear);
 cudaError_t attn_bwd_launch(AttnBwdArgs& a, const void* const* q, const void* const* k,
                             const void* const* v, cudaStream_t stream, int device, int64_t cap,
                             int sm_count);

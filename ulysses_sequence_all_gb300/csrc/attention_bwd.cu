@@ -918,7 +918,7 @@ __device__ __forceinline__ BqUnit<WIN> bq_unit(const AttnBwdArgs& a, int64_t u)
     t.n = int((keys + kAttnRows - 1) / kAttnRows);
     int near = 0;  // the first block (of all keys) that it sees keys of beside the first tokens
     if constexpr (WIN) {
-        t.set(s, max(int64_t(0), min(keys, t.pos0 + t.tok0 + 1 - s.window)));
+        t.set(s, max(int64_t(0), min(keys, t.pos0 + t.tok0 + 1 - s.window)), keys);
         near = t.begin / kAttnRows;
     }
     t.norm = 0.0f;

@@ -789,8 +789,7 @@ static cudaError_t pg_launch_rows(const PagedArgs& a, cudaStream_t stream, int d
 {
     if (a.rows == 8) return pg_launch<DP, F16, 1, 1>(a, stream, device, cap, sm_count);
     if (a.rows == 16) return pg_launch<DP, F16, 2, 1>(a, stream, device, cap, sm_count);
-    if (a.rows == 32) return pg_launch<DP, F16, 2, 2>(a, stream, device, cap, sm_count);
-    return pg_launch<DP, F16, 2, 4>(a, stream, device, cap, sm_count);
+    return pg_launch<DP, F16, 2, 2>(a, stream, device, cap, sm_count);
 }
 
 cudaError_t attn_paged_launch(PagedArgs& a, const void* const* k, const void* const* v,

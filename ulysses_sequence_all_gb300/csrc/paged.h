@@ -14,11 +14,18 @@
 
 namespace uly {
 
-constexpr unsigned kStatusBadPage = 4u;  // a page outside the pool was needed
 constexpr int kPagedTile = 16;           // keys that a warp takes at a time
 constexpr int kPagedWarps = 4;
 constexpr int kPagedBlock = kPagedTile * kPagedWarps;
-constexpr int kPagedMaxRows = 64;        // query rows of one pass over the keys
+constexpr int kPagedMaxRows = 32;        // query rows of one pass over the keys
+// Query rows a key head (group * tokens) up to which attention_paged.cu runs, above them the tensor cores'
+// long layout. Over pages, paged : long in us. 8 caches of 3,000-9,000 tokens, 8 key heads: 16 rows 44 : 70, 32
+// rows 55 : 71, 64 rows (in two passes) 89 : 72; of 30,000: 16 rows 158 : 203, 32 rows 218 : 204; 16 caches of
+// 12,000-32,000, 4 key heads, 32 rows 165 : 192; 32 windows of 4,096, 20 rows 142 : 122, 40 rows 245 : 124.
+constexpr int kPagedFewRows = 32;
+// Over contiguous keys with a window of 4,096, 8 key heads: 4 caches, 4 rows 22.8 : 26.6, 16 rows 28.0 : 26.6,
+// 32 rows 32.1 : 27.6; 32 caches, 4 rows 94 : 106, 32 rows 136 : 106.
+constexpr int kWindowFewRows = 8;
 
 struct AppendArgs {
     const uint8_t* src[2][kMaxW];  // new keys, values: (b, tokens, m_r, d)

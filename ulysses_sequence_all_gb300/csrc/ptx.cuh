@@ -18,6 +18,7 @@ constexpr int kSmemPerCtaMax = 227 * 1024;
 // Bits of the device status word.
 constexpr unsigned kStatusWaitTimeout = 1u;
 constexpr unsigned kStatusDrainTimeout = 2u;
+constexpr unsigned kStatusBadPage = 4u;  // a page outside its pool was needed
 
 // Non-negative a / b (b > 0), in 32-bit arithmetic when both fit, which is the common case.
 __device__ __forceinline__ int64_t div_fast(int64_t a, int64_t b)
