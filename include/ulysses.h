@@ -562,8 +562,8 @@ int ulysses_cache_append(ulysses_plan_t kv_plan, ulysses_plan_t cache_plan, cons
 /*
  * Attention of each batch element's last tokens over its pages: the query at position p sees the keys
  * j < kv_lens[bb] with j <= p and, with a window, j > p - window or j < sinks.
- *   q, o, lse   as ulysses_attention's, q_plan's S queries of each batch element (one, or a few drafted
- *               ones; any number is computed, in passes over the keys of 32 rows = g S / 32 each).
+ *   q, o, lse   as ulysses_attention's, q_plan's S queries of each batch element: one, a few drafted ones, or
+ *               a prompt.
  *   kv_lens     b device int32 (clamped to what the table has room for): the tokens in the cache, those
  *               of this call included (append them first).
  *   q_start     NULL: the queries are the last S tokens, positions kv_lens[bb] - S and on; or b device
@@ -571,12 +571,12 @@ int ulysses_cache_append(ulysses_plan_t kv_plan, ulysses_plan_t cache_plan, cons
  *   window      0: none; else >= 1. Pages that hold neither one of the first `sinks` tokens nor one of the
  *               window are not looked at: they may have been given back.
  *   sinks       >= 0; without a window it has no effect.
- *   workspace   device memory of ulysses_attention_paged_workspace bytes, 16-byte aligned: parts of
- *               sequences that several CTAs share. Its content does not matter and is not kept; two calls
- *               in flight at once need two.
+ *   workspace   device memory of ulysses_attention_paged_workspace bytes (0: may be NULL), 16-byte aligned:
+ *               parts of sequences that several CTAs share. Its content does not matter and is not kept; two
+ *               calls in flight at once need two.
  * Plans: the same W, d (a multiple of 8, at most 128) and dtype (ULY_BF16 or ULY_F16), n_r = g m_r with
  * g <= 64. Empty rows, what keys and values hold where no row sees it, precision, the CTA cap and statuses
- * are as ulysses_attention's; ULY_EALIGN for page_table off 4 bytes. Two launches on `stream`.
+ * are as ulysses_attention's; ULY_EALIGN for page_table off 4 bytes. One or two launches on `stream`.
  */
 int ulysses_attention_paged(ulysses_plan_t q_plan, ulysses_plan_t cache_plan, const void* const* q,
                             const void* const* k_pages, const void* const* v_pages, void* const* o,

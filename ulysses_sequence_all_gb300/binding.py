@@ -527,7 +527,7 @@ def ulysses_attention_paged(q_plan: Plan, cache_plan: Plan, q, k_pages, v_pages,
     sequence a page. page_table: int32 device tensor (b, pages a sequence); kv_lens: int32 device tensor
     of b entries; q_start the same or None (the queries are the last Sq tokens). window 0: none.
     `workspace` is a device tensor of at least ulysses_attention_paged_workspace(q_plan, cache_plan)
-    bytes."""
+    bytes (None where that is 0)."""
     table, pages = _page_table(page_table, q_plan.b)
     _check(_lib().ulysses_attention_paged(
         q_plan, cache_plan, _ptrs(q), _ptrs(k_pages), _ptrs(v_pages), _ptrs(out), _ptrs(lse), table,
@@ -561,7 +561,8 @@ def ulysses_a2a_4d_qk_fused_host(plan: Plan, q_host_in, k_host_in, q_host_out, k
 
 
 def ulysses_device_status() -> int:
-    """Synchronise; return and clear the kernels' device status word (0 = no wait timed out)."""
+    """Synchronise; return and clear the kernels' device status word (0 = no wait timed out and no page of
+    a cache was outside its pool)."""
     st = ctypes.c_uint()
     rc = _lib().ulysses_device_status(ctypes.byref(st))
     if rc not in (ULY_OK, ULY_EDEVICE):

@@ -25,6 +25,11 @@
 // the element type, over the columns they came from, and are A operands there. Warp 18 of the dQ
 // kernel zeroes what a key block holds past a ragged batch element's last key, the one of the dK, dV
 // kernel what rows that see no key hold. Warp 19 works out the units ahead.
+// With a window (WIN), dQ's tiles walk the blocks of their lists of keys (AttnBlocks) and dK, dV's blocks the
+// row tiles whose windows reach them. A first token is seen by every later row: the row tiles of its block
+// are cut into units of their own, whose fp32 sums a last kernel adds in order. Measured: 16,380 tokens x 8
+// heads of 128, window 2,048 and 4 first tokens in 418-432 us (dK, dV 241, dQ 192, statistics 15, the last 5,
+// alone), 0.75-0.77 PFLOP/s; units are 17 steps long, and their ends (7-8 us of 35) are what a long one hides.
 // Roundings: P and dS to the element type (relative errors of half a step each, in sums of either
 // sign), the gradients once; every sum, the statistics and the exponents are fp32.
 #include <cuda_bf16.h>

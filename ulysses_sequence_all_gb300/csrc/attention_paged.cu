@@ -2,7 +2,7 @@
 // in pages (or, without a table, over contiguous keys and values), with or without a sliding window.
 //
 // The query at position p sees the keys j < len with j <= p and (j > p - window or j < sinks). Per row
-// o = sum_j exp(s_j - m) v_j / l and lse = m + log l as in attention_fwd.cu; a row that sees no key
+// o = sum_j exp(s_j - m) v_j / l and lse = m + log l as in attention_fwd.cuh; a row that sees no key
 // gives zeros and -infinity.
 //
 // With R = group * tokens query rows a key head, each 4 d bytes of a key and its value carry 4 d R
@@ -16,11 +16,17 @@
 // leaves its parts as normalised fp32 outputs with their lse, which attn_paged_join_kernel adds in order:
 // the same bits from run to run.
 //
+// Measured (bf16, copy peak 6,767 GB/s): one token each on 16 caches of 12,000-32,768 tokens, 32 heads over 4 of
+// 128 in 118-120 us (0.88-0.90 of the peak), on 256 of 100-2,000, 64 heads over 8, in 171-172 us (0.89), with a
+// window of 4,096 on 32 sequences, 40 heads over 8, in 94-96 us (0.83); four drafted tokens on 8 caches of
+// 3,000-9,000 in 44-46 us (0.58), one short cache in 10.3 us: about 10 us of each are the launches, the first
+// copies' chain of loads (lengths, table, map, keys) and the last join. With 32 rows the products bound it.
+//
 // Products: S^T = K Q^T and O^T += V^T P^T with keys (and columns of V) as the 16 rows of an
 // m16n8k16 product, so that a tile of 8 query rows costs no more than its own work. A product of this
 // size reads its fragments straight from the tiles that the copies left and keeps its sums in
-// registers: at R = 8 the products take a tenth of the time that the copies take, and the fifth
-// generation's 128 rows and the trip through tensor memory would buy nothing. P^T's fragments are S^T's
+// registers; the fifth generation's 128 rows and the trip through tensor memory take longer up to 16 or 32 rows
+// (kPagedFewRows). P^T's fragments are S^T's
 // transposed, 8x8 blocks at a time.
 // P is rounded to the element type (fp16: times 2^7, so that many keys of little weight are not lost),
 // relative to a maximum that may lag by 2^8; maxima, sums and outputs are fp32.
