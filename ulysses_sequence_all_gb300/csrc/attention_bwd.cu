@@ -471,7 +471,10 @@ __global__ void __launch_bounds__(kAbThreads, 1)
     const int nk = (s.d + 15) / 16, halves = (s.d + 63) / 64;
     const AttnOrder& order = WIN ? a.kv_units : a.kv_order;
     const int64_t units = order.heads * order.blocks;
-    const bool cleans = WIN || s.q_start;  // warp 18 has tiles to look at
+    // Rows may see no key, and warp 18 has tiles to look at: a start before the first key; with a window and no
+    // first tokens, one that begins past the last key.
+    const bool cleans =
+        s.q_start || (WIN && s.sinks == 0 && (s.kv_lens || s.Skv + s.window - 1 < s.Sq));
     constexpr int K = L::kStages;
 
     if (threadIdx.x == 0) {
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(kAbThreads, 1)
             auto next_s = [&](bool first, bool last, uint32_t use, const Unit& u, int64_t tile) {
                 if (first) wait(&bars.k_full, use & 1);
                 if (!wait(&bars.q_full[ring.s], ring.phase)) return;
-                if ((WIN || (first && s.q_start)) && bk_unclean<WIN>(a, u, tile)) {
+                if (cleans && (WIN || first) && bk_unclean<WIN>(a, u, tile)) {
                     if (!wait(&bars.clean[ring.s], (cleaned >> ring.s) & 1)) return;
                     cleaned ^= 1u << ring.s;
                 }
