@@ -68,7 +68,7 @@ struct PagedEntry {
     int snk, lo, end;   // some row sees key j: j < snk, or lo <= j < end
     int len;
     int64_t pos0;       // position of query token 0
-    int64_t t0, t1;     // its tokens
+    int t0, t1;         // its tokens
     __device__ __forceinline__ int block(int j) const { return j < first ? j : near + j - first; }
     __device__ __forceinline__ bool sees(int a, int b) const  // any of keys a .. b - 1
     {
@@ -83,9 +83,9 @@ __device__ __forceinline__ PagedEntry paged_entry(const PagedArgs& a, int e)
     t.rg = e - t.bb * a.row_groups;
     t.len = a.kv_lens ? max(0, min(a.kv_lens[t.bb], a.room)) : a.room;
     t.pos0 = a.q_start ? int64_t(a.q_start[t.bb]) : a.from_end ? t.len - a.Sq : 0;
-    const int64_t row = int64_t(t.rg) * a.rows, rows = a.Sq * a.group;
-    t.t0 = div_fast(row, a.group);
-    t.t1 = div_fast(min(row + a.rows, rows) - 1, a.group) + 1;
+    const int row = t.rg * a.rows, rows = int(a.Sq) * a.group;  // (fewer than 2^27)
+    t.t0 = int(uint32_t(row) / uint32_t(a.group));
+    t.t1 = int(uint32_t(min(row + a.rows, rows) - 1) / uint32_t(a.group)) + 1;
     t.end = int(max(int64_t(0), min(int64_t(t.len), t.pos0 + t.t1)));
     t.lo = int(max(int64_t(0), min(int64_t(t.end), t.pos0 + t.t0 + 1 - a.window)));
     t.snk = min(a.sinks, t.lo);
@@ -371,15 +371,15 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         auto queries = [&]() {
             int r, kvh;
             place(&r, &kvh);
-            const int64_t row0 = int64_t(walk.en.rg) * kRows + (warp % RH) * kMine, row_end = a.Sq * a.group;
-            auto query = [&](int64_t row) {  // its first byte
-                const int64_t tok = div_fast(row, a.group);
+            const int row0 = walk.en.rg * kRows + (warp % RH) * kMine, row_end = int(a.Sq) * a.group;
+            auto query = [&](int row) {  // its first byte
+                const int tok = int(uint32_t(row) / uint32_t(a.group));
                 return a.q[r] + ((int64_t(walk.en.bb) * a.Sq + tok) * a.n[r] + kvh * a.group + row -
                                  tok * a.group) * a.d * 2;
             };
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const int64_t row = row0 + t * 8 + quad;
+                const int row = row0 + t * 8 + quad;
                 const uint8_t* src = query(row) + pair * 2;
 #pragma unroll
                 for (int ks = 0; ks < kD; ++ks)
@@ -400,8 +400,9 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             const int head = walk.head, from = walk.j, to_block = walk.stop();
             const int64_t place = int64_t(walk.e) * heads + head;
             const int64_t at_end = stop - walk.left + kPgEnd + en.n;  // where the sequence ends in the work
-            const int64_t pass0 = int64_t(en.rg) * kRows, row_end = a.Sq * a.group;
-            const int64_t row0 = pass0 + (warp % RH) * kMine;
+            // (fewer than 2^27 rows; no 64-bit divisions: see the join)
+            const int pass0 = en.rg * kRows, row_end = int(a.Sq) * a.group;
+            const int row0 = pass0 + (warp % RH) * kMine;
             // keys that every row sees: below hi_all, and from lo_all on or first tokens
             const int hi_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t0 + 1)));
             const int lo_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t1 - a.window)));
@@ -473,9 +474,11 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                             for (int t = 0; t < RT; ++t)
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
-                                    const int64_t row = row0 + t * 8 + pair + i;
-                                    const int64_t p = en.pos0 + div_fast(row, a.group);
-                                    const int64_t hi = min(int64_t(en.len), p + 1), lo = p + 1 - a.window;
+                                    const int row = row0 + t * 8 + pair + i;
+                                    const int64_t p = en.pos0 + int(uint32_t(row) / uint32_t(a.group));
+                                    const int hi = int(max(int64_t(0), min(int64_t(en.len), p + 1)));
+                                    const int lo =
+                                        int(max(int64_t(0), min(int64_t(en.len), p + 1 - a.window)));
 #pragma unroll
                                     for (int x = 0; x < 2; ++x) {
                                         const int key = key0 + quad + 8 * x;
@@ -591,10 +594,13 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                             *out_at(warp, t * 8 + pair + (x & 1), i * 16 + (x >> 1) * 8 + quad) = o[t][i][x];
             }
             pg_sync();
+            // (rolled, and with 32-bit divisions: what the products' loop and a sequence's end do not both fit of
+            // the instruction cache is fetched again at every end)
+#pragma unroll 1
             for (int it = threadIdx.x; it < kRows * (DP / 8); it += 32 * kPagedWarps) {
                 const int row = it / (DP / 8), col = it % (DP / 8) * 8;
                 const int rh = row / kMine, in = row - rh * kMine;  // the warps' group, the row in it
-                const int64_t to = pass0 + row;
+                const int to = pass0 + row;
                 if (col >= a.d) continue;
                 float top = -INFINITY, sum = 0.0f, y[8];
 #pragma unroll
@@ -628,8 +634,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                     dst[1] = make_float4(y[4], y[5], y[6], y[7]);
                     if (col == 0) a.part_lse[at_row] = lse;
                 } else if (to < row_end) {
-                    const int64_t tok = div_fast(to, a.group);
-                    const int64_t h = kvh * a.group + (to - tok * a.group);
+                    const int tok = int(uint32_t(to) / uint32_t(a.group));
+                    const int h = kvh * a.group + (to - tok * a.group);
                     st_v4(a.o[r] + (((int64_t(en.bb) * a.Sq + tok) * a.n[r] + h) * a.d + col) * 2,
                           make_uint4(E::pack(y[0], y[1]), E::pack(y[2], y[3]), E::pack(y[4], y[5]),
                                      E::pack(y[6], y[7])));
