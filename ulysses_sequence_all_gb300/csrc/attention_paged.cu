@@ -355,7 +355,6 @@ __global__ void __launch_bounds__(kPgThreads, 2)
 
     // the products
     regs_grow<kPgRegsProducts<DP, RT>>();
-    const int nk = (a.d + 15) / 16;
     const float sl2 = a.scale * 1.4426950408889634f;
     const int quad = lane >> 2, pair = (lane & 3) * 2;  // fragments: key (column of V); query row
     for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
@@ -445,7 +444,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                             fence_proxy_async_shared();  // (before the next copy into this stage)
                             __syncwarp();
                         }
-                        // S^T, in two sums (a sum of eight products waits for each of them)
+                        // S^T, in two sums (a sum of eight products waits for each of them). Columns past d are
+                        // zeros in the copies and in q: all DP are taken, with no branch between the products.
                         float s[RT][4], s2[RT][4];
 #pragma unroll
                         for (int t = 0; t < RT; ++t)
@@ -456,7 +456,6 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                             const int k = ((lane >> 3) & 1) * 8 + (lane & 7), w = lane >> 4;
 #pragma unroll
                             for (int ks = 0; ks < kD; ++ks) {
-                                if (ks >= nk) break;
                                 uint32_t x[4];
                                 pg_ldmatrix<false>(x, keys_at + (ks >> 2) * L::kHalf + k * 128 +
                                                           ((((ks & 3) * 2 + w) ^ (k & 7)) << 4));
@@ -535,7 +534,6 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                             const uint32_t v_at = keys_at + L::kV + k * 128;
 #pragma unroll
                             for (int i = 0; i < kD; ++i) {
-                                if (i >= nk) break;
                                 uint32_t x[4];
                                 pg_ldmatrix<true>(x, v_at + (i >> 2) * L::kHalf +
                                                          ((((i & 3) * 2 + w) ^ (k & 7)) << 4));
