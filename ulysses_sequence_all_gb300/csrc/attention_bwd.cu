@@ -28,8 +28,8 @@
 // With a window (WIN), dQ's tiles walk the blocks of their lists of keys (AttnBlocks) and dK, dV's blocks the
 // row tiles whose windows reach them. A first token is seen by every later row: the row tiles of its block
 // are cut into units of their own, whose fp32 sums a last kernel adds in order. Measured: 16,380 tokens x 8
-// heads of 128, window 2,048 and 4 first tokens in 418-432 us (dK, dV 241, dQ 192, statistics 15, the last 5,
-// alone), 0.75-0.77 PFLOP/s; units are 17 steps long, and their ends (7-8 us of 35) are what a long one hides.
+// heads of 128, window 2,048 and 4 first tokens in 413-432 us (dK, dV 241, dQ 192, statistics 15, the last 5,
+// alone), 0.75-0.78 PFLOP/s; units are 17 steps long, and their ends (7-8 us of 35) are what a long one hides.
 // Roundings: P and dS to the element type (relative errors of half a step each, in sums of either
 // sign), the gradients once; every sum, the statistics and the exponents are fp32.
 #include <cuda_bf16.h>

@@ -40,8 +40,8 @@
 // are those of its list of keys (AttnBlocks): the first tokens, then from its first row's window on, whatever
 // key that is; blocks without an edge of any row's are not masked. Bound as above, each unit's start and end
 // (about 4 us) weighing more the shorter its list is. Measured: 75,600 tokens x 8 heads of 128, window 10,800
-// and 3,600 first tokens in 2.49-2.62 ms, 1.54-1.62 PFLOP/s; 2 x 4,095 tokens, 32 heads over 8, window 1,024
-// and 4 first tokens in 0.117-0.131 ms, of whose cycles the tensor pipe is busy in 43 %.
+// and 3,600 first tokens in 2.45-2.62 ms, 1.54-1.64 PFLOP/s; 2 x 4,095 tokens, 32 heads over 8, window 1,024
+// and 4 first tokens in 0.117-0.133 ms, of whose cycles the tensor pipe is busy in 43 %.
 // Over pages (PAGED) the loading warp's lanes copy a page's rows each, its place in the table looked up a block
 // ahead; list rows that no row sees are copied from beyond the pool, which gives zeros. Measured: 8 caches of
 // 30,000 tokens, 8 key heads, 64 rows each in 205 us (0.71 of the copy peak), pages of 32 tokens.

@@ -17,10 +17,10 @@
 // the same bits from run to run.
 //
 // Measured (bf16, copy peak 6,767 GB/s): one token each on 16 caches of 12,000-32,768 tokens, 32 heads over 4 of
-// 128 in 118-120 us (0.88-0.90 of the peak), on 256 of 100-2,000, 64 heads over 8, in 171-172 us (0.89), with a
-// window of 4,096 on 32 sequences, 40 heads over 8, in 94-96 us (0.83); four drafted tokens on 8 caches of
-// 3,000-9,000 in 44-46 us (0.58), one short cache in 10.3 us: about 10 us of each are the launches, the first
-// copies' chain of loads (lengths, table, map, keys) and the last join. With 32 rows the products bound it.
+// 128 in 116 us (0.92 of the peak), on 256 of 100-2,000, 64 heads over 8, in 169 us (0.90), with a window of
+// 4,096 on 32 sequences, 40 heads over 8, in 93 us (0.85); four drafted tokens on 8 caches of 3,000-9,000 in
+// 42 us (0.62), one short cache in 9.8 us: about 10 us of each are the launches, the first copies' chain of
+// loads (lengths, table, map, keys) and the last join. 32 rows on the 16 caches take 124 us.
 //
 // Products: S^T = K Q^T and O^T += V^T P^T with keys (and columns of V) as the 16 rows of an
 // m16n8k16 product, so that a tile of 8 query rows costs no more than its own work. A product of this
@@ -50,7 +50,7 @@ static __device__ unsigned g_attn_paged_status;
 constexpr int kPgThreads = 2 * 32 * kPagedWarps;  // warps 0-3, and a warpgroup with the copying one
 // Registers a thread: 256 x 128 at launch = 128 x this + 128 x (256 - this), what the roles take
 template <int DP, int RT>
-constexpr int kPgRegsProducts = DP == 128 && RT == 2 ? 192 : 176;
+constexpr int kPgRegsProducts = DP == 128 ? (RT == 2 ? 200 : 184) : 176;
 constexpr float kPgRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 constexpr float kPgUpF16 = 7.0f;    // fp16 probabilities are held times 2^this
 constexpr int kPgJoinThreads = 256, kPgJoinParts = 8;
