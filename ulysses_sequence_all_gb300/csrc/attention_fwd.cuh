@@ -330,6 +330,12 @@ __device__ __forceinline__ bool af_unclean(const AttnShape& s, const AfUnit<WIN>
     return af_past(s, t, block) < kAttnRows;
 }
 
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t below(int n)
+{
+    return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 // PAGED: the keys lie in pages (with a window, that may be none).
 template <int DP, bool F16, int MODE, bool WIN, bool PAGED>
 __global__ void __launch_bounds__(kAfThreads, 1)
@@ -764,17 +770,21 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 for (int q = 0; q < 4; ++q) tmem_ld32(s_at + q * 32, x[q]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_wait_ld(x[q]);
-                if (WIN && j < edge) {  // between the first tokens and the row's window
+                if constexpr (WIN) {
+                    // keys in view: below the row's last, but those between the first tokens and its window
                     const int from = sinks - j * kAttnRows, to = low - j * kAttnRows;
-                    if (from < kAttnRows) {
+                    const bool begins = j < edge && from < kAttnRows;
+                    if (__any_sync(0xffffffffu, left < kAttnRows) || begins) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t see = below(left - q * 32);
+                            if (begins) see &= below(from - q * 32) | ~below(to - q * 32);
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                if (q * 32 + c >= from && q * 32 + c < to) x[q][c] = 0xFF800000u;
+                                if (!(see >> c & 1u)) x[q][c] = 0xFF800000u;  // -infinity
+                        }
                     }
-                }
-                if (__any_sync(0xffffffffu, left < kAttnRows)) {
+                } else if (__any_sync(0xffffffffu, left < kAttnRows)) {
                     const int seen = max(0, left);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
