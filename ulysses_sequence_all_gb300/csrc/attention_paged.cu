@@ -19,8 +19,8 @@
 // Measured (bf16, copy peak 6,767 GB/s): one token each on 16 caches of 12,000-32,768 tokens, 32 heads over 4 of
 // 128 in 116 us (0.92 of the peak), on 256 of 100-2,000, 64 heads over 8, in 169 us (0.90), with a window of
 // 4,096 on 32 sequences, 40 heads over 8, in 93 us (0.85); four drafted tokens on 8 caches of 3,000-9,000 in
-// 42 us (0.62), one short cache in 9.8 us: about 10 us of each are the launches, the first copies' chain of
-// loads (lengths, table, map, keys) and the last join. 32 rows on the 16 caches take 124 us.
+// 39 us (0.65), one short cache in 9.8 us: about 10 us of each are the launches, the first copies' chain of
+// loads (lengths, table, map, keys) and the last join. 32 rows on the 16 caches take 120 us.
 //
 // Products: S^T = K Q^T and O^T += V^T P^T with keys (and columns of V) as the 16 rows of an
 // m16n8k16 product, so that a tile of 8 query rows costs no more than its own work. A product of this
@@ -54,9 +54,12 @@ constexpr int kPgRegsProducts = DP == 128 ? (RT == 2 ? 200 : 184) : 176;
 constexpr float kPgRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 constexpr float kPgUpF16 = 7.0f;    // fp16 probabilities are held times 2^this
 constexpr int kPgJoinThreads = 256, kPgJoinParts = 8;
-// What a sequence's end (its join, the next one's queries) costs a CTA, in blocks of keys. 0, 1, 2, 3: one
-// token on 256 sequences of 100-2,000 keys 191, 173, 172, 174 us; of 100-200 keys 58, 56, 54, 54 us.
-constexpr int kPgEnd = 2;
+// What a sequence's end (its join, the next one's queries) costs a CTA, in blocks of keys, by the query rows of
+// a pass. 1, 2, 3 with 8 rows: one token on 256 sequences of 100-2,000 keys 166, 170, 171 us, of 100-200 keys 47,
+// 46, 46, on 8 of 3,000-9,000 38, 37, 37 (0: the first two 191 and 58 when the end was slower). 2, 3, 4, 7 with 16
+// rows on the first 186, 187, 192, 199, four tokens on the last 41, 39, 39, 39; 3, 4, 5, 7 with 32 rows on the first
+// 228, 217, 218, 225.
+constexpr int pg_end(int rows) { return rows <= 8 ? 2 : rows <= 16 ? 3 : 4; }
 
 // ---- what there is to do ----------------------------------------------------------------------------
 
@@ -101,21 +104,21 @@ struct PagedWalk {
     int64_t left;  // of the share, from the sequence's beginning (its end included) on
     int e, head, j;
     PagedEntry en;
-    __device__ __forceinline__ bool more() const { return left > j + kPgEnd; }
+    __device__ __forceinline__ bool more(const PagedArgs& a) const { return left > j + a.end; }
     // blocks of the sequence that are the share's: j .. stop() - 1
-    __device__ __forceinline__ int stop() const { return int(min(int64_t(en.n), left - kPgEnd)); }
+    __device__ __forceinline__ int stop(const PagedArgs& a) const { return int(min(int64_t(en.n), left - a.end)); }
     __device__ __forceinline__ void step(const PagedArgs& a)
     {
         if (++j < en.n) return;
         j = 0;
-        left -= en.n + kPgEnd;
+        left -= en.n + a.end;
         if (++head < a.m_begin[a.W]) return;
         head = 0;
-        if (more()) en = paged_entry(a, ++e);
+        if (more(a)) en = paged_entry(a, ++e);
     }
 };
 
-// The work is measured in blocks, a sequence (of one row group and head) of n as kPgEnd + n, its end first:
+// The work is measured in blocks, a sequence (of one row group and head) of n as `end` + n, its end first:
 // equal shares of that are equal times, however short the sequences are. A share that begins inside an end
 // begins with the sequence.
 __device__ __forceinline__ int64_t paged_share(int64_t total, int parts, int64_t c)  // where it begins
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     const int each = (entries + kPgThreads - 1) / kPgThreads;
     const int e0 = min(entries, int(threadIdx.x) * each), e1 = min(entries, e0 + each);
     int64_t mine = 0;
-    for (int e = e0; e < e1; ++e) mine += paged_entry(a, e).n + kPgEnd;
+    for (int e = e0; e < e1; ++e) mine += paged_entry(a, e).n + a.end;
     int64_t upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         if (begin >= (upto - mine) * heads && begin < upto * heads) {
             int64_t at = upto - mine;
             int e = e0;
-            for (int n; begin >= (at + (n = paged_entry(a, e).n + kPgEnd)) * heads; ++e) at += n;
+            for (int n; begin >= (at + (n = paged_entry(a, e).n + a.end)) * heads; ++e) at += n;
             sh.entry = e;
             sh.before = at;
         }
@@ -272,9 +275,9 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             walk.e = sh.entry;
             walk.en = paged_entry(a, walk.e);
             const int64_t off = begin - sh.before * heads;
-            walk.head = int(div_fast(off, walk.en.n + kPgEnd));
-            const int x = int(off - int64_t(walk.head) * (walk.en.n + kPgEnd));
-            walk.j = max(0, x - kPgEnd);
+            walk.head = int(div_fast(off, walk.en.n + a.end));
+            const int x = int(off - int64_t(walk.head) * (walk.en.n + a.end));
+            walk.j = max(0, x - a.end);
             walk.left = stop - begin + x;
         }
     };
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             bool live = false;             // a block is in hand
             auto look = [&]() {            // the walk's next block that any row sees anything of
                 live = false;
-                while (walk.more()) {
+                while (walk.more(a)) {
                     const int key0 = walk.en.block(walk.j) * kPagedBlock;
                     live = walk.en.sees(key0, key0 + kPagedBlock);
                     if (live) {
@@ -391,14 +394,14 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                     }
             }
         };
-        if (walk.more()) queries();
-        while (walk.more()) {
+        if (walk.more(a)) queries();
+        while (walk.more(a)) {
             const PagedEntry en = walk.en;
             int r, kvh;
             place(&r, &kvh);
-            const int head = walk.head, from = walk.j, to_block = walk.stop();
+            const int head = walk.head, from = walk.j, to_block = walk.stop(a);
             const int64_t place = int64_t(walk.e) * heads + head;
-            const int64_t at_end = stop - walk.left + kPgEnd + en.n;  // where the sequence ends in the work
+            const int64_t at_end = stop - walk.left + a.end + en.n;  // where the sequence ends in the work
             // (fewer than 2^27 rows; no 64-bit divisions: see the join)
             const int pass0 = en.rg * kRows, row_end = int(a.Sq) * a.group;
             const int row0 = pass0 + (warp % RH) * kMine;
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             }
             walk.j = to_block - 1;
             walk.step(a);
-            if (walk.more()) queries();  // (they arrive during the join)
+            if (walk.more(a)) queries();  // (they arrive during the join)
 
             // Join the warps: a row's maximum, sum and output.
             const bool whole = from == 0 && to_block == en.n;
@@ -753,6 +756,7 @@ void attn_paged_split(PagedArgs* a, int sm_count)
     while (a->rows < kPagedMaxRows && a->rows < rows) a->rows *= 2;
     a->row_groups = int32_t((rows + a->rows - 1) / a->rows);
     a->parts = 2 * sm_count;
+    a->end = pg_end(a->rows);
     const int64_t groups = int64_t(a->b) * a->row_groups * a->m_begin[a->W];
     a->by_group = groups <= a->parts;
     a->notes = int32_t(a->by_group ? groups : a->parts);

@@ -61,6 +61,7 @@ struct PagedArgs {
     int64_t window;          // beyond every position where there is none
     int32_t rows, row_groups;  // query rows of a pass (8, 16, 32, 64); passes of a key head
     int32_t parts;             // shares of all the work, one CTA at a time works on one
+    int32_t end;               // blocks that a sequence's end counts for in them
     int32_t by_group, notes;   // `shared` has an entry for each row group and head, or for each share
     float scale;
     uint32_t wait_us;
