@@ -97,7 +97,7 @@ constexpr int kAfS = 0, kAfO = 256;
 enum AfMode { kAfLong = 0, kAfShort = 1, kAfPaired = 2, kAfToken = 3 };
 constexpr int kAfTokenRows = 32;
 
-template <int DP, int MODE>
+template <int DP, int MODE, bool WIN>
 struct AfSmem {
     static constexpr int kTile = kAttnRows * DP * 2;  // a tile of 128 rows; a block of 128 keys
     static constexpr int kHalf = kAttnRows * 128;     // its part of 64 columns
@@ -114,7 +114,9 @@ struct AfSmem {
     // Units known at a time: a few, so that the next one's copies start early; single tokens the one
     // at work and the next, so that CTAs do not pile up what others could take (with four, 576 units
     // on 152 CTAs ended between 26 and 129 us).
-    static constexpr int kUnitSlots = kPaired ? 2 : kAfMaxUnitSlots;
+    // (two at least: the softmax threads hold a record until their unit's end, and the products ask for the
+    // next one before. Short windowed units too: the prompt of window 2,048 156 us with two, 158.5 with four.)
+    static constexpr int kUnitSlots = kPaired || WIN ? 2 : kAfMaxUnitSlots;
     static constexpr int kQ = kAfBarBytes;  // barriers first
     static constexpr int kRing = kQ + kSlots * kSlot;
     static constexpr int kTotal = kRing + kStages * kTile;
@@ -341,7 +343,7 @@ template <int DP, bool F16, int MODE, bool WIN, bool PAGED>
 __global__ void __launch_bounds__(kAfThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnFwdArgs a)
 {
-    using L = AfSmem<DP, MODE>;
+    using L = AfSmem<DP, MODE, WIN>;
     using E = ElemT<F16>;
     constexpr int K = L::kStages, Q = L::kSlots;
     constexpr bool PAIRED = L::kPaired;
@@ -988,7 +990,7 @@ static cudaError_t af_launch_mode(const AttnFwdArgs& a, cudaStream_t stream, int
 {
     static std::atomic<unsigned long long> raised{0};
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
-    constexpr int smem = AfSmem<DP, MODE>::kTotal + 1024;
+    constexpr int smem = AfSmem<DP, MODE, WIN>::kTotal + 1024;
     if (bit && !(raised.load() & bit)) {
         cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, F16, MODE, WIN, PAGED>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
