@@ -19,9 +19,9 @@ constexpr int kPagedWarps = 4;
 constexpr int kPagedBlock = kPagedTile * kPagedWarps;
 constexpr int kPagedMaxRows = 32;        // query rows of one pass over the keys
 // Query rows a key head (group * tokens) up to which attention_paged.cu runs, above them the tensor cores'
-// long layout. Over pages, paged : long in us, 32 rows: 8 caches of 3,000-9,000 tokens, 8 key heads 45 : 70;
-// 16 of 12,000-32,000, 4 key heads 123 : 191; 256 of 100-2,000, 8 key heads 247 : 354; 32 windows of 4,096, 20 rows
-// 109 : 123. 64 rows (four warps with 16 each, keys read once): 67 : 71, 203 : 193, 381 : 353, 176 : 124.
+// long layout. Over pages, paged : long in us, 32 rows: 8 caches of 3,000-9,000 tokens, 8 key heads 43 : 70;
+// 16 of 12,000-32,000, 4 key heads 120 : 191; 256 of 100-2,000, 8 key heads 217 : 354; 32 windows of 4,096, 20 rows
+// 106 : 123. 64 rows (four warps with 16 each, keys read once): 67 : 71, 203 : 193, 381 : 353, 176 : 124.
 constexpr int kPagedFewRows = 32;
 // Over contiguous keys with a window of 4,096, 8 key heads: 4 caches, 4 rows 22.8 : 26.6, 16 rows 25.8 : 26.7,
 // 32 rows 28.6 : 27.8; 32 caches, 4 rows 94 : 106, 32 rows 105.5 : 104.9.
