@@ -265,7 +265,8 @@ def prepare(case, seed):
     if op == "window_backward":
         # the forward's outputs, which a training step keeps for the backward
         o, lse = _plain_window(st)
-        st["o"], st["lse"] = o, lse
+        # (a tensor each: a rank's rows of one tensor need not begin at a 16-byte boundary)
+        st["o"], st["lse"] = o, [x.clone() for x in lse]
         st["go"] = [gen.randn(b, c["q_tokens"], n, d) for n in qn]
     if own:
         from ulysses_sequence_all_gb300 import binding as B
