@@ -611,7 +611,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
 #pragma unroll
                 for (int w = 0; w < kPagedWarps; w += RH) {
                     const float2 z = sh.ml[w + rh][in];
-                    if (!sh.used[w + rh] || stage < 0 || z.x == -INFINITY) continue;
+                    // (scores that were all NaN leave the maximum at minus infinity, but not the sum at 0)
+                    if (!sh.used[w + rh] || stage < 0 || (z.x == -INFINITY && z.y == 0.0f)) continue;
                     const float f = ex2((z.x - top) * sl2);
                     sum = fmaf(f, z.y, sum);
 #pragma unroll
