@@ -426,7 +426,10 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             auto look = [&](const Unit& t, int at) {
                 if constexpr (PAGED) {
                     const int v = at * kAttnRows + lane * a.pages.box, key = t.key(v);
-                    needed = lane * a.pages.box < kAttnRows && key < (v < t.pad ? s.sinks : t.len);
+                    // (a list from key 0 on holds keys between the first tokens and the unit's first window)
+                    const int64_t first = t.pos0 + int64_t(t.tok0) + 1 - s.window;
+                    needed = lane * a.pages.box < kAttnRows && key < (v < t.pad ? s.sinks : t.len) &&
+                             (key < s.sinks || int64_t(key) + a.pages.box > first);
                     page = a.pages.pages;  // beyond the pool a copy writes zeros
                     row = 0;
                     if (needed) {
