@@ -642,9 +642,9 @@ int ulysses_selftest_wait_timeout(unsigned limit_us, void* stream);
 /*
  * Self-test of the attention kernels' failure path: calls that this process makes from now on have a
  * limit of limit_us microseconds (0 .. 2,000,000, the default) on a wait in which nothing moves; with 0
- * a wait gives up at its second look, some ten microseconds in, so that any call with long units gives
- * up at once: its kernels set the timeout bit (1) of the device status word, leave outputs unwritten and
- * return normally. Set it back to 2,000,000 afterwards.
+ * a wait gives up at its second look, some ten microseconds in (few rows over pages or with a window: at its
+ * first), so that any call with long units gives up at once: its kernels set the timeout bit (1) of the device
+ * status word, leave outputs unwritten or incomplete and return normally. Set it back to 2,000,000 afterwards.
  */
 int ulysses_selftest_attention_wait_limit(unsigned limit_us);
 
