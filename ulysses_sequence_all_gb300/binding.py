@@ -241,6 +241,11 @@ class Plan:
 
 
 def ulysses_plan(W: int, b: int, seq_splits, head_splits, d: int, dtype: str) -> Plan:
+    """A plan of W ranks: seq_splits and head_splits have W entries each."""
+    seq_splits, head_splits = list(seq_splits), list(head_splits)
+    for splits, what in ((seq_splits, "seq_splits"), (head_splits, "head_splits")):
+        if len(splits) != W:  # (a ctypes array would fill up a short list with zeros)
+            raise ValueError(f"{what}: {len(splits)} entries for W = {W} ranks")
     out = ctypes.c_void_p()
     code = DTYPE_CODES.get(dtype, dtype if isinstance(dtype, int) else -1)
     _check(_lib().ulysses_plan(W, b, (_i64 * W)(*seq_splits), (_i64 * W)(*head_splits), d, code,
