@@ -197,15 +197,29 @@ def _page_table(x, b: int) -> tuple[int, int]:
 _PTR_ARRAYS: dict = {}  # the ctypes array type of each length (making one costs as much as filling it)
 
 
-def _ptrs(xs: Sequence) -> ctypes.Array:
-    n = len(xs)
+def _ptr_array(n: int):
     array = _PTR_ARRAYS.get(n)
     if array is None:
         array = _PTR_ARRAYS[n] = ctypes.c_void_p * n
-    try:
-        return array(*[x.data_ptr() for x in xs])
-    except AttributeError:  # addresses, or None, among them
-        return array(*[_addr(x) for x in xs])
+    return array
+
+
+def _ptrs(xs: Sequence) -> ctypes.Array:
+    return _ptr_array(len(xs))(*[_addr(x) for x in xs])
+
+
+def _rank_ptrs(plan: "Plan", *lists: Sequence, planes: int = 1) -> list:
+    """Addresses of lists of tensors, one for each of the plan's ranks (of a packed call: and plane)."""
+    n = max(planes, 0) * plan.W
+    array, out = _ptr_array(n), []
+    for xs in lists:
+        if len(xs) < n:  # (the library would read on past the array)
+            raise ValueError(f"{len(xs)} tensors for {n}: one for each of the plan's ranks")
+        try:
+            out.append(array(*[x.data_ptr() for x in xs]))
+        except (AttributeError, IndexError):  # addresses, or None, among them; more of them than ranks
+            out.append(_ptrs(xs))
+    return out
 
 
 def _stream(stream) -> int:
@@ -346,28 +360,28 @@ def ulysses_plan_rank_segments(plan: Plan, mode: int, rank: int) -> list:
 
 
 def ulysses_a2a_4d(plan: Plan, mode: int, ins: Sequence, outs: Sequence, stream=None):
-    _check(_lib().ulysses_a2a_4d(plan, mode, _ptrs(ins), _ptrs(outs), _stream(stream)),
+    _check(_lib().ulysses_a2a_4d(plan, mode, *_rank_ptrs(plan, ins, outs), _stream(stream)),
            "ulysses_a2a_4d")
 
 
 def ulysses_a2a_4d_engine(plan: Plan, mode: int, engine: int, ins: Sequence, outs: Sequence,
                           stream=None):
-    _check(_lib().ulysses_a2a_4d_engine(plan, mode, engine, _ptrs(ins), _ptrs(outs), _stream(stream)),
+    _check(_lib().ulysses_a2a_4d_engine(plan, mode, engine, *_rank_ptrs(plan, ins, outs), _stream(stream)),
            "ulysses_a2a_4d_engine")
 
 
 def ulysses_a2a_4d_qk_fused(plan: Plan, q_in, k_in, q_out, k_out, rms_w, eps: float,
                             rope_theta: float, stream=None):
-    _check(_lib().ulysses_a2a_4d_qk_fused(plan, _ptrs(q_in), _ptrs(k_in), _ptrs(q_out), _ptrs(k_out),
+    _check(_lib().ulysses_a2a_4d_qk_fused(plan, *_rank_ptrs(plan, q_in, k_in, q_out, k_out),
                                           _addr(rms_w), eps, rope_theta, _stream(stream)),
            "ulysses_a2a_4d_qk_fused")
 
 
 def ulysses_a2a_4d_qkv_fused(plan: Plan, qkv_in, q_out, k_out, v_out, rms_w, eps: float,
                              rope_theta: float, stream=None):
-    _check(_lib().ulysses_a2a_4d_qkv_fused(plan, _ptrs(qkv_in), _ptrs(q_out), _ptrs(k_out),
-                                           _ptrs(v_out), _addr(rms_w), eps, rope_theta,
-                                           _stream(stream)), "ulysses_a2a_4d_qkv_fused")
+    _check(_lib().ulysses_a2a_4d_qkv_fused(plan, *_rank_ptrs(plan, qkv_in, q_out, k_out, v_out),
+                                           _addr(rms_w), eps, rope_theta, _stream(stream)),
+           "ulysses_a2a_4d_qkv_fused")
 
 
 def ulysses_a2a_4d_packed_fused(plan: Plan, planes: int, q_plane: int, k_plane: int,
@@ -376,7 +390,8 @@ def ulysses_a2a_4d_packed_fused(plan: Plan, planes: int, q_plane: int, k_plane: 
     """outs: one sequence of W output tensors per plane (planes lists), flattened plane-major."""
     flat = [t for plane in outs for t in plane]
     _check(_lib().ulysses_a2a_4d_packed_fused(plan, planes, q_plane, k_plane, token_pitch,
-                                              _ptrs(packed_in), _ptrs(flat), _addr(rms_w), eps,
+                                              *_rank_ptrs(plan, packed_in),
+                                              *_rank_ptrs(plan, flat, planes=planes), _addr(rms_w), eps,
                                               rope_theta, _stream(stream)),
            "ulysses_a2a_4d_packed_fused")
 
@@ -394,7 +409,7 @@ def ulysses_a2a_4d_qk_fused_backward(plan: Plan, dq_out, dk_out, q_in, k_in, dq_
     """Backward of the fused call. `workspace` is a device tensor of at least
     ulysses_qk_fused_backward_workspace(plan) bytes."""
     _check(_lib().ulysses_a2a_4d_qk_fused_backward(
-        plan, _ptrs(dq_out), _ptrs(dk_out), _ptrs(q_in), _ptrs(k_in), _ptrs(dq_in), _ptrs(dk_in),
+        plan, *_rank_ptrs(plan, dq_out, dk_out, q_in, k_in, dq_in, dk_in),
         _addr(rms_w), _addr(dw), eps, rope_theta, _addr(workspace), _nbytes(workspace),
         _stream(stream)), "ulysses_a2a_4d_qk_fused_backward")
 
@@ -403,7 +418,7 @@ def ulysses_a2a_4d_qkv_fused_backward(plan: Plan, dqkv_out, qkv_in, dq_in, dk_in
                                       dw, eps: float, rope_theta: float, workspace, stream=None):
     """Backward of the interleaved QKV call into packed (b, s_q, 3, N, d) gradients."""
     _check(_lib().ulysses_a2a_4d_qkv_fused_backward(
-        plan, _ptrs(dqkv_out), _ptrs(qkv_in), _ptrs(dq_in), _ptrs(dk_in), _ptrs(dv_in),
+        plan, *_rank_ptrs(plan, dqkv_out, qkv_in, dq_in, dk_in, dv_in),
         _addr(rms_w), _addr(dw), eps, rope_theta, _addr(workspace), _nbytes(workspace),
         _stream(stream)), "ulysses_a2a_4d_qkv_fused_backward")
 
@@ -415,8 +430,8 @@ def ulysses_a2a_4d_packed_fused_backward(plan: Plan, planes: int, q_plane: int, 
     """grads: one sequence of W gradient tensors per plane, flattened plane-major."""
     flat = [t for plane in grads for t in plane]
     _check(_lib().ulysses_a2a_4d_packed_fused_backward(
-        plan, planes, q_plane, k_plane, token_pitch, _ptrs(dpacked_out), _ptrs(packed_in),
-        _ptrs(flat), _addr(rms_w), _addr(dw), eps, rope_theta, _addr(workspace),
+        plan, planes, q_plane, k_plane, token_pitch, *_rank_ptrs(plan, dpacked_out, packed_in),
+        *_rank_ptrs(plan, flat, planes=planes), _addr(rms_w), _addr(dw), eps, rope_theta, _addr(workspace),
         _nbytes(workspace), _stream(stream)), "ulysses_a2a_4d_packed_fused_backward")
 
 
@@ -426,7 +441,7 @@ def ulysses_a2a_4d_qk_fused_backward_static(plan: Plan, dq_out, dk_out, q_in, k_
     (no workspace argument; the call allocates nothing). Calls that may run at the same time on
     one device race on that array."""
     _check(_lib().ulysses_a2a_4d_qk_fused_backward_static(
-        plan, _ptrs(dq_out), _ptrs(dk_out), _ptrs(q_in), _ptrs(k_in), _ptrs(dq_in), _ptrs(dk_in),
+        plan, *_rank_ptrs(plan, dq_out, dk_out, q_in, k_in, dq_in, dk_in),
         _addr(rms_w), _addr(dw), eps, rope_theta, _stream(stream)),
         "ulysses_a2a_4d_qk_fused_backward_static")
 
@@ -446,11 +461,10 @@ def ulysses_attention(q_plan: Plan, kv_plan: Plan, q, k, v, out, lse, scale: flo
     k, v (b, Skv, m_r, d), lse (b, n_r, Sq) fp32. kv_lens, q_start: int32 device tensors of b
     entries or None. `workspace` is a device tensor of at least
     ulysses_attention_workspace(q_plan, kv_plan) bytes (None where that is 0)."""
-    _check(_lib().ulysses_attention(q_plan, kv_plan, _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out),
-                                    _ptrs(lse), _counts(kv_lens, q_plan.b, "kv_lens"),
-                                    _counts(q_start, q_plan.b, "q_start"), int(causal), scale,
-                                    _addr(workspace), _nbytes(workspace), _stream(stream)),
-           "ulysses_attention")
+    masks = _counts(kv_lens, q_plan.b, "kv_lens"), _counts(q_start, q_plan.b, "q_start")
+    _check(_lib().ulysses_attention(
+        q_plan, kv_plan, *_rank_ptrs(q_plan, q, k, v, out, lse), *masks, int(causal), scale,
+        _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention")
 
 
 def ulysses_attention_backward_workspace(q_plan: Plan, kv_plan: Plan) -> int:
@@ -467,10 +481,9 @@ def ulysses_attention_backward(q_plan: Plan, kv_plan: Plan, dq, dk, dv, q, k, v,
     """Gradient of ulysses_attention into dq, dk, dv from its inputs, its outputs and the gradient
     `go` of out. `workspace` is a device tensor of at least
     ulysses_attention_backward_workspace(q_plan, kv_plan) bytes."""
+    masks = _counts(kv_lens, q_plan.b, "kv_lens"), _counts(q_start, q_plan.b, "q_start")
     _check(_lib().ulysses_attention_backward(
-        q_plan, kv_plan, _ptrs(dq), _ptrs(dk), _ptrs(dv), _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out),
-        _ptrs(lse), _ptrs(go), _counts(kv_lens, q_plan.b, "kv_lens"),
-        _counts(q_start, q_plan.b, "q_start"), int(causal), scale,
+        q_plan, kv_plan, *_rank_ptrs(q_plan, dq, dk, dv, q, k, v, out, lse, go), *masks, int(causal), scale,
         _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_backward")
 
 
@@ -487,9 +500,9 @@ def ulysses_attention_window(q_plan: Plan, kv_plan: Plan, q, k, v, out, lse, sca
     """Causal attention in which the query at position p sees the keys j > p - window and the first
     `sinks` ones. Tensors and masks as ulysses_attention. `workspace` is a device tensor of at least
     ulysses_attention_window_workspace(q_plan, kv_plan, window, sinks) bytes (None where that is 0)."""
+    masks = _counts(kv_lens, q_plan.b, "kv_lens"), _counts(q_start, q_plan.b, "q_start")
     _check(_lib().ulysses_attention_window(
-        q_plan, kv_plan, _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out), _ptrs(lse),
-        _counts(kv_lens, q_plan.b, "kv_lens"), _counts(q_start, q_plan.b, "q_start"), window, sinks, scale,
+        q_plan, kv_plan, *_rank_ptrs(q_plan, q, k, v, out, lse), *masks, window, sinks, scale,
         _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_window")
 
 
@@ -509,11 +522,10 @@ def ulysses_attention_window_backward(q_plan: Plan, kv_plan: Plan, dq, dk, dv, q
     """Gradient of ulysses_attention_window into dq, dk, dv from its inputs, its outputs and the gradient
     `go` of out. `workspace` is a device tensor of at least
     ulysses_attention_window_backward_workspace(q_plan, kv_plan, window, sinks) bytes."""
+    masks = _counts(kv_lens, q_plan.b, "kv_lens"), _counts(q_start, q_plan.b, "q_start")
     _check(_lib().ulysses_attention_window_backward(
-        q_plan, kv_plan, _ptrs(dq), _ptrs(dk), _ptrs(dv), _ptrs(q), _ptrs(k), _ptrs(v), _ptrs(out),
-        _ptrs(lse), _ptrs(go), _counts(kv_lens, q_plan.b, "kv_lens"),
-        _counts(q_start, q_plan.b, "q_start"), window, sinks, scale, _addr(workspace), _nbytes(workspace),
-        _stream(stream)), "ulysses_attention_window_backward")
+        q_plan, kv_plan, *_rank_ptrs(q_plan, dq, dk, dv, q, k, v, out, lse, go), *masks, window, sinks, scale,
+        _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_window_backward")
 
 
 def ulysses_attention_paged_workspace(q_plan: Plan, cache_plan: Plan) -> int:
@@ -535,7 +547,7 @@ def ulysses_attention_paged(q_plan: Plan, cache_plan: Plan, q, k_pages, v_pages,
     bytes (None where that is 0)."""
     table, pages = _page_table(page_table, q_plan.b)
     _check(_lib().ulysses_attention_paged(
-        q_plan, cache_plan, _ptrs(q), _ptrs(k_pages), _ptrs(v_pages), _ptrs(out), _ptrs(lse), table,
+        q_plan, cache_plan, *_rank_ptrs(q_plan, q, k_pages, v_pages, out, lse), table,
         pages, _counts(kv_lens, q_plan.b, "kv_lens"), _counts(q_start, q_plan.b, "q_start"), window,
         sinks, scale, _addr(workspace), _nbytes(workspace), _stream(stream)), "ulysses_attention_paged")
 
@@ -546,23 +558,22 @@ def ulysses_cache_append(kv_plan: Plan, cache_plan: Plan, k, v, k_pages, v_pages
     sequences' pages, i < counts[bb] (None: all). starts, counts: int32 device tensors of b entries."""
     table, pages = _page_table(page_table, kv_plan.b)
     _check(_lib().ulysses_cache_append(
-        kv_plan, cache_plan, _ptrs(k), _ptrs(v), _ptrs(k_pages), _ptrs(v_pages), table, pages,
+        kv_plan, cache_plan, *_rank_ptrs(kv_plan, k, v, k_pages, v_pages), table, pages,
         _counts(starts, kv_plan.b, "starts"), _counts(counts, kv_plan.b, "counts"), _stream(stream)),
         "ulysses_cache_append")
 
 
 def ulysses_a2a_4d_host(plan: Plan, mode: int, host_in, host_out, dev_in, dev_out, stream=None):
-    _check(_lib().ulysses_a2a_4d_host(plan, mode, _ptrs(host_in), _ptrs(host_out), _ptrs(dev_in),
-                                      _ptrs(dev_out), _stream(stream)), "ulysses_a2a_4d_host")
+    _check(_lib().ulysses_a2a_4d_host(plan, mode, *_rank_ptrs(plan, host_in, host_out, dev_in, dev_out),
+                                      _stream(stream)), "ulysses_a2a_4d_host")
 
 
 def ulysses_a2a_4d_qk_fused_host(plan: Plan, q_host_in, k_host_in, q_host_out, k_host_out, q_in,
                                  k_in, q_out, k_out, rms_w, eps: float, rope_theta: float,
                                  stream=None):
     _check(_lib().ulysses_a2a_4d_qk_fused_host(
-        plan, _ptrs(q_host_in), _ptrs(k_host_in), _ptrs(q_host_out), _ptrs(k_host_out), _ptrs(q_in),
-        _ptrs(k_in), _ptrs(q_out), _ptrs(k_out), _addr(rms_w), eps, rope_theta, _stream(stream)),
-        "ulysses_a2a_4d_qk_fused_host")
+        plan, *_rank_ptrs(plan, q_host_in, k_host_in, q_host_out, k_host_out, q_in, k_in, q_out, k_out),
+        _addr(rms_w), eps, rope_theta, _stream(stream)), "ulysses_a2a_4d_qk_fused_host")
 
 
 def ulysses_device_status() -> int:
