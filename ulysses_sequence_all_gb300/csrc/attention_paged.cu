@@ -196,11 +196,16 @@ __device__ __forceinline__ uint32_t pg_transpose(uint32_t x)
     return y;
 }
 
-// A limit of nothing (the self-test's) is one look: a copy takes less time than the hardware may hold back a
-// second one for, so that no wait would ever run out.
+// A limit of nothing (the self-test's) is one look: a copy takes less time than the hardware may hold a try_wait
+// back for, so that no wait would ever run out.
 __device__ __forceinline__ bool pg_wait(uint64_t* bar, uint32_t parity, uint64_t limit)
 {
-    return limit == 0 ? mbar_test_wait(bar, parity) : mbar_wait_bounded(bar, parity, limit);
+    if (mbar_test_wait(bar, parity)) return true;
+    if (limit == 0) return false;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > limit) return false;
+    return true;
 }
 
 __device__ __forceinline__ void pg_sync()  // the four warps with products
@@ -618,8 +623,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
 #pragma unroll
                 for (int w = 0; w < kPagedWarps; w += RH) {
                     const float2 z = sh.ml[w + rh][in];
-                    // (scores that were all NaN leave the maximum at minus infinity, but not the sum at 0)
-                    if (!sh.used[w + rh] || stage < 0 || (z.x == -INFINITY && z.y == 0.0f)) continue;
+                    // (not by the maximum: scores that were all NaN leave that at minus infinity)
+                    if (!sh.used[w + rh] || stage < 0 || z.y == 0.0f) continue;
                     const float f = ex2((z.x - top) * sl2);
                     sum = fmaf(f, z.y, sum);
 #pragma unroll
