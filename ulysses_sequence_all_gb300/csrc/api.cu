@@ -1148,20 +1148,18 @@ void pages_args(const PagedArgs& p, AttnFwdArgs* a)
 
 bool pages_of_few_rows(const PagedArgs& a) { return a.Sq * a.group <= kPagedFewRows; }
 
-// Work shares and passes of a call; the bytes of its workspace and the places in it.
-int paged_setup(const DeviceInfo& dev, PagedArgs* a, void* workspace, size_t* bytes)
+// Work shares of a call; the bytes of its workspace and the places in it.
+size_t paged_setup(const DeviceInfo& dev, PagedArgs* a, void* workspace)
 {
     attn_paged_split(a, dev.sm_count);
-    if (int64_t(a->b) * a->row_groups >= int64_t(1) << 31) return ULY_EINVAL;
     const size_t rows = 2 * size_t(a->parts) * size_t(a->rows);
     const size_t o = rows * size_t(a->d) * sizeof(float), lse = rows * sizeof(float);
-    *bytes = o + lse + size_t(a->parts) * sizeof(PagedShared);
-    uint8_t* base = static_cast<uint8_t*>(workspace);
-    if (!base) return ULY_OK;
-    a->part_o = reinterpret_cast<float*>(base);
-    a->part_lse = reinterpret_cast<float*>(base + o);
-    a->shared = reinterpret_cast<PagedShared*>(base + o + lse);
-    return ULY_OK;
+    if (uint8_t* base = static_cast<uint8_t*>(workspace)) {
+        a->part_o = reinterpret_cast<float*>(base);
+        a->part_lse = reinterpret_cast<float*>(base + o);
+        a->shared = reinterpret_cast<PagedShared*>(base + o + lse);
+    }
+    return o + lse + size_t(a->parts) * sizeof(PagedShared);
 }
 
 size_t pages_setup(const DeviceInfo& dev, AttnFwdArgs* a)
@@ -1221,7 +1219,7 @@ int paged_device(const Plan& qp, PagedArgs& a, const int64_t* kv_bytes, const vo
         const cudaError_t e = attn_fwd_launch(f, q, k, v, stream, dev.device, attn_cap(qp), dev.sm_count);
         return e == cudaSuccess ? ULY_OK : cuda_fail(e);
     }
-    if ((rc = paged_setup(dev, &a, workspace, &need))) return rc;
+    need = paged_setup(dev, &a, workspace);
     if (!workspace || workspace_bytes < need) return ULY_EINVAL;
     if (!aligned16(workspace)) return ULY_EALIGN;
     outs.add(workspace, int64_t(need));
@@ -1233,7 +1231,7 @@ int paged_device(const Plan& qp, PagedArgs& a, const int64_t* kv_bytes, const vo
         a.o[r] = static_cast<uint8_t*>(o[r]);
         a.lse[r] = lse[r];
     }
-    const cudaError_t e = attn_paged_launch(a, k, v, stream, dev.device, attn_cap(qp), dev.sm_count);
+    const cudaError_t e = attn_paged_launch(a, k, v, stream, dev.device, attn_cap(qp));
     return e == cudaSuccess ? ULY_OK : cuda_fail(e);
 }
 
@@ -1246,11 +1244,11 @@ int paged_room(const Plan& cp, int64_t table_pages, int64_t* room)
     return ULY_OK;
 }
 
-// Attention over contiguous keys with a window. Few rows (those of one pass of the paged kernel, which
-// reads a batch element's keys as its only page) go there.
+// Attention over contiguous keys with a window. Few rows go to the paged kernel, which
+// reads a batch element's keys as its only page.
 bool window_of_few_rows(const Plan& qp, const Plan& kp)
 {
-        return kp.N > 0 && qp.S * (qp.N / kp.N) <= kWindowFewRows;
+    return kp.N > 0 && qp.S * (qp.N / kp.N) <= kWindowFewRows;
 }
 
 int window_pages(const Plan& qp, const Plan& kp, const Window& w, PagedArgs* a)
@@ -1694,7 +1692,8 @@ int ulysses_attention_window_workspace(ulysses_plan_t q_plan, ulysses_plan_t kv_
     if (window_of_few_rows(qp, kp)) {
         PagedArgs a;
         if ((rc = window_pages(qp, kp, w, &a)) || (rc = current_device(&dev))) return rc;
-        return paged_setup(dev, &a, nullptr, bytes);
+        *bytes = paged_setup(dev, &a, nullptr);
+        return ULY_OK;
     }
     AttnFwdArgs a;
     std::memset(&a, 0, sizeof a);
@@ -1756,7 +1755,8 @@ int ulysses_attention_paged_workspace(ulysses_plan_t q_plan, ulysses_plan_t cach
         *bytes = pages_setup(dev, &f);
         return ULY_OK;
     }
-    return paged_setup(dev, &a, nullptr, bytes);
+    *bytes = paged_setup(dev, &a, nullptr);
+    return ULY_OK;
 }
 
 int ulysses_attention_paged(ulysses_plan_t q_plan, ulysses_plan_t cache_plan, const void* const* q,

@@ -7,7 +7,7 @@
 //
 // With R = group * tokens query rows a key head, each 4 d bytes of a key and its value carry 4 d R
 // flops: below some 200 rows memory bounds it, and the design is made to keep copies in flight. All the
-// work (the blocks of 64 keys that any row of a (batch element, row group, key head) sees) is laid end
+// work (the blocks of 64 keys that any row of a (batch element, key head) sees) is laid end
 // to end and cut into as many equal shares as CTAs run at a time, two an SM, whatever the sequences'
 // lengths: a CTA finds its share from the lengths by one scan. Warp 4 walks the share and copies block
 // after block into a ring (tensor maps, a lane a page, the table read a block ahead); warps 0-3 take 16
@@ -54,8 +54,8 @@ constexpr int kPgRegsProducts = DP == 128 ? (RT == 2 ? 200 : 184) : 176;
 constexpr float kPgRescale = 8.0f;  // log2 of the growth of a row's maximum that forces a rescale
 constexpr float kPgUpF16 = 7.0f;    // fp16 probabilities are held times 2^this
 constexpr int kPgJoinThreads = 256, kPgJoinParts = 8;
-// What a sequence's end (its join, the next one's queries) costs a CTA, in blocks of keys, by the query rows of
-// a pass. 1, 2, 3 with 8 rows: one token on 256 sequences of 100-2,000 keys 166, 170, 171 us, of 100-200 keys 47,
+// What a sequence's end (its join, the next one's queries) costs a CTA, in blocks of keys, by the kernel's query
+// rows. 1, 2, 3 with 8 rows: one token on 256 sequences of 100-2,000 keys 166, 170, 171 us, of 100-200 keys 47,
 // 46, 46, on 8 of 3,000-9,000 38, 37, 37 (0: the first two 191 and 58 when the end was slower). 2, 3, 4, 7 with 16
 // rows on the first 186, 187, 192, 199, four tokens on the last 41, 39, 39, 39; 3, 4, 5, 7 with 32 rows on the first
 // 228, 217, 218, 225.
@@ -63,15 +63,14 @@ constexpr int pg_end(int rows) { return rows <= 8 ? 2 : rows <= 16 ? 3 : 4; }
 
 // ---- what there is to do ----------------------------------------------------------------------------
 
-// A batch element's row group: the keys that its rows see, and the blocks that hold them.
+// A batch element: the keys that its rows see, and the blocks that hold them.
 struct PagedEntry {
-    int bb, rg;
+    int bb;
     int n;              // blocks, one at least: rows that see no key are written as well
     int first, near;    // the first tokens' blocks 0 .. first - 1; the others from block `near` on
     int snk, lo, end;   // some row sees key j: j < snk, or lo <= j < end
     int len;
     int64_t pos0;       // position of query token 0
-    int t0, t1;         // its tokens
     __device__ __forceinline__ int block(int j) const { return j < first ? j : near + j - first; }
     __device__ __forceinline__ bool sees(int a, int b) const  // any of keys a .. b - 1
     {
@@ -79,18 +78,14 @@ struct PagedEntry {
     }
 };
 
-__device__ __forceinline__ PagedEntry paged_entry(const PagedArgs& a, int e)
+__device__ __forceinline__ PagedEntry paged_entry(const PagedArgs& a, int bb)
 {
     PagedEntry t;
-    t.bb = a.row_groups == 1 ? e : e / a.row_groups;
-    t.rg = e - t.bb * a.row_groups;
+    t.bb = bb;
     t.len = a.kv_lens ? max(0, min(a.kv_lens[t.bb], a.room)) : a.room;
     t.pos0 = a.q_start ? int64_t(a.q_start[t.bb]) : a.from_end ? t.len - a.Sq : 0;
-    const int row = t.rg * a.rows, rows = int(a.Sq) * a.group;  // (fewer than 2^27)
-    t.t0 = int(uint32_t(row) / uint32_t(a.group));
-    t.t1 = int(uint32_t(min(row + a.rows, rows) - 1) / uint32_t(a.group)) + 1;
-    t.end = int(max(int64_t(0), min(int64_t(t.len), t.pos0 + t.t1)));
-    t.lo = int(max(int64_t(0), min(int64_t(t.end), t.pos0 + t.t0 + 1 - a.window)));
+    t.end = int(max(int64_t(0), min(int64_t(t.len), t.pos0 + a.Sq)));
+    t.lo = int(max(int64_t(0), min(int64_t(t.end), t.pos0 + 1 - a.window)));
     t.snk = min(a.sinks, t.lo);
     t.near = t.lo / kPagedBlock;
     t.first = min((t.snk + kPagedBlock - 1) / kPagedBlock, t.near);
@@ -118,7 +113,7 @@ struct PagedWalk {
     }
 };
 
-// The work is measured in blocks, a sequence (of one row group and head) of n as `end` + n, its end first:
+// The work is measured in blocks, a sequence (of one head) of n as `end` + n, its end first:
 // equal shares of that are equal times, however short the sequences are. A share that begins inside an end
 // begins with the sequence.
 __device__ __forceinline__ int64_t paged_share(int64_t total, int parts, int64_t c)  // where it begins
@@ -222,7 +217,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     using L = PgSmem<DP>;
     using E = ElemT<F16>;
     constexpr int K = L::kStages, kD = DP / 16;
-    constexpr int kMine = 8 * RT, kRows = kMine * RH;  // query rows of a warp, of a pass
+    constexpr int kMine = 8 * RT, kRows = kMine * RH;  // query rows of a warp, of the kernel
     constexpr int kPartRows = 2048 / (DP * 4);         // rows of outputs in 16 rows of a tile's 128 bytes
     constexpr float kUp = F16 ? kPgUpF16 : 0.0f;
     extern __shared__ uint8_t smem_raw[];
@@ -242,9 +237,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     }
 
     // How many blocks there are, and in which entry a share begins.
-    const int entries = a.b * a.row_groups;
-    const int each = (entries + kPgThreads - 1) / kPgThreads;
-    const int e0 = min(entries, int(threadIdx.x) * each), e1 = min(entries, e0 + each);
+    const int each = (a.b + kPgThreads - 1) / kPgThreads;
+    const int e0 = min(a.b, int(threadIdx.x) * each), e1 = min(a.b, e0 + each);
     int64_t mine = 0;
     for (int e = e0; e < e1; ++e) mine += paged_entry(a, e).n + a.end;
     int64_t upto = mine;
@@ -374,7 +368,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     const int quad = lane >> 2, pair = (lane & 3) * 2;  // fragments: key (column of V); query row
     for (int c = blockIdx.x; c < a.parts; c += gridDim.x) {
         share(c);
-        PagedShared shared = {0, 0, 0, 0, 0};
+        PagedShared shared = {0, 0, 0, 0};
         uint32_t q[RT][kD][2];
         // The walk's rank and key head; this warp's queries of it.
         auto place = [&](int* r, int* kvh) {
@@ -385,7 +379,7 @@ __global__ void __launch_bounds__(kPgThreads, 2)
         auto queries = [&]() {
             int r, kvh;
             place(&r, &kvh);
-            const int row0 = walk.en.rg * kRows + (warp % RH) * kMine, row_end = int(a.Sq) * a.group;
+            const int row0 = (warp % RH) * kMine, row_end = int(a.Sq) * a.group;
             auto query = [&](int row) {  // its first byte
                 const int tok = int(uint32_t(row) / uint32_t(a.group));
                 return a.q[r] + ((int64_t(walk.en.bb) * a.Sq + tok) * a.n[r] + kvh * a.group + row -
@@ -415,11 +409,10 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             const int64_t place = int64_t(walk.e) * heads + head;
             const int64_t at_end = stop - walk.left + a.end + en.n;  // where the sequence ends in the work
             // (fewer than 2^27 rows; no 64-bit divisions: see the join)
-            const int pass0 = en.rg * kRows, row_end = int(a.Sq) * a.group;
-            const int row0 = pass0 + (warp % RH) * kMine;
+            const int row0 = (warp % RH) * kMine, row_end = int(a.Sq) * a.group;
             // keys that every row sees: below hi_all, and from lo_all on or first tokens
-            const int hi_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t0 + 1)));
-            const int lo_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + en.t1 - a.window)));
+            const int hi_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + 1)));
+            const int lo_all = int(max(int64_t(0), min(int64_t(en.len), en.pos0 + a.Sq - a.window)));
             float m[RT][2], l[RT][2], o[RT][kD][4];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
@@ -574,9 +567,9 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             const bool whole = from == 0 && to_block == en.n;
             const int64_t part = 2 * int64_t(c) + (from == 0 ? 1 : 0);
             if (from == 0) {
-                shared = {0, 0, 0, 0, 0};
-                if (!whole) shared = {paged_owner(total, a.parts, at_end - 1) - c + 1, c, en.bb, en.rg, head};
-                if (a.by_group && threadIdx.x == 0) a.shared[place] = shared;
+                shared = {0, 0, 0, 0};
+                if (!whole) shared = {paged_owner(total, a.parts, at_end - 1) - c + 1, c, en.bb, head};
+                if (a.by_sequence && threadIdx.x == 0) a.shared[place] = shared;
             }
 #pragma unroll
             for (int t = 0; t < RT; ++t)
@@ -613,7 +606,6 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             for (int it = threadIdx.x; it < kRows * (DP / 8); it += 32 * kPagedWarps) {
                 const int row = it / (DP / 8), col = it % (DP / 8) * 8;
                 const int rh = row / kMine, in = row - rh * kMine;  // the warps' group, the row in it
-                const int to = pass0 + row;
                 if (col >= a.d) continue;
                 float top = -INFINITY, sum = 0.0f, y[8];
 #pragma unroll
@@ -647,9 +639,9 @@ __global__ void __launch_bounds__(kPgThreads, 2)
                     dst[0] = make_float4(y[0], y[1], y[2], y[3]);
                     dst[1] = make_float4(y[4], y[5], y[6], y[7]);
                     if (col == 0) a.part_lse[at_row] = lse;
-                } else if (to < row_end) {
-                    const int tok = int(uint32_t(to) / uint32_t(a.group));
-                    const int h = kvh * a.group + (to - tok * a.group);
+                } else if (row < row_end) {
+                    const int tok = int(uint32_t(row) / uint32_t(a.group));
+                    const int h = kvh * a.group + (row - tok * a.group);
                     st_v4(a.o[r] + (((int64_t(en.bb) * a.Sq + tok) * a.n[r] + h) * a.d + col) * 2,
                           make_uint4(E::pack(y[0], y[1]), E::pack(y[2], y[3]), E::pack(y[4], y[5]),
                                      E::pack(y[6], y[7])));
@@ -660,13 +652,13 @@ __global__ void __launch_bounds__(kPgThreads, 2)
             pg_sync();
             if (stage >= 0 && lane == 0) mbar_arrive(&sh.empty[stage]);
         }
-        if (!a.by_group && threadIdx.x == 0) a.shared[c] = shared;
+        if (!a.by_sequence && threadIdx.x == 0) a.shared[c] = shared;
     }
     if (!ok && lane == 0) atomicOr(&g_attn_paged_status, kStatusWaitTimeout);
     let_next_start();
 }
 
-// Joins what several CTAs made of a row group: block x looks at note x. `y_rows` of its warps take
+// Joins what several CTAs made of a sequence: block x looks at note x. `y_rows` of its warps take
 // a row each, the others of a row every (warps / y_rows)-th part; a lane has 4 columns.
 template <bool F16>
 __global__ void __launch_bounds__(kPgJoinThreads, 2)
@@ -744,12 +736,11 @@ __global__ void __launch_bounds__(kPgJoinThreads, 2)
                 }
                 __syncthreads();
             }
-            const int64_t to = int64_t(s.group) * a.rows + row;
-            if (way != 0 || to >= a.Sq * a.group) continue;
+            if (way != 0 || row >= int(a.Sq) * a.group) continue;
             int r = 0;
             while (r + 1 < a.W && s.head >= a.m_begin[r + 1]) ++r;
-            const int64_t tok = div_fast(to, a.group);
-            const int64_t h = int64_t(s.head - a.m_begin[r]) * a.group + (to - tok * a.group);
+            const int tok = row / a.group;
+            const int64_t h = int64_t(s.head - a.m_begin[r]) * a.group + (row - tok * a.group);
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             if (lane * 4 < a.d)
                 st_v2(a.o[r] + (((int64_t(s.bb) * a.Sq + tok) * a.n[r] + h) * a.d + lane * 4) * 2,
@@ -764,20 +755,17 @@ __global__ void __launch_bounds__(kPgJoinThreads, 2)
 
 void attn_paged_split(PagedArgs* a, int sm_count)
 {
-    const int64_t rows = a->Sq * a->group;
     a->rows = 8;
-    while (a->rows < kPagedMaxRows && a->rows < rows) a->rows *= 2;
-    a->row_groups = int32_t((rows + a->rows - 1) / a->rows);
+    while (a->rows < a->Sq * a->group) a->rows *= 2;  // (kPagedFewRows at most)
     a->parts = 2 * sm_count;
     a->end = pg_end(a->rows);
-    const int64_t groups = int64_t(a->b) * a->row_groups * a->m_begin[a->W];
-    a->by_group = groups <= a->parts;
-    a->notes = int32_t(a->by_group ? groups : a->parts);
+    const int64_t all = int64_t(a->b) * a->m_begin[a->W];
+    a->by_sequence = all <= a->parts;
+    a->notes = int32_t(a->by_sequence ? all : a->parts);
 }
 
 template <int DP, bool F16, int RT, int RH>
-static cudaError_t pg_launch(const PagedArgs& a, cudaStream_t stream, int device, int64_t cap,
-                             int sm_count)
+static cudaError_t pg_launch(const PagedArgs& a, cudaStream_t stream, int device, int64_t cap)
 {
     static std::atomic<unsigned long long> raised{0};
     const unsigned long long bit = device >= 0 && device < 64 ? 1ull << device : 0;
@@ -811,16 +799,15 @@ static cudaError_t pg_launch(const PagedArgs& a, cudaStream_t stream, int device
 }
 
 template <int DP, bool F16>
-static cudaError_t pg_launch_rows(const PagedArgs& a, cudaStream_t stream, int device, int64_t cap,
-                                  int sm_count)
+static cudaError_t pg_launch_rows(const PagedArgs& a, cudaStream_t stream, int device, int64_t cap)
 {
-    if (a.rows == 8) return pg_launch<DP, F16, 1, 1>(a, stream, device, cap, sm_count);
-    if (a.rows == 16) return pg_launch<DP, F16, 2, 1>(a, stream, device, cap, sm_count);
-    return pg_launch<DP, F16, 2, 2>(a, stream, device, cap, sm_count);
+    if (a.rows == 8) return pg_launch<DP, F16, 1, 1>(a, stream, device, cap);
+    if (a.rows == 16) return pg_launch<DP, F16, 2, 1>(a, stream, device, cap);
+    return pg_launch<DP, F16, 2, 2>(a, stream, device, cap);
 }
 
 cudaError_t attn_paged_launch(PagedArgs& a, const void* const* k, const void* const* v,
-                              cudaStream_t stream, int device, int64_t cap, int sm_count)
+                              cudaStream_t stream, int device, int64_t cap)
 {
     if (a.m_begin[a.W] == 0) return cudaSuccess;
     for (int r = 0; r < a.W; ++r) {
@@ -831,10 +818,10 @@ cudaError_t attn_paged_launch(PagedArgs& a, const void* const* k, const void* co
             return cudaErrorInvalidValue;
     }
     if (a.d <= 64)
-        return a.f16 ? pg_launch_rows<64, true>(a, stream, device, cap, sm_count)
-                     : pg_launch_rows<64, false>(a, stream, device, cap, sm_count);
-    return a.f16 ? pg_launch_rows<128, true>(a, stream, device, cap, sm_count)
-                 : pg_launch_rows<128, false>(a, stream, device, cap, sm_count);
+        return a.f16 ? pg_launch_rows<64, true>(a, stream, device, cap)
+                     : pg_launch_rows<64, false>(a, stream, device, cap);
+    return a.f16 ? pg_launch_rows<128, true>(a, stream, device, cap)
+                 : pg_launch_rows<128, false>(a, stream, device, cap);
 }
 
 cudaError_t attn_paged_status(unsigned* status, bool clear)

@@ -17,11 +17,11 @@ namespace uly {
 constexpr int kPagedTile = 16;           // keys that a warp takes at a time
 constexpr int kPagedWarps = 4;
 constexpr int kPagedBlock = kPagedTile * kPagedWarps;
-constexpr int kPagedMaxRows = 32;        // query rows of one pass over the keys
 // Query rows a key head (group * tokens) up to which attention_paged.cu runs, above them the tensor cores'
 // long layout. Over pages, paged : long in us, 32 rows: 8 caches of 3,000-9,000 tokens, 8 key heads 43 : 70;
 // 16 of 12,000-32,000, 4 key heads 120 : 191; 256 of 100-2,000, 8 key heads 217 : 354; 32 windows of 4,096, 20 rows
-// 106 : 123. 64 rows (four warps with 16 each, keys read once): 67 : 71, 203 : 193, 381 : 353, 176 : 124.
+// 106 : 123. (With 64 rows, 16 for each of the four warps, it took 67 : 71, 203 : 193, 381 : 353, 176 : 124: no
+// such form is kept.)
 constexpr int kPagedFewRows = 32;
 // Over contiguous keys with a window of 4,096, 8 key heads: 4 caches, 4 rows 22.8 : 26.6, 16 rows 25.8 : 26.7,
 // 32 rows 28.6 : 27.8; 32 caches, 4 rows 94 : 106, 32 rows 105.5 : 104.9.
@@ -37,11 +37,11 @@ struct AppendArgs {
     int32_t W;
 };
 
-// A batch element's row group (`rows` query rows) of a key head that several shares of the work have
-// parts of: share `cta` its beginning, the next parts - 1 the rest.
+// A sequence (a batch element's key head) that several shares of the work have parts of: share `cta` its
+// beginning, the next parts - 1 the rest.
 struct PagedShared {
     int32_t parts;  // 0: none
-    int32_t cta, bb, group, head;
+    int32_t cta, bb, head;
 };
 
 struct PagedArgs {
@@ -59,10 +59,10 @@ struct PagedArgs {
     int32_t room;            // keys that a batch element's pages can hold
     int32_t sinks;
     int64_t window;          // beyond every position where there is none
-    int32_t rows, row_groups;  // query rows of a pass (8, 16, 32, 64); passes of a key head
-    int32_t parts;             // shares of all the work, one CTA at a time works on one
-    int32_t end;               // blocks that a sequence's end counts for in them
-    int32_t by_group, notes;   // `shared` has an entry for each row group and head, or for each share
+    int32_t rows;    // query rows of the kernel (8, 16, 32), of which the call's are the first
+    int32_t parts;   // shares of all the work, one CTA at a time works on one
+    int32_t end;     // blocks that a sequence's end counts for in them
+    int32_t by_sequence, notes;  // `shared` has an entry for each sequence, or for each share
     float scale;
     uint32_t wait_us;
     float* part_o;         // [2 parts][rows][d] normalised partial outputs
@@ -71,10 +71,10 @@ struct PagedArgs {
 };
 
 cudaError_t cache_append_launch(const AppendArgs& a, cudaStream_t stream, int64_t cap, int sm_count);
-// Rows, passes and shares from the shape and the device alone: a CTA cap changes no bit.
+// Rows and shares from the shape and the device alone: a CTA cap changes no bit.
 void attn_paged_split(PagedArgs* a, int sm_count);
 cudaError_t attn_paged_launch(PagedArgs& a, const void* const* k, const void* const* v,
-                              cudaStream_t stream, int device, int64_t cap, int sm_count);
+                              cudaStream_t stream, int device, int64_t cap);
 cudaError_t cache_append_status(unsigned* status, bool clear);
 cudaError_t attn_paged_status(unsigned* status, bool clear);
 
