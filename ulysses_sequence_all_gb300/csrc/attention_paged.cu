@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(kPgThreads, 2)
     }
 
     // How many blocks there are, and in which entry a share begins.
-    const int each = (a.b + kPgThreads - 1) / kPgThreads;
-    const int e0 = min(a.b, int(threadIdx.x) * each), e1 = min(a.b, e0 + each);
+    const int each = (a.b - 1) / kPgThreads + 1;
+    const int e0 = min(a.b, int(threadIdx.x) * each), e1 = e0 + min(each, a.b - e0);
     int64_t mine = 0;
     for (int e = e0; e < e1; ++e) mine += paged_entry(a, e).n + a.end;
     int64_t upto = mine;
