@@ -31,7 +31,8 @@ def attention_block(plan: B.Plan, qkv, rms_w, eps: float = 1e-6, rope_theta: flo
     """Attention of packed shards: qkv is W tensors (b, s_q, 3, N, d), rms_w (2, d) fp32 the norm
     weights of q and k. The plan's RoPE settings hold (ulysses_plan_set_rope_grid gives positions
     of several axes). kv_lens: b key counts where the batch is padded at its end. window, sinks: causal
-    attention to the last `window` tokens and the first `sinks`. Differentiable in qkv and rms_w. Returns W tensors (b, s_q, N, d)."""
+    attention to the last `window` tokens and the first `sinks`. Differentiable in qkv and rms_w.
+    Returns W tensors (b, s_q, N, d)."""
     q, k, v = A.qkv_fused(plan, qkv, rms_w, eps, rope_theta)
     o = A.attention(plan, plan, q, k, v, scale, causal, kv_lens, window=window, sinks=sinks)
     return A.a2a_4d(plan, o, mode=1)

@@ -23,7 +23,9 @@ plan for the backward:
 Inputs and outputs are lists of W tensors (one per virtual rank) on the current CUDA device;
 the outputs are new tensors the caller owns. The relayout can be differentiated again, the others
 once: a gradient of theirs raises where it is differentiated. Nothing here computes: every step runs in the
-library's kernels, on the current stream.
+library's kernels, on the current stream. A training step can be captured in a CUDA graph, warmed up on a side
+stream, while no result of an eager call on the same leaves is alive: their gradients would be accumulated on that
+call's stream, which torch refuses during the capture.
 """
 from __future__ import annotations
 

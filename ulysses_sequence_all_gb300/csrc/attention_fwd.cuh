@@ -44,7 +44,9 @@
 // and 4 first tokens in 0.117-0.133 ms, of whose cycles the tensor pipe is busy in 43 %.
 // Over pages (PAGED) the loading warp's lanes copy a page's rows each, its place in the table looked up a block
 // ahead; list rows that no row sees are copied from beyond the pool, which gives zeros. Measured: 8 caches of
-// 30,000 tokens, 8 key heads, 64 rows each in 205 us (0.71 of the copy peak), pages of 32 tokens.
+// 30,000 tokens, 8 key heads, 64 rows each in 205 us (0.71 of the copy peak), pages of 32 tokens; pieces of prompts,
+// 32 heads over 8 of 128, pages of 64: the last 2,048 of 8,000 tokens, 4 of them, in 640 us (1.46 PFLOP/s), of
+// 30,000, 2 of them, in 1.42 ms (1.37); whole prompts, 2 x 4,095, in 223 us (1.23 PFLOP/s; contiguous keys 183 us).
 //
 // With few rows (one tile of them: single tokens) both tiles of a CTA are those rows, each over its
 // own part of the keys; with too few units to fill the SMs the keys are split further. A part has

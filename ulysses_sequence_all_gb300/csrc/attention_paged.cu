@@ -17,9 +17,9 @@
 // the same bits from run to run.
 //
 // Measured (bf16, copy peak 6,767 GB/s): one token each on 16 caches of 12,000-32,768 tokens, 32 heads over 4 of
-// 128 in 116 us (0.92 of the peak), on 256 of 100-2,000, 64 heads over 8, in 169 us (0.90), with a window of
-// 4,096 on 32 sequences, 40 heads over 8, in 93 us (0.85); four drafted tokens on 8 caches of 3,000-9,000 in
-// 39 us (0.65), one short cache in 9.8 us: about 10 us of each are the launches, the first copies' chain of
+// 128 in 115-117 us (0.92 of the peak), on 256 of 100-2,000, 64 heads over 8, in 170-171 us (0.89), with a window of
+// 4,096 on 32 sequences, 40 heads over 8, in 92-94 us (0.86); four drafted tokens on 8 caches of 3,000-9,000 in
+// 39-41 us (0.65), one short cache in 9.3 us: about 10 us of each are the launches, the first copies' chain of
 // loads (lengths, table, map, keys) and the last join. 32 rows on the 16 caches take 120 us.
 //
 // Products: S^T = K Q^T and O^T += V^T P^T with keys (and columns of V) as the 16 rows of an

@@ -5,8 +5,8 @@
 // token a sequence by the launch. A warp takes 32 tokens of a rank's keys or values: a lane works out one
 // token's place (the divisions and the table, once a token), then the warp moves the tokens' rows of
 // m_r * d in 16-byte words, neighbouring lanes neighbouring words, several loads before their stores.
-// Measured: 4 x 16,380 tokens at most (ragged) of 8 heads of 128, W = 4, in 45 us, 5.1 TB/s read and written
-// (0.76 of the copy peak; a place worked out by every word's thread: 74 us); 256 sequences' one token, W = 8,
+// Measured: 4 x 16,380 tokens at most (ragged) of 8 heads of 128, W = 4, in 45-47 us, 4.9-5.1 TB/s read and
+// written (0.72-0.76 of the copy peak; a place worked out by every word's thread: 74 us); 256 sequences' one token, W = 8,
 // in 6.7 us.
 #include <cuda_runtime.h>
 

@@ -18,13 +18,13 @@ constexpr int kPagedTile = 16;           // keys that a warp takes at a time
 constexpr int kPagedWarps = 4;
 constexpr int kPagedBlock = kPagedTile * kPagedWarps;
 // Query rows a key head (group * tokens) up to which attention_paged.cu runs, above them the tensor cores'
-// long layout. Over pages, paged : long in us, 32 rows: 8 caches of 3,000-9,000 tokens, 8 key heads 43 : 70;
-// 16 of 12,000-32,000, 4 key heads 120 : 191; 256 of 100-2,000, 8 key heads 217 : 354; 32 windows of 4,096, 20 rows
-// 106 : 123. (With 64 rows, 16 for each of the four warps, it took 67 : 71, 203 : 193, 381 : 353, 176 : 124: no
-// such form is kept.)
+// long layout. Over pages, paged : long in us, 8, 16, 32 rows: 8 caches of 3,000-9,000 tokens, 8 key heads 46 : 72,
+// 49 : 73, 51 : 74; 16 of 12,000-32,000, 4 key heads 128 : 195, 131 : 196, 133 : 197; 256 of 100-2,000, 8 key heads
+// 180 : 357, 200 : 358, 230 : 359; 32 windows of 4,096, 20 rows 106 : 123. (With 64 rows, 16 for each of the four
+// warps, it took 67 : 71, 203 : 193, 381 : 353, 176 : 124: no such form is kept.)
 constexpr int kPagedFewRows = 32;
-// Over contiguous keys with a window of 4,096, 8 key heads: 4 caches, 4 rows 22.8 : 26.6, 16 rows 25.8 : 26.7,
-// 32 rows 28.6 : 27.8; 32 caches, 4 rows 94 : 106, 32 rows 105.5 : 104.9.
+// Over contiguous keys with a window of 4,096, 8 key heads, 4, 16, 32 rows: 4 caches 20.6 : 25.7, 24.8 : 25.5,
+// 27.8 : 26.7; 32 caches 91 : 105, 99 : 105, 104.6 : 105.4.
 constexpr int kWindowFewRows = 16;
 
 struct AppendArgs {
